@@ -10,4 +10,7 @@ from .binding import (FwError, fw_delta_decode_step, fw_delta_forward,  # noqa: 
                       fw_delta_forward_workspace_size, fw_device_status, fw_dpfp, fw_linear_forward,
                       fw_linear_forward_workspace_size, fw_delta_backward, fw_delta_backward_workspace_size,
                       fw_delta_forward_projected, fw_delta_forward_projected_workspace_size,
-                      fw_decode_stack_step, fw_decode_stack_workspace_size)
+                      fw_decode_stack_step, fw_decode_stack_workspace_size,
+                      fw_gated_delta_forward, fw_gated_delta_forward_workspace_size, fw_gated_delta_backward,
+                      fw_gated_delta_backward_workspace_size, fw_gated_delta_decode_step, fw_group_norm_act,
+                      fw_group_norm_act_backward, fw_group_norm_act_backward_workspace_size)

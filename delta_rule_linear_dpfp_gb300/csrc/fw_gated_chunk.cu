@@ -1,0 +1,792 @@
+// fw_gated_chunk.cu -- the gated delta rule over a sequence and its
+// gradients, in chunks of 64 tokens, fp32 on CUDA cores.
+//
+// The rule, per value head (a_t = exp(g_t)):
+//   W_t = a_t W_{t-1} + beta_t (v_t - a_t W_{t-1} k_t) k_t^T,  y_t = scale W_t q_t.
+// With G the running sum of g inside a chunk, D_ij = exp(G_i - G_j) for
+// j <= i, S the chunk's first state and S' its last, row i of each matrix
+// belonging to token i:
+//   A = strict_lower(beta_i D_ij k_i.k_j),   T = (I + A)^-1,
+//   X = beta (V - e^G K S^T),                U = T X,
+//   M = lower(scale D_ij q_i.k_j),           Y = scale e^G Q S^T + M U,
+//   S' = e^{G_C} S + (e^{G_C - G} U)^T K.
+// Every exponent is a difference of sums taken over later tokens minus
+// earlier ones, so nothing overflows for g <= 0 however strong the gate is;
+// the sums are formed in 64 bits and kept as a float pair, because a
+// difference of two large sums would lose the small one.
+//
+// Transposed, given dY and dS' (the gradient of the next chunk's state):
+//   dU = M^T dY + e^{G_C - G} K dS'^T,       dX = T^T dU,
+//   dS = e^{G_C} dS' + (scale e^G dY)^T Q - (beta e^G dX)^T K,
+// and per chunk, with E = lower(scale D dY U^T), F = strict_lower(D dX U^T):
+//   q-side   a_i = scale e^{G_i} S^T dY_i + sum_j E_ij k_j            (= dq_i)
+//   reader   h_i = e^{G_i} S^T dX_i + sum_j F_ij k_j
+//   writer   w_j = e^{G_C-G_j} dS'^T U_j + sum_i E_ij q_i - sum_i beta_i F_ij k_i
+//   dk = w - beta h,  dV = beta dX,  dbeta_i = dX_i.V_i - k_i.h_i,
+//   dG_i = q_i.a_i - beta_i k_i.h_i - k_i.w_i, and for the chunk's last token
+//   also e^{G_C} <S, dS'> + sum_j e^{G_C-G_j} k_j.(dS'^T U_j);
+//   dg_t = sum of dG_i over i >= t in the chunk.
+// Keys and queries scaled to unit length enter as r k with one fp32 r per
+// token, and dk = r (dk^ - k^ (k^.dk^)) comes back.
+//
+// Kernels: prep (per chunk: T, M and the per-token scalars), walk (the chunks
+// of a head in order, per slice of 32 value channels: a channel's row of the
+// state never meets another), reverse walk (the same backwards), grad (per
+// chunk and key head: the sums over its value heads stay in one CTA, so the
+// gradients of shared heads have a fixed order).
+#include "fw_common.cuh"
+#include "fw_gated.h"
+
+#include <algorithm>
+
+namespace fw {
+
+namespace {
+
+constexpr int C = kGatedChunk;
+constexpr int NT = 256;  // threads per CTA
+constexpr int NV = 32;   // value channels per walk CTA
+constexpr int LC = C + 4; // row stride of a C x C tile
+constexpr int LV = NV + 4;
+constexpr int TOK = 8; // floats per token: rk, rq, e^G, e^{G_C-G}, G high, G low, beta, unused
+constexpr float kGMin = -200.f; // e^g is 0 in fp32 below this: a gate of -inf is a sum that stays finite
+
+// Workspace, in floats: per chunk of every value head.
+struct Ws {
+    float *T, *M, *tok, *S, *dS, *U, *dX;
+};
+struct WsOff {
+    size_t T, M, tok, S, dS, U, dX, end;
+};
+WsOff ws_off(int BH, int L, int d_k, int d_v, bool backward) {
+    const size_t n = (size_t)BH * ((L + C - 1) / C);
+    WsOff o;
+    o.T = 0;
+    o.M = o.T + n * C * C;
+    o.tok = o.M + n * C * C;
+    o.S = o.tok + n * C * TOK;
+    if (!backward) {
+        o.dS = o.U = o.dX = o.end = o.S;
+        return o;
+    }
+    o.dS = o.S + n * d_v * d_k;
+    o.U = o.dS + n * d_v * d_k;
+    o.dX = o.U + n * C * d_v;
+    o.end = o.dX + n * C * d_v;
+    return o;
+}
+Ws ws_at(void *p, const WsOff &o) {
+    float *f = static_cast<float *>(p);
+    return {f + o.T, f + o.M, f + o.tok, f + o.S, f + o.dS, f + o.U, f + o.dX};
+}
+
+FW_DEV int seq_len(const GatedArgs &a, int b) {
+    return a.lengths ? min(max(__ldcg(a.lengths + b), 0), a.L) : a.L;
+}
+
+// rows x d of T (row stride lds) into fp32 shared memory; rows at or past
+// `valid` and channels at or past `cols` are zero (whatever is stored there).
+template <typename T>
+FW_DEV void load_tile(float *dst, int ldd, const T *src, size_t lds, int rows, int valid, int cols, int width) {
+    const int c8 = width >> 3;
+    for (int e = threadIdx.x; e < rows * c8; e += NT) {
+        const int i = e / c8, c = (e % c8) * 8;
+        float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (i < valid && c < cols)
+            load8(src + (size_t)i * lds + c, x);
+        float4 *d = reinterpret_cast<float4 *>(dst + i * ldd + c);
+        d[0] = make_float4(x[0], x[1], x[2], x[3]);
+        d[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+}
+
+FW_DEV float4 lds4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+
+// acc[r][s] += sum_k A[r][k] B[s][k] (K a multiple of 4).
+template <int R, int S>
+FW_DEV void mm_nt(float (&acc)[R][S], const float *A, int lda, int ra, const float *B, int ldb, int rb, int K) {
+#pragma unroll 2
+    for (int k = 0; k < K; k += 4) {
+        float4 a[R], b[S];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            a[r] = lds4(A + r * ra * lda + k);
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+            b[s] = lds4(B + s * rb * ldb + k);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                acc[r][s] = fmaf(a[r].w, b[s].w, fmaf(a[r].z, b[s].z, fmaf(a[r].y, b[s].y, fmaf(a[r].x, b[s].x, acc[r][s]))));
+    }
+}
+
+// acc[r][0..3] += sum_k A[k lda + r ra] B[k ldb .. + 3] * w[k]: A's rows run
+// along k (transposed use).
+template <int R>
+FW_DEV void mm_tn(float (&acc)[R][4], const float *A, int lda, int ra, const float *B, int ldb, int K) {
+#pragma unroll 4
+    for (int k = 0; k < K; ++k) {
+        const float4 b = lds4(B + k * ldb);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float x = A[k * lda + r * ra];
+            acc[r][0] = fmaf(x, b.x, acc[r][0]);
+            acc[r][1] = fmaf(x, b.y, acc[r][1]);
+            acc[r][2] = fmaf(x, b.z, acc[r][2]);
+            acc[r][3] = fmaf(x, b.w, acc[r][3]);
+        }
+    }
+}
+
+// acc[r][0..3] += sum_k A[r][k] B[k ldb .. + 3].
+template <int R>
+FW_DEV void mm_nn(float (&acc)[R][4], const float *A, int lda, int ra, const float *B, int ldb, int K) {
+#pragma unroll 2
+    for (int k = 0; k < K; k += 4) {
+        float4 a[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            a[r] = lds4(A + r * ra * lda + k);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float4 b = lds4(B + (k + u) * ldb);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float x = u == 0 ? a[r].x : u == 1 ? a[r].y : u == 2 ? a[r].z : a[r].w;
+                acc[r][0] = fmaf(x, b.x, acc[r][0]);
+                acc[r][1] = fmaf(x, b.y, acc[r][1]);
+                acc[r][2] = fmaf(x, b.z, acc[r][2]);
+                acc[r][3] = fmaf(x, b.w, acc[r][3]);
+            }
+        }
+    }
+}
+
+// T = (I + A)^-1 of the strictly lower triangular A (C x C, stride LC):
+// forward substitution inside the four 16 x 16 diagonal blocks, one thread
+// per column, then two doublings T21 = -T22 (A21 T11).
+FW_DEV void unit_lower_inverse(const float *A, float *T, float *tmp) {
+    const int tid = threadIdx.x;
+    for (int e = tid; e < C * C; e += NT)
+        if ((e >> 6) >> 4 < (e & 63) >> 4)
+            T[(e >> 6) * LC + (e & 63)] = 0.f;
+    if (tid < C) {
+        const int b0 = tid & ~15, j = tid & 15;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float s = i == j ? 1.f : 0.f;
+#pragma unroll
+            for (int m = 0; m < i; ++m)
+                s = fmaf(-A[(b0 + i) * LC + b0 + m], x[m], s);
+            x[i] = s;
+            T[(b0 + i) * LC + b0 + j] = s;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 16; h <= 32; h *= 2) {
+        const int per = h * h, n = (C / (2 * h)) * per;
+        for (int e = tid; e < n; e += NT) {
+            const int p = e / per, i = (e % per) / h, j = e % h, r0 = p * 2 * h;
+            float s = 0.f;
+            for (int m = j; m < h; ++m)
+                s = fmaf(A[(r0 + h + i) * LC + r0 + m], T[(r0 + m) * LC + r0 + j], s);
+            tmp[p * per + i * h + j] = s;
+        }
+        __syncthreads();
+        for (int e = tid; e < n; e += NT) {
+            const int p = e / per, i = (e % per) / h, j = e % h, r0 = p * 2 * h;
+            float s = 0.f;
+            for (int m = 0; m <= i; ++m)
+                s = fmaf(T[(r0 + h + i) * LC + r0 + h + m], tmp[p * per + m * h + j], s);
+            T[(r0 + h + i) * LC + r0 + j] = -s;
+        }
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------------ prep
+template <typename T>
+__global__ void __launch_bounds__(NT)
+    gated_prep_kernel(GatedArgs a, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ g,
+                      const T *__restrict__ beta, Ws ws) {
+    extern __shared__ __align__(16) float sm[];
+    const int ldk = a.d_k + 4;
+    float *kt = sm, *qt = kt + C * ldk, *At = qt + C * ldk, *Tt = At + C * LC, *tmp = Tt + C * LC, *tok = tmp + 1024;
+    const int tid = threadIdx.x, c = blockIdx.x, bh = blockIdx.y;
+    const int b = bh / a.H, h = bh % a.H, kh = b * a.Hk + h / (a.H / a.Hk);
+    griddep_launch_dependents();
+    griddep_wait();
+    const int n = min(C, seq_len(a, b) - c * C);
+    if (n <= 0)
+        return;
+    const size_t row0 = (size_t)c * C;
+    load_tile(kt, ldk, k + ((size_t)kh * a.L + row0) * a.d_k, a.d_k, C, n, a.d_k, a.d_k);
+    load_tile(qt, ldk, q + ((size_t)kh * a.L + row0) * a.d_k, a.d_k, C, n, a.d_k, a.d_k);
+    if (tid < 32) { // the running sums of g, two tokens a lane
+        const size_t t0 = (size_t)bh * a.L + row0;
+        double s[2];
+        float be[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = 2 * tid + e;
+            const float x = i < n ? io<T>::load(g + t0 + i) : 0.f;
+            s[e] = x < kGMin ? kGMin : x;
+            be[e] = i < n ? io<T>::load(beta + t0 + i) : 0.f;
+        }
+        s[1] += s[0];
+        double run = s[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double up = __shfl_up_sync(0xffffffffu, run, o);
+            if (tid >= o)
+                run += up;
+        }
+        const double before = run - s[1], all = __shfl_sync(0xffffffffu, run, 31);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const double G = before + s[e];
+            float *d = tok + (2 * tid + e) * TOK;
+            d[2] = expf((float)G);
+            d[3] = expf((float)(all - G));
+            d[4] = (float)G;
+            d[5] = (float)(G - (double)(float)G);
+            d[6] = be[e];
+            d[7] = 0.f;
+        }
+    }
+    __syncthreads();
+    if (tid < 2 * C) { // 1 / length of each key and query (0 for a row of zeros)
+        const float *x = (tid < C ? kt : qt) + (tid & 63) * ldk;
+        float ss = a.eps;
+        for (int m = 0; m < a.d_k; ++m)
+            ss = fmaf(x[m], x[m], ss);
+        tok[(tid & 63) * TOK + (tid >> 6)] = !a.l2norm ? 1.f : ss > 0.f ? 1.f / sqrtf(ss) : ss;
+    }
+    __syncthreads();
+    const size_t ch = (size_t)bh * gridDim.x + c;
+    {
+        const int ti = tid & 15, tj = tid >> 4;
+        float akk[4][4] = {}, aqk[4][4] = {};
+        mm_nt<4, 4>(akk, kt + ti * ldk, ldk, 16, kt + tj * ldk, ldk, 16, a.d_k);
+        mm_nt<4, 4>(aqk, qt + ti * ldk, ldk, 16, kt + tj * ldk, ldk, 16, a.d_k);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int i = ti + 16 * r, j = tj + 16 * s;
+                const float *di = tok + i * TOK, *dj = tok + j * TOK;
+                const float D = j <= i ? expf((di[4] - dj[4]) + (di[5] - dj[5])) : 0.f;
+                At[i * LC + j] = j < i ? di[6] * D * di[0] * dj[0] * akk[r][s] : 0.f;
+                ws.M[ch * C * C + i * C + j] = j <= i ? a.scale * D * di[1] * dj[0] * aqk[r][s] : 0.f;
+            }
+    }
+    __syncthreads();
+    unit_lower_inverse(At, Tt, tmp);
+    for (int e = tid; e < C * C; e += NT)
+        ws.T[ch * C * C + e] = Tt[(e >> 6) * LC + (e & 63)];
+    for (int e = tid; e < C * TOK; e += NT)
+        ws.tok[ch * C * TOK + e] = tok[e];
+}
+
+// ------------------------------------------------------------------ walk
+// One CTA per (value head, 32 value channels).  KEEP: the chunks' first
+// states and U stay in the workspace for the gradients (no answers then).
+template <typename T, bool KEEP>
+__global__ void __launch_bounds__(NT)
+    gated_walk_kernel(GatedArgs a, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+                      const float *__restrict__ W0, float *__restrict__ Wf, T *__restrict__ y, Ws ws) {
+    extern __shared__ __align__(16) float sm[];
+    const int ldk = a.d_k + 4, nC = (a.L + C - 1) / C;
+    float *S = sm, *kq = S + NV * ldk, *Tt = kq + 2 * C * ldk, *Mt = Tt + C * LC, *Xt = Mt + C * LC, *Ut = Xt + C * LV,
+          *tok = Ut + C * LV;
+    const int tid = threadIdx.x, ti = tid & 31, tj = tid >> 5, bh = blockIdx.y, n0 = blockIdx.x * NV;
+    const int b = bh / a.H, kh = b * a.Hk + (bh % a.H) / (a.H / a.Hk);
+    const int nv = min(NV, a.d_v - n0);
+    griddep_launch_dependents();
+    griddep_wait();
+    const int len = seq_len(a, b);
+    const size_t st0 = ((size_t)bh * a.d_v + n0) * a.d_k;
+    load_tile(S, ldk, W0 + st0, a.d_k, NV, W0 ? nv : 0, a.d_k, a.d_k);
+    for (int c = 0; c < nC; ++c) {
+        const int n = min(C, len - c * C);
+        if (n <= 0)
+            break;
+        const size_t ch = (size_t)bh * nC + c, t0 = (size_t)c * C;
+        const size_t krow = ((size_t)kh * a.L + t0) * a.d_k, vrow = ((size_t)bh * a.L + t0) * a.d_v + n0;
+        __syncthreads();
+        load_tile(kq, ldk, k + krow, a.d_k, C, n, a.d_k, a.d_k);
+        load_tile(kq + C * ldk, ldk, q + krow, a.d_k, C, n, a.d_k, a.d_k);
+        load_tile(Tt, LC, ws.T + ch * C * C, C, C, C, C, C);
+        if (!KEEP)
+            load_tile(Mt, LC, ws.M + ch * C * C, C, C, C, C, C);
+        load_tile(Xt, LV, v + vrow, a.d_v, C, n, nv, NV);
+        for (int e = tid; e < C * TOK; e += NT)
+            tok[e] = __ldcg(ws.tok + ch * C * TOK + e);
+        __syncthreads();
+        if (KEEP)
+            for (int e = tid; e < nv * a.d_k; e += NT)
+                ws.S[ch * a.d_v * a.d_k + (size_t)n0 * a.d_k + e] = S[(e / a.d_k) * ldk + e % a.d_k];
+        float acc[4][4] = {}; // rows ti, ti + 32 of K, then of Q; channels 4 tj ..
+        if (KEEP) {
+            float pk[2][4] = {};
+            mm_nt<2, 4>(pk, kq + ti * ldk, ldk, 32, S + tj * 4 * ldk, ldk, 1, a.d_k);
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    acc[r][s] = pk[r][s];
+        } else {
+            mm_nt<4, 4>(acc, kq + ti * ldk, ldk, 32, S + tj * 4 * ldk, ldk, 1, a.d_k);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float *d = tok + (ti + 32 * r) * TOK;
+            float *x = Xt + (ti + 32 * r) * LV + tj * 4;
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                x[s] = d[6] * (x[s] - d[2] * d[0] * acc[r][s]);
+        }
+        __syncthreads();
+        float u[2][4] = {};
+        mm_nn<2>(u, Tt + ti * LC, LC, 32, Xt + tj * 4, LV, C);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int i = ti + 32 * r;
+            *reinterpret_cast<float4 *>(Ut + i * LV + tj * 4) = make_float4(u[r][0], u[r][1], u[r][2], u[r][3]);
+            if (KEEP && tj * 4 < nv)
+                *reinterpret_cast<float4 *>(ws.U + (ch * C + i) * a.d_v + n0 + tj * 4) =
+                    make_float4(u[r][0], u[r][1], u[r][2], u[r][3]);
+        }
+        __syncthreads();
+        if (!KEEP) {
+            float o[2][4];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float *d = tok + (ti + 32 * r) * TOK;
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    o[r][s] = a.scale * d[2] * d[1] * acc[2 + r][s];
+            }
+            mm_nn<2>(o, Mt + ti * LC, LC, 32, Ut + tj * 4, LV, C);
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                if (ti + 32 * r < n && tj * 4 < nv)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        io<T>::store(y + vrow + (size_t)(ti + 32 * r) * a.d_v + tj * 4 + s, o[r][s]);
+        }
+        const float whole = tok[(C - 1) * TOK + 2];
+        __syncthreads();
+        for (int e = tid; e < C * NV; e += NT) { // rows of U weighted for the state
+            const float *d = tok + (e >> 5) * TOK;
+            Ut[(e >> 5) * LV + (e & 31)] *= d[3] * d[0];
+        }
+        __syncthreads();
+        if (4 * ti < a.d_k) {
+            float s[4][4] = {};
+            mm_tn<4>(s, Ut + tj * 4, LV, 1, kq + 4 * ti, ldk, C);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float *p = S + (tj * 4 + r) * ldk + 4 * ti;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    p[e] = fmaf(whole, p[e], s[r][e]);
+            }
+        }
+    }
+    __syncthreads();
+    if (!KEEP) {
+        if (Wf)
+            for (int e = tid; e < nv * a.d_k; e += NT)
+                Wf[st0 + e] = S[(e / a.d_k) * ldk + e % a.d_k];
+        for (size_t e = tid; e < (size_t)(a.L - len) * nv; e += NT) // no token, no answer
+            io<T>::store(y + ((size_t)bh * a.L + len + e / nv) * a.d_v + n0 + e % nv, 0.f);
+    }
+}
+
+// ---------------------------------------------------------- reverse walk
+template <typename T>
+__global__ void __launch_bounds__(NT)
+    gated_reverse_kernel(GatedArgs a, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ dy,
+                         const float *__restrict__ dWf, float *__restrict__ dW0, Ws ws) {
+    extern __shared__ __align__(16) float sm[];
+    const int ldk = a.d_k + 4, nC = (a.L + C - 1) / C;
+    float *D = sm, *kq = D + NV * ldk, *Tt = kq + 2 * C * ldk, *Mt = Tt + C * LC, *Yt = Mt + C * LC, *Ut = Yt + C * LV,
+          *tok = Ut + C * LV;
+    const int tid = threadIdx.x, ti = tid & 31, tj = tid >> 5, bh = blockIdx.y, n0 = blockIdx.x * NV;
+    const int b = bh / a.H, kh = b * a.Hk + (bh % a.H) / (a.H / a.Hk);
+    const int nv = min(NV, a.d_v - n0);
+    griddep_launch_dependents();
+    griddep_wait();
+    const int len = seq_len(a, b);
+    const size_t st0 = ((size_t)bh * a.d_v + n0) * a.d_k;
+    load_tile(D, ldk, dWf + st0, a.d_k, NV, dWf ? nv : 0, a.d_k, a.d_k);
+    for (int c = (len + C - 1) / C - 1; c >= 0; --c) {
+        const int n = min(C, len - c * C);
+        const size_t ch = (size_t)bh * nC + c, t0 = (size_t)c * C;
+        const size_t krow = ((size_t)kh * a.L + t0) * a.d_k, vrow = ((size_t)bh * a.L + t0) * a.d_v + n0;
+        __syncthreads();
+        load_tile(kq, ldk, k + krow, a.d_k, C, n, a.d_k, a.d_k);
+        load_tile(kq + C * ldk, ldk, q + krow, a.d_k, C, n, a.d_k, a.d_k);
+        load_tile(Tt, LC, ws.T + ch * C * C, C, C, C, C, C);
+        load_tile(Mt, LC, ws.M + ch * C * C, C, C, C, C, C);
+        load_tile(Yt, LV, dy + vrow, a.d_v, C, n, nv, NV);
+        for (int e = tid; e < C * TOK; e += NT)
+            tok[e] = __ldcg(ws.tok + ch * C * TOK + e);
+        __syncthreads();
+        for (int e = tid; e < nv * a.d_k; e += NT)
+            ws.dS[ch * a.d_v * a.d_k + (size_t)n0 * a.d_k + e] = D[(e / a.d_k) * ldk + e % a.d_k];
+        float u[2][4] = {};
+        mm_nt<2, 4>(u, kq + ti * ldk, ldk, 32, D + tj * 4 * ldk, ldk, 1, a.d_k);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float *d = tok + (ti + 32 * r) * TOK;
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                u[r][s] *= d[3] * d[0];
+        }
+        mm_tn<2>(u, Mt + ti, LC, 32, Yt + tj * 4, LV, C);
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            *reinterpret_cast<float4 *>(Ut + (ti + 32 * r) * LV + tj * 4) =
+                make_float4(u[r][0], u[r][1], u[r][2], u[r][3]);
+        __syncthreads();
+        float x[2][4] = {};
+        mm_tn<2>(x, Tt + ti, LC, 32, Ut + tj * 4, LV, C);
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int i = ti + 32 * r;
+            const float *d = tok + i * TOK;
+            if (tj * 4 < nv)
+                *reinterpret_cast<float4 *>(ws.dX + (ch * C + i) * a.d_v + n0 + tj * 4) =
+                    make_float4(x[r][0], x[r][1], x[r][2], x[r][3]);
+            const float wx = -d[6] * d[2] * d[0], wy = a.scale * d[2] * d[1];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                Ut[i * LV + tj * 4 + s] = wx * x[r][s];
+                Yt[i * LV + tj * 4 + s] *= wy;
+            }
+        }
+        const float whole = tok[(C - 1) * TOK + 2];
+        __syncthreads();
+        if (4 * ti < a.d_k) {
+            float s[4][4] = {};
+            mm_tn<4>(s, Ut + tj * 4, LV, 1, kq + 4 * ti, ldk, C);
+            mm_tn<4>(s, Yt + tj * 4, LV, 1, kq + C * ldk + 4 * ti, ldk, C);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float *p = D + (tj * 4 + r) * ldk + 4 * ti;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    p[e] = fmaf(whole, p[e], s[r][e]);
+            }
+        }
+    }
+    __syncthreads();
+    if (dW0)
+        for (int e = tid; e < nv * a.d_k; e += NT)
+            dW0[st0 + e] = D[(e / a.d_k) * ldk + e % a.d_k];
+}
+
+// ------------------------------------------------------------------ grad
+// One CTA per (chunk, key head); a warp owns 8 tokens (rows 8 w .. 8 w + 7)
+// and a lane 4 key channels, so every dot product over the key channels is
+// one warp reduction.
+template <typename T>
+__global__ void __launch_bounds__(NT)
+    gated_grad_kernel(GatedArgs a, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+                      const T *__restrict__ dy, T *__restrict__ dq, T *__restrict__ dk, T *__restrict__ dv,
+                      T *__restrict__ dg, T *__restrict__ dbeta, Ws ws) {
+    extern __shared__ __align__(16) float sm[];
+    const int ldk = a.d_k + 4, nC = gridDim.x, lv = NV + 4;
+    float *kt = sm, *qt = kt + C * ldk, *accq = qt + C * ldk, *acck = accq + C * a.d_k, *S0 = acck + C * a.d_k,
+          *S1 = S0 + NV * ldk, *Yt = S1 + NV * ldk, *Xt = Yt + C * lv, *Ut = Xt + C * lv, *Et = Ut + C * lv,
+          *Ft = Et + C * LC, *tok = Ft + C * LC, *red = tok + C * TOK; // red: dG [C], <S, dS'> per warp [8]
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, c = blockIdx.x, bk = blockIdx.y;
+    const int b = bk / a.Hk, grp = a.H / a.Hk, i0 = 8 * w, kc = 4 * lane;
+    const bool on = kc < a.d_k;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int n = min(C, seq_len(a, b) - c * C);
+    const size_t krow = ((size_t)bk * a.L + (size_t)c * C) * a.d_k;
+    const int rows = min(C, a.L - c * C); // rows that exist in memory
+    if (n <= 0) { // behind the sequence's end: no gradient
+        for (int e = tid; e < rows * a.d_k; e += NT) {
+            io<T>::store(dq + krow + e, 0.f);
+            io<T>::store(dk + krow + e, 0.f);
+        }
+        for (int m = 0; m < grp; ++m) {
+            const size_t r0 = (size_t)(bk * grp + m) * a.L + (size_t)c * C;
+            for (int e = tid; e < rows * a.d_v; e += NT)
+                io<T>::store(dv + r0 * a.d_v + e, 0.f);
+            for (int e = tid; e < rows; e += NT) {
+                io<T>::store(dg + r0 + e, 0.f);
+                io<T>::store(dbeta + r0 + e, 0.f);
+            }
+        }
+        return;
+    }
+    load_tile(kt, ldk, k + krow, a.d_k, C, n, a.d_k, a.d_k);
+    load_tile(qt, ldk, q + krow, a.d_k, C, n, a.d_k, a.d_k);
+    for (int m = 0; m < grp; ++m) {
+        const int bh = bk * grp + m;
+        const size_t ch = (size_t)bh * nC + c, r0 = (size_t)bh * a.L + (size_t)c * C;
+        __syncthreads();
+        for (int e = tid; e < C * TOK; e += NT)
+            tok[e] = __ldcg(ws.tok + ch * C * TOK + e);
+        __syncthreads();
+        if (m == 0) { // unit keys and queries (the same for every value head)
+            for (int e = tid; e < C * a.d_k; e += NT) {
+                const int i = e / a.d_k, x = i * ldk + e % a.d_k;
+                kt[x] *= tok[i * TOK];
+                qt[x] *= tok[i * TOK + 1];
+                accq[e] = acck[e] = 0.f;
+            }
+        }
+        float aq[8][4] = {}, ah[8][4] = {}, aw[8][4] = {}; // rows i0 + r, channels kc ..
+        float e_[4][4] = {}, f_[4][4] = {};               // E, F: rows (tid & 15) + 16 r, columns (tid >> 4) + 16 s
+        float xv[8] = {}, ss = 0.f;                        // dX_i . V_i (this lane's share), <S, dS'>
+        const int ei = tid & 15, ej = tid >> 4;
+        for (int n0 = 0; n0 < a.d_v; n0 += NV) {
+            const int nv = min(NV, a.d_v - n0);
+            __syncthreads();
+            load_tile(S0, ldk, ws.S + ch * a.d_v * a.d_k + (size_t)n0 * a.d_k, a.d_k, NV, nv, a.d_k, a.d_k);
+            load_tile(S1, ldk, ws.dS + ch * a.d_v * a.d_k + (size_t)n0 * a.d_k, a.d_k, NV, nv, a.d_k, a.d_k);
+            load_tile(Yt, lv, dy + r0 * a.d_v + n0, a.d_v, C, n, nv, NV);
+            load_tile(Xt, lv, ws.dX + ch * C * a.d_v + n0, a.d_v, C, n, nv, NV);
+            load_tile(Ut, lv, ws.U + ch * C * a.d_v + n0, a.d_v, C, n, nv, NV);
+            __syncthreads();
+            if (on) {
+                mm_nn<8>(aq, Yt + i0 * lv, lv, 1, S0 + kc, ldk, NV);
+                mm_nn<8>(ah, Xt + i0 * lv, lv, 1, S0 + kc, ldk, NV);
+                mm_nn<8>(aw, Ut + i0 * lv, lv, 1, S1 + kc, ldk, NV);
+            }
+            mm_nt<4, 4>(e_, Yt + ei * lv, lv, 16, Ut + ej * lv, lv, 16, NV);
+            mm_nt<4, 4>(f_, Xt + ei * lv, lv, 16, Ut + ej * lv, lv, 16, NV);
+            for (int e = tid; e < NV * a.d_k; e += NT) {
+                const int x = (e / a.d_k) * ldk + e % a.d_k;
+                ss = fmaf(S0[x], S1[x], ss);
+            }
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const int i = i0 + r;
+                if (i < n && lane < nv) {
+                    const size_t at = (r0 + i) * a.d_v + n0 + lane;
+                    const float x = Xt[i * lv + lane];
+                    xv[r] = fmaf(x, io<T>::load(v + at), xv[r]);
+                    io<T>::store(dv + at, tok[i * TOK + 6] * x);
+                }
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int i = ei + 16 * r, j = ej + 16 * s;
+                const float *di = tok + i * TOK, *dj = tok + j * TOK;
+                const float Dd = j <= i ? expf((di[4] - dj[4]) + (di[5] - dj[5])) : 0.f;
+                Et[i * LC + j] = j <= i ? a.scale * Dd * e_[r][s] : 0.f;
+                Ft[i * LC + j] = j < i ? Dd * f_[r][s] : 0.f;
+            }
+        ss = warp_sum(ss);
+        if (lane == 0)
+            red[C + w] = ss;
+        __syncthreads();
+        float last = 0.f; // what moves with the whole chunk's decay
+        if (on) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const float *d = tok + (i0 + r) * TOK;
+                const float4 kk = lds4(kt + (i0 + r) * ldk + kc);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    aq[r][e] *= a.scale * d[2];
+                    ah[r][e] *= d[2];
+                    aw[r][e] *= d[3];
+                }
+                last += aw[r][0] * kk.x + aw[r][1] * kk.y + aw[r][2] * kk.z + aw[r][3] * kk.w;
+            }
+            mm_nn<8>(aq, Et + i0 * LC, LC, 1, kt + kc, ldk, C);
+            mm_nn<8>(ah, Ft + i0 * LC, LC, 1, kt + kc, ldk, C);
+            mm_tn<8>(aw, Et + i0, LC, 1, qt + kc, ldk, C);
+        }
+        __syncthreads();
+        for (int e = tid; e < C * C; e += NT)
+            Ft[(e >> 6) * LC + (e & 63)] *= -tok[(e >> 6) * TOK + 6];
+        __syncthreads();
+        if (on)
+            mm_tn<8>(aw, Ft + i0, LC, 1, kt + kc, ldk, C);
+        last = warp_sum(last);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const int i = i0 + r;
+            const float be = tok[i * TOK + 6];
+            float qa = 0.f, kh = 0.f, kw = 0.f;
+            if (on) {
+                const float4 kk = lds4(kt + i * ldk + kc), qq = lds4(qt + i * ldk + kc);
+                qa = qq.x * aq[r][0] + qq.y * aq[r][1] + qq.z * aq[r][2] + qq.w * aq[r][3];
+                kh = kk.x * ah[r][0] + kk.y * ah[r][1] + kk.z * ah[r][2] + kk.w * ah[r][3];
+                kw = kk.x * aw[r][0] + kk.y * aw[r][1] + kk.z * aw[r][2] + kk.w * aw[r][3];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    accq[i * a.d_k + kc + e] += aq[r][e];
+                    acck[i * a.d_k + kc + e] += aw[r][e] - be * ah[r][e];
+                }
+            }
+            qa = warp_sum(qa);
+            kh = warp_sum(kh);
+            kw = warp_sum(kw);
+            const float xvs = warp_sum(xv[r]);
+            if (lane == 0) {
+                red[i] = qa - be * kh - kw;
+                if (i < n)
+                    io<T>::store(dbeta + r0 + i, xvs - kh);
+            }
+        }
+        if (lane == 0)
+            red[C + 8 + w] = last;
+        __syncthreads();
+        if (tid < 32) { // dg: the sums over later tokens, two a lane
+            float tail = 0.f;
+            for (int x = 0; x < 8; ++x)
+                tail += tok[(C - 1) * TOK + 2] * red[C + x] + red[C + 8 + x];
+            const float x1 = red[2 * lane + 1] + (lane == 31 ? tail : 0.f), x0 = red[2 * lane];
+            float run = x0 + x1;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float dn = __shfl_down_sync(0xffffffffu, run, o);
+                if (lane + o < 32)
+                    run += dn;
+            }
+            const float after = run - (x0 + x1);
+            if (2 * lane < n)
+                io<T>::store(dg + r0 + 2 * lane, run);
+            if (2 * lane + 1 < n)
+                io<T>::store(dg + r0 + 2 * lane + 1, after + x1);
+        }
+        for (int e = n * a.d_v + tid; e < rows * a.d_v; e += NT)
+            io<T>::store(dv + r0 * a.d_v + e, 0.f);
+        for (int i = n + tid; i < rows; i += NT) {
+            io<T>::store(dg + r0 + i, 0.f);
+            io<T>::store(dbeta + r0 + i, 0.f);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        const int i = i0 + r;
+        if (i >= rows)
+            break;
+        float4 kk = make_float4(0, 0, 0, 0), qq = kk, gk = kk, gq = kk;
+        if (on) {
+            kk = lds4(kt + i * ldk + kc);
+            qq = lds4(qt + i * ldk + kc);
+            gk = lds4(acck + i * a.d_k + kc);
+            gq = lds4(accq + i * a.d_k + kc);
+        }
+        float pk = 0.f, pq = 0.f;
+        if (a.l2norm) {
+            pk = warp_sum(kk.x * gk.x + kk.y * gk.y + kk.z * gk.z + kk.w * gk.w);
+            pq = warp_sum(qq.x * gq.x + qq.y * gq.y + qq.z * gq.z + qq.w * gq.w);
+        }
+        if (on) {
+            const float rk = i < n ? tok[i * TOK] : 0.f, rq = i < n ? tok[i * TOK + 1] : 0.f;
+            T *ok = dk + krow + (size_t)i * a.d_k + kc, *oq = dq + krow + (size_t)i * a.d_k + kc;
+            io<T>::store(ok, rk * (gk.x - kk.x * pk));
+            io<T>::store(ok + 1, rk * (gk.y - kk.y * pk));
+            io<T>::store(ok + 2, rk * (gk.z - kk.z * pk));
+            io<T>::store(ok + 3, rk * (gk.w - kk.w * pk));
+            io<T>::store(oq, rq * (gq.x - qq.x * pq));
+            io<T>::store(oq + 1, rq * (gq.y - qq.y * pq));
+            io<T>::store(oq + 2, rq * (gq.z - qq.z * pq));
+            io<T>::store(oq + 3, rq * (gq.w - qq.w * pq));
+        }
+    }
+}
+
+size_t prep_smem(int d_k) { return sizeof(float) * (2 * C * (d_k + 4) + 2 * C * LC + 1024 + C * TOK); }
+size_t walk_smem(int d_k) { return sizeof(float) * ((NV + 2 * C) * (d_k + 4) + 2 * C * LC + 2 * C * LV + C * TOK); }
+size_t grad_smem(int d_k) {
+    return sizeof(float) * (2 * (C + NV) * (d_k + 4) + 2 * C * d_k + 3 * C * (NV + 4) + 2 * C * LC + C * TOK + C + 16);
+}
+
+template <typename K> cudaError_t allow_smem(K *kern, size_t bytes) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <typename T>
+cudaError_t forward_t(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g, const void *beta,
+                      const float *W0, float *Wf, void *y, void *workspace, bool keep, bool backward, cudaStream_t st) {
+    const int BH = a.B * a.H, nC = (a.L + C - 1) / C;
+    const Ws ws = ws_at(workspace, ws_off(BH, a.L, a.d_k, a.d_v, backward));
+    cudaError_t e = allow_smem(gated_prep_kernel<T>, prep_smem(a.d_k));
+    if (e != cudaSuccess)
+        return e;
+    e = launch_pdl(gated_prep_kernel<T>, dim3(nC, BH), dim3(NT), prep_smem(a.d_k), st, a, (const T *)q, (const T *)k,
+                   (const T *)g, (const T *)beta, ws);
+    if (e != cudaSuccess)
+        return e;
+    auto *walk = keep ? gated_walk_kernel<T, true> : gated_walk_kernel<T, false>;
+    e = allow_smem(walk, walk_smem(a.d_k));
+    if (e != cudaSuccess)
+        return e;
+    return launch_pdl(walk, dim3((a.d_v + NV - 1) / NV, BH), dim3(NT), walk_smem(a.d_k), st, a, (const T *)q,
+                      (const T *)k, (const T *)v, W0, Wf, (T *)y, ws);
+}
+
+template <typename T>
+cudaError_t backward_t(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g,
+                       const void *beta, const float *W0, const void *dy, const float *dWf, void *dq, void *dk,
+                       void *dv, void *dg, void *dbeta, float *dW0, void *workspace, cudaStream_t st) {
+    const int BH = a.B * a.H, nC = (a.L + C - 1) / C;
+    const Ws ws = ws_at(workspace, ws_off(BH, a.L, a.d_k, a.d_v, true));
+    cudaError_t e = forward_t<T>(a, q, k, v, g, beta, W0, nullptr, nullptr, workspace, true, true, st);
+    if (e != cudaSuccess)
+        return e;
+    e = allow_smem(gated_reverse_kernel<T>, walk_smem(a.d_k));
+    if (e != cudaSuccess)
+        return e;
+    e = launch_pdl(gated_reverse_kernel<T>, dim3((a.d_v + NV - 1) / NV, BH), dim3(NT), walk_smem(a.d_k), st, a,
+                   (const T *)q, (const T *)k, (const T *)dy, dWf, dW0, ws);
+    if (e != cudaSuccess)
+        return e;
+    e = allow_smem(gated_grad_kernel<T>, grad_smem(a.d_k));
+    if (e != cudaSuccess)
+        return e;
+    return launch_pdl(gated_grad_kernel<T>, dim3(nC, a.B * a.Hk), dim3(NT), grad_smem(a.d_k), st, a, (const T *)q,
+                      (const T *)k, (const T *)v, (const T *)dy, (T *)dq, (T *)dk, (T *)dv, (T *)dg, (T *)dbeta, ws);
+}
+
+} // namespace
+
+size_t gated_forward_workspace_bytes(int B, int H, int L, int d_k, int d_v, int bf16) {
+    (void)bf16;
+    return sizeof(float) * ws_off(B * H, L, d_k, d_v, false).end;
+}
+size_t gated_backward_workspace_bytes(int B, int H, int L, int d_k, int d_v, int bf16) {
+    (void)bf16;
+    return sizeof(float) * ws_off(B * H, L, d_k, d_v, true).end;
+}
+
+cudaError_t launch_gated_forward(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g,
+                                 const void *beta, const float *W0, float *Wf, void *y, void *workspace, int bf16,
+                                 cudaStream_t st) {
+    return bf16 ? forward_t<__nv_bfloat16>(a, q, k, v, g, beta, W0, Wf, y, workspace, false, false, st)
+                : forward_t<float>(a, q, k, v, g, beta, W0, Wf, y, workspace, false, false, st);
+}
+
+cudaError_t launch_gated_backward(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g,
+                                  const void *beta, const float *W0, const void *dy, const float *dWf, void *dq,
+                                  void *dk, void *dv, void *dg, void *dbeta, float *dW0, void *workspace, int bf16,
+                                  cudaStream_t st) {
+    return bf16 ? backward_t<__nv_bfloat16>(a, q, k, v, g, beta, W0, dy, dWf, dq, dk, dv, dg, dbeta, dW0, workspace, st)
+                : backward_t<float>(a, q, k, v, g, beta, W0, dy, dWf, dq, dk, dv, dg, dbeta, dW0, workspace, st);
+}
+
+} // namespace fw

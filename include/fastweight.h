@@ -432,6 +432,119 @@ FW_API int fw_decode_stack_step(const fw_stack_layer *layers, int n_layers, cons
                                 float ln_eps, void *stream);
 
 /*
+ * The gated delta rule: the delta rule whose state decays before each write.
+ * Per value head, with a_t = exp(g_t):
+ *   W_t = a_t W_{t-1} + beta_t (v_t - a_t W_{t-1} k_t) outer k_t
+ *   y_t = scale W_t q_t                        (the read uses the updated W)
+ * g_t = 0 is the plain delta rule; g_t = -infinity (a_t = 0) forgets
+ * everything before token t.  Keys and queries come in feature space -- as
+ * fw_dpfp writes them, for instance -- and are used as they are (l2norm 0) or
+ * scaled to unit length, x / sqrt(sum x^2 + eps), inside the kernels
+ * (l2norm 1; a row of zeros stays zero, with eps 0 as well).
+ *
+ * Shared conventions of the three calls
+ *   q, k    : [B, Hk, L, d_k]   io_dtype
+ *   v, y    : [B, H, L, d_v]    io_dtype; value head h reads key head
+ *             h / (H / Hk); H must be a multiple of Hk
+ *   g       : [B, H, L]         io_dtype, the logarithm of the decay (<= 0 for
+ *             a decay; a positive g grows the state and may overflow it)
+ *   beta    : [B, H, L]         io_dtype
+ *   W*      : [B, H, d_v, d_k]  fp32
+ *   lengths : [B] int32 on the device, or NULL: sequence b ends after
+ *             lengths[b] tokens (clamped to 0 .. L).  What q, k, v, g, beta
+ *             and dy hold behind the end is not used, whatever it is; y and
+ *             the gradients are written as zero there.
+ *   d_k in {16, 32, 64, 128}; d_v a multiple of 16 up to 256; B H <= 65535.
+ * Calls return FW_ERR_INVALID_ARG for null, misaligned or missing pointers,
+ * bad sizes, a scale or eps that is not finite, eps < 0 or a small workspace,
+ * and FW_ERR_UNSUPPORTED for sizes outside the compiled set.  No call uses
+ * state of the library, so calls with workspaces of their own may run at the
+ * same time.  Results do not depend on the run (fixed summation orders).
+ */
+FW_API size_t fw_gated_delta_forward_workspace_size(int B, int Hk, int H, int L, int d_k, int d_v,
+                                                    int io_dtype);
+
+/*
+ * fw_gated_delta_forward -- the whole sequence, in chunks of 64 tokens.
+ *   W0      : initial state, or NULL for zeros
+ *   W_final : the state after each sequence's last token, or NULL to skip it;
+ *             W_final == W0 (in place) is allowed
+ *   workspace: device scratch of fw_gated_delta_forward_workspace_size()
+ *             bytes; contents on entry do not matter, garbage on return
+ * With L == 0 the final state is the initial one.
+ */
+FW_API int fw_gated_delta_forward(const void *q, const void *k, const void *v, const void *g, const void *beta,
+                                  const float *W0, float *W_final, void *y, const int32_t *lengths,
+                                  void *workspace, size_t workspace_bytes, int B, int Hk, int H, int L,
+                                  int d_k, int d_v, int l2norm, float scale, float eps, int io_dtype,
+                                  void *stream);
+
+FW_API size_t fw_gated_delta_backward_workspace_size(int B, int Hk, int H, int L, int d_k, int d_v,
+                                                     int io_dtype);
+
+/*
+ * fw_gated_delta_backward -- gradients of fw_gated_delta_forward from those
+ * of y and of the final state.
+ *   dy       : [B, H, L, d_v]  io_dtype, dL/dy
+ *   dW_final : dL/dW_final, or NULL for zeros
+ *   dq, dk (shaped as q, k; summed over the value heads that share a key
+ *   head), dv, dg, dbeta : io_dtype                          (written)
+ *   dW0      : dL/dW0, or NULL to skip it                    (written)
+ *   workspace: fw_gated_delta_backward_workspace_size() bytes
+ */
+FW_API int fw_gated_delta_backward(const void *q, const void *k, const void *v, const void *g,
+                                   const void *beta, const float *W0, const void *dy,
+                                   const float *dW_final, void *dq, void *dk, void *dv, void *dg,
+                                   void *dbeta, float *dW0, const int32_t *lengths, void *workspace,
+                                   size_t workspace_bytes, int B, int Hk, int H, int L, int d_k, int d_v,
+                                   int l2norm, float scale, float eps, int io_dtype, void *stream);
+
+/*
+ * fw_gated_delta_decode_step -- one new token per (batch, value head): q, k
+ * [B, Hk, d_k], v, y [B, H, d_v], g, beta [B, H], W read and written once.
+ */
+FW_API int fw_gated_delta_decode_step(const void *q, const void *k, const void *v, const void *g,
+                                      const void *beta, float *W, void *y, int B, int Hk, int H, int d_k,
+                                      int d_v, int l2norm, float scale, float eps, int io_dtype,
+                                      void *stream);
+
+typedef enum fw_act {
+    FW_ACT_NONE = 0,
+    FW_ACT_RELU = 1,
+    FW_ACT_SILU = 2, /* x sigmoid(x) */
+    FW_ACT_GELU = 3  /* x Phi(x), Phi the normal distribution function */
+} fw_act;
+
+/*
+ * fw_group_norm_act -- the heads' answers on their way to the output map: for
+ * each token, each head's d channels are normalised (a group norm with one
+ * group per head over channels-last rows), then the activation, or a gate's:
+ *   n = (x - mean) / sqrt(var + eps)  (the biased variance of the d channels)
+ *   z = n gamma + beta;   out = act(z), or z act(gate) with a gate
+ *   x           : [B, H, L, d]  io_dtype, head-major as the attention calls
+ *                 write it (L == 1: plain channels-last rows [B, H d])
+ *   gate        : [B, L, H d]   io_dtype, or NULL
+ *   gamma, beta : [H d]         fp32
+ *   out         : [B, L, H d]   io_dtype, token-major      (written)
+ *   d a multiple of 8 up to 256 (FW_ERR_UNSUPPORTED otherwise).
+ */
+FW_API int fw_group_norm_act(const void *x, const void *gate, const float *gamma, const float *beta, void *out,
+                             int B, int H, int L, int d, int act, int io_dtype, float eps, void *stream);
+
+FW_API size_t fw_group_norm_act_backward_workspace_size(int B, int H, int L, int d);
+
+/*
+ * fw_group_norm_act_backward -- gradients from dout [B, L, H d]: dx (shaped
+ * as x) and dgate (as gate; NULL exactly when gate is) in io_dtype, dgamma and
+ * dbeta [H d] fp32, summed over every token in a fixed order.  relu's
+ * derivative at 0 is 0.
+ */
+FW_API int fw_group_norm_act_backward(const void *x, const void *gate, const float *gamma, const float *beta,
+                                      const void *dout, void *dx, void *dgate, float *dgamma, float *dbeta,
+                                      void *workspace, size_t workspace_bytes, int B, int H, int L, int d,
+                                      int act, int io_dtype, float eps, void *stream);
+
+/*
  * fw_device_status -- waits for `stream`, then reports and clears the
  * device-side status word of the current device: FW_ERR_TIMEOUT if any
  * kernel of this library gave up a bounded wait (its outputs are then

@@ -1,0 +1,345 @@
+"""GPU parity of the gated delta rule (sequence, gradients, one token) against
+the fp64 oracle, and the calls its documentation allows.
+
+Tolerances, from the arithmetic.  fp32 I/O: sums of at most 256 products a
+term, 2^-24 each, so 2^-16 of the terms' sizes; the terms may cancel by a
+factor of four: 2^-14 of the largest value.  bf16 I/O: an operand that is not
+bf16 already may enter a product as two bf16 terms (2^-8 of it is left by the
+first, 2^-8 of that by the second: 2^-16); the state, X, T, U and one dropped
+product make 5 2^-16 of the terms' sizes, and with cancellation by three
+2^-12 of the largest value; gradients pass twice as many: 2^-11.  A bf16
+output is rounded once more, by at most 2^-8 of its own value.  dg is a
+difference: what the answers lose when the state decays less what the token
+itself wrote, so its terms are as large as dy.y of a token even where nothing
+is left (a first token without a state has dg = 0)."""
+import numpy as np
+import pytest
+import torch
+
+from delta_rule_linear_dpfp_gb300 import binding as fw
+from delta_rule_linear_dpfp_gb300 import build
+from oracle import gated
+from tests.parity_util import f64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    build.build()
+    fw.load()
+    yield
+    assert fw.fw_device_status() == fw.FW_OK
+
+
+def near(name, got, ref, grad=False, bf16=None, terms=0.0):
+    bf16 = got.dtype == torch.bfloat16 if bf16 is None else bf16
+    tol = (2.0 ** -11 if grad else 2.0 ** -12) if bf16 else 2.0 ** -14
+    ref = np.asarray(ref)
+    assert tuple(got.shape) == ref.shape, name
+    g = f64(got)
+    assert np.all(np.isfinite(g)), name
+    lim = tol * max(np.abs(ref).max() if ref.size else 0, terms, 1e-30)
+    if got.dtype == torch.bfloat16:
+        lim = lim + 2.0 ** -8 * np.abs(ref)
+    off = np.abs(g - ref)
+    assert np.all(off <= lim), (name, off.max(), np.abs(ref).max())
+
+
+def make(B, Hk, H, L, d_k, d_v, dtype, state, seed, keys="normal"):
+    r = torch.Generator().manual_seed(seed)
+    n = lambda *s: torch.randn(*s, generator=r)  # noqa: E731
+    d = dict(q=n(B, Hk, L, d_k), k=n(B, Hk, L, d_k), v=n(B, H, L, d_v),
+             g=-torch.rand(B, H, L, generator=r) * torch.exp(-4 * torch.rand(H, 1, generator=r)),
+             beta=torch.rand(B, H, L, generator=r))
+    if keys == "positive":   # strongly alike, as a feature map's are: T is far from the identity
+        d["k"] = d["k"].abs() / d_k ** 0.5
+        d["q"] = d["q"].abs() / d_k ** 0.5
+    d = {x: t.to(dtype) for x, t in d.items()}
+    d["W0"] = n(B, H, d_v, d_k) if state else None
+    return d
+
+
+def dev(d):
+    return {n: None if t is None else t.cuda() for n, t in d.items()}
+
+
+def host(d):
+    return {n: None if t is None else f64(t) for n, t in d.items()}
+
+
+# B, Hk, H, L, d_k, d_v, state, padded
+CASES = [
+    (1, 1, 1, 1, 16, 16, False, False),
+    (2, 1, 2, 2, 32, 48, True, False),
+    (1, 2, 2, 63, 64, 64, True, False),
+    (2, 1, 3, 64, 128, 32, False, False),
+    (1, 2, 4, 65, 64, 16, True, True),
+    (3, 2, 2, 130, 128, 128, True, True),
+    (1, 1, 1, 200, 16, 256, True, False),
+    (2, 2, 6, 257, 32, 80, False, True),
+    (1, 1, 2, 640, 128, 96, True, False),
+]
+
+
+def _lengths(B, L, seed):
+    r = np.random.default_rng(seed)
+    lens = r.integers(0, L + 1, B)
+    lens[0] = [L, L + 5, max(L - 1, 0)][seed % 3]       # past the end counts as the end
+    if B > 1:
+        lens[-1] = [0, -3, 1][seed % 3]                  # nothing at all
+    return lens
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "b{}k{}h{}l{}dk{}dv{}s{:d}p{:d}".format(*c))
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("l2norm", [True, False])
+def test_forward_and_gradients(case, dtype, l2norm):
+    B, Hk, H, L, d_k, d_v, state, padded = case
+    d = make(B, Hk, H, L, d_k, d_v, dtype, state, sum(case), "normal" if l2norm else "positive")
+    lens = _lengths(B, L, sum(case)) if padded else None
+    lt = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    x = dev(d)
+    if lens is not None:                                  # whatever lies behind the end is not used
+        for b, n in enumerate(lens):
+            for t in ("q", "k", "v", "g", "beta"):
+                x[t][b, :, max(int(n), 0):] = float("nan")
+    opt = dict(l2norm=l2norm, scale=0.6)
+    y, W = fw.fw_gated_delta_forward(**x, lengths=lt, **opt)
+    ref = host(d)
+    if lens is not None:                                  # (the oracle reads none of it either)
+        for b, n in enumerate(lens):
+            for t in ("q", "k", "v", "g", "beta"):
+                ref[t][b, :, max(int(n), 0):] = np.nan
+    yr, Wr = gated.gated_forward(**ref, lengths=lens, **opt)
+    bf16 = dtype == torch.bfloat16
+    near("y", y, yr)
+    near("W", W, Wr, bf16=bf16)
+    if lens is not None:
+        for b, n in enumerate(lens):
+            assert torch.all(y[b, :, max(int(n), 0):] == 0)
+
+    r = torch.Generator().manual_seed(1)
+    dy = torch.randn(B, H, L, d_v, generator=r).to(dtype)
+    dW = torch.randn(B, H, d_v, d_k, generator=r) if state else None
+    dyd = dy.cuda()
+    if lens is not None:
+        for b, n in enumerate(lens):
+            dyd[b, :, max(int(n), 0):] = float("inf")
+    got = fw.fw_gated_delta_backward(x["q"], x["k"], x["v"], x["g"], x["beta"], dyd, W0=x["W0"],
+                                     dW_final=None if dW is None else dW.cuda(), lengths=lt, **opt)
+    want = gated.gated_backward(ref["q"], ref["k"], ref["v"], ref["g"], ref["beta"], f64(dy), ref["W0"],
+                                None if dW is None else f64(dW), lengths=lens, **opt)
+    if lens is not None:                                  # zeros there, on both sides
+        want = list(want)
+        for w in want[:5]:
+            for b, n in enumerate(lens):
+                w[b, :, max(int(n), 0):] = 0
+    terms = np.abs(f64(dy) * yr).sum(-1).max()
+    for n, a, w in zip(("dq", "dk", "dv", "dg", "dbeta", "dW0"), got, want):
+        near(n, a, w, grad=True, bf16=bf16, terms=terms if n == "dg" else 0.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_strong_gates(dtype):
+    """Tokens that forget everything (-inf, and sums far past exp's range)
+    between others: no NaN, and the later tokens' decays keep their bits."""
+    d = make(2, 2, 2, 150, 64, 32, dtype, True, 7)
+    d["g"][:, :, 20] = -float("inf")
+    d["g"][:, 0, 70:75] = -90.0
+    d["g"][0, 1, 130] = -1e30
+    x = dev(d)
+    y, W = fw.fw_gated_delta_forward(**x)
+    yr, Wr = gated.gated_forward(**host(d))
+    near("y", y, yr)
+    near("W", W, Wr, bf16=dtype == torch.bfloat16)
+    dy = torch.randn(2, 2, 150, 32, generator=torch.Generator().manual_seed(2)).to(dtype)
+    got = fw.fw_gated_delta_backward(x["q"], x["k"], x["v"], x["g"], x["beta"], dy.cuda(), W0=x["W0"])
+    h = host(d)
+    want = gated.gated_backward(h["q"], h["k"], h["v"], h["g"], h["beta"], f64(dy), h["W0"])
+    for n, a, w in zip(("dq", "dk", "dv", "dg", "dbeta", "dW0"), got, want):
+        near(n, a, w, grad=True, bf16=dtype == torch.bfloat16)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_keys_of_zeros(eps):
+    d = make(1, 1, 2, 70, 32, 16, torch.bfloat16, True, 8)
+    d["k"][:, :, 3] = 0
+    d["q"][:, :, 66] = 0
+    x = dev(d)
+    y, W = fw.fw_gated_delta_forward(**x, eps=eps)
+    yr, Wr = gated.gated_forward(**host(d), eps=eps)
+    near("y", y, yr)
+    near("W", W, Wr, bf16=True)
+    assert torch.all(y[:, :, 66] == 0)
+    got = fw.fw_gated_delta_backward(x["q"], x["k"], x["v"], x["g"], x["beta"], torch.ones_like(x["v"]), W0=x["W0"], eps=eps)
+    assert all(torch.isfinite(t).all() for t in got)
+
+
+def test_a_nan_gate_is_not_hidden():
+    d = dev(make(1, 1, 2, 70, 32, 16, torch.bfloat16, True, 8))
+    d["g"][0, 0, 65] = float("nan")
+    y, _ = fw.fw_gated_delta_forward(**d)
+    assert torch.isfinite(y[0, 0, :64]).all() and torch.isnan(y[0, 0, 65:]).all() and torch.isfinite(y[0, 1]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("case", [(1, 1, 1, 16, 16), (3, 2, 4, 32, 48), (2, 1, 3, 64, 64), (5, 4, 4, 128, 256),
+                                  (2, 2, 2, 64, 208)], ids=str)
+def test_decode_is_the_sequence(case, dtype):
+    B, Hk, H, d_k, d_v = case
+    T = 5
+    d = make(B, Hk, H, T, d_k, d_v, dtype, True, sum(case))
+    x = dev(d)
+    W = x["W0"].clone()
+    ys = []
+    for t in range(T):
+        one = [x[n][:, :, t].clone() for n in ("q", "k", "v", "g", "beta")]
+        ys.append(fw.fw_gated_delta_decode_step(*one, W, scale=0.5))
+    yr, Wr = gated.gated_forward(**host(d), scale=0.5)
+    near("y", torch.stack(ys, 2), yr)
+    near("W", W, Wr, bf16=False)
+
+
+def test_decode_extremes():
+    d = make(2, 1, 2, 1, 64, 32, torch.bfloat16, True, 3)
+    d["g"][0] = -float("inf")
+    d["k"][1] = 0
+    one = {n: t[:, :, 0].contiguous().cuda() for n, t in d.items() if n != "W0"}
+    W = d["W0"].cuda()
+    y = fw.fw_gated_delta_decode_step(**one, W=W, eps=0.0)
+    yr, Wr = gated.gated_forward(**host(d), eps=0.0)
+    near("y", y, yr[:, :, 0])
+    near("W", W, Wr, bf16=False)
+
+
+def test_in_place_state_and_no_state():
+    d = dev(make(2, 2, 2, 100, 64, 48, torch.bfloat16, True, 9))
+    y, W = fw.fw_gated_delta_forward(**d)
+    W2 = d["W0"].clone()
+    y2, out = fw.fw_gated_delta_forward(**{**d, "W0": W2}, W_final=W2)
+    assert out is W2 and torch.equal(W, W2) and torch.equal(y, y2)
+    y3, none = fw.fw_gated_delta_forward(**d, return_state=False)
+    assert none is None and torch.equal(y, y3)
+
+
+def test_split_sequence_and_repeats():
+    """Two calls with the state passed on are one call; every repeat has the same bits."""
+    d = dev(make(2, 1, 2, 192, 128, 64, torch.bfloat16, True, 10))
+    y, W = fw.fw_gated_delta_forward(**d)
+    for _ in range(3):
+        y1, W1 = fw.fw_gated_delta_forward(**d)
+        assert torch.equal(y, y1) and torch.equal(W, W1)
+    a = {n: t[:, :, :128].contiguous() for n, t in d.items() if n != "W0"}
+    b = {n: t[:, :, 128:].contiguous() for n, t in d.items() if n != "W0"}
+    ya, Wa = fw.fw_gated_delta_forward(**a, W0=d["W0"])
+    yb, Wb = fw.fw_gated_delta_forward(**b, W0=Wa)
+    assert torch.equal(torch.cat([ya, yb], 2), y) and torch.equal(Wb, W)
+    dy = torch.randn_like(d["v"])
+    args = [d[n] for n in ("q", "k", "v", "g", "beta")]
+    first = fw.fw_gated_delta_backward(*args, dy, W0=d["W0"])
+    again = fw.fw_gated_delta_backward(*args, dy, W0=d["W0"])
+    assert all(torch.equal(s, t) for s, t in zip(first, again))
+
+
+@pytest.mark.parametrize("L", [0, 1])
+def test_empty(L):
+    d = dev(make(2, 1, 2, L, 32, 16, torch.bfloat16, True, 11))
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    y, W = fw.fw_gated_delta_forward(**d, lengths=lens)
+    assert torch.equal(W, d["W0"]) and torch.all(y == 0)
+    dW = torch.randn_like(d["W0"])
+    got = fw.fw_gated_delta_backward(*[d[n] for n in ("q", "k", "v", "g", "beta")], torch.ones_like(d["v"]), W0=d["W0"],
+                                     dW_final=dW, lengths=lens)
+    assert torch.equal(got[5], dW) and all(torch.all(t == 0) for t in got[:5])
+    e = {n: t[:0] for n, t in d.items()}
+    y, W = fw.fw_gated_delta_forward(**e)
+    assert y.shape[0] == 0 and W.shape[0] == 0
+
+
+def test_graphs_and_streams():
+    """Captured and replayed with new inputs, two graphs at once on two
+    streams, and a call on a stream that is not the current one."""
+    d = dev(make(2, 2, 2, 130, 64, 32, torch.bfloat16, True, 12))
+    e = dev(make(2, 2, 2, 130, 64, 32, torch.bfloat16, True, 13))
+    args = ("q", "k", "v", "g", "beta")
+
+    def both(x):
+        y, W = fw.fw_gated_delta_forward(**x)
+        return (y, W) + fw.fw_gated_delta_backward(*[x[n] for n in args], x["v"], W0=x["W0"])
+
+    want_d, want_e = both(d), both(e)
+    one = {n: t.clone() for n, t in d.items()}
+    two = {n: t.clone() for n, t in d.items()}
+    graphs = []
+    for x in (one, two):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = both(x)
+        graphs.append((g, out))
+    for n in one:
+        two[n].copy_(e[n])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(3):
+        for s, (g, _) in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for (_, out), want in zip(graphs, (want_d, want_e)):
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y, W = fw.fw_gated_delta_forward(**e, stream=s)
+    s.synchronize()
+    assert torch.equal(y, want_e[0]) and torch.equal(W, want_e[1])
+
+
+def test_refused_tensors():
+    d = dev(make(2, 1, 2, 20, 32, 16, torch.bfloat16, True, 14))
+    call = fw.fw_gated_delta_forward
+    for bad in (dict(q=d["q"].transpose(0, 1)), dict(k=d["k"][:, :, :19]), dict(g=d["g"].float()), dict(v=d["v"].cpu()),
+                dict(W0=d["W0"].bfloat16()), dict(W0=d["W0"][:1]), dict(v=d["v"][:, :1]), dict(beta=d["beta"][..., None])):
+        with pytest.raises(ValueError):
+            call(**{**d, **bad})
+    with pytest.raises(ValueError):
+        call(**d, lengths=torch.zeros(2, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError):
+        call(**d, y=torch.empty(2, 2, 20, 32, dtype=torch.bfloat16, device="cuda"))
+    three = dev(make(2, 2, 3, 20, 32, 16, torch.bfloat16, True, 14))
+    with pytest.raises(ValueError):
+        call(**three)
+    odd = dev(make(2, 1, 2, 20, 32, 24, torch.bfloat16, True, 14))
+    with pytest.raises(fw.FwError) as err:
+        call(**odd)
+    assert err.value.code == fw.FW_ERR_UNSUPPORTED
+    with pytest.raises(fw.FwError):
+        call(**d, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    buf = torch.empty(2 * 1 * 20 * 32 + 8, dtype=torch.bfloat16, device="cuda")[1:1 + 2 * 20 * 32].view(2, 1, 20, 32)
+    with pytest.raises(fw.FwError):
+        call(**{**d, "q": buf})
+
+
+def test_gradients_are_the_differences():
+    """Central differences of the fp32 forward along random directions.  The
+    loss is summed in 64 bits; y's error of 2^-14 of its size over a step of
+    2^-6 leaves 2^-7 of the slope's scale."""
+    d = dev(make(1, 1, 2, 90, 32, 32, torch.float32, True, 15))
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda t: torch.randn(t.shape, generator=gen, device="cuda")  # noqa: E731
+    dy, dW = rnd(d["v"]), rnd(d["W0"])
+    got = dict(zip(("q", "k", "v", "g", "beta", "W0"),
+                   fw.fw_gated_delta_backward(*[d[n] for n in ("q", "k", "v", "g", "beta")], dy, W0=d["W0"], dW_final=dW)))
+
+    def loss(x):
+        y, W = fw.fw_gated_delta_forward(**x)
+        return float((y.double() * dy).sum() + (W.double() * dW).sum())
+
+    for n in d:
+        way = torch.sign(got[n])                          # the steepest of the box: a large slope
+        step = 2.0 ** -8 * float(d[n].abs().mean())
+        diff = (loss({**d, n: d[n] + step * way}) - loss({**d, n: d[n] - step * way})) / (2 * step)
+        slope = float((got[n].double() * way).sum())
+        assert abs(diff - slope) <= 2.0 ** -6 * abs(slope), (n, diff, slope)
