@@ -36,6 +36,7 @@
 // gradients of shared heads have a fixed order).
 #include "fw_common.cuh"
 #include "fw_gated.h"
+#include "fw_gated_tc.h"
 
 #include <algorithm>
 
@@ -766,7 +767,10 @@ cudaError_t backward_t(const GatedArgs &a, const void *q, const void *k, const v
 } // namespace
 
 size_t gated_forward_workspace_bytes(int B, int H, int L, int d_k, int d_v, int bf16) {
-    (void)bf16;
+    if (bf16) {
+        const GatedRecord r = gated_forward_record(L, d_k, d_v);
+        return (size_t)B * H * r.nch * r.bytes;
+    }
     return sizeof(float) * ws_off(B * H, L, d_k, d_v, false).end;
 }
 size_t gated_backward_workspace_bytes(int B, int H, int L, int d_k, int d_v, int bf16) {
@@ -777,7 +781,7 @@ size_t gated_backward_workspace_bytes(int B, int H, int L, int d_k, int d_v, int
 cudaError_t launch_gated_forward(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g,
                                  const void *beta, const float *W0, float *Wf, void *y, void *workspace, int bf16,
                                  cudaStream_t st) {
-    return bf16 ? forward_t<__nv_bfloat16>(a, q, k, v, g, beta, W0, Wf, y, workspace, false, false, st)
+    return bf16 ? gated_tc_forward(a, q, k, v, g, beta, W0, Wf, y, workspace, st)
                 : forward_t<float>(a, q, k, v, g, beta, W0, Wf, y, workspace, false, false, st);
 }
 
