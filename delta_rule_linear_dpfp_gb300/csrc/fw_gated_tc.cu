@@ -71,58 +71,114 @@ FW_DEV void widen8(uint4 u, float (&o)[8]) {
 // terms, swizzled as the descriptors of fw_tc.cuh expect.  16-byte chunk c.
 FW_DEV uint32_t pair_chunk(int row, int c) { return (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)); }
 
+// 16 fp32 channels of a row in a "piece" (rows of 64 bytes, the base rows of
+// the walk): 16-byte chunk c, placed so that eight rows in a row of lanes meet
+// eight different bank groups.
+FW_DEV uint32_t piece_chunk(int row, int c) { return (uint32_t)(row * 64 + ((c ^ ((row >> 1) & 3)) << 4)); }
+
+// Sums kept as an unevaluated pair of floats (hi + lo, 48 bits).
+struct Pair {
+    float hi, lo;
+};
+FW_DEV Pair add(Pair a, Pair b) { // two-sum of the highs, the lows added to what it left
+    const float s = a.hi + b.hi, t = s - a.hi;
+    const float e = ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo);
+    const float h = s + e;
+    return {h, e - (h - s)};
+}
+
 // (I + A)^-1 of the strictly lower triangular A (row stride LC): forward
 // substitution in the four 16 x 16 diagonal blocks, one thread a column, then
-// two doublings T21 = -T22 (A21 T11).
+// two doublings T21 = -T22 (A21 T11), four columns a thread.
+template <int H> FW_DEV void double_inverse(const float *A, float *T, float *tmp) {
+    constexpr int Q = H / 4, N = (C / (2 * H)) * H * Q; // float4 outputs of all pairs of blocks
+    const int tid = threadIdx.x, p = tid / (H * Q), i = (tid / Q) % H, j = (tid % Q) * 4, r0 = p * 2 * H;
+    const float *a = A + (r0 + H + i) * LC + r0, *t11 = T + r0 * LC + r0 + j;
+    if (tid < N) {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int m = 0; m < H; m += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(a + m);
+            const float fm[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 t = *reinterpret_cast<const float4 *>(t11 + (m + e) * LC);
+                s.x = fmaf(fm[e], t.x, s.x);
+                s.y = fmaf(fm[e], t.y, s.y);
+                s.z = fmaf(fm[e], t.z, s.z);
+                s.w = fmaf(fm[e], t.w, s.w);
+            }
+        }
+        *reinterpret_cast<float4 *>(tmp + (p * H + i) * H + j) = s;
+    }
+    __syncthreads();
+    const float *t22 = T + (r0 + H + i) * LC + r0 + H, *u = tmp + p * H * H + j;
+    if (tid < N) {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int m = 0; m < H; m += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(t22 + m);
+            const float fm[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 t = *reinterpret_cast<const float4 *>(u + (m + e) * H);
+                s.x = fmaf(-fm[e], t.x, s.x);
+                s.y = fmaf(-fm[e], t.y, s.y);
+                s.z = fmaf(-fm[e], t.z, s.z);
+                s.w = fmaf(-fm[e], t.w, s.w);
+            }
+        }
+        *reinterpret_cast<float4 *>(T + (r0 + H + i) * LC + r0 + j) = s;
+    }
+    __syncthreads();
+}
+
 FW_DEV void unit_lower_inverse(const float *A, float *T, float *tmp) {
     const int tid = threadIdx.x;
-    for (int e = tid; e < C * C; e += NT)
-        if ((e >> 6) >> 4 < (e & 63) >> 4)
-            T[(e >> 6) * LC + (e & 63)] = 0.f;
+    for (int e = tid; e < C * C / 4; e += NT) {
+        const int r = e >> 4, c4 = (e & 15) * 4;
+        if (r >> 4 < c4 >> 4)
+            *reinterpret_cast<float4 *>(T + r * LC + c4) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     if (tid < C) {
         const int b0 = tid & ~15, j = tid & 15;
+        const float *Ab = A + b0 * LC + b0;
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            float s = i == j ? 1.f : 0.f;
+            float s = i == j ? 1.f : 0.f, s2 = 0.f;
 #pragma unroll
-            for (int m = 0; m < i; ++m)
-                s = fmaf(-A[(b0 + i) * LC + b0 + m], x[m], s);
-            x[i] = s;
-            T[(b0 + i) * LC + b0 + j] = s;
+            for (int m = 0; m < i; m += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(Ab + i * LC + m);
+                s = fmaf(-f.x, x[m], s);
+                if (m + 1 < i)
+                    s2 = fmaf(-f.y, x[m + 1], s2);
+                if (m + 2 < i)
+                    s = fmaf(-f.z, x[m + 2], s);
+                if (m + 3 < i)
+                    s2 = fmaf(-f.w, x[m + 3], s2);
+            }
+            x[i] = s + s2;
+            T[(b0 + i) * LC + b0 + j] = x[i];
         }
     }
     __syncthreads();
-#pragma unroll
-    for (int h = 16; h <= 32; h *= 2) {
-        const int per = h * h, n = (C / (2 * h)) * per;
-        for (int e = tid; e < n; e += NT) {
-            const int p = e / per, i = (e % per) / h, j = e % h, r0 = p * 2 * h;
-            float s = 0.f;
-#pragma unroll 8
-            for (int m = 0; m < h; ++m)
-                s = fmaf(A[(r0 + h + i) * LC + r0 + m], T[(r0 + m) * LC + r0 + j], s);
-            tmp[p * per + i * h + j] = s;
-        }
-        __syncthreads();
-        for (int e = tid; e < n; e += NT) {
-            const int p = e / per, i = (e % per) / h, j = e % h, r0 = p * 2 * h;
-            float s = 0.f;
-#pragma unroll 8
-            for (int m = 0; m < h; ++m)
-                s = fmaf(T[(r0 + h + i) * LC + r0 + h + m], tmp[p * per + m * h + j], s);
-            T[(r0 + h + i) * LC + r0 + j] = -s;
-        }
-        __syncthreads();
-    }
+    double_inverse<16>(A, T, tmp);
+    double_inverse<32>(A, T, tmp);
 }
 
+// A descriptor `bytes` further into its tile.
+FW_DEV uint64_t at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
+
 // ------------------------------------------------------------------ prep
-// One CTA per (chunk, value head).  Shared memory: the [K; Q] tile (K-major,
-// 128 rows; its first 64 rows also serve as the MN-major K), an operand
-// region (M and T as hi and lo tiles, then the stacked 128 x 64 matrices A1
-// and A2 in turn), the fp32 A / T work space (A's place is V's, then dY's,
-// once the inverse is done), per-token scalars.
+// One CTA per (chunk, value head), two to an SM.  Shared memory: the [K; Q]
+// tile (K-major, 128 rows; its first 64 rows also serve as the MN-major K),
+// an operand region (M and T as hi and lo tiles, then the stacked 128 x 64
+// matrices A1 and A2 in turn), the fp32 A / T work space (A's place is V's,
+// then dY's, later), per-token scalars.  What a product leaves goes back
+// through shared memory, from the operand region on, and out in bulk copies:
+// a row per lane stored directly costs a sector for every 16 bytes (measured:
+// 4400 of 37 000 cycles a chunk).
 struct PrepSmem {
     uint32_t kq, op, at, tt, tok, bar, bytes;
 };
@@ -138,17 +194,20 @@ __host__ __device__ inline PrepSmem prep_smem(int nkb, int nvb) {
     s.bytes = s.bar + 64 + 1024;
     return s;
 }
+constexpr uint32_t kStage = 65536; // bytes staged at once from the operand region on
+static_assert(32768 + C * LC * 8 + 4096 >= kStage, "op, at and tt hold a staged 64 KB");
 
-template <bool BWD>
+template <bool BWD, int NKB>
 __global__ void __launch_bounds__(NT, 2)
     gated_tc_prep_kernel(GatedArgs a, const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ k,
                          const __nv_bfloat16 *__restrict__ v, const __nv_bfloat16 *__restrict__ g,
                          const __nv_bfloat16 *__restrict__ beta, const __nv_bfloat16 *__restrict__ dy, uint8_t *ws,
                          GatedRecord rec, int tmem_cols, unsigned *status) {
+    constexpr int DKP = 64 * NKB;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int nkb = rec.nkb, dkp = 64 * nkb, nvb = (a.d_v + 63) / 64;
-    const PrepSmem o = prep_smem(nkb, nvb);
+    const int nvb = (a.d_v + 63) / 64;
+    const PrepSmem o = prep_smem(NKB, nvb);
     uint8_t *kq = sm + o.kq, *op = sm + o.op, *vt = sm + o.at;
     float *At = reinterpret_cast<float *>(sm + o.at), *tmp = At + C * LC, *Tt = reinterpret_cast<float *>(sm + o.tt);
     float *tok = reinterpret_cast<float *>(sm + o.tok); // per token: G hi, G lo, rk, beta, rq, e^G, e^{G_C-G}, -
@@ -162,75 +221,74 @@ __global__ void __launch_bounds__(NT, 2)
         griddep_launch_dependents();
         return;
     }
-    if (w == 0)
+    if (w == 0) {
         tmem_alloc(slot, (uint32_t)tmem_cols);
+        tmem_relinquish(); // or no second CTA is placed on the SM
+    }
     if (tid == 32) {
         mbar_init(bar, 1);
         fence_barrier_init();
     }
     // [K; Q], 16 bytes a thread and step; the row's lanes add its squares
     {
+        constexpr int PER = DKP / 8, STEPS = 2 * C * PER / NT; // chunks per row; 4 or 8 steps
         const __nv_bfloat16 *kg = k + ((size_t)kh * a.L + (size_t)c * C) * a.d_k;
         const __nv_bfloat16 *qg = q + ((size_t)kh * a.L + (size_t)c * C) * a.d_k;
-        const int per = dkp / 8, steps = 2 * C * per / NT; // chunks per row; 4 or 8 steps
-        const int ch = tid % per;
-        uint4 u[8];
+        const int ch = tid % PER;
+        uint4 u[STEPS];
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
-            const int row = (s * NT + tid) / per;
+        for (int s = 0; s < STEPS; ++s) {
+            const int row = (s * NT + tid) / PER;
             u[s] = make_uint4(0, 0, 0, 0);
-            if (s < steps && (row & 63) < n && ch * 8 < a.d_k)
+            if ((row & 63) < n && ch * 8 < a.d_k)
                 u[s] = __ldcg(reinterpret_cast<const uint4 *>((row < C ? kg : qg) + (size_t)(row & 63) * a.d_k) + ch);
         }
+        if (w == 1) { // the running sums of g, two tokens a lane
+            const size_t t0 = (size_t)bh * a.L + (size_t)c * C;
+            float x[2], be[2];
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
-            if (s >= steps)
-                break;
-            const int row = (s * NT + tid) / per;
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * lane + e;
+                x[e] = i < n ? io<__nv_bfloat16>::load(g + t0 + i) : 0.f;
+                x[e] = x[e] < kGMin ? kGMin : x[e];
+                be[e] = i < n ? io<__nv_bfloat16>::load(beta + t0 + i) : 0.f;
+            }
+            Pair run = add({x[0], 0.f}, {x[1], 0.f});
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const Pair up = {__shfl_up_sync(0xffffffffu, run.hi, m), __shfl_up_sync(0xffffffffu, run.lo, m)};
+                if (lane >= m)
+                    run = add(up, run);
+            }
+            const Pair all = {__shfl_sync(0xffffffffu, run.hi, 31), __shfl_sync(0xffffffffu, run.lo, 31)};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const Pair G = e ? run : add(run, {-x[1], 0.f});
+                float *d = tok + (2 * lane + e) * 8;
+                d[0] = G.hi;
+                d[1] = G.lo;
+                d[3] = be[e];
+                d[5] = expf(G.hi);
+                d[6] = expf((all.hi - G.hi) + (all.lo - G.lo));
+                d[7] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int row = (s * NT + tid) / PER;
             *reinterpret_cast<uint4 *>(kq + kmajor_chunk(row, ch * 8, 128)) = u[s];
             float x[8], ss = 0.f;
             widen8(u[s], x);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 ss = fmaf(x[e], x[e], ss);
-            for (int m = per / 2; m > 0; m >>= 1)
+#pragma unroll
+            for (int m = PER / 2; m > 0; m >>= 1)
                 ss += __shfl_xor_sync(0xffffffffu, ss, m);
             if (ch == 0) {
                 ss += a.eps;
                 tok[(row & 63) * 8 + (row < C ? 2 : 4)] = !a.l2norm ? 1.f : ss > 0.f ? 1.f / sqrtf(ss) : ss;
             }
-        }
-    }
-    if (w == 1) { // the running sums of g in 64 bits, two tokens a lane
-        const size_t t0 = (size_t)bh * a.L + (size_t)c * C;
-        double s[2];
-        float be[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int i = 2 * lane + e;
-            const float x = i < n ? io<__nv_bfloat16>::load(g + t0 + i) : 0.f;
-            s[e] = x < kGMin ? kGMin : x;
-            be[e] = i < n ? io<__nv_bfloat16>::load(beta + t0 + i) : 0.f;
-        }
-        s[1] += s[0];
-        double run = s[1];
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const double up = __shfl_up_sync(0xffffffffu, run, m);
-            if (lane >= m)
-                run += up;
-        }
-        const double before = run - s[1], all = __shfl_sync(0xffffffffu, run, 31);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const double G = before + s[e];
-            float *d = tok + (2 * lane + e) * 8;
-            d[0] = (float)G;
-            d[1] = (float)(G - (double)(float)G);
-            d[3] = be[e];
-            d[5] = expf((float)G);
-            d[6] = expf((float)(all - G));
-            d[7] = 0.f;
         }
     }
     fence_async_smem();
@@ -254,20 +312,23 @@ __global__ void __launch_bounds__(NT, 2)
         __syncthreads();
         tc_fence_after();
     };
-    const uint32_t kq_s = smem_u32(kq), op_s = smem_u32(op), vt_s = smem_u32(vt);
+    const uint64_t dKmaj = desc_sw128(smem_u32(kq), 16, 1024), dKmn = desc_sw128(smem_u32(kq), 16384, 1024);
+    const uint64_t dOp = desc_sw128(smem_u32(op), 16, 1024), dOpMn = desc_sw128(smem_u32(op), 8192, 1024);
+    const uint64_t dV = desc_sw128(smem_u32(vt), 8192, 1024);
     uint8_t *out = ws + rec.off(bh, c);
     if (tid == 0) { // K K^T (rows 0-63) and Q K^T
-        const uint32_t id = idesc_bf16(128, 64, 0, 0);
-        for (int s = 0; s < 4 * nkb; ++s) {
-            const uint64_t d = desc_sw128(kq_s + kmajor_step(s, 128), 16, 1024);
-            mma_bf16(tGram, d, d, id, s > 0);
+#pragma unroll
+        for (int s = 0; s < 4 * NKB; ++s) {
+            const uint64_t d = at(dKmaj, kmajor_step(s, 128));
+            mma_bf16(tGram, d, d, idesc_bf16(128, 64, 0, 0), s > 0);
         }
         mma_commit(bar);
         // the K (and Q) image for the walk, straight from the tile
         if (BWD) {
-            bulk_s2g(out + rec.KQ, kq, (uint32_t)nkb * 16384u);
+            bulk_s2g(out + rec.KQ, kq, (uint32_t)NKB * 16384u);
         } else {
-            for (int kb = 0; kb < nkb; ++kb)
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb)
                 bulk_s2g(out + rec.K + kb * 8192, kq + kb * 16384, 8192);
         }
         bulk_commit();
@@ -288,7 +349,7 @@ __global__ void __launch_bounds__(NT, 2)
                 const int j = j0 + e;
                 const float4 dj = *reinterpret_cast<const float4 *>(tok + j * 8);
                 const bool in = rr < C ? j < i : j <= i;
-                x[e] = in ? fi * dj.z * x[e] * expf((di.x - dj.x) + (di.y - dj.y)) : 0.f;
+                x[e] = in ? fi * dj.z * x[e] * __expf((di.x - dj.x) + (di.y - dj.y)) : 0.f;
             }
             if (rr < C) {
 #pragma unroll
@@ -299,113 +360,102 @@ __global__ void __launch_bounds__(NT, 2)
                 for (int e = 0; e < 16; e += 8) {
                     uint4 hi, lo;
                     split8(x + e, hi, lo);
-                    const uint32_t at = kmajor_chunk(i, j0 + e, 64);
-                    *reinterpret_cast<uint4 *>(op + at) = hi;
-                    *reinterpret_cast<uint4 *>(op + 8192 + at) = lo;
+                    const uint32_t to = kmajor_chunk(i, j0 + e, 64);
+                    *reinterpret_cast<uint4 *>(op + to) = hi;
+                    *reinterpret_cast<uint4 *>(op + 8192 + to) = lo;
                 }
             }
         }
     }
     __syncthreads();
     unit_lower_inverse(At, Tt, tmp);
+#pragma unroll
     for (int e = tid; e < C * 8; e += NT) { // T as hi and lo tiles
         const int r = e >> 3, j0 = (e & 7) * 8;
+        float x[8];
+#pragma unroll
+        for (int m = 0; m < 8; m += 4) {
+            const float4 t = *reinterpret_cast<const float4 *>(Tt + r * LC + j0 + m);
+            x[m] = t.x;
+            x[m + 1] = t.y;
+            x[m + 2] = t.z;
+            x[m + 3] = t.w;
+        }
         uint4 hi, lo;
-        split8(Tt + r * LC + j0, hi, lo);
-        const uint32_t at = kmajor_chunk(r, j0, 64);
-        *reinterpret_cast<uint4 *>(op + 16384 + at) = hi;
-        *reinterpret_cast<uint4 *>(op + 24576 + at) = lo;
+        split8(x, hi, lo);
+        const uint32_t to = kmajor_chunk(r, j0, 64);
+        *reinterpret_cast<uint4 *>(op + 16384 + to) = hi;
+        *reinterpret_cast<uint4 *>(op + 24576 + to) = lo;
     }
     hand_over();
     if (tid == 0) { // M T, or (M T)^T = T^T M^T
-        for (int t = 0; t < 3; ++t) { // hi hi, hi lo, lo hi
-            const uint32_t m = op_s + (t == 2 ? 8192u : 0u), tt = op_s + 16384u + (t == 1 ? 8192u : 0u);
+#pragma unroll
+        for (int t = 0; t < 3; ++t) // hi hi, hi lo, lo hi
+#pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const uint64_t dm = desc_sw128(m + kmajor_step(s, 64), 16, 1024);
-                const uint64_t dt = desc_sw128(tt + (uint32_t)s * 2048u, 8192, 1024);
+                const uint64_t dm = at(dOp, (t == 2 ? 8192u : 0u) + kmajor_step(s, 64));
+                const uint64_t dt = at(dOpMn, 16384u + (t == 1 ? 8192u : 0u) + (uint32_t)s * 2048u);
                 if (BWD)
                     mma_bf16(tMT, dt, dm, idesc_bf16(128, 64, 1, 0), (t | s) != 0);
                 else
                     mma_bf16(tMT, dm, dt, idesc_bf16(128, 64, 0, 1), (t | s) != 0);
             }
-        }
         mma_commit(bar);
     }
-    auto load_rows = [&](const __nv_bfloat16 *src) { // V or dY, MN-major 64-channel blocks
-        const __nv_bfloat16 *sg = src + ((size_t)bh * a.L + (size_t)c * C) * a.d_v;
-        for (int e = tid; e < C * nvb * 8; e += NT) {
-            const int r = e / (nvb * 8), ch = e % (nvb * 8);
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (r < n && ch * 8 < a.d_v)
-                u = __ldcg(reinterpret_cast<const uint4 *>(sg + (size_t)r * a.d_v) + ch);
-            *reinterpret_cast<uint4 *>(vt + kmajor_chunk(r, ch * 8, 64)) = u;
-        }
-    };
-    load_rows(v);
     finish();
     // Stacked left factors, hi tile then lo tile: rows 0-63 from T, rows
     // 64-127 from MT (TMEM lanes 0-63, so the warps that can read those
-    // lanes write the lower rows) or, for W", from T^T.
-    auto put = [&](int row, int j0, const float *x) {
+    // lanes hold the lower rows) or, for W", from T^T.
+    auto factor = [&](bool first, float (&x)[32]) {
+        if (rr >= C || (BWD && first)) {
 #pragma unroll
-        for (int e = 0; e < 16; e += 8) {
-            uint4 hi, lo;
-            split8(x + e, hi, lo);
-            const uint32_t at = kmajor_chunk(row, j0 + e, 128);
-            *reinterpret_cast<uint4 *>(op + at) = hi;
-            *reinterpret_cast<uint4 *>(op + 16384 + at) = lo;
-        }
-    };
-    auto build = [&](bool first) {
+            for (int e = 0; e < 32; ++e) {
+                const int j = 32 * half + e;
+                const float *d = tok + j * 8;
+                x[e] = rr >= C ? Tt[i * LC + j] * (first ? -d[3] * d[5] * d[2] : d[3]) : Tt[j * LC + i] * d[6] * d[2];
+            }
+        } else {
+            tmem_ld16(tMT + tmem_lane_base(w) + (uint32_t)(32 * half), x);
+            tmem_ld16(tMT + tmem_lane_base(w) + (uint32_t)(32 * half + 16), x + 16);
+            tmem_ld_wait();
+            if (!BWD) {
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            const int j0 = 32 * half + 16 * p;
-            float x[16];
-            if (rr >= C) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float *d = tok + (j0 + e) * 8;
-                    x[e] = Tt[i * LC + j0 + e] * (first ? -d[3] * d[5] * d[2] : d[3]);
-                }
-            } else if (BWD && first) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float *d = tok + (j0 + e) * 8;
-                    x[e] = Tt[(j0 + e) * LC + i] * d[6] * d[2];
-                }
-            } else {
-                tmem_ld16(tMT + tmem_lane_base(w) + (uint32_t)j0, x);
-                tmem_ld_wait();
-                if (!BWD) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float *d = tok + (j0 + e) * 8;
-                        x[e] *= first ? -d[3] * d[5] * d[2] : d[3];
-                    }
+                for (int e = 0; e < 32; ++e) {
+                    const float *d = tok + (32 * half + e) * 8;
+                    x[e] *= first ? -d[3] * d[5] * d[2] : d[3];
                 }
             }
-            put(rr ^ 64, j0, x);
         }
     };
-    auto multiply = [&](uint32_t d, uint32_t bsrc, uint32_t lbo, int N) {
+    auto put = [&](const float (&x)[32]) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+            uint4 hi, lo;
+            split8(x + e, hi, lo);
+            const uint32_t to = kmajor_chunk(rr ^ 64, 32 * half + e, 128);
+            *reinterpret_cast<uint4 *>(op + to) = hi;
+            *reinterpret_cast<uint4 *>(op + 16384 + to) = lo;
+        }
+    };
+    auto multiply = [&](uint32_t d, uint64_t db, uint32_t id) {
         if (tid == 0) {
-            const uint32_t id = idesc_bf16(128, N, 0, 1);
+#pragma unroll
             for (int t = 0; t < 2; ++t)
+#pragma unroll
                 for (int s = 0; s < 4; ++s)
-                    mma_bf16(d, desc_sw128(op_s + (uint32_t)t * 16384u + (uint32_t)s * 32u, 16, 1024),
-                             desc_sw128(bsrc + (uint32_t)s * 2048u, lbo, 1024), id, (t | s) != 0);
+                    mma_bf16(d, at(dOp, (uint32_t)(t * 16384 + s * 32)), at(db, (uint32_t)s * 2048u), id, (t | s) != 0);
             mma_commit(bar);
         }
     };
-    build(true);
+    float x2[32];
+    factor(true, x2);
+    put(x2);
     hand_over();
-    multiply(tA1, kq_s, 16384, dkp); // [-W'; ...] or [-W'; W"]
+    multiply(tA1, dKmn, idesc_bf16(128, DKP, 0, 1)); // [-W'; ...] or [-W'; W"]
+    factor(false, x2); // A2's rows wait in registers: A1's image takes the place of T
     finish();
-    build(false);
-    hand_over();
-    multiply(tA2, vt_s, 8192, a.d_v);
-    // meanwhile the first product's rows as hi and lo images
-    for (int p = half; p < dkp / 16; p += 2) {
+    __syncthreads();
+    for (int p = half; p < DKP / 16; p += 2) { // the product's rows as hi and lo images
         const int c0 = 16 * p;
         float x[16];
         tmem_ld16(tA1 + tmem_lane_base(w) + (uint32_t)c0, x);
@@ -425,17 +475,10 @@ __global__ void __launch_bounds__(NT, 2)
         for (int e = 0; e < 16; e += 8) {
             uint4 hi, lo;
             split8(x + e, hi, lo);
-            uint8_t *to;
-            size_t lo_at;
-            if (BWD) {
-                to = out + (rr < C ? rec.AF : rec.AR) + kmajor_chunk(i, c0 + e, 64);
-                lo_at = (size_t)nkb * 8192;
-            } else {
-                to = out + rec.A + kmajor_chunk(rr, c0 + e, 128);
-                lo_at = (size_t)nkb * 16384;
-            }
+            uint8_t *to = BWD ? op + (rr < C ? 0 : NKB * 16384) + kmajor_chunk(i, c0 + e, 64)
+                              : op + kmajor_chunk(rr, c0 + e, 128);
             *reinterpret_cast<uint4 *>(to) = hi;
-            *reinterpret_cast<uint4 *>(to + lo_at) = lo;
+            *reinterpret_cast<uint4 *>(to + NKB * (BWD ? 8192 : 16384)) = lo;
         }
     }
     if (tid < C) { // the walks' scalars
@@ -455,87 +498,121 @@ __global__ void __launch_bounds__(NT, 2)
             st[1] = reinterpret_cast<const float4 *>(d)[1];
         }
     }
+    auto ship = [&](size_t to, const uint8_t *from, uint32_t bytes) { // staged bytes out; their place is free after
+        fence_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        if (tid == 0) {
+            bulk_s2g(out + to, from, bytes);
+            bulk_commit();
+            bulk_wait_read();
+        }
+        __syncthreads();
+        tc_fence_after();
+    };
+    ship(BWD ? rec.AF : rec.A, op, (uint32_t)NKB * 32768u);
+    put(x2);
+    auto load_rows = [&](const __nv_bfloat16 *src) { // V or dY, MN-major 64-channel blocks
+        const __nv_bfloat16 *sg = src + ((size_t)bh * a.L + (size_t)c * C) * a.d_v;
+        for (int e = tid; e < C * nvb * 8; e += NT) {
+            const int r = e / (nvb * 8), ch = e % (nvb * 8);
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (r < n && ch * 8 < a.d_v)
+                u = __ldcg(reinterpret_cast<const uint4 *>(sg + (size_t)r * a.d_v) + ch);
+            *reinterpret_cast<uint4 *>(vt + kmajor_chunk(r, ch * 8, 64)) = u;
+        }
+    };
+    load_rows(v);
+    hand_over();
+    const uint32_t idv = idesc_bf16(128, a.d_v, 0, 1);
+    multiply(tA2, dV, idv);
     finish();
-    auto rows_out = [&](size_t base, int rows, int row, bool on) { // [slice][rows][32] fp32
-        for (int p = half; p < a.d_v / 16; p += 2) {
-            float x[16];
-            tmem_ld16(tA2 + tmem_lane_base(w) + (uint32_t)(16 * p), x);
-            tmem_ld_wait();
-            if (on) {
-                float4 *to = reinterpret_cast<float4 *>(out + base) + ((size_t)(p >> 1) * rows + row) * 8 + (p & 1) * 4;
+    // rows [r0, r0 + R) of the product as pieces [16 channels][R rows][16] fp32, `most` channels at a time
+    auto rows_out = [&](size_t to, int R, int r0, uint8_t *place, int most) {
+        for (int d0 = 0; d0 < a.d_v; d0 += most) {
+            const int np = min(most, a.d_v - d0) / 16;
+            for (int p = half; p < np; p += 2) {
+                float x[16];
+                tmem_ld16(tA2 + tmem_lane_base(w) + (uint32_t)(d0 + 16 * p), x);
+                tmem_ld_wait();
+                if (rr >= r0 && rr < r0 + R) {
+                    uint8_t *s = place + (size_t)p * R * 64;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    to[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<float4 *>(s + piece_chunk(rr - r0, e)) =
+                            make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+                }
             }
+            ship(to + (size_t)d0 * R * 4, place, (uint32_t)(np * R * 64));
         }
     };
     if (!BWD) {
-        rows_out(rec.base, 128, rr, true);
+        __syncthreads();
+        rows_out(rec.base, 128, 0, op, (int)kStage / 512);
     } else {
-        rows_out(rec.baseU, C, i, rr < C);
-        load_rows(dy); // V's place
+        rows_out(rec.baseU, C, 0, kq, NKB * 64); // (K and Q left with the first copies: ship() waited for all)
+        load_rows(dy);                          // V's place
         hand_over();
-        multiply(tA2, vt_s, 8192, a.d_v);
+        multiply(tA2, dV, idv);
         finish();
-        rows_out(rec.baseX, C, i, rr >= C);
+        __syncthreads();
+        rows_out(rec.baseX, C, C, op, (int)kStage / 256);
     }
     if (tid == 0)
         bulk_wait_all();
     tc_fence_before();
     __syncthreads();
-    if (w == 0) {
-        tmem_relinquish();
+    if (w == 0)
         tmem_dealloc(tm, (uint32_t)tmem_cols);
-    }
 }
 
 // ------------------------------------------------------------------ walk
-// One CTA per (value head, 32 value channels); thread (row 32 (w % 4) + lane,
-// 16 channels) holds 16 values of the state (row = key channel) and handles
-// 16 values of a token's row between the products.  Two records are in
-// flight; the values' base rows and dY are read a chunk ahead.
+// One CTA per (value head, 32 value channels).  Eight worker warps: thread
+// (row 32 (w % 4) + lane, 16 channels) holds 16 values of the state (row =
+// key channel) and handles 16 values of a token's row between the products.
+// A ninth warp's first lane asks for the records (two in flight) and issues
+// the MMAs, so that none of that is on a worker's path (measured: issuing
+// from a worker took 1500 of a chunk's 5900 cycles).  Workers tell it by two
+// mbarriers that the state's or the values' tile is written; its commits tell
+// them that a product is done.
 enum { kFwd = 0, kKeep = 1, kRev = 2 };
+constexpr int kWalkThreads = NT + 32;
 
-struct WalkSmem {
-    uint32_t b, scal, rec, z, u, bar, bytes; // b, scal: offsets inside a record
+template <int MODE, int NKB> struct Walk {
+    static constexpr int R = MODE == kFwd ? 128 : 64;  // rows of the A tile and of the base rows
+    static constexpr int RB = MODE == kRev ? 128 : 64; // tokens the B^T tile holds
+    static constexpr uint32_t A = NKB * R * 256, B = NKB * RB * 128, SCAL = MODE == kRev ? 1024 : 512;
+    static constexpr uint32_t b = A, scal = b + B, base = scal + 1024, rec = base + R * 128;
+    // A 128-row MMA reads 8 KB past a tile of 64 rows and a product of one
+    // 64-wide block reads one more: what follows in this order covers both.
+    static constexpr uint32_t z = 2 * rec, u = z + NKB * 8192, bar = u + RB * 128, bytes = bar + 64 + 1024;
+    static_assert(rec + b + B + (NKB == 1 ? B : 0) <= bar && bytes <= 232448, "reads stay inside shared memory");
 };
-template <int MODE> __host__ __device__ inline WalkSmem walk_smem(int nkb) {
-    WalkSmem s;
-    s.b = (uint32_t)nkb * (MODE == kFwd ? 32768 : 16384);
-    s.scal = s.b + (uint32_t)nkb * (MODE == kRev ? 16384 : 8192);
-    s.rec = s.scal + 1024;
-    s.z = 2 * s.rec;
-    s.u = s.z + (uint32_t)nkb * 8192;
-    s.bar = s.u + (MODE == kRev ? 16384 : 8192);
-    // a 128-row MMA reads 8 KB past a tile of 64 rows: into what follows, or into this slack
-    s.bytes = s.bar + 64 + 8192 + 1024;
-    return s;
-}
 
-template <int MODE>
-__global__ void __launch_bounds__(NT)
+template <int MODE, int NKB>
+__global__ void __launch_bounds__(kWalkThreads)
     gated_tc_walk_kernel(GatedArgs a, const __nv_bfloat16 *__restrict__ dy, const float *__restrict__ Z0,
                          float *__restrict__ Zf, __nv_bfloat16 *__restrict__ y, uint8_t *ws, GatedRecord rec,
                          unsigned *status) {
+    using L = Walk<MODE, NKB>;
+    constexpr int DKP = 64 * NKB;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int nkb = rec.nkb, dkp = 64 * nkb;
-    const WalkSmem o = walk_smem<MODE>(nkb);
-    uint8_t *zt = sm + o.z, *ut = sm + o.u;
-    uint64_t *full = reinterpret_cast<uint64_t *>(sm + o.bar), *m1 = full + 2, *m2 = full + 3;
-    uint32_t *slot = reinterpret_cast<uint32_t *>(full + 4);
+    uint8_t *zt = sm + L::z, *ut = sm + L::u;
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::bar), *m1 = full + 2, *m2 = full + 3, *zr = full + 4,
+             *ur = full + 5;
+    uint32_t *slot = reinterpret_cast<uint32_t *>(full + 6);
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, sl = blockIdx.x, bh = blockIdx.y, n0 = sl * NV;
     const int b = bh / a.H;
-    const int rr = 32 * (w & 3) + lane, hf = w >> 2, i = rr & 63;
-    const bool mine = n0 + 16 * hf < a.d_v; // these 16 channels exist (d_v is a multiple of 16)
-    const bool zrow = 32 * (w & 3) < dkp;   // this warp holds rows of the state
     griddep_wait();
     const int len = seq_len(a, b), nch = (len + C - 1) / C;
-    if (w == 0)
+    if (w == 0) {
         tmem_alloc(slot, 128);
+        tmem_relinquish();
+    }
     if (tid == 32) {
-        for (int e = 0; e < 4; ++e)
-            mbar_init(full + e, 1);
+        for (int e = 0; e < 6; ++e)
+            mbar_init(full + e, e < 4 ? 1 : NT / 32);
         fence_barrier_init();
     }
     tc_fence_before();
@@ -544,199 +621,207 @@ __global__ void __launch_bounds__(NT)
     griddep_launch_dependents();
     const uint32_t tm = *slot, tD1 = tm, tD2 = tm + 64;
     auto chunk_of = [&](int it) { return MODE == kRev ? nch - 1 - it : it; };
-    auto fetch = [&](int it) { // thread 0: a chunk's record
-        const uint8_t *src = ws + rec.off(bh, chunk_of(it));
-        uint8_t *dst = sm + (it & 1) * o.rec;
-        uint64_t *f = full + (it & 1);
-        if (MODE == kFwd) { // A, K and the scalars are one piece
-            const uint32_t bytes = (uint32_t)nkb * 40960u + 512u;
-            mbar_arrive_expect_tx(f, bytes);
-            bulk_g2s(dst, src + rec.A, bytes, f);
-        } else if (MODE == kKeep) {
-            mbar_arrive_expect_tx(f, (uint32_t)nkb * 24576u + 512u);
-            bulk_g2s(dst, src + rec.AF, (uint32_t)nkb * 16384u, f);
-            for (int kb = 0; kb < nkb; ++kb)
-                bulk_g2s(dst + o.b + kb * 8192, src + rec.KQ + kb * 16384, 8192, f);
-            bulk_g2s(dst + o.scal, src + rec.scalF, 512, f);
-        } else {
-            mbar_arrive_expect_tx(f, (uint32_t)nkb * 32768u + 1024u);
-            bulk_g2s(dst, src + rec.AR, (uint32_t)nkb * 16384u, f);
-            bulk_g2s(dst + o.b, src + rec.KQ, (uint32_t)nkb * 16384u, f);
-            bulk_g2s(dst + o.scal, src + rec.scalR, 1024, f);
-        }
-    };
-    float z[16], next[16]; // the state's rows; the next chunk's base row (or dY row)
-    auto ahead = [&](int it) {
-        const int c = chunk_of(it);
-        const uint8_t *r = ws + rec.off(bh, c);
-        if (MODE == kRev && rr >= C) {
-            const int n = min(C, len - c * C);
-#pragma unroll
-            for (int e = 0; e < 16; e += 8) {
-                float x[8] = {};
-                if (mine && i < n)
-                    load8(dy + ((size_t)bh * a.L + (size_t)c * C + i) * a.d_v + n0 + 16 * hf + e, x);
-#pragma unroll
-                for (int m = 0; m < 8; ++m)
-                    next[e + m] = x[m];
-            }
-            return;
-        }
-        const size_t base = MODE == kFwd ? rec.base : MODE == kKeep ? rec.baseU : rec.baseX;
-        const int rows = MODE == kFwd ? 128 : C;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (mine && rr < rows)
-                x = __ldcg(reinterpret_cast<const float4 *>(r + base) + ((size_t)sl * rows + rr) * 8 + hf * 4 + e);
-            next[4 * e] = x.x;
-            next[4 * e + 1] = x.y;
-            next[4 * e + 2] = x.z;
-            next[4 * e + 3] = x.w;
-        }
-    };
-    auto put = [&](uint8_t *tile, int row, const float *x) { // 16 channels of a pair tile's row
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            uint4 hi, lo;
-            split8(x + 8 * e, hi, lo);
-            *reinterpret_cast<uint4 *>(tile + pair_chunk(row, 2 * hf + e)) = hi;
-            *reinterpret_cast<uint4 *>(tile + pair_chunk(row, 4 + 2 * hf + e)) = lo;
-        }
-    };
-    if (tid == 0)
-        for (int it = 0; it < min(2, nch); ++it)
-            fetch(it);
-    if (nch > 0)
-        ahead(0);
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-        z[e] = Z0 && mine && rr < a.d_k
-                   ? __ldcg(Z0 + ((size_t)bh * a.d_v + n0 + 16 * hf + e) * a.d_k + rr)
-                   : 0.f;
-    if (zrow)
-        put(zt, rr, z);
     bool ok = true;
-    const uint32_t zt_s = smem_u32(zt), ut_s = smem_u32(ut);
-    for (int it = 0; it < nch; ++it) {
-        const int c = chunk_of(it), n = min(C, len - c * C);
-        uint8_t *r = sm + (it & 1) * o.rec;
-        const uint32_t r_s = smem_u32(r);
-        uint8_t *gr = ws + rec.off(bh, c);
-        fence_async_smem();
-        tc_fence_before();
-        __syncthreads();
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (ok)
-            ok = mbar_wait(full + (it & 1), (it >> 1) & 1, status);
-        if (tid == 0 && ok) {
-            tc_fence_after();
-            constexpr int R = MODE == kFwd ? 128 : 64; // rows of the A tile
-            for (int t = 0; t < 2; ++t) // hi rows times [Z hi | Z lo], lo rows times Z hi
-                for (int s = 0; s < 4 * nkb; ++s)
-                    mma_bf16(tD1, desc_sw128(r_s + (uint32_t)(t * nkb * R * 128) + kmajor_step(s, R), 16, 1024),
-                             desc_sw128(zt_s + (uint32_t)s * 2048u, 8192, 1024), idesc_bf16(128, t ? 32 : 64, 0, 1),
-                             (t | s) != 0);
-            mma_commit(m1);
-        }
-        if (MODE != kFwd && tid == 32) { // the state before this chunk, as it lies
-            bulk_s2g(gr + (MODE == kKeep ? rec.S : rec.dS) + (size_t)sl * dkp * 128, zt, (uint32_t)dkp * 128u);
-            bulk_commit();
-        }
-        const float *scal = reinterpret_cast<const float *>(r + o.scal);
-        const float whole = scal[MODE == kRev ? 2 * C : C];
-        float x[16], t0[16], t1[16];
-        if (MODE == kRev && rr >= C) { // dY's rows do not wait for the product
-            const float f = scal[C + i];
+            ok = mbar_wait(bar, parity, status);
+    };
+    if (w == NT / 32) {
+        if (lane == 0 && nch > 0) {
+            const uint32_t pieces = (uint32_t)min(2, (a.d_v - n0) / 16);
+            auto fetch = [&](int it) { // a chunk's record
+                const uint8_t *src = ws + rec.off(bh, chunk_of(it));
+                uint8_t *dst = sm + (it & 1) * L::rec;
+                uint64_t *f = full + (it & 1);
+                const uint32_t base = pieces * L::R * 64;
+                mbar_arrive_expect_tx(f, L::A + L::B + L::SCAL + base);
+                if (MODE == kFwd) { // A, K and the scalars are one piece
+                    bulk_g2s(dst, src + rec.A, L::A + L::B + L::SCAL, f);
+                } else {
+                    bulk_g2s(dst, src + (MODE == kKeep ? rec.AF : rec.AR), L::A, f);
+                    if (MODE == kKeep) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                x[e] = f * next[e];
-            put(ut, rr, x);
-        }
-        if (ok)
-            ok = mbar_wait(m1, it & 1, status);
-        tc_fence_after();
-        if (MODE == kFwd || rr < C) {
-            tmem_ld16(tD1 + tmem_lane_base(w) + (uint32_t)(16 * hf), t0);
-            tmem_ld16(tD1 + tmem_lane_base(w) + (uint32_t)(32 + 16 * hf), t1);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                x[e] = next[e] + (t0[e] + t1[e]);
-            if (rr < C) {
-                const float f = scal[i];
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    t0[e] = f * x[e];
-                put(ut, i, t0);
-            }
-        }
-        if (MODE != kFwd && tid == 32)
-            bulk_wait_read(); // the stored state has left its tile
-        fence_async_smem();
-        tc_fence_before();
-        __syncthreads();
-        if (tid == 0 && ok) {
-            tc_fence_after();
-            constexpr int R = MODE == kRev ? 128 : 64; // rows of the B^T tile
-            for (int s = 0; s < R / 16; ++s)
-                mma_bf16(tD2, desc_sw128(r_s + o.b + (uint32_t)s * 2048u, R * 128, 1024),
-                         desc_sw128(ut_s + (uint32_t)s * 2048u, 8192, 1024), idesc_bf16(128, 64, 1, 1), s > 0);
-            mma_commit(m2);
-        }
-        if (MODE == kFwd && rr >= C) {
-            if (mine && i < n) {
-                uint4 *to = reinterpret_cast<uint4 *>(y + ((size_t)bh * a.L + (size_t)c * C + i) * a.d_v + n0 + 16 * hf);
-                float p[8];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                    for (int m = 0; m < 8; ++m)
-                        p[m] = x[8 * e + m];
-                    store8(reinterpret_cast<__nv_bfloat16 *>(to + e), p);
+                        for (int kb = 0; kb < NKB; ++kb)
+                            bulk_g2s(dst + L::b + kb * 8192, src + rec.KQ + kb * 16384, 8192, f);
+                    } else {
+                        bulk_g2s(dst + L::b, src + rec.KQ, L::B, f);
+                    }
+                    bulk_g2s(dst + L::scal, src + (MODE == kKeep ? rec.scalF : rec.scalR), L::SCAL, f);
                 }
-            }
-        } else if (MODE != kFwd && rr < C) { // U, or dX, for the gradients: a pair tile's row
-            put(gr + (MODE == kKeep ? rec.U : rec.dX) + (size_t)sl * 8192, i, x);
-        }
-        if (it + 1 < nch)
-            ahead(it + 1);
-        if (ok)
-            ok = mbar_wait(m2, it & 1, status);
-        tc_fence_after();
-        if (tid == 0 && ok && it + 2 < nch)
-            fetch(it + 2);
-        if (zrow) {
-            tmem_ld16(tD2 + tmem_lane_base(w) + (uint32_t)(16 * hf), t0);
-            tmem_ld16(tD2 + tmem_lane_base(w) + (uint32_t)(32 + 16 * hf), t1);
-            tmem_ld_wait();
+                bulk_g2s(dst + L::base,
+                         src + (MODE == kFwd ? rec.base : MODE == kKeep ? rec.baseU : rec.baseX) + (size_t)sl * L::R * 128,
+                         base, f);
+            };
+            fetch(0);
+            if (nch > 1)
+                fetch(1);
+            const uint64_t dz = desc_sw128(smem_u32(zt), 8192, 1024), du = desc_sw128(smem_u32(ut), 8192, 1024);
+            const uint64_t dA0 = desc_sw128(smem_u32(sm), 16, 1024);
+            const uint64_t dB0 = desc_sw128(smem_u32(sm + L::b), L::RB * 128, 1024);
+            for (int it = 0; it < nch && ok; ++it) {
+                const uint64_t dA = at(dA0, (uint32_t)(it & 1) * L::rec), dB = at(dB0, (uint32_t)(it & 1) * L::rec);
+                wait(full + (it & 1), (it >> 1) & 1);
+                wait(zr, it & 1);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                // hi rows times [Z hi | Z lo], lo rows times Z hi
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                z[e] = fmaf(whole, z[e], t0[e] + t1[e]);
-            put(zt, rr, z);
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int s = 0; s < 4 * NKB; ++s)
+                        mma_bf16(tD1, at(dA, (uint32_t)(t * NKB * L::R * 128) + kmajor_step(s, L::R)),
+                                 at(dz, (uint32_t)s * 2048u), idesc_bf16(128, t ? 32 : 64, 0, 1), (t | s) != 0);
+                mma_commit(m1);
+                if (MODE != kFwd) { // the state before this chunk, as it lies
+                    bulk_s2g(ws + rec.off(bh, chunk_of(it)) + (MODE == kKeep ? rec.S : rec.dS) + (size_t)sl * DKP * 128, zt,
+                             (uint32_t)DKP * 128u);
+                    bulk_commit();
+                }
+                if (it > 0 && it + 1 < nch)
+                    fetch(it + 1); // the workers are through with the previous chunk
+                wait(ur, it & 1);
+                if (!ok)
+                    break;
+                if (MODE != kFwd)
+                    bulk_wait_read(); // the stored state has left its tile
+                tc_fence_after();
+#pragma unroll
+                for (int s = 0; s < L::RB / 16; ++s)
+                    mma_bf16(tD2, at(dB, (uint32_t)s * 2048u), at(du, (uint32_t)s * 2048u), idesc_bf16(128, 64, 1, 1),
+                             s > 0);
+                mma_commit(m2);
+            }
+            if (MODE != kFwd)
+                bulk_wait_all();
+            if (!ok) // a wait gave up: let the records that were asked for land first
+                for (int e = 0; e < 2; ++e)
+                    (void)mbar_wait(full + e, 0, status);
         }
-    }
-    if (Zf && mine && rr < a.d_k)
+        __syncwarp();
+    } else {
+        const int rr = 32 * (w & 3) + lane, hf = w >> 2, i = rr & 63;
+        const bool mine = n0 + 16 * hf < a.d_v; // these 16 channels exist (d_v is a multiple of 16)
+        const bool zrow = 32 * (w & 3) < DKP;   // this warp holds rows of the state
+        const bool values = MODE == kFwd || rr < C; // and of the values
+        const uint32_t lb = tmem_lane_base(w) + (uint32_t)(16 * hf);
+        float z[16], x[16], t0[16], t1[16];
+        uint4 ahead[2]; // kRev: dY's row of the next chunk
+        auto read_dy = [&](int it) {
+            const int c = chunk_of(it);
+            const bool in = mine && i < min(C, len - c * C);
+            const uint4 *from = reinterpret_cast<const uint4 *>(
+                dy + ((size_t)bh * a.L + (size_t)c * C + (in ? i : 0)) * a.d_v + (in ? n0 + 16 * hf : 0));
+            ahead[0] = in ? __ldcg(from) : make_uint4(0, 0, 0, 0);
+            ahead[1] = in ? __ldcg(from + 1) : make_uint4(0, 0, 0, 0);
+        };
+        auto put = [&](uint8_t *tile, int row, const float *v) { // 16 channels of a pair tile's row
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                uint4 hi, lo;
+                split8(v + 8 * e, hi, lo);
+                *reinterpret_cast<uint4 *>(tile + pair_chunk(row, 2 * hf + e)) = hi;
+                *reinterpret_cast<uint4 *>(tile + pair_chunk(row, 4 + 2 * hf + e)) = lo;
+            }
+        };
+        auto written = [&](uint64_t *bar) { // this warp's rows of a tile are written, its TMEM reads done
+            fence_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar);
+        };
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-            Zf[((size_t)bh * a.d_v + n0 + 16 * hf + e) * a.d_k + rr] = z[e];
-    if (MODE == kFwd) { // no token, no answer
-        const int nv = min(NV, a.d_v - n0);
-        const size_t c8 = nv / 8, cnt = (size_t)(a.L - len) * c8;
-        for (size_t e = tid; e < cnt; e += NT)
-            *reinterpret_cast<uint4 *>(y + ((size_t)bh * a.L + len + e / c8) * a.d_v + n0 + 8 * (e % c8)) =
-                make_uint4(0, 0, 0, 0);
+            z[e] = Z0 && mine && rr < a.d_k ? __ldcg(Z0 + ((size_t)bh * a.d_v + n0 + 16 * hf + e) * a.d_k + rr) : 0.f;
+        if (zrow)
+            put(zt, rr, z);
+        written(zr);
+        if (MODE == kRev && rr >= C && nch > 0)
+            read_dy(0);
+        for (int it = 0; it < nch; ++it) {
+            const int c = chunk_of(it), n = min(C, len - c * C);
+            const uint8_t *r = sm + (it & 1) * L::rec;
+            uint8_t *gr = ws + rec.off(bh, c);
+            wait(full + (it & 1), (it >> 1) & 1);
+            const float *scal = reinterpret_cast<const float *>(r + L::scal);
+            const float whole = scal[MODE == kRev ? 2 * C : C], f = scal[MODE == kRev && rr >= C ? C + i : i];
+            if (MODE == kRev && rr >= C) { // dY's rows do not wait for the product
+                widen8(ahead[0], reinterpret_cast<float(&)[8]>(x[0]));
+                widen8(ahead[1], reinterpret_cast<float(&)[8]>(x[8]));
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    x[e] *= f;
+                put(ut, rr, x);
+                if (it + 1 < nch)
+                    read_dy(it + 1);
+            }
+            if (values) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (mine)
+                        v = *reinterpret_cast<const float4 *>(r + L::base + hf * (L::R * 64) + piece_chunk(rr, e));
+                    x[4 * e] = v.x;
+                    x[4 * e + 1] = v.y;
+                    x[4 * e + 2] = v.z;
+                    x[4 * e + 3] = v.w;
+                }
+            }
+            wait(m1, it & 1);
+            tc_fence_after();
+            if (values) {
+                tmem_ld16(tD1 + lb, t0);
+                tmem_ld16(tD1 + lb + 32u, t1);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    x[e] += t0[e] + t1[e];
+                if (rr < C) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        t0[e] = f * x[e];
+                    put(ut, i, t0);
+                }
+            }
+            written(ur);
+            if (MODE == kFwd && rr >= C) {
+                if (mine && i < n) {
+                    __nv_bfloat16 *to = y + ((size_t)bh * a.L + (size_t)c * C + i) * a.d_v + n0 + 16 * hf;
+                    store8(to, reinterpret_cast<float(&)[8]>(x[0]));
+                    store8(to + 8, reinterpret_cast<float(&)[8]>(x[8]));
+                }
+            } else if (MODE != kFwd && rr < C) { // U, or dX, for the gradients: a pair tile's row
+                put(gr + (MODE == kKeep ? rec.U : rec.dX) + (size_t)sl * 8192, i, x);
+            }
+            wait(m2, it & 1);
+            tc_fence_after();
+            if (zrow) {
+                tmem_ld16(tD2 + lb, t0);
+                tmem_ld16(tD2 + lb + 32u, t1);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    z[e] = fmaf(whole, z[e], t0[e] + t1[e]);
+                put(zt, rr, z);
+            }
+            written(zr);
+        }
+        if (Zf && mine && rr < a.d_k)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                Zf[((size_t)bh * a.d_v + n0 + 16 * hf + e) * a.d_k + rr] = z[e];
+        if (MODE == kFwd) { // no token, no answer
+            const size_t c8 = min(NV, a.d_v - n0) / 8, cnt = (size_t)(a.L - len) * c8;
+            for (size_t e = tid; e < cnt; e += NT)
+                *reinterpret_cast<uint4 *>(y + ((size_t)bh * a.L + len + e / c8) * a.d_v + n0 + 8 * (e % c8)) =
+                    make_uint4(0, 0, 0, 0);
+        }
     }
-    if (!ok && tid == 0) // a wait gave up: let the records that were asked for land first
-        for (int e = 0; e < 2; ++e)
-            (void)mbar_wait(full + e, 0, status);
-    if (MODE != kFwd && tid == 32)
-        bulk_wait_all();
     tc_fence_before();
     __syncthreads();
-    if (w == 0) {
-        tmem_relinquish();
+    if (w == 0)
         tmem_dealloc(tm, 128);
-    }
 }
 
 template <typename K> cudaError_t allow_smem(K *kern, size_t bytes) {
@@ -746,32 +831,53 @@ template <typename K> cudaError_t allow_smem(K *kern, size_t bytes) {
     return e;
 }
 
-template <bool BWD>
+template <bool BWD, int NKB>
 cudaError_t launch_prep(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g,
                         const void *beta, const void *dy, void *ws, const GatedRecord &rec, unsigned *status,
                         cudaStream_t st) {
     using bf = __nv_bfloat16;
-    const uint32_t smem = prep_smem(rec.nkb, (a.d_v + 63) / 64).bytes;
-    cudaError_t e = allow_smem(gated_tc_prep_kernel<BWD>, smem);
+    auto *kern = gated_tc_prep_kernel<BWD, NKB>;
+    const uint32_t smem = prep_smem(NKB, (a.d_v + 63) / 64).bytes;
+    cudaError_t e = allow_smem(kern, smem);
     if (e != cudaSuccess)
         return e;
     // 128 columns for A1's product, d_v for A2's (MT's 64 lie there first)
     const int cols = a.d_v <= 128 ? 256 : 512;
-    return launch_pdl(gated_tc_prep_kernel<BWD>, dim3(rec.nch, a.B * a.H), dim3(NT), smem, st, a, (const bf *)q,
-                      (const bf *)k, (const bf *)v, (const bf *)g, (const bf *)beta, (const bf *)dy, (uint8_t *)ws, rec,
-                      cols, status);
+    return launch_pdl(kern, dim3(rec.nch, a.B * a.H), dim3(NT), smem, st, a, (const bf *)q, (const bf *)k,
+                      (const bf *)v, (const bf *)g, (const bf *)beta, (const bf *)dy, (uint8_t *)ws, rec, cols, status);
 }
 
-template <int MODE>
+template <int MODE, int NKB>
 cudaError_t launch_walk(const GatedArgs &a, const void *dy, const float *Z0, float *Zf, void *y, void *ws,
                         const GatedRecord &rec, unsigned *status, cudaStream_t st) {
     using bf = __nv_bfloat16;
-    const uint32_t smem = walk_smem<MODE>(rec.nkb).bytes;
-    cudaError_t e = allow_smem(gated_tc_walk_kernel<MODE>, smem);
+    auto *kern = gated_tc_walk_kernel<MODE, NKB>;
+    const uint32_t smem = Walk<MODE, NKB>::bytes;
+    cudaError_t e = allow_smem(kern, smem);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(gated_tc_walk_kernel<MODE>, dim3(rec.ns, a.B * a.H), dim3(NT), smem, st, a, (const bf *)dy, Z0,
-                      Zf, (bf *)y, (uint8_t *)ws, rec, status);
+    return launch_pdl(kern, dim3(rec.ns, a.B * a.H), dim3(kWalkThreads), smem, st, a, (const bf *)dy, Z0, Zf, (bf *)y,
+                      (uint8_t *)ws, rec, status);
+}
+
+template <int NKB>
+cudaError_t forward(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g, const void *beta,
+                    const float *W0, float *Wf, void *y, void *ws, const GatedRecord &rec, unsigned *status,
+                    cudaStream_t st) {
+    const cudaError_t e = launch_prep<false, NKB>(a, q, k, v, g, beta, nullptr, ws, rec, status, st);
+    return e != cudaSuccess ? e : launch_walk<kFwd, NKB>(a, nullptr, W0, Wf, y, ws, rec, status, st);
+}
+
+template <int NKB>
+cudaError_t walks(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g, const void *beta,
+                  const float *W0, const void *dy, const float *dWf, float *dW0, void *ws, const GatedRecord &rec,
+                  unsigned *status, cudaStream_t st) {
+    cudaError_t e = launch_prep<true, NKB>(a, q, k, v, g, beta, dy, ws, rec, status, st);
+    if (e == cudaSuccess)
+        e = launch_walk<kKeep, NKB>(a, nullptr, W0, nullptr, nullptr, ws, rec, status, st);
+    if (e == cudaSuccess)
+        e = launch_walk<kRev, NKB>(a, dy, dWf, dW0, nullptr, ws, rec, status, st);
+    return e;
 }
 
 } // namespace
@@ -783,10 +889,8 @@ cudaError_t gated_tc_forward(const GatedArgs &a, const void *q, const void *k, c
     if (e != cudaSuccess)
         return e;
     const GatedRecord rec = gated_forward_record(a.L, a.d_k, a.d_v);
-    e = launch_prep<false>(a, q, k, v, g, beta, nullptr, ws, rec, status, st);
-    if (e != cudaSuccess)
-        return e;
-    return launch_walk<kFwd>(a, nullptr, W0, Wf, y, ws, rec, status, st);
+    return rec.nkb == 1 ? forward<1>(a, q, k, v, g, beta, W0, Wf, y, ws, rec, status, st)
+                        : forward<2>(a, q, k, v, g, beta, W0, Wf, y, ws, rec, status, st);
 }
 
 cudaError_t gated_tc_walks(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g,
@@ -797,12 +901,8 @@ cudaError_t gated_tc_walks(const GatedArgs &a, const void *q, const void *k, con
     if (e != cudaSuccess)
         return e;
     const GatedRecord rec = gated_backward_record(a.L, a.d_k, a.d_v);
-    e = launch_prep<true>(a, q, k, v, g, beta, dy, ws, rec, status, st);
-    if (e == cudaSuccess)
-        e = launch_walk<kKeep>(a, nullptr, W0, nullptr, nullptr, ws, rec, status, st);
-    if (e == cudaSuccess)
-        e = launch_walk<kRev>(a, dy, dWf, dW0, nullptr, ws, rec, status, st);
-    return e;
+    return rec.nkb == 1 ? walks<1>(a, q, k, v, g, beta, W0, dy, dWf, dW0, ws, rec, status, st)
+                        : walks<2>(a, q, k, v, g, beta, W0, dy, dWf, dW0, ws, rec, status, st);
 }
 
 } // namespace fw

@@ -11,9 +11,9 @@ namespace fw {
 struct GatedRecord {
     int nkb, ns, nch;            // 64-wide blocks of d_k, 32-wide slices of d_v, chunks
     size_t bytes;                // per chunk
-    size_t A, K, scalF, base;    // forward: [-W'; Q'] hi, lo; K; scalars; [U'; Y'] fp32 [ns][128][32]
+    size_t A, K, scalF, base;    // forward: [-W'; Q'] hi, lo; K; scalars; [U'; Y'] fp32 pieces [d_v / 16][128][16]
     size_t AF, AR, KQ, scalR;    // backward: -W' and W" hi, lo (64 rows); [K; Q]; scalars
-    size_t baseU, baseX;         // U', X0: fp32 [ns][64][32]
+    size_t baseU, baseX;         // U', X0: fp32 pieces [d_v / 16][64][16]
     size_t U, dX, S, dS, tok;    // pair tiles [ns] of 64 (U, dX) and d_k (S, dS) rows; 8 floats a token
 
     __host__ __device__ size_t off(int64_t bh, int c) const { return ((size_t)bh * nch + c) * bytes; }
