@@ -774,7 +774,10 @@ size_t gated_forward_workspace_bytes(int B, int H, int L, int d_k, int d_v, int 
     return sizeof(float) * ws_off(B * H, L, d_k, d_v, false).end;
 }
 size_t gated_backward_workspace_bytes(int B, int H, int L, int d_k, int d_v, int bf16) {
-    (void)bf16;
+    if (bf16) {
+        const GatedRecord r = gated_backward_record(L, d_k, d_v);
+        return (size_t)B * H * r.nch * r.bytes;
+    }
     return sizeof(float) * ws_off(B * H, L, d_k, d_v, true).end;
 }
 
@@ -789,8 +792,10 @@ cudaError_t launch_gated_backward(const GatedArgs &a, const void *q, const void 
                                   const void *beta, const float *W0, const void *dy, const float *dWf, void *dq,
                                   void *dk, void *dv, void *dg, void *dbeta, float *dW0, void *workspace, int bf16,
                                   cudaStream_t st) {
-    return bf16 ? backward_t<__nv_bfloat16>(a, q, k, v, g, beta, W0, dy, dWf, dq, dk, dv, dg, dbeta, dW0, workspace, st)
-                : backward_t<float>(a, q, k, v, g, beta, W0, dy, dWf, dq, dk, dv, dg, dbeta, dW0, workspace, st);
+    if (!bf16)
+        return backward_t<float>(a, q, k, v, g, beta, W0, dy, dWf, dq, dk, dv, dg, dbeta, dW0, workspace, st);
+    const cudaError_t e = gated_tc_walks(a, q, k, v, g, beta, W0, dy, dWf, dW0, workspace, st);
+    return e != cudaSuccess ? e : gated_tc_grad(a, q, k, v, dy, dq, dk, dv, dg, dbeta, workspace, st);
 }
 
 } // namespace fw

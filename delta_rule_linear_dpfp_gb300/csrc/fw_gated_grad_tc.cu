@@ -1,0 +1,537 @@
+// fw_gated_grad_tc.cu -- the gradients of a chunk's tokens in the gated delta
+// rule (bf16 tensors), from what the two walks left: U, dX, the chunk's first
+// state S and the gradient dS' of its last one.
+//
+// With the names of fw_gated_chunk.cu, and everything in unit keys and
+// queries:
+//   a = scale e^G (dY S) + E K,   h = e^G (dX S) + F K,
+//   w = e^{G_C-G} (U dS') + E^T Q - F^T diag(beta) K,
+//   E = lower(scale D dY U^T),    F = strict_lower(D dX U^T),
+//   dq = a,  dk = w - beta h,  dV = beta dX,  dbeta_i = dX_i.V_i - k_i.h_i,
+//   dG_i = q_i.a_i - beta_i k_i.h_i - k_i.w_i  (+ the whole chunk's share in
+//   the last token), dg = the sums of dG over later tokens of the chunk.
+//
+// Five products on the tensor cores, each fp32 operand as two bf16 terms (see
+// fw_gated_tc.cu; the outputs are rounded to bf16 once, but dg is a difference
+// of its terms, and one term's 2^-9 would show in it):
+//   [dY; dX] S and [dY; dX] U^T (128 rows: dY, then dX) and U dS', summed over
+//   32-channel slices as the walks stored them, two slices in flight;
+//   then [E; F] K and [F; E]^T [K; Q].
+// One CTA per (chunk, key head) goes through the value heads that share the
+// key, so dq and dk are sums in a fixed order.
+#include "fw_gated.h"
+#include "fw_gated_tc.h"
+#include "fw_tc.cuh"
+
+#include <algorithm>
+
+namespace fw {
+
+cudaError_t status_word(unsigned **out); // fw_api.cu
+
+namespace {
+
+using namespace tc;
+using bf = __nv_bfloat16;
+
+constexpr int C = kGatedChunk;
+constexpr int NT = 256;
+
+FW_DEV void split8(const float *x, uint4 &hi, uint4 &lo) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        h[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+        l[e] = pack_bf16x2(x[2 * e] - __uint_as_float(h[e] << 16),
+                           x[2 * e + 1] - __uint_as_float(h[e] & 0xffff0000u));
+    }
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+FW_DEV void widen8(uint4 u, float (&o)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        o[2 * i] = __uint_as_float(w[i] << 16);
+        o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+FW_DEV uint32_t pair_chunk(int row, int c) { return (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)); }
+// 8 channels (chunk c of 4) of a pair tile's row: hi + lo.
+FW_DEV void pair8(const uint8_t *tile, int row, int c, float (&o)[8]) {
+    float l[8];
+    widen8(*reinterpret_cast<const uint4 *>(tile + pair_chunk(row, c)), o);
+    widen8(*reinterpret_cast<const uint4 *>(tile + pair_chunk(row, c + 4)), l);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        o[e] += l[e];
+}
+
+// Shared memory: [K; Q]; two slices (S, dS', [dY; dX], U), whose place the E
+// and F tiles (64 KB) and the staged reader rows take afterwards; the sums of
+// dq and dk over the value heads; scalars.
+struct GradSmem {
+    uint32_t slice, s, ds, yx, u, ef, stage, accq, acck, tok, red, bar, bytes;
+};
+__host__ __device__ inline GradSmem grad_smem(int nkb) {
+    GradSmem o;
+    o.ef = (uint32_t)nkb * 16384;
+    o.s = 0;
+    o.ds = (uint32_t)nkb * 8192;
+    o.yx = 2 * o.ds;
+    o.u = o.yx + 16384;
+    o.slice = o.u + 8192;
+    o.stage = o.ef + 65536;
+    const uint32_t a = o.ef + 2 * o.slice, b = o.stage + (uint32_t)nkb * 16384;
+    o.accq = a > b ? a : b;
+    o.acck = o.accq + (uint32_t)nkb * 16384;
+    o.tok = o.acck + (uint32_t)nkb * 16384;
+    o.red = o.tok + C * 32;
+    o.bar = o.red + 4 * (8 * C + 32);
+    o.bytes = o.bar + 64 + 1024;
+    return o;
+}
+
+template <int NKB>
+__global__ void __launch_bounds__(NT)
+    gated_tc_grad_kernel(GatedArgs a, const bf *__restrict__ q, const bf *__restrict__ k, const bf *__restrict__ v,
+                         const bf *__restrict__ dy, bf *__restrict__ dq, bf *__restrict__ dk, bf *__restrict__ dv,
+                         bf *__restrict__ dg, bf *__restrict__ dbeta, const uint8_t *ws, GatedRecord rec,
+                         unsigned *status) {
+    constexpr int DKP = 64 * NKB, HC = DKP / 2; // channels per thread of a row
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const GradSmem o = grad_smem(NKB);
+    uint8_t *kq = sm, *ef = sm + o.ef;
+    float *tok = reinterpret_cast<float *>(sm + o.tok); // per token: G hi, G lo, rk, beta, rq, e^G, e^{G_C-G}, -
+    float *red = reinterpret_cast<float *>(sm + o.red);
+    float *r_qa = red, *r_kh = red + 2 * C, *r_kw = red + 4 * C, *r_xv = red + 6 * C,
+          *r_ss = red + 8 * C, *r_last = r_ss + 8; // qa, kh, kw: one value per half
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + o.bar), *done = full + 2, *kqb = full + 4, *mm = full + 5;
+    uint32_t *slot = reinterpret_cast<uint32_t *>(full + 6);
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, c = blockIdx.x, bk = blockIdx.y;
+    const int b = bk / a.Hk, grp = a.H / a.Hk, ns = rec.ns;
+    const int rr = 32 * (w & 3) + lane, half = w >> 2, i = rr & 63;
+    griddep_wait();
+    const int len = a.lengths ? min(max(__ldcg(a.lengths + b), 0), a.L) : a.L;
+    const int n = min(C, len - c * C), rows = min(C, a.L - c * C); // tokens; rows in memory
+    const size_t krow = ((size_t)bk * a.L + (size_t)c * C) * a.d_k;
+    if (n <= 0) { // behind the sequence's end: no gradient
+        griddep_launch_dependents();
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        for (int e = tid; e < rows * a.d_k / 8; e += NT) {
+            reinterpret_cast<uint4 *>(dq + krow)[e] = zero;
+            reinterpret_cast<uint4 *>(dk + krow)[e] = zero;
+        }
+        for (int m = 0; m < grp; ++m) {
+            const size_t r0 = (size_t)(bk * grp + m) * a.L + (size_t)c * C;
+            for (int e = tid; e < rows * a.d_v / 8; e += NT)
+                reinterpret_cast<uint4 *>(dv + r0 * a.d_v)[e] = zero;
+            for (int e = tid; e < rows; e += NT) {
+                io<bf>::store(dg + r0 + e, 0.f);
+                io<bf>::store(dbeta + r0 + e, 0.f);
+            }
+        }
+        return;
+    }
+    if (w == 0) {
+        tmem_alloc(slot, 512);
+        tmem_relinquish();
+    }
+    if (tid == 32) {
+        for (int e = 0; e < 6; ++e)
+            mbar_init(full + e, 1);
+        fence_barrier_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_launch_dependents();
+    const uint32_t tm = *slot, tA = tm, tB = tm + 128, tW = tm + 192, tE = tm + 320;
+    const uint32_t lb = tmem_lane_base(w);
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (ok)
+            ok = mbar_wait(bar, parity, status);
+    };
+    auto record = [&](int m) { return ws + rec.off((int64_t)bk * grp + m, c); };
+    auto fetch = [&](int g) { // thread 0: slice g % ns of value head g / ns
+        const uint8_t *src = record(g / ns);
+        uint8_t *dst = ef + (g & 1) * o.slice;
+        uint64_t *f = full + (g & 1);
+        const int s = g % ns;
+        mbar_arrive_expect_tx(f, (uint32_t)(NKB * 16384 + 16384));
+        bulk_g2s(dst + o.s, src + rec.S + (size_t)s * NKB * 8192, NKB * 8192, f);
+        bulk_g2s(dst + o.ds, src + rec.dS + (size_t)s * NKB * 8192, NKB * 8192, f);
+        bulk_g2s(dst + o.yx + 8192, src + rec.dX + (size_t)s * 8192, 8192, f);
+        bulk_g2s(dst + o.u, src + rec.U + (size_t)s * 8192, 8192, f);
+    };
+    if (tid == 0) {
+        mbar_arrive_expect_tx(kqb, NKB * 16384);
+        bulk_g2s(kq, record(0) + rec.KQ, NKB * 16384, kqb);
+    }
+    const uint32_t kq_s = smem_u32(kq), ef_s = smem_u32(ef);
+    // a thread's part of the sums over the value heads: row i, channels half * HC ..
+    float4 *accq = reinterpret_cast<float4 *>(sm + o.accq) + (size_t)half * (HC / 4) * C + i;
+    float4 *acck = reinterpret_cast<float4 *>(sm + o.acck) + (size_t)half * (HC / 4) * C + i;
+    float4 *stage = reinterpret_cast<float4 *>(sm + o.stage) + (size_t)half * (HC / 4) * C + i;
+    int gs = 0; // slices seen
+    for (int m = 0; m < grp; ++m) {
+        const size_t r0 = (size_t)(bk * grp + m) * a.L + (size_t)c * C;
+        __syncthreads(); // the previous head's reads of the slices' place, tok and red are over
+        if (tid == 0 && ok) {
+            // generic reads and writes of the place end before the copies into it
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            fetch(gs);
+            if (ns > 1)
+                fetch(gs + 1);
+        }
+        if (tid < 2 * C)
+            reinterpret_cast<float4 *>(tok)[tid] =
+                __ldcg(reinterpret_cast<const float4 *>(record(m) + rec.tok) + tid);
+        float xv = 0.f, ss = 0.f;
+        const int yr = tid >> 2, yc = tid & 3; // dY, dX, V: row, 8 of 32 channels
+        for (int s = 0; s < ns; ++s, ++gs) {
+            uint8_t *sl = ef + (gs & 1) * o.slice;
+            const bool in = 32 * s + 8 * yc < a.d_v && yr < n;
+            const size_t at = (r0 + yr) * a.d_v + 32 * s + 8 * yc;
+            uint4 yv = make_uint4(0, 0, 0, 0), vv = yv;
+            if (in) {
+                yv = __ldcg(reinterpret_cast<const uint4 *>(dy + at));
+                vv = __ldcg(reinterpret_cast<const uint4 *>(v + at));
+            }
+            if (s >= 2) // the slice that lay here has been multiplied (dY's rows are not part of the copy)
+                wait(done + (gs & 1), ((gs >> 1) + 1) & 1);
+            *reinterpret_cast<uint4 *>(sl + o.yx + pair_chunk(yr, yc)) = yv;
+            *reinterpret_cast<uint4 *>(sl + o.yx + pair_chunk(yr, yc + 4)) = make_uint4(0, 0, 0, 0);
+            wait(full + (gs & 1), (gs >> 1) & 1);
+            if (s == 0)
+                __syncthreads(); // tok
+            {
+                float x[8], y[8];
+                pair8(sl + o.yx + 8192, yr, yc, x);
+                widen8(vv, y);
+                const float be = tok[yr * 8 + 3];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    xv = fmaf(x[e], y[e], xv);
+                    x[e] *= be;
+                }
+                if (in)
+                    store8(dv + at, x);
+            }
+#pragma unroll
+            for (int e = 0; e < DKP * 4 / NT; ++e) {
+                const int p = tid + e * NT;
+                float x[8], y[8];
+                pair8(sl + o.s, p >> 2, p & 3, x);
+                pair8(sl + o.ds, p >> 2, p & 3, y);
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    ss = fmaf(x[u], y[u], ss);
+            }
+            fence_async_smem();
+            tc_fence_before();
+            __syncthreads();
+            if (tid == 0 && ok) {
+                tc_fence_after();
+                const uint32_t base = ef_s + (uint32_t)(gs & 1) * o.slice;
+                for (int t = 0; t < 3; ++t) { // hi hi, hi lo, lo hi
+                    const uint32_t ta = t == 2 ? 64u : 0u, tb = t == 1 ? 64u : 0u;
+                    for (int e = 0; e < 2; ++e) {
+                        const uint64_t yx = desc_sw128(base + o.yx + ta + e * 32, 16, 1024);
+                        const uint32_t acc = (s | t | e) != 0;
+                        mma_bf16(tA, yx, desc_sw128(base + o.s + tb + e * 32, 16, 1024), idesc_bf16(128, DKP, 0, 0), acc);
+                        mma_bf16(tB, yx, desc_sw128(base + o.u + tb + e * 32, 16, 1024), idesc_bf16(128, 64, 0, 0), acc);
+                        mma_bf16(tW, desc_sw128(base + o.u + ta + e * 32, 16, 1024),
+                                 desc_sw128(base + o.ds + tb + e * 32, 16, 1024), idesc_bf16(128, DKP, 0, 0), acc);
+                    }
+                }
+                mma_commit(done + (gs & 1));
+                if (s >= 1 && s + 1 < ns) { // the other buffer's slice is done: its successor
+                    wait(done + ((gs + 1) & 1), ((gs - 1) >> 1) & 1);
+                    if (ok)
+                        fetch(gs + 1);
+                }
+            }
+        }
+        // every product of this head's slices (one commit covers those before it)
+        wait(done + ((gs - 1) & 1), ((gs - 1) >> 1) & 1);
+        tc_fence_after();
+        if (m == 0)
+            wait(kqb, 0);
+        xv += __shfl_xor_sync(0xffffffffu, xv, 1);
+        xv += __shfl_xor_sync(0xffffffffu, xv, 2);
+        if (yc == 0)
+            r_xv[yr] = xv;
+        ss = warp_sum(ss);
+        if (lane == 0)
+            r_ss[w] = ss;
+        const float4 di = *reinterpret_cast<const float4 *>(tok + i * 8);
+        const float4 dj_ = *reinterpret_cast<const float4 *>(tok + i * 8 + 4); // rq, e^G, e^{G_C-G}
+        // E and F, as [E; F] rk_j (K-major) and as [F (-beta rk_i); E rq_i]
+        {
+            const float fr = rr < C ? dj_.x : -di.w * di.z;
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int j0 = 32 * half + 16 * p;
+                float x[16], y[16];
+                tmem_ld16(tB + lb + (uint32_t)j0, x);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int j = j0 + e;
+                    const float4 dj = *reinterpret_cast<const float4 *>(tok + j * 8);
+                    const bool in = rr < C ? j <= i : j < i;
+                    const float t = in ? (rr < C ? a.scale : 1.f) * x[e] * expf((di.x - dj.x) + (di.y - dj.y)) : 0.f;
+                    x[e] = t * dj.z;
+                    y[e] = t * fr;
+                }
+#pragma unroll
+                for (int e = 0; e < 16; e += 8) {
+                    uint4 hi, lo;
+                    const uint32_t to = kmajor_chunk(rr, j0 + e, 128), to2 = kmajor_chunk(rr ^ 64, j0 + e, 128);
+                    split8(x + e, hi, lo);
+                    *reinterpret_cast<uint4 *>(ef + to) = hi;
+                    *reinterpret_cast<uint4 *>(ef + 16384 + to) = lo;
+                    split8(y + e, hi, lo);
+                    *reinterpret_cast<uint4 *>(ef + 32768 + to2) = hi;
+                    *reinterpret_cast<uint4 *>(ef + 49152 + to2) = lo;
+                }
+            }
+        }
+        float x[HC]; // rows of a (rr < 64) or h
+        const float fs = rr < C ? a.scale * dj_.y : dj_.y;
+#pragma unroll
+        for (int p = 0; p < HC; p += 16) {
+            float t[16];
+            tmem_ld16(tA + lb + (uint32_t)(half * HC + p), t);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                x[p + e] = fs * t[e];
+        }
+        fence_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        if (tid == 0 && ok) {
+            tc_fence_after();
+            for (int t = 0; t < 2; ++t)
+                for (int s = 0; s < 4; ++s)
+                    mma_bf16(tA, desc_sw128(ef_s + (uint32_t)t * 16384u + (uint32_t)s * 32u, 16, 1024),
+                             desc_sw128(kq_s + (uint32_t)s * 2048u, 16384, 1024), idesc_bf16(128, DKP, 0, 1),
+                             (t | s) != 0);
+            for (int t = 0; t < 2; ++t)
+                for (int s = 0; s < 8; ++s)
+                    mma_bf16(tE, desc_sw128(ef_s + 32768u + (uint32_t)t * 16384u + (uint32_t)s * 2048u, 16384, 1024),
+                             desc_sw128(kq_s + (uint32_t)s * 2048u, 16384, 1024), idesc_bf16(128, DKP, 1, 1),
+                             (t | s) != 0);
+            mma_commit(mm);
+        }
+        // k_j . (e^{G_C-G_j} dS'^T U_j), for the chunk's decay
+        auto kq_row = [&](int row, int p, float (&u)[8]) {
+            widen8(*reinterpret_cast<const uint4 *>(kq + kmajor_chunk(row, half * HC + p, 128)), u);
+        };
+        float last = 0.f;
+        if (rr < C) {
+#pragma unroll
+            for (int p = 0; p < HC; p += 16) {
+                float t[16];
+                tmem_ld16(tW + lb + (uint32_t)(half * HC + p), t);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; e += 8) {
+                    float u[8];
+                    kq_row(i, p + e, u);
+#pragma unroll
+                    for (int m2 = 0; m2 < 8; ++m2)
+                        last = fmaf(u[m2], t[e + m2], last);
+                }
+            }
+            last = warp_sum(last * di.z * dj_.z);
+            if (lane == 0)
+                r_last[w] = last; // warps 0, 1, 4, 5
+        }
+        wait(mm, (uint32_t)m & 1);
+        tc_fence_after();
+        {
+            float dot = 0.f; // q.a or k.h, this half's channels
+#pragma unroll
+            for (int p = 0; p < HC; p += 16) {
+                float t[16];
+                tmem_ld16(tA + lb + (uint32_t)(half * HC + p), t);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; e += 8) {
+                    float u[8];
+                    kq_row(rr ^ 64, p + e, u); // rows of a meet Q (tile rows 64 ..), rows of h meet K
+#pragma unroll
+                    for (int m2 = 0; m2 < 8; ++m2) {
+                        x[p + e + m2] += t[e + m2];
+                        dot = fmaf(u[m2], x[p + e + m2], dot);
+                    }
+                }
+            }
+            if (rr < C)
+                r_qa[half * C + i] = dot * dj_.x;
+            else
+                r_kh[half * C + i] = dot * di.z;
+        }
+        if (rr >= C) {
+#pragma unroll
+            for (int p = 0; p < HC; p += 4)
+                stage[(p / 4) * C] = make_float4(-di.w * x[p], -di.w * x[p + 1], -di.w * x[p + 2], -di.w * x[p + 3]);
+        } else {
+#pragma unroll
+            for (int p = 0; p < HC; p += 4) {
+                float4 t = make_float4(x[p], x[p + 1], x[p + 2], x[p + 3]);
+                if (m > 0) {
+                    const float4 s = accq[(p / 4) * C];
+                    t = make_float4(t.x + s.x, t.y + s.y, t.z + s.z, t.w + s.w);
+                }
+                accq[(p / 4) * C] = t;
+            }
+        }
+        __syncthreads();
+        if (rr < C) {
+            float dot = 0.f;
+#pragma unroll
+            for (int p = 0; p < HC; p += 16) {
+                float t[16], u1[16];
+                tmem_ld16(tW + lb + (uint32_t)(half * HC + p), t);
+                tmem_ld16(tE + lb + (uint32_t)(half * HC + p), u1);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; e += 8) {
+                    float u[8];
+                    kq_row(i, p + e, u);
+#pragma unroll
+                    for (int m2 = 0; m2 < 8; ++m2) {
+                        t[e + m2] = fmaf(dj_.z, t[e + m2], u1[e + m2]);
+                        dot = fmaf(u[m2], t[e + m2], dot);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const float4 s = stage[((p + e) / 4) * C];
+                    float4 r = make_float4(t[e] + s.x, t[e + 1] + s.y, t[e + 2] + s.z, t[e + 3] + s.w);
+                    if (m > 0) {
+                        const float4 o4 = acck[((p + e) / 4) * C];
+                        r = make_float4(r.x + o4.x, r.y + o4.y, r.z + o4.z, r.w + o4.w);
+                    }
+                    acck[((p + e) / 4) * C] = r;
+                }
+            }
+            r_kw[half * C + i] = dot * di.z;
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (w == 0) { // dg: the sums over later tokens, two a lane; dbeta
+            float G2[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int t = 2 * lane + e;
+                const float kh = r_kh[t] + r_kh[C + t];
+                G2[e] = r_qa[t] + r_qa[C + t] - tok[t * 8 + 3] * kh - (r_kw[t] + r_kw[C + t]);
+                if (t < n)
+                    io<bf>::store(dbeta + r0 + t, r_xv[t] - kh);
+            }
+            if (lane == 31) {
+                float s8 = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    s8 += r_ss[e];
+                G2[1] += tok[(C - 1) * 8 + 5] * s8 + (r_last[0] + r_last[1]) + (r_last[4] + r_last[5]);
+            }
+            float run = G2[0] + G2[1];
+#pragma unroll
+            for (int e = 1; e < 32; e <<= 1) {
+                const float dn = __shfl_down_sync(0xffffffffu, run, e);
+                if (lane + e < 32)
+                    run += dn;
+            }
+            const float own = G2[0] + G2[1];
+            if (2 * lane < n)
+                io<bf>::store(dg + r0 + 2 * lane, run);
+            if (2 * lane + 1 < n)
+                io<bf>::store(dg + r0 + 2 * lane + 1, (run - own) + G2[1]);
+        }
+        for (int e = n * a.d_v / 8 + tid; e < rows * a.d_v / 8; e += NT)
+            reinterpret_cast<uint4 *>(dv + r0 * a.d_v)[e] = make_uint4(0, 0, 0, 0);
+        for (int t = n + tid; t < rows; t += NT) {
+            io<bf>::store(dg + r0 + t, 0.f);
+            io<bf>::store(dbeta + r0 + t, 0.f);
+        }
+    }
+    // dq (the threads of rows 64 ..) and dk: back through the unit length
+    __syncthreads(); // dg has been read off; red is free
+    {
+        const float4 *acc = rr < C ? acck : accq;
+        const float r = i >= n ? 0.f : tok[i * 8 + (rr < C ? 2 : 4)];
+        float dot = 0.f;
+#pragma unroll
+        for (int p = 0; p < HC; p += 8) {
+            float u[8];
+            widen8(*reinterpret_cast<const uint4 *>(kq + kmajor_chunk(rr, half * HC + p, 128)), u);
+            const float4 s = acc[(p / 4) * C], t = acc[(p / 4 + 1) * C];
+            dot += u[0] * s.x + u[1] * s.y + u[2] * s.z + u[3] * s.w + u[4] * t.x + u[5] * t.y + u[6] * t.z + u[7] * t.w;
+        }
+        red[half * 2 * C + rr] = dot * r;
+        __syncthreads();
+        const float f = a.l2norm ? (red[rr] + red[2 * C + rr]) * r : 0.f;
+        if (i < rows) {
+            bf *to = (rr < C ? dk : dq) + krow + (size_t)i * a.d_k;
+#pragma unroll
+            for (int p = 0; p < HC; p += 8) {
+                float u[8];
+                widen8(*reinterpret_cast<const uint4 *>(kq + kmajor_chunk(rr, half * HC + p, 128)), u);
+                const float4 s = acc[(p / 4) * C], t = acc[(p / 4 + 1) * C];
+                const float g8[8] = {s.x, s.y, s.z, s.w, t.x, t.y, t.z, t.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    u[e] = i < n ? r * (g8[e] - u[e] * f) : 0.f;
+                if (half * HC + p < a.d_k)
+                    store8(to + half * HC + p, u);
+            }
+        }
+    }
+    if (!ok && tid == 0) // a wait gave up: let what was asked for land first
+        for (int e = 0; e < 2; ++e)
+            (void)mbar_wait(full + e, 0, status);
+    tc_fence_before();
+    __syncthreads();
+    if (w == 0)
+        tmem_dealloc(tm, 512);
+}
+
+template <int NKB>
+cudaError_t launch(const GatedArgs &a, const void *q, const void *k, const void *v, const void *dy, void *dq, void *dk,
+                   void *dv, void *dg, void *dbeta, const void *ws, const GatedRecord &rec, unsigned *status,
+                   cudaStream_t st) {
+    auto *kern = gated_tc_grad_kernel<NKB>;
+    const uint32_t smem = grad_smem(NKB).bytes;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e != cudaSuccess)
+        return e;
+    return launch_pdl(kern, dim3(rec.nch, a.B * a.Hk), dim3(NT), smem, st, a, (const bf *)q, (const bf *)k,
+                      (const bf *)v, (const bf *)dy, (bf *)dq, (bf *)dk, (bf *)dv, (bf *)dg, (bf *)dbeta,
+                      (const uint8_t *)ws, rec, status);
+}
+
+} // namespace
+
+cudaError_t gated_tc_grad(const GatedArgs &a, const void *q, const void *k, const void *v, const void *dy, void *dq,
+                          void *dk, void *dv, void *dg, void *dbeta, const void *ws, cudaStream_t st) {
+    unsigned *status = nullptr;
+    cudaError_t e = status_word(&status);
+    if (e != cudaSuccess)
+        return e;
+    const GatedRecord rec = gated_backward_record(a.L, a.d_k, a.d_v);
+    return rec.nkb == 1 ? launch<1>(a, q, k, v, dy, dq, dk, dv, dg, dbeta, ws, rec, status, st)
+                        : launch<2>(a, q, k, v, dy, dq, dk, dv, dg, dbeta, ws, rec, status, st);
+}
+
+} // namespace fw
