@@ -506,41 +506,25 @@ def fw_selftest_flag_timeout(limit_us: int = 2000, stream=None):
     _check(load().fw_selftest_flag_timeout(int(limit_us), _stream(stream)), "fw_selftest_flag_timeout")
 
 
-def _here(tensors):
-    """(name, tensor) pairs are contiguous tensors of the current CUDA device:
-    the library launches on that device whatever the tensors say."""
+def _here(names, *tensors):
+    """The tensors (None aside) are contiguous and on the current CUDA device,
+    the one the library launches on; returns the device's current stream."""
     dev = torch.cuda.current_device()
-    for name, t in tensors:
-        if t is not None and (not t.is_cuda or not t.is_contiguous() or t.get_device() != dev):
-            raise ValueError(f"{name} must be a contiguous tensor on the current CUDA device")
-
-
-class _Queue:
-    """Where a call's outputs and scratch are allocated: on the stream it is
-    enqueued on, so that the allocator hands their memory on in its order."""
-
-    def __init__(self, stream):
-        self.ctx = None if stream is None else torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+    for i, t in enumerate(tensors):
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError(f"{names.split()[i]} must be a contiguous tensor on the current CUDA device")
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _data(t):
     return None if t is None else t.data_ptr()
 
 
-def _scratch(need, workspace, device):
-    """(pointer, bytes, keeper) of the caller's workspace, or of a new one."""
+def _scratch(need, workspace, like):
+    """The caller's workspace, or a new one of `need` bytes, and its bytes."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+        workspace = like.new_empty(-(-need // like.element_size()))
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def _gated_shapes(where, q, k, v, g, beta, states, lengths, dy=None):
@@ -548,20 +532,21 @@ def _gated_shapes(where, q, k, v, g, beta, states, lengths, dy=None):
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError(f"{where}: q must be [B,Hk,L,d_k] and v [B,H,L,d_v]")
     B, Hk, L, d_k = q.shape
-    H, d_v = v.shape[1], v.shape[3]
+    _, H, _, d_v = v.shape
     if (k.shape != q.shape or v.shape != (B, H, L, d_v) or g.shape != (B, H, L) or beta.shape != g.shape or
             (dy is not None and dy.shape != v.shape)):
         raise ValueError(f"{where}: shape mismatch among q, k, v, g, beta" + (", dy" if dy is not None else ""))
     if Hk == 0 or H == 0 or H % Hk:
         raise ValueError(f"{where}: the value heads must be a multiple of the key heads")
-    if not (q.dtype == k.dtype == v.dtype == g.dtype == beta.dtype) or (dy is not None and dy.dtype != q.dtype):
+    dt = q.dtype
+    if k.dtype != dt or v.dtype != dt or g.dtype != dt or beta.dtype != dt or (dy is not None and dy.dtype != dt):
         raise ValueError(f"{where}: the activations must share the I/O dtype")
-    for name, t in states:
+    for t in states:
         if t is not None and (t.dtype != torch.float32 or t.shape != (B, H, d_v, d_k)):
-            raise ValueError(f"{name} must be fp32 [B,H,d_v,d_k]")
+            raise ValueError(f"{where}: states and their gradients must be fp32 [B,H,d_v,d_k]")
     if lengths is not None and (lengths.dtype != torch.int32 or lengths.shape != (B,)):
-        raise ValueError("lengths must be int32 [B]")
-    return B, Hk, H, L, d_k, d_v, _dtype_code(q.dtype)
+        raise ValueError(f"{where}: lengths must be int32 [B]")
+    return B, Hk, H, L, d_k, d_v, _dtype_code(dt)
 
 
 def fw_gated_delta_forward_workspace_size(B, Hk, H, L, d_k, d_v, io_dtype) -> int:
@@ -569,28 +554,34 @@ def fw_gated_delta_forward_workspace_size(B, Hk, H, L, d_k, d_v, io_dtype) -> in
     return int(load().fw_gated_delta_forward_workspace_size(B, Hk, H, L, d_k, d_v, code))
 
 
+# The calls below take the stream they are enqueued on as the current one:
+# outputs and scratch are then allocated on it too, and the allocator hands
+# their memory on in its order.
+
 def fw_gated_delta_forward(q, k, v, g, beta, W0=None, lengths=None, l2norm: bool = True, scale: float = 1.0,
                            eps: float = 1e-6, return_state: bool = True, y=None, W_final=None, workspace=None,
                            stream=None):
     """The gated delta rule over q, k [B,Hk,L,d_k], v [B,H,L,d_v], g (log
     decay), beta [B,H,L].  Returns (y, W_final or None); lengths (int32 [B])
     ends each sequence early."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fw_gated_delta_forward(q, k, v, g, beta, W0, lengths, l2norm, scale, eps, return_state, y, W_final,
+                                          workspace)
     lib = load()
-    _here((("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("W0", W0), ("lengths", lengths), ("y", y),
-           ("W_final", W_final), ("workspace", workspace)))
-    shape = _gated_shapes("fw_gated_delta_forward", q, k, v, g, beta, (("W0", W0), ("W_final", W_final)), lengths)
+    st = _here("q k v g beta W0 lengths y W_final workspace", q, k, v, g, beta, W0, lengths, y, W_final, workspace)
+    shape = _gated_shapes("fw_gated_delta_forward", q, k, v, g, beta, (W0, W_final), lengths)
     B, Hk, H, L, d_k, d_v, code = shape
-    if y is not None and (y.dtype != v.dtype or y.shape != v.shape):
+    if y is None:
+        y = torch.empty_like(v)
+    elif y.dtype != v.dtype or y.shape != v.shape:
         raise ValueError("y must have v's shape and dtype")
-    with _Queue(stream) as st:
-        if y is None:
-            y = torch.empty_like(v)
-        if W_final is None and return_state:
-            W_final = torch.empty(B, H, d_v, d_k, dtype=torch.float32, device=q.device)
-        ws, ws_bytes, keep = _scratch(lib.fw_gated_delta_forward_workspace_size(*shape), workspace, q.device)
-        rc = lib.fw_gated_delta_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-                                        _data(W0), _data(W_final), y.data_ptr(), _data(lengths), ws, ws_bytes, B, Hk, H,
-                                        L, d_k, d_v, int(bool(l2norm)), scale, eps, code, st)
+    if W_final is None and return_state:
+        W_final = torch.empty(B, H, d_v, d_k, dtype=torch.float32, device=q.device)
+    workspace, ws_bytes = _scratch(lib.fw_gated_delta_forward_workspace_size(*shape), workspace, q)
+    rc = lib.fw_gated_delta_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _data(W0),
+                                    _data(W_final), y.data_ptr(), _data(lengths), workspace.data_ptr(), ws_bytes, B, Hk,
+                                    H, L, d_k, d_v, 1 if l2norm else 0, scale, eps, code, st)
     _check(rc, "fw_gated_delta_forward")
     return y, W_final
 
@@ -605,19 +596,21 @@ def fw_gated_delta_backward(q, k, v, g, beta, dy, W0=None, dW_final=None, length
                             stream=None):
     """Gradients of fw_gated_delta_forward from dy [B,H,L,d_v] (and dW_final):
     (dq, dk, dv, dg, dbeta, dW0 or None)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fw_gated_delta_backward(q, k, v, g, beta, dy, W0, dW_final, lengths, l2norm, scale, eps, return_dW0,
+                                           workspace)
     lib = load()
-    _here((("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("dy", dy), ("W0", W0), ("dW_final", dW_final),
-           ("lengths", lengths), ("workspace", workspace)))
-    shape = _gated_shapes("fw_gated_delta_backward", q, k, v, g, beta, (("W0", W0), ("dW_final", dW_final)), lengths, dy)
+    st = _here("q k v g beta dy W0 dW_final lengths workspace", q, k, v, g, beta, dy, W0, dW_final, lengths, workspace)
+    shape = _gated_shapes("fw_gated_delta_backward", q, k, v, g, beta, (W0, dW_final), lengths, dy)
     B, Hk, H, L, d_k, d_v, code = shape
-    with _Queue(stream) as st:
-        dq, dk, dv, dg, dbeta = (torch.empty_like(t) for t in (q, k, v, g, beta))
-        dW0 = torch.empty(B, H, d_v, d_k, dtype=torch.float32, device=q.device) if return_dW0 else None
-        ws, ws_bytes, keep = _scratch(lib.fw_gated_delta_backward_workspace_size(*shape), workspace, q.device)
-        rc = lib.fw_gated_delta_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-                                         _data(W0), dy.data_ptr(), _data(dW_final), dq.data_ptr(), dk.data_ptr(),
-                                         dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _data(dW0), _data(lengths), ws,
-                                         ws_bytes, B, Hk, H, L, d_k, d_v, int(bool(l2norm)), scale, eps, code, st)
+    dq, dk, dv, dg, dbeta = (torch.empty_like(t) for t in (q, k, v, g, beta))
+    dW0 = torch.empty(B, H, d_v, d_k, dtype=torch.float32, device=q.device) if return_dW0 else None
+    workspace, ws_bytes = _scratch(lib.fw_gated_delta_backward_workspace_size(*shape), workspace, q)
+    rc = lib.fw_gated_delta_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _data(W0),
+                                     dy.data_ptr(), _data(dW_final), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                     dg.data_ptr(), dbeta.data_ptr(), _data(dW0), _data(lengths), workspace.data_ptr(),
+                                     ws_bytes, B, Hk, H, L, d_k, d_v, 1 if l2norm else 0, scale, eps, code, st)
     _check(rc, "fw_gated_delta_backward")
     return dq, dk, dv, dg, dbeta, dW0
 
@@ -626,28 +619,30 @@ def fw_gated_delta_decode_step(q, k, v, g, beta, W, l2norm: bool = True, scale: 
                                y=None, stream=None):
     """One token per (b, value head): q, k [B,Hk,d_k]; v [B,H,d_v]; g, beta
     [B,H]; W fp32 [B,H,d_v,d_k] updated in place.  Returns y [B,H,d_v]."""
-    _here((("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("W", W), ("y", y)))
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fw_gated_delta_decode_step(q, k, v, g, beta, W, l2norm, scale, eps, y)
+    st = _here("q k v g beta W y", q, k, v, g, beta, W, y)
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q must be [B,Hk,d_k] and v [B,H,d_v]")
     B, Hk, d_k = q.shape
-    _, H, d_v = v.shape
-    if k.shape != q.shape or v.shape[0] != B or g.shape != (B, H) or beta.shape != g.shape:
+    Bv, H, d_v = v.shape
+    if k.shape != q.shape or Bv != B or g.shape != (B, H) or beta.shape != g.shape:
         raise ValueError("shape mismatch among q, k, v, g, beta")
     if Hk == 0 or H == 0 or H % Hk:
         raise ValueError("the value heads must be a multiple of the key heads")
     dt = q.dtype
-    if not (k.dtype == v.dtype == g.dtype == beta.dtype == dt):
+    if k.dtype != dt or v.dtype != dt or g.dtype != dt or beta.dtype != dt:
         raise ValueError("q, k, v, g, beta must share the I/O dtype")
     if W.dtype != torch.float32 or W.shape != (B, H, d_v, d_k):
         raise ValueError("W must be fp32 [B,H,d_v,d_k]")
-    if y is not None and (y.dtype != dt or y.shape != v.shape):
+    if y is None:
+        y = torch.empty_like(v)
+    elif y.dtype != dt or y.shape != v.shape:
         raise ValueError("y must have v's shape and dtype")
-    with _Queue(stream) as st:
-        if y is None:
-            y = torch.empty_like(v)
-        rc = load().fw_gated_delta_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-                                               W.data_ptr(), y.data_ptr(), B, Hk, H, d_k, d_v, int(bool(l2norm)), scale,
-                                               eps, _dtype_code(dt), st)
+    rc = load().fw_gated_delta_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                                           W.data_ptr(), y.data_ptr(), B, Hk, H, d_k, d_v, 1 if l2norm else 0, scale, eps,
+                                           _dtype_code(dt), st)
     _check(rc, "fw_gated_delta_decode_step")
     return y
 
@@ -656,12 +651,12 @@ def _norm_shapes(x, gamma, beta, gate, act, dout=None):
     if x.dim() != 4:
         raise ValueError("x must be [B,H,L,d]")
     B, H, L, d = x.shape
-    for name, t in (("gamma", gamma), ("beta", beta)):
+    for t in (gamma, beta):
         if t.dtype != torch.float32 or t.shape != (H * d,):
-            raise ValueError(f"{name} must be fp32 [H d]")
-    for name, t in (("gate", gate), ("dout", dout)):
+            raise ValueError("gamma and beta must be fp32 [H d]")
+    for t in (gate, dout):
         if t is not None and (t.dtype != x.dtype or t.shape != (B, L, H * d)):
-            raise ValueError(f"{name} must be [B,L,H d] in x's dtype")
+            raise ValueError("gate and dout must be [B,L,H d] in x's dtype")
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
     return B, H, L, d
@@ -671,15 +666,17 @@ def fw_group_norm_act(x, gamma, beta, gate=None, act: str = "none", eps: float =
     """Each head's channels normalised for each token, then act, or act of a
     gate: x [B,H,L,d] (head-major), gamma, beta fp32 [H d], gate [B,L,H d] or
     None.  Returns out [B,L,H d] (token-major)."""
-    _here((("x", x), ("gamma", gamma), ("beta", beta), ("gate", gate), ("out", out)))
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fw_group_norm_act(x, gamma, beta, gate, act, eps, out)
+    st = _here("x gamma beta gate out", x, gamma, beta, gate, out)
     B, H, L, d = _norm_shapes(x, gamma, beta, gate, act)
-    if out is not None and (out.dtype != x.dtype or out.shape != (B, L, H * d)):
+    if out is None:
+        out = x.new_empty(B, L, H * d)
+    elif out.dtype != x.dtype or out.shape != (B, L, H * d):
         raise ValueError("out must be [B,L,H d] in x's dtype")
-    with _Queue(stream) as st:
-        if out is None:
-            out = torch.empty(B, L, H * d, dtype=x.dtype, device=x.device)
-        rc = load().fw_group_norm_act(x.data_ptr(), _data(gate), gamma.data_ptr(), beta.data_ptr(), out.data_ptr(), B, H,
-                                      L, d, ACTIVATIONS[act], _dtype_code(x.dtype), eps, st)
+    rc = load().fw_group_norm_act(x.data_ptr(), _data(gate), gamma.data_ptr(), beta.data_ptr(), out.data_ptr(), B, H, L,
+                                  d, ACTIVATIONS[act], _dtype_code(x.dtype), eps, st)
     _check(rc, "fw_group_norm_act")
     return out
 
@@ -692,17 +689,19 @@ def fw_group_norm_act_backward(x, gamma, beta, dout, gate=None, act: str = "none
                                stream=None):
     """Gradients of fw_group_norm_act from dout [B,L,H d]:
     (dx, dgate or None, dgamma, dbeta)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fw_group_norm_act_backward(x, gamma, beta, dout, gate, act, eps, workspace)
     lib = load()
-    _here((("x", x), ("gamma", gamma), ("beta", beta), ("dout", dout), ("gate", gate), ("workspace", workspace)))
+    st = _here("x gamma beta dout gate workspace", x, gamma, beta, dout, gate, workspace)
     B, H, L, d = _norm_shapes(x, gamma, beta, gate, act, dout)
-    with _Queue(stream) as st:
-        dx = torch.empty_like(x)
-        dgate = None if gate is None else torch.empty_like(gate)
-        dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(beta)
-        ws, ws_bytes, keep = _scratch(lib.fw_group_norm_act_backward_workspace_size(B, H, L, d), workspace, x.device)
-        rc = lib.fw_group_norm_act_backward(x.data_ptr(), _data(gate), gamma.data_ptr(), beta.data_ptr(),
-                                            dout.data_ptr(), dx.data_ptr(), _data(dgate), dgamma.data_ptr(),
-                                            dbeta.data_ptr(), ws, ws_bytes, B, H, L, d, ACTIVATIONS[act],
-                                            _dtype_code(x.dtype), eps, st)
+    dx = torch.empty_like(x)
+    dgate = None if gate is None else torch.empty_like(gate)
+    dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(beta)
+    workspace, ws_bytes = _scratch(lib.fw_group_norm_act_backward_workspace_size(B, H, L, d), workspace, x)
+    rc = lib.fw_group_norm_act_backward(x.data_ptr(), _data(gate), gamma.data_ptr(), beta.data_ptr(), dout.data_ptr(),
+                                        dx.data_ptr(), _data(dgate), dgamma.data_ptr(), dbeta.data_ptr(),
+                                        workspace.data_ptr(), ws_bytes, B, H, L, d, ACTIVATIONS[act],
+                                        _dtype_code(x.dtype), eps, st)
     _check(rc, "fw_group_norm_act_backward")
     return dx, dgate, dgamma, dbeta

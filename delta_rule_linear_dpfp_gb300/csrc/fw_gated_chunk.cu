@@ -1,5 +1,7 @@
 // fw_gated_chunk.cu -- the gated delta rule over a sequence and its
-// gradients, in chunks of 64 tokens, fp32 on CUDA cores.
+// gradients, in chunks of 64 tokens: fp32 tensors, on CUDA cores (bf16 tensors
+// take the same algebra to the tensor cores: fw_gated_tc.cu,
+// fw_gated_grad_tc.cu).
 //
 // The rule, per value head (a_t = exp(g_t)):
 //   W_t = a_t W_{t-1} + beta_t (v_t - a_t W_{t-1} k_t) k_t^T,  y_t = scale W_t q_t.
@@ -210,10 +212,9 @@ FW_DEV void unit_lower_inverse(const float *A, float *T, float *tmp) {
 }
 
 // ------------------------------------------------------------------ prep
-template <typename T>
 __global__ void __launch_bounds__(NT)
-    gated_prep_kernel(GatedArgs a, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ g,
-                      const T *__restrict__ beta, Ws ws) {
+    gated_prep_kernel(GatedArgs a, const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ g,
+                      const float *__restrict__ beta, Ws ws) {
     extern __shared__ __align__(16) float sm[];
     const int ldk = a.d_k + 4;
     float *kt = sm, *qt = kt + C * ldk, *At = qt + C * ldk, *Tt = At + C * LC, *tmp = Tt + C * LC, *tok = tmp + 1024;
@@ -234,9 +235,9 @@ __global__ void __launch_bounds__(NT)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int i = 2 * tid + e;
-            const float x = i < n ? io<T>::load(g + t0 + i) : 0.f;
+            const float x = i < n ? io<float>::load(g + t0 + i) : 0.f;
             s[e] = x < kGMin ? kGMin : x;
-            be[e] = i < n ? io<T>::load(beta + t0 + i) : 0.f;
+            be[e] = i < n ? io<float>::load(beta + t0 + i) : 0.f;
         }
         s[1] += s[0];
         double run = s[1];
@@ -296,10 +297,10 @@ __global__ void __launch_bounds__(NT)
 // ------------------------------------------------------------------ walk
 // One CTA per (value head, 32 value channels).  KEEP: the chunks' first
 // states and U stay in the workspace for the gradients (no answers then).
-template <typename T, bool KEEP>
+template <bool KEEP>
 __global__ void __launch_bounds__(NT)
-    gated_walk_kernel(GatedArgs a, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
-                      const float *__restrict__ W0, float *__restrict__ Wf, T *__restrict__ y, Ws ws) {
+    gated_walk_kernel(GatedArgs a, const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
+                      const float *__restrict__ W0, float *__restrict__ Wf, float *__restrict__ y, Ws ws) {
     extern __shared__ __align__(16) float sm[];
     const int ldk = a.d_k + 4, nC = (a.L + C - 1) / C;
     float *S = sm, *kq = S + NV * ldk, *Tt = kq + 2 * C * ldk, *Mt = Tt + C * LC, *Xt = Mt + C * LC, *Ut = Xt + C * LV,
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(NT)
                 if (ti + 32 * r < n && tj * 4 < nv)
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
-                        io<T>::store(y + vrow + (size_t)(ti + 32 * r) * a.d_v + tj * 4 + s, o[r][s]);
+                        io<float>::store(y + vrow + (size_t)(ti + 32 * r) * a.d_v + tj * 4 + s, o[r][s]);
         }
         const float whole = tok[(C - 1) * TOK + 2];
         __syncthreads();
@@ -405,14 +406,13 @@ __global__ void __launch_bounds__(NT)
             for (int e = tid; e < nv * a.d_k; e += NT)
                 Wf[st0 + e] = S[(e / a.d_k) * ldk + e % a.d_k];
         for (size_t e = tid; e < (size_t)(a.L - len) * nv; e += NT) // no token, no answer
-            io<T>::store(y + ((size_t)bh * a.L + len + e / nv) * a.d_v + n0 + e % nv, 0.f);
+            io<float>::store(y + ((size_t)bh * a.L + len + e / nv) * a.d_v + n0 + e % nv, 0.f);
     }
 }
 
 // ---------------------------------------------------------- reverse walk
-template <typename T>
 __global__ void __launch_bounds__(NT)
-    gated_reverse_kernel(GatedArgs a, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ dy,
+    gated_reverse_kernel(GatedArgs a, const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ dy,
                          const float *__restrict__ dWf, float *__restrict__ dW0, Ws ws) {
     extern __shared__ __align__(16) float sm[];
     const int ldk = a.d_k + 4, nC = (a.L + C - 1) / C;
@@ -498,11 +498,10 @@ __global__ void __launch_bounds__(NT)
 // One CTA per (chunk, key head); a warp owns 8 tokens (rows 8 w .. 8 w + 7)
 // and a lane 4 key channels, so every dot product over the key channels is
 // one warp reduction.
-template <typename T>
 __global__ void __launch_bounds__(NT)
-    gated_grad_kernel(GatedArgs a, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
-                      const T *__restrict__ dy, T *__restrict__ dq, T *__restrict__ dk, T *__restrict__ dv,
-                      T *__restrict__ dg, T *__restrict__ dbeta, Ws ws) {
+    gated_grad_kernel(GatedArgs a, const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
+                      const float *__restrict__ dy, float *__restrict__ dq, float *__restrict__ dk, float *__restrict__ dv,
+                      float *__restrict__ dg, float *__restrict__ dbeta, Ws ws) {
     extern __shared__ __align__(16) float sm[];
     const int ldk = a.d_k + 4, nC = gridDim.x, lv = NV + 4;
     float *kt = sm, *qt = kt + C * ldk, *accq = qt + C * ldk, *acck = accq + C * a.d_k, *S0 = acck + C * a.d_k,
@@ -518,16 +517,16 @@ __global__ void __launch_bounds__(NT)
     const int rows = min(C, a.L - c * C); // rows that exist in memory
     if (n <= 0) { // behind the sequence's end: no gradient
         for (int e = tid; e < rows * a.d_k; e += NT) {
-            io<T>::store(dq + krow + e, 0.f);
-            io<T>::store(dk + krow + e, 0.f);
+            io<float>::store(dq + krow + e, 0.f);
+            io<float>::store(dk + krow + e, 0.f);
         }
         for (int m = 0; m < grp; ++m) {
             const size_t r0 = (size_t)(bk * grp + m) * a.L + (size_t)c * C;
             for (int e = tid; e < rows * a.d_v; e += NT)
-                io<T>::store(dv + r0 * a.d_v + e, 0.f);
+                io<float>::store(dv + r0 * a.d_v + e, 0.f);
             for (int e = tid; e < rows; e += NT) {
-                io<T>::store(dg + r0 + e, 0.f);
-                io<T>::store(dbeta + r0 + e, 0.f);
+                io<float>::store(dg + r0 + e, 0.f);
+                io<float>::store(dbeta + r0 + e, 0.f);
             }
         }
         return;
@@ -579,8 +578,8 @@ __global__ void __launch_bounds__(NT)
                 if (i < n && lane < nv) {
                     const size_t at = (r0 + i) * a.d_v + n0 + lane;
                     const float x = Xt[i * lv + lane];
-                    xv[r] = fmaf(x, io<T>::load(v + at), xv[r]);
-                    io<T>::store(dv + at, tok[i * TOK + 6] * x);
+                    xv[r] = fmaf(x, io<float>::load(v + at), xv[r]);
+                    io<float>::store(dv + at, tok[i * TOK + 6] * x);
                 }
             }
         }
@@ -647,7 +646,7 @@ __global__ void __launch_bounds__(NT)
             if (lane == 0) {
                 red[i] = qa - be * kh - kw;
                 if (i < n)
-                    io<T>::store(dbeta + r0 + i, xvs - kh);
+                    io<float>::store(dbeta + r0 + i, xvs - kh);
             }
         }
         if (lane == 0)
@@ -667,15 +666,15 @@ __global__ void __launch_bounds__(NT)
             }
             const float after = run - (x0 + x1);
             if (2 * lane < n)
-                io<T>::store(dg + r0 + 2 * lane, run);
+                io<float>::store(dg + r0 + 2 * lane, run);
             if (2 * lane + 1 < n)
-                io<T>::store(dg + r0 + 2 * lane + 1, after + x1);
+                io<float>::store(dg + r0 + 2 * lane + 1, after + x1);
         }
         for (int e = n * a.d_v + tid; e < rows * a.d_v; e += NT)
-            io<T>::store(dv + r0 * a.d_v + e, 0.f);
+            io<float>::store(dv + r0 * a.d_v + e, 0.f);
         for (int i = n + tid; i < rows; i += NT) {
-            io<T>::store(dg + r0 + i, 0.f);
-            io<T>::store(dbeta + r0 + i, 0.f);
+            io<float>::store(dg + r0 + i, 0.f);
+            io<float>::store(dbeta + r0 + i, 0.f);
         }
     }
     __syncthreads();
@@ -698,15 +697,15 @@ __global__ void __launch_bounds__(NT)
         }
         if (on) {
             const float rk = i < n ? tok[i * TOK] : 0.f, rq = i < n ? tok[i * TOK + 1] : 0.f;
-            T *ok = dk + krow + (size_t)i * a.d_k + kc, *oq = dq + krow + (size_t)i * a.d_k + kc;
-            io<T>::store(ok, rk * (gk.x - kk.x * pk));
-            io<T>::store(ok + 1, rk * (gk.y - kk.y * pk));
-            io<T>::store(ok + 2, rk * (gk.z - kk.z * pk));
-            io<T>::store(ok + 3, rk * (gk.w - kk.w * pk));
-            io<T>::store(oq, rq * (gq.x - qq.x * pq));
-            io<T>::store(oq + 1, rq * (gq.y - qq.y * pq));
-            io<T>::store(oq + 2, rq * (gq.z - qq.z * pq));
-            io<T>::store(oq + 3, rq * (gq.w - qq.w * pq));
+            float *ok = dk + krow + (size_t)i * a.d_k + kc, *oq = dq + krow + (size_t)i * a.d_k + kc;
+            io<float>::store(ok, rk * (gk.x - kk.x * pk));
+            io<float>::store(ok + 1, rk * (gk.y - kk.y * pk));
+            io<float>::store(ok + 2, rk * (gk.z - kk.z * pk));
+            io<float>::store(ok + 3, rk * (gk.w - kk.w * pk));
+            io<float>::store(oq, rq * (gq.x - qq.x * pq));
+            io<float>::store(oq + 1, rq * (gq.y - qq.y * pq));
+            io<float>::store(oq + 2, rq * (gq.z - qq.z * pq));
+            io<float>::store(oq + 3, rq * (gq.w - qq.w * pq));
         }
     }
 }
@@ -717,51 +716,47 @@ size_t grad_smem(int d_k) {
     return sizeof(float) * (2 * (C + NV) * (d_k + 4) + 2 * C * d_k + 3 * C * (NV + 4) + 2 * C * LC + C * TOK + C + 16);
 }
 
-template <typename K> cudaError_t allow_smem(K *kern, size_t bytes) {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
-template <typename T>
-cudaError_t forward_t(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g, const void *beta,
+cudaError_t forward_f32(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g, const void *beta,
                       const float *W0, float *Wf, void *y, void *workspace, bool keep, bool backward, cudaStream_t st) {
     const int BH = a.B * a.H, nC = (a.L + C - 1) / C;
     const Ws ws = ws_at(workspace, ws_off(BH, a.L, a.d_k, a.d_v, backward));
-    cudaError_t e = allow_smem(gated_prep_kernel<T>, prep_smem(a.d_k));
+    static std::atomic<uint64_t> allowed_prep{0}, allowed_walk[2];
+    cudaError_t e = allow_smem(gated_prep_kernel, allowed_prep);
     if (e != cudaSuccess)
         return e;
-    e = launch_pdl(gated_prep_kernel<T>, dim3(nC, BH), dim3(NT), prep_smem(a.d_k), st, a, (const T *)q, (const T *)k,
-                   (const T *)g, (const T *)beta, ws);
+    e = launch_pdl(gated_prep_kernel, dim3(nC, BH), dim3(NT), prep_smem(a.d_k), st, a, (const float *)q, (const float *)k,
+                   (const float *)g, (const float *)beta, ws);
     if (e != cudaSuccess)
         return e;
-    auto *walk = keep ? gated_walk_kernel<T, true> : gated_walk_kernel<T, false>;
-    e = allow_smem(walk, walk_smem(a.d_k));
+    auto *walk = keep ? gated_walk_kernel<true> : gated_walk_kernel<false>;
+    e = allow_smem(walk, allowed_walk[keep]);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(walk, dim3((a.d_v + NV - 1) / NV, BH), dim3(NT), walk_smem(a.d_k), st, a, (const T *)q,
-                      (const T *)k, (const T *)v, W0, Wf, (T *)y, ws);
+    return launch_pdl(walk, dim3((a.d_v + NV - 1) / NV, BH), dim3(NT), walk_smem(a.d_k), st, a, (const float *)q,
+                      (const float *)k, (const float *)v, W0, Wf, (float *)y, ws);
 }
 
-template <typename T>
-cudaError_t backward_t(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g,
+cudaError_t backward_f32(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g,
                        const void *beta, const float *W0, const void *dy, const float *dWf, void *dq, void *dk,
                        void *dv, void *dg, void *dbeta, float *dW0, void *workspace, cudaStream_t st) {
     const int BH = a.B * a.H, nC = (a.L + C - 1) / C;
     const Ws ws = ws_at(workspace, ws_off(BH, a.L, a.d_k, a.d_v, true));
-    cudaError_t e = forward_t<T>(a, q, k, v, g, beta, W0, nullptr, nullptr, workspace, true, true, st);
+    cudaError_t e = forward_f32(a, q, k, v, g, beta, W0, nullptr, nullptr, workspace, true, true, st);
     if (e != cudaSuccess)
         return e;
-    e = allow_smem(gated_reverse_kernel<T>, walk_smem(a.d_k));
+    static std::atomic<uint64_t> allowed_reverse{0}, allowed_grad{0};
+    e = allow_smem(gated_reverse_kernel, allowed_reverse);
     if (e != cudaSuccess)
         return e;
-    e = launch_pdl(gated_reverse_kernel<T>, dim3((a.d_v + NV - 1) / NV, BH), dim3(NT), walk_smem(a.d_k), st, a,
-                   (const T *)q, (const T *)k, (const T *)dy, dWf, dW0, ws);
+    e = launch_pdl(gated_reverse_kernel, dim3((a.d_v + NV - 1) / NV, BH), dim3(NT), walk_smem(a.d_k), st, a,
+                   (const float *)q, (const float *)k, (const float *)dy, dWf, dW0, ws);
     if (e != cudaSuccess)
         return e;
-    e = allow_smem(gated_grad_kernel<T>, grad_smem(a.d_k));
+    e = allow_smem(gated_grad_kernel, allowed_grad);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(gated_grad_kernel<T>, dim3(nC, a.B * a.Hk), dim3(NT), grad_smem(a.d_k), st, a, (const T *)q,
-                      (const T *)k, (const T *)v, (const T *)dy, (T *)dq, (T *)dk, (T *)dv, (T *)dg, (T *)dbeta, ws);
+    return launch_pdl(gated_grad_kernel, dim3(nC, a.B * a.Hk), dim3(NT), grad_smem(a.d_k), st, a, (const float *)q,
+                      (const float *)k, (const float *)v, (const float *)dy, (float *)dq, (float *)dk, (float *)dv, (float *)dg, (float *)dbeta, ws);
 }
 
 } // namespace
@@ -785,7 +780,7 @@ cudaError_t launch_gated_forward(const GatedArgs &a, const void *q, const void *
                                  const void *beta, const float *W0, float *Wf, void *y, void *workspace, int bf16,
                                  cudaStream_t st) {
     return bf16 ? gated_tc_forward(a, q, k, v, g, beta, W0, Wf, y, workspace, st)
-                : forward_t<float>(a, q, k, v, g, beta, W0, Wf, y, workspace, false, false, st);
+                : forward_f32(a, q, k, v, g, beta, W0, Wf, y, workspace, false, false, st);
 }
 
 cudaError_t launch_gated_backward(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g,
@@ -793,7 +788,7 @@ cudaError_t launch_gated_backward(const GatedArgs &a, const void *q, const void 
                                   void *dk, void *dv, void *dg, void *dbeta, float *dW0, void *workspace, int bf16,
                                   cudaStream_t st) {
     if (!bf16)
-        return backward_t<float>(a, q, k, v, g, beta, W0, dy, dWf, dq, dk, dv, dg, dbeta, dW0, workspace, st);
+        return backward_f32(a, q, k, v, g, beta, W0, dy, dWf, dq, dk, dv, dg, dbeta, dW0, workspace, st);
     const cudaError_t e = gated_tc_walks(a, q, k, v, g, beta, W0, dy, dWf, dW0, workspace, st);
     return e != cudaSuccess ? e : gated_tc_grad(a, q, k, v, dy, dq, dk, dv, dg, dbeta, workspace, st);
 }

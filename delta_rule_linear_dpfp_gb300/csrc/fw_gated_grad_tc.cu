@@ -511,9 +511,8 @@ cudaError_t launch(const GatedArgs &a, const void *q, const void *k, const void 
                    cudaStream_t st) {
     auto *kern = gated_tc_grad_kernel<NKB>;
     const uint32_t smem = grad_smem(NKB).bytes;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(kern, allowed);
     if (e != cudaSuccess)
         return e;
     return launch_pdl(kern, dim3(rec.nch, a.B * a.Hk), dim3(NT), smem, st, a, (const bf *)q, (const bf *)k,

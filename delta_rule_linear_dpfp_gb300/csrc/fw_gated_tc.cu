@@ -824,13 +824,6 @@ __global__ void __launch_bounds__(kWalkThreads)
         tmem_dealloc(tm, 128);
 }
 
-template <typename K> cudaError_t allow_smem(K *kern, size_t bytes) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-    return e;
-}
-
 template <bool BWD, int NKB>
 cudaError_t launch_prep(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g,
                         const void *beta, const void *dy, void *ws, const GatedRecord &rec, unsigned *status,
@@ -838,7 +831,8 @@ cudaError_t launch_prep(const GatedArgs &a, const void *q, const void *k, const 
     using bf = __nv_bfloat16;
     auto *kern = gated_tc_prep_kernel<BWD, NKB>;
     const uint32_t smem = prep_smem(NKB, (a.d_v + 63) / 64).bytes;
-    cudaError_t e = allow_smem(kern, smem);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(kern, allowed);
     if (e != cudaSuccess)
         return e;
     // 128 columns for A1's product, d_v for A2's (MT's 64 lie there first)
@@ -853,7 +847,8 @@ cudaError_t launch_walk(const GatedArgs &a, const void *dy, const float *Z0, flo
     using bf = __nv_bfloat16;
     auto *kern = gated_tc_walk_kernel<MODE, NKB>;
     const uint32_t smem = Walk<MODE, NKB>::bytes;
-    cudaError_t e = allow_smem(kern, smem);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(kern, allowed);
     if (e != cudaSuccess)
         return e;
     return launch_pdl(kern, dim3(rec.ns, a.B * a.H), dim3(kWalkThreads), smem, st, a, (const bf *)dy, Z0, Zf, (bf *)y,
