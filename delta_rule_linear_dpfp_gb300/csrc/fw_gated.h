@@ -38,9 +38,9 @@ struct NormArgs {
 };
 size_t group_norm_backward_workspace_bytes(int B, int H, int L, int d);
 cudaError_t launch_group_norm(const NormArgs &a, const void *x, const void *gate, const float *gamma,
-                              const float *beta, void *out, int bf16, int num_sms, cudaStream_t st);
+                              const float *beta, void *out, int bf16, cudaStream_t st);
 cudaError_t launch_group_norm_backward(const NormArgs &a, const void *x, const void *gate, const float *gamma,
                                        const float *beta, const void *dout, void *dx, void *dgate, float *dgamma,
-                                       float *dbeta, void *workspace, int bf16, int num_sms, cudaStream_t st);
+                                       float *dbeta, void *workspace, int bf16, cudaStream_t st);
 
 } // namespace fw

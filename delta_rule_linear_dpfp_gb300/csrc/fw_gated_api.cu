@@ -8,10 +8,6 @@
 #include <climits>
 #include <cmath>
 
-namespace fw {
-cudaError_t device_sms(int *out); // fw_api.cu
-} // namespace fw
-
 namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -37,7 +33,7 @@ int check_norm(int B, int H, int L, int d, int act, int io_dtype, float eps) {
     if (B < 0 || H < 0 || L < 0 || d <= 0 || act < FW_ACT_NONE || act > FW_ACT_GELU || !dtype_ok(io_dtype) ||
         !std::isfinite(eps) || eps < 0.f)
         return FW_ERR_INVALID_ARG;
-    if (d % 8 || d > 256 || H > kMaxHeads || (int64_t)H * d > INT_MAX / 2 || (int64_t)B * H > INT_MAX)
+    if (d % 8 || d > 256 || H > kMaxHeads || (int64_t)H * d > INT_MAX / 2 || (int64_t)B * L > INT_MAX)
         return FW_ERR_UNSUPPORTED;
     return FW_OK;
 }
@@ -143,11 +139,8 @@ FW_API int fw_group_norm_act(const void *x, const void *gate, const float *gamma
         return FW_OK;
     if (!usable(x) || !usable(gamma) || !usable(beta) || !usable(out) || (gate && !aligned16(gate)))
         return FW_ERR_INVALID_ARG;
-    int sms = 0;
-    if (fw::device_sms(&sms) != cudaSuccess)
-        return FW_ERR_CUDA;
     const fw::NormArgs a{B, H, L, d, act, eps};
-    return cuda_status(fw::launch_group_norm(a, x, gate, gamma, beta, out, io_dtype == FW_DTYPE_BF16, sms,
+    return cuda_status(fw::launch_group_norm(a, x, gate, gamma, beta, out, io_dtype == FW_DTYPE_BF16,
                                              static_cast<cudaStream_t>(stream)));
 }
 
@@ -178,12 +171,9 @@ FW_API int fw_group_norm_act_backward(const void *x, const void *gate, const flo
         (gate && (!aligned16(gate) || !usable(dgate))) || (!gate && dgate) || !usable(workspace) ||
         workspace_bytes < fw_group_norm_act_backward_workspace_size(B, H, L, d))
         return FW_ERR_INVALID_ARG;
-    int sms = 0;
-    if (fw::device_sms(&sms) != cudaSuccess)
-        return FW_ERR_CUDA;
     const fw::NormArgs a{B, H, L, d, act, eps};
     return cuda_status(fw::launch_group_norm_backward(a, x, gate, gamma, beta, dout, dx, dgate, dgamma, dbeta,
-                                                      workspace, io_dtype == FW_DTYPE_BF16, sms, st));
+                                                      workspace, io_dtype == FW_DTYPE_BF16, st));
 }
 
 } // extern "C"

@@ -526,7 +526,8 @@ typedef enum fw_act {
  *   gate        : [B, L, H d]   io_dtype, or NULL
  *   gamma, beta : [H d]         fp32
  *   out         : [B, L, H d]   io_dtype, token-major      (written)
- *   d a multiple of 8 up to 256 (FW_ERR_UNSUPPORTED otherwise).
+ *   d a multiple of 8 up to 256, H <= 65535, B L < 2^31 (FW_ERR_UNSUPPORTED
+ *   otherwise).
  */
 FW_API int fw_group_norm_act(const void *x, const void *gate, const float *gamma, const float *beta, void *out,
                              int B, int H, int L, int d, int act, int io_dtype, float eps, void *stream);
