@@ -175,10 +175,10 @@ FW_DEV uint64_t at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); 
 // tile (K-major, 128 rows; its first 64 rows also serve as the MN-major K),
 // an operand region (M and T as hi and lo tiles, then the stacked 128 x 64
 // matrices A1 and A2 in turn), the fp32 A / T work space (A's place is V's,
-// then dY's, later), per-token scalars.  What a product leaves goes back
-// through shared memory, from the operand region on, and out in bulk copies:
-// a row per lane stored directly costs a sector for every 16 bytes (measured:
-// 4400 of 37 000 cycles a chunk).
+// then dY's, later), per-token scalars.  What a product leaves goes out by
+// warps: 32 rows are staged as 4 KB that lie together in the record too, and
+// one lane sends them (stored from registers, a row per lane, every 16 bytes
+// cost a sector: 8000 of a chunk's 20 000 cycles).
 struct PrepSmem {
     uint32_t kq, op, at, tt, tok, bar, bytes;
 };
@@ -194,8 +194,6 @@ __host__ __device__ inline PrepSmem prep_smem(int nkb, int nvb) {
     s.bytes = s.bar + 64 + 1024;
     return s;
 }
-constexpr uint32_t kStage = 65536; // bytes staged at once from the operand region on
-static_assert(32768 + C * LC * 8 + 4096 >= kStage, "op, at and tt hold a staged 64 KB");
 
 template <bool BWD, int NKB>
 __global__ void __launch_bounds__(NT, 2)
@@ -229,7 +227,7 @@ __global__ void __launch_bounds__(NT, 2)
         mbar_init(bar, 1);
         fence_barrier_init();
     }
-    // [K; Q], 16 bytes a thread and step; the row's lanes add its squares
+    // [K; Q], 16 bytes a thread and step
     {
         constexpr int PER = DKP / 8, STEPS = 2 * C * PER / NT; // chunks per row; 4 or 8 steps
         const __nv_bfloat16 *kg = k + ((size_t)kh * a.L + (size_t)c * C) * a.d_k;
@@ -277,18 +275,6 @@ __global__ void __launch_bounds__(NT, 2)
         for (int s = 0; s < STEPS; ++s) {
             const int row = (s * NT + tid) / PER;
             *reinterpret_cast<uint4 *>(kq + kmajor_chunk(row, ch * 8, 128)) = u[s];
-            float x[8], ss = 0.f;
-            widen8(u[s], x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-            for (int m = PER / 2; m > 0; m >>= 1)
-                ss += __shfl_xor_sync(0xffffffffu, ss, m);
-            if (ch == 0) {
-                ss += a.eps;
-                tok[(row & 63) * 8 + (row < C ? 2 : 4)] = !a.l2norm ? 1.f : ss > 0.f ? 1.f / sqrtf(ss) : ss;
-            }
         }
     }
     fence_async_smem();
@@ -316,11 +302,11 @@ __global__ void __launch_bounds__(NT, 2)
     const uint64_t dOp = desc_sw128(smem_u32(op), 16, 1024), dOpMn = desc_sw128(smem_u32(op), 8192, 1024);
     const uint64_t dV = desc_sw128(smem_u32(vt), 8192, 1024);
     uint8_t *out = ws + rec.off(bh, c);
-    if (tid == 0) { // K K^T (rows 0-63) and Q K^T
+    if (tid == 0) { // K K^T (rows 0-63), Q K^T and Q Q^T: the diagonals are the rows' squared lengths
 #pragma unroll
         for (int s = 0; s < 4 * NKB; ++s) {
             const uint64_t d = at(dKmaj, kmajor_step(s, 128));
-            mma_bf16(tGram, d, d, idesc_bf16(128, 64, 0, 0), s > 0);
+            mma_bf16(tGram, d, d, idesc_bf16(128, 128, 0, 0), s > 0);
         }
         mma_commit(bar);
         // the K (and Q) image for the walk, straight from the tile
@@ -335,6 +321,18 @@ __global__ void __launch_bounds__(NT, 2)
     }
     finish();
     const int rr = 32 * (w & 3) + lane, half = w >> 2, i = rr & 63;
+    if (half == 0) { // 1 / length (0 for a row of zeros)
+        float x[32], ss = 0.f;
+        tmem_ld16(tGram + tmem_lane_base(w) + (uint32_t)(32 * w), x);
+        tmem_ld16(tGram + tmem_lane_base(w) + (uint32_t)(32 * w + 16), x + 16);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            ss = e == lane ? x[e] : ss;
+        ss += a.eps;
+        tok[i * 8 + (rr < C ? 2 : 4)] = !a.l2norm ? 1.f : ss > 0.f ? 1.f / sqrtf(ss) : ss;
+    }
+    __syncthreads();
     {
         const float4 di = *reinterpret_cast<const float4 *>(tok + i * 8);
         const float fi = rr < C ? di.w * di.z : a.scale * tok[i * 8 + 4];
@@ -447,40 +445,36 @@ __global__ void __launch_bounds__(NT, 2)
             mma_commit(bar);
         }
     };
+    auto load_rows = [&](const __nv_bfloat16 *src) { // V or dY, MN-major 64-channel blocks
+        const __nv_bfloat16 *sg = src + ((size_t)bh * a.L + (size_t)c * C) * a.d_v;
+        for (int e = tid; e < C * nvb * 8; e += 2 * NT) { // (two 64-channel halves of a row pair: 2 NT divides C nvb 8)
+            uint4 u[2];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int r = (e + m * NT) / (nvb * 8), ch = (e + m * NT) % (nvb * 8);
+                u[m] = make_uint4(0, 0, 0, 0);
+                if (r < n && ch * 8 < a.d_v)
+                    u[m] = __ldcg(reinterpret_cast<const uint4 *>(sg + (size_t)r * a.d_v) + ch);
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int r = (e + m * NT) / (nvb * 8), ch = (e + m * NT) % (nvb * 8);
+                *reinterpret_cast<uint4 *>(vt + kmajor_chunk(r, ch * 8, 64)) = u[m];
+            }
+        }
+    };
     float x2[32];
     factor(true, x2);
     put(x2);
     hand_over();
     multiply(tA1, dKmn, idesc_bf16(128, DKP, 0, 1)); // [-W'; ...] or [-W'; W"]
-    factor(false, x2); // A2's rows wait in registers: A1's image takes the place of T
+    load_rows(v); // A's place
+    factor(false, x2);
     finish();
-    __syncthreads();
-    for (int p = half; p < DKP / 16; p += 2) { // the product's rows as hi and lo images
-        const int c0 = 16 * p;
-        float x[16];
-        tmem_ld16(tA1 + tmem_lane_base(w) + (uint32_t)c0, x);
-        tmem_ld_wait();
-        if (!BWD && rr >= C) {
-            const float f = a.scale * tok[i * 8 + 5] * tok[i * 8 + 4];
-#pragma unroll
-            for (int e = 0; e < 16; e += 8) {
-                float y[8];
-                widen8(*reinterpret_cast<const uint4 *>(kq + kmajor_chunk(rr, c0 + e, 128)), y);
-#pragma unroll
-                for (int m = 0; m < 8; ++m)
-                    x[e + m] = fmaf(f, y[m], x[e + m]);
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < 16; e += 8) {
-            uint4 hi, lo;
-            split8(x + e, hi, lo);
-            uint8_t *to = BWD ? op + (rr < C ? 0 : NKB * 16384) + kmajor_chunk(i, c0 + e, 64)
-                              : op + kmajor_chunk(rr, c0 + e, 128);
-            *reinterpret_cast<uint4 *>(to) = hi;
-            *reinterpret_cast<uint4 *>(to + NKB * (BWD ? 8192 : 16384)) = lo;
-        }
-    }
+    put(x2);
+    hand_over();
+    const uint32_t idv = idesc_bf16(128, a.d_v, 0, 1);
+    multiply(tA2, dV, idv);
     if (tid < C) { // the walks' scalars
         const float *d = tok + tid * 8;
         float *sf = reinterpret_cast<float *>(out + rec.scalF);
@@ -498,67 +492,121 @@ __global__ void __launch_bounds__(NT, 2)
             st[1] = reinterpret_cast<const float4 *>(d)[1];
         }
     }
-    auto ship = [&](size_t to, const uint8_t *from, uint32_t bytes) { // staged bytes out; their place is free after
-        fence_async_smem();
-        tc_fence_before();
-        __syncthreads();
-        if (tid == 0) {
-            bulk_s2g(out + to, from, bytes);
-            bulk_commit();
-            bulk_wait_read();
-        }
-        __syncthreads();
-        tc_fence_after();
-    };
-    ship(BWD ? rec.AF : rec.A, op, (uint32_t)NKB * 32768u);
-    put(x2);
-    auto load_rows = [&](const __nv_bfloat16 *src) { // V or dY, MN-major 64-channel blocks
-        const __nv_bfloat16 *sg = src + ((size_t)bh * a.L + (size_t)c * C) * a.d_v;
-        for (int e = tid; e < C * nvb * 8; e += NT) {
-            const int r = e / (nvb * 8), ch = e % (nvb * 8);
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (r < n && ch * 8 < a.d_v)
-                u = __ldcg(reinterpret_cast<const uint4 *>(sg + (size_t)r * a.d_v) + ch);
-            *reinterpret_cast<uint4 *>(vt + kmajor_chunk(r, ch * 8, 64)) = u;
-        }
-    };
-    load_rows(v);
-    hand_over();
-    const uint32_t idv = idesc_bf16(128, a.d_v, 0, 1);
-    multiply(tA2, dV, idv);
     finish();
-    // rows [r0, r0 + R) of the product as pieces [16 channels][R rows][16] fp32, `most` channels at a time
-    auto rows_out = [&](size_t to, int R, int r0, uint8_t *place, int most) {
-        for (int d0 = 0; d0 < a.d_v; d0 += most) {
-            const int np = min(most, a.d_v - d0) / 16;
-            for (int p = half; p < np; p += 2) {
-                float x[16];
-                tmem_ld16(tA2 + tmem_lane_base(w) + (uint32_t)(d0 + 16 * p), x);
-                tmem_ld_wait();
-                if (rr >= r0 && rr < r0 + R) {
-                    uint8_t *s = place + (size_t)p * R * 64;
+    // rows [r0, r0 + R) of the product as pieces [16 channels][R rows][16]
+    // fp32: a warp stages two pieces of its rows at a time and sends them
+    uint8_t *mine = (NKB == 2 ? kq : vt) + w * 4096; // (NKB 2: these rows of K and Q are this warp's own)
+    auto sent = [&]() { // what this warp sent has left its place
+        if (lane == 0)
+            bulk_wait_read();
+        __syncwarp();
+    };
+    auto rows_out = [&](size_t to, int R, int r0) {
+        if (rr < r0 || rr >= r0 + R)
+            return;
+        for (int p0 = half; p0 < a.d_v / 16; p0 += 4) {
+            sent();
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        *reinterpret_cast<float4 *>(s + piece_chunk(rr - r0, e)) =
-                            make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+            for (int e = 0; e < 2; ++e) {
+                const int p = p0 + 2 * e;
+                if (p >= a.d_v / 16)
+                    break;
+                float x[16];
+                tmem_ld16(tA2 + tmem_lane_base(w) + (uint32_t)(16 * p), x);
+                tmem_ld_wait();
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    *reinterpret_cast<float4 *>(mine + 2048 * e + piece_chunk(lane, m)) =
+                        make_float4(x[4 * m], x[4 * m + 1], x[4 * m + 2], x[4 * m + 3]);
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (p0 + 2 * e < a.d_v / 16)
+                        bulk_s2g(out + to + ((size_t)(p0 + 2 * e) * R + 32 * (w & 3) - r0) * 64, mine + 2048 * e, 2048);
+                bulk_commit();
+            }
+        }
+    };
+    // the first product's rows as hi and lo images
+    auto images_out = [&]() {
+        uint8_t *hi_at = NKB == 2 ? op + w * 4096 : op, *lo_at = NKB == 2 ? vt + w * 4096 : op + 16384;
+#pragma unroll
+        for (int p = 0; p < DKP / 32; ++p) {
+            const int c0 = half * (DKP / 2) + 16 * p;
+            float x[16];
+            tmem_ld16(tA1 + tmem_lane_base(w) + (uint32_t)c0, x);
+            tmem_ld_wait();
+            if (!BWD && rr >= C) {
+                const float f = a.scale * tok[i * 8 + 5] * tok[i * 8 + 4];
+#pragma unroll
+                for (int e = 0; e < 16; e += 8) {
+                    float y[8];
+                    widen8(*reinterpret_cast<const uint4 *>(kq + kmajor_chunk(rr, c0 + e, 128)), y);
+#pragma unroll
+                    for (int m = 0; m < 8; ++m)
+                        x[e + m] = fmaf(f, y[m], x[e + m]);
                 }
             }
-            ship(to + (size_t)d0 * R * 4, place, (uint32_t)(np * R * 64));
+#pragma unroll
+            for (int e = 0; e < 16; e += 8) {
+                uint4 hi, lo;
+                split8(x + e, hi, lo);
+                const uint32_t to = kmajor_chunk(NKB == 2 ? lane : rr, (c0 + e) & 63, 128); // (one 64-wide block)
+                *reinterpret_cast<uint4 *>(hi_at + to) = hi;
+                *reinterpret_cast<uint4 *>(lo_at + to) = lo;
+            }
+        }
+        fence_async_smem();
+        if (NKB == 2) { // this warp's rows of block `half`
+            __syncwarp();
+            if (lane == 0) {
+                uint8_t *to = BWD ? out + (rr < C ? rec.AF : rec.AR) + half * 8192 + (w & 1) * 4096
+                                  : out + rec.A + half * 16384 + (w & 3) * 4096;
+                bulk_s2g(to, hi_at, 4096);
+                bulk_s2g(to + NKB * (BWD ? 8192 : 16384), lo_at, 4096);
+                bulk_commit();
+            }
+        } else { // two warps share a row
+            __syncthreads();
+            if (tid == 0) {
+                if (BWD) {
+                    bulk_s2g(out + rec.AF, op, 8192);
+                    bulk_s2g(out + rec.AF + 8192, op + 16384, 8192);
+                    bulk_s2g(out + rec.AR, op + 8192, 8192);
+                    bulk_s2g(out + rec.AR + 8192, op + 24576, 8192);
+                } else {
+                    bulk_s2g(out + rec.A, op, 32768);
+                }
+                bulk_commit();
+            }
         }
     };
+    if (tid == 0)
+        bulk_wait_read(); // the K (and Q) image has left
+    __syncthreads();
     if (!BWD) {
-        __syncthreads();
-        rows_out(rec.base, 128, 0, op, (int)kStage / 512);
+        images_out();
+        rows_out(rec.base, 128, 0);
     } else {
-        rows_out(rec.baseU, C, 0, kq, NKB * 64); // (K and Q left with the first copies: ship() waited for all)
-        load_rows(dy);                          // V's place
+        if (NKB == 2) {
+            rows_out(rec.baseU, C, 0);
+            load_rows(dy); // V's place
+        } else { // one place for both
+            rows_out(rec.baseU, C, 0);
+            sent();
+            __syncthreads();
+            load_rows(dy);
+        }
         hand_over();
         multiply(tA2, dV, idv);
         finish();
-        __syncthreads();
-        rows_out(rec.baseX, C, C, op, (int)kStage / 256);
+        images_out();
+        rows_out(rec.baseX, C, C);
     }
-    if (tid == 0)
+    if (lane == 0)
         bulk_wait_all();
     tc_fence_before();
     __syncthreads();
@@ -585,7 +633,7 @@ template <int MODE, int NKB> struct Walk {
     static constexpr uint32_t b = A, scal = b + B, base = scal + 1024, rec = base + R * 128;
     // A 128-row MMA reads 8 KB past a tile of 64 rows and a product of one
     // 64-wide block reads one more: what follows in this order covers both.
-    static constexpr uint32_t z = 2 * rec, u = z + NKB * 8192, bar = u + RB * 128, bytes = bar + 64 + 1024;
+    static constexpr uint32_t z = 2 * rec, u = z + NKB * 8192, bar = u + RB * 128, bytes = bar + 128 + 1024;
     static_assert(rec + b + B + (NKB == 1 ? B : 0) <= bar && bytes <= 232448, "reads stay inside shared memory");
 };
 
@@ -599,9 +647,9 @@ __global__ void __launch_bounds__(kWalkThreads)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *zt = sm + L::z, *ut = sm + L::u;
-    uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::bar), *m1 = full + 2, *m2 = full + 3, *zr = full + 4,
-             *ur = full + 5;
-    uint32_t *slot = reinterpret_cast<uint32_t *>(full + 6);
+    uint64_t *fullA = reinterpret_cast<uint64_t *>(sm + L::bar), *fullB = fullA + 2, *m1 = fullA + 4, *m2 = fullA + 5,
+             *zr = fullA + 6, *ur = fullA + 7;
+    uint32_t *slot = reinterpret_cast<uint32_t *>(fullA + 8);
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, sl = blockIdx.x, bh = blockIdx.y, n0 = sl * NV;
     const int b = bh / a.H;
     griddep_wait();
@@ -611,8 +659,8 @@ __global__ void __launch_bounds__(kWalkThreads)
         tmem_relinquish();
     }
     if (tid == 32) {
-        for (int e = 0; e < 6; ++e)
-            mbar_init(full + e, e < 4 ? 1 : NT / 32);
+        for (int e = 0; e < 8; ++e)
+            mbar_init(fullA + e, e < 6 ? 1 : e == 7 && MODE != kRev ? NT / 64 : NT / 32);
         fence_barrier_init();
     }
     tc_fence_before();
@@ -629,16 +677,23 @@ __global__ void __launch_bounds__(kWalkThreads)
     if (w == NT / 32) {
         if (lane == 0 && nch > 0) {
             const uint32_t pieces = (uint32_t)min(2, (a.d_v - n0) / 16);
-            auto fetch = [&](int it) { // a chunk's record
+            // a chunk's A, and the rest of its record: each as soon as the
+            // product that last read its place is done
+            auto fetch_a = [&](int it) {
+                mbar_arrive_expect_tx(fullA + (it & 1), L::A);
+                bulk_g2s(sm + (it & 1) * L::rec,
+                         ws + rec.off(bh, chunk_of(it)) + (MODE == kFwd ? rec.A : MODE == kKeep ? rec.AF : rec.AR), L::A,
+                         fullA + (it & 1));
+            };
+            auto fetch_b = [&](int it) {
                 const uint8_t *src = ws + rec.off(bh, chunk_of(it));
                 uint8_t *dst = sm + (it & 1) * L::rec;
-                uint64_t *f = full + (it & 1);
+                uint64_t *f = fullB + (it & 1);
                 const uint32_t base = pieces * L::R * 64;
-                mbar_arrive_expect_tx(f, L::A + L::B + L::SCAL + base);
-                if (MODE == kFwd) { // A, K and the scalars are one piece
-                    bulk_g2s(dst, src + rec.A, L::A + L::B + L::SCAL, f);
+                mbar_arrive_expect_tx(f, L::B + L::SCAL + base);
+                if (MODE == kFwd) { // K and the scalars are one piece
+                    bulk_g2s(dst + L::b, src + rec.K, L::B + L::SCAL, f);
                 } else {
-                    bulk_g2s(dst, src + (MODE == kKeep ? rec.AF : rec.AR), L::A, f);
                     if (MODE == kKeep) {
 #pragma unroll
                         for (int kb = 0; kb < NKB; ++kb)
@@ -652,15 +707,16 @@ __global__ void __launch_bounds__(kWalkThreads)
                          src + (MODE == kFwd ? rec.base : MODE == kKeep ? rec.baseU : rec.baseX) + (size_t)sl * L::R * 128,
                          base, f);
             };
-            fetch(0);
-            if (nch > 1)
-                fetch(1);
+            for (int it = 0; it < min(2, nch); ++it) {
+                fetch_a(it);
+                fetch_b(it);
+            }
             const uint64_t dz = desc_sw128(smem_u32(zt), 8192, 1024), du = desc_sw128(smem_u32(ut), 8192, 1024);
             const uint64_t dA0 = desc_sw128(smem_u32(sm), 16, 1024);
             const uint64_t dB0 = desc_sw128(smem_u32(sm + L::b), L::RB * 128, 1024);
             for (int it = 0; it < nch && ok; ++it) {
                 const uint64_t dA = at(dA0, (uint32_t)(it & 1) * L::rec), dB = at(dB0, (uint32_t)(it & 1) * L::rec);
-                wait(full + (it & 1), (it >> 1) & 1);
+                wait(fullA + (it & 1), (it >> 1) & 1);
                 wait(zr, it & 1);
                 if (!ok)
                     break;
@@ -679,7 +735,8 @@ __global__ void __launch_bounds__(kWalkThreads)
                     bulk_commit();
                 }
                 if (it > 0 && it + 1 < nch)
-                    fetch(it + 1); // the workers are through with the previous chunk
+                    fetch_b(it + 1); // the workers are through with the previous chunk
+                wait(fullB + (it & 1), (it >> 1) & 1);
                 wait(ur, it & 1);
                 if (!ok)
                     break;
@@ -691,12 +748,14 @@ __global__ void __launch_bounds__(kWalkThreads)
                     mma_bf16(tD2, at(dB, (uint32_t)s * 2048u), at(du, (uint32_t)s * 2048u), idesc_bf16(128, 64, 1, 1),
                              s > 0);
                 mma_commit(m2);
+                if (it + 2 < nch)
+                    fetch_a(it + 2); // the workers have seen this chunk's first product
             }
             if (MODE != kFwd)
                 bulk_wait_all();
             if (!ok) // a wait gave up: let the records that were asked for land first
-                for (int e = 0; e < 2; ++e)
-                    (void)mbar_wait(full + e, 0, status);
+                for (int e = 0; e < 4; ++e)
+                    (void)mbar_wait(fullA + e, 0, status);
         }
         __syncwarp();
     } else {
@@ -743,7 +802,7 @@ __global__ void __launch_bounds__(kWalkThreads)
             const int c = chunk_of(it), n = min(C, len - c * C);
             const uint8_t *r = sm + (it & 1) * L::rec;
             uint8_t *gr = ws + rec.off(bh, c);
-            wait(full + (it & 1), (it >> 1) & 1);
+            wait(fullB + (it & 1), (it >> 1) & 1);
             const float *scal = reinterpret_cast<const float *>(r + L::scal);
             const float whole = scal[MODE == kRev ? 2 * C : C], f = scal[MODE == kRev && rr >= C ? C + i : i];
             if (MODE == kRev && rr >= C) { // dY's rows do not wait for the product
@@ -784,7 +843,8 @@ __global__ void __launch_bounds__(kWalkThreads)
                     put(ut, i, t0);
                 }
             }
-            written(ur);
+            if (MODE == kRev || rr < C)
+                written(ur);
             if (MODE == kFwd && rr >= C) {
                 if (mine && i < n) {
                     __nv_bfloat16 *to = y + ((size_t)bh * a.L + (size_t)c * C + i) * a.d_v + n0 + 16 * hf;
