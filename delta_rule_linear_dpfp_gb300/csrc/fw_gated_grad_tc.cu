@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(NT)
     };
     if (tid == 0) {
         mbar_arrive_expect_tx(kqb, NKB * 16384);
-        bulk_g2s(kq, record(0) + rec.KQ, NKB * 16384, kqb);
+        bulk_g2s(kq, record(0) + rec.K, NKB * 16384, kqb);
     }
     const uint32_t kq_s = smem_u32(kq), ef_s = smem_u32(ef);
     // a thread's part of the sums over the value heads: row i, channels half * HC ..

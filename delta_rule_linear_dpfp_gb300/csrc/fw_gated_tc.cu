@@ -310,8 +310,8 @@ __global__ void __launch_bounds__(NT, 2)
         }
         mma_commit(bar);
         // the K (and Q) image for the walk, straight from the tile
-        if (BWD) {
-            bulk_s2g(out + rec.KQ, kq, (uint32_t)NKB * 16384u);
+        if (BWD) { // (blocks of 128 rows)
+            bulk_s2g(out + rec.K, kq, (uint32_t)NKB * 16384u);
         } else {
 #pragma unroll
             for (int kb = 0; kb < NKB; ++kb)
@@ -530,9 +530,11 @@ __global__ void __launch_bounds__(NT, 2)
             }
         }
     };
-    // the first product's rows as hi and lo images
+    // the first product's rows as images: per 64-wide block 64 hi rows, then
+    // the same 64 rows' lo terms
     auto images_out = [&]() {
-        uint8_t *hi_at = NKB == 2 ? op + w * 4096 : op, *lo_at = NKB == 2 ? vt + w * 4096 : op + 16384;
+        uint8_t *hi_at = NKB == 2 ? op + w * 4096 : op + (rr < C ? 0 : 16384),
+                *lo_at = NKB == 2 ? vt + w * 4096 : hi_at + 8192;
 #pragma unroll
         for (int p = 0; p < DKP / 32; ++p) {
             const int c0 = half * (DKP / 2) + 16 * p;
@@ -554,7 +556,7 @@ __global__ void __launch_bounds__(NT, 2)
             for (int e = 0; e < 16; e += 8) {
                 uint4 hi, lo;
                 split8(x + e, hi, lo);
-                const uint32_t to = kmajor_chunk(NKB == 2 ? lane : rr, (c0 + e) & 63, 128); // (one 64-wide block)
+                const uint32_t to = kmajor_chunk(NKB == 2 ? lane : i, (c0 + e) & 63, 64); // (one 64-wide block)
                 *reinterpret_cast<uint4 *>(hi_at + to) = hi;
                 *reinterpret_cast<uint4 *>(lo_at + to) = lo;
             }
@@ -563,23 +565,15 @@ __global__ void __launch_bounds__(NT, 2)
         if (NKB == 2) { // this warp's rows of block `half`
             __syncwarp();
             if (lane == 0) {
-                uint8_t *to = BWD ? out + (rr < C ? rec.AF : rec.AR) + half * 8192 + (w & 1) * 4096
-                                  : out + rec.A + half * 16384 + (w & 3) * 4096;
+                uint8_t *to = out + (rr < C ? rec.A : rec.A2) + half * 16384 + (w & 1) * 4096;
                 bulk_s2g(to, hi_at, 4096);
-                bulk_s2g(to + NKB * (BWD ? 8192 : 16384), lo_at, 4096);
+                bulk_s2g(to + 8192, lo_at, 4096);
                 bulk_commit();
             }
         } else { // two warps share a row
             __syncthreads();
             if (tid == 0) {
-                if (BWD) {
-                    bulk_s2g(out + rec.AF, op, 8192);
-                    bulk_s2g(out + rec.AF + 8192, op + 16384, 8192);
-                    bulk_s2g(out + rec.AR, op + 8192, 8192);
-                    bulk_s2g(out + rec.AR + 8192, op + 24576, 8192);
-                } else {
-                    bulk_s2g(out + rec.A, op, 32768);
-                }
+                bulk_s2g(out + rec.A, op, 32768); // (A2 lies behind A)
                 bulk_commit();
             }
         }
@@ -592,10 +586,10 @@ __global__ void __launch_bounds__(NT, 2)
         rows_out(rec.base, 128, 0);
     } else {
         if (NKB == 2) {
-            rows_out(rec.baseU, C, 0);
+            rows_out(rec.base, C, 0);
             load_rows(dy); // V's place
         } else { // one place for both
-            rows_out(rec.baseU, C, 0);
+            rows_out(rec.base, C, 0);
             sent();
             __syncthreads();
             load_rows(dy);
@@ -604,7 +598,7 @@ __global__ void __launch_bounds__(NT, 2)
         multiply(tA2, dV, idv);
         finish();
         images_out();
-        rows_out(rec.baseX, C, C);
+        rows_out(rec.base2, C, C);
     }
     if (lane == 0)
         bulk_wait_all();
@@ -615,26 +609,38 @@ __global__ void __launch_bounds__(NT, 2)
 }
 
 // ------------------------------------------------------------------ walk
-// One CTA per (value head, 32 value channels).  Eight worker warps: thread
-// (row 32 (w % 4) + lane, 16 channels) holds 16 values of the state (row =
-// key channel) and handles 16 values of a token's row between the products.
-// A ninth warp's first lane asks for the records (two in flight) and issues
-// the MMAs, so that none of that is on a worker's path (measured: issuing
-// from a worker took 1500 of a chunk's 5900 cycles).  Workers tell it by two
-// mbarriers that the state's or the values' tile is written; its commits tell
-// them that a product is done.
+// One CTA per (value head, 32 value channels).  An MMA of 128 rows takes the
+// same time for any N up to 128 here (66 cycles), so the serial product has
+// the hi and the lo rows of its 64 x d_k factor stacked as its 128 rows, 8
+// MMAs of it for d_k 128, against [Z hi | Z lo] side by side; the answers'
+// product follows while the values are on their way, and the state's product
+// after that.  (One tile of W' and Q' rows, hi then lo, had 16 MMAs on the
+// serial path: 1.6 us a chunk instead of 1.2.)
+//
+// Eight worker warps.  Warps 0, 1, 4, 5 read the hi rows' result, warps 2, 3,
+// 6, 7 the lo rows' of the same tokens (a warp reaches 32 of the 128 TMEM
+// lanes); the two swap halves of their 16 channels through shared memory and
+// each finishes 8 channels.  Thread (row 32 (w % 4) + lane, 16 channels) also
+// holds 16 values of the fp32 state (row = key channel).  A ninth warp's first
+// lane issues the MMAs and a tenth's asks for the records, each part as soon
+// as the product that last read its place is done, so that none of that is on
+// a worker's path.  Workers tell them by two mbarriers that the state's or
+// the values' tile is written; commits tell workers that a product is done.
 enum { kFwd = 0, kKeep = 1, kRev = 2 };
-constexpr int kWalkThreads = NT + 32;
+constexpr int kWalkThreads = NT + 64;
 
 template <int MODE, int NKB> struct Walk {
-    static constexpr int R = MODE == kFwd ? 128 : 64;  // rows of the A tile and of the base rows
-    static constexpr int RB = MODE == kRev ? 128 : 64; // tokens the B^T tile holds
-    static constexpr uint32_t A = NKB * R * 256, B = NKB * RB * 128, SCAL = MODE == kRev ? 1024 : 512;
-    static constexpr uint32_t b = A, scal = b + B, base = scal + 1024, rec = base + R * 128;
-    // A 128-row MMA reads 8 KB past a tile of 64 rows and a product of one
-    // 64-wide block reads one more: what follows in this order covers both.
-    static constexpr uint32_t z = 2 * rec, u = z + NKB * 8192, bar = u + RB * 128, bytes = bar + 128 + 1024;
+    static constexpr int RB = MODE == kRev ? 128 : 64;     // tokens the B^T tile holds
+    static constexpr int RV = MODE == kFwd ? 128 : 64;     // base rows: U', then Y'
+    static constexpr uint32_t A = NKB * 16384 * (MODE == kFwd ? 2 : 1), B = NKB * RB * 128,
+                              SCAL = MODE == kRev ? 1024 : 512;
+    static constexpr uint32_t b = A, base = b + B, rec = base + RV * 128;
+    // A product of one 64-wide block reads one more (its rows go unused): what
+    // follows in this order covers it.
+    static constexpr uint32_t z = 2 * rec, u = z + NKB * 8192, swap = u + RB * 128, scal = swap + 8192,
+                              bar = scal + 2 * SCAL, bytes = bar + 128 + 1024;
     static_assert(rec + b + B + (NKB == 1 ? B : 0) <= bar && bytes <= 232448, "reads stay inside shared memory");
+    static constexpr uint32_t cols = MODE == kFwd ? 256 : 128; // TMEM: the values' 64, the state's 64, the answers' 64
 };
 
 template <int MODE, int NKB>
@@ -648,87 +654,103 @@ __global__ void __launch_bounds__(kWalkThreads)
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *zt = sm + L::z, *ut = sm + L::u;
     uint64_t *fullA = reinterpret_cast<uint64_t *>(sm + L::bar), *fullB = fullA + 2, *m1 = fullA + 4, *m2 = fullA + 5,
-             *zr = fullA + 6, *ur = fullA + 7;
-    uint32_t *slot = reinterpret_cast<uint32_t *>(fullA + 8);
+             *my = fullA + 6, *zr = fullA + 7, *ur = fullA + 8;
+    uint32_t *slot = reinterpret_cast<uint32_t *>(fullA + 9);
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, sl = blockIdx.x, bh = blockIdx.y, n0 = sl * NV;
     const int b = bh / a.H;
     griddep_wait();
     const int len = seq_len(a, b), nch = (len + C - 1) / C;
     if (w == 0) {
-        tmem_alloc(slot, 128);
+        tmem_alloc(slot, L::cols);
         tmem_relinquish();
     }
     if (tid == 32) {
-        for (int e = 0; e < 8; ++e)
-            mbar_init(fullA + e, e < 6 ? 1 : e == 7 && MODE != kRev ? NT / 64 : NT / 32);
+        for (int e = 0; e < 7; ++e)
+            mbar_init(fullA + e, 1);
+        mbar_init(zr, NT / 32);
+        mbar_init(ur, NT / 32 + (MODE == kFwd ? 0 : 1)); // the state's copy has left its tile, too
         fence_barrier_init();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     griddep_launch_dependents();
-    const uint32_t tm = *slot, tD1 = tm, tD2 = tm + 64;
+    const uint32_t tm = *slot, tU = tm, tZ = tm + 64, tY = tm + 128;
     auto chunk_of = [&](int it) { return MODE == kRev ? nch - 1 - it : it; };
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (ok)
             ok = mbar_wait(bar, parity, status);
     };
-    if (w == NT / 32) {
-        if (lane == 0 && nch > 0) {
-            const uint32_t pieces = (uint32_t)min(2, (a.d_v - n0) / 16);
-            // a chunk's A, and the rest of its record: each as soon as the
-            // product that last read its place is done
-            auto fetch_a = [&](int it) {
-                mbar_arrive_expect_tx(fullA + (it & 1), L::A);
-                bulk_g2s(sm + (it & 1) * L::rec,
-                         ws + rec.off(bh, chunk_of(it)) + (MODE == kFwd ? rec.A : MODE == kKeep ? rec.AF : rec.AR), L::A,
-                         fullA + (it & 1));
-            };
-            auto fetch_b = [&](int it) {
-                const uint8_t *src = ws + rec.off(bh, chunk_of(it));
-                uint8_t *dst = sm + (it & 1) * L::rec;
-                uint64_t *f = fullB + (it & 1);
-                const uint32_t base = pieces * L::R * 64;
-                mbar_arrive_expect_tx(f, L::B + L::SCAL + base);
-                if (MODE == kFwd) { // K and the scalars are one piece
-                    bulk_g2s(dst + L::b, src + rec.K, L::B + L::SCAL, f);
-                } else {
-                    if (MODE == kKeep) {
-#pragma unroll
-                        for (int kb = 0; kb < NKB; ++kb)
-                            bulk_g2s(dst + L::b + kb * 8192, src + rec.KQ + kb * 16384, 8192, f);
-                    } else {
-                        bulk_g2s(dst + L::b, src + rec.KQ, L::B, f);
-                    }
-                    bulk_g2s(dst + L::scal, src + (MODE == kKeep ? rec.scalF : rec.scalR), L::SCAL, f);
-                }
-                bulk_g2s(dst + L::base,
-                         src + (MODE == kFwd ? rec.base : MODE == kKeep ? rec.baseU : rec.baseX) + (size_t)sl * L::R * 128,
-                         base, f);
-            };
-            for (int it = 0; it < min(2, nch); ++it) {
-                fetch_a(it);
-                fetch_b(it);
-            }
+    if (w == NT / 32) { // the MMAs
+        if (lane == 0) {
             const uint64_t dz = desc_sw128(smem_u32(zt), 8192, 1024), du = desc_sw128(smem_u32(ut), 8192, 1024);
             const uint64_t dA0 = desc_sw128(smem_u32(sm), 16, 1024);
             const uint64_t dB0 = desc_sw128(smem_u32(sm + L::b), L::RB * 128, 1024);
-            for (int it = 0; it < nch && ok; ++it) {
+            for (int it = 0; it < nch; ++it) {
                 const uint64_t dA = at(dA0, (uint32_t)(it & 1) * L::rec), dB = at(dB0, (uint32_t)(it & 1) * L::rec);
                 wait(fullA + (it & 1), (it >> 1) & 1);
                 wait(zr, it & 1);
                 if (!ok)
                     break;
                 tc_fence_after();
-                // hi rows times [Z hi | Z lo], lo rows times Z hi
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int s = 0; s < 4 * NKB; ++s)
+                    mma_bf16(tU, at(dA, kmajor_step(s, 128)), at(dz, (uint32_t)s * 2048u), idesc_bf16(128, 64, 0, 1),
+                             s > 0);
+                mma_commit(m1);
+                if (MODE == kFwd) {
 #pragma unroll
                     for (int s = 0; s < 4 * NKB; ++s)
-                        mma_bf16(tD1, at(dA, (uint32_t)(t * NKB * L::R * 128) + kmajor_step(s, L::R)),
-                                 at(dz, (uint32_t)s * 2048u), idesc_bf16(128, t ? 32 : 64, 0, 1), (t | s) != 0);
-                mma_commit(m1);
+                        mma_bf16(tY, at(dA, (uint32_t)NKB * 16384u + kmajor_step(s, 128)), at(dz, (uint32_t)s * 2048u),
+                                 idesc_bf16(128, 64, 0, 1), s > 0);
+                    mma_commit(my);
+                }
+                wait(fullB + (it & 1), (it >> 1) & 1);
+                wait(ur, it & 1);
+                if (!ok)
+                    break;
+                tc_fence_after();
+#pragma unroll
+                for (int s = 0; s < L::RB / 16; ++s)
+                    mma_bf16(tZ, at(dB, (uint32_t)s * 2048u), at(du, (uint32_t)s * 2048u), idesc_bf16(128, 64, 1, 1),
+                             s > 0);
+                mma_commit(m2);
+            }
+        }
+        __syncwarp();
+    } else if (w == NT / 32 + 1) { // the copies
+        if (lane == 0) {
+            const uint32_t pieces = (uint32_t)min(2, (a.d_v - n0) / 16);
+            auto fetch_a = [&](int it) {
+                mbar_arrive_expect_tx(fullA + (it & 1), L::A);
+                bulk_g2s(sm + (it & 1) * L::rec, ws + rec.off(bh, chunk_of(it)) + (MODE == kRev ? rec.A2 : rec.A), L::A,
+                         fullA + (it & 1));
+            };
+            auto fetch_b = [&](int it) {
+                const uint8_t *src = ws + rec.off(bh, chunk_of(it));
+                uint8_t *dst = sm + (it & 1) * L::rec;
+                uint64_t *f = fullB + (it & 1);
+                const uint32_t base = pieces * L::RV * 64;
+                mbar_arrive_expect_tx(f, L::B + L::SCAL + base);
+                if (MODE == kKeep) {
+#pragma unroll
+                    for (int kb = 0; kb < NKB; ++kb)
+                        bulk_g2s(dst + L::b + kb * 8192, src + rec.K + kb * 16384, 8192, f);
+                } else {
+                    bulk_g2s(dst + L::b, src + rec.K, L::B, f);
+                }
+                bulk_g2s(sm + L::scal + (it & 1) * L::SCAL, src + (MODE == kRev ? rec.scalR : rec.scalF), L::SCAL, f);
+                bulk_g2s(dst + L::base, src + (MODE == kRev ? rec.base2 : rec.base) + (size_t)sl * L::RV * 128, base, f);
+            };
+            for (int it = 0; it < min(2, nch); ++it) {
+                fetch_a(it);
+                fetch_b(it);
+            }
+            for (int it = 0; it < nch; ++it) {
+                wait(zr, it & 1);
+                if (!ok)
+                    break;
                 if (MODE != kFwd) { // the state before this chunk, as it lies
                     bulk_s2g(ws + rec.off(bh, chunk_of(it)) + (MODE == kKeep ? rec.S : rec.dS) + (size_t)sl * DKP * 128, zt,
                              (uint32_t)DKP * 128u);
@@ -736,20 +758,15 @@ __global__ void __launch_bounds__(kWalkThreads)
                 }
                 if (it > 0 && it + 1 < nch)
                     fetch_b(it + 1); // the workers are through with the previous chunk
-                wait(fullB + (it & 1), (it >> 1) & 1);
-                wait(ur, it & 1);
-                if (!ok)
-                    break;
-                if (MODE != kFwd)
-                    bulk_wait_read(); // the stored state has left its tile
-                tc_fence_after();
-#pragma unroll
-                for (int s = 0; s < L::RB / 16; ++s)
-                    mma_bf16(tD2, at(dB, (uint32_t)s * 2048u), at(du, (uint32_t)s * 2048u), idesc_bf16(128, 64, 1, 1),
-                             s > 0);
-                mma_commit(m2);
-                if (it + 2 < nch)
-                    fetch_a(it + 2); // the workers have seen this chunk's first product
+                if (MODE != kFwd) {
+                    bulk_wait_read();
+                    mbar_arrive(ur);
+                } else {
+                    wait(my, it & 1);
+                }
+                wait(ur, it & 1); // (they have seen the values' product)
+                if (ok && it + 2 < nch)
+                    fetch_a(it + 2);
             }
             if (MODE != kFwd)
                 bulk_wait_all();
@@ -759,13 +776,12 @@ __global__ void __launch_bounds__(kWalkThreads)
         }
         __syncwarp();
     } else {
-        const int rr = 32 * (w & 3) + lane, hf = w >> 2, i = rr & 63;
+        const int rr = 32 * (w & 3) + lane, hf = w >> 2, i = rr & 63, c8 = (w >> 1) & 1; // c8: which 8 of the 16 channels
         const bool mine = n0 + 16 * hf < a.d_v; // these 16 channels exist (d_v is a multiple of 16)
         const bool zrow = 32 * (w & 3) < DKP;   // this warp holds rows of the state
-        const bool values = MODE == kFwd || rr < C; // and of the values
         const uint32_t lb = tmem_lane_base(w) + (uint32_t)(16 * hf);
-        float z[16], x[16], t0[16], t1[16];
-        uint4 ahead[2]; // kRev: dY's row of the next chunk
+        float z[16], x[8], y8[8], t0[16], t1[16];
+        uint4 ahead[2]; // kRev, lo rows' warps: dY's row of the next chunk
         auto read_dy = [&](int it) {
             const int c = chunk_of(it);
             const bool in = mine && i < min(C, len - c * C);
@@ -774,14 +790,11 @@ __global__ void __launch_bounds__(kWalkThreads)
             ahead[0] = in ? __ldcg(from) : make_uint4(0, 0, 0, 0);
             ahead[1] = in ? __ldcg(from + 1) : make_uint4(0, 0, 0, 0);
         };
-        auto put = [&](uint8_t *tile, int row, const float *v) { // 16 channels of a pair tile's row
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                uint4 hi, lo;
-                split8(v + 8 * e, hi, lo);
-                *reinterpret_cast<uint4 *>(tile + pair_chunk(row, 2 * hf + e)) = hi;
-                *reinterpret_cast<uint4 *>(tile + pair_chunk(row, 4 + 2 * hf + e)) = lo;
-            }
+        auto put8 = [&](uint8_t *tile, int row, int c, const float *v) { // 8 channels (chunk c of 4) of a pair tile's row
+            uint4 hi, lo;
+            split8(v, hi, lo);
+            *reinterpret_cast<uint4 *>(tile + pair_chunk(row, c)) = hi;
+            *reinterpret_cast<uint4 *>(tile + pair_chunk(row, c + 4)) = lo;
         };
         auto written = [&](uint64_t *bar) { // this warp's rows of a tile are written, its TMEM reads done
             fence_async_smem();
@@ -790,80 +803,113 @@ __global__ void __launch_bounds__(kWalkThreads)
             if (lane == 0)
                 mbar_arrive(bar);
         };
+        // this thread's 8 channels of a product: hi rows' sum plus lo rows', added to v
+        const int pair = (w & 1) + 2 * hf;
+        float4 *give = reinterpret_cast<float4 *>(sm + L::swap) + pair * 128 + c8 * 64 + lane;
+        const float4 *take = reinterpret_cast<const float4 *>(sm + L::swap) + pair * 128 + (c8 ^ 1) * 64 + lane;
+        auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory"); }; // warps w and w ^ 2
+        auto product = [&](uint32_t t, float (&v)[8]) {
+            tmem_ld16(t + lb, t0);
+            if (c8 == 0)
+                tmem_ld16(t + lb + 32u, t1);
+            tmem_ld_wait();
+            if (c8 == 0) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    t0[e] += t1[e];
+                give[0] = make_float4(t0[8], t0[9], t0[10], t0[11]);
+                give[32] = make_float4(t0[12], t0[13], t0[14], t0[15]);
+            } else {
+                give[0] = make_float4(t0[0], t0[1], t0[2], t0[3]);
+                give[32] = make_float4(t0[4], t0[5], t0[6], t0[7]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    t0[e] = t0[8 + e];
+            }
+            meet();
+            const float4 p = take[0], q = take[32];
+            v[0] += t0[0] + p.x;
+            v[1] += t0[1] + p.y;
+            v[2] += t0[2] + p.z;
+            v[3] += t0[3] + p.w;
+            v[4] += t0[4] + q.x;
+            v[5] += t0[5] + q.y;
+            v[6] += t0[6] + q.z;
+            v[7] += t0[7] + q.w;
+        };
+        auto base8 = [&](const uint8_t *r, int row, float (&v)[8]) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (mine)
+                    p = *reinterpret_cast<const float4 *>(r + L::base + hf * (L::RV * 64) + piece_chunk(row, 2 * c8 + e));
+                v[4 * e] = p.x;
+                v[4 * e + 1] = p.y;
+                v[4 * e + 2] = p.z;
+                v[4 * e + 3] = p.w;
+            }
+        };
 #pragma unroll
         for (int e = 0; e < 16; ++e)
             z[e] = Z0 && mine && rr < a.d_k ? __ldcg(Z0 + ((size_t)bh * a.d_v + n0 + 16 * hf + e) * a.d_k + rr) : 0.f;
-        if (zrow)
-            put(zt, rr, z);
+        if (zrow) {
+            put8(zt, rr, 2 * hf, z);
+            put8(zt, rr, 2 * hf + 1, z + 8);
+        }
         written(zr);
-        if (MODE == kRev && rr >= C && nch > 0)
+        if (MODE == kRev && c8 && nch > 0)
             read_dy(0);
         for (int it = 0; it < nch; ++it) {
             const int c = chunk_of(it), n = min(C, len - c * C);
             const uint8_t *r = sm + (it & 1) * L::rec;
             uint8_t *gr = ws + rec.off(bh, c);
             wait(fullB + (it & 1), (it >> 1) & 1);
-            const float *scal = reinterpret_cast<const float *>(r + L::scal);
-            const float whole = scal[MODE == kRev ? 2 * C : C], f = scal[MODE == kRev && rr >= C ? C + i : i];
-            if (MODE == kRev && rr >= C) { // dY's rows do not wait for the product
-                widen8(ahead[0], reinterpret_cast<float(&)[8]>(x[0]));
-                widen8(ahead[1], reinterpret_cast<float(&)[8]>(x[8]));
+            const float *scal = reinterpret_cast<const float *>(sm + L::scal + (it & 1) * L::SCAL);
+            const float whole = scal[MODE == kRev ? 2 * C : C], f = scal[i];
+            if (MODE == kRev && c8) { // dY's rows do not wait for the product
+                const float fy = scal[C + i];
+                widen8(ahead[0], reinterpret_cast<float(&)[8]>(t0[0]));
+                widen8(ahead[1], reinterpret_cast<float(&)[8]>(t0[8]));
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    x[e] *= f;
-                put(ut, rr, x);
+                    t0[e] *= fy;
+                put8(ut, C + i, 2 * hf, t0);
+                put8(ut, C + i, 2 * hf + 1, t0 + 8);
                 if (it + 1 < nch)
                     read_dy(it + 1);
             }
-            if (values) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (mine)
-                        v = *reinterpret_cast<const float4 *>(r + L::base + hf * (L::R * 64) + piece_chunk(rr, e));
-                    x[4 * e] = v.x;
-                    x[4 * e + 1] = v.y;
-                    x[4 * e + 2] = v.z;
-                    x[4 * e + 3] = v.w;
-                }
-            }
+            base8(r, i, x);
+            if (MODE == kFwd)
+                base8(r, C + i, y8);
             wait(m1, it & 1);
             tc_fence_after();
-            if (values) {
-                tmem_ld16(tD1 + lb, t0);
-                tmem_ld16(tD1 + lb + 32u, t1);
-                tmem_ld_wait();
+            product(tU, x);
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    x[e] += t0[e] + t1[e];
-                if (rr < C) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        t0[e] = f * x[e];
-                    put(ut, i, t0);
-                }
-            }
-            if (MODE == kRev || rr < C)
-                written(ur);
-            if (MODE == kFwd && rr >= C) {
-                if (mine && i < n) {
-                    __nv_bfloat16 *to = y + ((size_t)bh * a.L + (size_t)c * C + i) * a.d_v + n0 + 16 * hf;
-                    store8(to, reinterpret_cast<float(&)[8]>(x[0]));
-                    store8(to + 8, reinterpret_cast<float(&)[8]>(x[8]));
-                }
-            } else if (MODE != kFwd && rr < C) { // U, or dX, for the gradients: a pair tile's row
-                put(gr + (MODE == kKeep ? rec.U : rec.dX) + (size_t)sl * 8192, i, x);
+            for (int e = 0; e < 8; ++e)
+                t0[e] = f * x[e];
+            put8(ut, i, 2 * hf + c8, t0);
+            written(ur);
+            if (MODE == kFwd) {
+                wait(my, it & 1);
+                tc_fence_after();
+                meet(); // the other has taken what the first product left
+                product(tY, y8);
+                if (mine && i < n)
+                    store8(y + ((size_t)bh * a.L + (size_t)c * C + i) * a.d_v + n0 + 16 * hf + 8 * c8, y8);
+            } else { // U, or dX, for the gradients: a pair tile's row
+                put8(gr + (MODE == kKeep ? rec.U : rec.dX) + (size_t)sl * 8192, i, 2 * hf + c8, x);
             }
             wait(m2, it & 1);
             tc_fence_after();
             if (zrow) {
-                tmem_ld16(tD2 + lb, t0);
-                tmem_ld16(tD2 + lb + 32u, t1);
+                tmem_ld16(tZ + lb, t0);
+                tmem_ld16(tZ + lb + 32u, t1);
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     z[e] = fmaf(whole, z[e], t0[e] + t1[e]);
-                put(zt, rr, z);
+                put8(zt, rr, 2 * hf, z);
+                put8(zt, rr, 2 * hf + 1, z + 8);
             }
             written(zr);
         }
@@ -872,16 +918,16 @@ __global__ void __launch_bounds__(kWalkThreads)
             for (int e = 0; e < 16; ++e)
                 Zf[((size_t)bh * a.d_v + n0 + 16 * hf + e) * a.d_k + rr] = z[e];
         if (MODE == kFwd) { // no token, no answer
-            const size_t c8 = min(NV, a.d_v - n0) / 8, cnt = (size_t)(a.L - len) * c8;
+            const size_t c16 = min(NV, a.d_v - n0) / 8, cnt = (size_t)(a.L - len) * c16;
             for (size_t e = tid; e < cnt; e += NT)
-                *reinterpret_cast<uint4 *>(y + ((size_t)bh * a.L + len + e / c8) * a.d_v + n0 + 8 * (e % c8)) =
+                *reinterpret_cast<uint4 *>(y + ((size_t)bh * a.L + len + e / c16) * a.d_v + n0 + 8 * (e % c16)) =
                     make_uint4(0, 0, 0, 0);
         }
     }
     tc_fence_before();
     __syncthreads();
     if (w == 0)
-        tmem_dealloc(tm, 128);
+        tmem_dealloc(tm, L::cols);
 }
 
 template <bool BWD, int NKB>

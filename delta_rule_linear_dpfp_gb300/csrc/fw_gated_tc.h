@@ -11,9 +11,11 @@ namespace fw {
 struct GatedRecord {
     int nkb, ns, nch;            // 64-wide blocks of d_k, 32-wide slices of d_v, chunks
     size_t bytes;                // per chunk
-    size_t A, K, scalF, base;    // forward: [-W'; Q'] hi, lo; K; scalars; [U'; Y'] fp32 pieces [d_v / 16][128][16]
-    size_t AF, AR, KQ, scalR;    // backward: -W' and W" hi, lo (64 rows); [K; Q]; scalars
-    size_t baseU, baseX;         // U', X0: fp32 pieces [d_v / 16][64][16]
+    // Images of 64 hi rows and the same rows' lo terms per 64-wide block: A is
+    // -W', A2 is Q' (forward) or W" (backward); K is the chunk's keys, in the
+    // backward [keys; queries] per 64-wide block.
+    size_t A, A2, K, scalF, scalR;
+    size_t base, base2;          // fp32 pieces [d_v / 16][rows][16]: [U'; Y'] (128 rows), or U' and X0 (64 rows)
     size_t U, dX, S, dS, tok;    // pair tiles [ns] of 64 (U, dX) and d_k (S, dS) rows; 8 floats a token
 
     __host__ __device__ size_t off(int64_t bh, int c) const { return ((size_t)bh * nch + c) * bytes; }
@@ -29,7 +31,8 @@ inline GatedRecord gated_shape_record(int L, int d_k, int d_v) {
 inline GatedRecord gated_forward_record(int L, int d_k, int d_v) {
     GatedRecord r = gated_shape_record(L, d_k, d_v);
     r.A = 0;
-    r.K = r.A + (size_t)r.nkb * 32768;
+    r.A2 = r.A + (size_t)r.nkb * 16384;
+    r.K = r.A2 + (size_t)r.nkb * 16384;
     r.scalF = r.K + (size_t)r.nkb * 8192;
     r.base = r.scalF + 512;
     r.bytes = r.base + (size_t)r.ns * 16384;
@@ -37,15 +40,15 @@ inline GatedRecord gated_forward_record(int L, int d_k, int d_v) {
 }
 inline GatedRecord gated_backward_record(int L, int d_k, int d_v) {
     GatedRecord r = gated_shape_record(L, d_k, d_v);
-    r.AF = 0;
-    r.AR = r.AF + (size_t)r.nkb * 16384;
-    r.KQ = r.AR + (size_t)r.nkb * 16384;
-    r.scalF = r.KQ + (size_t)r.nkb * 16384;
+    r.A = 0;
+    r.A2 = r.A + (size_t)r.nkb * 16384;
+    r.K = r.A2 + (size_t)r.nkb * 16384;
+    r.scalF = r.K + (size_t)r.nkb * 16384;
     r.scalR = r.scalF + 512;
     r.tok = r.scalR + 1024;
-    r.baseU = r.tok + 2048;
-    r.baseX = r.baseU + (size_t)r.ns * 8192;
-    r.U = r.baseX + (size_t)r.ns * 8192;
+    r.base = r.tok + 2048;
+    r.base2 = r.base + (size_t)r.ns * 8192;
+    r.U = r.base2 + (size_t)r.ns * 8192;
     r.dX = r.U + (size_t)r.ns * 8192;
     r.S = r.dX + (size_t)r.ns * 8192;
     r.dS = r.S + (size_t)r.ns * r.nkb * 8192;
