@@ -90,45 +90,51 @@ FW_DEV Pair add(Pair a, Pair b) { // two-sum of the highs, the lows added to wha
 // (I + A)^-1 of the strictly lower triangular A (row stride LC): forward
 // substitution in the four 16 x 16 diagonal blocks, one thread a column, then
 // two doublings T21 = -T22 (A21 T11), four columns a thread.
-template <int H> FW_DEV void double_inverse(const float *A, float *T, float *tmp) {
-    constexpr int Q = H / 4, N = (C / (2 * H)) * H * Q; // float4 outputs of all pairs of blocks
-    const int tid = threadIdx.x, p = tid / (H * Q), i = (tid / Q) % H, j = (tid % Q) * 4, r0 = p * 2 * H;
-    const float *a = A + (r0 + H + i) * LC + r0, *t11 = T + r0 * LC + r0 + j;
-    if (tid < N) {
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+// R rows a thread: more products for each value read from shared memory.
+template <int H, int R> FW_DEV void block_product(const float *a, int lda, const float *b, int ldb, float (&s)[R][4]) {
 #pragma unroll
-        for (int m = 0; m < H; m += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(a + m);
-            const float fm[4] = {f.x, f.y, f.z, f.w};
+    for (int m = 0; m < H; m += 4) {
+        float f[R][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float4 t = *reinterpret_cast<const float4 *>(t11 + (m + e) * LC);
-                s.x = fmaf(fm[e], t.x, s.x);
-                s.y = fmaf(fm[e], t.y, s.y);
-                s.z = fmaf(fm[e], t.z, s.z);
-                s.w = fmaf(fm[e], t.w, s.w);
+        for (int r = 0; r < R; ++r) {
+            const float4 t = *reinterpret_cast<const float4 *>(a + r * (H / R) * lda + m);
+            f[r][0] = t.x;
+            f[r][1] = t.y;
+            f[r][2] = t.z;
+            f[r][3] = t.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float4 t = *reinterpret_cast<const float4 *>(b + (m + e) * ldb);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                s[r][0] = fmaf(f[r][e], t.x, s[r][0]);
+                s[r][1] = fmaf(f[r][e], t.y, s[r][1]);
+                s[r][2] = fmaf(f[r][e], t.z, s[r][2]);
+                s[r][3] = fmaf(f[r][e], t.w, s[r][3]);
             }
         }
-        *reinterpret_cast<float4 *>(tmp + (p * H + i) * H + j) = s;
+    }
+}
+template <int H, int R> FW_DEV void double_inverse(const float *A, float *T, float *tmp) {
+    constexpr int Q = H / 4, N = (C / (2 * H)) * (H / R) * Q; // threads: pair of blocks, row, four columns
+    const int tid = threadIdx.x, p = tid / (H / R * Q), i = (tid / Q) % (H / R), j = (tid % Q) * 4, r0 = p * 2 * H;
+    if (tid < N) {
+        float s[R][4] = {};
+        block_product<H, R>(A + (r0 + H + i) * LC + r0, LC, T + r0 * LC + r0 + j, LC, s);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            *reinterpret_cast<float4 *>(tmp + (p * H + i + r * (H / R)) * H + j) =
+                make_float4(s[r][0], s[r][1], s[r][2], s[r][3]);
     }
     __syncthreads();
-    const float *t22 = T + (r0 + H + i) * LC + r0 + H, *u = tmp + p * H * H + j;
     if (tid < N) {
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        float s[R][4] = {};
+        block_product<H, R>(T + (r0 + H + i) * LC + r0 + H, LC, tmp + p * H * H + j, H, s);
 #pragma unroll
-        for (int m = 0; m < H; m += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(t22 + m);
-            const float fm[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float4 t = *reinterpret_cast<const float4 *>(u + (m + e) * H);
-                s.x = fmaf(-fm[e], t.x, s.x);
-                s.y = fmaf(-fm[e], t.y, s.y);
-                s.z = fmaf(-fm[e], t.z, s.z);
-                s.w = fmaf(-fm[e], t.w, s.w);
-            }
-        }
-        *reinterpret_cast<float4 *>(T + (r0 + H + i) * LC + r0 + j) = s;
+        for (int r = 0; r < R; ++r)
+            *reinterpret_cast<float4 *>(T + (r0 + H + i + r * (H / R)) * LC + r0 + j) =
+                make_float4(-s[r][0], -s[r][1], -s[r][2], -s[r][3]);
     }
     __syncthreads();
 }
@@ -163,8 +169,8 @@ FW_DEV void unit_lower_inverse(const float *A, float *T, float *tmp) {
         }
     }
     __syncthreads();
-    double_inverse<16>(A, T, tmp);
-    double_inverse<32>(A, T, tmp);
+    double_inverse<16, 1>(A, T, tmp);
+    double_inverse<32, 2>(A, T, tmp);
 }
 
 // A descriptor `bytes` further into its tile.
@@ -644,10 +650,9 @@ template <int MODE, int NKB> struct Walk {
 };
 
 template <int MODE, int NKB>
-__global__ void __launch_bounds__(kWalkThreads)
-    gated_tc_walk_kernel(GatedArgs a, const __nv_bfloat16 *__restrict__ dy, const float *__restrict__ Z0,
-                         float *__restrict__ Zf, __nv_bfloat16 *__restrict__ y, uint8_t *ws, GatedRecord rec,
-                         unsigned *status) {
+FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const float *__restrict__ Z0,
+                 float *__restrict__ Zf, __nv_bfloat16 *__restrict__ y, uint8_t *ws, const GatedRecord &rec,
+                 unsigned *status) {
     using L = Walk<MODE, NKB>;
     constexpr int DKP = 64 * NKB;
     extern __shared__ uint8_t smem_raw[];
@@ -781,8 +786,8 @@ __global__ void __launch_bounds__(kWalkThreads)
         const bool zrow = 32 * (w & 3) < DKP;   // this warp holds rows of the state
         const uint32_t lb = tmem_lane_base(w) + (uint32_t)(16 * hf);
         float z[16], x[8], y8[8], t0[16], t1[16];
-        uint4 ahead[2]; // kRev, lo rows' warps: dY's row of the next chunk
-        auto read_dy = [&](int it) {
+        uint4 even[2], odd[2]; // kRev, lo rows' warps: dY's rows of the next two chunks
+        auto read_dy = [&](int it, uint4 (&ahead)[2]) {
             const int c = chunk_of(it);
             const bool in = mine && i < min(C, len - c * C);
             const uint4 *from = reinterpret_cast<const uint4 *>(
@@ -857,9 +862,13 @@ __global__ void __launch_bounds__(kWalkThreads)
             put8(zt, rr, 2 * hf + 1, z + 8);
         }
         written(zr);
-        if (MODE == kRev && c8 && nch > 0)
-            read_dy(0);
-        for (int it = 0; it < nch; ++it) {
+        if (MODE == kRev && c8) {
+            if (nch > 0)
+                read_dy(0, even);
+            if (nch > 1)
+                read_dy(1, odd);
+        }
+        auto step = [&](int it, uint4 (&ahead)[2]) {
             const int c = chunk_of(it), n = min(C, len - c * C);
             const uint8_t *r = sm + (it & 1) * L::rec;
             uint8_t *gr = ws + rec.off(bh, c);
@@ -875,8 +884,8 @@ __global__ void __launch_bounds__(kWalkThreads)
                     t0[e] *= fy;
                 put8(ut, C + i, 2 * hf, t0);
                 put8(ut, C + i, 2 * hf + 1, t0 + 8);
-                if (it + 1 < nch)
-                    read_dy(it + 1);
+                if (it + 2 < nch)
+                    read_dy(it + 2, ahead);
             }
             base8(r, i, x);
             if (MODE == kFwd)
@@ -912,6 +921,11 @@ __global__ void __launch_bounds__(kWalkThreads)
                 put8(zt, rr, 2 * hf + 1, z + 8);
             }
             written(zr);
+        };
+        for (int it = 0; it < nch; it += 2) { // (by twos, so that each dY row has registers of its own)
+            step(it, even);
+            if (it + 1 < nch)
+                step(it + 1, odd);
         }
         if (Zf && mine && rr < a.d_k)
 #pragma unroll
@@ -928,6 +942,25 @@ __global__ void __launch_bounds__(kWalkThreads)
     __syncthreads();
     if (w == 0)
         tmem_dealloc(tm, L::cols);
+}
+
+template <int NKB>
+__global__ void __launch_bounds__(kWalkThreads)
+    gated_tc_walk_kernel(GatedArgs a, const float *__restrict__ W0, float *__restrict__ Wf,
+                         __nv_bfloat16 *__restrict__ y, uint8_t *ws, GatedRecord rec, unsigned *status) {
+    walk<kFwd, NKB>(a, nullptr, W0, Wf, y, ws, rec, status);
+}
+// The backward's two walks need only the preparation, not each other: one
+// launch (B4 H8 L512, 64 CTAs each: 13 us and 15 us in two launches).
+template <int NKB>
+__global__ void __launch_bounds__(kWalkThreads)
+    gated_tc_both_walks_kernel(GatedArgs a, const __nv_bfloat16 *__restrict__ dy, const float *__restrict__ W0,
+                               const float *__restrict__ dWf, float *__restrict__ dW0, uint8_t *ws, GatedRecord rec,
+                               unsigned *status) {
+    if (blockIdx.z == 0)
+        walk<kRev, NKB>(a, dy, dWf, dW0, nullptr, ws, rec, status);
+    else
+        walk<kKeep, NKB>(a, nullptr, W0, nullptr, nullptr, ws, rec, status);
 }
 
 template <bool BWD, int NKB>
@@ -947,26 +980,20 @@ cudaError_t launch_prep(const GatedArgs &a, const void *q, const void *k, const 
                       (const bf *)v, (const bf *)g, (const bf *)beta, (const bf *)dy, (uint8_t *)ws, rec, cols, status);
 }
 
-template <int MODE, int NKB>
-cudaError_t launch_walk(const GatedArgs &a, const void *dy, const float *Z0, float *Zf, void *y, void *ws,
-                        const GatedRecord &rec, unsigned *status, cudaStream_t st) {
-    using bf = __nv_bfloat16;
-    auto *kern = gated_tc_walk_kernel<MODE, NKB>;
-    const uint32_t smem = Walk<MODE, NKB>::bytes;
-    static std::atomic<uint64_t> allowed{0};
-    const cudaError_t e = allow_smem(kern, allowed);
-    if (e != cudaSuccess)
-        return e;
-    return launch_pdl(kern, dim3(rec.ns, a.B * a.H), dim3(kWalkThreads), smem, st, a, (const bf *)dy, Z0, Zf, (bf *)y,
-                      (uint8_t *)ws, rec, status);
-}
-
 template <int NKB>
 cudaError_t forward(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g, const void *beta,
                     const float *W0, float *Wf, void *y, void *ws, const GatedRecord &rec, unsigned *status,
                     cudaStream_t st) {
     const cudaError_t e = launch_prep<false, NKB>(a, q, k, v, g, beta, nullptr, ws, rec, status, st);
-    return e != cudaSuccess ? e : launch_walk<kFwd, NKB>(a, nullptr, W0, Wf, y, ws, rec, status, st);
+    if (e != cudaSuccess)
+        return e;
+    auto *kern = gated_tc_walk_kernel<NKB>;
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t w = allow_smem(kern, allowed);
+    if (w != cudaSuccess)
+        return w;
+    return launch_pdl(kern, dim3(rec.ns, a.B * a.H), dim3(kWalkThreads), Walk<kFwd, NKB>::bytes, st, a, W0, Wf,
+                      (__nv_bfloat16 *)y, (uint8_t *)ws, rec, status);
 }
 
 template <int NKB>
@@ -974,11 +1001,16 @@ cudaError_t walks(const GatedArgs &a, const void *q, const void *k, const void *
                   const float *W0, const void *dy, const float *dWf, float *dW0, void *ws, const GatedRecord &rec,
                   unsigned *status, cudaStream_t st) {
     cudaError_t e = launch_prep<true, NKB>(a, q, k, v, g, beta, dy, ws, rec, status, st);
-    if (e == cudaSuccess)
-        e = launch_walk<kKeep, NKB>(a, nullptr, W0, nullptr, nullptr, ws, rec, status, st);
-    if (e == cudaSuccess)
-        e = launch_walk<kRev, NKB>(a, dy, dWf, dW0, nullptr, ws, rec, status, st);
-    return e;
+    if (e != cudaSuccess)
+        return e;
+    auto *kern = gated_tc_both_walks_kernel<NKB>;
+    static std::atomic<uint64_t> allowed{0};
+    e = allow_smem(kern, allowed);
+    if (e != cudaSuccess)
+        return e;
+    static_assert(Walk<kRev, NKB>::bytes >= Walk<kKeep, NKB>::bytes, "one launch, the larger of the two");
+    return launch_pdl(kern, dim3(rec.ns, a.B * a.H, 2), dim3(kWalkThreads), Walk<kRev, NKB>::bytes, st, a,
+                      (const __nv_bfloat16 *)dy, W0, dWf, dW0, (uint8_t *)ws, rec, status);
 }
 
 } // namespace
