@@ -80,6 +80,14 @@ cudaError_t status_word(unsigned **out) {
         *out = di.status;
     return e;
 }
+// SMs of the current device (for the gated rule's launchers).
+cudaError_t device_sms(int *out) {
+    DeviceInfo di;
+    cudaError_t e = device_info(&di);
+    if (e == cudaSuccess)
+        *out = di.num_sms;
+    return e;
+}
 } // namespace fw
 
 extern "C" {

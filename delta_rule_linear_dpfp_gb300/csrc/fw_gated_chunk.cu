@@ -763,8 +763,8 @@ cudaError_t backward_f32(const GatedArgs &a, const void *q, const void *k, const
 
 size_t gated_forward_workspace_bytes(int B, int H, int L, int d_k, int d_v, int bf16) {
     if (bf16) {
-        const GatedRecord r = gated_forward_record(L, d_k, d_v);
-        return (size_t)B * H * r.nch * r.bytes;
+        const GatedRecord r = gated_forward_record(L, d_k, d_v); // and the state between two segments
+        return (size_t)B * H * (r.nch * r.bytes + sizeof(float) * d_v * d_k);
     }
     return sizeof(float) * ws_off(B * H, L, d_k, d_v, false).end;
 }

@@ -30,6 +30,7 @@
 namespace fw {
 
 cudaError_t status_word(unsigned **out); // fw_api.cu
+cudaError_t device_sms(int *out);
 
 namespace {
 
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(NT, 2)
     gated_tc_prep_kernel(GatedArgs a, const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ k,
                          const __nv_bfloat16 *__restrict__ v, const __nv_bfloat16 *__restrict__ g,
                          const __nv_bfloat16 *__restrict__ beta, const __nv_bfloat16 *__restrict__ dy, uint8_t *ws,
-                         GatedRecord rec, int tmem_cols, unsigned *status) {
+                         GatedRecord rec, int c0, int beside, int tmem_cols, unsigned *status) {
     constexpr int DKP = 64 * NKB;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -217,12 +218,20 @@ __global__ void __launch_bounds__(NT, 2)
     float *tok = reinterpret_cast<float *>(sm + o.tok); // per token: G hi, G lo, rk, beta, rq, e^G, e^{G_C-G}, -
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + o.bar);
     uint32_t *slot = reinterpret_cast<uint32_t *>(bar + 1);
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, c = blockIdx.x, bh = blockIdx.y;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, c = c0 + blockIdx.x, bh = blockIdx.y;
     const int b = bh / a.H, h = bh % a.H, kh = b * a.Hk + h / (a.H / a.Hk);
-    griddep_wait();
+    // `beside`: the preceding kernel is a walk over earlier chunks of this
+    // call, which has itself waited for everything before it and writes
+    // nothing that is read here.  The grid's last CTA waits for it at its end,
+    // so that this kernel does not complete before the walk does.
+    const bool last = blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1;
+    if (!beside)
+        griddep_wait();
     const int n = min(C, seq_len(a, b) - c * C);
     if (n <= 0) {
         griddep_launch_dependents();
+        if (beside && last)
+            griddep_wait();
         return;
     }
     if (w == 0) {
@@ -612,6 +621,8 @@ __global__ void __launch_bounds__(NT, 2)
     __syncthreads();
     if (w == 0)
         tmem_dealloc(tm, (uint32_t)tmem_cols);
+    if (beside && last)
+        griddep_wait();
 }
 
 // ------------------------------------------------------------------ walk
@@ -643,16 +654,16 @@ template <int MODE, int NKB> struct Walk {
     static constexpr uint32_t b = A, base = b + B, rec = base + RV * 128;
     // A product of one 64-wide block reads one more (its rows go unused): what
     // follows in this order covers it.
-    static constexpr uint32_t z = 2 * rec, u = z + NKB * 8192, swap = u + RB * 128, scal = swap + 8192,
-                              bar = scal + 2 * SCAL, bytes = bar + 128 + 1024;
+    static constexpr uint32_t z = 2 * rec, u = z + NKB * 8192, scal = u + RB * 128, bar = scal + 2 * SCAL,
+                              bytes = bar + 128 + 1024;
     static_assert(rec + b + B + (NKB == 1 ? B : 0) <= bar && bytes <= 232448, "reads stay inside shared memory");
     static constexpr uint32_t cols = MODE == kFwd ? 256 : 128; // TMEM: the values' 64, the state's 64, the answers' 64
 };
 
 template <int MODE, int NKB>
 FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const float *__restrict__ Z0,
-                 float *__restrict__ Zf, __nv_bfloat16 *__restrict__ y, uint8_t *ws, const GatedRecord &rec,
-                 unsigned *status) {
+                 float *__restrict__ Zf, __nv_bfloat16 *__restrict__ y, uint8_t *ws, const GatedRecord &rec, int c0,
+                 int c1, unsigned *status) {
     using L = Walk<MODE, NKB>;
     constexpr int DKP = 64 * NKB;
     extern __shared__ uint8_t smem_raw[];
@@ -664,7 +675,7 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, sl = blockIdx.x, bh = blockIdx.y, n0 = sl * NV;
     const int b = bh / a.H;
     griddep_wait();
-    const int len = seq_len(a, b), nch = (len + C - 1) / C;
+    const int len = seq_len(a, b), nch = max(0, min(c1, (len + C - 1) / C) - c0); // of chunks c0 .. c1 - 1
     if (w == 0) {
         tmem_alloc(slot, L::cols);
         tmem_relinquish();
@@ -681,7 +692,7 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
     tc_fence_after();
     griddep_launch_dependents();
     const uint32_t tm = *slot, tU = tm, tZ = tm + 64, tY = tm + 128;
-    auto chunk_of = [&](int it) { return MODE == kRev ? nch - 1 - it : it; };
+    auto chunk_of = [&](int it) { return c0 + (MODE == kRev ? nch - 1 - it : it); };
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (ok)
@@ -808,12 +819,12 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
             if (lane == 0)
                 mbar_arrive(bar);
         };
-        // this thread's 8 channels of a product: hi rows' sum plus lo rows', added to v
-        const int pair = (w & 1) + 2 * hf;
-        float4 *give = reinterpret_cast<float4 *>(sm + L::swap) + pair * 128 + c8 * 64 + lane;
-        const float4 *take = reinterpret_cast<const float4 *>(sm + L::swap) + pair * 128 + (c8 ^ 1) * 64 + lane;
-        auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory"); }; // warps w and w ^ 2
-        auto product = [&](uint32_t t, float (&v)[8]) {
+        // this thread's 8 channels of a product: hi rows' sum plus lo rows',
+        // added to v; the two warps swap in the 2 KB of base rows that were theirs
+        auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + (w & 1) + 2 * hf) : "memory"); }; // warps w, w ^ 2
+        auto product = [&](uint32_t t, uint8_t *place, float (&v)[8]) {
+            float4 *give = reinterpret_cast<float4 *>(place) + c8 * 64 + lane;
+            const float4 *take = reinterpret_cast<const float4 *>(place) + (c8 ^ 1) * 64 + lane;
             tmem_ld16(t + lb, t0);
             if (c8 == 0)
                 tmem_ld16(t + lb + 32u, t1);
@@ -870,7 +881,7 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
         }
         auto step = [&](int it, uint4 (&ahead)[2]) {
             const int c = chunk_of(it), n = min(C, len - c * C);
-            const uint8_t *r = sm + (it & 1) * L::rec;
+            uint8_t *r = sm + (it & 1) * L::rec, *place = r + L::base + hf * (L::RV * 64) + (w & 1) * 2048;
             uint8_t *gr = ws + rec.off(bh, c);
             wait(fullB + (it & 1), (it >> 1) & 1);
             const float *scal = reinterpret_cast<const float *>(sm + L::scal + (it & 1) * L::SCAL);
@@ -890,9 +901,10 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
             base8(r, i, x);
             if (MODE == kFwd)
                 base8(r, C + i, y8);
+            meet(); // both have read their base rows
             wait(m1, it & 1);
             tc_fence_after();
-            product(tU, x);
+            product(tU, place, x);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 t0[e] = f * x[e];
@@ -901,8 +913,7 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
             if (MODE == kFwd) {
                 wait(my, it & 1);
                 tc_fence_after();
-                meet(); // the other has taken what the first product left
-                product(tY, y8);
+                product(tY, place + 4096, y8);
                 if (mine && i < n)
                     store8(y + ((size_t)bh * a.L + (size_t)c * C + i) * a.d_v + n0 + 16 * hf + 8 * c8, y8);
             } else { // U, or dX, for the gradients: a pair tile's row
@@ -931,7 +942,7 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
 #pragma unroll
             for (int e = 0; e < 16; ++e)
                 Zf[((size_t)bh * a.d_v + n0 + 16 * hf + e) * a.d_k + rr] = z[e];
-        if (MODE == kFwd) { // no token, no answer
+        if (MODE == kFwd && c1 == rec.nch) { // no token, no answer
             const size_t c16 = min(NV, a.d_v - n0) / 8, cnt = (size_t)(a.L - len) * c16;
             for (size_t e = tid; e < cnt; e += NT)
                 *reinterpret_cast<uint4 *>(y + ((size_t)bh * a.L + len + e / c16) * a.d_v + n0 + 8 * (e % c16)) =
@@ -947,8 +958,8 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
 template <int NKB>
 __global__ void __launch_bounds__(kWalkThreads)
     gated_tc_walk_kernel(GatedArgs a, const float *__restrict__ W0, float *__restrict__ Wf,
-                         __nv_bfloat16 *__restrict__ y, uint8_t *ws, GatedRecord rec, unsigned *status) {
-    walk<kFwd, NKB>(a, nullptr, W0, Wf, y, ws, rec, status);
+                         __nv_bfloat16 *__restrict__ y, uint8_t *ws, GatedRecord rec, int c0, int c1, unsigned *status) {
+    walk<kFwd, NKB>(a, nullptr, W0, Wf, y, ws, rec, c0, c1, status);
 }
 // The backward's two walks need only the preparation, not each other: one
 // launch (B4 H8 L512, 64 CTAs each: 13 us and 15 us in two launches).
@@ -958,15 +969,15 @@ __global__ void __launch_bounds__(kWalkThreads)
                                const float *__restrict__ dWf, float *__restrict__ dW0, uint8_t *ws, GatedRecord rec,
                                unsigned *status) {
     if (blockIdx.z == 0)
-        walk<kRev, NKB>(a, dy, dWf, dW0, nullptr, ws, rec, status);
+        walk<kRev, NKB>(a, dy, dWf, dW0, nullptr, ws, rec, 0, rec.nch, status);
     else
-        walk<kKeep, NKB>(a, nullptr, W0, nullptr, nullptr, ws, rec, status);
+        walk<kKeep, NKB>(a, nullptr, W0, nullptr, nullptr, ws, rec, 0, rec.nch, status);
 }
 
 template <bool BWD, int NKB>
 cudaError_t launch_prep(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g,
-                        const void *beta, const void *dy, void *ws, const GatedRecord &rec, unsigned *status,
-                        cudaStream_t st) {
+                        const void *beta, const void *dy, void *ws, const GatedRecord &rec, int c0, int c1, bool beside,
+                        unsigned *status, cudaStream_t st) {
     using bf = __nv_bfloat16;
     auto *kern = gated_tc_prep_kernel<BWD, NKB>;
     const uint32_t smem = prep_smem(NKB, (a.d_v + 63) / 64).bytes;
@@ -976,31 +987,53 @@ cudaError_t launch_prep(const GatedArgs &a, const void *q, const void *k, const 
         return e;
     // 128 columns for A1's product, d_v for A2's (MT's 64 lie there first)
     const int cols = a.d_v <= 128 ? 256 : 512;
-    return launch_pdl(kern, dim3(rec.nch, a.B * a.H), dim3(NT), smem, st, a, (const bf *)q, (const bf *)k,
-                      (const bf *)v, (const bf *)g, (const bf *)beta, (const bf *)dy, (uint8_t *)ws, rec, cols, status);
+    return launch_pdl(kern, dim3(c1 - c0, a.B * a.H), dim3(NT), smem, st, a, (const bf *)q, (const bf *)k,
+                      (const bf *)v, (const bf *)g, (const bf *)beta, (const bf *)dy, (uint8_t *)ws, rec, c0,
+                      (int)beside, cols, status);
+}
+
+// Chunks in a segment of the forward.  Where the walk's CTAs leave most SMs
+// idle, a sequence is cut into segments and the preparation of one runs on the
+// idle SMs beside the walk over the one before.  A segment is a whole number
+// of waves of preparing CTAs (two an SM) and at least kMinSegment chunks, since
+// each costs the walk a start.  (16 heads, 16 381 tokens, d 128: %%A%% us in
+// one piece, %%B%% us in segments of 33 chunks; B2 H8 L2048, d_v 64: %%C%% us and
+// %%D%% us in two of 16.)
+constexpr int kMinSegment = 16;
+int segment_chunks(const GatedArgs &a, const GatedRecord &rec, int num_sms) {
+    const int64_t heads = (int64_t)a.B * a.H, walkers = heads * rec.ns;
+    if (2 * walkers > num_sms)
+        return rec.nch;
+    const int wave = (int)std::max<int64_t>(1, 2 * (num_sms - walkers) / heads);
+    const int seg = (kMinSegment + wave - 1) / wave * wave, n = (rec.nch + seg / 2) / seg;
+    return n < 2 ? rec.nch : (rec.nch + n - 1) / n;
 }
 
 template <int NKB>
 cudaError_t forward(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g, const void *beta,
-                    const float *W0, float *Wf, void *y, void *ws, const GatedRecord &rec, unsigned *status,
-                    cudaStream_t st) {
-    const cudaError_t e = launch_prep<false, NKB>(a, q, k, v, g, beta, nullptr, ws, rec, status, st);
-    if (e != cudaSuccess)
-        return e;
+                    const float *W0, float *Wf, void *y, void *ws, const GatedRecord &rec, int num_sms,
+                    unsigned *status, cudaStream_t st) {
     auto *kern = gated_tc_walk_kernel<NKB>;
     static std::atomic<uint64_t> allowed{0};
-    const cudaError_t w = allow_smem(kern, allowed);
-    if (w != cudaSuccess)
-        return w;
-    return launch_pdl(kern, dim3(rec.ns, a.B * a.H), dim3(kWalkThreads), Walk<kFwd, NKB>::bytes, st, a, W0, Wf,
-                      (__nv_bfloat16 *)y, (uint8_t *)ws, rec, status);
+    cudaError_t e = allow_smem(kern, allowed);
+    const int seg = segment_chunks(a, rec, num_sms);
+    float *between = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + rec.off((int64_t)a.B * a.H, 0));
+    for (int c0 = 0; c0 < rec.nch && e == cudaSuccess; c0 += seg) {
+        const int c1 = std::min(rec.nch, c0 + seg);
+        e = launch_prep<false, NKB>(a, q, k, v, g, beta, nullptr, ws, rec, c0, c1, c0 > 0, status, st);
+        if (e == cudaSuccess)
+            e = launch_pdl(kern, dim3(rec.ns, a.B * a.H), dim3(kWalkThreads), Walk<kFwd, NKB>::bytes, st, a,
+                           c0 == 0 ? W0 : between, c1 == rec.nch ? Wf : between, (__nv_bfloat16 *)y, (uint8_t *)ws, rec,
+                           c0, c1, status);
+    }
+    return e;
 }
 
 template <int NKB>
 cudaError_t walks(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g, const void *beta,
                   const float *W0, const void *dy, const float *dWf, float *dW0, void *ws, const GatedRecord &rec,
                   unsigned *status, cudaStream_t st) {
-    cudaError_t e = launch_prep<true, NKB>(a, q, k, v, g, beta, dy, ws, rec, status, st);
+    cudaError_t e = launch_prep<true, NKB>(a, q, k, v, g, beta, dy, ws, rec, 0, rec.nch, false, status, st);
     if (e != cudaSuccess)
         return e;
     auto *kern = gated_tc_both_walks_kernel<NKB>;
@@ -1018,12 +1051,15 @@ cudaError_t walks(const GatedArgs &a, const void *q, const void *k, const void *
 cudaError_t gated_tc_forward(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g,
                              const void *beta, const float *W0, float *Wf, void *y, void *ws, cudaStream_t st) {
     unsigned *status = nullptr;
+    int sms = 0;
     cudaError_t e = status_word(&status);
+    if (e == cudaSuccess)
+        e = device_sms(&sms);
     if (e != cudaSuccess)
         return e;
     const GatedRecord rec = gated_forward_record(a.L, a.d_k, a.d_v);
-    return rec.nkb == 1 ? forward<1>(a, q, k, v, g, beta, W0, Wf, y, ws, rec, status, st)
-                        : forward<2>(a, q, k, v, g, beta, W0, Wf, y, ws, rec, status, st);
+    return rec.nkb == 1 ? forward<1>(a, q, k, v, g, beta, W0, Wf, y, ws, rec, sms, status, st)
+                        : forward<2>(a, q, k, v, g, beta, W0, Wf, y, ws, rec, sms, status, st);
 }
 
 cudaError_t gated_tc_walks(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g,
