@@ -197,7 +197,7 @@ __host__ __device__ inline PrepSmem prep_smem(int nkb, int nvb) {
     const uint32_t work = C * LC * 4 + 4096, v = (uint32_t)nvb * 8192;
     s.tt = s.at + (work > v ? work : v);
     s.tok = s.tt + C * LC * 4;
-    s.bar = s.tok + C * 32;
+    s.bar = s.tok + C * 44;
     s.bytes = s.bar + 64 + 1024;
     return s;
 }
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(NT, 2)
     gated_tc_prep_kernel(GatedArgs a, const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ k,
                          const __nv_bfloat16 *__restrict__ v, const __nv_bfloat16 *__restrict__ g,
                          const __nv_bfloat16 *__restrict__ beta, const __nv_bfloat16 *__restrict__ dy, uint8_t *ws,
-                         GatedRecord rec, int c0, int beside, int tmem_cols, unsigned *status) {
+                         GatedRecord rec, int c0, int beside, int ahead, int tmem_cols, unsigned *status) {
     constexpr int DKP = 64 * NKB;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -216,6 +216,7 @@ __global__ void __launch_bounds__(NT, 2)
     uint8_t *kq = sm + o.kq, *op = sm + o.op, *vt = sm + o.at;
     float *At = reinterpret_cast<float *>(sm + o.at), *tmp = At + C * LC, *Tt = reinterpret_cast<float *>(sm + o.tt);
     float *tok = reinterpret_cast<float *>(sm + o.tok); // per token: G hi, G lo, rk, beta, rq, e^G, e^{G_C-G}, -
+    float *cw = tok + 8 * C, *cb = cw + C, *cd = cb + C; // -beta e^G rk, beta, e^{G_C-G} rk
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + o.bar);
     uint32_t *slot = reinterpret_cast<uint32_t *>(bar + 1);
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, c = c0 + blockIdx.x, bh = blockIdx.y;
@@ -241,6 +242,20 @@ __global__ void __launch_bounds__(NT, 2)
     if (tid == 32) {
         mbar_init(bar, 1);
         fence_barrier_init();
+    }
+    if (tid == 64) { // into L2 what the CTA that takes this one's place will read (these are inputs)
+        const int64_t next = (int64_t)blockIdx.y * gridDim.x + blockIdx.x + ahead;
+        if (next < (int64_t)gridDim.x * gridDim.y) {
+            const int nc = c0 + (int)(next % gridDim.x), nbh = (int)(next / gridDim.x);
+            const size_t nk = (size_t)(nbh / a.H * a.Hk + nbh % a.H / (a.H / a.Hk)) * a.L + (size_t)nc * C;
+            const size_t nv = (size_t)nbh * a.L + (size_t)nc * C;
+            const uint32_t rows = (uint32_t)min(C, a.L - nc * C);
+            l2_prefetch(k + nk * a.d_k, rows * a.d_k * 2);
+            l2_prefetch(q + nk * a.d_k, rows * a.d_k * 2);
+            l2_prefetch(v + nv * a.d_v, rows * a.d_v * 2);
+            if (BWD)
+                l2_prefetch(dy + nv * a.d_v, rows * a.d_v * 2);
+        }
     }
     // [K; Q], 16 bytes a thread and step
     {
@@ -345,7 +360,14 @@ __global__ void __launch_bounds__(NT, 2)
         for (int e = 0; e < 32; ++e)
             ss = e == lane ? x[e] : ss;
         ss += a.eps;
-        tok[i * 8 + (rr < C ? 2 : 4)] = !a.l2norm ? 1.f : ss > 0.f ? 1.f / sqrtf(ss) : ss;
+        ss = !a.l2norm ? 1.f : ss > 0.f ? 1.f / sqrtf(ss) : ss;
+        tok[i * 8 + (rr < C ? 2 : 4)] = ss;
+        if (rr < C) {
+            const float be = tok[i * 8 + 3];
+            cw[i] = -be * tok[i * 8 + 5] * ss;
+            cb[i] = be;
+            cd[i] = tok[i * 8 + 6] * ss;
+        }
     }
     __syncthreads();
     {
@@ -420,24 +442,34 @@ __global__ void __launch_bounds__(NT, 2)
     // 64-127 from MT (TMEM lanes 0-63, so the warps that can read those
     // lanes hold the lower rows) or, for W", from T^T.
     auto factor = [&](bool first, float (&x)[32]) {
-        if (rr >= C || (BWD && first)) {
+        const float *coef = (BWD && first && rr < C ? cd : first ? cw : cb) + 32 * half;
+        if (rr >= C) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const int j = 32 * half + e;
-                const float *d = tok + j * 8;
-                x[e] = rr >= C ? Tt[i * LC + j] * (first ? -d[3] * d[5] * d[2] : d[3]) : Tt[j * LC + i] * d[6] * d[2];
+            for (int e = 0; e < 32; e += 4) {
+                const float4 t = *reinterpret_cast<const float4 *>(Tt + i * LC + 32 * half + e);
+                x[e] = t.x;
+                x[e + 1] = t.y;
+                x[e + 2] = t.z;
+                x[e + 3] = t.w;
             }
+        } else if (BWD && first) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                x[e] = Tt[(32 * half + e) * LC + i];
         } else {
             tmem_ld16(tMT + tmem_lane_base(w) + (uint32_t)(32 * half), x);
             tmem_ld16(tMT + tmem_lane_base(w) + (uint32_t)(32 * half + 16), x + 16);
             tmem_ld_wait();
-            if (!BWD) {
+            if (BWD)
+                return;
+        }
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const float *d = tok + (32 * half + e) * 8;
-                    x[e] *= first ? -d[3] * d[5] * d[2] : d[3];
-                }
-            }
+        for (int e = 0; e < 32; e += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(coef + e);
+            x[e] *= f.x;
+            x[e + 1] *= f.y;
+            x[e + 2] *= f.z;
+            x[e + 3] *= f.w;
         }
     };
     auto put = [&](const float (&x)[32]) {
@@ -977,7 +1009,7 @@ __global__ void __launch_bounds__(kWalkThreads)
 template <bool BWD, int NKB>
 cudaError_t launch_prep(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g,
                         const void *beta, const void *dy, void *ws, const GatedRecord &rec, int c0, int c1, bool beside,
-                        unsigned *status, cudaStream_t st) {
+                        int num_sms, unsigned *status, cudaStream_t st) {
     using bf = __nv_bfloat16;
     auto *kern = gated_tc_prep_kernel<BWD, NKB>;
     const uint32_t smem = prep_smem(NKB, (a.d_v + 63) / 64).bytes;
@@ -989,17 +1021,17 @@ cudaError_t launch_prep(const GatedArgs &a, const void *q, const void *k, const 
     const int cols = a.d_v <= 128 ? 256 : 512;
     return launch_pdl(kern, dim3(c1 - c0, a.B * a.H), dim3(NT), smem, st, a, (const bf *)q, (const bf *)k,
                       (const bf *)v, (const bf *)g, (const bf *)beta, (const bf *)dy, (uint8_t *)ws, rec, c0,
-                      (int)beside, cols, status);
+                      (int)beside, 2 * num_sms, cols, status);
 }
 
 // Chunks in a segment of the forward.  Where the walk's CTAs leave most SMs
 // idle, a sequence is cut into segments and the preparation of one runs on the
 // idle SMs beside the walk over the one before.  A segment is a whole number
 // of waves of preparing CTAs (two an SM) and at least kMinSegment chunks, since
-// each costs the walk a start.  (16 heads, 16 381 tokens, d 128: %%A%% us in
-// one piece, %%B%% us in segments of 33 chunks; B2 H8 L2048, d_v 64: %%C%% us and
-// %%D%% us in two of 16.)
-constexpr int kMinSegment = 16;
+// each costs the walk a start.  (16 heads, 16 381 tokens, d 128: 624 us in
+// one piece, 506 in segments of 22 chunks, 742 in segments of 11; B2 H8 L2048,
+// d_v 64: 85 us in one piece, 77 in two of 16.)
+constexpr int kMinSegment = 12;
 int segment_chunks(const GatedArgs &a, const GatedRecord &rec, int num_sms) {
     const int64_t heads = (int64_t)a.B * a.H, walkers = heads * rec.ns;
     if (2 * walkers > num_sms)
@@ -1020,7 +1052,7 @@ cudaError_t forward(const GatedArgs &a, const void *q, const void *k, const void
     float *between = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + rec.off((int64_t)a.B * a.H, 0));
     for (int c0 = 0; c0 < rec.nch && e == cudaSuccess; c0 += seg) {
         const int c1 = std::min(rec.nch, c0 + seg);
-        e = launch_prep<false, NKB>(a, q, k, v, g, beta, nullptr, ws, rec, c0, c1, c0 > 0, status, st);
+        e = launch_prep<false, NKB>(a, q, k, v, g, beta, nullptr, ws, rec, c0, c1, c0 > 0, num_sms, status, st);
         if (e == cudaSuccess)
             e = launch_pdl(kern, dim3(rec.ns, a.B * a.H), dim3(kWalkThreads), Walk<kFwd, NKB>::bytes, st, a,
                            c0 == 0 ? W0 : between, c1 == rec.nch ? Wf : between, (__nv_bfloat16 *)y, (uint8_t *)ws, rec,
@@ -1032,8 +1064,8 @@ cudaError_t forward(const GatedArgs &a, const void *q, const void *k, const void
 template <int NKB>
 cudaError_t walks(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g, const void *beta,
                   const float *W0, const void *dy, const float *dWf, float *dW0, void *ws, const GatedRecord &rec,
-                  unsigned *status, cudaStream_t st) {
-    cudaError_t e = launch_prep<true, NKB>(a, q, k, v, g, beta, dy, ws, rec, 0, rec.nch, false, status, st);
+                  int num_sms, unsigned *status, cudaStream_t st) {
+    cudaError_t e = launch_prep<true, NKB>(a, q, k, v, g, beta, dy, ws, rec, 0, rec.nch, false, num_sms, status, st);
     if (e != cudaSuccess)
         return e;
     auto *kern = gated_tc_both_walks_kernel<NKB>;
@@ -1066,12 +1098,15 @@ cudaError_t gated_tc_walks(const GatedArgs &a, const void *q, const void *k, con
                            const void *beta, const float *W0, const void *dy, const float *dWf, float *dW0, void *ws,
                            cudaStream_t st) {
     unsigned *status = nullptr;
+    int sms = 0;
     cudaError_t e = status_word(&status);
+    if (e == cudaSuccess)
+        e = device_sms(&sms);
     if (e != cudaSuccess)
         return e;
     const GatedRecord rec = gated_backward_record(a.L, a.d_k, a.d_v);
-    return rec.nkb == 1 ? walks<1>(a, q, k, v, g, beta, W0, dy, dWf, dW0, ws, rec, status, st)
-                        : walks<2>(a, q, k, v, g, beta, W0, dy, dWf, dW0, ws, rec, status, st);
+    return rec.nkb == 1 ? walks<1>(a, q, k, v, g, beta, W0, dy, dWf, dW0, ws, rec, sms, status, st)
+                        : walks<2>(a, q, k, v, g, beta, W0, dy, dWf, dW0, ws, rec, sms, status, st);
 }
 
 } // namespace fw
