@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(NT, 2)
     {
         const float4 di = *reinterpret_cast<const float4 *>(tok + i * 8);
         const float fi = rr < C ? di.w * di.z : a.scale * tok[i * 8 + 4];
-#pragma unroll
+#pragma unroll 1
         for (int p = 0; p < 2; ++p) {
             const int j0 = 32 * half + 16 * p;
             float x[16];
@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(NT, 2)
             return;
         for (int p0 = half; p0 < a.d_v / 16; p0 += 4) {
             sent();
-#pragma unroll
+#pragma unroll 1
             for (int e = 0; e < 2; ++e) {
                 const int p = p0 + 2 * e;
                 if (p >= a.d_v / 16)
@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(NT, 2)
     auto images_out = [&]() {
         uint8_t *hi_at = NKB == 2 ? op + w * 4096 : op + (rr < C ? 0 : 16384),
                 *lo_at = NKB == 2 ? vt + w * 4096 : hi_at + 8192;
-#pragma unroll
+#pragma unroll 1
         for (int p = 0; p < DKP / 32; ++p) {
             const int c0 = half * (DKP / 2) + 16 * p;
             float x[16];
