@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(NT, 2)
 }
 
 // ------------------------------------------------------------------ walk
-// One CTA per (value head, 32 value channels).  An MMA of 128 rows takes the
+// One CTA per (value head, TP tiles of 32 value channels).  An MMA of 128 rows takes the
 // same time for any N up to 128 here (66 cycles), so the serial product has
 // the hi and the lo rows of its 64 x d_k factor stacked as its 128 rows, 8
 // MMAs of it for d_k 128, against [Z hi | Z lo] side by side; the answers'
@@ -666,45 +666,50 @@ __global__ void __launch_bounds__(NT, 2)
 // after that.  (One tile of W' and Q' rows, hi then lo, had 16 MMAs on the
 // serial path: 1.6 us a chunk instead of 1.2.)
 //
-// Eight worker warps.  Warps 0, 1, 4, 5 read the hi rows' result, warps 2, 3,
+// Eight worker warps a tile.  Of a tile's, warps 0, 1, 4, 5 read the hi rows' result, warps 2, 3,
 // 6, 7 the lo rows' of the same tokens (a warp reaches 32 of the 128 TMEM
 // lanes); the two swap halves of their 16 channels through shared memory and
 // each finishes 8 channels.  Thread (row 32 (w % 4) + lane, 16 channels) also
-// holds 16 values of the fp32 state (row = key channel).  A ninth warp's first
-// lane issues the MMAs and a tenth's asks for the records, each part as soon
+// holds 16 values of the fp32 state (row = key channel).  One more warp's first
+// lane issues the MMAs and another's asks for the records, each part as soon
 // as the product that last read its place is done, so that none of that is on
 // a worker's path.  Workers tell them by two mbarriers that the state's or
 // the values' tile is written; commits tell workers that a product is done.
+//
+// TP: with one tile a CTA the chain of a chunk is shortest; two tiles read the
+// records half as often, which is what counts once there are more CTAs than
+// SMs (the backward at B8 H16 L2048, 1024 CTAs with one tile: 955 us with one
+// tile, its walks 341, at 9 TB/s out of L2; 893 with two).
 enum { kFwd = 0, kKeep = 1, kRev = 2 };
-constexpr int kWalkThreads = NT + 64;
+constexpr int walk_threads(int TP) { return NT * TP + 64; }
 
-template <int MODE, int NKB> struct Walk {
+template <int MODE, int NKB, int TP> struct Walk {
     static constexpr int RB = MODE == kRev ? 128 : 64;     // tokens the B^T tile holds
     static constexpr int RV = MODE == kFwd ? 128 : 64;     // base rows: U', then Y'
     static constexpr uint32_t A = NKB * 16384 * (MODE == kFwd ? 2 : 1), B = NKB * RB * 128,
-                              SCAL = MODE == kRev ? 1024 : 512;
-    static constexpr uint32_t b = A, base = b + B, rec = base + RV * 128;
+                              SCAL = MODE == kRev ? 528 : 512;
+    static constexpr uint32_t b = A, base = b + B, rec = base + TP * RV * 128;
     // A product of one 64-wide block reads one more (its rows go unused): what
     // follows in this order covers it.
-    static constexpr uint32_t z = 2 * rec, u = z + NKB * 8192, scal = u + RB * 128, bar = scal + 2 * SCAL,
+    static constexpr uint32_t z = 2 * rec, u = z + TP * NKB * 8192, scal = u + TP * RB * 128, bar = scal + 2 * SCAL,
                               bytes = bar + 128 + 1024;
     static_assert(rec + b + B + (NKB == 1 ? B : 0) <= bar && bytes <= 232448, "reads stay inside shared memory");
-    static constexpr uint32_t cols = MODE == kFwd ? 256 : 128; // TMEM: the values' 64, the state's 64, the answers' 64
+    static constexpr uint32_t cols = TP * (MODE == kFwd ? 256 : 128); // TMEM: a tile's values, state, answers: 64 each
 };
 
-template <int MODE, int NKB>
+template <int MODE, int NKB, int TP>
 FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const float *__restrict__ Z0,
                  float *__restrict__ Zf, __nv_bfloat16 *__restrict__ y, uint8_t *ws, const GatedRecord &rec, int c0,
                  int c1, unsigned *status) {
-    using L = Walk<MODE, NKB>;
-    constexpr int DKP = 64 * NKB;
+    using L = Walk<MODE, NKB, TP>;
+    constexpr int DKP = 64 * NKB, WORKERS = 8 * TP;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *zt = sm + L::z, *ut = sm + L::u;
     uint64_t *fullA = reinterpret_cast<uint64_t *>(sm + L::bar), *fullB = fullA + 2, *m1 = fullA + 4, *m2 = fullA + 5,
              *my = fullA + 6, *zr = fullA + 7, *ur = fullA + 8;
     uint32_t *slot = reinterpret_cast<uint32_t *>(fullA + 9);
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, sl = blockIdx.x, bh = blockIdx.y, n0 = sl * NV;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, sl = blockIdx.x, bh = blockIdx.y, n0 = sl * TP * NV;
     const int b = bh / a.H;
     griddep_wait();
     const int len = seq_len(a, b), nch = max(0, min(c1, (len + C - 1) / C) - c0); // of chunks c0 .. c1 - 1
@@ -715,24 +720,25 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
     if (tid == 32) {
         for (int e = 0; e < 7; ++e)
             mbar_init(fullA + e, 1);
-        mbar_init(zr, NT / 32);
-        mbar_init(ur, NT / 32 + (MODE == kFwd ? 0 : 1)); // the state's copy has left its tile, too
+        mbar_init(zr, WORKERS);
+        mbar_init(ur, WORKERS + (MODE == kFwd ? 0 : 1)); // the state's copy has left its tile, too
         fence_barrier_init();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     griddep_launch_dependents();
-    const uint32_t tm = *slot, tU = tm, tZ = tm + 64, tY = tm + 128;
+    const uint32_t tm = *slot, tU = tm, tZ = tm + 64 * TP, tY = tm + 128 * TP;
     auto chunk_of = [&](int it) { return c0 + (MODE == kRev ? nch - 1 - it : it); };
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (ok)
             ok = mbar_wait(bar, parity, status);
     };
-    if (w == NT / 32) { // the MMAs
+    if (w == WORKERS) { // the MMAs
         if (lane == 0) {
-            const uint64_t dz = desc_sw128(smem_u32(zt), 8192, 1024), du = desc_sw128(smem_u32(ut), 8192, 1024);
+            const uint64_t dz = desc_sw128(smem_u32(zt), DKP * 128, 1024),
+                           du = desc_sw128(smem_u32(ut), L::RB * 128, 1024);
             const uint64_t dA0 = desc_sw128(smem_u32(sm), 16, 1024);
             const uint64_t dB0 = desc_sw128(smem_u32(sm + L::b), L::RB * 128, 1024);
             for (int it = 0; it < nch; ++it) {
@@ -744,14 +750,14 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
                 tc_fence_after();
 #pragma unroll
                 for (int s = 0; s < 4 * NKB; ++s)
-                    mma_bf16(tU, at(dA, kmajor_step(s, 128)), at(dz, (uint32_t)s * 2048u), idesc_bf16(128, 64, 0, 1),
+                    mma_bf16(tU, at(dA, kmajor_step(s, 128)), at(dz, (uint32_t)s * 2048u), idesc_bf16(128, 64 * TP, 0, 1),
                              s > 0);
                 mma_commit(m1);
                 if (MODE == kFwd) {
 #pragma unroll
                     for (int s = 0; s < 4 * NKB; ++s)
                         mma_bf16(tY, at(dA, (uint32_t)NKB * 16384u + kmajor_step(s, 128)), at(dz, (uint32_t)s * 2048u),
-                                 idesc_bf16(128, 64, 0, 1), s > 0);
+                                 idesc_bf16(128, 64 * TP, 0, 1), s > 0);
                     mma_commit(my);
                 }
                 wait(fullB + (it & 1), (it >> 1) & 1);
@@ -761,15 +767,15 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
                 tc_fence_after();
 #pragma unroll
                 for (int s = 0; s < L::RB / 16; ++s)
-                    mma_bf16(tZ, at(dB, (uint32_t)s * 2048u), at(du, (uint32_t)s * 2048u), idesc_bf16(128, 64, 1, 1),
+                    mma_bf16(tZ, at(dB, (uint32_t)s * 2048u), at(du, (uint32_t)s * 2048u), idesc_bf16(128, 64 * TP, 1, 1),
                              s > 0);
                 mma_commit(m2);
             }
         }
         __syncwarp();
-    } else if (w == NT / 32 + 1) { // the copies
+    } else if (w == WORKERS + 1) { // the copies
         if (lane == 0) {
-            const uint32_t pieces = (uint32_t)min(2, (a.d_v - n0) / 16);
+            const uint32_t pieces = (uint32_t)min(2 * TP, (a.d_v - n0) / 16), tiles = (pieces + 1) / 2;
             auto fetch_a = [&](int it) {
                 mbar_arrive_expect_tx(fullA + (it & 1), L::A);
                 bulk_g2s(sm + (it & 1) * L::rec, ws + rec.off(bh, chunk_of(it)) + (MODE == kRev ? rec.A2 : rec.A), L::A,
@@ -789,7 +795,7 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
                     bulk_g2s(dst + L::b, src + rec.K, L::B, f);
                 }
                 bulk_g2s(sm + L::scal + (it & 1) * L::SCAL, src + (MODE == kRev ? rec.scalR : rec.scalF), L::SCAL, f);
-                bulk_g2s(dst + L::base, src + (MODE == kRev ? rec.base2 : rec.base) + (size_t)sl * L::RV * 128, base, f);
+                bulk_g2s(dst + L::base, src + (MODE == kRev ? rec.base2 : rec.base) + (size_t)sl * TP * L::RV * 128, base, f);
             };
             for (int it = 0; it < min(2, nch); ++it) {
                 fetch_a(it);
@@ -800,8 +806,8 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
                 if (!ok)
                     break;
                 if (MODE != kFwd) { // the state before this chunk, as it lies
-                    bulk_s2g(ws + rec.off(bh, chunk_of(it)) + (MODE == kKeep ? rec.S : rec.dS) + (size_t)sl * DKP * 128, zt,
-                             (uint32_t)DKP * 128u);
+                    bulk_s2g(ws + rec.off(bh, chunk_of(it)) + (MODE == kKeep ? rec.S : rec.dS) + (size_t)sl * TP * DKP * 128,
+                             zt, tiles * DKP * 128u);
                     bulk_commit();
                 }
                 if (it > 0 && it + 1 < nch)
@@ -825,9 +831,11 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
         __syncwarp();
     } else {
         const int rr = 32 * (w & 3) + lane, hf = w >> 2, i = rr & 63, c8 = (w >> 1) & 1; // c8: which 8 of the 16 channels
+        const int tile = hf >> 1, h2 = hf & 1; // which tile, which half of it
         const bool mine = n0 + 16 * hf < a.d_v; // these 16 channels exist (d_v is a multiple of 16)
         const bool zrow = 32 * (w & 3) < DKP;   // this warp holds rows of the state
-        const uint32_t lb = tmem_lane_base(w) + (uint32_t)(16 * hf);
+        const uint32_t lb = tmem_lane_base(w) + (uint32_t)(64 * tile + 16 * h2);
+        uint8_t *zt_ = zt + tile * DKP * 128, *ut_ = ut + tile * L::RB * 128;
         float z[16], x[8], y8[8], t0[16], t1[16];
         uint4 even[2], odd[2]; // kRev, lo rows' warps: dY's rows of the next two chunks
         auto read_dy = [&](int it, uint4 (&ahead)[2]) {
@@ -901,8 +909,8 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
         for (int e = 0; e < 16; ++e)
             z[e] = Z0 && mine && rr < a.d_k ? __ldcg(Z0 + ((size_t)bh * a.d_v + n0 + 16 * hf + e) * a.d_k + rr) : 0.f;
         if (zrow) {
-            put8(zt, rr, 2 * hf, z);
-            put8(zt, rr, 2 * hf + 1, z + 8);
+            put8(zt_, rr, 2 * h2, z);
+            put8(zt_, rr, 2 * h2 + 1, z + 8);
         }
         written(zr);
         if (MODE == kRev && c8) {
@@ -925,8 +933,8 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     t0[e] *= fy;
-                put8(ut, C + i, 2 * hf, t0);
-                put8(ut, C + i, 2 * hf + 1, t0 + 8);
+                put8(ut_, C + i, 2 * h2, t0);
+                put8(ut_, C + i, 2 * h2 + 1, t0 + 8);
                 if (it + 2 < nch)
                     read_dy(it + 2, ahead);
             }
@@ -940,7 +948,7 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 t0[e] = f * x[e];
-            put8(ut, i, 2 * hf + c8, t0);
+            put8(ut_, i, 2 * h2 + c8, t0);
             written(ur);
             if (MODE == kFwd) {
                 wait(my, it & 1);
@@ -948,8 +956,8 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
                 product(tY, place + 4096, y8);
                 if (mine && i < n)
                     store8(y + ((size_t)bh * a.L + (size_t)c * C + i) * a.d_v + n0 + 16 * hf + 8 * c8, y8);
-            } else { // U, or dX, for the gradients: a pair tile's row
-                put8(gr + (MODE == kKeep ? rec.U : rec.dX) + (size_t)sl * 8192, i, 2 * hf + c8, x);
+            } else if (sl * TP + tile < rec.ns) { // U, or dX, for the gradients: a pair tile's row
+                put8(gr + (MODE == kKeep ? rec.U : rec.dX) + (size_t)(sl * TP + tile) * 8192, i, 2 * h2 + c8, x);
             }
             wait(m2, it & 1);
             tc_fence_after();
@@ -960,8 +968,8 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     z[e] = fmaf(whole, z[e], t0[e] + t1[e]);
-                put8(zt, rr, 2 * hf, z);
-                put8(zt, rr, 2 * hf + 1, z + 8);
+                put8(zt_, rr, 2 * h2, z);
+                put8(zt_, rr, 2 * h2 + 1, z + 8);
             }
             written(zr);
         };
@@ -988,22 +996,22 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
 }
 
 template <int NKB>
-__global__ void __launch_bounds__(kWalkThreads)
+__global__ void __launch_bounds__(walk_threads(1))
     gated_tc_walk_kernel(GatedArgs a, const float *__restrict__ W0, float *__restrict__ Wf,
                          __nv_bfloat16 *__restrict__ y, uint8_t *ws, GatedRecord rec, int c0, int c1, unsigned *status) {
-    walk<kFwd, NKB>(a, nullptr, W0, Wf, y, ws, rec, c0, c1, status);
+    walk<kFwd, NKB, 1>(a, nullptr, W0, Wf, y, ws, rec, c0, c1, status);
 }
 // The backward's two walks need only the preparation, not each other: one
 // launch (B4 H8 L512, 64 CTAs each: 13 us and 15 us in two launches).
-template <int NKB>
-__global__ void __launch_bounds__(kWalkThreads)
+template <int NKB, int TP>
+__global__ void __launch_bounds__(walk_threads(TP))
     gated_tc_both_walks_kernel(GatedArgs a, const __nv_bfloat16 *__restrict__ dy, const float *__restrict__ W0,
                                const float *__restrict__ dWf, float *__restrict__ dW0, uint8_t *ws, GatedRecord rec,
                                unsigned *status) {
     if (blockIdx.z == 0)
-        walk<kRev, NKB>(a, dy, dWf, dW0, nullptr, ws, rec, 0, rec.nch, status);
+        walk<kRev, NKB, TP>(a, dy, dWf, dW0, nullptr, ws, rec, 0, rec.nch, status);
     else
-        walk<kKeep, NKB>(a, nullptr, W0, nullptr, nullptr, ws, rec, 0, rec.nch, status);
+        walk<kKeep, NKB, TP>(a, nullptr, W0, nullptr, nullptr, ws, rec, 0, rec.nch, status);
 }
 
 template <bool BWD, int NKB>
@@ -1054,11 +1062,25 @@ cudaError_t forward(const GatedArgs &a, const void *q, const void *k, const void
         const int c1 = std::min(rec.nch, c0 + seg);
         e = launch_prep<false, NKB>(a, q, k, v, g, beta, nullptr, ws, rec, c0, c1, c0 > 0, num_sms, status, st);
         if (e == cudaSuccess)
-            e = launch_pdl(kern, dim3(rec.ns, a.B * a.H), dim3(kWalkThreads), Walk<kFwd, NKB>::bytes, st, a,
+            e = launch_pdl(kern, dim3(rec.ns, a.B * a.H), dim3(walk_threads(1)), Walk<kFwd, NKB, 1>::bytes, st, a,
                            c0 == 0 ? W0 : between, c1 == rec.nch ? Wf : between, (__nv_bfloat16 *)y, (uint8_t *)ws, rec,
                            c0, c1, status);
     }
     return e;
+}
+
+template <int NKB, int TP>
+cudaError_t launch_both(const GatedArgs &a, const float *W0, const void *dy, const float *dWf, float *dW0, void *ws,
+                        const GatedRecord &rec, unsigned *status, cudaStream_t st) {
+    auto *kern = gated_tc_both_walks_kernel<NKB, TP>;
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(kern, allowed);
+    if (e != cudaSuccess)
+        return e;
+    constexpr uint32_t smem = Walk<kRev, NKB, TP>::bytes;
+    static_assert(smem >= Walk<kKeep, NKB, TP>::bytes, "one launch, the larger of the two");
+    return launch_pdl(kern, dim3((rec.ns + TP - 1) / TP, a.B * a.H, 2), dim3(walk_threads(TP)), smem, st, a,
+                      (const __nv_bfloat16 *)dy, W0, dWf, dW0, (uint8_t *)ws, rec, status);
 }
 
 template <int NKB>
@@ -1068,14 +1090,9 @@ cudaError_t walks(const GatedArgs &a, const void *q, const void *k, const void *
     cudaError_t e = launch_prep<true, NKB>(a, q, k, v, g, beta, dy, ws, rec, 0, rec.nch, false, num_sms, status, st);
     if (e != cudaSuccess)
         return e;
-    auto *kern = gated_tc_both_walks_kernel<NKB>;
-    static std::atomic<uint64_t> allowed{0};
-    e = allow_smem(kern, allowed);
-    if (e != cudaSuccess)
-        return e;
-    static_assert(Walk<kRev, NKB>::bytes >= Walk<kKeep, NKB>::bytes, "one launch, the larger of the two");
-    return launch_pdl(kern, dim3(rec.ns, a.B * a.H, 2), dim3(kWalkThreads), Walk<kRev, NKB>::bytes, st, a,
-                      (const __nv_bfloat16 *)dy, W0, dWf, dW0, (uint8_t *)ws, rec, status);
+    if (rec.ns > 1 && 2 * (int64_t)rec.ns * a.B * a.H > num_sms)
+        return launch_both<NKB, 2>(a, W0, dy, dWf, dW0, ws, rec, status, st);
+    return launch_both<NKB, 1>(a, W0, dy, dWf, dW0, ws, rec, status, st);
 }
 
 } // namespace
