@@ -35,7 +35,8 @@ using namespace tc;
 using bf = __nv_bfloat16;
 
 constexpr int C = kGatedChunk;
-constexpr int NT = 256;
+constexpr int PARTS = 4;         // the warps that share 32 rows split their columns
+constexpr int NT = 128 * PARTS;
 
 FW_DEV void split8(const float *x, uint4 &hi, uint4 &lo) {
     uint32_t h[4], l[4];
@@ -87,7 +88,7 @@ __host__ __device__ inline GradSmem grad_smem(int nkb) {
     o.acck = o.accq + (uint32_t)nkb * 16384;
     o.tok = o.acck + (uint32_t)nkb * 16384;
     o.red = o.tok + C * 32;
-    o.bar = o.red + 4 * (8 * C + 32);
+    o.bar = o.red + 4 * ((3 * PARTS + 1) * C + 32);
     o.bytes = o.bar + 64 + 1024;
     return o;
 }
@@ -98,20 +99,20 @@ __global__ void __launch_bounds__(NT)
                          const bf *__restrict__ dy, bf *__restrict__ dq, bf *__restrict__ dk, bf *__restrict__ dv,
                          bf *__restrict__ dg, bf *__restrict__ dbeta, const uint8_t *ws, GatedRecord rec,
                          unsigned *status) {
-    constexpr int DKP = 64 * NKB, HC = DKP / 2; // channels per thread of a row
+    constexpr int DKP = 64 * NKB, HC = DKP / PARTS; // channels per thread of a row
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const GradSmem o = grad_smem(NKB);
     uint8_t *kq = sm, *ef = sm + o.ef;
     float *tok = reinterpret_cast<float *>(sm + o.tok); // per token: G hi, G lo, rk, beta, rq, e^G, e^{G_C-G}, -
     float *red = reinterpret_cast<float *>(sm + o.red);
-    float *r_qa = red, *r_kh = red + 2 * C, *r_kw = red + 4 * C, *r_xv = red + 6 * C,
-          *r_ss = red + 8 * C, *r_last = r_ss + 8; // qa, kh, kw: one value per half
+    float *r_qa = red, *r_kh = red + PARTS * C, *r_kw = red + 2 * PARTS * C, *r_xv = red + 3 * PARTS * C,
+          *r_ss = r_xv + C, *r_last = r_ss + 16; // qa, kh, kw: one value per part
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + o.bar), *done = full + 2, *kqb = full + 4, *mm = full + 5;
     uint32_t *slot = reinterpret_cast<uint32_t *>(full + 6);
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, c = blockIdx.x, bk = blockIdx.y;
     const int b = bk / a.Hk, grp = a.H / a.Hk, ns = rec.ns;
-    const int rr = 32 * (w & 3) + lane, half = w >> 2, i = rr & 63;
+    const int rr = 32 * (w & 3) + lane, part = w >> 2, i = rr & 63;
     griddep_wait();
     const int len = a.lengths ? min(max(__ldcg(a.lengths + b), 0), a.L) : a.L;
     const int n = min(C, len - c * C), rows = min(C, a.L - c * C); // tokens; rows in memory
@@ -171,10 +172,10 @@ __global__ void __launch_bounds__(NT)
         bulk_g2s(kq, record(0) + rec.K, NKB * 16384, kqb);
     }
     const uint32_t kq_s = smem_u32(kq), ef_s = smem_u32(ef);
-    // a thread's part of the sums over the value heads: row i, channels half * HC ..
-    float4 *accq = reinterpret_cast<float4 *>(sm + o.accq) + (size_t)half * (HC / 4) * C + i;
-    float4 *acck = reinterpret_cast<float4 *>(sm + o.acck) + (size_t)half * (HC / 4) * C + i;
-    float4 *stage = reinterpret_cast<float4 *>(sm + o.stage) + (size_t)half * (HC / 4) * C + i;
+    // a thread's part of the sums over the value heads: row i, channels part * HC ..
+    float4 *accq = reinterpret_cast<float4 *>(sm + o.accq) + (size_t)part * (HC / 4) * C + i;
+    float4 *acck = reinterpret_cast<float4 *>(sm + o.acck) + (size_t)part * (HC / 4) * C + i;
+    float4 *stage = reinterpret_cast<float4 *>(sm + o.stage) + (size_t)part * (HC / 4) * C + i;
     int gs = 0; // slices seen
     for (int m = 0; m < grp; ++m) {
         const size_t r0 = (size_t)(bk * grp + m) * a.L + (size_t)c * C;
@@ -190,10 +191,12 @@ __global__ void __launch_bounds__(NT)
             reinterpret_cast<float4 *>(tok)[tid] =
                 __ldcg(reinterpret_cast<const float4 *>(record(m) + rec.tok) + tid);
         float xv = 0.f, ss = 0.f;
-        const int yr = tid >> 2, yc = tid & 3; // dY, dX, V: row, 8 of 32 channels
+        // the first 256 threads: a row and 8 of 32 channels of dY, dX, V; the others: <S, dS'>
+        const bool rowed = tid < 256;
+        const int yr = (tid >> 2) & 63, yc = tid & 3;
         for (int s = 0; s < ns; ++s, ++gs) {
             uint8_t *sl = ef + (gs & 1) * o.slice;
-            const bool in = 32 * s + 8 * yc < a.d_v && yr < n;
+            const bool in = rowed && 32 * s + 8 * yc < a.d_v && yr < n;
             const size_t at = (r0 + yr) * a.d_v + 32 * s + 8 * yc;
             uint4 yv = make_uint4(0, 0, 0, 0), vv = yv;
             if (in) {
@@ -202,12 +205,14 @@ __global__ void __launch_bounds__(NT)
             }
             if (s >= 2) // the slice that lay here has been multiplied (dY's rows are not part of the copy)
                 wait(done + (gs & 1), ((gs >> 1) + 1) & 1);
-            *reinterpret_cast<uint4 *>(sl + o.yx + pair_chunk(yr, yc)) = yv;
-            *reinterpret_cast<uint4 *>(sl + o.yx + pair_chunk(yr, yc + 4)) = make_uint4(0, 0, 0, 0);
+            if (rowed) {
+                *reinterpret_cast<uint4 *>(sl + o.yx + pair_chunk(yr, yc)) = yv;
+                *reinterpret_cast<uint4 *>(sl + o.yx + pair_chunk(yr, yc + 4)) = make_uint4(0, 0, 0, 0);
+            }
             wait(full + (gs & 1), (gs >> 1) & 1);
             if (s == 0)
                 __syncthreads(); // tok
-            {
+            if (rowed) {
                 float x[8], y[8];
                 pair8(sl + o.yx + 8192, yr, yc, x);
                 widen8(vv, y);
@@ -219,16 +224,17 @@ __global__ void __launch_bounds__(NT)
                 }
                 if (in)
                     store8(dv + at, x);
-            }
+            } else {
 #pragma unroll
-            for (int e = 0; e < DKP * 4 / NT; ++e) {
-                const int p = tid + e * NT;
-                float x[8], y[8];
-                pair8(sl + o.s, p >> 2, p & 3, x);
-                pair8(sl + o.ds, p >> 2, p & 3, y);
+                for (int e = 0; e < DKP * 4 / 256; ++e) {
+                    const int p = tid - 256 + e * 256;
+                    float x[8], y[8];
+                    pair8(sl + o.s, p >> 2, p & 3, x);
+                    pair8(sl + o.ds, p >> 2, p & 3, y);
 #pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    ss = fmaf(x[u], y[u], ss);
+                    for (int u = 0; u < 8; ++u)
+                        ss = fmaf(x[u], y[u], ss);
+                }
             }
             fence_async_smem();
             tc_fence_before();
@@ -262,7 +268,7 @@ __global__ void __launch_bounds__(NT)
             wait(kqb, 0);
         xv += __shfl_xor_sync(0xffffffffu, xv, 1);
         xv += __shfl_xor_sync(0xffffffffu, xv, 2);
-        if (yc == 0)
+        if (rowed && yc == 0)
             r_xv[yr] = xv;
         ss = warp_sum(ss);
         if (lane == 0)
@@ -272,9 +278,8 @@ __global__ void __launch_bounds__(NT)
         // E and F, as [E; F] rk_j (K-major) and as [F (-beta rk_i); E rq_i]
         {
             const float fr = rr < C ? dj_.x : -di.w * di.z;
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const int j0 = 32 * half + 16 * p;
+            {
+                const int j0 = 16 * part;
                 float x[16], y[16];
                 tmem_ld16(tB + lb + (uint32_t)j0, x);
                 tmem_ld_wait();
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(NT)
 #pragma unroll
         for (int p = 0; p < HC; p += 16) {
             float t[16];
-            tmem_ld16(tA + lb + (uint32_t)(half * HC + p), t);
+            tmem_ld16(tA + lb + (uint32_t)(part * HC + p), t);
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 16; ++e)
@@ -330,14 +335,14 @@ __global__ void __launch_bounds__(NT)
         }
         // k_j . (e^{G_C-G_j} dS'^T U_j), for the chunk's decay
         auto kq_row = [&](int row, int p, float (&u)[8]) {
-            widen8(*reinterpret_cast<const uint4 *>(kq + kmajor_chunk(row, half * HC + p, 128)), u);
+            widen8(*reinterpret_cast<const uint4 *>(kq + kmajor_chunk(row, part * HC + p, 128)), u);
         };
         float last = 0.f;
         if (rr < C) {
 #pragma unroll
             for (int p = 0; p < HC; p += 16) {
                 float t[16];
-                tmem_ld16(tW + lb + (uint32_t)(half * HC + p), t);
+                tmem_ld16(tW + lb + (uint32_t)(part * HC + p), t);
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; e += 8) {
@@ -350,16 +355,16 @@ __global__ void __launch_bounds__(NT)
             }
             last = warp_sum(last * di.z * dj_.z);
             if (lane == 0)
-                r_last[w] = last; // warps 0, 1, 4, 5
+                r_last[w] = last; // (warps with w & 2 == 0)
         }
         wait(mm, (uint32_t)m & 1);
         tc_fence_after();
         {
-            float dot = 0.f; // q.a or k.h, this half's channels
+            float dot = 0.f; // q.a or k.h, this part's channels
 #pragma unroll
             for (int p = 0; p < HC; p += 16) {
                 float t[16];
-                tmem_ld16(tA + lb + (uint32_t)(half * HC + p), t);
+                tmem_ld16(tA + lb + (uint32_t)(part * HC + p), t);
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; e += 8) {
@@ -373,9 +378,9 @@ __global__ void __launch_bounds__(NT)
                 }
             }
             if (rr < C)
-                r_qa[half * C + i] = dot * dj_.x;
+                r_qa[part * C + i] = dot * dj_.x;
             else
-                r_kh[half * C + i] = dot * di.z;
+                r_kh[part * C + i] = dot * di.z;
         }
         if (rr >= C) {
 #pragma unroll
@@ -398,8 +403,8 @@ __global__ void __launch_bounds__(NT)
 #pragma unroll
             for (int p = 0; p < HC; p += 16) {
                 float t[16], u1[16];
-                tmem_ld16(tW + lb + (uint32_t)(half * HC + p), t);
-                tmem_ld16(tE + lb + (uint32_t)(half * HC + p), u1);
+                tmem_ld16(tW + lb + (uint32_t)(part * HC + p), t);
+                tmem_ld16(tE + lb + (uint32_t)(part * HC + p), u1);
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; e += 8) {
@@ -422,7 +427,7 @@ __global__ void __launch_bounds__(NT)
                     acck[((p + e) / 4) * C] = r;
                 }
             }
-            r_kw[half * C + i] = dot * di.z;
+            r_kw[part * C + i] = dot * di.z;
         }
         tc_fence_before();
         __syncthreads();
@@ -432,17 +437,25 @@ __global__ void __launch_bounds__(NT)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int t = 2 * lane + e;
-                const float kh = r_kh[t] + r_kh[C + t];
-                G2[e] = r_qa[t] + r_qa[C + t] - tok[t * 8 + 3] * kh - (r_kw[t] + r_kw[C + t]);
+                float qa = 0.f, kh = 0.f, kw = 0.f;
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p) {
+                    qa += r_qa[p * C + t];
+                    kh += r_kh[p * C + t];
+                    kw += r_kw[p * C + t];
+                }
+                G2[e] = qa - tok[t * 8 + 3] * kh - kw;
                 if (t < n)
                     io<bf>::store(dbeta + r0 + t, r_xv[t] - kh);
             }
             if (lane == 31) {
-                float s8 = 0.f;
+                float s = 0.f, l = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    s8 += r_ss[e];
-                G2[1] += tok[(C - 1) * 8 + 5] * s8 + (r_last[0] + r_last[1]) + (r_last[4] + r_last[5]);
+                for (int e = 0; e < NT / 32; ++e) {
+                    s += r_ss[e];
+                    l += e & 2 ? 0.f : r_last[e];
+                }
+                G2[1] += tok[(C - 1) * 8 + 5] * s + l;
             }
             float run = G2[0] + G2[1];
 #pragma unroll
@@ -473,26 +486,26 @@ __global__ void __launch_bounds__(NT)
 #pragma unroll
         for (int p = 0; p < HC; p += 8) {
             float u[8];
-            widen8(*reinterpret_cast<const uint4 *>(kq + kmajor_chunk(rr, half * HC + p, 128)), u);
+            widen8(*reinterpret_cast<const uint4 *>(kq + kmajor_chunk(rr, part * HC + p, 128)), u);
             const float4 s = acc[(p / 4) * C], t = acc[(p / 4 + 1) * C];
             dot += u[0] * s.x + u[1] * s.y + u[2] * s.z + u[3] * s.w + u[4] * t.x + u[5] * t.y + u[6] * t.z + u[7] * t.w;
         }
-        red[half * 2 * C + rr] = dot * r;
+        red[part * 2 * C + rr] = dot * r;
         __syncthreads();
-        const float f = a.l2norm ? (red[rr] + red[2 * C + rr]) * r : 0.f;
+        const float f = a.l2norm ? (red[rr] + red[2 * C + rr] + red[4 * C + rr] + red[6 * C + rr]) * r : 0.f;
         if (i < rows) {
             bf *to = (rr < C ? dk : dq) + krow + (size_t)i * a.d_k;
 #pragma unroll
             for (int p = 0; p < HC; p += 8) {
                 float u[8];
-                widen8(*reinterpret_cast<const uint4 *>(kq + kmajor_chunk(rr, half * HC + p, 128)), u);
+                widen8(*reinterpret_cast<const uint4 *>(kq + kmajor_chunk(rr, part * HC + p, 128)), u);
                 const float4 s = acc[(p / 4) * C], t = acc[(p / 4 + 1) * C];
                 const float g8[8] = {s.x, s.y, s.z, s.w, t.x, t.y, t.z, t.w};
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     u[e] = i < n ? r * (g8[e] - u[e] * f) : 0.f;
-                if (half * HC + p < a.d_k)
-                    store8(to + half * HC + p, u);
+                if (part * HC + p < a.d_k)
+                    store8(to + part * HC + p, u);
             }
         }
     }
