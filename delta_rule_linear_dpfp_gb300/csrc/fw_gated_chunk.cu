@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(NT)
     __syncthreads();
     const size_t ch = (size_t)bh * gridDim.x + c;
     {
-        const int ti = tid & 15, tj = tid >> 4;
+        const int ti = (tid & 7) + 8 * ((tid >> 5) & 1), tj = ((tid >> 3) & 3) + 4 * (tid >> 6);
         float akk[4][4] = {}, aqk[4][4] = {};
         mm_nt<4, 4>(akk, kt + ti * ldk, ldk, 16, kt + tj * ldk, ldk, 16, a.d_k);
         mm_nt<4, 4>(aqk, qt + ti * ldk, ldk, 16, kt + tj * ldk, ldk, 16, a.d_k);
@@ -294,44 +294,115 @@ __global__ void __launch_bounds__(NT)
         ws.tok[ch * C * TOK + e] = tok[e];
 }
 
+// 16-byte asynchronous copies into shared memory; `in` false writes zeros.
+FW_DEV void copy16(float *dst, const float *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(in ? 16 : 0)
+                 : "memory");
+}
+FW_DEV void copies_sent() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> FW_DEV void copies_done() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// rows x width (a power of two, given as the logarithm of its quarter) of a
+// tensor whose rows at or past `valid` and columns at or past `cols` read as zero.
+FW_DEV void copy_tile(float *dst, int ldd, const float *src, size_t lds, int rows, int valid, int cols, int log_w4) {
+    for (int e = threadIdx.x; e < rows << log_w4; e += NT) {
+        const int i = e >> log_w4, c = (e & ((1 << log_w4) - 1)) * 4;
+        const bool in = i < valid && c < cols;
+        copy16(dst + i * ldd + c, in ? src + (size_t)i * lds + c : src, in);
+    }
+}
+FW_DEV int log2_of(int x) { return 31 - __clz(x); }
+
+// A thread's rows (ti + 32 r) and columns (4 tj ..) of a tile: a warp covers 8
+// rows by 4 column groups, so that both operands' 16-byte reads are one
+// wavefront each (32 rows a warp took four for one of them).
+FW_DEV int row_of(int tid) { return (tid & 7) + 8 * ((tid >> 5) & 3); }
+FW_DEV int column_of(int tid) { return ((tid >> 3) & 3) + 4 * (tid >> 7); }
+
+// Z[n][k] <- whole Z[n][k] + sum_t A[t][n] B[t][k] (+ the same of A2, B2):
+// the state's 32 x d_k, four rows and four columns a thread.
+FW_DEV void update_state(float *Z, int ldk, float whole, const float *A, const float *B, const float *A2,
+                         const float *B2, int d_k) {
+    const int kg = d_k / 4, k4 = (threadIdx.x % kg) * 4, n0 = (threadIdx.x / kg) * 4;
+    if (n0 >= NV)
+        return;
+    float s[4][4] = {};
+    for (int src = 0; src < (A2 ? 2 : 1); ++src) {
+        const float *a = (src ? A2 : A) + n0, *b = (src ? B2 : B) + k4;
+#pragma unroll 4
+        for (int t = 0; t < C; ++t) {
+            const float4 x = lds4(a + t * LV), y = lds4(b + t * ldk);
+            const float xr[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                s[r][0] = fmaf(xr[r], y.x, s[r][0]);
+                s[r][1] = fmaf(xr[r], y.y, s[r][1]);
+                s[r][2] = fmaf(xr[r], y.z, s[r][2]);
+                s[r][3] = fmaf(xr[r], y.w, s[r][3]);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        float *p = Z + (n0 + r) * ldk + k4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            p[e] = fmaf(whole, p[e], s[r][e]);
+    }
+}
+
 // ------------------------------------------------------------------ walk
-// One CTA per (value head, 32 value channels).  KEEP: the chunks' first
-// states and U stay in the workspace for the gradients (no answers then).
+// One CTA per (value head, 32 value channels).  A chunk's keys, queries,
+// values and scalars are copied a chunk ahead into a second buffer, T and M as
+// soon as the chunk before has used its own.  KEEP: the chunks' first states
+// and U stay in the workspace for the gradients (no answers then).
 template <bool KEEP>
 __global__ void __launch_bounds__(NT)
     gated_walk_kernel(GatedArgs a, const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
                       const float *__restrict__ W0, float *__restrict__ Wf, float *__restrict__ y, Ws ws) {
     extern __shared__ __align__(16) float sm[];
-    const int ldk = a.d_k + 4, nC = (a.L + C - 1) / C;
-    float *S = sm, *kq = S + NV * ldk, *Tt = kq + 2 * C * ldk, *Mt = Tt + C * LC, *Xt = Mt + C * LC, *Ut = Xt + C * LV,
-          *tok = Ut + C * LV;
-    const int tid = threadIdx.x, ti = tid & 31, tj = tid >> 5, bh = blockIdx.y, n0 = blockIdx.x * NV;
+    const int ldk = a.d_k + 4, nC = (a.L + C - 1) / C, lk4 = log2_of(a.d_k / 4), ahead = 2 * C * ldk + C * LV + C * TOK;
+    float *S = sm, *Tt = S + NV * ldk, *Mt = Tt + C * LC, *Ut = Mt + C * LC, *buf = Ut + C * LV; // buf: K, Q, V, tok; twice
+    const int tid = threadIdx.x, ti = row_of(tid), tj = column_of(tid), bh = blockIdx.y, n0 = blockIdx.x * NV;
     const int b = bh / a.H, kh = b * a.Hk + (bh % a.H) / (a.H / a.Hk);
     const int nv = min(NV, a.d_v - n0);
     griddep_launch_dependents();
     griddep_wait();
-    const int len = seq_len(a, b);
+    const int len = seq_len(a, b), nch = (len + C - 1) / C;
     const size_t st0 = ((size_t)bh * a.d_v + n0) * a.d_k;
-    load_tile(S, ldk, W0 + st0, a.d_k, NV, W0 ? nv : 0, a.d_k, a.d_k);
-    for (int c = 0; c < nC; ++c) {
+    auto fetch = [&](int c) {
+        float *p = buf + (c & 1) * ahead;
         const int n = min(C, len - c * C);
-        if (n <= 0)
-            break;
-        const size_t ch = (size_t)bh * nC + c, t0 = (size_t)c * C;
-        const size_t krow = ((size_t)kh * a.L + t0) * a.d_k, vrow = ((size_t)bh * a.L + t0) * a.d_v + n0;
-        __syncthreads();
-        load_tile(kq, ldk, k + krow, a.d_k, C, n, a.d_k, a.d_k);
-        load_tile(kq + C * ldk, ldk, q + krow, a.d_k, C, n, a.d_k, a.d_k);
-        load_tile(Tt, LC, ws.T + ch * C * C, C, C, C, C, C);
+        const size_t t0 = (size_t)c * C, krow = ((size_t)kh * a.L + t0) * a.d_k;
+        copy_tile(p, ldk, k + krow, a.d_k, C, n, a.d_k, lk4);
         if (!KEEP)
-            load_tile(Mt, LC, ws.M + ch * C * C, C, C, C, C, C);
-        load_tile(Xt, LV, v + vrow, a.d_v, C, n, nv, NV);
-        for (int e = tid; e < C * TOK; e += NT)
-            tok[e] = __ldcg(ws.tok + ch * C * TOK + e);
-        __syncthreads();
+            copy_tile(p + C * ldk, ldk, q + krow, a.d_k, C, n, a.d_k, lk4);
+        copy_tile(p + 2 * C * ldk, LV, v + ((size_t)bh * a.L + t0) * a.d_v + n0, a.d_v, C, n, nv, 3);
+        copy_tile(p + 2 * C * ldk + C * LV, TOK, ws.tok + ((size_t)bh * nC + c) * C * TOK, TOK, C, C, TOK, 1);
+    };
+    auto fetch_sq = [&](float *dst, const float *src, int c) {
+        copy_tile(dst, LC, src + ((size_t)bh * nC + c) * C * C, C, C, C, C, 4);
+    };
+    load_tile(S, ldk, W0 + st0, a.d_k, NV, W0 ? nv : 0, a.d_k, a.d_k);
+    if (nch > 0) {
+        fetch(0);
+        fetch_sq(Tt, ws.T, 0);
+        if (!KEEP)
+            fetch_sq(Mt, ws.M, 0);
+    }
+    copies_sent();
+    for (int c = 0; c < nch; ++c) {
+        const int n = min(C, len - c * C);
+        const size_t ch = (size_t)bh * nC + c, vrow = ((size_t)bh * a.L + (size_t)c * C) * a.d_v + n0;
+        float *kq = buf + (c & 1) * ahead, *Xt = kq + 2 * C * ldk, *tok = Xt + C * LV;
+        copies_done<0>();
+        __syncthreads(); // this chunk is here, and the last one's buffers are free
+        if (c + 1 < nch)
+            fetch(c + 1);
         if (KEEP)
-            for (int e = tid; e < nv * a.d_k; e += NT)
-                ws.S[ch * a.d_v * a.d_k + (size_t)n0 * a.d_k + e] = S[(e / a.d_k) * ldk + e % a.d_k];
+            for (int e = tid; e < nv << lk4; e += NT)
+                *reinterpret_cast<float4 *>(ws.S + ch * a.d_v * a.d_k + (size_t)n0 * a.d_k + 4 * e) =
+                    lds4(S + (e >> lk4) * ldk + (e & ((1 << lk4) - 1)) * 4);
         float acc[4][4] = {}; // rows ti, ti + 32 of K, then of Q; channels 4 tj ..
         if (KEEP) {
             float pk[2][4] = {};
@@ -364,6 +435,8 @@ __global__ void __launch_bounds__(NT)
                     make_float4(u[r][0], u[r][1], u[r][2], u[r][3]);
         }
         __syncthreads();
+        if (c + 1 < nch)
+            fetch_sq(Tt, ws.T, c + 1);
         if (!KEEP) {
             float o[2][4];
 #pragma unroll
@@ -377,36 +450,32 @@ __global__ void __launch_bounds__(NT)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
                 if (ti + 32 * r < n && tj * 4 < nv)
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        io<float>::store(y + vrow + (size_t)(ti + 32 * r) * a.d_v + tj * 4 + s, o[r][s]);
+                    *reinterpret_cast<float4 *>(y + vrow + (size_t)(ti + 32 * r) * a.d_v + tj * 4) =
+                        make_float4(o[r][0], o[r][1], o[r][2], o[r][3]);
+            __syncthreads();
+            if (c + 1 < nch)
+                fetch_sq(Mt, ws.M, c + 1);
         }
-        const float whole = tok[(C - 1) * TOK + 2];
+        copies_sent();
+        // rows of U weighted for the state, where X was
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int i = ti + 32 * r;
+            const float f = tok[i * TOK + 3] * tok[i * TOK];
+            *reinterpret_cast<float4 *>(Xt + i * LV + tj * 4) =
+                make_float4(f * u[r][0], f * u[r][1], f * u[r][2], f * u[r][3]);
+        }
         __syncthreads();
-        for (int e = tid; e < C * NV; e += NT) { // rows of U weighted for the state
-            const float *d = tok + (e >> 5) * TOK;
-            Ut[(e >> 5) * LV + (e & 31)] *= d[3] * d[0];
-        }
-        __syncthreads();
-        if (4 * ti < a.d_k) {
-            float s[4][4] = {};
-            mm_tn<4>(s, Ut + tj * 4, LV, 1, kq + 4 * ti, ldk, C);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                float *p = S + (tj * 4 + r) * ldk + 4 * ti;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    p[e] = fmaf(whole, p[e], s[r][e]);
-            }
-        }
+        update_state(S, ldk, tok[(C - 1) * TOK + 2], Xt, kq, nullptr, nullptr, a.d_k);
     }
+    copies_done<0>();
     __syncthreads();
     if (!KEEP) {
         if (Wf)
             for (int e = tid; e < nv * a.d_k; e += NT)
                 Wf[st0 + e] = S[(e / a.d_k) * ldk + e % a.d_k];
         for (size_t e = tid; e < (size_t)(a.L - len) * nv; e += NT) // no token, no answer
-            io<float>::store(y + ((size_t)bh * a.L + len + e / nv) * a.d_v + n0 + e % nv, 0.f);
+            y[((size_t)bh * a.L + len + e / nv) * a.d_v + n0 + e % nv] = 0.f;
     }
 }
 
@@ -415,32 +484,44 @@ __global__ void __launch_bounds__(NT)
     gated_reverse_kernel(GatedArgs a, const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ dy,
                          const float *__restrict__ dWf, float *__restrict__ dW0, Ws ws) {
     extern __shared__ __align__(16) float sm[];
-    const int ldk = a.d_k + 4, nC = (a.L + C - 1) / C;
-    float *D = sm, *kq = D + NV * ldk, *Tt = kq + 2 * C * ldk, *Mt = Tt + C * LC, *Yt = Mt + C * LC, *Ut = Yt + C * LV,
-          *tok = Ut + C * LV;
-    const int tid = threadIdx.x, ti = tid & 31, tj = tid >> 5, bh = blockIdx.y, n0 = blockIdx.x * NV;
+    const int ldk = a.d_k + 4, nC = (a.L + C - 1) / C, lk4 = log2_of(a.d_k / 4), ahead = 2 * C * ldk + C * LV + C * TOK;
+    float *D = sm, *Tt = D + NV * ldk, *Mt = Tt + C * LC, *Ut = Mt + C * LC, *buf = Ut + C * LV; // buf: K, Q, dY, tok; twice
+    const int tid = threadIdx.x, ti = row_of(tid), tj = column_of(tid), bh = blockIdx.y, n0 = blockIdx.x * NV;
     const int b = bh / a.H, kh = b * a.Hk + (bh % a.H) / (a.H / a.Hk);
     const int nv = min(NV, a.d_v - n0);
     griddep_launch_dependents();
     griddep_wait();
-    const int len = seq_len(a, b);
+    const int len = seq_len(a, b), nch = (len + C - 1) / C;
     const size_t st0 = ((size_t)bh * a.d_v + n0) * a.d_k;
-    load_tile(D, ldk, dWf + st0, a.d_k, NV, dWf ? nv : 0, a.d_k, a.d_k);
-    for (int c = (len + C - 1) / C - 1; c >= 0; --c) {
+    auto fetch = [&](int c) {
+        float *p = buf + (c & 1) * ahead;
         const int n = min(C, len - c * C);
-        const size_t ch = (size_t)bh * nC + c, t0 = (size_t)c * C;
-        const size_t krow = ((size_t)kh * a.L + t0) * a.d_k, vrow = ((size_t)bh * a.L + t0) * a.d_v + n0;
-        __syncthreads();
-        load_tile(kq, ldk, k + krow, a.d_k, C, n, a.d_k, a.d_k);
-        load_tile(kq + C * ldk, ldk, q + krow, a.d_k, C, n, a.d_k, a.d_k);
-        load_tile(Tt, LC, ws.T + ch * C * C, C, C, C, C, C);
-        load_tile(Mt, LC, ws.M + ch * C * C, C, C, C, C, C);
-        load_tile(Yt, LV, dy + vrow, a.d_v, C, n, nv, NV);
-        for (int e = tid; e < C * TOK; e += NT)
-            tok[e] = __ldcg(ws.tok + ch * C * TOK + e);
-        __syncthreads();
-        for (int e = tid; e < nv * a.d_k; e += NT)
-            ws.dS[ch * a.d_v * a.d_k + (size_t)n0 * a.d_k + e] = D[(e / a.d_k) * ldk + e % a.d_k];
+        const size_t t0 = (size_t)c * C, krow = ((size_t)kh * a.L + t0) * a.d_k;
+        copy_tile(p, ldk, k + krow, a.d_k, C, n, a.d_k, lk4);
+        copy_tile(p + C * ldk, ldk, q + krow, a.d_k, C, n, a.d_k, lk4);
+        copy_tile(p + 2 * C * ldk, LV, dy + ((size_t)bh * a.L + t0) * a.d_v + n0, a.d_v, C, n, nv, 3);
+        copy_tile(p + 2 * C * ldk + C * LV, TOK, ws.tok + ((size_t)bh * nC + c) * C * TOK, TOK, C, C, TOK, 1);
+    };
+    auto fetch_sq = [&](float *dst, const float *src, int c) {
+        copy_tile(dst, LC, src + ((size_t)bh * nC + c) * C * C, C, C, C, C, 4);
+    };
+    load_tile(D, ldk, dWf + st0, a.d_k, NV, dWf ? nv : 0, a.d_k, a.d_k);
+    if (nch > 0) {
+        fetch(nch - 1);
+        fetch_sq(Tt, ws.T, nch - 1);
+        fetch_sq(Mt, ws.M, nch - 1);
+    }
+    copies_sent();
+    for (int c = nch - 1; c >= 0; --c) {
+        const size_t ch = (size_t)bh * nC + c;
+        float *kq = buf + (c & 1) * ahead, *Yt = kq + 2 * C * ldk, *tok = Yt + C * LV;
+        copies_done<0>();
+        __syncthreads(); // this chunk is here, and the last one's buffers are free
+        if (c > 0)
+            fetch(c - 1);
+        for (int e = tid; e < nv << lk4; e += NT)
+            *reinterpret_cast<float4 *>(ws.dS + ch * a.d_v * a.d_k + (size_t)n0 * a.d_k + 4 * e) =
+                lds4(D + (e >> lk4) * ldk + (e & ((1 << lk4) - 1)) * 4);
         float u[2][4] = {};
         mm_nt<2, 4>(u, kq + ti * ldk, ldk, 32, D + tj * 4 * ldk, ldk, 1, a.d_k);
 #pragma unroll
@@ -456,9 +537,14 @@ __global__ void __launch_bounds__(NT)
             *reinterpret_cast<float4 *>(Ut + (ti + 32 * r) * LV + tj * 4) =
                 make_float4(u[r][0], u[r][1], u[r][2], u[r][3]);
         __syncthreads();
+        if (c > 0)
+            fetch_sq(Mt, ws.M, c - 1);
         float x[2][4] = {};
         mm_tn<2>(x, Tt + ti, LC, 32, Ut + tj * 4, LV, C);
         __syncthreads();
+        if (c > 0)
+            fetch_sq(Tt, ws.T, c - 1);
+        copies_sent();
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int i = ti + 32 * r;
@@ -473,21 +559,10 @@ __global__ void __launch_bounds__(NT)
                 Yt[i * LV + tj * 4 + s] *= wy;
             }
         }
-        const float whole = tok[(C - 1) * TOK + 2];
         __syncthreads();
-        if (4 * ti < a.d_k) {
-            float s[4][4] = {};
-            mm_tn<4>(s, Ut + tj * 4, LV, 1, kq + 4 * ti, ldk, C);
-            mm_tn<4>(s, Yt + tj * 4, LV, 1, kq + C * ldk + 4 * ti, ldk, C);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                float *p = D + (tj * 4 + r) * ldk + 4 * ti;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    p[e] = fmaf(whole, p[e], s[r][e]);
-            }
-        }
+        update_state(D, ldk, tok[(C - 1) * TOK + 2], Ut, kq, Yt, kq + C * ldk, a.d_k);
     }
+    copies_done<0>();
     __syncthreads();
     if (dW0)
         for (int e = tid; e < nv * a.d_k; e += NT)
@@ -711,7 +786,9 @@ __global__ void __launch_bounds__(NT)
 }
 
 size_t prep_smem(int d_k) { return sizeof(float) * (2 * C * (d_k + 4) + 2 * C * LC + 1024 + C * TOK); }
-size_t walk_smem(int d_k) { return sizeof(float) * ((NV + 2 * C) * (d_k + 4) + 2 * C * LC + 2 * C * LV + C * TOK); }
+size_t walk_smem(int d_k) {
+    return sizeof(float) * (NV * (d_k + 4) + 2 * C * LC + C * LV + 2 * (2 * C * (d_k + 4) + C * LV + C * TOK));
+}
 size_t grad_smem(int d_k) {
     return sizeof(float) * (2 * (C + NV) * (d_k + 4) + 2 * C * d_k + 3 * C * (NV + 4) + 2 * C * LC + C * TOK + C + 16);
 }
