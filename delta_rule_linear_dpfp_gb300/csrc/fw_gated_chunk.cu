@@ -44,13 +44,14 @@
 
 namespace fw {
 
+cudaError_t device_sms(int *out); // fw_api.cu
+
 namespace {
 
 constexpr int C = kGatedChunk;
 constexpr int NT = 256;  // threads per CTA
-constexpr int NV = 32;   // value channels per walk CTA
+constexpr int NV = 32;   // value channels per slice of the gradient kernel
 constexpr int LC = C + 4; // row stride of a C x C tile
-constexpr int LV = NV + 4;
 constexpr int TOK = 8; // floats per token: rk, rq, e^G, e^{G_C-G}, G high, G low, beta, unused
 constexpr float kGMin = -200.f; // e^g is 0 in fp32 below this: a gate of -inf is a sum that stays finite
 
@@ -313,14 +314,21 @@ FW_DEV void copy_tile(float *dst, int ldd, const float *src, size_t lds, int row
 }
 FW_DEV int log2_of(int x) { return 31 - __clz(x); }
 
-// A thread's rows (ti + 32 r) and columns (4 tj ..) of a tile: a warp covers 8
-// rows by 4 column groups, so that both operands' 16-byte reads are one
-// wavefront each (32 rows a warp took four for one of them).
-FW_DEV int row_of(int tid) { return (tid & 7) + 8 * ((tid >> 5) & 3); }
-FW_DEV int column_of(int tid) { return ((tid >> 3) & 3) + 4 * (tid >> 7); }
+// A walk CTA's channels: 32, or 16 where that still leaves SMs idle (the work
+// of a chunk is what a chunk takes then; B1 H4 L333 d 64: 61 us with 32,
+// 50 with 16).  A thread's rows of a tile are ti + S r (S = 64 / R, R rows of
+// each 64) and its columns 4 tj ..; a warp covers 8 rows by 4 column groups, so
+// that both operands' 16-byte reads are one wavefront each (32 rows a warp took
+// four for one of them).
+template <int NV> struct Tile {
+    static constexpr int R = NV / 16, S = C / R, LV = NV + 4, LOG4 = NV == 32 ? 3 : 2;
+    static FW_DEV int row(int tid) { return (tid & 7) + 8 * ((tid >> 5) & (8 / R - 1)); }
+    static FW_DEV int column(int tid) { return ((tid >> 3) & 3) + 4 * ((tid >> 5) / (8 / R)); }
+};
 
 // Z[n][k] <- whole Z[n][k] + sum_t A[t][n] B[t][k] (+ the same of A2, B2):
 // the state's 32 x d_k, four rows and four columns a thread.
+template <int NV>
 FW_DEV void update_state(float *Z, int ldk, float whole, const float *A, const float *B, const float *A2,
                          const float *B2, int d_k) {
     const int kg = d_k / 4, k4 = (threadIdx.x % kg) * 4, n0 = (threadIdx.x / kg) * 4;
@@ -331,7 +339,7 @@ FW_DEV void update_state(float *Z, int ldk, float whole, const float *A, const f
         const float *a = (src ? A2 : A) + n0, *b = (src ? B2 : B) + k4;
 #pragma unroll 4
         for (int t = 0; t < C; ++t) {
-            const float4 x = lds4(a + t * LV), y = lds4(b + t * ldk);
+            const float4 x = lds4(a + t * Tile<NV>::LV), y = lds4(b + t * ldk);
             const float xr[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -352,18 +360,20 @@ FW_DEV void update_state(float *Z, int ldk, float whole, const float *A, const f
 }
 
 // ------------------------------------------------------------------ walk
-// One CTA per (value head, 32 value channels).  A chunk's keys, queries,
+// One CTA per (value head, NV value channels).  A chunk's keys, queries,
 // values and scalars are copied a chunk ahead into a second buffer, T and M as
 // soon as the chunk before has used its own.  KEEP: the chunks' first states
 // and U stay in the workspace for the gradients (no answers then).
-template <bool KEEP>
+template <bool KEEP, int NV>
 __global__ void __launch_bounds__(NT)
     gated_walk_kernel(GatedArgs a, const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
                       const float *__restrict__ W0, float *__restrict__ Wf, float *__restrict__ y, Ws ws) {
+    using W = Tile<NV>;
+    constexpr int R = W::R, LV = W::LV;
     extern __shared__ __align__(16) float sm[];
     const int ldk = a.d_k + 4, nC = (a.L + C - 1) / C, lk4 = log2_of(a.d_k / 4), ahead = 2 * C * ldk + C * LV + C * TOK;
     float *S = sm, *Tt = S + NV * ldk, *Mt = Tt + C * LC, *Ut = Mt + C * LC, *buf = Ut + C * LV; // buf: K, Q, V, tok; twice
-    const int tid = threadIdx.x, ti = row_of(tid), tj = column_of(tid), bh = blockIdx.y, n0 = blockIdx.x * NV;
+    const int tid = threadIdx.x, ti = W::row(tid), tj = W::column(tid), bh = blockIdx.y, n0 = blockIdx.x * NV;
     const int b = bh / a.H, kh = b * a.Hk + (bh % a.H) / (a.H / a.Hk);
     const int nv = min(NV, a.d_v - n0);
     griddep_launch_dependents();
@@ -377,7 +387,7 @@ __global__ void __launch_bounds__(NT)
         copy_tile(p, ldk, k + krow, a.d_k, C, n, a.d_k, lk4);
         if (!KEEP)
             copy_tile(p + C * ldk, ldk, q + krow, a.d_k, C, n, a.d_k, lk4);
-        copy_tile(p + 2 * C * ldk, LV, v + ((size_t)bh * a.L + t0) * a.d_v + n0, a.d_v, C, n, nv, 3);
+        copy_tile(p + 2 * C * ldk, LV, v + ((size_t)bh * a.L + t0) * a.d_v + n0, a.d_v, C, n, nv, W::LOG4);
         copy_tile(p + 2 * C * ldk + C * LV, TOK, ws.tok + ((size_t)bh * nC + c) * C * TOK, TOK, C, C, TOK, 1);
     };
     auto fetch_sq = [&](float *dst, const float *src, int c) {
@@ -403,32 +413,32 @@ __global__ void __launch_bounds__(NT)
             for (int e = tid; e < nv << lk4; e += NT)
                 *reinterpret_cast<float4 *>(ws.S + ch * a.d_v * a.d_k + (size_t)n0 * a.d_k + 4 * e) =
                     lds4(S + (e >> lk4) * ldk + (e & ((1 << lk4) - 1)) * 4);
-        float acc[4][4] = {}; // rows ti, ti + 32 of K, then of Q; channels 4 tj ..
+        float acc[2 * R][4] = {}; // rows of K, then of Q
         if (KEEP) {
-            float pk[2][4] = {};
-            mm_nt<2, 4>(pk, kq + ti * ldk, ldk, 32, S + tj * 4 * ldk, ldk, 1, a.d_k);
+            float pk[R][4] = {};
+            mm_nt<R, 4>(pk, kq + ti * ldk, ldk, W::S, S + tj * 4 * ldk, ldk, 1, a.d_k);
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
                     acc[r][s] = pk[r][s];
         } else {
-            mm_nt<4, 4>(acc, kq + ti * ldk, ldk, 32, S + tj * 4 * ldk, ldk, 1, a.d_k);
+            mm_nt<2 * R, 4>(acc, kq + ti * ldk, ldk, W::S, S + tj * 4 * ldk, ldk, 1, a.d_k);
         }
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const float *d = tok + (ti + 32 * r) * TOK;
-            float *x = Xt + (ti + 32 * r) * LV + tj * 4;
+        for (int r = 0; r < R; ++r) {
+            const float *d = tok + (ti + W::S * r) * TOK;
+            float *x = Xt + (ti + W::S * r) * LV + tj * 4;
 #pragma unroll
             for (int s = 0; s < 4; ++s)
                 x[s] = d[6] * (x[s] - d[2] * d[0] * acc[r][s]);
         }
         __syncthreads();
-        float u[2][4] = {};
-        mm_nn<2>(u, Tt + ti * LC, LC, 32, Xt + tj * 4, LV, C);
+        float u[R][4] = {};
+        mm_nn<R>(u, Tt + ti * LC, LC, W::S, Xt + tj * 4, LV, C);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int i = ti + 32 * r;
+        for (int r = 0; r < R; ++r) {
+            const int i = ti + W::S * r;
             *reinterpret_cast<float4 *>(Ut + i * LV + tj * 4) = make_float4(u[r][0], u[r][1], u[r][2], u[r][3]);
             if (KEEP && tj * 4 < nv)
                 *reinterpret_cast<float4 *>(ws.U + (ch * C + i) * a.d_v + n0 + tj * 4) =
@@ -438,19 +448,19 @@ __global__ void __launch_bounds__(NT)
         if (c + 1 < nch)
             fetch_sq(Tt, ws.T, c + 1);
         if (!KEEP) {
-            float o[2][4];
+            float o[R][4];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float *d = tok + (ti + 32 * r) * TOK;
+            for (int r = 0; r < R; ++r) {
+                const float *d = tok + (ti + W::S * r) * TOK;
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
-                    o[r][s] = a.scale * d[2] * d[1] * acc[2 + r][s];
+                    o[r][s] = a.scale * d[2] * d[1] * acc[R + r][s];
             }
-            mm_nn<2>(o, Mt + ti * LC, LC, 32, Ut + tj * 4, LV, C);
+            mm_nn<R>(o, Mt + ti * LC, LC, W::S, Ut + tj * 4, LV, C);
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-                if (ti + 32 * r < n && tj * 4 < nv)
-                    *reinterpret_cast<float4 *>(y + vrow + (size_t)(ti + 32 * r) * a.d_v + tj * 4) =
+            for (int r = 0; r < R; ++r)
+                if (ti + W::S * r < n && tj * 4 < nv)
+                    *reinterpret_cast<float4 *>(y + vrow + (size_t)(ti + W::S * r) * a.d_v + tj * 4) =
                         make_float4(o[r][0], o[r][1], o[r][2], o[r][3]);
             __syncthreads();
             if (c + 1 < nch)
@@ -459,14 +469,14 @@ __global__ void __launch_bounds__(NT)
         copies_sent();
         // rows of U weighted for the state, where X was
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int i = ti + 32 * r;
+        for (int r = 0; r < R; ++r) {
+            const int i = ti + W::S * r;
             const float f = tok[i * TOK + 3] * tok[i * TOK];
             *reinterpret_cast<float4 *>(Xt + i * LV + tj * 4) =
                 make_float4(f * u[r][0], f * u[r][1], f * u[r][2], f * u[r][3]);
         }
         __syncthreads();
-        update_state(S, ldk, tok[(C - 1) * TOK + 2], Xt, kq, nullptr, nullptr, a.d_k);
+        update_state<NV>(S, ldk, tok[(C - 1) * TOK + 2], Xt, kq, nullptr, nullptr, a.d_k);
     }
     copies_done<0>();
     __syncthreads();
@@ -480,13 +490,16 @@ __global__ void __launch_bounds__(NT)
 }
 
 // ---------------------------------------------------------- reverse walk
+template <int NV>
 __global__ void __launch_bounds__(NT)
     gated_reverse_kernel(GatedArgs a, const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ dy,
                          const float *__restrict__ dWf, float *__restrict__ dW0, Ws ws) {
+    using W = Tile<NV>;
+    constexpr int R = W::R, LV = W::LV;
     extern __shared__ __align__(16) float sm[];
     const int ldk = a.d_k + 4, nC = (a.L + C - 1) / C, lk4 = log2_of(a.d_k / 4), ahead = 2 * C * ldk + C * LV + C * TOK;
     float *D = sm, *Tt = D + NV * ldk, *Mt = Tt + C * LC, *Ut = Mt + C * LC, *buf = Ut + C * LV; // buf: K, Q, dY, tok; twice
-    const int tid = threadIdx.x, ti = row_of(tid), tj = column_of(tid), bh = blockIdx.y, n0 = blockIdx.x * NV;
+    const int tid = threadIdx.x, ti = W::row(tid), tj = W::column(tid), bh = blockIdx.y, n0 = blockIdx.x * NV;
     const int b = bh / a.H, kh = b * a.Hk + (bh % a.H) / (a.H / a.Hk);
     const int nv = min(NV, a.d_v - n0);
     griddep_launch_dependents();
@@ -499,7 +512,7 @@ __global__ void __launch_bounds__(NT)
         const size_t t0 = (size_t)c * C, krow = ((size_t)kh * a.L + t0) * a.d_k;
         copy_tile(p, ldk, k + krow, a.d_k, C, n, a.d_k, lk4);
         copy_tile(p + C * ldk, ldk, q + krow, a.d_k, C, n, a.d_k, lk4);
-        copy_tile(p + 2 * C * ldk, LV, dy + ((size_t)bh * a.L + t0) * a.d_v + n0, a.d_v, C, n, nv, 3);
+        copy_tile(p + 2 * C * ldk, LV, dy + ((size_t)bh * a.L + t0) * a.d_v + n0, a.d_v, C, n, nv, W::LOG4);
         copy_tile(p + 2 * C * ldk + C * LV, TOK, ws.tok + ((size_t)bh * nC + c) * C * TOK, TOK, C, C, TOK, 1);
     };
     auto fetch_sq = [&](float *dst, const float *src, int c) {
@@ -522,32 +535,32 @@ __global__ void __launch_bounds__(NT)
         for (int e = tid; e < nv << lk4; e += NT)
             *reinterpret_cast<float4 *>(ws.dS + ch * a.d_v * a.d_k + (size_t)n0 * a.d_k + 4 * e) =
                 lds4(D + (e >> lk4) * ldk + (e & ((1 << lk4) - 1)) * 4);
-        float u[2][4] = {};
-        mm_nt<2, 4>(u, kq + ti * ldk, ldk, 32, D + tj * 4 * ldk, ldk, 1, a.d_k);
+        float u[R][4] = {};
+        mm_nt<R, 4>(u, kq + ti * ldk, ldk, W::S, D + tj * 4 * ldk, ldk, 1, a.d_k);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const float *d = tok + (ti + 32 * r) * TOK;
+        for (int r = 0; r < R; ++r) {
+            const float *d = tok + (ti + W::S * r) * TOK;
 #pragma unroll
             for (int s = 0; s < 4; ++s)
                 u[r][s] *= d[3] * d[0];
         }
-        mm_tn<2>(u, Mt + ti, LC, 32, Yt + tj * 4, LV, C);
+        mm_tn<R>(u, Mt + ti, LC, W::S, Yt + tj * 4, LV, C);
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-            *reinterpret_cast<float4 *>(Ut + (ti + 32 * r) * LV + tj * 4) =
+        for (int r = 0; r < R; ++r)
+            *reinterpret_cast<float4 *>(Ut + (ti + W::S * r) * LV + tj * 4) =
                 make_float4(u[r][0], u[r][1], u[r][2], u[r][3]);
         __syncthreads();
         if (c > 0)
             fetch_sq(Mt, ws.M, c - 1);
-        float x[2][4] = {};
-        mm_tn<2>(x, Tt + ti, LC, 32, Ut + tj * 4, LV, C);
+        float x[R][4] = {};
+        mm_tn<R>(x, Tt + ti, LC, W::S, Ut + tj * 4, LV, C);
         __syncthreads();
         if (c > 0)
             fetch_sq(Tt, ws.T, c - 1);
         copies_sent();
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int i = ti + 32 * r;
+        for (int r = 0; r < R; ++r) {
+            const int i = ti + W::S * r;
             const float *d = tok + i * TOK;
             if (tj * 4 < nv)
                 *reinterpret_cast<float4 *>(ws.dX + (ch * C + i) * a.d_v + n0 + tj * 4) =
@@ -560,7 +573,7 @@ __global__ void __launch_bounds__(NT)
             }
         }
         __syncthreads();
-        update_state(D, ldk, tok[(C - 1) * TOK + 2], Ut, kq, Yt, kq + C * ldk, a.d_k);
+        update_state<NV>(D, ldk, tok[(C - 1) * TOK + 2], Ut, kq, Yt, kq + C * ldk, a.d_k);
     }
     copies_done<0>();
     __syncthreads();
@@ -786,54 +799,82 @@ __global__ void __launch_bounds__(NT)
 }
 
 size_t prep_smem(int d_k) { return sizeof(float) * (2 * C * (d_k + 4) + 2 * C * LC + 1024 + C * TOK); }
-size_t walk_smem(int d_k) {
-    return sizeof(float) * (NV * (d_k + 4) + 2 * C * LC + C * LV + 2 * (2 * C * (d_k + 4) + C * LV + C * TOK));
+size_t walk_smem(int d_k, int nv) {
+    return sizeof(float) *
+           (nv * (d_k + 4) + 2 * C * LC + C * (nv + 4) + 2 * (2 * C * (d_k + 4) + C * (nv + 4) + C * TOK));
+}
+// Channels per walk CTA (see Tile).
+cudaError_t walk_channels(const GatedArgs &a, int *nv) {
+    int sms = 0;
+    const cudaError_t e = device_sms(&sms);
+    *nv = 2 * (int64_t)a.B * a.H * ((a.d_v + 31) / 32) <= sms ? 16 : 32;
+    return e;
 }
 size_t grad_smem(int d_k) {
     return sizeof(float) * (2 * (C + NV) * (d_k + 4) + 2 * C * d_k + 3 * C * (NV + 4) + 2 * C * LC + C * TOK + C + 16);
 }
 
-cudaError_t forward_f32(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g, const void *beta,
-                      const float *W0, float *Wf, void *y, void *workspace, bool keep, bool backward, cudaStream_t st) {
-    const int BH = a.B * a.H, nC = (a.L + C - 1) / C;
-    const Ws ws = ws_at(workspace, ws_off(BH, a.L, a.d_k, a.d_v, backward));
-    static std::atomic<uint64_t> allowed_prep{0}, allowed_walk[2];
-    cudaError_t e = allow_smem(gated_prep_kernel, allowed_prep);
-    if (e != cudaSuccess)
-        return e;
-    e = launch_pdl(gated_prep_kernel, dim3(nC, BH), dim3(NT), prep_smem(a.d_k), st, a, (const float *)q, (const float *)k,
-                   (const float *)g, (const float *)beta, ws);
-    if (e != cudaSuccess)
-        return e;
-    auto *walk = keep ? gated_walk_kernel<true> : gated_walk_kernel<false>;
-    e = allow_smem(walk, allowed_walk[keep]);
-    if (e != cudaSuccess)
-        return e;
-    return launch_pdl(walk, dim3((a.d_v + NV - 1) / NV, BH), dim3(NT), walk_smem(a.d_k), st, a, (const float *)q,
-                      (const float *)k, (const float *)v, W0, Wf, (float *)y, ws);
+template <typename... KArgs, typename... Args>
+cudaError_t launch_smem(void (*kern)(KArgs...), std::atomic<uint64_t> &allowed, dim3 grid, size_t smem, cudaStream_t st,
+                        Args... args) {
+    const cudaError_t e = allow_smem(kern, allowed);
+    return e != cudaSuccess ? e : launch_pdl(kern, grid, dim3(NT), smem, st, args...);
 }
 
-cudaError_t backward_f32(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g,
-                       const void *beta, const float *W0, const void *dy, const float *dWf, void *dq, void *dk,
-                       void *dv, void *dg, void *dbeta, float *dW0, void *workspace, cudaStream_t st) {
-    const int BH = a.B * a.H, nC = (a.L + C - 1) / C;
-    const Ws ws = ws_at(workspace, ws_off(BH, a.L, a.d_k, a.d_v, true));
-    cudaError_t e = forward_f32(a, q, k, v, g, beta, W0, nullptr, nullptr, workspace, true, true, st);
+template <bool KEEP, int NV>
+cudaError_t launch_walk(const GatedArgs &a, const float *q, const float *k, const float *v, const float *W0, float *Wf,
+                        float *y, const Ws &ws, cudaStream_t st) {
+    static std::atomic<uint64_t> allowed{0};
+    return launch_smem(gated_walk_kernel<KEEP, NV>, allowed, dim3((a.d_v + NV - 1) / NV, a.B * a.H),
+                       walk_smem(a.d_k, NV), st, a, q, k, v, W0, Wf, y, ws);
+}
+template <int NV>
+cudaError_t launch_reverse(const GatedArgs &a, const float *q, const float *k, const float *dy, const float *dWf,
+                           float *dW0, const Ws &ws, cudaStream_t st) {
+    static std::atomic<uint64_t> allowed{0};
+    return launch_smem(gated_reverse_kernel<NV>, allowed, dim3((a.d_v + NV - 1) / NV, a.B * a.H), walk_smem(a.d_k, NV),
+                       st, a, q, k, dy, dWf, dW0, ws);
+}
+
+cudaError_t prepare_f32(const GatedArgs &a, const float *q, const float *k, const float *g, const float *beta,
+                        const Ws &ws, cudaStream_t st) {
+    static std::atomic<uint64_t> allowed{0};
+    return launch_smem(gated_prep_kernel, allowed, dim3((a.L + C - 1) / C, a.B * a.H), prep_smem(a.d_k), st, a, q, k, g,
+                       beta, ws);
+}
+
+cudaError_t forward_f32(const GatedArgs &a, const float *q, const float *k, const float *v, const float *g,
+                        const float *beta, const float *W0, float *Wf, float *y, void *workspace, cudaStream_t st) {
+    const Ws ws = ws_at(workspace, ws_off(a.B * a.H, a.L, a.d_k, a.d_v, false));
+    int nv = 0;
+    cudaError_t e = walk_channels(a, &nv);
+    if (e == cudaSuccess)
+        e = prepare_f32(a, q, k, g, beta, ws, st);
     if (e != cudaSuccess)
         return e;
-    static std::atomic<uint64_t> allowed_reverse{0}, allowed_grad{0};
-    e = allow_smem(gated_reverse_kernel, allowed_reverse);
+    return nv == 16 ? launch_walk<false, 16>(a, q, k, v, W0, Wf, y, ws, st)
+                    : launch_walk<false, 32>(a, q, k, v, W0, Wf, y, ws, st);
+}
+
+cudaError_t backward_f32(const GatedArgs &a, const float *q, const float *k, const float *v, const float *g,
+                         const float *beta, const float *W0, const float *dy, const float *dWf, float *dq, float *dk,
+                         float *dv, float *dg, float *dbeta, float *dW0, void *workspace, cudaStream_t st) {
+    const Ws ws = ws_at(workspace, ws_off(a.B * a.H, a.L, a.d_k, a.d_v, true));
+    int nv = 0;
+    cudaError_t e = walk_channels(a, &nv);
+    if (e == cudaSuccess)
+        e = prepare_f32(a, q, k, g, beta, ws, st);
+    if (e == cudaSuccess)
+        e = nv == 16 ? launch_walk<true, 16>(a, q, k, v, W0, nullptr, nullptr, ws, st)
+                     : launch_walk<true, 32>(a, q, k, v, W0, nullptr, nullptr, ws, st);
+    if (e == cudaSuccess)
+        e = nv == 16 ? launch_reverse<16>(a, q, k, dy, dWf, dW0, ws, st)
+                     : launch_reverse<32>(a, q, k, dy, dWf, dW0, ws, st);
     if (e != cudaSuccess)
         return e;
-    e = launch_pdl(gated_reverse_kernel, dim3((a.d_v + NV - 1) / NV, BH), dim3(NT), walk_smem(a.d_k), st, a,
-                   (const float *)q, (const float *)k, (const float *)dy, dWf, dW0, ws);
-    if (e != cudaSuccess)
-        return e;
-    e = allow_smem(gated_grad_kernel, allowed_grad);
-    if (e != cudaSuccess)
-        return e;
-    return launch_pdl(gated_grad_kernel, dim3(nC, a.B * a.Hk), dim3(NT), grad_smem(a.d_k), st, a, (const float *)q,
-                      (const float *)k, (const float *)v, (const float *)dy, (float *)dq, (float *)dk, (float *)dv, (float *)dg, (float *)dbeta, ws);
+    static std::atomic<uint64_t> allowed{0};
+    return launch_smem(gated_grad_kernel, allowed, dim3((a.L + C - 1) / C, a.B * a.Hk), grad_smem(a.d_k), st, a, q, k, v,
+                       dy, dq, dk, dv, dg, dbeta, ws);
 }
 
 } // namespace
@@ -856,18 +897,24 @@ size_t gated_backward_workspace_bytes(int B, int H, int L, int d_k, int d_v, int
 cudaError_t launch_gated_forward(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g,
                                  const void *beta, const float *W0, float *Wf, void *y, void *workspace, int bf16,
                                  cudaStream_t st) {
-    return bf16 ? gated_tc_forward(a, q, k, v, g, beta, W0, Wf, y, workspace, st)
-                : forward_f32(a, q, k, v, g, beta, W0, Wf, y, workspace, false, false, st);
+    if (bf16)
+        return gated_tc_forward(a, q, k, v, g, beta, W0, Wf, y, workspace, st);
+    auto f = [](const void *p) { return static_cast<const float *>(p); };
+    return forward_f32(a, f(q), f(k), f(v), f(g), f(beta), W0, Wf, static_cast<float *>(y), workspace, st);
 }
 
 cudaError_t launch_gated_backward(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g,
                                   const void *beta, const float *W0, const void *dy, const float *dWf, void *dq,
                                   void *dk, void *dv, void *dg, void *dbeta, float *dW0, void *workspace, int bf16,
                                   cudaStream_t st) {
-    if (!bf16)
-        return backward_f32(a, q, k, v, g, beta, W0, dy, dWf, dq, dk, dv, dg, dbeta, dW0, workspace, st);
-    const cudaError_t e = gated_tc_walks(a, q, k, v, g, beta, W0, dy, dWf, dW0, workspace, st);
-    return e != cudaSuccess ? e : gated_tc_grad(a, q, k, v, dy, dq, dk, dv, dg, dbeta, workspace, st);
+    if (bf16) {
+        const cudaError_t e = gated_tc_walks(a, q, k, v, g, beta, W0, dy, dWf, dW0, workspace, st);
+        return e != cudaSuccess ? e : gated_tc_grad(a, q, k, v, dy, dq, dk, dv, dg, dbeta, workspace, st);
+    }
+    auto f = [](const void *p) { return static_cast<const float *>(p); };
+    auto o = [](void *p) { return static_cast<float *>(p); };
+    return backward_f32(a, f(q), f(k), f(v), f(g), f(beta), W0, f(dy), dWf, o(dq), o(dk), o(dv), o(dg), o(dbeta), dW0,
+                        workspace, st);
 }
 
 } // namespace fw

@@ -18,9 +18,9 @@
 // differences) and shuffles among the row's lanes.  A CTA stays on one head,
 // so gamma and beta sit in registers and so do the backward's dgamma and
 // dbeta until the end: one partial row per CTA, added by a second kernel in a
-// fixed order (no atomics).  Two rows of a lane group are in flight at a time,
-// and the activations use the fast exponential and division (2^-21 of the
-// value), or the arithmetic would cost as much as the bytes.
+// fixed order (no atomics).  The next rows are requested before the current ones
+// are worked on, and the arithmetic is on pairs of floats with single-instruction
+// exponentials and reciprocals, or it would cost as much as the bytes.
 #include "fw_common.cuh"
 #include "fw_gated.h"
 
@@ -33,37 +33,93 @@ namespace {
 constexpr int kT = 256;
 enum { kNone = 0, kRelu = 1, kSilu = 2, kGelu = 3 };
 
-// x sigmoid(x) needs no guard: far below 0 the exponential is infinite and the
-// quotient 0.
-FW_DEV float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// Two floats that one instruction adds or multiplies (each rounded as the
+// single instruction rounds it): the kernels are near the instruction rate.
+struct F2 {
+    unsigned long long v;
+};
+FW_DEV F2 pack(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+FW_DEV float2 unpack(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+FW_DEV F2 both(float x) { return pack(x, x); }
+FW_DEV F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+FW_DEV F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+FW_DEV F2 operator+(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+FW_DEV float sum(F2 a) {
+    const float2 t = unpack(a);
+    return t.x + t.y;
+}
 
 // (A variant of the kernels for each: as a branch per element it made them
 // bound by instructions, 36 an element and 49 us where the bytes take 30.)
-template <int ACT> FW_DEV float act(float x) {
+// The exponential and the reciprocal as single instructions (2^-22 of the
+// value; denormal results are 0).  x sigmoid(x) needs no guard: far below 0 the
+// exponential is infinite and the reciprocal 0.
+FW_DEV float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+FW_DEV float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+FW_DEV F2 sigmoid(F2 x) {
+    const float2 t = unpack(x * both(-kLog2e));
+    const float2 e = unpack(pack(ex2(t.x), ex2(t.y)) + both(1.f));
+    return pack(rcp(e.x), rcp(e.y));
+}
+FW_DEV float relu(float x) { return x > 0.f ? x : x != x ? x : 0.f; } // NaN stays NaN
+FW_DEV float phi(float x) { return 0.5f * (1.f + erff(x * 0.70710678118654752f)); }
+template <int ACT> FW_DEV F2 act(F2 x) {
+    const float2 t = unpack(x);
     if (ACT == kRelu)
-        return x > 0.f ? x : x != x ? x : 0.f; // NaN stays NaN
+        return pack(relu(t.x), relu(t.y));
     if (ACT == kSilu)
         return x * sigmoid(x);
     if (ACT == kGelu)
-        return 0.5f * x * (1.f + erff(x * 0.70710678118654752f));
+        return x * pack(phi(t.x), phi(t.y));
     return x;
 }
 // act(x) and its derivative.
-template <int ACT> FW_DEV void act_grad(float x, float &f, float &df) {
+template <int ACT> FW_DEV void act_grad(F2 x, F2 &f, F2 &df) {
+    const float2 t = unpack(x);
     if (ACT == kRelu) {
-        f = act<kRelu>(x);
-        df = x > 0.f ? 1.f : 0.f;
+        f = pack(relu(t.x), relu(t.y));
+        df = pack(t.x > 0.f ? 1.f : 0.f, t.y > 0.f ? 1.f : 0.f);
     } else if (ACT == kSilu) {
-        const float s = sigmoid(x);
+        const F2 s = sigmoid(x);
         f = x * s;
-        df = s * fmaf(x, 1.f - s, 1.f);
+        df = fma2(f, fma2(s, both(-1.f), both(1.f)), s); // s (1 + x (1 - s))
     } else if (ACT == kGelu) {
-        const float p = 0.5f * (1.f + erff(x * 0.70710678118654752f));
+        const F2 p = pack(phi(t.x), phi(t.y));
+        const float2 q = unpack(x * x * both(-0.5f * kLog2e));
         f = x * p;
-        df = fmaf(x * 0.39894228040143268f, __expf(-0.5f * x * x), p);
+        df = fma2(x * both(0.39894228040143268f), pack(ex2(q.x), ex2(q.y)), p);
     } else {
         f = x;
-        df = 1.f;
+        df = both(1.f);
     }
 }
 
@@ -74,25 +130,15 @@ template <int LPR> FW_DEV float row_sum(float x) {
     return x;
 }
 
-// n = (x - mean) r of a row held 8 channels a lane (lanes at or past d hold
-// zeros and stay zero); returns r.
-template <int LPR> FW_DEV float normalise(float (&x)[8], bool on, float inv_d, float eps) {
-    float s = 0.f;
+// x - mean of a row held 8 channels a lane (lanes at or past d hold zeros and
+// stay zero); returns r.
+template <int LPR> FW_DEV float centre(F2 (&x)[4], bool on, float inv_d, float eps) {
+    const F2 mean = both(-inv_d * row_sum<LPR>(sum((x[0] + x[1]) + (x[2] + x[3]))));
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        s += x[e];
-    const float mean = row_sum<LPR>(s) * inv_d;
-    float ss = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        x[e] = on ? x[e] - mean : 0.f;
-        ss = fmaf(x[e], x[e], ss);
-    }
-    const float r = 1.f / sqrtf(fmaf(row_sum<LPR>(ss), inv_d, eps));
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        x[e] *= r;
-    return r;
+    for (int e = 0; e < 4; ++e)
+        x[e] = on ? x[e] + mean : F2{0};
+    const float ss = sum(fma2(x[0], x[0], x[1] * x[1]) + fma2(x[2], x[2], x[3] * x[3]));
+    return rsqrtf(fmaf(row_sum<LPR>(ss), inv_d, eps));
 }
 
 // 8 channels as they were loaded.
@@ -102,13 +148,11 @@ template <> struct Raw8<__nv_bfloat16> {
     FW_DEV void load(const __nv_bfloat16 *p, bool here) {
         u = here ? __ldcs(reinterpret_cast<const uint4 *>(p)) : make_uint4(0, 0, 0, 0);
     }
-    FW_DEV void widen(float (&o)[8]) const {
+    FW_DEV void widen(F2 (&o)[4]) const {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            o[2 * i] = __uint_as_float(w[i] << 16);
-            o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+        for (int i = 0; i < 4; ++i)
+            o[i] = pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     }
 };
 template <> struct Raw8<float> {
@@ -117,74 +161,122 @@ template <> struct Raw8<float> {
         a = here ? __ldcs(reinterpret_cast<const float4 *>(p)) : make_float4(0.f, 0.f, 0.f, 0.f);
         b = here ? __ldcs(reinterpret_cast<const float4 *>(p) + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    FW_DEV void widen(float (&o)[8]) const {
-        o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
-        o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+    FW_DEV void widen(F2 (&o)[4]) const {
+        o[0] = pack(a.x, a.y);
+        o[1] = pack(a.z, a.w);
+        o[2] = pack(b.x, b.y);
+        o[3] = pack(b.z, b.w);
     }
 };
 
-constexpr int U = 2; // rows in flight per lane group
-
-// Where row `row` of (b, l) starts: in x (head-major) and in out (token-major).
-struct Rows {
-    int64_t x, out;
-};
-FW_DEV Rows rows_of(const NormArgs &a, unsigned row, int h, int c0) {
-    const unsigned b = row / (unsigned)a.L, l = row - b * (unsigned)a.L;
-    return {(((int64_t)b * a.H + h) * a.L + l) * a.d + c0, ((int64_t)row * a.H + h) * a.d + c0};
+template <typename T> FW_DEV void store4(T *p, const F2 (&v)[4]) {
+    float o[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 t = unpack(v[e]);
+        o[2 * e] = t.x;
+        o[2 * e + 1] = t.y;
+    }
+    store8(p, o);
+}
+FW_DEV void load_pairs(const float *p, F2 (&o)[4]) {
+    float t[8];
+    load8(p, t);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        o[e] = pack(t[2 * e], t[2 * e + 1]);
 }
 
+// A lane group's walk over the rows (b, l) of a head, `step` rows at a time:
+// where the row lies in x (head-major) and in out (token-major), by additions.
+struct Walk {
+    unsigned row, rows, step, l, L, step_l;
+    int64_t x, out, dx, dx_wrap, dout;
+    FW_DEV Walk(const NormArgs &a, unsigned first, unsigned step_, int h, int c0) {
+        row = first;
+        rows = (unsigned)(a.B * (int64_t)a.L);
+        step = step_;
+        L = (unsigned)a.L;
+        const unsigned b = row / L, step_b = step / L;
+        l = row - b * L;
+        step_l = step - step_b * L;
+        x = (((int64_t)b * a.H + h) * a.L + l) * a.d + c0;
+        out = ((int64_t)row * a.H + h) * a.d + c0;
+        dx = ((int64_t)step_b * a.H * a.L + step_l) * a.d;
+        dx_wrap = (int64_t)(a.H - 1) * a.L * a.d; // past the end of one sequence: the next one's same head
+        dout = (int64_t)step * a.H * a.d;
+    }
+    FW_DEV bool here() const { return row < rows; }
+    FW_DEV void next() {
+        row += step;
+        l += step_l;
+        x += dx;
+        out += dout;
+        if (l >= L) {
+            l -= L;
+            x += dx_wrap;
+        }
+    }
+};
+
 template <int LPR, int ACT, bool GATE, typename T>
-__global__ void __launch_bounds__(kT)
+__global__ void __launch_bounds__(kT, 3)
     group_norm_kernel(NormArgs a, const T *__restrict__ x, const T *__restrict__ gate, const float *__restrict__ gamma,
                       const float *__restrict__ beta, T *__restrict__ out) {
     constexpr unsigned RPC = kT / LPR; // rows per CTA and step
     const int c0 = 8 * (threadIdx.x % LPR), h = blockIdx.y;
-    const unsigned slot = threadIdx.x / LPR, rows = (unsigned)(a.B * (int64_t)a.L), step = gridDim.x * RPC;
     const bool on = c0 < a.d;
     const float inv_d = 1.f / (float)a.d;
     griddep_launch_dependents();
     griddep_wait();
     x = after_wait(x);
     gate = after_wait(gate);
-    float ga[8] = {}, be[8] = {};
+    F2 ga[4] = {}, be[4] = {};
     if (on) {
-        load8(gamma + h * a.d + c0, ga);
-        load8(beta + h * a.d + c0, be);
+        load_pairs(gamma + h * a.d + c0, ga);
+        load_pairs(beta + h * a.d + c0, be);
     }
-    for (unsigned base = blockIdx.x * RPC; base < rows; base += U * step) {
-        Raw8<T> rx[U], rg[U];
-        Rows at[U];
-        bool here[U];
+    Walk at(a, blockIdx.x * RPC + threadIdx.x / LPR, gridDim.x * RPC, h, c0);
+    constexpr int D = sizeof(T) == 2 ? 2 : 1; // rows requested ahead (64 to 96 bytes a lane)
+    Raw8<T> rx[D], rg[D];
+    int64_t to[D];
+    bool here[D];
+    auto request = [&](int u) {
+        here[u] = on && at.here();
+        to[u] = at.out;
+        rx[u].load(x + at.x, here[u]);
+        if (GATE)
+            rg[u].load(gate + at.out, here[u]);
+        at.next();
+    };
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const unsigned row = base + u * step + slot;
-            here[u] = on && row < rows;
-            at[u] = rows_of(a, here[u] ? row : 0, h, here[u] ? c0 : 0);
-            rx[u].load(x + at[u].x, here[u]);
-            if (GATE)
-                rg[u].load(gate + at[u].out, here[u]);
-        }
+    for (int u = 0; u < D; ++u)
+        request(u);
+    // (the loop's trip count is the CTA's, so that the shuffles meet)
+    for (unsigned base = blockIdx.x * RPC; base < at.rows; base += D * at.step) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float v[8], z[8];
+        for (int u = 0; u < D; ++u) {
+            F2 v[4], z[4];
             rx[u].widen(v);
-            normalise<LPR>(v, here[u], inv_d, a.eps);
             if (GATE)
                 rg[u].widen(z);
+            const bool mine = here[u];
+            const int64_t o = to[u];
+            request(u);
+            const F2 r = both(centre<LPR>(v, mine, inv_d, a.eps));
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float y = fmaf(v[e], ga[e], be[e]);
+            for (int e = 0; e < 4; ++e) {
+                const F2 y = fma2(v[e] * r, ga[e], be[e]);
                 v[e] = GATE ? y * act<ACT>(z[e]) : act<ACT>(y);
             }
-            if (here[u])
-                store8(out + at[u].out, v);
+            if (mine)
+                store4(out + o, v);
         }
     }
 }
 
 template <int LPR, int ACT, bool GATE, typename T>
-__global__ void __launch_bounds__(kT)
+__global__ void __launch_bounds__(kT, 2)
     group_norm_backward_kernel(NormArgs a, const T *__restrict__ x, const T *__restrict__ gate,
                                const float *__restrict__ gamma, const float *__restrict__ beta,
                                const T *__restrict__ dout, T *__restrict__ dx, T *__restrict__ dgate,
@@ -192,7 +284,7 @@ __global__ void __launch_bounds__(kT)
     constexpr unsigned RPC = kT / LPR;
     __shared__ float red[2][RPC][8 * LPR];
     const int c0 = 8 * (threadIdx.x % LPR), h = blockIdx.y;
-    const unsigned slot = threadIdx.x / LPR, rows = (unsigned)(a.B * (int64_t)a.L), step = gridDim.x * RPC;
+    const unsigned slot = threadIdx.x / LPR;
     const bool on = c0 < a.d;
     const float inv_d = 1.f / (float)a.d;
     griddep_launch_dependents();
@@ -200,67 +292,75 @@ __global__ void __launch_bounds__(kT)
     x = after_wait(x);
     gate = after_wait(gate);
     dout = after_wait(dout);
-    float ga[8] = {}, be[8] = {}, dga[8] = {}, dbe[8] = {};
+    F2 ga[4] = {}, be[4] = {}, dga[4] = {}, dbe[4] = {};
     if (on) {
-        load8(gamma + h * a.d + c0, ga);
-        load8(beta + h * a.d + c0, be);
+        load_pairs(gamma + h * a.d + c0, ga);
+        load_pairs(beta + h * a.d + c0, be);
     }
-    for (unsigned base = blockIdx.x * RPC; base < rows; base += U * step) {
-        Raw8<T> rx[U], rg[U], rd[U];
-        Rows at[U];
-        bool here[U];
+    Walk at(a, blockIdx.x * RPC + slot, gridDim.x * RPC, h, c0);
+    constexpr int D = sizeof(T) == 2 ? 2 : 1; // rows requested ahead (64 to 96 bytes a lane)
+    Raw8<T> rx[D], rg[D], rd[D];
+    int64_t to[D], from[D];
+    bool here[D];
+    auto request = [&](int u) {
+        here[u] = on && at.here();
+        to[u] = at.out;
+        from[u] = at.x;
+        rx[u].load(x + at.x, here[u]);
+        rd[u].load(dout + at.out, here[u]);
+        if (GATE)
+            rg[u].load(gate + at.out, here[u]);
+        at.next();
+    };
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const unsigned row = base + u * step + slot;
-            here[u] = on && row < rows;
-            at[u] = rows_of(a, here[u] ? row : 0, h, here[u] ? c0 : 0);
-            rx[u].load(x + at[u].x, here[u]);
-            rd[u].load(dout + at[u].out, here[u]);
-            if (GATE)
-                rg[u].load(gate + at[u].out, here[u]);
-        }
+    for (int u = 0; u < D; ++u)
+        request(u);
+    for (unsigned base = blockIdx.x * RPC; base < at.rows; base += D * at.step) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float n[8], t[8], dz[8];
+        for (int u = 0; u < D; ++u) {
+            F2 n[4], t[4], dz[4];
             rx[u].widen(n);
             rd[u].widen(dz);
-            const float r = normalise<LPR>(n, here[u], inv_d, a.eps);
             if (GATE)
                 rg[u].widen(t);
-            float s1 = 0.f, s2 = 0.f;
+            const bool mine = here[u];
+            const int64_t o = to[u], i = from[u];
+            request(u);
+            const float r = centre<LPR>(n, mine, inv_d, a.eps);
+            F2 s1 = {0}, s2 = {0};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float z = fmaf(n[e], ga[e], be[e]);
-                float f, df;
+            for (int e = 0; e < 4; ++e) {
+                n[e] = n[e] * both(r);
+                const F2 z = fma2(n[e], ga[e], be[e]);
+                F2 f, df;
                 act_grad<ACT>(GATE ? t[e] : z, f, df);
                 if (GATE) {
                     t[e] = dz[e] * z * df;
-                    dz[e] *= f;
+                    dz[e] = dz[e] * f;
                 } else {
-                    dz[e] *= df;
+                    dz[e] = dz[e] * df;
                 }
-                dga[e] = fmaf(dz[e], n[e], dga[e]);
-                dbe[e] += dz[e];
-                dz[e] *= ga[e];
-                s1 += dz[e];
-                s2 = fmaf(dz[e], n[e], s2);
+                dga[e] = fma2(dz[e], n[e], dga[e]);
+                dbe[e] = dbe[e] + dz[e];
+                dz[e] = dz[e] * ga[e];
+                s1 = s1 + dz[e];
+                s2 = fma2(dz[e], n[e], s2);
             }
-            s1 = row_sum<LPR>(s1) * inv_d;
-            s2 = row_sum<LPR>(s2) * inv_d;
-            if (here[u]) {
+            const F2 m1 = both(-inv_d * row_sum<LPR>(sum(s1))), m2 = both(-inv_d * row_sum<LPR>(sum(s2)));
+            if (mine) {
                 if (GATE)
-                    store8(dgate + at[u].out, t);
+                    store4(dgate + o, t);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    dz[e] = r * (dz[e] - s1 - n[e] * s2);
-                store8(dx + at[u].x, dz);
+                for (int e = 0; e < 4; ++e)
+                    dz[e] = both(r) * fma2(n[e], m2, dz[e] + m1);
+                store4(dx + i, dz);
             }
         }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        red[0][slot][c0 + e] = dga[e];
-        red[1][slot][c0 + e] = dbe[e];
+    for (int e = 0; e < 4; ++e) {
+        *reinterpret_cast<float2 *>(&red[0][slot][c0 + 2 * e]) = unpack(dga[e]);
+        *reinterpret_cast<float2 *>(&red[1][slot][c0 + 2 * e]) = unpack(dbe[e]);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < 2 * a.d; e += kT) {
@@ -296,9 +396,11 @@ __global__ void __launch_bounds__(kT)
     }
 }
 
-// CTAs per head: enough to fill the SMs (kCtas in all), no more than the rows
-// give.
-constexpr int kCtas = 152 * 8, kBackwardCtas = 152 * 4;
+// CTAs per head: what the SMs hold at once (three an SM, two in the backward:
+// registers), no more than the rows give.  (B16 H8 L2048 d 128: 31.4 us in one
+// wave, 33 in two, 37 with four CTAs an SM, whose 64 registers
+// spill; the gradients 62 us in one wave, 66 in two, 105 with three CTAs an SM.)
+constexpr int kCtas = 152 * 3, kBackwardCtas = 152 * 2;
 int parts_of(int B, int H, int L, int d, int ctas) {
     int lpr = 1;
     while (8 * lpr < d)
