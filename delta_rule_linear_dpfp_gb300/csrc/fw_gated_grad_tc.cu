@@ -35,8 +35,9 @@ using namespace tc;
 using bf = __nv_bfloat16;
 
 constexpr int C = kGatedChunk;
-constexpr int PARTS = 4;         // the warps that share 32 rows split their columns
-constexpr int NT = 128 * PARTS;
+// The warps that share 32 rows split their columns: 16 warps, or 8 for d_k <= 64,
+// where two CTAs share an SM's registers.
+__host__ __device__ constexpr int parts_of(int nkb) { return 2 * nkb; }
 
 FW_DEV void split8(const float *x, uint4 &hi, uint4 &lo) {
     uint32_t h[4], l[4];
@@ -70,11 +71,14 @@ FW_DEV void pair8(const uint8_t *tile, int row, int c, float (&o)[8]) {
 
 // Shared memory: [K; Q]; two slices (S, dS', [dY; dX], U), whose place the E
 // and F tiles (64 KB) and the staged reader rows take afterwards; the sums of
-// dq and dk over the value heads; scalars.
+// dq and dk over the value heads -- in the place of the E and F tiles, too,
+// where a key head has one value head, so that for d_k <= 64 two CTAs fit an
+// SM (B4 H8 L512, 256 CTAs: the whole backward 57 us with one an SM, 52 with
+// two); scalars.
 struct GradSmem {
     uint32_t slice, s, ds, yx, u, ef, stage, accq, acck, tok, red, bar, bytes;
 };
-__host__ __device__ inline GradSmem grad_smem(int nkb) {
+__host__ __device__ inline GradSmem grad_smem(int nkb, bool alone) {
     GradSmem o;
     o.ef = (uint32_t)nkb * 16384;
     o.s = 0;
@@ -83,26 +87,30 @@ __host__ __device__ inline GradSmem grad_smem(int nkb) {
     o.u = o.yx + 16384;
     o.slice = o.u + 8192;
     o.stage = o.ef + 65536;
-    const uint32_t a = o.ef + 2 * o.slice, b = o.stage + (uint32_t)nkb * 16384;
-    o.accq = a > b ? a : b;
+    const uint32_t a = o.ef + 2 * o.slice, b = o.stage + (uint32_t)nkb * 16384, end = a > b ? a : b;
+    o.accq = alone ? o.ef : end;
     o.acck = o.accq + (uint32_t)nkb * 16384;
-    o.tok = o.acck + (uint32_t)nkb * 16384;
+    // (an MMA of 128 rows reads 8 KB past a slice's U, one of 64 columns 16 KB
+    // past the last F tile: into what follows, or into this slack)
+    o.tok = alone ? end + 8192 : o.acck + (uint32_t)nkb * 16384;
     o.red = o.tok + C * 32;
-    o.bar = o.red + 4 * ((3 * PARTS + 1) * C + 32);
+    o.bar = o.red + 4 * ((3 * parts_of(nkb) + 1) * C + 32);
     o.bytes = o.bar + 64 + 1024;
     return o;
 }
 
 template <int NKB>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
     gated_tc_grad_kernel(GatedArgs a, const bf *__restrict__ q, const bf *__restrict__ k, const bf *__restrict__ v,
                          const bf *__restrict__ dy, bf *__restrict__ dq, bf *__restrict__ dk, bf *__restrict__ dv,
                          bf *__restrict__ dg, bf *__restrict__ dbeta, const uint8_t *ws, GatedRecord rec,
                          unsigned *status) {
+    constexpr int PARTS = parts_of(NKB), NT = 128 * PARTS;
     constexpr int DKP = 64 * NKB, HC = DKP / PARTS; // channels per thread of a row
+    constexpr uint32_t kCols = 256 * NKB;               // TMEM: three products of DKP columns, one of 64
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const GradSmem o = grad_smem(NKB);
+    const GradSmem o = grad_smem(NKB, a.H == a.Hk);
     uint8_t *kq = sm, *ef = sm + o.ef;
     float *tok = reinterpret_cast<float *>(sm + o.tok); // per token: G hi, G lo, rk, beta, rq, e^G, e^{G_C-G}, -
     float *red = reinterpret_cast<float *>(sm + o.red);
@@ -136,7 +144,7 @@ __global__ void __launch_bounds__(NT)
         return;
     }
     if (w == 0) {
-        tmem_alloc(slot, 512);
+        tmem_alloc(slot, kCols);
         tmem_relinquish();
     }
     if (tid == 32) {
@@ -148,7 +156,7 @@ __global__ void __launch_bounds__(NT)
     __syncthreads();
     tc_fence_after();
     griddep_launch_dependents();
-    const uint32_t tm = *slot, tA = tm, tB = tm + 128, tW = tm + 192, tE = tm + 320;
+    const uint32_t tm = *slot, tA = tm, tB = tm + DKP, tW = tB + 64, tE = tW + DKP;
     const uint32_t lb = tmem_lane_base(w);
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -191,8 +199,8 @@ __global__ void __launch_bounds__(NT)
             reinterpret_cast<float4 *>(tok)[tid] =
                 __ldcg(reinterpret_cast<const float4 *>(record(m) + rec.tok) + tid);
         float xv = 0.f, ss = 0.f;
-        // the first 256 threads: a row and 8 of 32 channels of dY, dX, V; the others: <S, dS'>
-        const bool rowed = tid < 256;
+        // 256 threads: a row and 8 of 32 channels of dY, dX, V; the others, if any: <S, dS'>
+        const bool rowed = tid < 256, squared = NT == 256 || !rowed;
         const int yr = (tid >> 2) & 63, yc = tid & 3;
         for (int s = 0; s < ns; ++s, ++gs) {
             uint8_t *sl = ef + (gs & 1) * o.slice;
@@ -224,10 +232,11 @@ __global__ void __launch_bounds__(NT)
                 }
                 if (in)
                     store8(dv + at, x);
-            } else {
+            }
+            if (squared) {
 #pragma unroll
                 for (int e = 0; e < DKP * 4 / 256; ++e) {
-                    const int p = tid - 256 + e * 256;
+                    const int p = (tid & 255) + e * 256;
                     float x[8], y[8];
                     pair8(sl + o.s, p >> 2, p & 3, x);
                     pair8(sl + o.ds, p >> 2, p & 3, y);
@@ -278,8 +287,9 @@ __global__ void __launch_bounds__(NT)
         // E and F, as [E; F] rk_j (K-major) and as [F (-beta rk_i); E rq_i]
         {
             const float fr = rr < C ? dj_.x : -di.w * di.z;
-            {
-                const int j0 = 16 * part;
+#pragma unroll
+            for (int p = 0; p < 64 / PARTS; p += 16) {
+                const int j0 = 64 / PARTS * part + p;
                 float x[16], y[16];
                 tmem_ld16(tB + lb + (uint32_t)j0, x);
                 tmem_ld_wait();
@@ -492,7 +502,11 @@ __global__ void __launch_bounds__(NT)
         }
         red[part * 2 * C + rr] = dot * r;
         __syncthreads();
-        const float f = a.l2norm ? (red[rr] + red[2 * C + rr] + red[4 * C + rr] + red[6 * C + rr]) * r : 0.f;
+        float f = 0.f;
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p)
+            f += red[p * 2 * C + rr];
+        f = a.l2norm ? f * r : 0.f;
         if (i < rows) {
             bf *to = (rr < C ? dk : dq) + krow + (size_t)i * a.d_k;
 #pragma unroll
@@ -515,7 +529,7 @@ __global__ void __launch_bounds__(NT)
     tc_fence_before();
     __syncthreads();
     if (w == 0)
-        tmem_dealloc(tm, 512);
+        tmem_dealloc(tm, kCols);
 }
 
 template <int NKB>
@@ -523,12 +537,12 @@ cudaError_t launch(const GatedArgs &a, const void *q, const void *k, const void 
                    void *dv, void *dg, void *dbeta, const void *ws, const GatedRecord &rec, unsigned *status,
                    cudaStream_t st) {
     auto *kern = gated_tc_grad_kernel<NKB>;
-    const uint32_t smem = grad_smem(NKB).bytes;
+    const uint32_t smem = grad_smem(NKB, a.H == a.Hk).bytes;
     static std::atomic<uint64_t> allowed{0};
     const cudaError_t e = allow_smem(kern, allowed);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(kern, dim3(rec.nch, a.B * a.Hk), dim3(NT), smem, st, a, (const bf *)q, (const bf *)k,
+    return launch_pdl(kern, dim3(rec.nch, a.B * a.Hk), dim3(128 * parts_of(NKB)), smem, st, a, (const bf *)q, (const bf *)k,
                       (const bf *)v, (const bf *)dy, (bf *)dq, (bf *)dk, (bf *)dv, (bf *)dg, (bf *)dbeta,
                       (const uint8_t *)ws, rec, status);
 }
