@@ -8,6 +8,7 @@ kernels.  There is no fallback: if the library is missing the import of a
 function raises, and a non-zero status raises FwError.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -520,6 +521,12 @@ def _data(t):
     return None if t is None else t.data_ptr()
 
 
+@functools.lru_cache(maxsize=4096)
+def _size(query, *shape):
+    """A workspace size, which depends on the shape alone."""
+    return getattr(load(), query)(*shape)
+
+
 def _scratch(need, workspace, like):
     """The caller's workspace, or a new one of `need` bytes, and its bytes."""
     if workspace is None:
@@ -578,7 +585,7 @@ def fw_gated_delta_forward(q, k, v, g, beta, W0=None, lengths=None, l2norm: bool
         raise ValueError("y must have v's shape and dtype")
     if W_final is None and return_state:
         W_final = torch.empty(B, H, d_v, d_k, dtype=torch.float32, device=q.device)
-    workspace, ws_bytes = _scratch(lib.fw_gated_delta_forward_workspace_size(*shape), workspace, q)
+    workspace, ws_bytes = _scratch(_size("fw_gated_delta_forward_workspace_size", *shape), workspace, q)
     rc = lib.fw_gated_delta_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _data(W0),
                                     _data(W_final), y.data_ptr(), _data(lengths), workspace.data_ptr(), ws_bytes, B, Hk,
                                     H, L, d_k, d_v, 1 if l2norm else 0, scale, eps, code, st)
@@ -606,7 +613,7 @@ def fw_gated_delta_backward(q, k, v, g, beta, dy, W0=None, dW_final=None, length
     B, Hk, H, L, d_k, d_v, code = shape
     dq, dk, dv, dg, dbeta = (torch.empty_like(t) for t in (q, k, v, g, beta))
     dW0 = torch.empty(B, H, d_v, d_k, dtype=torch.float32, device=q.device) if return_dW0 else None
-    workspace, ws_bytes = _scratch(lib.fw_gated_delta_backward_workspace_size(*shape), workspace, q)
+    workspace, ws_bytes = _scratch(_size("fw_gated_delta_backward_workspace_size", *shape), workspace, q)
     rc = lib.fw_gated_delta_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _data(W0),
                                      dy.data_ptr(), _data(dW_final), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
                                      dg.data_ptr(), dbeta.data_ptr(), _data(dW0), _data(lengths), workspace.data_ptr(),
@@ -698,7 +705,7 @@ def fw_group_norm_act_backward(x, gamma, beta, dout, gate=None, act: str = "none
     dx = torch.empty_like(x)
     dgate = None if gate is None else torch.empty_like(gate)
     dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(beta)
-    workspace, ws_bytes = _scratch(lib.fw_group_norm_act_backward_workspace_size(B, H, L, d), workspace, x)
+    workspace, ws_bytes = _scratch(_size("fw_group_norm_act_backward_workspace_size", B, H, L, d), workspace, x)
     rc = lib.fw_group_norm_act_backward(x.data_ptr(), _data(gate), gamma.data_ptr(), beta.data_ptr(), dout.data_ptr(),
                                         dx.data_ptr(), _data(dgate), dgamma.data_ptr(), dbeta.data_ptr(),
                                         workspace.data_ptr(), ws_bytes, B, H, L, d, ACTIVATIONS[act],

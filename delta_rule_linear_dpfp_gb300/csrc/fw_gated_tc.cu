@@ -663,7 +663,8 @@ __global__ void __launch_bounds__(NT, 2)
 // the hi and the lo rows of its 64 x d_k factor stacked as its 128 rows, 8
 // MMAs of it for d_k 128, against [Z hi | Z lo] side by side; the answers'
 // product follows while the values are on their way, and the state's product
-// after that.  (One tile of W' and Q' rows, hi then lo, had 16 MMAs on the
+// after that.  (Two threads issuing half of it each into accumulators of their
+// own were no faster: the MMAs, not their issue, take the time.)  (One tile of W' and Q' rows, hi then lo, had 16 MMAs on the
 // serial path: 1.6 us a chunk instead of 1.2.)
 //
 // Eight worker warps a tile.  Of a tile's, warps 0, 1, 4, 5 read the hi rows' result, warps 2, 3,
@@ -973,10 +974,15 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
             }
             written(zr);
         };
-        for (int it = 0; it < nch; it += 2) { // (by twos, so that each dY row has registers of its own)
-            step(it, even);
-            if (it + 1 < nch)
-                step(it + 1, odd);
+        if constexpr (MODE == kRev) { // by twos, so that each dY row has registers of its own
+            for (int it = 0; it < nch; it += 2) {
+                step(it, even);
+                if (it + 1 < nch)
+                    step(it + 1, odd);
+            }
+        } else {
+            for (int it = 0; it < nch; ++it)
+                step(it, even);
         }
         if (Zf && mine && rr < a.d_k)
 #pragma unroll

@@ -83,6 +83,7 @@ CASES = [
     (1, 1, 2, 640, 128, 96, True, False),
     (5, 2, 6, 70, 128, 80, True, True),       # more CTAs than SMs, an odd number of 32-channel slices
     (10, 3, 3, 65, 64, 96, False, False),
+    (1, 1, 2, 130, 128, 256, True, False),    # the widest state
     (2, 4, 8, 1600, 64, 48, True, True),      # long enough for the forward to go in segments
 ]
 
