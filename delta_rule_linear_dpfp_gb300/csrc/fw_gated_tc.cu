@@ -402,6 +402,29 @@ __global__ void __launch_bounds__(NT, 2)
             }
         }
     }
+    // V or dY as an MN-major tile of 64-channel blocks: two rows' 16-byte chunks a
+    // thread and block, requested and stored apart so that V's way is under the
+    // inverse (the first two blocks; a wider V follows when its turn comes)
+    auto request_rows = [&](const __nv_bfloat16 *src, int blk, uint4 (&u)[2]) {
+        const int r = tid >> 2, ch = 8 * blk + 2 * (tid & 3);
+        const uint4 *from = reinterpret_cast<const uint4 *>(src + ((size_t)bh * a.L + (size_t)c * C + r) * a.d_v) + ch;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            u[m] = make_uint4(0, 0, 0, 0);
+            if (r < n && (ch + m) * 8 < a.d_v)
+                u[m] = __ldcg(from + m);
+        }
+    };
+    auto store_rows = [&](int blk, const uint4 (&u)[2]) {
+        const int r = tid >> 2, ch = 8 * blk + 2 * (tid & 3);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+            *reinterpret_cast<uint4 *>(vt + kmajor_chunk(r, (ch + m) * 8, 64)) = u[m];
+    };
+    uint4 v0[2], v1[2];
+    request_rows(v, 0, v0);
+    if (nvb > 1)
+        request_rows(v, 1, v1);
     __syncthreads();
     unit_lower_inverse(At, Tt, tmp);
 #pragma unroll
@@ -492,30 +515,18 @@ __global__ void __launch_bounds__(NT, 2)
             mma_commit(bar);
         }
     };
-    auto load_rows = [&](const __nv_bfloat16 *src) { // V or dY, MN-major 64-channel blocks
-        const __nv_bfloat16 *sg = src + ((size_t)bh * a.L + (size_t)c * C) * a.d_v;
-        for (int e = tid; e < C * nvb * 8; e += 2 * NT) { // (two 64-channel halves of a row pair: 2 NT divides C nvb 8)
-            uint4 u[2];
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const int r = (e + m * NT) / (nvb * 8), ch = (e + m * NT) % (nvb * 8);
-                u[m] = make_uint4(0, 0, 0, 0);
-                if (r < n && ch * 8 < a.d_v)
-                    u[m] = __ldcg(reinterpret_cast<const uint4 *>(sg + (size_t)r * a.d_v) + ch);
-            }
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const int r = (e + m * NT) / (nvb * 8), ch = (e + m * NT) % (nvb * 8);
-                *reinterpret_cast<uint4 *>(vt + kmajor_chunk(r, ch * 8, 64)) = u[m];
-            }
-        }
-    };
     float x2[32];
     factor(true, x2);
     put(x2);
     hand_over();
     multiply(tA1, dKmn, idesc_bf16(128, DKP, 0, 1)); // [-W'; ...] or [-W'; W"]
-    load_rows(v); // A's place
+    store_rows(0, v0); // A's place
+    if (nvb > 1)
+        store_rows(1, v1);
+    for (int blk = 2; blk < nvb; ++blk) {
+        request_rows(v, blk, v0);
+        store_rows(blk, v0);
+    }
     factor(false, x2);
     finish();
     put(x2);
@@ -548,11 +559,20 @@ __global__ void __launch_bounds__(NT, 2)
             bulk_wait_read();
         __syncwarp();
     };
-    auto rows_out = [&](size_t to, int R, int r0) {
+    // (`two`: the images' hi terms have left or are leaving the operand region,
+    // and every other pair of pieces goes there: one copy may be on its way)
+    auto rows_out = [&](size_t to, int R, int r0, bool two) {
         if (rr < r0 || rr >= r0 + R)
             return;
         for (int p0 = half; p0 < a.d_v / 16; p0 += 4) {
-            sent();
+            uint8_t *place = two && (p0 & 4) ? op + w * 4096 : mine;
+            if (two) {
+                if (lane == 0)
+                    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                __syncwarp();
+            } else {
+                sent();
+            }
 #pragma unroll 1
             for (int e = 0; e < 2; ++e) {
                 const int p = p0 + 2 * e;
@@ -563,7 +583,7 @@ __global__ void __launch_bounds__(NT, 2)
                 tmem_ld_wait();
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
-                    *reinterpret_cast<float4 *>(mine + 2048 * e + piece_chunk(lane, m)) =
+                    *reinterpret_cast<float4 *>(place + 2048 * e + piece_chunk(lane, m)) =
                         make_float4(x[4 * m], x[4 * m + 1], x[4 * m + 2], x[4 * m + 3]);
             }
             fence_async_smem();
@@ -572,7 +592,7 @@ __global__ void __launch_bounds__(NT, 2)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
                     if (p0 + 2 * e < a.d_v / 16)
-                        bulk_s2g(out + to + ((size_t)(p0 + 2 * e) * R + 32 * (w & 3) - r0) * 64, mine + 2048 * e, 2048);
+                        bulk_s2g(out + to + ((size_t)(p0 + 2 * e) * R + 32 * (w & 3) - r0) * 64, place + 2048 * e, 2048);
                 bulk_commit();
             }
         }
@@ -630,22 +650,27 @@ __global__ void __launch_bounds__(NT, 2)
     __syncthreads();
     if (!BWD) {
         images_out();
-        rows_out(rec.base, 128, 0);
+        rows_out(rec.base, 128, 0, NKB == 2);
     } else {
-        if (NKB == 2) {
-            rows_out(rec.base, C, 0);
-            load_rows(dy); // V's place
-        } else { // one place for both
-            rows_out(rec.base, C, 0);
+        for (int blk = 0; blk < min(nvb, 2); ++blk)
+            request_rows(dy, blk, blk ? v1 : v0);
+        rows_out(rec.base, C, 0, false);
+        if (NKB == 1) { // V's place holds both these rows and dY
             sent();
             __syncthreads();
-            load_rows(dy);
+        }
+        store_rows(0, v0); // V's place
+        if (nvb > 1)
+            store_rows(1, v1);
+        for (int blk = 2; blk < nvb; ++blk) {
+            request_rows(dy, blk, v0);
+            store_rows(blk, v0);
         }
         hand_over();
         multiply(tA2, dV, idv);
         finish();
         images_out();
-        rows_out(rec.base2, C, C);
+        rows_out(rec.base2, C, C, NKB == 2);
     }
     if (lane == 0)
         bulk_wait_all();
