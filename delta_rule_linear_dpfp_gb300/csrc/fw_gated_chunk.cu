@@ -39,6 +39,7 @@
 #include "fw_common.cuh"
 #include "fw_gated.h"
 #include "fw_gated_tc.h"
+#include "fw_gated_tiles.cuh"
 
 #include <algorithm>
 
@@ -53,7 +54,6 @@ constexpr int NT = 256;  // threads per CTA
 constexpr int NV = 32;   // value channels per slice of the gradient kernel
 constexpr int LC = C + 4; // row stride of a C x C tile
 constexpr int TOK = 8; // floats per token: rk, rq, e^G, e^{G_C-G}, G high, G low, beta, unused
-constexpr float kGMin = -200.f; // e^g is 0 in fp32 below this: a gate of -inf is a sum that stays finite
 
 // Workspace, in floats: per chunk of every value head.
 struct Ws {
@@ -84,14 +84,9 @@ Ws ws_at(void *p, const WsOff &o) {
     return {f + o.T, f + o.M, f + o.tok, f + o.S, f + o.dS, f + o.U, f + o.dX};
 }
 
-FW_DEV int seq_len(const GatedArgs &a, int b) {
-    return a.lengths ? min(max(__ldcg(a.lengths + b), 0), a.L) : a.L;
-}
-
-// rows x d of T (row stride lds) into fp32 shared memory; rows at or past
+// rows x width of a tensor (row stride lds) into shared memory; rows at or past
 // `valid` and channels at or past `cols` are zero (whatever is stored there).
-template <typename T>
-FW_DEV void load_tile(float *dst, int ldd, const T *src, size_t lds, int rows, int valid, int cols, int width) {
+FW_DEV void load_tile(float *dst, int ldd, const float *src, size_t lds, int rows, int valid, int cols, int width) {
     const int c8 = width >> 3;
     for (int e = threadIdx.x; e < rows * c8; e += NT) {
         const int i = e / c8, c = (e % c8) * 8;

@@ -21,6 +21,7 @@
 // key, so dq and dk are sums in a fixed order.
 #include "fw_gated.h"
 #include "fw_gated_tc.h"
+#include "fw_gated_tiles.cuh"
 #include "fw_tc.cuh"
 
 #include <algorithm>
@@ -39,26 +40,6 @@ constexpr int C = kGatedChunk;
 // where two CTAs share an SM's registers.
 __host__ __device__ constexpr int parts_of(int nkb) { return 2 * nkb; }
 
-FW_DEV void split8(const float *x, uint4 &hi, uint4 &lo) {
-    uint32_t h[4], l[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        h[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
-        l[e] = pack_bf16x2(x[2 * e] - __uint_as_float(h[e] << 16),
-                           x[2 * e + 1] - __uint_as_float(h[e] & 0xffff0000u));
-    }
-    hi = make_uint4(h[0], h[1], h[2], h[3]);
-    lo = make_uint4(l[0], l[1], l[2], l[3]);
-}
-FW_DEV void widen8(uint4 u, float (&o)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        o[2 * i] = __uint_as_float(w[i] << 16);
-        o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-FW_DEV uint32_t pair_chunk(int row, int c) { return (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)); }
 // 8 channels (chunk c of 4) of a pair tile's row: hi + lo.
 FW_DEV void pair8(const uint8_t *tile, int row, int c, float (&o)[8]) {
     float l[8];
@@ -122,8 +103,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
     const int b = bk / a.Hk, grp = a.H / a.Hk, ns = rec.ns;
     const int rr = 32 * (w & 3) + lane, part = w >> 2, i = rr & 63;
     griddep_wait();
-    const int len = a.lengths ? min(max(__ldcg(a.lengths + b), 0), a.L) : a.L;
-    const int n = min(C, len - c * C), rows = min(C, a.L - c * C); // tokens; rows in memory
+    const int n = min(C, seq_len(a, b) - c * C), rows = min(C, a.L - c * C); // tokens; rows in memory
     const size_t krow = ((size_t)bk * a.L + (size_t)c * C) * a.d_k;
     if (n <= 0) { // behind the sequence's end: no gradient
         griddep_launch_dependents();

@@ -17,6 +17,9 @@ Contents
                                        without the z normaliser), plain C
   chunked.delta_forward_chunked     -- O2: the chunked (WY / UT) form in numpy,
                                        for tiny brute-force checks of O1
+  gated.gated_forward, gated.gated_backward, gated.group_norm_act -- the gated
+                                       delta rule, its gradients, and the group
+                                       norm behind it, numpy fp64
   stack.stack_step, stack.layer_norm -- one token through the token-wise layer
                                        stack (projections, decode step, output
                                        map, LayerNorm, feed-forward), numpy fp64
@@ -28,7 +31,9 @@ each routine follows.  Parity is pinned by tests/test_oracle_*.py against
 hand-worked examples (tests/golden/), closed forms, invariants, an FFT
 identity and the independent chunked form O2; tests/test_oracle_mutants.py
 shows that planted mistakes in fw_oracle.c fail those pins, and
-tests/test_oracle_stack.py does the same for stack.py.  No function is
+tests/test_oracle_stack.py does the same for stack.py, and
+tests/test_gated_oracle.py pins gated.py to this oracle, hand-worked values and
+central differences.  No function is
 left unpinned.
 """
 import ctypes

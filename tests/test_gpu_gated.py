@@ -347,3 +347,73 @@ def test_gradients_are_the_differences():
         diff = (loss({**d, n: d[n] + step * way}) - loss({**d, n: d[n] - step * way})) / (2 * step)
         slope = float((got[n].double() * way).sum())
         assert abs(diff - slope) <= 2.0 ** -6 * abs(slope), (n, diff, slope)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 1, 2, 130, 64, 48), (5, 2, 6, 70, 128, 80), (1, 1, 1, 3, 16, 16)], ids=str)
+def test_a_workspace_of_anything(shape, dtype):
+    """What a workspace holds on entry does not matter: all ones (NaN in every type) gives the same bits."""
+    B, Hk, H, L, d_k, d_v = shape
+    d = dev(make(B, Hk, H, L, d_k, d_v, dtype, True, 16))
+    args = [d[n] for n in ("q", "k", "v", "g", "beta")]
+    lens = torch.full((B,), max(L - 20, 1), dtype=torch.int32, device="cuda")
+    got = []
+    for fill in (0, 255):
+        n = fw.fw_gated_delta_forward_workspace_size(B, Hk, H, L, d_k, d_v, dtype)
+        m = fw.fw_gated_delta_backward_workspace_size(B, Hk, H, L, d_k, d_v, dtype)
+        ws = torch.full((max(n, m),), fill, dtype=torch.uint8, device="cuda")
+        out = fw.fw_gated_delta_forward(*args, W0=d["W0"], lengths=lens, workspace=ws)
+        ws.fill_(fill)
+        out += fw.fw_gated_delta_backward(*args, d["v"], W0=d["W0"], dW_final=d["W0"], lengths=lens, workspace=ws)
+        got.append(out)
+    assert all(torch.isfinite(t).all() for t in got[0])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_two_streams_at_once():
+    """Calls with workspaces of their own on two streams: the bits of the calls alone."""
+    ds = [dev(make(2, 2, 4, 1600, 64, 64, torch.bfloat16, True, s)) for s in (17, 18)]
+    args = ("q", "k", "v", "g", "beta")
+
+    def work(d):
+        y, W = fw.fw_gated_delta_forward(**d)
+        return (y, W) + fw.fw_gated_delta_backward(*[d[n] for n in args], y, W0=d["W0"])
+
+    want = [work(d) for d in ds]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ds]
+    outs = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(work(ds[i]))
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(a, b) for r in o for a, b in zip(r, w))
+
+
+def test_decode_in_a_graph():
+    """One captured step replayed for token after token: the sequence's answers."""
+    d = make(3, 1, 2, 6, 64, 32, torch.bfloat16, True, 19)
+    x = dev(d)
+    one = {n: x[n][:, :, 0].clone() for n in ("q", "k", "v", "g", "beta")}
+    W = x["W0"].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = fw.fw_gated_delta_decode_step(**one, W=W)
+    ys = []
+    for t in range(6):
+        for n in one:
+            one[n].copy_(x[n][:, :, t])
+        graph.replay()
+        ys.append(y.clone())
+    yr, Wr = gated.gated_forward(**host(d))
+    near("y", torch.stack(ys, 2), yr)
+    near("W", W, Wr, bf16=False)
+
+
+def test_lengths_are_refused_unaligned():
+    d = dev(make(3, 1, 2, 20, 32, 16, torch.bfloat16, True, 20))
+    lens = torch.full((4,), 5, dtype=torch.int32, device="cuda")[1:]
+    with pytest.raises(fw.FwError):
+        fw.fw_gated_delta_forward(**d, lengths=lens)
