@@ -530,7 +530,7 @@ def _size(query, *shape):
 def _scratch(need, workspace, like):
     """The caller's workspace, or a new one of `need` bytes, and its bytes."""
     if workspace is None:
-        workspace = like.new_empty(-(-need // like.element_size()))
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -679,7 +679,7 @@ def fw_group_norm_act(x, gamma, beta, gate=None, act: str = "none", eps: float =
     st = _here("x gamma beta gate out", x, gamma, beta, gate, out)
     B, H, L, d = _norm_shapes(x, gamma, beta, gate, act)
     if out is None:
-        out = x.new_empty(B, L, H * d)
+        out = torch.empty(B, L, H * d, dtype=x.dtype, device=x.device)
     elif out.dtype != x.dtype or out.shape != (B, L, H * d):
         raise ValueError("out must be [B,L,H d] in x's dtype")
     rc = load().fw_group_norm_act(x.data_ptr(), _data(gate), gamma.data_ptr(), beta.data_ptr(), out.data_ptr(), B, H, L,

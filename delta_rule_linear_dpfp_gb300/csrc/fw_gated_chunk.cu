@@ -49,10 +49,8 @@ cudaError_t device_sms(int *out); // fw_api.cu
 
 namespace {
 
-constexpr int C = kGatedChunk;
-constexpr int NT = 256;  // threads per CTA
+constexpr int C = kGatedChunk, NT = kGatedThreads, LC = kGatedLd;
 constexpr int NV = 32;   // value channels per slice of the gradient kernel
-constexpr int LC = C + 4; // row stride of a C x C tile
 constexpr int TOK = 8; // floats per token: rk, rq, e^G, e^{G_C-G}, G high, G low, beta, unused
 
 // Workspace, in floats: per chunk of every value head.
@@ -163,49 +161,24 @@ FW_DEV void mm_nn(float (&acc)[R][4], const float *A, int lda, int ra, const flo
     }
 }
 
-// T = (I + A)^-1 of the strictly lower triangular A (C x C, stride LC):
-// forward substitution inside the four 16 x 16 diagonal blocks, one thread
-// per column, then two doublings T21 = -T22 (A21 T11).
-FW_DEV void unit_lower_inverse(const float *A, float *T, float *tmp) {
-    const int tid = threadIdx.x;
-    for (int e = tid; e < C * C; e += NT)
-        if ((e >> 6) >> 4 < (e & 63) >> 4)
-            T[(e >> 6) * LC + (e & 63)] = 0.f;
-    if (tid < C) {
-        const int b0 = tid & ~15, j = tid & 15;
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float s = i == j ? 1.f : 0.f;
-#pragma unroll
-            for (int m = 0; m < i; ++m)
-                s = fmaf(-A[(b0 + i) * LC + b0 + m], x[m], s);
-            x[i] = s;
-            T[(b0 + i) * LC + b0 + j] = s;
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int h = 16; h <= 32; h *= 2) {
-        const int per = h * h, n = (C / (2 * h)) * per;
-        for (int e = tid; e < n; e += NT) {
-            const int p = e / per, i = (e % per) / h, j = e % h, r0 = p * 2 * h;
-            float s = 0.f;
-            for (int m = j; m < h; ++m)
-                s = fmaf(A[(r0 + h + i) * LC + r0 + m], T[(r0 + m) * LC + r0 + j], s);
-            tmp[p * per + i * h + j] = s;
-        }
-        __syncthreads();
-        for (int e = tid; e < n; e += NT) {
-            const int p = e / per, i = (e % per) / h, j = e % h, r0 = p * 2 * h;
-            float s = 0.f;
-            for (int m = 0; m <= i; ++m)
-                s = fmaf(T[(r0 + h + i) * LC + r0 + h + m], tmp[p * per + m * h + j], s);
-            T[(r0 + h + i) * LC + r0 + j] = -s;
-        }
-        __syncthreads();
+// 16-byte asynchronous copies into shared memory; `in` false writes zeros.
+FW_DEV void copy16(float *dst, const float *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(in ? 16 : 0)
+                 : "memory");
+}
+FW_DEV void copies_sent() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> FW_DEV void copies_done() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// rows x width (a power of two, given as the logarithm of its quarter) of a
+// tensor whose rows at or past `valid` and columns at or past `cols` read as zero.
+FW_DEV void copy_tile(float *dst, int ldd, const float *src, size_t lds, int rows, int valid, int cols, int log_w4) {
+    for (int e = threadIdx.x; e < rows << log_w4; e += NT) {
+        const int i = e >> log_w4, c = (e & ((1 << log_w4) - 1)) * 4;
+        const bool in = i < valid && c < cols;
+        copy16(dst + i * ldd + c, in ? src + (size_t)i * lds + c : src, in);
     }
 }
+FW_DEV int log2_of(int x) { return 31 - __clz(x); }
 
 // ------------------------------------------------------------------ prep
 __global__ void __launch_bounds__(NT)
@@ -222,47 +195,48 @@ __global__ void __launch_bounds__(NT)
     if (n <= 0)
         return;
     const size_t row0 = (size_t)c * C;
-    load_tile(kt, ldk, k + ((size_t)kh * a.L + row0) * a.d_k, a.d_k, C, n, a.d_k, a.d_k);
-    load_tile(qt, ldk, q + ((size_t)kh * a.L + row0) * a.d_k, a.d_k, C, n, a.d_k, a.d_k);
+    const int lk4 = log2_of(a.d_k / 4);
+    copy_tile(kt, ldk, k + ((size_t)kh * a.L + row0) * a.d_k, a.d_k, C, n, a.d_k, lk4);
+    copy_tile(qt, ldk, q + ((size_t)kh * a.L + row0) * a.d_k, a.d_k, C, n, a.d_k, lk4);
+    copies_sent();
     if (tid < 32) { // the running sums of g, two tokens a lane
         const size_t t0 = (size_t)bh * a.L + row0;
-        double s[2];
-        float be[2];
+        float x[2], be[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int i = 2 * tid + e;
-            const float x = i < n ? io<float>::load(g + t0 + i) : 0.f;
-            s[e] = x < kGMin ? kGMin : x;
+            x[e] = i < n ? io<float>::load(g + t0 + i) : 0.f;
+            x[e] = x[e] < kGMin ? kGMin : x[e];
             be[e] = i < n ? io<float>::load(beta + t0 + i) : 0.f;
         }
-        s[1] += s[0];
-        double run = s[1];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double up = __shfl_up_sync(0xffffffffu, run, o);
-            if (tid >= o)
-                run += up;
-        }
-        const double before = run - s[1], all = __shfl_sync(0xffffffffu, run, 31);
+        Pair run, all;
+        running_sum(x, tid, run, all);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const double G = before + s[e];
+            const Pair G = e ? run : add(run, {-x[1], 0.f});
             float *d = tok + (2 * tid + e) * TOK;
-            d[2] = expf((float)G);
-            d[3] = expf((float)(all - G));
-            d[4] = (float)G;
-            d[5] = (float)(G - (double)(float)G);
+            d[2] = expf(G.hi);
+            d[3] = expf((all.hi - G.hi) + (all.lo - G.lo));
+            d[4] = G.hi;
+            d[5] = G.lo;
             d[6] = be[e];
             d[7] = 0.f;
         }
     }
+    copies_done<0>();
     __syncthreads();
-    if (tid < 2 * C) { // 1 / length of each key and query (0 for a row of zeros)
-        const float *x = (tid < C ? kt : qt) + (tid & 63) * ldk;
-        float ss = a.eps;
-        for (int m = 0; m < a.d_k; ++m)
-            ss = fmaf(x[m], x[m], ss);
-        tok[(tid & 63) * TOK + (tid >> 6)] = !a.l2norm ? 1.f : ss > 0.f ? 1.f / sqrtf(ss) : ss;
+    { // 1 / length of each key and query (0 for a row of zeros): two lanes a row, every other 16 bytes
+        const int row = tid >> 1;
+        const float *x = (row < C ? kt : qt) + (row & 63) * ldk + 4 * (tid & 1);
+        float ss = 0.f;
+        for (int m = 0; m < a.d_k; m += 8) {
+            const float4 t = lds4(x + m);
+            ss = fmaf(t.x, t.x, fmaf(t.y, t.y, fmaf(t.z, t.z, fmaf(t.w, t.w, ss))));
+        }
+        ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+        ss += a.eps;
+        if ((tid & 1) == 0)
+            tok[(row & 63) * TOK + (row >> 6)] = !a.l2norm ? 1.f : ss > 0.f ? 1.f / sqrtf(ss) : ss;
     }
     __syncthreads();
     const size_t ch = (size_t)bh * gridDim.x + c;
@@ -289,25 +263,6 @@ __global__ void __launch_bounds__(NT)
     for (int e = tid; e < C * TOK; e += NT)
         ws.tok[ch * C * TOK + e] = tok[e];
 }
-
-// 16-byte asynchronous copies into shared memory; `in` false writes zeros.
-FW_DEV void copy16(float *dst, const float *src, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
-                 "r"(in ? 16 : 0)
-                 : "memory");
-}
-FW_DEV void copies_sent() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> FW_DEV void copies_done() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-// rows x width (a power of two, given as the logarithm of its quarter) of a
-// tensor whose rows at or past `valid` and columns at or past `cols` read as zero.
-FW_DEV void copy_tile(float *dst, int ldd, const float *src, size_t lds, int rows, int valid, int cols, int log_w4) {
-    for (int e = threadIdx.x; e < rows << log_w4; e += NT) {
-        const int i = e >> log_w4, c = (e & ((1 << log_w4) - 1)) * 4;
-        const bool in = i < valid && c < cols;
-        copy16(dst + i * ldd + c, in ? src + (size_t)i * lds + c : src, in);
-    }
-}
-FW_DEV int log2_of(int x) { return 31 - __clz(x); }
 
 // A walk CTA's channels: 32, or 16 where that still leaves SMs idle (the work
 // of a chunk is what a chunk takes then; B1 H4 L333 d 64: 61 us with 32,

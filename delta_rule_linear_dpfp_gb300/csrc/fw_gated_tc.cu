@@ -37,112 +37,13 @@ namespace {
 
 using namespace tc;
 
-constexpr int C = kGatedChunk;
-constexpr int NT = 256;
+constexpr int C = kGatedChunk, NT = kGatedThreads, LC = kGatedLd;
 constexpr int NV = 32;    // value channels per walk CTA
-constexpr int LC = C + 4; // row stride of an fp32 C x C tile
 
 // 16 fp32 channels of a row in a "piece" (rows of 64 bytes, the base rows of
 // the walk): 16-byte chunk c, placed so that eight rows in a row of lanes meet
 // eight different bank groups.
 FW_DEV uint32_t piece_chunk(int row, int c) { return (uint32_t)(row * 64 + ((c ^ ((row >> 1) & 3)) << 4)); }
-
-// Sums kept as an unevaluated pair of floats (hi + lo, 48 bits).
-struct Pair {
-    float hi, lo;
-};
-FW_DEV Pair add(Pair a, Pair b) { // two-sum of the highs, the lows added to what it left
-    const float s = a.hi + b.hi, t = s - a.hi;
-    const float e = ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo);
-    const float h = s + e;
-    return {h, e - (h - s)};
-}
-
-// (I + A)^-1 of the strictly lower triangular A (row stride LC): forward
-// substitution in the four 16 x 16 diagonal blocks, one thread a column, then
-// two doublings T21 = -T22 (A21 T11), four columns a thread.
-// R rows a thread: more products for each value read from shared memory.
-template <int H, int R> FW_DEV void block_product(const float *a, int lda, const float *b, int ldb, float (&s)[R][4]) {
-#pragma unroll
-    for (int m = 0; m < H; m += 4) {
-        float f[R][4];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const float4 t = *reinterpret_cast<const float4 *>(a + r * (H / R) * lda + m);
-            f[r][0] = t.x;
-            f[r][1] = t.y;
-            f[r][2] = t.z;
-            f[r][3] = t.w;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float4 t = *reinterpret_cast<const float4 *>(b + (m + e) * ldb);
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                s[r][0] = fmaf(f[r][e], t.x, s[r][0]);
-                s[r][1] = fmaf(f[r][e], t.y, s[r][1]);
-                s[r][2] = fmaf(f[r][e], t.z, s[r][2]);
-                s[r][3] = fmaf(f[r][e], t.w, s[r][3]);
-            }
-        }
-    }
-}
-template <int H, int R> FW_DEV void double_inverse(const float *A, float *T, float *tmp) {
-    constexpr int Q = H / 4, N = (C / (2 * H)) * (H / R) * Q; // threads: pair of blocks, row, four columns
-    const int tid = threadIdx.x, p = tid / (H / R * Q), i = (tid / Q) % (H / R), j = (tid % Q) * 4, r0 = p * 2 * H;
-    if (tid < N) {
-        float s[R][4] = {};
-        block_product<H, R>(A + (r0 + H + i) * LC + r0, LC, T + r0 * LC + r0 + j, LC, s);
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            *reinterpret_cast<float4 *>(tmp + (p * H + i + r * (H / R)) * H + j) =
-                make_float4(s[r][0], s[r][1], s[r][2], s[r][3]);
-    }
-    __syncthreads();
-    if (tid < N) {
-        float s[R][4] = {};
-        block_product<H, R>(T + (r0 + H + i) * LC + r0 + H, LC, tmp + p * H * H + j, H, s);
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            *reinterpret_cast<float4 *>(T + (r0 + H + i + r * (H / R)) * LC + r0 + j) =
-                make_float4(-s[r][0], -s[r][1], -s[r][2], -s[r][3]);
-    }
-    __syncthreads();
-}
-
-FW_DEV void unit_lower_inverse(const float *A, float *T, float *tmp) {
-    const int tid = threadIdx.x;
-    for (int e = tid; e < C * C / 4; e += NT) {
-        const int r = e >> 4, c4 = (e & 15) * 4;
-        if (r >> 4 < c4 >> 4)
-            *reinterpret_cast<float4 *>(T + r * LC + c4) = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    if (tid < C) {
-        const int b0 = tid & ~15, j = tid & 15;
-        const float *Ab = A + b0 * LC + b0;
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float s = i == j ? 1.f : 0.f, s2 = 0.f;
-#pragma unroll
-            for (int m = 0; m < i; m += 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(Ab + i * LC + m);
-                s = fmaf(-f.x, x[m], s);
-                if (m + 1 < i)
-                    s2 = fmaf(-f.y, x[m + 1], s2);
-                if (m + 2 < i)
-                    s = fmaf(-f.z, x[m + 2], s);
-                if (m + 3 < i)
-                    s2 = fmaf(-f.w, x[m + 3], s2);
-            }
-            x[i] = s + s2;
-            T[(b0 + i) * LC + b0 + j] = x[i];
-        }
-    }
-    __syncthreads();
-    double_inverse<16, 1>(A, T, tmp);
-    double_inverse<32, 2>(A, T, tmp);
-}
 
 // A descriptor `bytes` further into its tile.
 FW_DEV uint64_t at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
@@ -251,14 +152,8 @@ __global__ void __launch_bounds__(NT, 2)
                 x[e] = x[e] < kGMin ? kGMin : x[e];
                 be[e] = i < n ? io<__nv_bfloat16>::load(beta + t0 + i) : 0.f;
             }
-            Pair run = add({x[0], 0.f}, {x[1], 0.f});
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const Pair up = {__shfl_up_sync(0xffffffffu, run.hi, m), __shfl_up_sync(0xffffffffu, run.lo, m)};
-                if (lane >= m)
-                    run = add(up, run);
-            }
-            const Pair all = {__shfl_sync(0xffffffffu, run.hi, 31), __shfl_sync(0xffffffffu, run.lo, 31)};
+            Pair run, all;
+            running_sum(x, lane, run, all);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const Pair G = e ? run : add(run, {-x[1], 0.f});
