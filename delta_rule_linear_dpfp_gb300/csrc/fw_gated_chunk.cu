@@ -40,6 +40,7 @@
 #include "fw_gated.h"
 #include "fw_gated_tc.h"
 #include "fw_gated_tiles.cuh"
+#include "fw_pairs.cuh"
 
 #include <algorithm>
 
@@ -99,47 +100,88 @@ FW_DEV void load_tile(float *dst, int ldd, const float *src, size_t lds, int row
 
 FW_DEV float4 lds4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 
+// Products of tiles in shared memory, on pairs of floats: one instruction for
+// two products (B8 H16 L512 d 128: forward 438 -> 417 us; with few heads the
+// walks wait for shared memory and barriers, and it makes no difference).
+struct Quad { // 16 bytes as two pairs
+    F2 a, b;
+};
+FW_DEV Quad ldq(const float *p) {
+    const ulonglong2 t = *reinterpret_cast<const ulonglong2 *>(p);
+    return {{t.x}, {t.y}};
+}
+
 // acc[r][s] += sum_k A[r][k] B[s][k] (K a multiple of 4).
 template <int R, int S>
 FW_DEV void mm_nt(float (&acc)[R][S], const float *A, int lda, int ra, const float *B, int ldb, int rb, int K) {
+    F2 t[R][S] = {};
 #pragma unroll 2
     for (int k = 0; k < K; k += 4) {
-        float4 a[R], b[S];
+        Quad a[R], b[S];
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            a[r] = lds4(A + r * ra * lda + k);
+            a[r] = ldq(A + r * ra * lda + k);
 #pragma unroll
         for (int s = 0; s < S; ++s)
-            b[s] = lds4(B + s * rb * ldb + k);
+            b[s] = ldq(B + s * rb * ldb + k);
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int s = 0; s < S; ++s)
-                acc[r][s] = fmaf(a[r].w, b[s].w, fmaf(a[r].z, b[s].z, fmaf(a[r].y, b[s].y, fmaf(a[r].x, b[s].x, acc[r][s]))));
+                t[r][s] = fma2(a[r].b, b[s].b, fma2(a[r].a, b[s].a, t[r][s]));
     }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+            acc[r][s] += sum(t[r][s]);
 }
 
-// acc[r][0..3] += sum_k A[k lda + r ra] B[k ldb .. + 3] * w[k]: A's rows run
-// along k (transposed use).
-template <int R>
-FW_DEV void mm_tn(float (&acc)[R][4], const float *A, int lda, int ra, const float *B, int ldb, int K) {
-#pragma unroll 4
-    for (int k = 0; k < K; ++k) {
-        const float4 b = lds4(B + k * ldb);
+// Four columns' sums as two pairs.
+template <int R> struct Columns {
+    F2 t[R][2];
+    FW_DEV Columns(const float (&acc)[R][4]) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const float x = A[k * lda + r * ra];
-            acc[r][0] = fmaf(x, b.x, acc[r][0]);
-            acc[r][1] = fmaf(x, b.y, acc[r][1]);
-            acc[r][2] = fmaf(x, b.z, acc[r][2]);
-            acc[r][3] = fmaf(x, b.w, acc[r][3]);
+            t[r][0] = pack(acc[r][0], acc[r][1]);
+            t[r][1] = pack(acc[r][2], acc[r][3]);
         }
     }
+    FW_DEV void add(int r, float x, const Quad &y) {
+        t[r][0] = fma2(both(x), y.a, t[r][0]);
+        t[r][1] = fma2(both(x), y.b, t[r][1]);
+    }
+    FW_DEV void get(float (&acc)[R][4]) const {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float2 p = unpack(t[r][0]), q = unpack(t[r][1]);
+            acc[r][0] = p.x;
+            acc[r][1] = p.y;
+            acc[r][2] = q.x;
+            acc[r][3] = q.y;
+        }
+    }
+};
+
+// acc[r][0..3] += sum_k A[k lda + r ra] B[k ldb .. + 3]: A's rows run along k
+// (transposed use).
+template <int R>
+FW_DEV void mm_tn(float (&acc)[R][4], const float *A, int lda, int ra, const float *B, int ldb, int K) {
+    Columns<R> t(acc);
+#pragma unroll 4
+    for (int k = 0; k < K; ++k) {
+        const Quad b = ldq(B + k * ldb);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            t.add(r, A[k * lda + r * ra], b);
+    }
+    t.get(acc);
 }
 
 // acc[r][0..3] += sum_k A[r][k] B[k ldb .. + 3].
 template <int R>
 FW_DEV void mm_nn(float (&acc)[R][4], const float *A, int lda, int ra, const float *B, int ldb, int K) {
+    Columns<R> t(acc);
 #pragma unroll 2
     for (int k = 0; k < K; k += 4) {
         float4 a[R];
@@ -148,17 +190,13 @@ FW_DEV void mm_nn(float (&acc)[R][4], const float *A, int lda, int ra, const flo
             a[r] = lds4(A + r * ra * lda + k);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const float4 b = lds4(B + (k + u) * ldb);
+            const Quad b = ldq(B + (k + u) * ldb);
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float x = u == 0 ? a[r].x : u == 1 ? a[r].y : u == 2 ? a[r].z : a[r].w;
-                acc[r][0] = fmaf(x, b.x, acc[r][0]);
-                acc[r][1] = fmaf(x, b.y, acc[r][1]);
-                acc[r][2] = fmaf(x, b.z, acc[r][2]);
-                acc[r][3] = fmaf(x, b.w, acc[r][3]);
-            }
+            for (int r = 0; r < R; ++r)
+                t.add(r, u == 0 ? a[r].x : u == 1 ? a[r].y : u == 2 ? a[r].z : a[r].w, b);
         }
     }
+    t.get(acc);
 }
 
 // 16-byte asynchronous copies into shared memory; `in` false writes zeros.
@@ -265,8 +303,8 @@ __global__ void __launch_bounds__(NT)
 }
 
 // A walk CTA's channels: 32, or 16 where that still leaves SMs idle (the work
-// of a chunk is what a chunk takes then; B1 H4 L333 d 64: 61 us with 32,
-// 50 with 16).  A thread's rows of a tile are ti + S r (S = 64 / R, R rows of
+// of a chunk is what a chunk takes then; B1 H4 L333 d 64: 61 us with
+// 32, 50 with 16).  A thread's rows of a tile are ti + S r (S = 64 / R, R rows of
 // each 64) and its columns 4 tj ..; a warp covers 8 rows by 4 column groups, so
 // that both operands' 16-byte reads are one wavefront each (32 rows a warp took
 // four for one of them).
@@ -285,21 +323,20 @@ FW_DEV void update_state(float *Z, int ldk, float whole, const float *A, const f
     if (n0 >= NV)
         return;
     float s[4][4] = {};
+    Columns<4> sums(s);
     for (int src = 0; src < (A2 ? 2 : 1); ++src) {
         const float *a = (src ? A2 : A) + n0, *b = (src ? B2 : B) + k4;
 #pragma unroll 4
         for (int t = 0; t < C; ++t) {
-            const float4 x = lds4(a + t * Tile<NV>::LV), y = lds4(b + t * ldk);
-            const float xr[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                s[r][0] = fmaf(xr[r], y.x, s[r][0]);
-                s[r][1] = fmaf(xr[r], y.y, s[r][1]);
-                s[r][2] = fmaf(xr[r], y.z, s[r][2]);
-                s[r][3] = fmaf(xr[r], y.w, s[r][3]);
-            }
+            const float4 x = lds4(a + t * Tile<NV>::LV);
+            const Quad y = ldq(b + t * ldk);
+            sums.add(0, x.x, y);
+            sums.add(1, x.y, y);
+            sums.add(2, x.z, y);
+            sums.add(3, x.w, y);
         }
     }
+    sums.get(s);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         float *p = Z + (n0 + r) * ldk + k4;

@@ -23,6 +23,7 @@
 // exponentials and reciprocals, or it would cost as much as the bytes.
 #include "fw_common.cuh"
 #include "fw_gated.h"
+#include "fw_pairs.cuh"
 
 #include <algorithm>
 
@@ -32,42 +33,6 @@ namespace {
 
 constexpr int kT = 256;
 enum { kNone = 0, kRelu = 1, kSilu = 2, kGelu = 3 };
-
-// Two floats that one instruction adds or multiplies (each rounded as the
-// single instruction rounds it): the kernels are near the instruction rate.
-struct F2 {
-    unsigned long long v;
-};
-FW_DEV F2 pack(float lo, float hi) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-    return r;
-}
-FW_DEV float2 unpack(F2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-FW_DEV F2 both(float x) { return pack(x, x); }
-FW_DEV F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-FW_DEV F2 operator*(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-FW_DEV F2 operator+(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-FW_DEV float sum(F2 a) {
-    const float2 t = unpack(a);
-    return t.x + t.y;
-}
 
 // (A variant of the kernels for each: as a branch per element it made them
 // bound by instructions, 36 an element and 49 us where the bytes take 30.)
