@@ -1,6 +1,7 @@
 // fw_gated.h -- host interface of the gated delta rule's kernels
-// (fw_gated_chunk.cu, fw_gated_decode.cu), for the argument-checking C ABI in
-// fw_gated_api.cu.
+// (fw_gated_chunk.cu, fw_gated_tc.cu, fw_gated_grad_tc.cu, fw_gated_decode.cu)
+// and of the group norm's (fw_group_norm.cu), for the argument-checking C ABI
+// in fw_gated_api.cu.
 #pragma once
 #include <cuda_runtime.h>
 #include <stddef.h>

@@ -56,7 +56,7 @@ FW_DEV uint64_t at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); 
 // then dY's, later), per-token scalars.  What a product leaves goes out by
 // warps: 32 rows are staged as 4 KB that lie together in the record too, and
 // one lane sends them (stored from registers, a row per lane, every 16 bytes
-// cost a sector: 8000 of a chunk's 20 000 cycles).
+// cost a sector: 317 us for 4096 chunks of d 128 where this took 249).
 struct PrepSmem {
     uint32_t kq, op, at, tt, tok, bar, bytes;
 };
@@ -553,14 +553,15 @@ __global__ void __launch_bounds__(NT, 2)
 // the hi and the lo rows of its 64 x d_k factor stacked as its 128 rows, 8
 // MMAs of it for d_k 128, against [Z hi | Z lo] side by side; the answers'
 // product follows while the values are on their way, and the state's product
-// after that.  (Two threads issuing half of it each into accumulators of their
-// own were no faster: the MMAs, not their issue, take the time.)  (One tile of W' and Q' rows, hi then lo, had 16 MMAs on the
-// serial path: 1.6 us a chunk instead of 1.2.)
+// after that.  (One tile of W' and Q' rows, hi then lo, had 16 MMAs on the
+// serial path: 1.6 us a chunk instead of 1.45.  Two threads issuing half of the
+// product each, into accumulators of their own, were no faster: the MMAs, not
+// their issue, take the time.)
 //
-// Eight worker warps a tile.  Of a tile's, warps 0, 1, 4, 5 read the hi rows' result, warps 2, 3,
-// 6, 7 the lo rows' of the same tokens (a warp reaches 32 of the 128 TMEM
-// lanes); the two swap halves of their 16 channels through shared memory and
-// each finishes 8 channels.  Thread (row 32 (w % 4) + lane, 16 channels) also
+// Eight worker warps a tile.  Of a tile's, warps 0, 1, 4, 5 read the hi rows'
+// result, warps 2, 3, 6, 7 the lo rows' of the same tokens (a warp reaches 32
+// of the 128 TMEM lanes); the two swap halves of their 16 channels through
+// shared memory and each finishes 8 channels.  Thread (row 32 (w % 4) + lane, 16 channels) also
 // holds 16 values of the fp32 state (row = key channel).  One more warp's first
 // lane issues the MMAs and another's asks for the records, each part as soon
 // as the product that last read its place is done, so that none of that is on
