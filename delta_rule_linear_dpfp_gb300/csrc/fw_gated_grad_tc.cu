@@ -40,6 +40,11 @@ constexpr int C = kGatedChunk;
 // where two CTAs share an SM's registers.
 __host__ __device__ constexpr int parts_of(int nkb) { return 2 * nkb; }
 
+// 16 bytes on their way into shared memory, or zeros.
+FW_DEV void copy16(void *to, const void *from, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(in ? 16 : 0) : "memory");
+}
+
 // 8 channels (chunk c of 4) of a pair tile's row: hi + lo.
 FW_DEV void pair8(const uint8_t *tile, int row, int c, float (&o)[8]) {
     float l[8];
@@ -51,31 +56,30 @@ FW_DEV void pair8(const uint8_t *tile, int row, int c, float (&o)[8]) {
 }
 
 // Shared memory: [K; Q]; two slices (S, dS', [dY; dX], U), whose place the E
-// and F tiles (64 KB) and the staged reader rows take afterwards; the sums of
+// and F tiles (64 KB) take afterwards; the sums of
 // dq and dk over the value heads -- in the place of the E and F tiles, too,
 // where a key head has one value head, so that for d_k <= 64 two CTAs fit an
 // SM (B4 H8 L512, 256 CTAs: the whole backward 57 us with one an SM, 52 with
 // two); scalars.
 struct GradSmem {
-    uint32_t slice, s, ds, yx, u, ef, stage, accq, acck, tok, red, bar, bytes;
+    uint32_t slice, s, ds, yx, u, ef, accq, acck, tok, v, red, bar, bytes;
 };
 __host__ __device__ inline GradSmem grad_smem(int nkb, bool alone) {
     GradSmem o;
     o.ef = (uint32_t)nkb * 16384;
-    o.s = 0;
-    o.ds = (uint32_t)nkb * 8192;
-    o.yx = 2 * o.ds;
-    o.u = o.yx + 16384;
-    o.slice = o.u + 8192;
-    o.stage = o.ef + 65536;
-    const uint32_t a = o.ef + 2 * o.slice, b = o.stage + (uint32_t)nkb * 16384, end = a > b ? a : b;
+    o.s = 0; // U follows S, so that one product reads both
+    o.u = (uint32_t)nkb * 8192;
+    o.ds = o.u + 8192;
+    o.yx = o.ds + (uint32_t)nkb * 8192;
+    o.slice = o.yx + 16384;
+    const uint32_t end = o.ef + 2 * o.slice; // (the E and F tiles are shorter)
     o.accq = alone ? o.ef : end;
     o.acck = o.accq + (uint32_t)nkb * 16384;
-    // (an MMA of 128 rows reads 8 KB past a slice's U, one of 64 columns 16 KB
-    // past the last F tile: into what follows, or into this slack)
-    o.tok = alone ? end + 8192 : o.acck + (uint32_t)nkb * 16384;
-    o.red = o.tok + C * 32;
-    o.bar = o.red + 4 * ((3 * parts_of(nkb) + 1) * C + 32);
+    // (U as 128 rows reads 8 KB past it, of dS')
+    o.tok = alone ? end : o.acck + (uint32_t)nkb * 16384;
+    o.v = o.tok + 2 * C * 32;
+    o.red = o.v + 2 * C * 64;
+    o.bar = o.red + 4 * ((4 * parts_of(nkb) + 1) * C + 32);
     o.bytes = o.bar + 64 + 1024;
     return o;
 }
@@ -95,8 +99,8 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
     uint8_t *kq = sm, *ef = sm + o.ef;
     float *tok = reinterpret_cast<float *>(sm + o.tok); // per token: G hi, G lo, rk, beta, rq, e^G, e^{G_C-G}, -
     float *red = reinterpret_cast<float *>(sm + o.red);
-    float *r_qa = red, *r_kh = red + PARTS * C, *r_kw = red + 2 * PARTS * C, *r_xv = red + 3 * PARTS * C,
-          *r_ss = r_xv + C, *r_last = r_ss + 16; // qa, kh, kw: one value per part
+    float *r_qa = red, *r_kh = red + PARTS * C, *r_kw = red + 2 * PARTS * C, *r_kl = red + 3 * PARTS * C,
+          *r_xv = red + 4 * PARTS * C, *r_ss = r_xv + C, *r_last = r_ss + 16; // qa, kh, kw, kl: one value per part
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + o.bar), *done = full + 2, *kqb = full + 4, *mm = full + 5;
     uint32_t *slot = reinterpret_cast<uint32_t *>(full + 6);
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, c = blockIdx.x, bk = blockIdx.y;
@@ -163,11 +167,27 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
     // a thread's part of the sums over the value heads: row i, channels part * HC ..
     float4 *accq = reinterpret_cast<float4 *>(sm + o.accq) + (size_t)part * (HC / 4) * C + i;
     float4 *acck = reinterpret_cast<float4 *>(sm + o.acck) + (size_t)part * (HC / 4) * C + i;
-    float4 *stage = reinterpret_cast<float4 *>(sm + o.stage) + (size_t)part * (HC / 4) * C + i;
+    // 256 threads: a row and 8 of 32 channels of dY, dX, V; the others, if any: <S, dS'>
+    const bool rowed = tid < 256, squared = NT == 256 || !rowed;
+    const int yr = (tid >> 2) & 63, yc = tid & 3;
     int gs = 0; // slices seen
-    for (int m = 0; m < grp; ++m) {
-        const size_t r0 = (size_t)(bk * grp + m) * a.L + (size_t)c * C;
-        __syncthreads(); // the previous head's reads of the slices' place, tok and red are over
+    auto row_at = [&](int m, int s) { // dY's and V's 8 channels of slice s, value head m
+        return ((size_t)(bk * grp + m) * a.L + (size_t)c * C + yr) * a.d_v + 32 * s + 8 * yc;
+    };
+    auto row_in = [&](int s) { return 32 * s + 8 * yc < a.d_v && yr < n; };
+    auto request = [&](int m, int s, int g) { // into slice g's place; dY has no lo terms
+        if (rowed) {
+            uint8_t *yx = ef + (g & 1) * o.slice + o.yx;
+            const bool in = row_in(s);
+            const size_t at = in ? row_at(m, s) : 0;
+            copy16(yx + pair_chunk(yr, yc), dy + at, in);
+            copy16(sm + o.v + (g & 1) * (C * 64) + tid * 16, v + at, in);
+            *reinterpret_cast<uint4 *>(yx + pair_chunk(yr, yc + 4)) = make_uint4(0, 0, 0, 0);
+        }
+    };
+    // a head's first two slices and its scalars: asked for as soon as their
+    // places are free, the next head's while this one's last sums are taken
+    auto begin = [&](int m) {
         if (tid == 0 && ok) {
             // generic reads and writes of the place end before the copies into it
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -175,43 +195,35 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
             if (ns > 1)
                 fetch(gs + 1);
         }
+        request(m, 0, gs);
+        if (ns > 1)
+            request(m, 1, gs + 1);
         if (tid < 2 * C)
-            reinterpret_cast<float4 *>(tok)[tid] =
-                __ldcg(reinterpret_cast<const float4 *>(record(m) + rec.tok) + tid);
+            copy16(sm + o.tok + (m & 1) * (C * 32) + tid * 16, record(m) + rec.tok + tid * 16, true);
+    };
+    begin(0);
+    for (int m = 0; m < grp; ++m) {
+        const size_t r0 = (size_t)(bk * grp + m) * a.L + (size_t)c * C;
+        tok = reinterpret_cast<float *>(sm + o.tok) + (m & 1) * (C * 8);
         float xv = 0.f, ss = 0.f;
-        // 256 threads: a row and 8 of 32 channels of dY, dX, V; the others, if any: <S, dS'>
-        const bool rowed = tid < 256, squared = NT == 256 || !rowed;
-        const int yr = (tid >> 2) & 63, yc = tid & 3;
         for (int s = 0; s < ns; ++s, ++gs) {
             uint8_t *sl = ef + (gs & 1) * o.slice;
-            const bool in = rowed && 32 * s + 8 * yc < a.d_v && yr < n;
-            const size_t at = (r0 + yr) * a.d_v + 32 * s + 8 * yc;
-            uint4 yv = make_uint4(0, 0, 0, 0), vv = yv;
-            if (in) {
-                yv = __ldcg(reinterpret_cast<const uint4 *>(dy + at));
-                vv = __ldcg(reinterpret_cast<const uint4 *>(v + at));
-            }
-            if (s >= 2) // the slice that lay here has been multiplied (dY's rows are not part of the copy)
-                wait(done + (gs & 1), ((gs >> 1) + 1) & 1);
-            if (rowed) {
-                *reinterpret_cast<uint4 *>(sl + o.yx + pair_chunk(yr, yc)) = yv;
-                *reinterpret_cast<uint4 *>(sl + o.yx + pair_chunk(yr, yc + 4)) = make_uint4(0, 0, 0, 0);
-            }
+            asm volatile("cp.async.wait_all;" ::: "memory"); // this thread's parts of this slice's rows (and tok)
             wait(full + (gs & 1), (gs >> 1) & 1);
             if (s == 0)
                 __syncthreads(); // tok
             if (rowed) {
                 float x[8], y[8];
                 pair8(sl + o.yx + 8192, yr, yc, x);
-                widen8(vv, y);
+                widen8(*reinterpret_cast<const uint4 *>(sm + o.v + (gs & 1) * (C * 64) + tid * 16), y);
                 const float be = tok[yr * 8 + 3];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     xv = fmaf(x[e], y[e], xv);
                     x[e] *= be;
                 }
-                if (in)
-                    store8(dv + at, x);
+                if (row_in(s))
+                    store8(dv + row_at(m, s), x);
             }
             if (squared) {
 #pragma unroll
@@ -228,6 +240,12 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
             fence_async_smem();
             tc_fence_before();
             __syncthreads();
+            if (s >= 1 && s + 1 < ns) { // the other place's slice is done: its successor
+                wait(done + ((gs + 1) & 1), ((gs - 1) >> 1) & 1);
+                if (tid == 0 && ok)
+                    fetch(gs + 1);
+                request(m, s + 1, gs + 1);
+            }
             if (tid == 0 && ok) {
                 tc_fence_after();
                 const uint32_t base = ef_s + (uint32_t)(gs & 1) * o.slice;
@@ -236,18 +254,13 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                     for (int e = 0; e < 2; ++e) {
                         const uint64_t yx = desc_sw128(base + o.yx + ta + e * 32, 16, 1024);
                         const uint32_t acc = (s | t | e) != 0;
-                        mma_bf16(tA, yx, desc_sw128(base + o.s + tb + e * 32, 16, 1024), idesc_bf16(128, DKP, 0, 0), acc);
-                        mma_bf16(tB, yx, desc_sw128(base + o.u + tb + e * 32, 16, 1024), idesc_bf16(128, 64, 0, 0), acc);
+                        mma_bf16(tA, yx, desc_sw128(base + o.s + tb + e * 32, 16, 1024), // S and U: tA and tB
+                                 idesc_bf16(128, DKP + 64, 0, 0), acc);
                         mma_bf16(tW, desc_sw128(base + o.u + ta + e * 32, 16, 1024),
                                  desc_sw128(base + o.ds + tb + e * 32, 16, 1024), idesc_bf16(128, DKP, 0, 0), acc);
                     }
                 }
                 mma_commit(done + (gs & 1));
-                if (s >= 1 && s + 1 < ns) { // the other buffer's slice is done: its successor
-                    wait(done + ((gs + 1) & 1), ((gs - 1) >> 1) & 1);
-                    if (ok)
-                        fetch(gs + 1);
-                }
             }
         }
         // every product of this head's slices (one commit covers those before it)
@@ -278,7 +291,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                     const int j = j0 + e;
                     const float4 dj = *reinterpret_cast<const float4 *>(tok + j * 8);
                     const bool in = rr < C ? j <= i : j < i;
-                    const float t = in ? (rr < C ? a.scale : 1.f) * x[e] * expf((di.x - dj.x) + (di.y - dj.y)) : 0.f;
+                    const float t = in ? (rr < C ? a.scale : 1.f) * x[e] * __expf((di.x - dj.x) + (di.y - dj.y)) : 0.f;
                     x[e] = t * dj.z;
                     y[e] = t * fr;
                 }
@@ -316,11 +329,9 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                     mma_bf16(tA, desc_sw128(ef_s + (uint32_t)t * 16384u + (uint32_t)s * 32u, 16, 1024),
                              desc_sw128(kq_s + (uint32_t)s * 2048u, 16384, 1024), idesc_bf16(128, DKP, 0, 1),
                              (t | s) != 0);
-            for (int t = 0; t < 2; ++t)
-                for (int s = 0; s < 8; ++s)
-                    mma_bf16(tE, desc_sw128(ef_s + 32768u + (uint32_t)t * 16384u + (uint32_t)s * 2048u, 16384, 1024),
-                             desc_sw128(kq_s + (uint32_t)s * 2048u, 16384, 1024), idesc_bf16(128, DKP, 1, 1),
-                             (t | s) != 0);
+            for (int s = 0; s < 8; ++s) // rows 0 - 63 from the hi terms, 64 - 127 from the lo terms
+                mma_bf16(tE, desc_sw128(ef_s + 32768u + (uint32_t)s * 2048u, 16384, 1024),
+                         desc_sw128(kq_s + (uint32_t)s * 2048u, 16384, 1024), idesc_bf16(128, DKP, 1, 1), s != 0);
             mma_commit(mm);
         }
         // k_j . (e^{G_C-G_j} dS'^T U_j), for the chunk's decay
@@ -349,6 +360,8 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
         }
         wait(mm, (uint32_t)m & 1);
         tc_fence_after();
+        if (m + 1 < grp) // (the E and F tiles have been read; the sums lie in their place only if grp is 1)
+            begin(m + 1);
         {
             float dot = 0.f; // q.a or k.h, this part's channels
 #pragma unroll
@@ -372,10 +385,34 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
             else
                 r_kh[part * C + i] = dot * di.z;
         }
-        if (rr >= C) {
+        if (rr >= C) { // -beta h, and w's part of the lo terms
+            float dot = 0.f;
 #pragma unroll
-            for (int p = 0; p < HC; p += 4)
-                stage[(p / 4) * C] = make_float4(-di.w * x[p], -di.w * x[p + 1], -di.w * x[p + 2], -di.w * x[p + 3]);
+            for (int p = 0; p < HC; p += 16) {
+                float t[16];
+                tmem_ld16(tE + lb + (uint32_t)(part * HC + p), t);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; e += 8) {
+                    float u[8];
+                    kq_row(i, p + e, u);
+#pragma unroll
+                    for (int m2 = 0; m2 < 8; ++m2) {
+                        dot = fmaf(u[m2], t[e + m2], dot);
+                        t[e + m2] = fmaf(-di.w, x[p + e + m2], t[e + m2]);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    float4 r = make_float4(t[e], t[e + 1], t[e + 2], t[e + 3]);
+                    if (m > 0) {
+                        const float4 s = acck[((p + e) / 4) * C];
+                        r = make_float4(r.x + s.x, r.y + s.y, r.z + s.z, r.w + s.w);
+                    }
+                    acck[((p + e) / 4) * C] = r;
+                }
+            }
+            r_kl[part * C + i] = dot * di.z;
         } else {
 #pragma unroll
             for (int p = 0; p < HC; p += 4) {
@@ -408,13 +445,8 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                 }
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
-                    const float4 s = stage[((p + e) / 4) * C];
-                    float4 r = make_float4(t[e] + s.x, t[e + 1] + s.y, t[e + 2] + s.z, t[e + 3] + s.w);
-                    if (m > 0) {
-                        const float4 o4 = acck[((p + e) / 4) * C];
-                        r = make_float4(r.x + o4.x, r.y + o4.y, r.z + o4.z, r.w + o4.w);
-                    }
-                    acck[((p + e) / 4) * C] = r;
+                    const float4 s = acck[((p + e) / 4) * C]; // (the row's other thread left its part)
+                    acck[((p + e) / 4) * C] = make_float4(t[e] + s.x, t[e + 1] + s.y, t[e + 2] + s.z, t[e + 3] + s.w);
                 }
             }
             r_kw[part * C + i] = dot * di.z;
@@ -432,7 +464,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                 for (int p = 0; p < PARTS; ++p) {
                     qa += r_qa[p * C + t];
                     kh += r_kh[p * C + t];
-                    kw += r_kw[p * C + t];
+                    kw += r_kw[p * C + t] + r_kl[p * C + t];
                 }
                 G2[e] = qa - tok[t * 8 + 3] * kh - kw;
                 if (t < n)
