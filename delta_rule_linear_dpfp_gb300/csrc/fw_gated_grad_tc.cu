@@ -106,6 +106,10 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, c = blockIdx.x, bk = blockIdx.y;
     const int b = bk / a.Hk, grp = a.H / a.Hk, ns = rec.ns;
     const int rr = 32 * (w & 3) + lane, part = w >> 2, i = rr & 63;
+    // One thread asks for the slices and issues the products.  Of 16 warps its
+    // warp is left out of the work on the slices, which runs meanwhile.
+    constexpr int BOSS = NKB == 2 ? 15 : 0;
+    const bool boss = tid == 32 * BOSS;
     griddep_wait();
     const int n = min(C, seq_len(a, b) - c * C), rows = min(C, a.L - c * C); // tokens; rows in memory
     const size_t krow = ((size_t)bk * a.L + (size_t)c * C) * a.d_k;
@@ -127,48 +131,19 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
         }
         return;
     }
-    if (w == 0) {
-        tmem_alloc(slot, kCols);
-        tmem_relinquish();
-    }
-    if (tid == 32) {
-        for (int e = 0; e < 6; ++e)
-            mbar_init(full + e, 1);
-        fence_barrier_init();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    griddep_launch_dependents();
-    const uint32_t tm = *slot, tA = tm, tB = tm + DKP, tW = tB + 64, tE = tW + DKP;
-    const uint32_t lb = tmem_lane_base(w);
     bool ok = true;
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (ok)
-            ok = mbar_wait(bar, parity, status);
-    };
     auto record = [&](int m) { return ws + rec.off((int64_t)bk * grp + m, c); };
-    auto fetch = [&](int g) { // thread 0: slice g % ns of value head g / ns
-        const uint8_t *src = record(g / ns);
+    auto fetch = [&](const uint8_t *src, int s, int g) { // boss: slice s of a record, as the g-th of all
         uint8_t *dst = ef + (g & 1) * o.slice;
         uint64_t *f = full + (g & 1);
-        const int s = g % ns;
         mbar_arrive_expect_tx(f, (uint32_t)(NKB * 16384 + 16384));
         bulk_g2s(dst + o.s, src + rec.S + (size_t)s * NKB * 8192, NKB * 8192, f);
         bulk_g2s(dst + o.ds, src + rec.dS + (size_t)s * NKB * 8192, NKB * 8192, f);
         bulk_g2s(dst + o.yx + 8192, src + rec.dX + (size_t)s * 8192, 8192, f);
         bulk_g2s(dst + o.u, src + rec.U + (size_t)s * 8192, 8192, f);
     };
-    if (tid == 0) {
-        mbar_arrive_expect_tx(kqb, NKB * 16384);
-        bulk_g2s(kq, record(0) + rec.K, NKB * 16384, kqb);
-    }
-    const uint32_t kq_s = smem_u32(kq), ef_s = smem_u32(ef);
-    // a thread's part of the sums over the value heads: row i, channels part * HC ..
-    float4 *accq = reinterpret_cast<float4 *>(sm + o.accq) + (size_t)part * (HC / 4) * C + i;
-    float4 *acck = reinterpret_cast<float4 *>(sm + o.acck) + (size_t)part * (HC / 4) * C + i;
-    // 256 threads: a row and 8 of 32 channels of dY, dX, V; the others, if any: <S, dS'>
-    const bool rowed = tid < 256, squared = NT == 256 || !rowed;
+    // 256 threads: a row and 8 of 32 channels of dY, dX, V; seven of the other warps, if any: <S, dS'>
+    const bool rowed = tid < 256, squared = NT == 256 || (!rowed && w != BOSS);
     const int yr = (tid >> 2) & 63, yc = tid & 3;
     int gs = 0; // slices seen
     auto row_at = [&](int m, int s) { // dY's and V's 8 channels of slice s, value head m
@@ -188,20 +163,48 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
     // a head's first two slices and its scalars: asked for as soon as their
     // places are free, the next head's while this one's last sums are taken
     auto begin = [&](int m) {
-        if (tid == 0 && ok) {
+        const uint8_t *src = record(m);
+        if (boss && ok) {
             // generic reads and writes of the place end before the copies into it
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            fetch(gs);
+            fetch(src, 0, gs);
             if (ns > 1)
-                fetch(gs + 1);
+                fetch(src, 1, gs + 1);
         }
         request(m, 0, gs);
         if (ns > 1)
             request(m, 1, gs + 1);
         if (tid < 2 * C)
-            copy16(sm + o.tok + (m & 1) * (C * 32) + tid * 16, record(m) + rec.tok + tid * 16, true);
+            copy16(sm + o.tok + (m & 1) * (C * 32) + tid * 16, src + rec.tok + tid * 16, true);
     };
+    if (boss) {
+        for (int e = 0; e < 6; ++e)
+            mbar_init(full + e, 1);
+        fence_barrier_init();
+    }
     begin(0);
+    if (boss) {
+        mbar_arrive_expect_tx(kqb, NKB * 16384);
+        bulk_g2s(kq, record(0) + rec.K, NKB * 16384, kqb);
+    }
+    if (w == 0) {
+        tmem_alloc(slot, kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_launch_dependents();
+    const uint32_t tm = *slot, tA = tm, tB = tm + DKP, tW = tB + 64, tE = tW + DKP;
+    const uint32_t lb = tmem_lane_base(w);
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (ok)
+            ok = mbar_wait(bar, parity, status);
+    };
+    const uint32_t kq_s = smem_u32(kq), ef_s = smem_u32(ef);
+    // a thread's part of the sums over the value heads: row i, channels part * HC ..
+    float4 *accq = reinterpret_cast<float4 *>(sm + o.accq) + (size_t)part * (HC / 4) * C + i;
+    float4 *acck = reinterpret_cast<float4 *>(sm + o.acck) + (size_t)part * (HC / 4) * C + i;
     for (int m = 0; m < grp; ++m) {
         const size_t r0 = (size_t)(bk * grp + m) * a.L + (size_t)c * C;
         tok = reinterpret_cast<float *>(sm + o.tok) + (m & 1) * (C * 8);
@@ -227,8 +230,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
             }
             if (squared) {
 #pragma unroll
-                for (int e = 0; e < DKP * 4 / 256; ++e) {
-                    const int p = (tid & 255) + e * 256;
+                for (int p = tid % 256; p < DKP * 4; p += NT == 256 ? 256 : 224) {
                     float x[8], y[8];
                     pair8(sl + o.s, p >> 2, p & 3, x);
                     pair8(sl + o.ds, p >> 2, p & 3, y);
@@ -242,11 +244,9 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
             __syncthreads();
             if (s >= 1 && s + 1 < ns) { // the other place's slice is done: its successor
                 wait(done + ((gs + 1) & 1), ((gs - 1) >> 1) & 1);
-                if (tid == 0 && ok)
-                    fetch(gs + 1);
                 request(m, s + 1, gs + 1);
             }
-            if (tid == 0 && ok) {
+            if (boss && ok) {
                 tc_fence_after();
                 const uint32_t base = ef_s + (uint32_t)(gs & 1) * o.slice;
                 for (int t = 0; t < 3; ++t) { // hi hi, hi lo, lo hi
@@ -261,6 +261,11 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                     }
                 }
                 mma_commit(done + (gs & 1));
+                if (s + 2 < ns) { // this place's next slice, as soon as it may come
+                    wait(done + (gs & 1), (gs >> 1) & 1);
+                    if (ok)
+                        fetch(record(m), s + 2, gs + 2);
+                }
             }
         }
         // every product of this head's slices (one commit covers those before it)
@@ -322,7 +327,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
         fence_async_smem();
         tc_fence_before();
         __syncthreads();
-        if (tid == 0 && ok) {
+        if (boss && ok) {
             tc_fence_after();
             for (int t = 0; t < 2; ++t)
                 for (int s = 0; s < 4; ++s)
@@ -454,7 +459,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        if (w == 0) { // dg: the sums over later tokens, two a lane; dbeta
+        if (w == BOSS) { // dg: the sums over later tokens, two a lane; dbeta
             float G2[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -519,23 +524,29 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
         for (int p = 0; p < PARTS; ++p)
             f += red[p * 2 * C + rr];
         f = a.l2norm ? f * r : 0.f;
-        if (i < rows) {
-            bf *to = (rr < C ? dk : dq) + krow + (size_t)i * a.d_k;
+        // through shared memory (rows of DKP + 8), so that a row leaves by neighbouring lanes
+        uint8_t *place = ef + 2 * NKB * 16384;
+        constexpr int PITCH = DKP * 2 + 16;
 #pragma unroll
-            for (int p = 0; p < HC; p += 8) {
-                float u[8];
-                widen8(*reinterpret_cast<const uint4 *>(kq + kmajor_chunk(rr, part * HC + p, 128)), u);
-                const float4 s = acc[(p / 4) * C], t = acc[(p / 4 + 1) * C];
-                const float g8[8] = {s.x, s.y, s.z, s.w, t.x, t.y, t.z, t.w};
+        for (int p = 0; p < HC; p += 8) {
+            float u[8];
+            widen8(*reinterpret_cast<const uint4 *>(kq + kmajor_chunk(rr, part * HC + p, 128)), u);
+            const float4 s = acc[(p / 4) * C], t = acc[(p / 4 + 1) * C];
+            const float g8[8] = {s.x, s.y, s.z, s.w, t.x, t.y, t.z, t.w};
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    u[e] = i < n ? r * (g8[e] - u[e] * f) : 0.f;
-                if (part * HC + p < a.d_k)
-                    store8(to + part * HC + p, u);
-            }
+            for (int e = 0; e < 8; ++e)
+                u[e] = i < n ? r * (g8[e] - u[e] * f) : 0.f;
+            store8(reinterpret_cast<bf *>(place + rr * PITCH) + part * HC + p, u);
+        }
+        __syncthreads();
+        const int chunks = a.d_k / 8;
+        for (int e = tid; e < 2 * rows * chunks; e += NT) {
+            const int row = e / chunks, ch = e - row * chunks, to = row < rows ? row : row - rows; // dk's rows, then dq's
+            *reinterpret_cast<uint4 *>((row < rows ? dk : dq) + krow + (size_t)to * a.d_k + 8 * ch) =
+                *reinterpret_cast<const uint4 *>(place + (row < rows ? row : C + to) * PITCH + 16 * ch);
         }
     }
-    if (!ok && tid == 0) // a wait gave up: let what was asked for land first
+    if (!ok && boss) // a wait gave up: let what was asked for land first
         for (int e = 0; e < 2; ++e)
             (void)mbar_wait(full + e, 0, status);
     tc_fence_before();
