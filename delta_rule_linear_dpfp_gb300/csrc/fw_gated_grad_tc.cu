@@ -19,6 +19,16 @@
 //   then [E; F] K and [F; E]^T [K; Q].
 // One CTA per (chunk, key head) goes through the value heads that share the
 // key, so dq and dk are sums in a fixed order.
+//
+// What bounds it: for d_k > 64 one CTA an SM (tensor memory, shared memory),
+// and a head's 224 KB (d 128) come in four slices of which two fit.  B8 H16
+// L2048, two value heads a key head: 346 us, 2.7 TB/s; a head takes 21 000
+// cycles: 10 700 of slices (their copies), 1 100 for the last product, 3 700
+// for E and F, 1 500 for the second products, 3 700 for the sums.  It took
+// 28 600 when the next slice was asked for after a product had been issued
+// instead of when its place was free, the next head's after the sums, and dY
+// and V came through registers (375 us); 23 300 with the products issued by a
+// warp that shared in the work on the slices.
 #include "fw_gated.h"
 #include "fw_gated_tc.h"
 #include "fw_gated_tiles.cuh"
@@ -55,12 +65,12 @@ FW_DEV void pair8(const uint8_t *tile, int row, int c, float (&o)[8]) {
         o[e] += l[e];
 }
 
-// Shared memory: [K; Q]; two slices (S, dS', [dY; dX], U), whose place the E
-// and F tiles (64 KB) take afterwards; the sums of
-// dq and dk over the value heads -- in the place of the E and F tiles, too,
-// where a key head has one value head, so that for d_k <= 64 two CTAs fit an
-// SM (B4 H8 L512, 256 CTAs: the whole backward 57 us with one an SM, 52 with
-// two); scalars.
+// Shared memory: [K; Q]; two slices (S, U, dS', [dY; dX]), whose place the E
+// and F tiles (64 KB) take afterwards; the sums of dq and dk over the value
+// heads -- in the place of the E and F tiles, too, where a key head has one
+// value head, so that for d_k <= 64 two CTAs fit an SM (B4 H8 L512, 256 CTAs:
+// the whole backward 57 us with one an SM, 52 with two); scalars of this head
+// and the next; V's rows of two slices.
 struct GradSmem {
     uint32_t slice, s, ds, yx, u, ef, accq, acck, tok, v, red, bar, bytes;
 };
@@ -97,7 +107,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const GradSmem o = grad_smem(NKB, a.H == a.Hk);
     uint8_t *kq = sm, *ef = sm + o.ef;
-    float *tok = reinterpret_cast<float *>(sm + o.tok); // per token: G hi, G lo, rk, beta, rq, e^G, e^{G_C-G}, -
+    float *tok = reinterpret_cast<float *>(sm + o.tok);
     float *red = reinterpret_cast<float *>(sm + o.red);
     float *r_qa = red, *r_kh = red + PARTS * C, *r_kw = red + 2 * PARTS * C, *r_kl = red + 3 * PARTS * C,
           *r_xv = red + 4 * PARTS * C, *r_ss = r_xv + C, *r_last = r_ss + 16; // qa, kh, kw, kl: one value per part
@@ -219,7 +229,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                 float x[8], y[8];
                 pair8(sl + o.yx + 8192, yr, yc, x);
                 widen8(*reinterpret_cast<const uint4 *>(sm + o.v + (gs & 1) * (C * 64) + tid * 16), y);
-                const float be = tok[yr * 8 + 3];
+                const float be = tok[kBeta + yr];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     xv = fmaf(x[e], y[e], xv);
@@ -280,11 +290,11 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
         ss = warp_sum(ss);
         if (lane == 0)
             r_ss[w] = ss;
-        const float4 di = *reinterpret_cast<const float4 *>(tok + i * 8);
-        const float4 dj_ = *reinterpret_cast<const float4 *>(tok + i * 8 + 4); // rq, e^G, e^{G_C-G}
+        const float be = tok[kBeta + i], rk = tok[kRk + i], rq = tok[kRq + i];
         // E and F, as [E; F] rk_j (K-major) and as [F (-beta rk_i); E rq_i]
         {
-            const float fr = rr < C ? dj_.x : -di.w * di.z;
+            const float ghi = tok[kGhi + i], glo = tok[kGlo + i];
+            const F2 fr = both(rr < C ? rq : -be * rk), fs = both(rr < C ? a.scale : 1.f);
 #pragma unroll
             for (int p = 0; p < 64 / PARTS; p += 16) {
                 const int j0 = 64 / PARTS * part + p;
@@ -292,13 +302,22 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                 tmem_ld16(tB + lb + (uint32_t)j0, x);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int j = j0 + e;
-                    const float4 dj = *reinterpret_cast<const float4 *>(tok + j * 8);
-                    const bool in = rr < C ? j <= i : j < i;
-                    const float t = in ? (rr < C ? a.scale : 1.f) * x[e] * __expf((di.x - dj.x) + (di.y - dj.y)) : 0.f;
-                    x[e] = t * dj.z;
-                    y[e] = t * fr;
+                for (int e = 0; e < 16; e += 4) {
+                    F2 d[2];
+                    decay4(tok, j0 + e, ghi, glo, d);
+                    const ulonglong2 rj = *reinterpret_cast<const ulonglong2 *>(tok + kRk + j0 + e);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int j = j0 + e + 2 * u;
+                        float2 t = unpack(fs * pack(x[e + 2 * u], x[e + 2 * u + 1]) * d[u]);
+                        t.x = (rr < C ? j <= i : j < i) ? t.x : 0.f;
+                        t.y = (rr < C ? j + 1 <= i : j + 1 < i) ? t.y : 0.f;
+                        const float2 s = unpack(pack(t.x, t.y) * F2{u ? rj.y : rj.x}), r = unpack(pack(t.x, t.y) * fr);
+                        x[e + 2 * u] = s.x;
+                        x[e + 2 * u + 1] = s.y;
+                        y[e + 2 * u] = r.x;
+                        y[e + 2 * u + 1] = r.y;
+                    }
                 }
 #pragma unroll
                 for (int e = 0; e < 16; e += 8) {
@@ -314,7 +333,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
             }
         }
         float x[HC]; // rows of a (rr < 64) or h
-        const float fs = rr < C ? a.scale * dj_.y : dj_.y;
+        const float eg = tok[kEG + i], fs = rr < C ? a.scale * eg : eg;
 #pragma unroll
         for (int p = 0; p < HC; p += 16) {
             float t[16];
@@ -359,7 +378,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                         last = fmaf(u[m2], t[e + m2], last);
                 }
             }
-            last = warp_sum(last * di.z * dj_.z);
+            last = warp_sum(last * rk * tok[kEC + i]);
             if (lane == 0)
                 r_last[w] = last; // (warps with w & 2 == 0)
         }
@@ -386,9 +405,9 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                 }
             }
             if (rr < C)
-                r_qa[part * C + i] = dot * dj_.x;
+                r_qa[part * C + i] = dot * rq;
             else
-                r_kh[part * C + i] = dot * di.z;
+                r_kh[part * C + i] = dot * rk;
         }
         if (rr >= C) { // -beta h, and w's part of the lo terms
             float dot = 0.f;
@@ -404,7 +423,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
 #pragma unroll
                     for (int m2 = 0; m2 < 8; ++m2) {
                         dot = fmaf(u[m2], t[e + m2], dot);
-                        t[e + m2] = fmaf(-di.w, x[p + e + m2], t[e + m2]);
+                        t[e + m2] = fmaf(-be, x[p + e + m2], t[e + m2]);
                     }
                 }
 #pragma unroll
@@ -417,7 +436,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                     acck[((p + e) / 4) * C] = r;
                 }
             }
-            r_kl[part * C + i] = dot * di.z;
+            r_kl[part * C + i] = dot * rk;
         } else {
 #pragma unroll
             for (int p = 0; p < HC; p += 4) {
@@ -431,6 +450,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
         }
         __syncthreads();
         if (rr < C) {
+            const float ec = tok[kEC + i];
             float dot = 0.f;
 #pragma unroll
             for (int p = 0; p < HC; p += 16) {
@@ -444,7 +464,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                     kq_row(i, p + e, u);
 #pragma unroll
                     for (int m2 = 0; m2 < 8; ++m2) {
-                        t[e + m2] = fmaf(dj_.z, t[e + m2], u1[e + m2]);
+                        t[e + m2] = fmaf(ec, t[e + m2], u1[e + m2]);
                         dot = fmaf(u[m2], t[e + m2], dot);
                     }
                 }
@@ -454,7 +474,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                     acck[((p + e) / 4) * C] = make_float4(t[e] + s.x, t[e + 1] + s.y, t[e + 2] + s.z, t[e + 3] + s.w);
                 }
             }
-            r_kw[part * C + i] = dot * di.z;
+            r_kw[part * C + i] = dot * rk;
         }
         tc_fence_before();
         __syncthreads();
@@ -471,7 +491,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                     kh += r_kh[p * C + t];
                     kw += r_kw[p * C + t] + r_kl[p * C + t];
                 }
-                G2[e] = qa - tok[t * 8 + 3] * kh - kw;
+                G2[e] = qa - tok[kBeta + t] * kh - kw;
                 if (t < n)
                     io<bf>::store(dbeta + r0 + t, r_xv[t] - kh);
             }
@@ -482,7 +502,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                     s += r_ss[e];
                     l += e & 2 ? 0.f : r_last[e];
                 }
-                G2[1] += tok[(C - 1) * 8 + 5] * s + l;
+                G2[1] += tok[kEG + C - 1] * s + l;
             }
             float run = G2[0] + G2[1];
 #pragma unroll
@@ -508,7 +528,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
     __syncthreads(); // dg has been read off; red is free
     {
         const float4 *acc = rr < C ? acck : accq;
-        const float r = i >= n ? 0.f : tok[i * 8 + (rr < C ? 2 : 4)];
+        const float r = i >= n ? 0.f : tok[(rr < C ? kRk : kRq) + i];
         float dot = 0.f;
 #pragma unroll
         for (int p = 0; p < HC; p += 8) {

@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(NT, 2)
     const PrepSmem o = prep_smem(NKB, nvb);
     uint8_t *kq = sm + o.kq, *op = sm + o.op, *vt = sm + o.at;
     float *At = reinterpret_cast<float *>(sm + o.at), *tmp = At + C * LC, *Tt = reinterpret_cast<float *>(sm + o.tt);
-    float *tok = reinterpret_cast<float *>(sm + o.tok); // per token: G hi, G lo, rk, beta, rq, e^G, e^{G_C-G}, -
+    float *tok = reinterpret_cast<float *>(sm + o.tok);
     float *cw = tok + 8 * C, *cb = cw + C, *cd = cb + C; // -beta e^G rk, beta, e^{G_C-G} rk
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + o.bar);
     uint32_t *slot = reinterpret_cast<uint32_t *>(bar + 1);
@@ -157,13 +157,12 @@ __global__ void __launch_bounds__(NT, 2)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const Pair G = e ? run : add(run, {-x[1], 0.f});
-                float *d = tok + (2 * lane + e) * 8;
-                d[0] = G.hi;
-                d[1] = G.lo;
-                d[3] = be[e];
-                d[5] = expf(G.hi);
-                d[6] = expf((all.hi - G.hi) + (all.lo - G.lo));
-                d[7] = 0.f;
+                float *d = tok + 2 * lane + e;
+                d[kGhi] = G.hi;
+                d[kGlo] = G.lo;
+                d[kBeta] = be[e];
+                d[kEG] = expf(G.hi);
+                d[kEC] = expf((all.hi - G.hi) + (all.lo - G.lo));
             }
         }
 #pragma unroll
@@ -226,18 +225,18 @@ __global__ void __launch_bounds__(NT, 2)
             ss = e == lane ? x[e] : ss;
         ss += a.eps;
         ss = !a.l2norm ? 1.f : ss > 0.f ? 1.f / sqrtf(ss) : ss;
-        tok[i * 8 + (rr < C ? 2 : 4)] = ss;
+        tok[(rr < C ? kRk : kRq) + i] = ss;
         if (rr < C) {
-            const float be = tok[i * 8 + 3];
-            cw[i] = -be * tok[i * 8 + 5] * ss;
+            const float be = tok[kBeta + i];
+            cw[i] = -be * tok[kEG + i] * ss;
             cb[i] = be;
-            cd[i] = tok[i * 8 + 6] * ss;
+            cd[i] = tok[kEC + i] * ss;
         }
     }
     __syncthreads();
     {
-        const float4 di = *reinterpret_cast<const float4 *>(tok + i * 8);
-        const float fi = rr < C ? di.w * di.z : a.scale * tok[i * 8 + 4];
+        const float ghi = tok[kGhi + i], glo = tok[kGlo + i];
+        const F2 fi = both(rr < C ? tok[kBeta + i] * tok[kRk + i] : a.scale * tok[kRq + i]);
 #pragma unroll 1
         for (int p = 0; p < 2; ++p) {
             const int j0 = 32 * half + 16 * p;
@@ -245,11 +244,17 @@ __global__ void __launch_bounds__(NT, 2)
             tmem_ld16(tGram + tmem_lane_base(w) + (uint32_t)j0, x);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int j = j0 + e;
-                const float4 dj = *reinterpret_cast<const float4 *>(tok + j * 8);
-                const bool in = rr < C ? j < i : j <= i;
-                x[e] = in ? fi * dj.z * x[e] * __expf((di.x - dj.x) + (di.y - dj.y)) : 0.f;
+            for (int e = 0; e < 16; e += 4) {
+                F2 d[2];
+                decay4(tok, j0 + e, ghi, glo, d);
+                const ulonglong2 rk = *reinterpret_cast<const ulonglong2 *>(tok + kRk + j0 + e);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int j = j0 + e + 2 * u;
+                    const float2 t = unpack(fi * F2{u ? rk.y : rk.x} * pack(x[e + 2 * u], x[e + 2 * u + 1]) * d[u]);
+                    x[e + 2 * u] = (rr < C ? j < i : j <= i) ? t.x : 0.f;
+                    x[e + 2 * u + 1] = (rr < C ? j + 1 < i : j + 1 <= i) ? t.y : 0.f;
+                }
             }
             if (rr < C) {
 #pragma unroll
@@ -399,20 +404,21 @@ __global__ void __launch_bounds__(NT, 2)
     const uint32_t idv = idesc_bf16(128, a.d_v, 0, 1);
     multiply(tA2, dV, idv);
     if (tid < C) { // the walks' scalars
-        const float *d = tok + tid * 8;
+        const float *d = tok + tid;
         float *sf = reinterpret_cast<float *>(out + rec.scalF);
-        sf[tid] = d[6] * d[2];
+        sf[tid] = d[kEC] * d[kRk];
         if (tid == 0)
-            sf[C] = tok[(C - 1) * 8 + 5];
+            sf[C] = tok[kEG + C - 1];
         if (BWD) {
             float *sr = reinterpret_cast<float *>(out + rec.scalR);
-            sr[tid] = -d[3] * d[5] * d[2];
-            sr[C + tid] = a.scale * d[5] * d[4];
+            sr[tid] = -d[kBeta] * d[kEG] * d[kRk];
+            sr[C + tid] = a.scale * d[kEG] * d[kRq];
             if (tid == 0)
-                sr[2 * C] = tok[(C - 1) * 8 + 5];
-            float4 *st = reinterpret_cast<float4 *>(out + rec.tok) + 2 * tid;
-            st[0] = reinterpret_cast<const float4 *>(d)[0];
-            st[1] = reinterpret_cast<const float4 *>(d)[1];
+                sr[2 * C] = tok[kEG + C - 1];
+            float *st = reinterpret_cast<float *>(out + rec.tok) + tid;
+#pragma unroll
+            for (int e = 0; e <= kEC; e += C)
+                st[e] = d[e];
         }
     }
     finish();
@@ -474,7 +480,7 @@ __global__ void __launch_bounds__(NT, 2)
             tmem_ld16(tA1 + tmem_lane_base(w) + (uint32_t)c0, x);
             tmem_ld_wait();
             if (!BWD && rr >= C) {
-                const float f = a.scale * tok[i * 8 + 5] * tok[i * 8 + 4];
+                const float f = a.scale * tok[kEG + i] * tok[kRq + i];
 #pragma unroll
                 for (int e = 0; e < 16; e += 8) {
                     float y[8];

@@ -16,7 +16,7 @@ struct GatedRecord {
     // backward [keys; queries] per 64-wide block.
     size_t A, A2, K, scalF, scalR;
     size_t base, base2;          // fp32 pieces [d_v / 16][rows][16]: [U'; Y'] (128 rows), or U' and X0 (64 rows)
-    size_t U, dX, S, dS, tok;    // pair tiles [ns] of 64 (U, dX) and d_k (S, dS) rows; 8 floats a token
+    size_t U, dX, S, dS, tok;    // pair tiles [ns] of 64 (U, dX) and d_k (S, dS) rows; the tokens' scalars
 
     __host__ __device__ size_t off(int64_t bh, int c) const { return ((size_t)bh * nch + c) * bytes; }
 };

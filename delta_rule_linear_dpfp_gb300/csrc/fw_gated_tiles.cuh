@@ -4,6 +4,7 @@
 
 #include "fw_common.cuh"
 #include "fw_gated.h"
+#include "fw_pairs.cuh"
 
 namespace fw {
 
@@ -43,11 +44,28 @@ FW_DEV void split8(const float *x, uint4 &hi, uint4 &lo) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         h[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
-        l[e] = pack_bf16x2(x[2 * e] - __uint_as_float(h[e] << 16),
-                           x[2 * e + 1] - __uint_as_float(h[e] & 0xffff0000u));
+        const float2 d = unpack(pack(x[2 * e], x[2 * e + 1]) -
+                                pack(__uint_as_float(h[e] << 16), __uint_as_float(h[e] & 0xffff0000u)));
+        l[e] = pack_bf16x2(d.x, d.y);
     }
     hi = make_uint4(h[0], h[1], h[2], h[3]);
     lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// The tensor-core kernels' scalars of a chunk's tokens, [7][64]: G (the
+// running sum of g) as hi and lo, 1 / |k|, beta, 1 / |q|, e^G, e^{G_C - G}.
+enum { kGhi = 0, kGlo = 64, kRk = 128, kBeta = 192, kRq = 256, kEG = 320, kEC = 384 };
+
+// e^{G_i - G_j} of four tokens j; (ghi, glo) is G_i.
+FW_DEV void decay4(const float *tok, int j, float ghi, float glo, F2 (&d)[2]) {
+    const ulonglong2 h = *reinterpret_cast<const ulonglong2 *>(tok + kGhi + j);
+    const ulonglong2 l = *reinterpret_cast<const ulonglong2 *>(tok + kGlo + j);
+    const F2 hp[2] = {{h.x}, {h.y}}, lp[2] = {{l.x}, {l.y}};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const float2 t = unpack(((both(ghi) - hp[e]) + (both(glo) - lp[e])) * both(1.4426950408889634f));
+        d[e] = pack(ex2(t.x), ex2(t.y));
+    }
 }
 
 FW_DEV void widen8(uint4 u, float (&o)[8]) {

@@ -39,11 +39,6 @@ enum { kNone = 0, kRelu = 1, kSilu = 2, kGelu = 3 };
 // The exponential and the reciprocal as single instructions (2^-22 of the
 // value; denormal results are 0).  x sigmoid(x) needs no guard: far below 0 the
 // exponential is infinite and the reciprocal 0.
-FW_DEV float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 FW_DEV float rcp(float x) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));

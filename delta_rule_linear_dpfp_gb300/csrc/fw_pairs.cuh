@@ -36,6 +36,13 @@ FW_DEV F2 operator+(F2 a, F2 b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
     return r;
 }
+FW_DEV F2 operator-(F2 a, F2 b) { return fma2(b, both(-1.f), a); } // (one rounding)
+// 2^x in one instruction (2^-22 of it; denormal results are 0).
+FW_DEV float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 FW_DEV float sum(F2 a) {
     const float2 t = unpack(a);
     return t.x + t.y;
