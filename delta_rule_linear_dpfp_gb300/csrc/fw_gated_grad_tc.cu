@@ -56,13 +56,13 @@ FW_DEV void copy16(void *to, const void *from, bool in) {
 }
 
 // 8 channels (chunk c of 4) of a pair tile's row: hi + lo.
-FW_DEV void pair8(const uint8_t *tile, int row, int c, float (&o)[8]) {
-    float l[8];
+FW_DEV void pair8(const uint8_t *tile, int row, int c, F2 (&o)[4]) {
+    F2 l[4];
     widen8(*reinterpret_cast<const uint4 *>(tile + pair_chunk(row, c)), o);
     widen8(*reinterpret_cast<const uint4 *>(tile + pair_chunk(row, c + 4)), l);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        o[e] += l[e];
+    for (int e = 0; e < 4; ++e)
+        o[e] = o[e] + l[e];
 }
 
 // Shared memory: [K; Q]; two slices (S, U, dS', [dY; dX]), whose place the E
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
     for (int m = 0; m < grp; ++m) {
         const size_t r0 = (size_t)(bk * grp + m) * a.L + (size_t)c * C;
         tok = reinterpret_cast<float *>(sm + o.tok) + (m & 1) * (C * 8);
-        float xv = 0.f, ss = 0.f;
+        F2 xv2 = both(0.f), ss2 = both(0.f);
         for (int s = 0; s < ns; ++s, ++gs) {
             uint8_t *sl = ef + (gs & 1) * o.slice;
             asm volatile("cp.async.wait_all;" ::: "memory"); // this thread's parts of this slice's rows (and tok)
@@ -226,27 +226,30 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
             if (s == 0)
                 __syncthreads(); // tok
             if (rowed) {
-                float x[8], y[8];
+                F2 x[4], y[4];
+                float t[8];
                 pair8(sl + o.yx + 8192, yr, yc, x);
                 widen8(*reinterpret_cast<const uint4 *>(sm + o.v + (gs & 1) * (C * 64) + tid * 16), y);
-                const float be = tok[kBeta + yr];
+                const F2 be = both(tok[kBeta + yr]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    xv = fmaf(x[e], y[e], xv);
-                    x[e] *= be;
+                for (int e = 0; e < 4; ++e) {
+                    xv2 = fma2(x[e], y[e], xv2);
+                    const float2 d = unpack(x[e] * be);
+                    t[2 * e] = d.x;
+                    t[2 * e + 1] = d.y;
                 }
                 if (row_in(s))
-                    store8(dv + row_at(m, s), x);
+                    store8(dv + row_at(m, s), t);
             }
             if (squared) {
 #pragma unroll
                 for (int p = tid % 256; p < DKP * 4; p += NT == 256 ? 256 : 224) {
-                    float x[8], y[8];
+                    F2 x[4], y[4];
                     pair8(sl + o.s, p >> 2, p & 3, x);
                     pair8(sl + o.ds, p >> 2, p & 3, y);
 #pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        ss = fmaf(x[u], y[u], ss);
+                    for (int u = 0; u < 4; ++u)
+                        ss2 = fma2(x[u], y[u], ss2);
                 }
             }
             fence_async_smem();
@@ -283,6 +286,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
         tc_fence_after();
         if (m == 0)
             wait(kqb, 0);
+        float xv = sum(xv2), ss = sum(ss2);
         xv += __shfl_xor_sync(0xffffffffu, xv, 1);
         xv += __shfl_xor_sync(0xffffffffu, xv, 2);
         if (rowed && yc == 0)
@@ -359,10 +363,10 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
             mma_commit(mm);
         }
         // k_j . (e^{G_C-G_j} dS'^T U_j), for the chunk's decay
-        auto kq_row = [&](int row, int p, float (&u)[8]) {
+        auto kq_row = [&](int row, int p, F2 (&u)[4]) {
             widen8(*reinterpret_cast<const uint4 *>(kq + kmajor_chunk(row, part * HC + p, 128)), u);
         };
-        float last = 0.f;
+        F2 last2 = both(0.f);
         if (rr < C) {
 #pragma unroll
             for (int p = 0; p < HC; p += 16) {
@@ -371,14 +375,14 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; e += 8) {
-                    float u[8];
+                    F2 u[4];
                     kq_row(i, p + e, u);
 #pragma unroll
-                    for (int m2 = 0; m2 < 8; ++m2)
-                        last = fmaf(u[m2], t[e + m2], last);
+                    for (int m2 = 0; m2 < 4; ++m2)
+                        last2 = fma2(u[m2], pack(t[e + 2 * m2], t[e + 2 * m2 + 1]), last2);
                 }
             }
-            last = warp_sum(last * rk * tok[kEC + i]);
+            const float last = warp_sum(sum(last2) * rk * tok[kEC + i]);
             if (lane == 0)
                 r_last[w] = last; // (warps with w & 2 == 0)
         }
@@ -387,7 +391,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
         if (m + 1 < grp) // (the E and F tiles have been read; the sums lie in their place only if grp is 1)
             begin(m + 1);
         {
-            float dot = 0.f; // q.a or k.h, this part's channels
+            F2 dot2 = both(0.f); // q.a or k.h, this part's channels
 #pragma unroll
             for (int p = 0; p < HC; p += 16) {
                 float t[16];
@@ -395,22 +399,27 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; e += 8) {
-                    float u[8];
+                    F2 u[4];
                     kq_row(rr ^ 64, p + e, u); // rows of a meet Q (tile rows 64 ..), rows of h meet K
 #pragma unroll
-                    for (int m2 = 0; m2 < 8; ++m2) {
-                        x[p + e + m2] += t[e + m2];
-                        dot = fmaf(u[m2], x[p + e + m2], dot);
+                    for (int m2 = 0; m2 < 8; m2 += 2) {
+                        float *xe = x + p + e + m2;
+                        const F2 r = pack(xe[0], xe[1]) + pack(t[e + m2], t[e + m2 + 1]);
+                        dot2 = fma2(u[m2 / 2], r, dot2);
+                        const float2 d = unpack(r);
+                        xe[0] = d.x;
+                        xe[1] = d.y;
                     }
                 }
             }
+            const float dot = sum(dot2);
             if (rr < C)
                 r_qa[part * C + i] = dot * rq;
             else
                 r_kh[part * C + i] = dot * rk;
         }
         if (rr >= C) { // -beta h, and w's part of the lo terms
-            float dot = 0.f;
+            F2 dot2 = both(0.f);
 #pragma unroll
             for (int p = 0; p < HC; p += 16) {
                 float t[16];
@@ -418,12 +427,15 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; e += 8) {
-                    float u[8];
+                    F2 u[4];
                     kq_row(i, p + e, u);
 #pragma unroll
-                    for (int m2 = 0; m2 < 8; ++m2) {
-                        dot = fmaf(u[m2], t[e + m2], dot);
-                        t[e + m2] = fmaf(-be, x[p + e + m2], t[e + m2]);
+                    for (int m2 = 0; m2 < 8; m2 += 2) {
+                        const F2 r = pack(t[e + m2], t[e + m2 + 1]);
+                        dot2 = fma2(u[m2 / 2], r, dot2);
+                        const float2 d = unpack(fma2(both(-be), pack(x[p + e + m2], x[p + e + m2 + 1]), r));
+                        t[e + m2] = d.x;
+                        t[e + m2 + 1] = d.y;
                     }
                 }
 #pragma unroll
@@ -436,7 +448,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                     acck[((p + e) / 4) * C] = r;
                 }
             }
-            r_kl[part * C + i] = dot * rk;
+            r_kl[part * C + i] = sum(dot2) * rk;
         } else {
 #pragma unroll
             for (int p = 0; p < HC; p += 4) {
@@ -450,8 +462,8 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
         }
         __syncthreads();
         if (rr < C) {
-            const float ec = tok[kEC + i];
-            float dot = 0.f;
+            const F2 ec = both(tok[kEC + i]);
+            F2 dot2 = both(0.f);
 #pragma unroll
             for (int p = 0; p < HC; p += 16) {
                 float t[16], u1[16];
@@ -460,12 +472,15 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; e += 8) {
-                    float u[8];
+                    F2 u[4];
                     kq_row(i, p + e, u);
 #pragma unroll
-                    for (int m2 = 0; m2 < 8; ++m2) {
-                        t[e + m2] = fmaf(ec, t[e + m2], u1[e + m2]);
-                        dot = fmaf(u[m2], t[e + m2], dot);
+                    for (int m2 = 0; m2 < 8; m2 += 2) {
+                        const F2 r = fma2(ec, pack(t[e + m2], t[e + m2 + 1]), pack(u1[e + m2], u1[e + m2 + 1]));
+                        dot2 = fma2(u[m2 / 2], r, dot2);
+                        const float2 d = unpack(r);
+                        t[e + m2] = d.x;
+                        t[e + m2 + 1] = d.y;
                     }
                 }
 #pragma unroll
@@ -474,7 +489,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                     acck[((p + e) / 4) * C] = make_float4(t[e] + s.x, t[e + 1] + s.y, t[e + 2] + s.z, t[e + 3] + s.w);
                 }
             }
-            r_kw[part * C + i] = dot * rk;
+            r_kw[part * C + i] = sum(dot2) * rk;
         }
         tc_fence_before();
         __syncthreads();

@@ -77,6 +77,14 @@ FW_DEV void widen8(uint4 u, float (&o)[8]) {
     }
 }
 
+FW_DEV void widen8(uint4 u, F2 (&o)[4]) {
+    float x[8];
+    widen8(u, x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        o[e] = pack(x[2 * e], x[2 * e + 1]);
+}
+
 // A "pair tile": rows of 128 bytes, 32 channels' hi terms then their lo terms,
 // swizzled as the descriptors of fw_tc.cuh expect.  16-byte chunk c of a row.
 FW_DEV uint32_t pair_chunk(int row, int c) { return (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)); }
