@@ -22,13 +22,13 @@
 //
 // What bounds it: for d_k > 64 one CTA an SM (tensor memory, shared memory),
 // and a head's 224 KB (d 128) come in four slices of which two fit.  B8 H16
-// L2048, two value heads a key head: 346 us, 2.7 TB/s; a head takes 21 000
-// cycles: 10 700 of slices (their copies), 1 100 for the last product, 3 700
-// for E and F, 1 500 for the second products, 3 700 for the sums.  It took
+// L2048, two value heads a key head: 324 us, 3.4 TB/s; a head takes 19 700
+// cycles: 10 300 of slices (their copies), 1 100 for the last product, 2 600
+// for E and F, 1 500 for the second products, 3 600 for the sums.  It took
 // 28 600 when the next slice was asked for after a product had been issued
 // instead of when its place was free, the next head's after the sums, and dY
 // and V came through registers (375 us); 23 300 with the products issued by a
-// warp that shared in the work on the slices.
+// warp that shared in the work on the slices; 21 000 without pairs of floats.
 #include "fw_gated.h"
 #include "fw_gated_tc.h"
 #include "fw_gated_tiles.cuh"
@@ -434,18 +434,9 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                         const F2 r = pack(t[e + m2], t[e + m2 + 1]);
                         dot2 = fma2(u[m2 / 2], r, dot2);
                         const float2 d = unpack(fma2(both(-be), pack(x[p + e + m2], x[p + e + m2 + 1]), r));
-                        t[e + m2] = d.x;
-                        t[e + m2 + 1] = d.y;
+                        x[p + e + m2] = d.x;
+                        x[p + e + m2 + 1] = d.y;
                     }
-                }
-#pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    float4 r = make_float4(t[e], t[e + 1], t[e + 2], t[e + 3]);
-                    if (m > 0) {
-                        const float4 s = acck[((p + e) / 4) * C];
-                        r = make_float4(r.x + s.x, r.y + s.y, r.z + s.z, r.w + s.w);
-                    }
-                    acck[((p + e) / 4) * C] = r;
                 }
             }
             r_kl[part * C + i] = sum(dot2) * rk;
@@ -459,9 +450,6 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                 }
                 accq[(p / 4) * C] = t;
             }
-        }
-        __syncthreads();
-        if (rr < C) {
             const F2 ec = both(tok[kEC + i]);
             F2 dot2 = both(0.f);
 #pragma unroll
@@ -485,8 +473,12 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                 }
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
-                    const float4 s = acck[((p + e) / 4) * C]; // (the row's other thread left its part)
-                    acck[((p + e) / 4) * C] = make_float4(t[e] + s.x, t[e + 1] + s.y, t[e + 2] + s.z, t[e + 3] + s.w);
+                    float4 r = make_float4(t[e], t[e + 1], t[e + 2], t[e + 3]);
+                    if (m > 0) {
+                        const float4 s = acck[((p + e) / 4) * C];
+                        r = make_float4(r.x + s.x, r.y + s.y, r.z + s.z, r.w + s.w);
+                    }
+                    acck[((p + e) / 4) * C] = r;
                 }
             }
             r_kw[part * C + i] = sum(dot2) * rk;
@@ -494,6 +486,13 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
+        if (rr >= C) { // the row's other thread has left its part
+#pragma unroll
+            for (int p = 0; p < HC; p += 4) {
+                const float4 s = acck[(p / 4) * C];
+                acck[(p / 4) * C] = make_float4(s.x + x[p], s.y + x[p + 1], s.z + x[p + 2], s.w + x[p + 3]);
+            }
+        }
         if (w == BOSS) { // dg: the sums over later tokens, two a lane; dbeta
             float G2[2];
 #pragma unroll
