@@ -56,7 +56,8 @@ FW_DEV uint64_t at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); 
 // then dY's, later), per-token scalars.  What a product leaves goes out by
 // warps: 32 rows are staged as 4 KB that lie together in the record too, and
 // one lane sends them (stored from registers, a row per lane, every 16 bytes
-// cost a sector: 317 us for 4096 chunks of d 128 where this took 249).
+// cost a sector: 317 us for 4096 chunks of d 128 where this took 249, and takes
+// 225 with V requested ahead and the decays on pairs of floats).
 struct PrepSmem {
     uint32_t kq, op, at, tt, tok, bar, bytes;
 };
@@ -577,7 +578,8 @@ __global__ void __launch_bounds__(NT, 2)
 // TP: with one tile a CTA the chain of a chunk is shortest; two tiles read the
 // records half as often, which is what counts once there are more CTAs than
 // SMs (the backward at B8 H16 L2048, 1024 CTAs with one tile: 955 us with one
-// tile, its walks 341, at 9 TB/s out of L2; 893 with two).
+// tile, its walks 341, at 9 TB/s out of L2; 893 with two; 742 - 762 with the
+// faster preparation and gradients of now).
 enum { kFwd = 0, kKeep = 1, kRev = 2 };
 constexpr int walk_threads(int TP) { return NT * TP + 64; }
 
@@ -941,7 +943,8 @@ cudaError_t launch_prep(const GatedArgs &a, const void *q, const void *k, const 
 // of waves of preparing CTAs (two an SM) and at least kMinSegment chunks, since
 // each costs the walk a start.  (16 heads, 16 381 tokens, d 128: 624 us in
 // one piece, 506 in segments of 22 chunks, 742 in segments of 11; B2 H8 L2048,
-// d_v 64: 85 us in one piece, 77 in two of 16.)
+// d_v 64: 85 us in one piece, 77 in two of 16.  With a faster preparation the
+// two take 466 and 72 us.)
 constexpr int kMinSegment = 12;
 int segment_chunks(const GatedArgs &a, const GatedRecord &rec, int num_sms) {
     const int64_t heads = (int64_t)a.B * a.H, walkers = heads * rec.ns;

@@ -457,7 +457,10 @@ FW_API int fw_decode_stack_step(const fw_stack_layer *layers, int n_layers, cons
  *   d_k in {16, 32, 64, 128}; d_v a multiple of 16 up to 256; B H <= 65535.
  * With bf16 I/O an fp32 operand of a tensor-core product is two bf16 terms
  * (2^-16 of it is left at most) and sums and the state are fp32; an infinity
- * among them becomes NaN.  With fp32 I/O everything is fp32.
+ * among them becomes NaN.  With fp32 I/O everything is fp32.  The sequence
+ * calls go by chunks of 64 tokens: a NaN or an infinity in a token's inputs
+ * may reach the answers and gradients of every token of its chunk, and of all
+ * that the state carries it to (a padded token's values reach nothing).
  * Calls return FW_ERR_INVALID_ARG for null, misaligned or missing pointers,
  * bad sizes, a scale or eps that is not finite, eps < 0 or a small workspace,
  * and FW_ERR_UNSUPPORTED for sizes outside the compiled set.  No call uses
