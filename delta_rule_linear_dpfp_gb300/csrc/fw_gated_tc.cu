@@ -45,6 +45,24 @@ constexpr int NV = 32;    // value channels per walk CTA
 // eight different bank groups.
 FW_DEV uint32_t piece_chunk(int row, int c) { return (uint32_t)(row * 64 + ((c ^ ((row >> 1) & 3)) << 4)); }
 
+// On pairs of floats: v + o, f v.
+template <int N> FW_DEV void add_to(float *v, const float *o) {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+        const float2 d = unpack(pack(v[e], v[e + 1]) + pack(o[e], o[e + 1]));
+        v[e] = d.x;
+        v[e + 1] = d.y;
+    }
+}
+template <int N> FW_DEV void scaled(float *to, float f, const float *v) {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+        const float2 d = unpack(both(f) * pack(v[e], v[e + 1]));
+        to[e] = d.x;
+        to[e + 1] = d.y;
+    }
+}
+
 // A descriptor `bytes` further into its tile.
 FW_DEV uint64_t at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
 
@@ -770,9 +788,7 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
                 tmem_ld16(t + lb + 32u, t1);
             tmem_ld_wait();
             if (c8 == 0) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    t0[e] += t1[e];
+                add_to<16>(t0, t1);
                 give[0] = make_float4(t0[8], t0[9], t0[10], t0[11]);
                 give[32] = make_float4(t0[12], t0[13], t0[14], t0[15]);
             } else {
@@ -782,16 +798,11 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
                 for (int e = 0; e < 8; ++e)
                     t0[e] = t0[8 + e];
             }
+            add_to<8>(v, t0);
             meet();
             const float4 p = take[0], q = take[32];
-            v[0] += t0[0] + p.x;
-            v[1] += t0[1] + p.y;
-            v[2] += t0[2] + p.z;
-            v[3] += t0[3] + p.w;
-            v[4] += t0[4] + q.x;
-            v[5] += t0[5] + q.y;
-            v[6] += t0[6] + q.z;
-            v[7] += t0[7] + q.w;
+            const float o8[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+            add_to<8>(v, o8);
         };
         auto base8 = [&](const uint8_t *r, int row, float (&v)[8]) {
 #pragma unroll
@@ -830,9 +841,7 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
                 const float fy = scal[C + i];
                 widen8(ahead[0], reinterpret_cast<float(&)[8]>(t0[0]));
                 widen8(ahead[1], reinterpret_cast<float(&)[8]>(t0[8]));
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    t0[e] *= fy;
+                scaled<16>(t0, fy, t0);
                 put8(ut_, C + i, 2 * h2, t0);
                 put8(ut_, C + i, 2 * h2 + 1, t0 + 8);
                 if (it + 2 < nch)
@@ -845,9 +854,7 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
             wait(m1, it & 1);
             tc_fence_after();
             product(tU, place, x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                t0[e] = f * x[e];
+            scaled<8>(t0, f, x);
             put8(ut_, i, 2 * h2 + c8, t0);
             written(ur);
             if (MODE == kFwd) {
@@ -865,9 +872,13 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
                 tmem_ld16(tZ + lb, t0);
                 tmem_ld16(tZ + lb + 32u, t1);
                 tmem_ld_wait();
+                add_to<16>(t0, t1);
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    z[e] = fmaf(whole, z[e], t0[e] + t1[e]);
+                for (int e = 0; e < 16; e += 2) {
+                    const float2 d = unpack(fma2(both(whole), pack(z[e], z[e + 1]), pack(t0[e], t0[e + 1])));
+                    z[e] = d.x;
+                    z[e + 1] = d.y;
+                }
                 put8(zt_, rr, 2 * h2, z);
                 put8(zt_, rr, 2 * h2 + 1, z + 8);
             }
@@ -943,8 +954,8 @@ cudaError_t launch_prep(const GatedArgs &a, const void *q, const void *k, const 
 // of waves of preparing CTAs (two an SM) and at least kMinSegment chunks, since
 // each costs the walk a start.  (16 heads, 16 381 tokens, d 128: 624 us in
 // one piece, 506 in segments of 22 chunks, 742 in segments of 11; B2 H8 L2048,
-// d_v 64: 85 us in one piece, 77 in two of 16.  With a faster preparation the
-// two take 466 and 72 us.)
+// d_v 64: 85 us in one piece, 77 in two of 16.  With a faster preparation and
+// pairs of floats the two take 461 and 71 us.)
 constexpr int kMinSegment = 12;
 int segment_chunks(const GatedArgs &a, const GatedRecord &rec, int num_sms) {
     const int64_t heads = (int64_t)a.B * a.H, walkers = heads * rec.ns;
