@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(NT, 2)
 // TP: with one tile a CTA the chain of a chunk is shortest; two tiles read the
 // records half as often, which is what counts once there are more CTAs than
 // SMs (the backward at B8 H16 L2048, 1024 CTAs with one tile: 955 us with one
-// tile, its walks 341, at 9 TB/s out of L2; 893 with two; 742 - 762 with the
+// tile, its walks 341, at 9 TB/s out of L2; 893 with two; 759 with the
 // faster preparation and gradients of now).
 enum { kFwd = 0, kKeep = 1, kRev = 2 };
 constexpr int walk_threads(int TP) { return NT * TP + 64; }
