@@ -592,6 +592,7 @@ __global__ void __launch_bounds__(NT, 2)
 // as the product that last read its place is done, so that none of that is on
 // a worker's path.  Workers tell them by two mbarriers that the state's or
 // the values' tile is written; commits tell workers that a product is done.
+// (tests/test_gated_walk_order.py goes through every order of these steps.)
 //
 // TP: with one tile a CTA the chain of a chunk is shortest; two tiles read the
 // records half as often, which is what counts once there are more CTAs than
@@ -638,8 +639,11 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
     if (tid == 32) {
         for (int e = 0; e < 7; ++e)
             mbar_init(fullA + e, 1);
-        mbar_init(zr, WORKERS);
-        mbar_init(ur, WORKERS + (MODE == kFwd ? 0 : 1)); // the state's copy has left its tile, too
+        // A wait knows a phase by its parity, so each role that waits has to
+        // have seen one phase before the next but one can end: the copies' warp
+        // arrives, too, on one of the two barriers that every chunk passes.
+        mbar_init(zr, WORKERS + (MODE == kFwd ? 1 : 0));
+        mbar_init(ur, WORKERS + (MODE == kFwd ? 0 : 1)); // the state's copy has left its tile
         fence_barrier_init();
     }
     tc_fence_before();
@@ -715,6 +719,8 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
                 bulk_g2s(sm + L::scal + (it & 1) * L::SCAL, src + (MODE == kRev ? rec.scalR : rec.scalF), L::SCAL, f);
                 bulk_g2s(dst + L::base, src + (MODE == kRev ? rec.base2 : rec.base) + (size_t)sl * TP * L::RV * 128, base, f);
             };
+            if (MODE == kFwd)
+                mbar_arrive(zr);
             for (int it = 0; it < min(2, nch); ++it) {
                 fetch_a(it);
                 fetch_b(it);
@@ -739,6 +745,8 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
                 wait(ur, it & 1); // (they have seen the values' product)
                 if (ok && it + 2 < nch)
                     fetch_a(it + 2);
+                if (MODE == kFwd)
+                    mbar_arrive(zr);
             }
             if (MODE != kFwd)
                 bulk_wait_all();
