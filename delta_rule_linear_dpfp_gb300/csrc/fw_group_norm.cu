@@ -286,7 +286,9 @@ __global__ void __launch_bounds__(kT, 2)
             const bool mine = here[u];
             const int64_t o = to[u], i = from[u];
             request(u);
-            const float r = centre<LPR>(n, mine, inv_d, a.eps);
+            // (a row that is not there has no deviation: with eps 0 its r is infinite, and
+            // 0 times that would be in the sums over the rows)
+            const float r1 = centre<LPR>(n, mine, inv_d, a.eps), r = mine ? r1 : 0.f;
             F2 s1 = {0}, s2 = {0};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {

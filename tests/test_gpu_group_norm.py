@@ -177,3 +177,45 @@ def test_a_layer_end_to_end():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(again[4], out) and torch.equal(again[3], W)
+
+
+def sizes_of_terms(x, gamma, beta, z, do, act, eps):
+    """Per channel, the sums of |dz| (|n| + 1) over the tokens: what dgamma and dbeta add up."""
+    x, gamma, beta, z, do = (None if t is None else f64(t) for t in (x, gamma, beta, z, do))
+    B, H, L, d = x.shape
+    c = x - x.mean(-1, keepdims=True)
+    n = (c / np.sqrt((c * c).mean(-1, keepdims=True) + eps)).transpose(0, 2, 1, 3)
+    f, df = gated._act(n * gamma.reshape(H, d) + beta.reshape(H, d) if z is None else z.reshape(B, L, H, d), act)
+    dz = do.reshape(B, L, H, d) * (df if z is None else f)
+    return (np.abs(dz) * (np.abs(n) + 1)).sum((0, 1)).reshape(-1)
+
+
+# dgamma and dbeta: a term is off by 2^-19 of |dz| (|n| + 1) (the mean's 13 2^-24 of twice the deviation,
+# the root, the activation), and goes through at most 300 additions of 2^-24 each: 2^-15 of the terms' sizes.
+TERMS = 2.0 ** -15
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1, 8), (1, 2, 63, 32), (1, 2, 64, 32), (1, 2, 65, 32), (1, 2, 129, 32), (2, 3, 130, 48),
+                                   (3, 2, 70, 256), (5, 1, 700, 128)], ids=str)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("act, gate", [("none", False), ("silu", False), ("gelu", False), ("silu", True)])
+def test_without_eps(shape, dtype, act, gate):
+    """eps 0: rows past the last one have no deviation and no part in the sums over the rows."""
+    x, gamma, beta, z, do = make(*shape, dtype, gate, sum(shape))
+    dv = lambda t: None if t is None else t.cuda()  # noqa: E731
+    kw = dict(act=act, gate=dv(z), eps=0.0)
+    out = fw.fw_group_norm_act(dv(x), dv(gamma), dv(beta), **kw)
+    dx, dgate, dgamma, dbeta = fw.fw_group_norm_act_backward(dv(x), dv(gamma), dv(beta), dv(do), **kw)
+    o = [None if t is None else f64(t) for t in (x, gamma, beta, z)]
+    ref = gated.group_norm_act(*o, act, eps=0.0)
+    rx, rz, rg, rb = gated.group_norm_act(*o, act, eps=0.0, dout=f64(do))
+    tol = 2.0 ** -18 + 2.0 ** -24 * 64
+    near("out", out, ref, np.abs(ref).max() + 1, tol)
+    # dx of a row is of the size of what goes into it, over the row's deviation
+    c = o[0] - o[0].mean(-1, keepdims=True)
+    near("dx", dx, rx, np.abs(f64(do)).max() * np.abs(o[1]).max() * 4 / np.sqrt((c * c).mean(-1, keepdims=True)), 8 * tol)
+    if gate:
+        near("dgate", dgate, rz, np.abs(rz).max() + 1, 4 * tol)
+    big = sizes_of_terms(x, gamma, beta, z, do, act, 0.0)
+    near("dgamma", dgamma, rg, big, TERMS)
+    near("dbeta", dbeta, rb, big, TERMS)
