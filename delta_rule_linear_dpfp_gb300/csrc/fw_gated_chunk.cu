@@ -896,7 +896,7 @@ cudaError_t launch_gated_backward(const GatedArgs &a, const void *q, const void 
                                   cudaStream_t st) {
     if (bf16) {
         const cudaError_t e = gated_tc_walks(a, q, k, v, g, beta, W0, dy, dWf, dW0, workspace, st);
-        return e != cudaSuccess ? e : gated_tc_grad(a, q, k, v, dy, dq, dk, dv, dg, dbeta, workspace, st);
+        return e != cudaSuccess ? e : gated_tc_grad(a, v, dy, dq, dk, dv, dg, dbeta, workspace, st);
     }
     auto f = [](const void *p) { return static_cast<const float *>(p); };
     auto o = [](void *p) { return static_cast<float *>(p); };

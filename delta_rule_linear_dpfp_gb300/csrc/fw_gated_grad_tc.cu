@@ -96,10 +96,9 @@ __host__ __device__ inline GradSmem grad_smem(int nkb, bool alone) {
 
 template <int NKB>
 __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
-    gated_tc_grad_kernel(GatedArgs a, const bf *__restrict__ q, const bf *__restrict__ k, const bf *__restrict__ v,
-                         const bf *__restrict__ dy, bf *__restrict__ dq, bf *__restrict__ dk, bf *__restrict__ dv,
-                         bf *__restrict__ dg, bf *__restrict__ dbeta, const uint8_t *ws, GatedRecord rec,
-                         unsigned *status) {
+    gated_tc_grad_kernel(GatedArgs a, const bf *__restrict__ v, const bf *__restrict__ dy, bf *__restrict__ dq,
+                         bf *__restrict__ dk, bf *__restrict__ dv, bf *__restrict__ dg, bf *__restrict__ dbeta,
+                         const uint8_t *ws, GatedRecord rec, unsigned *status) {
     constexpr int PARTS = parts_of(NKB), NT = 128 * PARTS;
     constexpr int DKP = 64 * NKB, HC = DKP / PARTS; // channels per thread of a row
     constexpr uint32_t kCols = 256 * NKB;               // TMEM: three products of DKP columns, one of 64
@@ -590,31 +589,30 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
 }
 
 template <int NKB>
-cudaError_t launch(const GatedArgs &a, const void *q, const void *k, const void *v, const void *dy, void *dq, void *dk,
-                   void *dv, void *dg, void *dbeta, const void *ws, const GatedRecord &rec, unsigned *status,
-                   cudaStream_t st) {
+cudaError_t launch(const GatedArgs &a, const void *v, const void *dy, void *dq, void *dk, void *dv, void *dg,
+                   void *dbeta, const void *ws, const GatedRecord &rec, unsigned *status, cudaStream_t st) {
     auto *kern = gated_tc_grad_kernel<NKB>;
     const uint32_t smem = grad_smem(NKB, a.H == a.Hk).bytes;
     static std::atomic<uint64_t> allowed{0};
     const cudaError_t e = allow_smem(kern, allowed);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(kern, dim3(rec.nch, a.B * a.Hk), dim3(128 * parts_of(NKB)), smem, st, a, (const bf *)q, (const bf *)k,
-                      (const bf *)v, (const bf *)dy, (bf *)dq, (bf *)dk, (bf *)dv, (bf *)dg, (bf *)dbeta,
-                      (const uint8_t *)ws, rec, status);
+    return launch_pdl(kern, dim3(rec.nch, a.B * a.Hk), dim3(128 * parts_of(NKB)), smem, st, a, (const bf *)v,
+                      (const bf *)dy, (bf *)dq, (bf *)dk, (bf *)dv, (bf *)dg, (bf *)dbeta, (const uint8_t *)ws, rec,
+                      status);
 }
 
 } // namespace
 
-cudaError_t gated_tc_grad(const GatedArgs &a, const void *q, const void *k, const void *v, const void *dy, void *dq,
-                          void *dk, void *dv, void *dg, void *dbeta, const void *ws, cudaStream_t st) {
+cudaError_t gated_tc_grad(const GatedArgs &a, const void *v, const void *dy, void *dq, void *dk, void *dv, void *dg,
+                          void *dbeta, const void *ws, cudaStream_t st) {
     unsigned *status = nullptr;
     cudaError_t e = status_word(&status);
     if (e != cudaSuccess)
         return e;
     const GatedRecord rec = gated_backward_record(a.L, a.d_k, a.d_v);
-    return rec.nkb == 1 ? launch<1>(a, q, k, v, dy, dq, dk, dv, dg, dbeta, ws, rec, status, st)
-                        : launch<2>(a, q, k, v, dy, dq, dk, dv, dg, dbeta, ws, rec, status, st);
+    return rec.nkb == 1 ? launch<1>(a, v, dy, dq, dk, dv, dg, dbeta, ws, rec, status, st)
+                        : launch<2>(a, v, dy, dq, dk, dv, dg, dbeta, ws, rec, status, st);
 }
 
 } // namespace fw

@@ -62,8 +62,9 @@ cudaError_t gated_tc_forward(const GatedArgs &a, const void *q, const void *k, c
 cudaError_t gated_tc_walks(const GatedArgs &a, const void *q, const void *k, const void *v, const void *g,
                            const void *beta, const float *W0, const void *dy, const float *dWf, float *dW0, void *ws,
                            cudaStream_t st);
-// The gradients of the tokens from what gated_tc_walks left.
-cudaError_t gated_tc_grad(const GatedArgs &a, const void *q, const void *k, const void *v, const void *dy, void *dq,
-                          void *dk, void *dv, void *dg, void *dbeta, const void *ws, cudaStream_t st);
+// The gradients of the tokens from what gated_tc_walks left (the keys and
+// queries are in the records).
+cudaError_t gated_tc_grad(const GatedArgs &a, const void *v, const void *dy, void *dq, void *dk, void *dv, void *dg,
+                          void *dbeta, const void *ws, cudaStream_t st);
 
 } // namespace fw
