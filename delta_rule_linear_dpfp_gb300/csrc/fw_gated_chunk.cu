@@ -229,6 +229,10 @@ __global__ void __launch_bounds__(NT)
     const int b = bh / a.H, h = bh % a.H, kh = b * a.Hk + h / (a.H / a.Hk);
     griddep_launch_dependents();
     griddep_wait();
+    q = after_wait(q);
+    k = after_wait(k);
+    g = after_wait(g);
+    beta = after_wait(beta);
     const int n = min(C, seq_len(a, b) - c * C);
     if (n <= 0)
         return;
@@ -365,6 +369,10 @@ __global__ void __launch_bounds__(NT)
     const int nv = min(NV, a.d_v - n0);
     griddep_launch_dependents();
     griddep_wait();
+    q = after_wait(q);
+    k = after_wait(k);
+    v = after_wait(v);
+    W0 = after_wait(W0);
     const int len = seq_len(a, b), nch = (len + C - 1) / C;
     const size_t st0 = ((size_t)bh * a.d_v + n0) * a.d_k;
     auto fetch = [&](int c) {
@@ -491,6 +499,10 @@ __global__ void __launch_bounds__(NT)
     const int nv = min(NV, a.d_v - n0);
     griddep_launch_dependents();
     griddep_wait();
+    q = after_wait(q);
+    k = after_wait(k);
+    dy = after_wait(dy);
+    dWf = after_wait(dWf);
     const int len = seq_len(a, b), nch = (len + C - 1) / C;
     const size_t st0 = ((size_t)bh * a.d_v + n0) * a.d_k;
     auto fetch = [&](int c) {
@@ -587,6 +599,10 @@ __global__ void __launch_bounds__(NT)
     const bool on = kc < a.d_k;
     griddep_launch_dependents();
     griddep_wait();
+    q = after_wait(q);
+    k = after_wait(k);
+    v = after_wait(v);
+    dy = after_wait(dy);
     const int n = min(C, seq_len(a, b) - c * C);
     const size_t krow = ((size_t)bk * a.L + (size_t)c * C) * a.d_k;
     const int rows = min(C, a.L - c * C); // rows that exist in memory

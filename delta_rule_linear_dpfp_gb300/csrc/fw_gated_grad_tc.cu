@@ -120,6 +120,8 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
     constexpr int BOSS = NKB == 2 ? 15 : 0;
     const bool boss = tid == 32 * BOSS;
     griddep_wait();
+    v = after_wait(v);
+    dy = after_wait(dy);
     const int n = min(C, seq_len(a, b) - c * C), rows = min(C, a.L - c * C); // tokens; rows in memory
     const size_t krow = ((size_t)bk * a.L + (size_t)c * C) * a.d_k;
     if (n <= 0) { // behind the sequence's end: no gradient

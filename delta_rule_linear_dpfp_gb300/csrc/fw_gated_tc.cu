@@ -118,6 +118,12 @@ __global__ void __launch_bounds__(NT, 2)
     const bool last = blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1;
     if (!beside)
         griddep_wait();
+    q = after_wait(q);
+    k = after_wait(k);
+    v = after_wait(v);
+    g = after_wait(g);
+    beta = after_wait(beta);
+    dy = after_wait(dy);
     const int n = min(C, seq_len(a, b) - c * C);
     if (n <= 0) {
         griddep_launch_dependents();
@@ -631,6 +637,8 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, sl = blockIdx.x, bh = blockIdx.y, n0 = sl * TP * NV;
     const int b = bh / a.H;
     griddep_wait();
+    dy = after_wait(dy);
+    Z0 = after_wait(Z0);
     const int len = seq_len(a, b), nch = max(0, min(c1, (len + C - 1) / C) - c0); // of chunks c0 .. c1 - 1
     if (w == 0) {
         tmem_alloc(slot, L::cols);

@@ -12,8 +12,9 @@ constexpr int kGatedThreads = 256;          // per CTA of the preparing kernels
 constexpr int kGatedLd = kGatedChunk + 4;   // row stride of an fp32 chunk x chunk tile
 constexpr float kGMin = -200.f; // e^g is 0 in fp32 below this: a gate of -inf is a sum that stays finite
 
+// (called after griddep_wait)
 FW_DEV int seq_len(const GatedArgs &a, int b) {
-    return a.lengths ? min(max(__ldcg(a.lengths + b), 0), a.L) : a.L;
+    return a.lengths ? min(max(__ldcg(after_wait(a.lengths) + b), 0), a.L) : a.L;
 }
 
 // Sums kept as an unevaluated pair of floats (hi + lo, 48 bits).

@@ -191,6 +191,8 @@ __global__ void __launch_bounds__(kT, 3)
     griddep_wait();
     x = after_wait(x);
     gate = after_wait(gate);
+    gamma = after_wait(gamma);
+    beta = after_wait(beta);
     F2 ga[4] = {}, be[4] = {};
     if (on) {
         load_pairs(gamma + h * a.d + c0, ga);
@@ -251,6 +253,8 @@ __global__ void __launch_bounds__(kT, 2)
     griddep_wait();
     x = after_wait(x);
     gate = after_wait(gate);
+    gamma = after_wait(gamma);
+    beta = after_wait(beta);
     dout = after_wait(dout);
     F2 ga[4] = {}, be[4] = {}, dga[4] = {}, dbe[4] = {};
     if (on) {
