@@ -417,3 +417,172 @@ def test_lengths_are_refused_unaligned():
     lens = torch.full((4,), 5, dtype=torch.int32, device="cuda")[1:]
     with pytest.raises(fw.FwError):
         fw.fw_gated_delta_forward(**d, lengths=lens)
+
+
+# ---- a forward in several segments: preparation beside the walk over the segment before
+
+def segments(B, H, L, d_v):
+    """How many segments the forward takes (the rule of csrc/fw_gated_tc.cu)."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    chunks, heads = -(-L // 64), B * H
+    walkers = heads * -(-d_v // 32)
+    if 2 * walkers > sms:
+        return 1
+    wave = max(1, 2 * (sms - walkers) // heads)
+    seg = -(-12 // wave) * wave
+    n = (chunks + seg // 2) // seg
+    return 1 if n < 2 else -(-chunks // -(-chunks // n))
+
+
+# B, Hk, H, L, d_k, d_v
+LONG = [(3, 3, 6, 2301, 64, 48), (2, 8, 8, 3800, 128, 64), (1, 8, 16, 4500, 128, 128)]
+
+
+def by_parts(d, lens, chunks=8):
+    """The same sequence in calls of a few chunks each, which take one segment each."""
+    L, W, ys = d["v"].shape[2], d["W0"], []
+    for t in range(0, L, 64 * chunks):
+        part = {n: x[:, :, t:t + 64 * chunks].contiguous() for n, x in d.items() if n != "W0"}
+        left = None if lens is None else (lens - t).clamp(min=0).to(torch.int32)
+        y, W = fw.fw_gated_delta_forward(**part, W0=W, lengths=left)
+        ys.append(y)
+    return torch.cat(ys, 2), W
+
+
+@pytest.mark.parametrize("case", LONG, ids=str)
+@pytest.mark.parametrize("ends", [None, 0.2, 0.5, 0.9, 0.0], ids=str)
+def test_segments_are_the_parts(case, ends):
+    """One call in three segments and more has the bits of its parts, called one
+    by one: sequences that end in the first, a middle, the last segment, or
+    before any; every repeat as well, and the state in place."""
+    B, Hk, H, L, d_k, d_v = case
+    assert segments(B, H, L, d_v) >= 3
+    d = dev(make(B, Hk, H, L, d_k, d_v, torch.bfloat16, True, 21))
+    lens = None
+    if ends is not None:
+        lens = torch.full((B,), int(ends * L), dtype=torch.int32, device="cuda")
+        lens[-1] = L - 3 if B > 1 else lens[-1]
+    y, W = by_parts(d, lens)
+    for _ in range(3):
+        y1, W1 = fw.fw_gated_delta_forward(**d, lengths=lens)
+        assert torch.equal(y, y1) and torch.equal(W, W1)
+    same = d["W0"].clone()
+    y1, _ = fw.fw_gated_delta_forward(**{**d, "W0": same}, W_final=same, lengths=lens)
+    assert torch.equal(y, y1) and torch.equal(W, same)
+
+
+def test_segments_against_the_oracle():
+    B, Hk, H, L, d_k, d_v = LONG[0]
+    d = make(B, Hk, H, L, d_k, d_v, torch.bfloat16, True, 22)
+    y, W = fw.fw_gated_delta_forward(**dev(d))
+    yr, Wr = gated.gated_forward(**host(d))
+    near("y", y, yr)
+    near("W", W, Wr, bf16=True)
+
+
+@pytest.mark.parametrize("case", LONG, ids=str)
+def test_segments_in_graphs_and_on_streams(case):
+    """Captured and replayed on new inputs, a workspace of one call reused by the
+    next, and two calls at once on two streams."""
+    B, Hk, H, L, d_k, d_v = case
+    ds = [dev(make(B, Hk, H, L, d_k, d_v, torch.bfloat16, True, s)) for s in (23, 24)]
+    want = [by_parts(d, None) for d in ds]
+    x = {n: t.clone() for n, t in ds[0].items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = fw.fw_gated_delta_forward(**x)
+    for i in (0, 1, 1, 0):
+        for n in x:
+            x[n].copy_(ds[i][n])
+        graph.replay()
+        graph.replay()                                    # (at once behind the first, in the same workspace)
+        assert all(torch.equal(a, b) for a, b in zip(got, want[i]))
+    ws = torch.empty(fw.fw_gated_delta_forward_workspace_size(B, Hk, H, L, d_k, d_v, torch.bfloat16), dtype=torch.uint8,
+                     device="cuda")
+    outs = [fw.fw_gated_delta_forward(**ds[i & 1], workspace=ws) for i in range(6)]
+    for i, out in enumerate(outs):
+        assert all(torch.equal(a, b) for a, b in zip(out, want[i & 1]))
+    streams, outs = [torch.cuda.Stream() for _ in ds], []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            outs.append((i, fw.fw_gated_delta_forward(**ds[i], stream=s)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for i, out in outs for a, b in zip(out, want[i]))
+
+
+def test_features_written_by_the_kernel_before():
+    """Keys and queries that fw_dpfp writes immediately before, into the same
+    buffers again and again, a long (segmented) call and gates and betas written by a copy: no
+    call sees what a buffer held before."""
+    B, H, L, d_key, d_v = 2, 4, 6400, 32, 32
+    assert segments(B, H, L, d_v) >= 2
+    r = torch.Generator(device="cuda").manual_seed(25)
+    raw = [torch.randn(2, B, H, L, d_key, generator=r, device="cuda").bfloat16() for _ in range(3)]
+    v = torch.randn(B, H, L, d_v, generator=r, device="cuda").bfloat16()
+    g = -torch.rand(3, B, H, L, generator=r, device="cuda").bfloat16()
+    be = torch.rand(3, B, H, L, generator=r, device="cuda").bfloat16()
+
+    def alone(i):
+        q, k = fw.fw_dpfp(raw[i][0]), fw.fw_dpfp(raw[i][1])
+        torch.cuda.synchronize()
+        out = fw.fw_gated_delta_forward(q, k, v, g[i].clone(), be[i].clone())
+        torch.cuda.synchronize()
+        return out
+
+    want = [alone(i) for i in range(3)]
+    q, k = (torch.empty(B, H, L, 2 * d_key, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    gi, bi = g[0].clone(), be[0].clone()
+    outs = []
+    for i in (0, 1, 2, 0, 2, 1):
+        gi.copy_(g[i])
+        bi.copy_(be[i])
+        fw.fw_dpfp(raw[i][0], out=q)
+        fw.fw_dpfp(raw[i][1], out=k)
+        outs.append((i, fw.fw_gated_delta_forward(q, k, v, gi, bi)))
+    assert all(torch.equal(a, b) for i, out in outs for a, b in zip(out, want[i]))
+
+
+# ---- how much the states keep
+
+def off_by(got, ref):
+    ref = np.asarray(ref)
+    return np.linalg.norm(f64(got) - ref) / np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("case", [(2, 2, 4, 640, 128, 96), (2, 4, 4, 500, 64, 64), (1, 1, 2, 900, 32, 128)], ids=str)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_states_keep_their_bits(case, dtype):
+    """The 2-norm of the states' errors.  bf16 tensors: a value in two bf16 terms
+    is off by 2^-18 of itself (root mean square: each term leaves 2^-9.3, the
+    dropped product of the second terms is as large); five operands of that kind
+    lie between the inputs and the state (T, M, W', S, U), their errors add in
+    squares, and the difference v - S k takes terms of up to sqrt(2) of its own
+    size: sqrt(5) sqrt(2) 2^-18 < 2^-16.  The gradient goes through as many
+    again: 2^-15.  fp32 tensors: six products of up to 128 terms, each off by
+    sqrt(128) 2^-25, the same difference: below 2^-19, and 2^-18 for the gradient."""
+    B, Hk, H, L, d_k, d_v = case
+    d = make(B, Hk, H, L, d_k, d_v, dtype, True, sum(case))
+    x, h = dev(d), host(d)
+    bits = 16 if dtype == torch.bfloat16 else 19
+    y, W = fw.fw_gated_delta_forward(**x, scale=0.5)
+    yr, Wr = gated.gated_forward(**h, scale=0.5)
+    assert off_by(W, Wr) <= 2.0 ** -bits
+    if dtype == torch.float32:
+        assert off_by(y, yr) <= 2.0 ** -19
+    else:
+        # An answer off by 2^-16 of the answers' size before its rounding goes to the other neighbour where the
+        # exact one lies that near the middle of two: for normal answers 2^-7 sqrt(2 / pi) (1 + ln 2^7) = 4 % at most.
+        there = torch.from_numpy(yr).float().bfloat16()
+        other = (y.cpu() != there).float().mean()
+        assert other <= 0.04, float(other)
+    r = torch.Generator().manual_seed(1)
+    dy, dW = torch.randn(B, H, L, d_v, generator=r).to(dtype), torch.randn(B, H, d_v, d_k, generator=r)
+    args = ("q", "k", "v", "g", "beta")
+    got = fw.fw_gated_delta_backward(*[x[n] for n in args], dy.cuda(), W0=x["W0"], dW_final=dW.cuda(), scale=0.5)
+    want = gated.gated_backward(*[h[n] for n in args], f64(dy), h["W0"], f64(dW), scale=0.5)
+    assert off_by(got[5], want[5]) <= 2.0 ** -(bits - 1)
+    if dtype == torch.float32:
+        for n, a, w in zip(("dq", "dk", "dv"), got, want):
+            assert off_by(a, w) <= 2.0 ** -18, n

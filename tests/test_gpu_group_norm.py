@@ -219,3 +219,37 @@ def test_without_eps(shape, dtype, act, gate):
     big = sizes_of_terms(x, gamma, beta, z, do, act, 0.0)
     near("dgamma", dgamma, rg, big, TERMS)
     near("dbeta", dbeta, rb, big, TERMS)
+
+
+@pytest.mark.parametrize("shape", [(4, 3, 3000, 32), (2, 5, 1111, 96), (1, 1, 9000, 8)], ids=str)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("act, gate", [("none", False), ("gelu", False), ("silu", True)])
+def test_parameters_by_the_terms(shape, dtype, act, gate):
+    x, gamma, beta, z, do = make(*shape, dtype, gate, sum(shape))
+    dv = lambda t: None if t is None else t.cuda()  # noqa: E731
+    _, _, dgamma, dbeta = fw.fw_group_norm_act_backward(dv(x), dv(gamma), dv(beta), dv(do), act=act, gate=dv(z))
+    o = [None if t is None else f64(t) for t in (x, gamma, beta, z)]
+    _, _, rg, rb = gated.group_norm_act(*o, act, dout=f64(do))
+    big = sizes_of_terms(x, gamma, beta, z, do, act, 1e-5)
+    near("dgamma", dgamma, rg, big, TERMS)
+    near("dbeta", dbeta, rb, big, TERMS)
+
+
+@pytest.mark.parametrize("row", [0, 63, 64, 2431, 2432, 2495, 4863, 4864, 4868])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_one_row_alone(row, dtype):
+    """Only one token has a gradient: the parameters' are its terms, once, and
+    no other row gets any (8 heads of 32 channels: 64 rows a CTA, 38 CTAs a head)."""
+    B, H, L, d = 1, 8, 4869, 32
+    x, gamma, beta, _, do = make(B, H, L, d, dtype, False, 11)
+    only = torch.zeros_like(do)
+    only[:, row] = do[:, row]
+    dx, _, dgamma, dbeta = fw.fw_group_norm_act_backward(x.cuda(), gamma.cuda(), beta.cuda(), only.cuda())
+    o = [f64(x), f64(gamma), f64(beta), None]
+    _, _, rg, rb = gated.group_norm_act(*o, "none", dout=f64(only))
+    big = sizes_of_terms(x, gamma, beta, None, only, "none", 1e-5)
+    near("dgamma", dgamma, rg, big, TERMS)
+    near("dbeta", dbeta, rb, big, TERMS)
+    assert torch.all(dx[:, :, row] != 0)
+    dx[:, :, row] = 0
+    assert torch.all(dx == 0)
