@@ -586,3 +586,92 @@ def test_states_keep_their_bits(case, dtype):
     if dtype == torch.float32:
         for n, a, w in zip(("dq", "dk", "dv"), got, want):
             assert off_by(a, w) <= 2.0 ** -18, n
+
+
+# ---- other calls that the documentation allows
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_decode_with_keys_as_given(dtype):
+    d = make(3, 2, 4, 4, 64, 48, dtype, True, 26, "positive")
+    x, W, ys = dev(d), d["W0"].cuda(), []
+    for t in range(4):
+        one = [x[n][:, :, t].contiguous() for n in ("q", "k", "v", "g", "beta")]
+        ys.append(fw.fw_gated_delta_decode_step(*one, W, l2norm=False, scale=-0.5))
+    yr, Wr = gated.gated_forward(**host(d), l2norm=False, scale=-0.5)
+    near("y", torch.stack(ys, 2), yr)
+    near("W", W, Wr, bf16=False)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("given", [(False, True), (True, False), (False, False)], ids=["dW", "W0", "neither"])
+def test_gradients_of_either_state(given, dtype):
+    """A gradient of the last state without a first state, and the other way round."""
+    d = make(2, 1, 3, 100, 32, 48, dtype, given[0], 27)
+    x, h = dev(d), host(d)
+    r = torch.Generator().manual_seed(4)
+    dy = torch.randn(2, 3, 100, 48, generator=r).to(dtype)
+    dW = torch.randn(2, 3, 48, 32, generator=r) if given[1] else None
+    args = ("q", "k", "v", "g", "beta")
+    call = dict(W0=x["W0"], dW_final=None if dW is None else dW.cuda(), scale=-0.7)
+    got = fw.fw_gated_delta_backward(*[x[n] for n in args], dy.cuda(), **call)
+    want = gated.gated_backward(*[h[n] for n in args], f64(dy), h["W0"], None if dW is None else f64(dW), scale=-0.7)
+    yr, _ = gated.gated_forward(**h, scale=-0.7)
+    terms = np.abs(f64(dy) * yr).sum(-1).max()
+    for n, a, w in zip(("dq", "dk", "dv", "dg", "dbeta", "dW0"), got, want):
+        near(n, a, w, grad=True, bf16=dtype == torch.bfloat16, terms=terms if n == "dg" else 0.0)
+    less = fw.fw_gated_delta_backward(*[x[n] for n in args], dy.cuda(), **call, return_dW0=False)
+    assert less[5] is None and all(torch.equal(a, b) for a, b in zip(got[:5], less[:5]))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_a_scale_of_nothing(dtype):
+    d = dev(make(1, 1, 2, 70, 32, 16, dtype, True, 28))
+    y, W = fw.fw_gated_delta_forward(**d, scale=0.0)
+    _, W1 = fw.fw_gated_delta_forward(**d)
+    assert torch.all(y == 0) and torch.equal(W, W1)
+
+
+def test_the_most_heads():
+    """B H = 65 535, the last the grid takes: the bits of the batch in two parts; one more is refused."""
+    B, L = 65535, 2
+    r = torch.Generator(device="cuda").manual_seed(29)
+    q, k, v, dy = (torch.randn(B, 1, L, 16, generator=r, device="cuda").bfloat16() for _ in range(4))
+    g, be = (torch.rand(B, 1, L, generator=r, device="cuda").bfloat16() for _ in range(2))
+    ins = (q, k, v, -g, be)
+
+    def both(lo, hi):
+        part = [t[lo:hi].contiguous() for t in ins]
+        return fw.fw_gated_delta_forward(*part) + fw.fw_gated_delta_backward(*part, dy[lo:hi].contiguous())
+
+    whole, a, b = both(0, B), both(0, 30000), both(30000, B)
+    assert all(torch.equal(w, torch.cat(p)) for w, p in zip(whole, zip(a, b)))
+    one = [t[:, :, 0].contiguous() for t in ins]
+    W = torch.randn(B, 1, 16, 16, generator=r, device="cuda")
+    halves = [W[:30000].clone(), W[30000:].clone()]
+    y = fw.fw_gated_delta_decode_step(*one, W)
+    ys = [fw.fw_gated_delta_decode_step(*[t[s].contiguous() for t in one], w)
+          for s, w in zip((slice(0, 30000), slice(30000, B)), halves)]
+    assert torch.equal(y, torch.cat(ys)) and torch.equal(W, torch.cat(halves))
+    more = [torch.cat([t, t[:1]]) for t in ins]
+    with pytest.raises(fw.FwError) as err:
+        fw.fw_gated_delta_forward(*more)
+    assert err.value.code == fw.FW_ERR_UNSUPPORTED
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 values and 2^34 bytes of workspace: the bits of the sequence in two calls."""
+    H, L, d_v, cut = 2, 4200001, 256, 64 * 65000
+    if torch.cuda.mem_get_info()[0] < 80e9:
+        pytest.skip("needs 60 GB")
+    r = torch.Generator(device="cuda").manual_seed(30)
+    n = lambda *s: torch.randn(*s, generator=r, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    ins = (n(1, 1, L, 16), n(1, 1, L, 16), n(1, H, L, d_v), -torch.rand(1, H, L, generator=r, device="cuda").bfloat16(),
+           torch.rand(1, H, L, generator=r, device="cuda").bfloat16())
+    assert ins[2].numel() > 2 ** 31
+    y, W = fw.fw_gated_delta_forward(*ins)
+    y1, W1 = fw.fw_gated_delta_forward(*[t[:, :, :cut].contiguous() for t in ins])
+    assert torch.equal(y[:, :, :cut], y1)
+    y2, W2 = fw.fw_gated_delta_forward(*[t[:, :, cut:].contiguous() for t in ins], W0=W1)
+    assert torch.equal(y[:, :, cut:], y2) and torch.equal(W, W2)
+    del y, y1, y2, ins
+    torch.cuda.empty_cache()

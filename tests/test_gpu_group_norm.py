@@ -253,3 +253,25 @@ def test_one_row_alone(row, dtype):
     assert torch.all(dx[:, :, row] != 0)
     dx[:, :, row] = 0
     assert torch.all(dx == 0)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 values: the last tokens have the bits of a call of their own."""
+    H, L, d = 16, 1100003, 128
+    if torch.cuda.mem_get_info()[0] < 60e9:
+        pytest.skip("needs 40 GB")
+    r = torch.Generator(device="cuda").manual_seed(12)
+    x = torch.randn(1, H, L, d, generator=r, device="cuda", dtype=torch.bfloat16)
+    gate = torch.randn(1, L, H * d, generator=r, device="cuda", dtype=torch.bfloat16)
+    gamma, beta = (torch.randn(H * d, generator=r, device="cuda") for _ in range(2))
+    assert x.numel() > 2 ** 31
+    out = fw.fw_group_norm_act(x, gamma, beta, gate=gate, act="silu")
+    dx, dgate, dgamma, _ = fw.fw_group_norm_act_backward(x, gamma, beta, out, gate=gate, act="silu")
+    assert torch.isfinite(dgamma).all()
+    for s in (slice(0, 500), slice(L - 500, L)):
+        xs, zs, os = x[:, :, s].contiguous(), gate[:, s].contiguous(), out[:, s].contiguous()
+        assert torch.equal(fw.fw_group_norm_act(xs, gamma, beta, gate=zs, act="silu"), os)
+        dxs, dzs, _, _ = fw.fw_group_norm_act_backward(xs, gamma, beta, os, gate=zs, act="silu")
+        assert torch.equal(dx[:, :, s], dxs) and torch.equal(dgate[:, s], dzs)
+    del x, gate, out, dx, dgate
+    torch.cuda.empty_cache()
