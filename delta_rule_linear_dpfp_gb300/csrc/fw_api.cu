@@ -80,7 +80,7 @@ cudaError_t status_word(unsigned **out) {
         *out = di.status;
     return e;
 }
-// SMs of the current device (for the gated rule's launchers).
+// SMs of the current device (for the gated rule's and the group norm's launchers).
 cudaError_t device_sms(int *out) {
     DeviceInfo di;
     cudaError_t e = device_info(&di);

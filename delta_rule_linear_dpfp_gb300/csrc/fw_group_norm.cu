@@ -29,6 +29,8 @@
 
 namespace fw {
 
+cudaError_t device_sms(int *out); // fw_api.cu
+
 namespace {
 
 constexpr int kT = 256;
@@ -362,11 +364,12 @@ __global__ void __launch_bounds__(kT)
     }
 }
 
-// CTAs per head: what the SMs hold at once (three an SM, two in the backward:
-// registers), no more than the rows give.  (B16 H8 L2048 d 128: 31.4 us in one
-// wave, 33 in two, 37 with four CTAs an SM, whose 64 registers
-// spill; the gradients 62 us in one wave, 66 in two, 105 with three CTAs an SM.)
-constexpr int kCtas = 152 * 3, kBackwardCtas = 152 * 2;
+// CTAs per head: what the device's SMs hold at once (three an SM, two in the
+// backward: registers), no more than the rows give.  (B16 H8 L2048 d 128: 31.4 us
+// in one wave, 33 in two, 37 with four CTAs an SM, whose 64 registers spill; the
+// gradients 62 us in one wave, 66 in two, 105 with three CTAs an SM.)
+constexpr int kCtasPerSm = 3, kBackwardCtasPerSm = 2;
+constexpr int kMostSms = 152; // (a GB300's: the workspace holds the partial rows of so many)
 int parts_of(int B, int H, int L, int d, int ctas) {
     int lpr = 1;
     while (8 * lpr < d)
@@ -384,13 +387,13 @@ struct Launch {
     void *dx, *dgate;
     float *part;
     cudaStream_t st;
+    int parts; // CTAs of a head
 
     template <int LPR, int ACT, bool GATE, typename T> cudaError_t run() const {
         if (dout)
-            return launch_pdl(group_norm_backward_kernel<LPR, ACT, GATE, T>,
-                              dim3(parts_of(a.B, a.H, a.L, a.d, kBackwardCtas), a.H), dim3(kT), 0, st, a, (const T *)x,
-                              (const T *)gate, gamma, beta, (const T *)dout, (T *)dx, (T *)dgate, part);
-        return launch_pdl(group_norm_kernel<LPR, ACT, GATE, T>, dim3(parts_of(a.B, a.H, a.L, a.d, kCtas), a.H), dim3(kT), 0, st, a, (const T *)x,
+            return launch_pdl(group_norm_backward_kernel<LPR, ACT, GATE, T>, dim3(parts, a.H), dim3(kT), 0, st, a,
+                              (const T *)x, (const T *)gate, gamma, beta, (const T *)dout, (T *)dx, (T *)dgate, part);
+        return launch_pdl(group_norm_kernel<LPR, ACT, GATE, T>, dim3(parts, a.H), dim3(kT), 0, st, a, (const T *)x,
                           (const T *)gate, gamma, beta, (T *)out);
     }
     template <int LPR, int ACT, bool GATE> cudaError_t dtype(int bf16) const {
@@ -420,24 +423,33 @@ struct Launch {
 } // namespace
 
 size_t group_norm_backward_workspace_bytes(int B, int H, int L, int d) {
-    return sizeof(float) * 2 * (size_t)parts_of(B, H, L, d, kBackwardCtas) * H * d;
+    return sizeof(float) * 2 * (size_t)parts_of(B, H, L, d, kBackwardCtasPerSm * kMostSms) * H * d;
 }
 
 cudaError_t launch_group_norm(const NormArgs &a, const void *x, const void *gate, const float *gamma,
                               const float *beta, void *out, int bf16, cudaStream_t st) {
-    return Launch{a, x, gate, gamma, beta, out, nullptr, nullptr, nullptr, nullptr, st}.go(bf16);
+    int sms = 0;
+    const cudaError_t e = device_sms(&sms);
+    if (e != cudaSuccess)
+        return e;
+    const int parts = parts_of(a.B, a.H, a.L, a.d, kCtasPerSm * sms);
+    return Launch{a, x, gate, gamma, beta, out, nullptr, nullptr, nullptr, nullptr, st, parts}.go(bf16);
 }
 
 cudaError_t launch_group_norm_backward(const NormArgs &a, const void *x, const void *gate, const float *gamma,
                                        const float *beta, const void *dout, void *dx, void *dgate, float *dgamma,
                                        float *dbeta, void *workspace, int bf16, cudaStream_t st) {
     float *part = static_cast<float *>(workspace);
-    cudaError_t e = Launch{a, x, gate, gamma, beta, nullptr, dout, dx, dgate, part, st}.go(bf16);
+    int sms = 0;
+    cudaError_t e = device_sms(&sms);
     if (e != cudaSuccess)
         return e;
-    const int ch = a.H * a.d;
+    const int parts = parts_of(a.B, a.H, a.L, a.d, kBackwardCtasPerSm * std::min(sms, kMostSms)), ch = a.H * a.d;
+    e = Launch{a, x, gate, gamma, beta, nullptr, dout, dx, dgate, part, st, parts}.go(bf16);
+    if (e != cudaSuccess)
+        return e;
     return launch_pdl(group_norm_params_kernel, dim3((2 * ch + 31) / 32), dim3(kT), 0, st, (const float *)part, dgamma,
-                      dbeta, parts_of(a.B, a.H, a.L, a.d, kBackwardCtas), ch);
+                      dbeta, parts, ch);
 }
 
 } // namespace fw
