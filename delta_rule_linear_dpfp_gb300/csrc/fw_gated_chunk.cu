@@ -199,12 +199,7 @@ FW_DEV void mm_nn(float (&acc)[R][4], const float *A, int lda, int ra, const flo
     t.get(acc);
 }
 
-// 16-byte asynchronous copies into shared memory; `in` false writes zeros.
-FW_DEV void copy16(float *dst, const float *src, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
-                 "r"(in ? 16 : 0)
-                 : "memory");
-}
+// A thread's asynchronous copies (copy16) in groups.
 FW_DEV void copies_sent() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> FW_DEV void copies_done() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 // rows x width (a power of two, given as the logarithm of its quarter) of a

@@ -50,11 +50,6 @@ constexpr int C = kGatedChunk;
 // where two CTAs share an SM's registers.
 __host__ __device__ constexpr int parts_of(int nkb) { return 2 * nkb; }
 
-// 16 bytes on their way into shared memory, or zeros.
-FW_DEV void copy16(void *to, const void *from, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(in ? 16 : 0) : "memory");
-}
-
 // 8 channels (chunk c of 4) of a pair tile's row: hi + lo.
 FW_DEV void pair8(const uint8_t *tile, int row, int c, F2 (&o)[4]) {
     F2 l[4];

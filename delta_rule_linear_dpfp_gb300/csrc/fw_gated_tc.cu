@@ -966,9 +966,14 @@ cudaError_t launch_prep(const GatedArgs &a, const void *q, const void *k, const 
 
 // Chunks in a segment of the forward.  Where the walk's CTAs leave most SMs
 // idle, a sequence is cut into segments and the preparation of one runs on the
-// idle SMs beside the walk over the one before.  A segment is a whole number
-// of waves of preparing CTAs (two an SM) and at least kMinSegment chunks, since
-// each costs the walk a start.  (16 heads, 16 381 tokens, d 128: 624 us in
+// idle SMs beside the walk over the one before.  The length wanted is a whole
+// number of waves of preparing CTAs (two an SM) and at least kMinSegment
+// chunks, since each segment costs the walk a start; the sequence is then cut
+// into equal segments, as many as come nearest to that length, so that none
+// is a stump.  A segment may so be a few chunks longer or shorter than wanted,
+// and its last wave of preparing CTAs partly empty (B2 H8 L2048: 16 chunks
+// where a wave holds 15).  The first is prepared by every SM and is as long as
+// the others all the same.  (16 heads, 16 381 tokens, d 128: 624 us in
 // one piece, 506 in segments of 22 chunks, 742 in segments of 11; B2 H8 L2048,
 // d_v 64: 85 us in one piece, 77 in two of 16.  With a faster preparation and
 // pairs of floats the two take 461 and 71 us.)

@@ -17,6 +17,13 @@ FW_DEV int seq_len(const GatedArgs &a, int b) {
     return a.lengths ? min(max(__ldcg(after_wait(a.lengths) + b), 0), a.L) : a.L;
 }
 
+// 16 bytes on their way into shared memory by an asynchronous copy; `in` false: zeros.
+FW_DEV void copy16(void *to, const void *from, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+                 "r"(in ? 16 : 0)
+                 : "memory");
+}
+
 // Sums kept as an unevaluated pair of floats (hi + lo, 48 bits).
 struct Pair {
     float hi, lo;
@@ -90,10 +97,8 @@ FW_DEV void widen8(uint4 u, F2 (&o)[4]) {
 // swizzled as the descriptors of fw_tc.cuh expect.  16-byte chunk c of a row.
 FW_DEV uint32_t pair_chunk(int row, int c) { return (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)); }
 
-// (I + A)^-1 of the strictly lower triangular A (row stride kGatedLd): forward
-// substitution in the four 16 x 16 diagonal blocks, one thread a column, then
-// two doublings T21 = -T22 (A21 T11), four columns a thread.
-// R rows a thread: more products for each value read from shared memory.
+// s += R rows of a (H / R apart) times four columns of b, over H terms; more
+// rows a thread are more products for each value read from shared memory.
 template <int H, int R> FW_DEV void block_product(const float *a, int lda, const float *b, int ldb, float (&s)[R][4]) {
 #pragma unroll
     for (int m = 0; m < H; m += 4) {
@@ -119,6 +124,8 @@ template <int H, int R> FW_DEV void block_product(const float *a, int lda, const
         }
     }
 }
+// One doubling: T21 = -T22 (A21 T11) in each pair of H x H diagonal blocks, R
+// rows and four columns a thread.
 template <int H, int R> FW_DEV void double_inverse(const float *A, float *T, float *tmp) {
     constexpr int Q = H / 4, N = (kGatedChunk / (2 * H)) * (H / R) * Q; // threads: pair of blocks, row, four columns
     const int tid = threadIdx.x, p = tid / (H / R * Q), i = (tid / Q) % (H / R), j = (tid % Q) * 4, r0 = p * 2 * H;
@@ -142,6 +149,9 @@ template <int H, int R> FW_DEV void double_inverse(const float *A, float *T, flo
     __syncthreads();
 }
 
+// (I + A)^-1 of the strictly lower triangular A (row stride kGatedLd): forward
+// substitution in the four 16 x 16 diagonal blocks, one thread a column, then
+// two doublings.
 FW_DEV void unit_lower_inverse(const float *A, float *T, float *tmp) {
     const int tid = threadIdx.x;
     for (int e = tid; e < kGatedChunk * kGatedChunk / 4; e += kGatedThreads) {
