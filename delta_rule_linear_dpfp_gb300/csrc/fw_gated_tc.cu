@@ -632,8 +632,8 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *zt = sm + L::z, *ut = sm + L::u;
     uint64_t *fullA = reinterpret_cast<uint64_t *>(sm + L::bar), *fullB = fullA + 2, *m1 = fullA + 4, *m2 = fullA + 5,
-             *my = fullA + 6, *zr = fullA + 7, *ur = fullA + 8;
-    uint32_t *slot = reinterpret_cast<uint32_t *>(fullA + 9);
+             *my = fullA + 6, *zr = fullA + 8, *ur = fullA + 9;
+    uint32_t *slot = reinterpret_cast<uint32_t *>(fullA + 10);
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, sl = blockIdx.x, bh = blockIdx.y, n0 = sl * TP * NV;
     const int b = bh / a.H;
     griddep_wait();
@@ -645,11 +645,14 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
         tmem_relinquish();
     }
     if (tid == 32) {
-        for (int e = 0; e < 7; ++e)
+        for (int e = 0; e < 8; ++e)
             mbar_init(fullA + e, 1);
-        // A wait knows a phase by its parity, so each role that waits has to
-        // have seen one phase before the next but one can end: the copies' warp
-        // arrives, too, on one of the two barriers that every chunk passes.
+        // A wait knows a phase by its parity, so a role that waits has to see a
+        // phase before the next one ends.  The workers and the issuer of the MMAs
+        // need one another for that; the forward's copies' warp does not need to
+        // be seen by anyone, so it arrives for the state, too, and the answers'
+        // product has two barriers, for the chunks in turn (the product after
+        // next needs what this warp asks for behind its wait).
         mbar_init(zr, WORKERS + (MODE == kFwd ? 1 : 0));
         mbar_init(ur, WORKERS + (MODE == kFwd ? 0 : 1)); // the state's copy has left its tile
         fence_barrier_init();
@@ -688,7 +691,7 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
                     for (int s = 0; s < 4 * NKB; ++s)
                         mma_bf16(tY, at(dA, (uint32_t)NKB * 16384u + kmajor_step(s, 128)), at(dz, (uint32_t)s * 2048u),
                                  idesc_bf16(128, 64 * TP, 0, 1), s > 0);
-                    mma_commit(my);
+                    mma_commit(my + (it & 1));
                 }
                 wait(fullB + (it & 1), (it >> 1) & 1);
                 wait(ur, it & 1);
@@ -737,6 +740,8 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
                 wait(zr, it & 1);
                 if (!ok)
                     break;
+                if (MODE == kFwd)
+                    mbar_arrive(zr);
                 if (MODE != kFwd) { // the state before this chunk, as it lies
                     bulk_s2g(ws + rec.off(bh, chunk_of(it)) + (MODE == kKeep ? rec.S : rec.dS) + (size_t)sl * TP * DKP * 128,
                              zt, tiles * DKP * 128u);
@@ -748,13 +753,13 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
                     bulk_wait_read();
                     mbar_arrive(ur);
                 } else {
-                    wait(my, it & 1);
+                    wait(my + (it & 1), (it >> 1) & 1);
                 }
-                wait(ur, it & 1); // (they have seen the values' product)
+                if (MODE != kFwd)
+                    wait(ur, it & 1); // (they have seen the values' product)
+                // (the answers' product ends behind the values')
                 if (ok && it + 2 < nch)
                     fetch_a(it + 2);
-                if (MODE == kFwd)
-                    mbar_arrive(zr);
             }
             if (MODE != kFwd)
                 bulk_wait_all();
@@ -874,7 +879,7 @@ FW_DEV void walk(const GatedArgs &a, const __nv_bfloat16 *__restrict__ dy, const
             put8(ut_, i, 2 * h2 + c8, t0);
             written(ur);
             if (MODE == kFwd) {
-                wait(my, it & 1);
+                wait(my + (it & 1), (it >> 1) & 1);
                 tc_fence_after();
                 product(tY, place + 4096, y8);
                 if (mine && i < n)
