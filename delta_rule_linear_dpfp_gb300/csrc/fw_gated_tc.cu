@@ -603,8 +603,9 @@ __global__ void __launch_bounds__(NT, 2)
 // TP: with one tile a CTA the chain of a chunk is shortest; two tiles read the
 // records half as often, which is what counts once there are more CTAs than
 // SMs (the backward at B8 H16 L2048, 1024 CTAs with one tile: 955 us with one
-// tile, its walks 341, at 9 TB/s out of L2; 893 with two; 759 with the
-// faster preparation and gradients of now).
+// tile, its walks 341, at 9 TB/s out of L2; 893 with two; 715 to 790, by the
+// box, with the faster preparation and gradients of now, the walks 288).  Two
+// tiles for d_k > 64 are 18 warps of 96 registers, which spill 24 bytes.
 enum { kFwd = 0, kKeep = 1, kRev = 2 };
 constexpr int walk_threads(int TP) { return NT * TP + 64; }
 
@@ -981,7 +982,7 @@ cudaError_t launch_prep(const GatedArgs &a, const void *q, const void *k, const 
 // the others all the same.  (16 heads, 16 381 tokens, d 128: 624 us in
 // one piece, 506 in segments of 22 chunks, 742 in segments of 11; B2 H8 L2048,
 // d_v 64: 85 us in one piece, 77 in two of 16.  With a faster preparation and
-// pairs of floats the two take 461 and 71 us.)
+// pairs of floats the two take 468 and 72 us.)
 constexpr int kMinSegment = 12;
 int segment_chunks(const GatedArgs &a, const GatedRecord &rec, int num_sms) {
     const int64_t heads = (int64_t)a.B * a.H, walkers = heads * rec.ns;

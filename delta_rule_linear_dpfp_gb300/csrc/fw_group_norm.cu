@@ -39,7 +39,8 @@ enum { kNone = 0, kRelu = 1, kSilu = 2, kGelu = 3 };
 // (A variant of the kernels for each: as a branch per element it made them
 // bound by instructions, 36 an element and 49 us where the bytes take 30.)
 // The exponential and the reciprocal as single instructions (2^-22 of the
-// value; denormal results are 0).  x sigmoid(x) needs no guard: far below 0 the
+// value, and 2^-24 |x| log2 e for the exponent's own rounding; denormal results
+// are 0).  x sigmoid(x) needs no guard: far below 0 the
 // exponential is infinite and the reciprocal 0.
 FW_DEV float rcp(float x) {
     float r;

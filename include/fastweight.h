@@ -457,7 +457,9 @@ FW_API int fw_decode_stack_step(const fw_stack_layer *layers, int n_layers, cons
  *   d_k in {16, 32, 64, 128}; d_v a multiple of 16 up to 256; B H <= 65535.
  * With bf16 I/O an fp32 operand of a tensor-core product is two bf16 terms
  * (2^-16 of it is left at most) and sums and the state are fp32; an infinity
- * among them becomes NaN.  With fp32 I/O everything is fp32.  The sequence
+ * among them becomes NaN.  W_final and dW0 are then off by 3e-6 of their size
+ * (2-norm; up to 8.5e-6 for d_k 16, the narrowest), where fp32 I/O, for which
+ * everything is fp32, leaves 2e-7 to 4e-7.  The sequence
  * calls go by chunks of 64 tokens: a NaN or an infinity in a token's inputs
  * may reach the answers and gradients of every token of its chunk, and of all
  * that the state carries it to (a padded token's values reach nothing).
@@ -465,7 +467,11 @@ FW_API int fw_decode_stack_step(const fw_stack_layer *layers, int n_layers, cons
  * bad sizes, a scale or eps that is not finite, eps < 0 or a small workspace,
  * and FW_ERR_UNSUPPORTED for sizes outside the compiled set.  No call uses
  * state of the library, so calls with workspaces of their own may run at the
- * same time.  Results do not depend on the run (fixed summation orders).
+ * same time.  The workspaces are large, by the chunk and value head: with bf16
+ * I/O 147 968 bytes forward and 364 032 backward at d_k = d_v = 128 (74 240
+ * and 151 040 at 64), so 607 MB for 16 heads of 16 381 tokens and 1.5 GB for
+ * the gradients of 8 sequences of 2048; a long sequence may be given in pieces,
+ * W_final of one as W0 of the next, for the same bits if they end on chunks.  Results do not depend on the run (fixed summation orders).
  */
 FW_API size_t fw_gated_delta_forward_workspace_size(int B, int Hk, int H, int L, int d_k, int d_v,
                                                     int io_dtype);
@@ -532,6 +538,7 @@ typedef enum fw_act {
  *   gate        : [B, L, H d]   io_dtype, or NULL
  *   gamma, beta : [H d]         fp32
  *   out         : [B, L, H d]   io_dtype, token-major      (written)
+ *   eps         : >= 0; with 0, a head whose channels are all alike gives NaN
  *   d a multiple of 8 up to 256, H <= 65535, B L < 2^31 (FW_ERR_UNSUPPORTED
  *   otherwise).
  */
