@@ -24,10 +24,15 @@
 //   q-side   a_i = scale e^{G_i} S^T dY_i + sum_j E_ij k_j            (= dq_i)
 //   reader   h_i = e^{G_i} S^T dX_i + sum_j F_ij k_j
 //   writer   w_j = e^{G_C-G_j} dS'^T U_j + sum_i E_ij q_i - sum_i beta_i F_ij k_i
-//   dk = w - beta h,  dV = beta dX,  dbeta_i = dX_i.V_i - k_i.h_i,
-//   dG_i = q_i.a_i - beta_i k_i.h_i - k_i.w_i, and for the chunk's last token
-//   also e^{G_C} <S, dS'> + sum_j e^{G_C-G_j} k_j.(dS'^T U_j);
-//   dg_t = sum of dG_i over i >= t in the chunk.
+//   dk = w - beta h,  dV = beta dX,  dbeta_i = dX_i.V_i - k_i.h_i.
+// dg_t is the sum of everything that decays by token t, from what was there
+// before it to what comes with it or after:
+//   dg_t = e^{G_C} <S, dS'> + sum_{i >= t} R_i + sum_{j < t} W_j + sum_{i >= t > j} P_ij,
+//   R_i = e^{G_i} (scale q_i.S^T dY_i - beta_i k_i.S^T dX_i),  W_j = e^{G_C-G_j} k_j.dS'^T U_j,
+//   P_ij = E_ij q_i.k_j - beta_i F_ij k_i.k_j.
+// (As the sums over i >= t of q_i.a_i - beta_i k_i.h_i - k_i.w_i, the pairs on
+// one side of t would cancel, and what they leave is all there is where the
+// gates are strong, or nothing was there before.)
 // Keys and queries scaled to unit length enter as r k with one fp32 r per
 // token, and dk = r (dk^ - k^ (k^.dk^)) comes back.
 //
@@ -588,7 +593,8 @@ __global__ void __launch_bounds__(NT)
     const int ldk = a.d_k + 4, nC = gridDim.x, lv = NV + 4;
     float *kt = sm, *qt = kt + C * ldk, *accq = qt + C * ldk, *acck = accq + C * a.d_k, *S0 = acck + C * a.d_k,
           *S1 = S0 + NV * ldk, *Yt = S1 + NV * ldk, *Xt = Yt + C * lv, *Ut = Xt + C * lv, *Et = Ut + C * lv,
-          *Ft = Et + C * LC, *tok = Ft + C * LC, *red = tok + C * TOK; // red: dG [C], <S, dS'> per warp [8]
+          *Ft = Et + C * LC, *tok = Ft + C * LC, *red = tok + C * TOK; // red: R [C], W [C], pairs across [C], <S, dS'> per warp [8]
+    float *Pt = Yt; // (after the slices)
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, c = blockIdx.x, bk = blockIdx.y;
     const int b = bk / a.Hk, grp = a.H / a.Hk, i0 = 8 * w, kc = 4 * lane;
     const bool on = kc < a.d_k;
@@ -677,27 +683,72 @@ __global__ void __launch_bounds__(NT)
                 const int i = ei + 16 * r, j = ej + 16 * s;
                 const float *di = tok + i * TOK, *dj = tok + j * TOK;
                 const float Dd = j <= i ? expf((di[4] - dj[4]) + (di[5] - dj[5])) : 0.f;
-                Et[i * LC + j] = j <= i ? a.scale * Dd * e_[r][s] : 0.f;
-                Ft[i * LC + j] = j < i ? Dd * f_[r][s] : 0.f;
+                e_[r][s] = j <= i ? a.scale * Dd * e_[r][s] : 0.f;
+                f_[r][s] = j < i ? Dd * f_[r][s] : 0.f;
+                Et[i * LC + j] = e_[r][s];
+                Ft[i * LC + j] = f_[r][s];
             }
+        { // P, from the unit keys' and queries' products
+            float x[4][4] = {};
+            mm_nt<4, 4>(x, qt + ei * ldk, ldk, 16, kt + ej * ldk, ldk, 16, a.d_k);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    e_[r][s] = ej + 16 * s < ei + 16 * r ? e_[r][s] * x[r][s] : 0.f;
+                    x[r][s] = 0.f;
+                }
+            mm_nt<4, 4>(x, kt + ei * ldk, ldk, 16, kt + ej * ldk, ldk, 16, a.d_k);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const int i = ei + 16 * r, j = ej + 16 * s;
+                    Pt[i * LC + j] = j < i ? fmaf(-tok[i * TOK + 6] * f_[r][s], x[r][s], e_[r][s]) : 0.f;
+                }
+        }
         ss = warp_sum(ss);
         if (lane == 0)
-            red[C + w] = ss;
+            red[3 * C + w] = ss;
         __syncthreads();
-        float last = 0.f; // what moves with the whole chunk's decay
-        if (on) {
+        { // the pairs across each token: columns' sums over the rows from it on, eight tokens a warp
+            float c0 = 0.f, c1 = 0.f;
+            for (int i = i0 + 8; i < C; ++i) {
+                c0 += Pt[i * LC + lane];
+                c1 += Pt[i * LC + lane + 32];
+            }
+            for (int t = i0 + 7; t >= i0; --t) {
+                c0 += Pt[t * LC + lane];
+                c1 += Pt[t * LC + lane + 32];
+                const float s = warp_sum((lane < t ? c0 : 0.f) + (lane + 32 < t ? c1 : 0.f));
+                if (lane == 0)
+                    red[2 * C + t] = s;
+            }
+        }
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const float *d = tok + (i0 + r) * TOK;
-                const float4 kk = lds4(kt + (i0 + r) * ldk + kc);
+        for (int r = 0; r < 8; ++r) { // R and W
+            const float *d = tok + (i0 + r) * TOK;
+            float ra = 0.f, rw = 0.f;
+            if (on) {
+                const float4 kk = lds4(kt + (i0 + r) * ldk + kc), qq = lds4(qt + (i0 + r) * ldk + kc);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     aq[r][e] *= a.scale * d[2];
                     ah[r][e] *= d[2];
                     aw[r][e] *= d[3];
                 }
-                last += aw[r][0] * kk.x + aw[r][1] * kk.y + aw[r][2] * kk.z + aw[r][3] * kk.w;
+                ra = (qq.x * aq[r][0] + qq.y * aq[r][1] + qq.z * aq[r][2] + qq.w * aq[r][3]) -
+                     d[6] * (kk.x * ah[r][0] + kk.y * ah[r][1] + kk.z * ah[r][2] + kk.w * ah[r][3]);
+                rw = kk.x * aw[r][0] + kk.y * aw[r][1] + kk.z * aw[r][2] + kk.w * aw[r][3];
             }
+            ra = warp_sum(ra);
+            rw = warp_sum(rw);
+            if (lane == 0) {
+                red[i0 + r] = ra;
+                red[C + i0 + r] = rw;
+            }
+        }
+        if (on) {
             mm_nn<8>(aq, Et + i0 * LC, LC, 1, kt + kc, ldk, C);
             mm_nn<8>(ah, Ft + i0 * LC, LC, 1, kt + kc, ldk, C);
             mm_tn<8>(aw, Et + i0, LC, 1, qt + kc, ldk, C);
@@ -708,53 +759,36 @@ __global__ void __launch_bounds__(NT)
         __syncthreads();
         if (on)
             mm_tn<8>(aw, Ft + i0, LC, 1, kt + kc, ldk, C);
-        last = warp_sum(last);
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
             const int i = i0 + r;
             const float be = tok[i * TOK + 6];
-            float qa = 0.f, kh = 0.f, kw = 0.f;
+            float kh = 0.f;
             if (on) {
-                const float4 kk = lds4(kt + i * ldk + kc), qq = lds4(qt + i * ldk + kc);
-                qa = qq.x * aq[r][0] + qq.y * aq[r][1] + qq.z * aq[r][2] + qq.w * aq[r][3];
+                const float4 kk = lds4(kt + i * ldk + kc);
                 kh = kk.x * ah[r][0] + kk.y * ah[r][1] + kk.z * ah[r][2] + kk.w * ah[r][3];
-                kw = kk.x * aw[r][0] + kk.y * aw[r][1] + kk.z * aw[r][2] + kk.w * aw[r][3];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     accq[i * a.d_k + kc + e] += aq[r][e];
                     acck[i * a.d_k + kc + e] += aw[r][e] - be * ah[r][e];
                 }
             }
-            qa = warp_sum(qa);
             kh = warp_sum(kh);
-            kw = warp_sum(kw);
             const float xvs = warp_sum(xv[r]);
-            if (lane == 0) {
-                red[i] = qa - be * kh - kw;
-                if (i < n)
-                    io<float>::store(dbeta + r0 + i, xvs - kh);
-            }
+            if (lane == 0 && i < n)
+                io<float>::store(dbeta + r0 + i, xvs - kh);
         }
-        if (lane == 0)
-            red[C + 8 + w] = last;
         __syncthreads();
-        if (tid < 32) { // dg: the sums over later tokens, two a lane
-            float tail = 0.f;
+        if (tid < 32) { // dg, two tokens a lane
+            float z = 0.f;
             for (int x = 0; x < 8; ++x)
-                tail += tok[(C - 1) * TOK + 2] * red[C + x] + red[C + 8 + x];
-            const float x1 = red[2 * lane + 1] + (lane == 31 ? tail : 0.f), x0 = red[2 * lane];
-            float run = x0 + x1;
+                z += red[3 * C + x];
+            float x[2];
+            gated_decay_grads(tok[(C - 1) * TOK + 2] * z, red + 2 * lane, red + C + 2 * lane, red + 2 * C + 2 * lane, lane, x);
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float dn = __shfl_down_sync(0xffffffffu, run, o);
-                if (lane + o < 32)
-                    run += dn;
-            }
-            const float after = run - (x0 + x1);
-            if (2 * lane < n)
-                io<float>::store(dg + r0 + 2 * lane, run);
-            if (2 * lane + 1 < n)
-                io<float>::store(dg + r0 + 2 * lane + 1, after + x1);
+            for (int e = 0; e < 2; ++e)
+                if (2 * lane + e < n)
+                    io<float>::store(dg + r0 + 2 * lane + e, x[e]);
         }
         for (int e = n * a.d_v + tid; e < rows * a.d_v; e += NT)
             io<float>::store(dv + r0 * a.d_v + e, 0.f);
@@ -809,7 +843,7 @@ cudaError_t walk_channels(const GatedArgs &a, int *nv) {
     return e;
 }
 size_t grad_smem(int d_k) {
-    return sizeof(float) * (2 * (C + NV) * (d_k + 4) + 2 * C * d_k + 3 * C * (NV + 4) + 2 * C * LC + C * TOK + C + 16);
+    return sizeof(float) * (2 * (C + NV) * (d_k + 4) + 2 * C * d_k + 3 * C * (NV + 4) + 2 * C * LC + C * TOK + 3 * C + 8);
 }
 
 template <typename... KArgs, typename... Args>

@@ -8,15 +8,15 @@
 //   w = e^{G_C-G} (U dS') + E^T Q - F^T diag(beta) K,
 //   E = lower(scale D dY U^T),    F = strict_lower(D dX U^T),
 //   dq = a,  dk = w - beta h,  dV = beta dX,  dbeta_i = dX_i.V_i - k_i.h_i,
-//   dG_i = q_i.a_i - beta_i k_i.h_i - k_i.w_i  (+ the whole chunk's share in
-//   the last token), dg = the sums of dG over later tokens of the chunk.
+//   dg_t = e^{G_C} <S, dS'> + sum_{i >= t} R_i + sum_{j < t} W_j + sum_{i >= t > j} P_ij:
+//   what a token reads of S (R), writes to dS' (W), and the pairs with E and F (P).
 //
-// Five products on the tensor cores, each fp32 operand as two bf16 terms (see
-// fw_gated_tc.cu; the outputs are rounded to bf16 once, but dg is a difference
-// of its terms, and one term's 2^-9 would show in it):
+// Six products on the tensor cores, each fp32 operand as two bf16 terms (see
+// fw_gated_tc.cu; one term's 2^-9 would show beside the outputs' rounding):
+//   [Q; K] K^T, for P;
 //   [dY; dX] S and [dY; dX] U^T (128 rows: dY, then dX) and U dS', summed over
 //   32-channel slices as the walks stored them, two slices in flight;
-//   then [E; F] K and [F; E]^T [K; Q].
+//   then [E; F] K and [E; F]^T [Q; K].
 // One CTA per (chunk, key head) goes through the value heads that share the
 // key, so dq and dk are sums in a fixed order.
 //
@@ -60,12 +60,13 @@ FW_DEV void pair8(const uint8_t *tile, int row, int c, F2 (&o)[4]) {
         o[e] = o[e] + l[e];
 }
 
-// Shared memory: [K; Q]; two slices (S, U, dS', [dY; dX]), whose place the E
+// Shared memory: [Q; K]; two slices (S, U, dS', [dY; dX]), whose place the E
 // and F tiles (64 KB) take afterwards; the sums of dq and dk over the value
 // heads -- in the place of the E and F tiles, too, where a key head has one
 // value head, so that for d_k <= 64 two CTAs fit an SM (B4 H8 L512, 256 CTAs:
 // the whole backward 57 us with one an SM, 52 with two); scalars of this head
-// and the next; V's rows of two slices.
+// and the next; V's rows of two slices, whose place the sums over P take
+// afterwards.
 struct GradSmem {
     uint32_t slice, s, ds, yx, u, ef, accq, acck, tok, v, red, bar, bytes;
 };
@@ -84,7 +85,7 @@ __host__ __device__ inline GradSmem grad_smem(int nkb, bool alone) {
     o.tok = alone ? end : o.acck + (uint32_t)nkb * 16384;
     o.v = o.tok + 2 * C * 32;
     o.red = o.v + 2 * C * 64;
-    o.bar = o.red + 4 * ((4 * parts_of(nkb) + 1) * C + 32);
+    o.bar = o.red + 4 * ((4 * parts_of(nkb) + 2) * C + 16);
     o.bytes = o.bar + 64 + 1024;
     return o;
 }
@@ -103,8 +104,11 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
     uint8_t *kq = sm, *ef = sm + o.ef;
     float *tok = reinterpret_cast<float *>(sm + o.tok);
     float *red = reinterpret_cast<float *>(sm + o.red);
-    float *r_qa = red, *r_kh = red + PARTS * C, *r_kw = red + 2 * PARTS * C, *r_kl = red + 3 * PARTS * C,
-          *r_xv = red + 4 * PARTS * C, *r_ss = r_xv + C, *r_last = r_ss + 16; // qa, kh, kw, kl: one value per part
+    // one value per part: q.a and k.h of what is read of S, k.h in all, W; then dX.V, the pairs across, <S, dS'>
+    float *r_qa = red, *r_k0 = red + PARTS * C, *r_kh = red + 2 * PARTS * C, *r_w = red + 3 * PARTS * C,
+          *r_xv = red + 4 * PARTS * C, *r_c = r_xv + C, *r_ss = r_c + C;
+    // P's sums: over the columns of a block of 16 before a token, of a warp's rows from it on, and whole rows of a block
+    float *p_part = reinterpret_cast<float *>(sm + o.v), *p_row = p_part + 4 * C;
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + o.bar), *done = full + 2, *kqb = full + 4, *mm = full + 5;
     uint32_t *slot = reinterpret_cast<uint32_t *>(full + 6);
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, c = blockIdx.x, bk = blockIdx.y;
@@ -113,6 +117,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
     // One thread asks for the slices and issues the products.  Of 16 warps its
     // warp is left out of the work on the slices, which runs meanwhile.
     constexpr int BOSS = NKB == 2 ? 15 : 0;
+    constexpr int ADDER = NKB == 2 ? 14 : 2; // the warp that adds up P (it has less to do than one of rows 0 - 63)
     const bool boss = tid == 32 * BOSS;
     griddep_wait();
     v = after_wait(v);
@@ -184,14 +189,19 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
             copy16(sm + o.tok + (m & 1) * (C * 32) + tid * 16, src + rec.tok + tid * 16, true);
     };
     if (boss) {
-        for (int e = 0; e < 6; ++e)
+        for (int e = 0; e < 5; ++e)
             mbar_init(full + e, 1);
+        mbar_init(mm, 2); // the products; P's sums have been read
         fence_barrier_init();
     }
     begin(0);
     if (boss) {
         mbar_arrive_expect_tx(kqb, NKB * 16384);
-        bulk_g2s(kq, record(0) + rec.K, NKB * 16384, kqb);
+        for (int kb = 0; kb < NKB; ++kb) { // (the record has the keys first)
+            const uint8_t *src = record(0) + rec.K + kb * 16384;
+            bulk_g2s(kq + kb * 16384, src + 8192, 8192, kqb);
+            bulk_g2s(kq + kb * 16384 + 8192, src, 8192, kqb);
+        }
     }
     if (w == 0) {
         tmem_alloc(slot, kCols);
@@ -255,8 +265,16 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                 wait(done + ((gs + 1) & 1), ((gs - 1) >> 1) & 1);
                 request(m, s + 1, gs + 1);
             }
+            if (boss && s == 0 && m == 0)
+                wait(kqb, 0);
             if (boss && ok) {
                 tc_fence_after();
+                if (s == 0) { // [Q; K] K^T, where the later products' E^T [Q; K] will be
+#pragma unroll
+                    for (int e = 0; e < 4 * NKB; ++e)
+                        mma_bf16(tE, desc_sw128(kq_s + kmajor_step(e, 128), 16, 1024),
+                                 desc_sw128(kq_s + 8192 + kmajor_step(e, 128), 16, 1024), idesc_bf16(128, 64, 0, 0), e > 0);
+                }
                 const uint32_t base = ef_s + (uint32_t)(gs & 1) * o.slice;
                 for (int t = 0; t < 3; ++t) { // hi hi, hi lo, lo hi
                     const uint32_t ta = t == 2 ? 64u : 0u, tb = t == 1 ? 64u : 0u;
@@ -291,7 +309,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
         if (lane == 0)
             r_ss[w] = ss;
         const float be = tok[kBeta + i], rk = tok[kRk + i], rq = tok[kRq + i];
-        // E and F, as [E; F] rk_j (K-major) and as [F (-beta rk_i); E rq_i]
+        // E and F, as [E; F] rk_j (K-major) and as [E rq_i; F (-beta rk_i)]
         {
             const float ghi = tok[kGhi + i], glo = tok[kGlo + i];
             const F2 fr = both(rr < C ? rq : -be * rk), fs = both(rr < C ? a.scale : 1.f);
@@ -322,14 +340,41 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
 #pragma unroll
                 for (int e = 0; e < 16; e += 8) {
                     uint4 hi, lo;
-                    const uint32_t to = kmajor_chunk(rr, j0 + e, 128), to2 = kmajor_chunk(rr ^ 64, j0 + e, 128);
+                    const uint32_t to = kmajor_chunk(rr, j0 + e, 128);
                     split8(x + e, hi, lo);
                     *reinterpret_cast<uint4 *>(ef + to) = hi;
                     *reinterpret_cast<uint4 *>(ef + 16384 + to) = lo;
                     split8(y + e, hi, lo);
-                    *reinterpret_cast<uint4 *>(ef + 32768 + to2) = hi;
-                    *reinterpret_cast<uint4 *>(ef + 49152 + to2) = lo;
+                    *reinterpret_cast<uint4 *>(ef + 32768 + to) = hi;
+                    *reinterpret_cast<uint4 *>(ef + 49152 + to) = lo;
                 }
+                // P (x fr [Q; K] K^T below the diagonal), added up along the row: y[e] is
+                // what lies before token j0 + e + 1, if that is not behind the row's own
+                tmem_ld16(tE + lb + (uint32_t)j0, y);
+                tmem_ld_wait();
+                const float fp = unpack(fr).x;
+                float run = 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const bool below = j0 + e < i;
+                    run += below ? x[e] * fp * y[e] : 0.f;
+                    y[e] = below ? run : 0.f;
+                }
+                p_row[(j0 >> 4) * 2 * C + rr] = run;
+                // over the warp's rows: halves of the values against halves of the lanes
+#pragma unroll
+                for (int h = 8; h > 0; h >>= 1) {
+                    const bool up = lane & (2 * h);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (e < h) {
+                            const float give = up ? y[e] : y[e + h], keep = up ? y[e + h] : y[e];
+                            y[e] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * h);
+                        }
+                }
+                y[0] += __shfl_xor_sync(0xffffffffu, y[0], 1);
+                if ((lane & 1) == 0 && j0 + (lane >> 1) + 1 < C)
+                    p_part[(w & 3) * C + j0 + (lane >> 1) + 1] = y[0];
             }
         }
         float x[HC]; // rows of a (rr < 64) or h
@@ -351,19 +396,59 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
             for (int t = 0; t < 2; ++t)
                 for (int s = 0; s < 4; ++s)
                     mma_bf16(tA, desc_sw128(ef_s + (uint32_t)t * 16384u + (uint32_t)s * 32u, 16, 1024),
-                             desc_sw128(kq_s + (uint32_t)s * 2048u, 16384, 1024), idesc_bf16(128, DKP, 0, 1),
+                             desc_sw128(kq_s + 8192u + (uint32_t)s * 2048u, 16384, 1024), idesc_bf16(128, DKP, 0, 1),
                              (t | s) != 0);
             for (int s = 0; s < 8; ++s) // rows 0 - 63 from the hi terms, 64 - 127 from the lo terms
                 mma_bf16(tE, desc_sw128(ef_s + 32768u + (uint32_t)s * 2048u, 16384, 1024),
                          desc_sw128(kq_s + (uint32_t)s * 2048u, 16384, 1024), idesc_bf16(128, DKP, 1, 1), s != 0);
             mma_commit(mm);
         }
-        // k_j . (e^{G_C-G_j} dS'^T U_j), for the chunk's decay
+        if (w == ADDER) { // the pairs across each token, two tokens a lane
+            float c2[2], b2[2] = {0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                c2[e] = 0.f;
+                const int t = 2 * lane + e;
+                if (t > 0)
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        c2[e] += p_part[p * C + t];
+            }
+#pragma unroll
+            for (int p = 0; p < 3; ++p) { // whole blocks of columns before a token's own
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    b2[e] += p_row[p * 2 * C + 2 * lane + e] + p_row[p * 2 * C + C + 2 * lane + e];
+                const float from1 = lanes_after(b2[0] + b2[1], lane) + b2[1];
+                if ((2 * lane - 1) >> 4 == p + 1)
+                    c2[0] += from1 + b2[0];
+                if ((2 * lane) >> 4 == p + 1)
+                    c2[1] += from1;
+            }
+            r_c[2 * lane] = c2[0];
+            r_c[2 * lane + 1] = c2[1];
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(mm);
+        }
+        // what is read of S (rows of a meet Q, rows of h meet K), and W
         auto kq_row = [&](int row, int p, F2 (&u)[4]) {
             widen8(*reinterpret_cast<const uint4 *>(kq + kmajor_chunk(row, part * HC + p, 128)), u);
         };
-        F2 last2 = both(0.f);
+        {
+            F2 read2 = both(0.f);
+#pragma unroll
+            for (int p = 0; p < HC; p += 8) {
+                F2 u[4];
+                kq_row(rr, p, u);
+#pragma unroll
+                for (int m2 = 0; m2 < 4; ++m2)
+                    read2 = fma2(u[m2], pack(x[p + 2 * m2], x[p + 2 * m2 + 1]), read2);
+            }
+            (rr < C ? r_qa : r_k0)[part * C + i] = sum(read2) * (rr < C ? rq : rk);
+        }
         if (rr < C) {
+            F2 w2 = both(0.f);
 #pragma unroll
             for (int p = 0; p < HC; p += 16) {
                 float t[16];
@@ -372,22 +457,20 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
 #pragma unroll
                 for (int e = 0; e < 16; e += 8) {
                     F2 u[4];
-                    kq_row(i, p + e, u);
+                    kq_row(C + i, p + e, u);
 #pragma unroll
                     for (int m2 = 0; m2 < 4; ++m2)
-                        last2 = fma2(u[m2], pack(t[e + 2 * m2], t[e + 2 * m2 + 1]), last2);
+                        w2 = fma2(u[m2], pack(t[e + 2 * m2], t[e + 2 * m2 + 1]), w2);
                 }
             }
-            const float last = warp_sum(sum(last2) * rk * tok[kEC + i]);
-            if (lane == 0)
-                r_last[w] = last; // (warps with w & 2 == 0)
+            r_w[part * C + i] = sum(w2) * rk * tok[kEC + i];
         }
         wait(mm, (uint32_t)m & 1);
         tc_fence_after();
         if (m + 1 < grp) // (the E and F tiles have been read; the sums lie in their place only if grp is 1)
             begin(m + 1);
         {
-            F2 dot2 = both(0.f); // q.a or k.h, this part's channels
+            F2 dot2 = both(0.f); // k.h, this part's channels
 #pragma unroll
             for (int p = 0; p < HC; p += 16) {
                 float t[16];
@@ -395,47 +478,37 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; e += 8) {
-                    F2 u[4];
-                    kq_row(rr ^ 64, p + e, u); // rows of a meet Q (tile rows 64 ..), rows of h meet K
+                    F2 u[4] = {};
+                    if (rr >= C)
+                        kq_row(rr, p + e, u);
 #pragma unroll
                     for (int m2 = 0; m2 < 8; m2 += 2) {
                         float *xe = x + p + e + m2;
                         const F2 r = pack(xe[0], xe[1]) + pack(t[e + m2], t[e + m2 + 1]);
-                        dot2 = fma2(u[m2 / 2], r, dot2);
+                        if (rr >= C)
+                            dot2 = fma2(u[m2 / 2], r, dot2);
                         const float2 d = unpack(r);
                         xe[0] = d.x;
                         xe[1] = d.y;
                     }
                 }
             }
-            const float dot = sum(dot2);
-            if (rr < C)
-                r_qa[part * C + i] = dot * rq;
-            else
-                r_kh[part * C + i] = dot * rk;
+            if (rr >= C)
+                r_kh[part * C + i] = sum(dot2) * rk;
         }
         if (rr >= C) { // -beta h, and w's part of the lo terms
-            F2 dot2 = both(0.f);
 #pragma unroll
             for (int p = 0; p < HC; p += 16) {
                 float t[16];
                 tmem_ld16(tE + lb + (uint32_t)(part * HC + p), t);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; e += 8) {
-                    F2 u[4];
-                    kq_row(i, p + e, u);
-#pragma unroll
-                    for (int m2 = 0; m2 < 8; m2 += 2) {
-                        const F2 r = pack(t[e + m2], t[e + m2 + 1]);
-                        dot2 = fma2(u[m2 / 2], r, dot2);
-                        const float2 d = unpack(fma2(both(-be), pack(x[p + e + m2], x[p + e + m2 + 1]), r));
-                        x[p + e + m2] = d.x;
-                        x[p + e + m2 + 1] = d.y;
-                    }
+                for (int e = 0; e < 16; e += 2) {
+                    const float2 d = unpack(fma2(both(-be), pack(x[p + e], x[p + e + 1]), pack(t[e], t[e + 1])));
+                    x[p + e] = d.x;
+                    x[p + e + 1] = d.y;
                 }
             }
-            r_kl[part * C + i] = sum(dot2) * rk;
         } else {
 #pragma unroll
             for (int p = 0; p < HC; p += 4) {
@@ -447,7 +520,6 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                 accq[(p / 4) * C] = t;
             }
             const F2 ec = both(tok[kEC + i]);
-            F2 dot2 = both(0.f);
 #pragma unroll
             for (int p = 0; p < HC; p += 16) {
                 float t[16], u1[16];
@@ -455,17 +527,10 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                 tmem_ld16(tE + lb + (uint32_t)(part * HC + p), u1);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; e += 8) {
-                    F2 u[4];
-                    kq_row(i, p + e, u);
-#pragma unroll
-                    for (int m2 = 0; m2 < 8; m2 += 2) {
-                        const F2 r = fma2(ec, pack(t[e + m2], t[e + m2 + 1]), pack(u1[e + m2], u1[e + m2 + 1]));
-                        dot2 = fma2(u[m2 / 2], r, dot2);
-                        const float2 d = unpack(r);
-                        t[e + m2] = d.x;
-                        t[e + m2 + 1] = d.y;
-                    }
+                for (int e = 0; e < 16; e += 2) {
+                    const float2 d = unpack(fma2(ec, pack(t[e], t[e + 1]), pack(u1[e], u1[e + 1])));
+                    t[e] = d.x;
+                    t[e + 1] = d.y;
                 }
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
@@ -477,7 +542,6 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                     acck[((p + e) / 4) * C] = r;
                 }
             }
-            r_kw[part * C + i] = sum(dot2) * rk;
         }
         tc_fence_before();
         __syncthreads();
@@ -489,43 +553,32 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
                 acck[(p / 4) * C] = make_float4(s.x + x[p], s.y + x[p + 1], s.z + x[p + 2], s.w + x[p + 3]);
             }
         }
-        if (w == BOSS) { // dg: the sums over later tokens, two a lane; dbeta
-            float G2[2];
+        if (w == BOSS) { // dg and dbeta, two tokens a lane
+            float R[2], W[2], out[2], z = 0.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int t = 2 * lane + e;
-                float qa = 0.f, kh = 0.f, kw = 0.f;
+                float qa = 0.f, k0 = 0.f, kh = 0.f;
+                W[e] = 0.f;
 #pragma unroll
                 for (int p = 0; p < PARTS; ++p) {
                     qa += r_qa[p * C + t];
+                    k0 += r_k0[p * C + t];
                     kh += r_kh[p * C + t];
-                    kw += r_kw[p * C + t] + r_kl[p * C + t];
+                    W[e] += r_w[p * C + t];
                 }
-                G2[e] = qa - tok[kBeta + t] * kh - kw;
+                R[e] = qa - tok[kBeta + t] * k0;
                 if (t < n)
                     io<bf>::store(dbeta + r0 + t, r_xv[t] - kh);
             }
-            if (lane == 31) {
-                float s = 0.f, l = 0.f;
 #pragma unroll
-                for (int e = 0; e < NT / 32; ++e) {
-                    s += r_ss[e];
-                    l += e & 2 ? 0.f : r_last[e];
-                }
-                G2[1] += tok[kEG + C - 1] * s + l;
-            }
-            float run = G2[0] + G2[1];
+            for (int e = 0; e < NT / 32; ++e)
+                z += r_ss[e];
+            gated_decay_grads(tok[kEG + C - 1] * z, R, W, r_c + 2 * lane, lane, out);
 #pragma unroll
-            for (int e = 1; e < 32; e <<= 1) {
-                const float dn = __shfl_down_sync(0xffffffffu, run, e);
-                if (lane + e < 32)
-                    run += dn;
-            }
-            const float own = G2[0] + G2[1];
-            if (2 * lane < n)
-                io<bf>::store(dg + r0 + 2 * lane, run);
-            if (2 * lane + 1 < n)
-                io<bf>::store(dg + r0 + 2 * lane + 1, (run - own) + G2[1]);
+            for (int e = 0; e < 2; ++e)
+                if (2 * lane + e < n)
+                    io<bf>::store(dg + r0 + 2 * lane + e, out[e]);
         }
         for (int e = n * a.d_v / 8 + tid; e < rows * a.d_v / 8; e += NT)
             reinterpret_cast<uint4 *>(dv + r0 * a.d_v)[e] = make_uint4(0, 0, 0, 0);
@@ -543,7 +596,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
 #pragma unroll
         for (int p = 0; p < HC; p += 8) {
             float u[8];
-            widen8(*reinterpret_cast<const uint4 *>(kq + kmajor_chunk(rr, part * HC + p, 128)), u);
+            widen8(*reinterpret_cast<const uint4 *>(kq + kmajor_chunk(rr ^ 64, part * HC + p, 128)), u);
             const float4 s = acc[(p / 4) * C], t = acc[(p / 4 + 1) * C];
             dot += u[0] * s.x + u[1] * s.y + u[2] * s.z + u[3] * s.w + u[4] * t.x + u[5] * t.y + u[6] * t.z + u[7] * t.w;
         }
@@ -560,7 +613,7 @@ __global__ void __launch_bounds__(128 * parts_of(NKB), NKB == 1 ? 2 : 1)
 #pragma unroll
         for (int p = 0; p < HC; p += 8) {
             float u[8];
-            widen8(*reinterpret_cast<const uint4 *>(kq + kmajor_chunk(rr, part * HC + p, 128)), u);
+            widen8(*reinterpret_cast<const uint4 *>(kq + kmajor_chunk(rr ^ 64, part * HC + p, 128)), u);
             const float4 s = acc[(p / 4) * C], t = acc[(p / 4 + 1) * C];
             const float g8[8] = {s.x, s.y, s.z, s.w, t.x, t.y, t.z, t.w};
 #pragma unroll

@@ -60,6 +60,34 @@ FW_DEV void split8(const float *x, uint4 &hi, uint4 &lo) {
     lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
+// Of 64 values, two a lane: the sum over the lanes after this one, or before it.
+FW_DEV float lanes_after(float x, int lane) {
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const float up = __shfl_down_sync(0xffffffffu, x, m);
+        x += lane + m < 32 ? up : 0.f;
+    }
+    x = __shfl_down_sync(0xffffffffu, x, 1);
+    return lane < 31 ? x : 0.f;
+}
+FW_DEV float lanes_before(float x, int lane) {
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const float up = __shfl_up_sync(0xffffffffu, x, m);
+        x += lane >= m ? up : 0.f;
+    }
+    x = __shfl_up_sync(0xffffffffu, x, 1);
+    return lane > 0 ? x : 0.f;
+}
+// dg of a lane's two tokens of 64 (the formula at the head of
+// fw_gated_chunk.cu): the state's part z, the readers R from a token on, the
+// writers W before it, the pairs c across it.  One warp.
+FW_DEV void gated_decay_grads(float z, const float *R, const float *W, const float *c, int lane, float (&dg)[2]) {
+    const float later = lanes_after(R[0] + R[1], lane), earlier = lanes_before(W[0] + W[1], lane);
+    dg[0] = ((later + R[1]) + R[0]) + earlier + (c[0] + z);
+    dg[1] = (later + R[1]) + (earlier + W[0]) + (c[1] + z);
+}
+
 // The tensor-core kernels' scalars of a chunk's tokens, [7][64]: G (the
 // running sum of g) as hi and lo, 1 / |k|, beta, 1 / |q|, e^G, e^{G_C - G}.
 enum { kGhi = 0, kGlo = 64, kRk = 128, kBeta = 192, kRq = 256, kEG = 320, kEC = 384 };

@@ -675,3 +675,68 @@ def test_offsets_past_32_bits():
     assert torch.equal(y[:, :, cut:], y2) and torch.equal(W, W2)
     del y, y1, y2, ins
     torch.cuda.empty_cache()
+
+
+# ---- the gates' gradients
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("case", [(2, 1, 2, 1, 16, 16), (1, 2, 2, 1, 128, 64), (3, 2, 4, 5, 64, 48), (1, 1, 2, 130, 32, 80),
+                                  (2, 2, 4, 200, 128, 128)], ids=str)
+def test_nothing_to_forget(case, dtype):
+    """Where nothing was there before a token its gate does not matter: dg is 0
+    there, not what rounding leaves; so too behind a gate of -inf."""
+    B, Hk, H, L, d_k, d_v = case
+    d = make(B, Hk, H, L, d_k, d_v, dtype, False, sum(case))
+    if L > 4:
+        d["g"][:, 0, [3, L - 1]] = -float("inf")
+    if L > 64:
+        d["g"][:, 1, 64] = -float("inf")                  # a chunk's first token
+    x = dev(d)
+    args = ("q", "k", "v", "g", "beta")
+    r = torch.Generator().manual_seed(31)
+    dy, dW = torch.randn(B, H, L, d_v, generator=r).to(dtype), torch.randn(B, H, d_v, d_k, generator=r)
+    dg = fw.fw_gated_delta_backward(*[x[n] for n in args], dy.cuda(), dW_final=dW.cuda())[3]
+    assert torch.all(dg[:, :, 0] == 0)
+    assert torch.all(dg[torch.isinf(x["g"])] == 0)
+    want = gated.gated_backward(*[host(d)[n] for n in args], f64(dy), dW=f64(dW))[3]
+    assert L == 1 or np.count_nonzero(want) > 0
+    assert torch.all((dg.cpu() != 0) == torch.from_numpy(np.abs(want) > 1e-30))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("case", [(1, 1, 1, 70, 16, 16), (2, 1, 3, 150, 64, 48), (1, 2, 4, 200, 128, 128), (1, 1, 2, 257, 32, 80)],
+                         ids=str)
+def test_gradients_of_strong_gates(case, dtype):
+    """Gates that leave e^-8 to e^-16 of everything: dg carries that factor, and
+    so do its errors (no difference of large terms): dg e^-g within 2^-11 of its largest, as the other gradients
+    (fp32 tensors: 2^-14), the exponent's rounding of 2^-19 among it."""
+    B, Hk, H, L, d_k, d_v = case
+    d = make(B, Hk, H, L, d_k, d_v, dtype, True, sum(case))
+    r = torch.Generator().manual_seed(32)
+    d["g"] = (-8 - 8 * torch.rand(B, H, L, generator=r)).to(dtype)
+    x, h = dev(d), host(d)
+    args = ("q", "k", "v", "g", "beta")
+    dy, dW = torch.randn(B, H, L, d_v, generator=r).to(dtype), torch.randn(B, H, d_v, d_k, generator=r)
+    got = fw.fw_gated_delta_backward(*[x[n] for n in args], dy.cuda(), W0=x["W0"], dW_final=dW.cuda(), scale=0.7)
+    want = gated.gated_backward(*[h[n] for n in args], f64(dy), h["W0"], f64(dW), scale=0.7)
+    rise = np.exp(-h["g"])
+    off, ref = np.abs(f64(got[3]) - want[3]) * rise, np.abs(want[3]) * rise
+    bf16 = dtype == torch.bfloat16
+    assert np.all(off <= (2.0 ** -11 if bf16 else 2.0 ** -14) * ref.max() + (2.0 ** -8 * ref if bf16 else 0)), (off.max(), ref.max())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("case", [(2, 2, 4, 640, 128, 96), (2, 4, 4, 500, 64, 64), (1, 1, 2, 900, 32, 128)], ids=str)
+def test_gate_gradients_keep_their_bits(case, dtype):
+    """The 2-norm of dg's errors: bf16 tensors, the rounding's 2^-9 (root mean
+    square at most) and 2^-13 of sums of 64 and more two-term products; fp32
+    tensors, as the other gradients, 2^-18."""
+    B, Hk, H, L, d_k, d_v = case
+    d = make(B, Hk, H, L, d_k, d_v, dtype, True, sum(case))
+    x, h = dev(d), host(d)
+    args = ("q", "k", "v", "g", "beta")
+    r = torch.Generator().manual_seed(33)
+    dy, dW = torch.randn(B, H, L, d_v, generator=r).to(dtype), torch.randn(B, H, d_v, d_k, generator=r)
+    got = fw.fw_gated_delta_backward(*[x[n] for n in args], dy.cuda(), W0=x["W0"], dW_final=dW.cuda(), scale=0.5)
+    want = gated.gated_backward(*[h[n] for n in args], f64(dy), h["W0"], f64(dW), scale=0.5)
+    assert off_by(got[3], want[3]) <= (2.0 ** -9 + 2.0 ** -13 if dtype == torch.bfloat16 else 2.0 ** -18)
