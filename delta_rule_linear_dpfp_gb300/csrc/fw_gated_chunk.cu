@@ -32,7 +32,9 @@
 //   P_ij = E_ij q_i.k_j - beta_i F_ij k_i.k_j.
 // (As the sums over i >= t of q_i.a_i - beta_i k_i.h_i - k_i.w_i, the pairs on
 // one side of t would cancel, and what they leave is all there is where the
-// gates are strong, or nothing was there before.)
+// gates are strong, or nothing was there before: 1325 us instead of 1389 for
+// the gradients of B8 H16 L512 d 128, and dg wrong by more than its own size
+// behind gates of e^-8.)
 // Keys and queries scaled to unit length enter as r k with one fp32 r per
 // token, and dk = r (dk^ - k^ (k^.dk^)) comes back.
 //

@@ -22,7 +22,8 @@
 //
 // What bounds it: for d_k > 64 one CTA an SM (tensor memory, shared memory),
 // and a head's 224 KB (d 128) come in four slices of which two fit.  B8 H16
-// L2048, two value heads a key head: 324 us, 3.4 TB/s; a head takes 19 700
+// L2048, two value heads a key head: 325 us, 3.0 TB/s (299 without the sums
+// over P, which dg cannot do without); without them a head takes 19 700
 // cycles: 10 300 of slices (their copies), 1 100 for the last product, 2 600
 // for E and F, 1 500 for the second products, 3 600 for the sums.  It took
 // 28 600 when the next slice was asked for after a product had been issued

@@ -471,7 +471,8 @@ FW_API int fw_decode_stack_step(const fw_stack_layer *layers, int n_layers, cons
  * I/O 147 968 bytes forward and 364 032 backward at d_k = d_v = 128 (74 240
  * and 151 040 at 64), so 607 MB for 16 heads of 16 381 tokens and 1.5 GB for
  * the gradients of 8 sequences of 2048; a long sequence may be given in pieces,
- * W_final of one as W0 of the next, for the same bits if they end on chunks.  Results do not depend on the run (fixed summation orders).
+ * W_final of one as W0 of the next, for the same bits if they end on chunks.
+ * Results do not depend on the run (fixed summation orders).
  */
 FW_API size_t fw_gated_delta_forward_workspace_size(int B, int Hk, int H, int L, int d_k, int d_v,
                                                     int io_dtype);
