@@ -534,6 +534,14 @@ def _scratch(need, workspace, like):
     return workspace, workspace.numel() * workspace.element_size()
 
 
+def _fits(*tensors):
+    """The C ABI takes sizes as int, and a larger one would arrive as what its
+    low bits say (a tensor of fewer values than that has none)."""
+    for t in tensors:
+        if t.numel() > 0x7FFFFFFF and max(t.shape) > 0x7FFFFFFF:
+            raise ValueError("every size must be below 2^31")
+
+
 def _gated_shapes(where, q, k, v, g, beta, states, lengths, dy=None):
     """Checks shared by the sequence calls; returns (B, Hk, H, L, d_k, d_v, dtype code)."""
     if q.dim() != 4 or v.dim() != 4:
@@ -543,6 +551,7 @@ def _gated_shapes(where, q, k, v, g, beta, states, lengths, dy=None):
     if (k.shape != q.shape or v.shape != (B, H, L, d_v) or g.shape != (B, H, L) or beta.shape != g.shape or
             (dy is not None and dy.shape != v.shape)):
         raise ValueError(f"{where}: shape mismatch among q, k, v, g, beta" + (", dy" if dy is not None else ""))
+    _fits(q, v)
     if Hk == 0 or H == 0 or H % Hk:
         raise ValueError(f"{where}: the value heads must be a multiple of the key heads")
     dt = q.dtype
@@ -636,6 +645,7 @@ def fw_gated_delta_decode_step(q, k, v, g, beta, W, l2norm: bool = True, scale: 
     Bv, H, d_v = v.shape
     if k.shape != q.shape or Bv != B or g.shape != (B, H) or beta.shape != g.shape:
         raise ValueError("shape mismatch among q, k, v, g, beta")
+    _fits(q, v)
     if Hk == 0 or H == 0 or H % Hk:
         raise ValueError("the value heads must be a multiple of the key heads")
     dt = q.dtype
@@ -658,6 +668,7 @@ def _norm_shapes(x, gamma, beta, gate, act, dout=None):
     if x.dim() != 4:
         raise ValueError("x must be [B,H,L,d]")
     B, H, L, d = x.shape
+    _fits(x)
     for t in (gamma, beta):
         if t.dtype != torch.float32 or t.shape != (H * d,):
             raise ValueError("gamma and beta must be fp32 [H d]")

@@ -112,3 +112,19 @@ def test_norm_refusals(lib):
         assert c(eps=-1.0) == E and c(eps=float("inf")) == E
         assert c(d=12) == U and c(d=264) == U and c(H=70000) == U
     assert call(B=0, x=None, out=None) == OK and call(L=0, x=None, out=None) == OK
+
+
+def test_sizes_past_an_int_are_refused():
+    """A length of 2^32 + 5 is not one of 5 (tensors without memory: the checks come before any call)."""
+    import torch
+    m = dict(dtype=torch.bfloat16, device="meta")
+    L = 2 ** 32 + 5
+    f = torch.empty(8, dtype=torch.float32, device="meta")
+    with pytest.raises(ValueError, match="2\\^31"):
+        binding._norm_shapes(torch.empty(1, 1, L, 8, **m), f, f, None, "none")
+    assert binding._norm_shapes(torch.empty(1, 1, 2 ** 31 - 1, 8, **m), f, f, None, "none") == (1, 1, 2 ** 31 - 1, 8)
+    q, v, g = torch.empty(1, 1, L, 16, **m), torch.empty(1, 2, L, 16, **m), torch.empty(1, 2, L, **m)
+    with pytest.raises(ValueError, match="2\\^31"):
+        binding._gated_shapes("call", q, q, v, g, g, (), None)
+    q, v, g = (t[:, :, :70] for t in (q, v, g))
+    assert binding._gated_shapes("call", q, q, v, g, g, (), None)[3] == 70
