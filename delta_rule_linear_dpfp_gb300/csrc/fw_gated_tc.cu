@@ -603,8 +603,8 @@ __global__ void __launch_bounds__(NT, 2)
 // TP: with one tile a CTA the chain of a chunk is shortest; two tiles read the
 // records half as often, which is what counts once there are more CTAs than
 // SMs (the backward at B8 H16 L2048, 1024 CTAs with one tile: 955 us with one
-// tile, its walks 341, at 9 TB/s out of L2; 893 with two; 715 to 790, by the
-// box, with the faster preparation and gradients of now, the walks 288).  Two
+// tile, its walks 341, at 9 TB/s out of L2; 893 with two; 715 to 805, by the
+// machine, with the faster preparation and gradients of now, the walks 288).  Two
 // tiles for d_k > 64 are 18 warps of 96 registers, which spill 24 bytes.
 enum { kFwd = 0, kKeep = 1, kRev = 2 };
 constexpr int walk_threads(int TP) { return NT * TP + 64; }
