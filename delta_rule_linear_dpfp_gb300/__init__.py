@@ -13,4 +13,7 @@ from .binding import (FwError, fw_delta_decode_step, fw_delta_forward,  # noqa: 
                       fw_decode_stack_step, fw_decode_stack_workspace_size,
                       fw_gated_delta_forward, fw_gated_delta_forward_workspace_size, fw_gated_delta_backward,
                       fw_gated_delta_backward_workspace_size, fw_gated_delta_decode_step, fw_group_norm_act,
-                      fw_group_norm_act_backward, fw_group_norm_act_backward_workspace_size)
+                      fw_group_norm_act_backward, fw_group_norm_act_backward_workspace_size, fw_embedding,
+                      fw_embedding_backward, fw_embedding_backward_workspace_size, fw_layer_norm,
+                      fw_layer_norm_backward, fw_layer_norm_backward_workspace_size, fw_vocab_loss,
+                      fw_vocab_loss_backward, fw_vocab_loss_backward_workspace_size, fw_vocab_loss_workspace_size)

@@ -35,10 +35,17 @@ EXPORTS = ("fw_status_string", "fw_dpfp", "fw_delta_forward_workspace_size", "fw
            "fw_decode_stack_workspace_size", "fw_decode_stack_step",
            "fw_gated_delta_forward_workspace_size", "fw_gated_delta_forward",
            "fw_gated_delta_backward_workspace_size", "fw_gated_delta_backward", "fw_gated_delta_decode_step",
-           "fw_group_norm_act", "fw_group_norm_act_backward_workspace_size", "fw_group_norm_act_backward")
+           "fw_group_norm_act", "fw_group_norm_act_backward_workspace_size", "fw_group_norm_act_backward",
+           "fw_embedding", "fw_embedding_backward_workspace_size", "fw_embedding_backward",
+           "fw_layer_norm", "fw_layer_norm_backward_workspace_size", "fw_layer_norm_backward",
+           "fw_vocab_loss_workspace_size", "fw_vocab_loss", "fw_vocab_loss_backward_workspace_size",
+           "fw_vocab_loss_backward")
 
 #: fw_act of fastweight.h by name
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+
+#: fw_index of fastweight.h by the tokens' dtype
+INDEX_TYPES = {torch.int32: 0, torch.int64: 1}
 
 #: the members of fw_stack_layer, in order
 STACK_FIELDS = ("W_in", "W_o", "b_o", "ln_gamma", "ln_beta", "W_1", "b_1", "W_2", "b_2", "W")
@@ -131,6 +138,25 @@ def load(path: str = None) -> ctypes.CDLL:
     lib.fw_group_norm_act_backward_workspace_size.argtypes = [i32] * 4
     lib.fw_group_norm_act_backward.restype = i32
     lib.fw_group_norm_act_backward.argtypes = [vp] * 10 + [sz] + [i32] * 6 + [f32, vp]
+    lib.fw_embedding.restype = i32
+    lib.fw_embedding.argtypes = [vp] * 3 + [i64, i32, i32, f32, i32, i32, vp]
+    lib.fw_embedding_backward_workspace_size.restype = sz
+    lib.fw_embedding_backward_workspace_size.argtypes = [i64, i32, i32]
+    lib.fw_embedding_backward.restype = i32
+    lib.fw_embedding_backward.argtypes = [vp] * 4 + [sz, i64, i32, i32, f32, i32, i32, i32, vp]
+    lib.fw_layer_norm.restype = i32
+    lib.fw_layer_norm.argtypes = [vp] * 6 + [i64, i32, f32, i32, vp]
+    lib.fw_layer_norm_backward_workspace_size.restype = sz
+    lib.fw_layer_norm_backward_workspace_size.argtypes = [i64, i32]
+    lib.fw_layer_norm_backward.restype = i32
+    lib.fw_layer_norm_backward.argtypes = [vp] * 8 + [sz, i64, i32, f32, i32, vp]
+    for n in ("fw_vocab_loss_workspace_size", "fw_vocab_loss_backward_workspace_size"):
+        getattr(lib, n).restype = sz
+        getattr(lib, n).argtypes = [i32] * 3
+    lib.fw_vocab_loss.restype = i32
+    lib.fw_vocab_loss.argtypes = [vp] * 7 + [sz] + [i32] * 4 + [vp]
+    lib.fw_vocab_loss_backward.restype = i32
+    lib.fw_vocab_loss_backward.argtypes = [vp] * 11 + [sz] + [i32] * 4 + [vp]
     lib.fw_selftest_umma.restype = i32
     lib.fw_selftest_umma.argtypes = [vp, vp, vp] + [i32] * 5 + [vp]
     if path is None:
@@ -723,3 +749,194 @@ def fw_group_norm_act_backward(x, gamma, beta, dout, gate=None, act: str = "none
                                         _dtype_code(x.dtype), eps, st)
     _check(rc, "fw_group_norm_act_backward")
     return dx, dgate, dgamma, dbeta
+
+
+def _index_type(ids, name):
+    if ids.dtype not in INDEX_TYPES:
+        raise TypeError(f"{name} must be int32 or int64")
+    return INDEX_TYPES[ids.dtype]
+
+
+def fw_embedding(ids, table, scale: float = 1.0, out=None, stream=None):
+    """scale table[ids]: ids of any shape, table [V,D] -> [*ids.shape, D] in
+    the table's dtype.  A negative id gives a row of zeros (padding), one past
+    the table a row of NaN."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fw_embedding(ids, table, scale, out)
+    st = _here("ids table out", ids, table, out)
+    if table.dim() != 2:
+        raise ValueError("table must be [V,D]")
+    V, D = table.shape
+    _fits(table)
+    if out is None:
+        out = torch.empty(*ids.shape, D, dtype=table.dtype, device=table.device)
+    elif out.dtype != table.dtype or out.shape != (*ids.shape, D):
+        raise ValueError("out must be [*ids.shape, D] in the table's dtype")
+    rc = load().fw_embedding(ids.data_ptr(), table.data_ptr(), out.data_ptr(), ids.numel(), V, D, scale,
+                             _index_type(ids, "ids"), _dtype_code(table.dtype), st)
+    _check(rc, "fw_embedding")
+    return out
+
+
+def fw_embedding_backward_workspace_size(N, V, D) -> int:
+    return int(load().fw_embedding_backward_workspace_size(N, V, D))
+
+
+def fw_embedding_backward(ids, dout, V: int = None, scale: float = 1.0, dtable=None, accumulate: bool = False,
+                          workspace=None, stream=None):
+    """The table's gradient [V,D] from dout [*ids.shape, D], summed in the
+    tokens' order; with accumulate it is added to dtable (in place)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fw_embedding_backward(ids, dout, V, scale, dtable, accumulate, workspace)
+    lib = load()
+    st = _here("ids dout dtable workspace", ids, dout, dtable, workspace)
+    if dout.dim() < 1 or dout.shape[:-1] != ids.shape:
+        raise ValueError("dout must be [*ids.shape, D]")
+    D = dout.shape[-1]
+    if dtable is None:
+        if V is None or accumulate:
+            raise ValueError("pass V, or the dtable to write (and to accumulate into)")
+        if not 0 < V <= 0x7FFFFFFF:
+            raise ValueError("V must be positive and below 2^31")
+        dtable = torch.empty(V, D, dtype=dout.dtype, device=dout.device)
+    elif dtable.dtype != dout.dtype or dtable.dim() != 2 or dtable.shape != (dtable.shape[0] if V is None else V, D):
+        raise ValueError("dtable must be [V,D] in dout's dtype")
+    _fits(dtable)
+    N, V = ids.numel(), dtable.shape[0]
+    workspace, ws_bytes = _scratch(_size("fw_embedding_backward_workspace_size", N, V, D), workspace, dout)
+    rc = lib.fw_embedding_backward(ids.data_ptr(), dout.data_ptr(), dtable.data_ptr(), workspace.data_ptr(), ws_bytes, N, V,
+                                   D, scale, 1 if accumulate else 0, _index_type(ids, "ids"), _dtype_code(dout.dtype), st)
+    _check(rc, "fw_embedding_backward")
+    return dtable
+
+
+def _layer_norm_shapes(x, params, same):
+    if x.dim() < 1:
+        raise ValueError("x must be [..., d]")
+    d = x.shape[-1]
+    if d > 0x7FFFFFFF:
+        raise ValueError("d must be below 2^31")
+    for t in params:
+        if t is not None and (t.dtype != torch.float32 or t.shape != (d,)):
+            raise ValueError("gamma and beta must be fp32 [d]")
+    for t in same:
+        if t is not None and (t.dtype != x.dtype or t.shape != x.shape):
+            raise ValueError("every activation must have x's shape and dtype")
+    return x.numel() // d if d else 0, d
+
+
+def fw_layer_norm(x, gamma=None, beta=None, residual=None, eps: float = 1e-5, out=None, sum=None, stream=None):
+    """The norm over the last axis of x [..., d], or of x + residual; gamma,
+    beta fp32 [d] or None.  Returns out, or (out, sum) with a residual."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fw_layer_norm(x, gamma, beta, residual, eps, out, sum)
+    st = _here("x gamma beta residual out sum", x, gamma, beta, residual, out, sum)
+    rows, d = _layer_norm_shapes(x, (gamma, beta), (residual, out, sum))
+    if out is None:
+        out = torch.empty_like(x)
+    if residual is not None and sum is None:
+        sum = torch.empty_like(x)
+    elif residual is None and sum is not None:
+        raise ValueError("sum goes with a residual")
+    rc = load().fw_layer_norm(x.data_ptr(), _data(residual), _data(gamma), _data(beta), out.data_ptr(), _data(sum), rows, d,
+                              eps, _dtype_code(x.dtype), st)
+    _check(rc, "fw_layer_norm")
+    return out if residual is None else (out, sum)
+
+
+def fw_layer_norm_backward_workspace_size(rows, d) -> int:
+    return int(load().fw_layer_norm_backward_workspace_size(rows, d))
+
+
+def fw_layer_norm_backward(x, gamma, dout, dsum=None, eps: float = 1e-5, return_params: bool = True, dx=None,
+                           workspace=None, stream=None):
+    """Gradients of fw_layer_norm at what it normalised (x, or the sum it
+    returned) from dout, with the residual stream's own gradient dsum added to
+    dx: (dx, dgamma or None, dbeta or None)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fw_layer_norm_backward(x, gamma, dout, dsum, eps, return_params, dx, workspace)
+    lib = load()
+    st = _here("x gamma dout dsum dx workspace", x, gamma, dout, dsum, dx, workspace)
+    rows, d = _layer_norm_shapes(x, (gamma,), (dout, dsum, dx))
+    if dx is None:
+        dx = torch.empty_like(x)
+    dgamma = dbeta = None
+    ws_bytes = 0
+    if return_params:
+        dgamma, dbeta = (torch.empty(d, dtype=torch.float32, device=x.device) for _ in range(2))
+        workspace, ws_bytes = _scratch(_size("fw_layer_norm_backward_workspace_size", rows, d), workspace, x)
+    rc = lib.fw_layer_norm_backward(x.data_ptr(), _data(gamma), dout.data_ptr(), _data(dsum), dx.data_ptr(), _data(dgamma),
+                                    _data(dbeta), _data(workspace), ws_bytes, rows, d, eps, _dtype_code(x.dtype), st)
+    _check(rc, "fw_layer_norm_backward")
+    return dx, dgamma, dbeta
+
+
+def _vocab_shapes(h, W, targets, bias, floats):
+    """(N, V, D) of h [..., D], W [V,D] and targets [...]."""
+    if h.dim() < 1 or W.dim() != 2 or h.shape[-1] != W.shape[1] or targets.shape != h.shape[:-1]:
+        raise ValueError("h must be [..., D], W [V,D] and targets [...]")
+    if h.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
+        raise TypeError("h and W must be bf16")
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != W.shape[:1]):
+        raise ValueError("bias must be fp32 [V]")
+    for t in floats:
+        if t is not None and (t.dtype != torch.float32 or t.shape != targets.shape):
+            raise ValueError("loss, lse and dloss must be fp32 of the targets' shape")
+    N, (V, D) = targets.numel(), W.shape
+    if max(N, V, D) > 0x7FFFFFFF:
+        raise ValueError("every size must be below 2^31")
+    return N, V, D
+
+
+def fw_vocab_loss_workspace_size(N, V, D) -> int:
+    return int(load().fw_vocab_loss_workspace_size(N, V, D))
+
+
+def fw_vocab_loss(h, W, targets, bias=None, loss=None, lse=None, workspace=None, stream=None):
+    """Softmax cross entropy of the answers h [..., D] over the vocabulary of
+    the output map W [V,D] (bf16; bias fp32 [V] or None), without keeping the
+    logits: (loss, lse), fp32 of the targets' shape.  A negative target is
+    padding: both are 0."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fw_vocab_loss(h, W, targets, bias, loss, lse, workspace)
+    st = _here("h W targets bias loss lse workspace", h, W, targets, bias, loss, lse, workspace)
+    N, V, D = _vocab_shapes(h, W, targets, bias, (loss, lse))
+    if loss is None:
+        loss = torch.empty(targets.shape, dtype=torch.float32, device=h.device)
+    if lse is None:
+        lse = torch.empty_like(loss)
+    workspace, ws_bytes = _scratch(_size("fw_vocab_loss_workspace_size", N, V, D), workspace, h)
+    rc = load().fw_vocab_loss(h.data_ptr(), W.data_ptr(), _data(bias), targets.data_ptr(), loss.data_ptr(), lse.data_ptr(),
+                              workspace.data_ptr(), ws_bytes, N, V, D, _index_type(targets, "targets"), st)
+    _check(rc, "fw_vocab_loss")
+    return loss, lse
+
+
+def fw_vocab_loss_backward_workspace_size(N, V, D) -> int:
+    return int(load().fw_vocab_loss_backward_workspace_size(N, V, D))
+
+
+def fw_vocab_loss_backward(h, W, targets, loss, lse, dloss, bias=None, return_dh: bool = True, return_dW: bool = True,
+                           workspace=None, stream=None):
+    """Gradients of sum(dloss loss) from what fw_vocab_loss returned:
+    (dh or None, dW or None, dbias or None without a bias)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fw_vocab_loss_backward(h, W, targets, loss, lse, dloss, bias, return_dh, return_dW, workspace)
+    lib = load()
+    st = _here("h W targets loss lse dloss bias workspace", h, W, targets, loss, lse, dloss, bias, workspace)
+    N, V, D = _vocab_shapes(h, W, targets, bias, (loss, lse, dloss))
+    dh = torch.empty_like(h) if return_dh else None
+    dW = torch.empty_like(W) if return_dW else None
+    dbias = None if bias is None else torch.empty_like(bias)
+    workspace, ws_bytes = _scratch(_size("fw_vocab_loss_backward_workspace_size", N, V, D), workspace, h)
+    rc = lib.fw_vocab_loss_backward(h.data_ptr(), W.data_ptr(), _data(bias), targets.data_ptr(), loss.data_ptr(),
+                                    lse.data_ptr(), dloss.data_ptr(), _data(dh), _data(dW), _data(dbias),
+                                    workspace.data_ptr(), ws_bytes, N, V, D, _index_type(targets, "targets"), st)
+    _check(rc, "fw_vocab_loss_backward")
+    return dh, dW, dbias

@@ -50,6 +50,8 @@ cudaError_t tc_prepare_x_launch(const void *x, const void *W_all, int ldw, void 
 // A 2-D TMA map of a row-major bf16 matrix [rows, cols] (row stride ld
 // elements) in boxes of box_rows x 64 columns, 128-byte swizzle.
 cudaError_t make_bf16_map(CUtensorMap *map, const void *base, int rows, int cols, int ld, int box_rows);
+// The same of an fp32 matrix, in boxes of box_rows x 32 columns.
+cudaError_t make_f32_sw128_map(CUtensorMap *map, const void *base, int rows, int cols, int ld, int box_rows);
 
 // The sum rule (linear attention), bf16 I/O: W_i = W_{i-1} + v_i phi(k_i)^T,
 // y_i = W_i phi(q_i), divided by z_i . phi(q_i) (z_i = sum of phi(k)) when

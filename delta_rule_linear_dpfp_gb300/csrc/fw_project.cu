@@ -613,6 +613,20 @@ cudaError_t make_bf16_map(CUtensorMap *map, const void *base, int rows, int cols
     return make_map(map, base, rows, cols, ld, box_rows);
 }
 
+cudaError_t make_f32_sw128_map(CUtensorMap *map, const void *base, int rows, int cols, int ld, int box_rows) {
+    EncodeTiled fn = encoder();
+    if (!fn)
+        return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 4};
+    const cuuint32_t box[2] = {32u, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1u, 1u};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void *>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 int gemm_slices(int M, int N, int K) {
     const int tiles = ((M + 127) / 128) * ((N + 127) / 128), nk = K / 64;
     if (tiles >= kTargetCtas / 2 || nk <= 1)

@@ -1,0 +1,871 @@
+// fw_vocab.cu -- the loss at a model's end: softmax cross entropy of the
+// answers h [N, D] over a vocabulary whose output map is W [V, D], with the
+// gradients, without the N x V logits.
+//
+//   z_n = W h_n + b;  lse_n = log sum_v exp z_nv;  loss_n = lse_n - z_n,t
+//   g_nv = dloss_n (exp(z_nv - lse_n) - [v = t_n])
+//   dh = g W,  dW = g^T h,  db = sum_n g_n
+// for the target t_n of token n; tokens whose target is negative are padding
+// (no loss, no gradient, whatever h holds).
+//
+// Bound by the tensor cores: 2 N V D operations forward, 6 N V D backward (the
+// logits are formed again).  All four products run on one kernel: a pair of
+// CTAs (two SMs) owns 256 x 256 tiles of the output, the operands come by TMA in
+// steps of 64 of the contraction, each CTA fetching half of A's rows and half of
+// B's, and one thread of the pair issues the MMAs (tcgen05, cta_group::2, fp32
+// accumulators in both CTAs' TMEM, 128 rows each).  A tile's accumulator takes
+// half of TMEM, so the epilogue of one tile (8 warps, 128 columns of a row per
+// thread) runs while the next is formed.
+//
+// Forward: the epilogue turns a row's 128 columns into (max, sum of
+// exponentials) and picks out the target's logit; a second kernel joins a
+// token's parts.  Backward, by pieces of the vocabulary of at most 512 MB of
+// (bf16) g: one product forms the logits again and its epilogue writes
+//   G = (exp(z - lse) - [v = t]) / q,   q = 1 - p_t = -expm1(-loss),
+// then dh += G W and dW = G^T (w h) with w = q dloss (dh's rows take w at the
+// end, in 32 bits).  What is rounded to bf16 on the way is G, whose largest entry
+// is exactly -1 at the target, and w h, element by element: errors that are as
+// independent as those of the rounded outputs.  Rounding (p - 1) dloss itself
+// would put one relative error of up to 2^-8 into a whole row of dh and dW.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "fw_ends.h"
+#include "fw_forward_tc.h"
+#include "fw_pairs.cuh"
+#include "fw_tc.cuh"
+
+namespace fw {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kT = 384;       // warp 0: copies, 1: products, 2: TMEM, 4 .. 11: epilogue
+constexpr int kTile = 256;    // rows and columns of a pair's tile
+constexpr int kStages = 5;
+constexpr int kStageBytes = 32768; // half of A's rows and half of B's, 64 of the contraction
+constexpr int kOutOff = kStages * kStageBytes;
+constexpr int kOutBytes = 8 * 8192; // two boxes of 32 rows x 128 bytes per epilogue warp
+constexpr int kBarOff = kOutOff + kOutBytes;
+constexpr int kSmem = kBarOff + 256 + 1024;
+static_assert(kSmem <= 227 * 1024, "one CTA's shared memory");
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kQMin = 1e-7f; // q below it (p_t = 1 in 32 bits) divides nothing
+
+enum Mode {
+    kLoss, // parts of the logits' log-sum-exp, the targets' logits
+    kGrad, // G, and its columns' sums
+    kSum,  // the product in fp32, written or added
+    kOut   // the product in bf16
+};
+
+struct GemmArgs {
+    int mt, nt;         // tiles of the output
+    int kb, per, splits; // 64-steps of the contraction, and those of a split (kSum)
+    int group;          // tile rows that are walked together
+    int b0;             // B's first row: this piece's first vocabulary entry (kOut: 0)
+    int N, V;           // rows and columns of the output that are there
+    int rows_a_split;   // kSum: rows between the splits' outputs
+    int add;            // kSum: added to what is there
+    const float *bias;  // kLoss, kGrad: of this piece, or null
+    Tokens targets;
+    int vocab;          // all of the vocabulary's entries
+    float2 *part;       // kLoss: [ceil(V / 128)][N] (max, sum)
+    float *target_z;    // kLoss: [N]
+    const float *loss, *lse, *dloss;
+    float *colsum;      // kGrad: [ceil(N / 32)][ldc] or null
+    int ldc;
+};
+
+FW_DEV uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+FW_DEV void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+FW_DEV uint32_t leader_addr(const void *p) { // the pair's first CTA's location of the same name
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+    return a;
+}
+// A box into this CTA's shared memory, its bytes counted on the leader's barrier.
+FW_DEV void tma_load_pair(void *dst, const void *map, int x, int y, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+FW_DEV void tma_store(const void *map, const void *src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(src)), "r"(x), "r"(y)
+                 : "memory");
+}
+FW_DEV void tma_add(const void *map, const void *src, int x, int y) {
+    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(src)), "r"(x), "r"(y)
+                 : "memory");
+}
+FW_DEV void bulk_wait_read_but_one() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+FW_DEV void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+// Arrive on `bar` of both CTAs once every MMA issued so far has completed.
+FW_DEV void commit_pair(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     smem_u32(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+FW_DEV void arrive_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+FW_DEV void tmem_ld32(uint32_t taddr, float (&r)[32]) {
+    uint32_t u[32];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+                   "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]),
+                   "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]),
+                   "=r"(u[23]), "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]),
+                   "=r"(u[30]), "=r"(u[31])
+                 : "r"(taddr));
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        r[i] = __uint_as_float(u[i]);
+}
+
+// Columns c0 .. c0 + 31 of a row of logits: bias added, -inf past the vocabulary.
+FW_DEV void finish_logits(float (&z)[32], const GemmArgs &a, int c0) {
+    if (a.bias && c0 + 32 <= a.V) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            const float4 b = __ldcg(reinterpret_cast<const float4 *>(a.bias + c0 + j));
+            z[j] += b.x;
+            z[j + 1] += b.y;
+            z[j + 2] += b.z;
+            z[j + 3] += b.w;
+        }
+    } else if (c0 + 32 > a.V) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            z[j] = c0 + j < a.V ? z[j] + (a.bias ? __ldcg(a.bias + c0 + j) : 0.f) : -INFINITY;
+    }
+}
+
+// Lane l's sum over the warp's lanes of x[l]: halves are exchanged and added.
+FW_DEV float columns_sum(float (&x)[32], int lane) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int j = 0; j < o; ++j) {
+            const float give = up ? x[j] : x[j + o], keep = up ? x[j + o] : x[j];
+            x[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    }
+    return x[0];
+}
+
+// A_MN, B_MN: the operand's memory runs along the output (its rows are the contraction).
+template <Mode MODE, bool A_MN, bool B_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
+    vocab_gemm_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                      const __grid_constant__ CUtensorMap tc_, GemmArgs g, unsigned *status) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *full = (uint64_t *)(smem + kBarOff); // [kStages] (leader's) both CTAs' copies of a step have landed
+    uint64_t *empty = full + kStages;              // [kStages] the step's MMAs are done
+    uint64_t *ready = empty + kStages;             // [2] a tile's accumulator is complete
+    uint64_t *taken = ready + 2;                   // [2] (leader's) ... and has been read by both CTAs
+    uint32_t *slot = (uint32_t *)(taken + 2);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int a_split = g.mt * g.nt, tiles = a_split * g.splits;
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(ready + s, 1);
+            mbar_init(taken + s, 16);
+        }
+        fence_barrier_init();
+    }
+    if (warp == 2) { // (both CTAs' warps: the allocation is the pair's)
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync(); // the barriers stand in both CTAs
+    tc_fence_after();
+    griddep_launch_dependents();
+    griddep_wait();
+    g.bias = after_wait(g.bias);
+    g.targets.p = after_wait(g.targets.p);
+    g.loss = after_wait(g.loss);
+    g.lse = after_wait(g.lse);
+    g.dloss = after_wait(g.dloss);
+    const uint32_t tm = *slot;
+
+    // tile t of this pair's walk: rows mb, columns nb (groups of tile rows, column by column), split z
+    struct At {
+        int mb, nb, k0, k1, z;
+    };
+    auto tile_at = [&](int t) {
+        At p;
+        p.z = t / a_split;
+        int r = t - p.z * a_split;
+        const int whole = g.group * g.nt, gi = r / whole;
+        r -= gi * whole;
+        const int rows = min(g.group, g.mt - gi * g.group);
+        p.nb = r / rows;
+        p.mb = gi * g.group + r - p.nb * rows;
+        p.k0 = p.z * g.per;
+        p.k1 = min(g.kb, p.k0 + g.per);
+        return p;
+    };
+
+    if (warp == 0 && lane == 0) { // copies
+        uint32_t step = 0;
+        bool ok = true;
+        for (int t = pair; ok && t < tiles; t += pairs) {
+            const At p = tile_at(t);
+            const int m = p.mb * kTile + (int)rank * 128, n = p.nb * kTile + (int)rank * 128;
+            for (int k = p.k0; k < p.k1; ++k, ++step) {
+                const uint32_t s = step % kStages, use = step / kStages;
+                if (use > 0 && !mbar_wait(empty + s, (use - 1) & 1, status)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t *a = smem + s * kStageBytes, *b = a + 16384;
+                const uint32_t bar = leader_addr(full + s);
+                if (rank == 0)
+                    mbar_arrive_expect_tx(full + s, 2 * kStageBytes);
+                if (A_MN) {
+                    tma_load_pair(a, &ta, m, 64 * k, bar);
+                    tma_load_pair(a + 8192, &ta, m + 64, 64 * k, bar);
+                } else {
+                    tma_load_pair(a, &ta, 64 * k, m, bar);
+                }
+                if (B_MN) {
+                    tma_load_pair(b, &tb, n, g.b0 + 64 * k, bar);
+                    tma_load_pair(b + 8192, &tb, n + 64, g.b0 + 64 * k, bar);
+                } else {
+                    tma_load_pair(b, &tb, 64 * k, g.b0 + n, bar);
+                }
+            }
+        }
+        // no arrival of the MMAs' commits is under way to this CTA when it leaves
+        for (uint32_t s = 0; ok && s < kStages && s < step; ++s) {
+            const uint32_t uses = (step - s + kStages - 1) / kStages;
+            ok = mbar_wait(empty + s, (uses - 1) & 1, status);
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) { // products
+        const uint32_t idesc = idesc_bf16(256, 256, A_MN, B_MN);
+        uint32_t step = 0, it = 0;
+        bool ok = true;
+        for (int t = pair; ok && t < tiles; t += pairs, ++it) {
+            const At p = tile_at(t);
+            const uint32_t buf = it & 1, d = tm + buf * 256;
+            if (it >= 2 && !mbar_wait(taken + buf, ((it >> 1) - 1) & 1, status))
+                break;
+            tc_fence_after();
+            for (int k = p.k0; k < p.k1; ++k, ++step) {
+                const uint32_t s = step % kStages;
+                if (!mbar_wait(full + s, (step / kStages) & 1, status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t a = smem_u32(smem + s * kStageBytes), b = a + 16384;
+#pragma unroll
+                for (int st = 0; st < 4; ++st) {
+                    const uint64_t da = A_MN ? desc_sw128(a + st * 2048, 8192, 1024) : desc_sw128(a + st * 32, 16, 1024);
+                    const uint64_t db = B_MN ? desc_sw128(b + st * 2048, 8192, 1024) : desc_sw128(b + st * 32, 16, 1024);
+                    mma_pair(d, da, db, idesc, k > p.k0 || st > 0);
+                }
+                commit_pair(empty + s);
+            }
+            commit_pair(ready + buf);
+        }
+        // every read of an accumulator has been told of
+        for (uint32_t buf = 0; ok && buf < 2 && buf < it; ++buf)
+            ok = mbar_wait(taken + buf, (((it - buf + 1) >> 1) - 1) & 1, status);
+    } else if (warp >= 4) { // epilogue: lane = row
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        uint8_t *out = smem + kOutOff + (warp - 4) * 8192;
+        uint32_t it = 0, box = 0; // tiles, and boxes stored, so far
+        // the next staging box, free of earlier stores
+        auto next_box = [&]() {
+            if (lane == 0)
+                bulk_wait_read_but_one();
+            __syncwarp();
+            return out + (box++ & 1) * 4096;
+        };
+        auto put = [&](uint8_t *to, int x, int y, bool there) { // the box leaves
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (there) {
+                    if (MODE == kSum && g.add)
+                        tma_add(&tc_, to, x, y);
+                    else
+                        tma_store(&tc_, to, x, y);
+                }
+                bulk_commit();
+            }
+        };
+        for (int t = pair; t < tiles; t += pairs, ++it) {
+            const At p = tile_at(t);
+            const uint32_t buf = it & 1;
+            const int row0 = p.mb * kTile + (int)rank * 128 + 32 * quarter, row = row0 + lane;
+            const int col0 = p.nb * kTile + 128 * half;
+            int target = -1;
+            float lse = 0.f, rq = 0.f, at_target = 0.f, weight = 0.f;
+            if (MODE == kLoss || MODE == kGrad) {
+                if (row < g.N) {
+                    target = token_at(g.targets, row, g.vocab);
+                    if (target == g.vocab) // past the vocabulary: the loss is NaN, there is no gradient
+                        target = -1;
+                }
+                if (MODE == kGrad && target >= 0) {
+                    const float qt = -expm1f(-__ldcg(g.loss + row));
+                    lse = __ldcg(g.lse + row);
+                    weight = __ldcg(g.dloss + row);
+                    rq = 1.f / fmaxf(qt, kQMin);
+                    at_target = -qt;
+                }
+                target -= g.b0; // (negative: not in this piece, or none)
+            }
+            const bool live = rq != 0.f;
+            if (!mbar_wait(ready + buf, (it >> 1) & 1, status))
+                break;
+            tc_fence_after();
+            const uint32_t acc = tm + tmem_lane_base(warp) + buf * 256 + 128 * half;
+            if (MODE == kLoss) {
+                float top = -INFINITY, total = 0.f;
+#pragma unroll 1
+                for (int c = 0; c < 128 && col0 + c < g.V; c += 32) {
+                    float z[32];
+                    tmem_ld32(acc + c, z);
+                    finish_logits(z, g, col0 + c);
+                    const int k = target - col0 - c;
+                    if (k >= 0 && k < 32) {
+                        float tz = z[0];
+#pragma unroll
+                        for (int j = 1; j < 32; ++j)
+                            tz = j == k ? z[j] : tz;
+                        g.target_z[row] = tz;
+                    }
+                    float m = z[0];
+#pragma unroll
+                    for (int j = 1; j < 32; ++j)
+                        m = fmaxf(m, z[j]);
+                    m = fmaxf(m, top);
+                    const float ref = m == -INFINITY ? 0.f : m; // (a part that is masked throughout sums to 0)
+                    total *= ex2((top - ref) * kLog2e);
+                    top = m;
+                    F2 s = {0};
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float2 e = unpack((pack(z[j], z[j + 1]) + both(-ref)) * both(kLog2e));
+                        s = s + pack(ex2(e.x), ex2(e.y));
+                    }
+                    total += sum(s);
+                }
+                if (row < g.N && col0 < g.V)
+                    g.part[(size_t)(col0 / 128) * g.N + row] = make_float2(top, total);
+            } else if (MODE == kGrad) {
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 64) {
+                    uint8_t *to = next_box();
+#pragma unroll 1
+                    for (int c1 = c; c1 < c + 64; c1 += 32) {
+                        float z[32];
+                        tmem_ld32(acc + c1, z);
+                        finish_logits(z, g, col0 + c1);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            const float2 e = unpack((pack(z[j], z[j + 1]) + both(-lse)) * both(kLog2e));
+                            z[j] = live ? ex2(e.x) : 0.f;
+                            z[j + 1] = live ? ex2(e.y) : 0.f;
+                        }
+                        const int k = target - col0 - c1;
+                        if (k >= 0 && k < 32)
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                z[j] = j == k ? at_target : z[j];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) {
+                            uint4 u;
+                            u.x = pack_bf16x2(z[j] * rq, z[j + 1] * rq);
+                            u.y = pack_bf16x2(z[j + 2] * rq, z[j + 3] * rq);
+                            u.z = pack_bf16x2(z[j + 4] * rq, z[j + 5] * rq);
+                            u.w = pack_bf16x2(z[j + 6] * rq, z[j + 7] * rq);
+                            *reinterpret_cast<uint4 *>(to + lane * 128 + ((((c1 - c + j) >> 3) ^ (lane & 7)) << 4)) = u;
+                        }
+                        if (g.colsum) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                z[j] *= weight;
+                            const float s = columns_sum(z, lane);
+                            if (row0 < g.N)
+                                g.colsum[(size_t)(row0 / 32) * g.ldc + col0 + c1 + lane] = s;
+                        }
+                    }
+                    put(to, col0 + c, row0, row0 < g.N);
+                }
+            } else {
+                constexpr int kW = MODE == kOut ? 64 : 32; // columns of a box of 128 bytes
+                const int y = row0 + (MODE == kSum ? p.z * g.rows_a_split : 0);
+#pragma unroll 1
+                for (int c = 0; c < 128; c += kW) {
+                    uint8_t *to = next_box();
+#pragma unroll
+                    for (int c1 = 0; c1 < kW; c1 += 32) {
+                        float z[32];
+                        tmem_ld32(acc + c + c1, z);
+                        if (MODE == kOut) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 8) {
+                                uint4 u;
+                                u.x = pack_bf16x2(z[j], z[j + 1]);
+                                u.y = pack_bf16x2(z[j + 2], z[j + 3]);
+                                u.z = pack_bf16x2(z[j + 4], z[j + 5]);
+                                u.w = pack_bf16x2(z[j + 6], z[j + 7]);
+                                *reinterpret_cast<uint4 *>(to + lane * 128 + ((((c1 + j) >> 3) ^ (lane & 7)) << 4)) = u;
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4)
+                                *reinterpret_cast<float4 *>(to + lane * 128 + (((j >> 2) ^ (lane & 7)) << 4)) =
+                                    make_float4(z[j], z[j + 1], z[j + 2], z[j + 3]);
+                        }
+                    }
+                    put(to, col0 + c, y, row0 < g.N && col0 + c < g.V);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                arrive_at(leader_addr(taken + buf));
+        }
+        if (MODE != kLoss && lane == 0)
+            bulk_wait_all();
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync(); // nothing is under way between the CTAs
+    tc_fence_after();
+    if (warp == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512) : "memory");
+}
+
+// ------------------------------------------------------------ small kernels
+constexpr int kS = 256;
+
+// A token's parts joined: 32 tokens of a CTA and 8 threads for each, or one
+// token and 256 where there are few.
+__global__ void __launch_bounds__(kS)
+    join_parts_kernel(const float2 *part, const float *target_z, Tokens targets, float *loss, float *lse, int N, int V,
+                      int nparts, int tokens) {
+    __shared__ float2 red[kS];
+    griddep_launch_dependents();
+    griddep_wait();
+    part = after_wait(part);
+    target_z = after_wait(target_z);
+    targets.p = after_wait(targets.p);
+    const int slices = kS / tokens, i = threadIdx.x % tokens, w = threadIdx.x / tokens;
+    const int n = blockIdx.x * tokens + i;
+    float top = -INFINITY, total = 0.f;
+    auto join = [&](float2 p) {
+        const float m = fmaxf(top, p.x), ref = m == -INFINITY ? 0.f : m;
+        total = total * ex2((top - ref) * kLog2e) + p.y * ex2((p.x - ref) * kLog2e);
+        top = m;
+    };
+    if (n < N)
+        for (int k = w; k < nparts; k += 8 * slices) {
+            float2 p[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                p[u] = k + u * slices < nparts ? __ldcg(part + (size_t)(k + u * slices) * N + n)
+                                               : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                join(p[u]);
+        }
+    red[threadIdx.x] = make_float2(top, total);
+    for (int o = slices / 2; o > 0; o >>= 1) {
+        __syncthreads();
+        if (w < o) {
+            join(red[threadIdx.x + o * tokens]);
+            red[threadIdx.x] = make_float2(top, total);
+        }
+    }
+    if (w == 0 && n < N) {
+        const int t = token_at(targets, n, V);
+        const float l = logf(total);
+        loss[n] = t < 0 ? 0.f : t >= V ? __int_as_float(0x7fffffff) : (top - __ldcg(target_z + n)) + l;
+        lse[n] = t < 0 ? 0.f : top + l;
+    }
+}
+
+// w_n of a token, 0 for one without a gradient.
+FW_DEV float token_weight(const Tokens &targets, const float *loss, const float *dloss, int n, int V) {
+    const int t = token_at(targets, n, V);
+    return t < 0 || t >= V ? 0.f : fmaxf(-expm1f(-__ldcg(loss + n)), kQMin) * __ldcg(dloss + n);
+}
+FW_DEV bool has_target(const Tokens &targets, int n, int V) {
+    const int t = token_at(targets, n, V);
+    return t >= 0 && t < V;
+}
+
+// w h in bf16; zeros for the tokens without a gradient, whatever h holds there.
+__global__ void __launch_bounds__(kS)
+    weighted_rows_kernel(const __nv_bfloat16 *h, Tokens targets, const float *loss, const float *dloss,
+                         __nv_bfloat16 *wh, int N, int V, int D, int lg) {
+    griddep_launch_dependents();
+    griddep_wait();
+    h = after_wait(h);
+    targets.p = after_wait(targets.p);
+    loss = after_wait(loss);
+    dloss = after_wait(dloss);
+    const int n = (int)(blockIdx.x * (kS >> lg) + (threadIdx.x >> lg)), lane = threadIdx.x & ((1 << lg) - 1);
+    if (n >= N)
+        return;
+    const bool live = has_target(targets, n, V);
+    const float w = token_weight(targets, loss, dloss, n, V);
+    for (int c = 8 * lane; c < D; c += 8 << lg) {
+        float v[8];
+        if (live)
+            load8(h + (size_t)n * D + c, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = live ? w * v[e] : 0.f;
+        store8(wh + (size_t)n * D + c, v);
+    }
+}
+
+// The splits' sums joined in order, rounded once; TOKENS: rows are tokens and
+// take their weight.
+template <bool TOKENS>
+__global__ void __launch_bounds__(kS)
+    join_splits_kernel(const float *part, __nv_bfloat16 *out, int rows, int D, int splits, int64_t a_split, Tokens targets,
+                       const float *loss, const float *dloss, int V, int lg) {
+    griddep_launch_dependents();
+    griddep_wait();
+    part = after_wait(part);
+    targets.p = after_wait(targets.p);
+    loss = after_wait(loss);
+    dloss = after_wait(dloss);
+    const int n = (int)(blockIdx.x * (kS >> lg) + (threadIdx.x >> lg)), lane = threadIdx.x & ((1 << lg) - 1);
+    if (n >= rows)
+        return;
+    const bool live = !TOKENS || has_target(targets, n, V);
+    const float w = TOKENS ? token_weight(targets, loss, dloss, n, V) : 1.f;
+    for (int c = 8 * lane; c < D; c += 8 << lg) {
+        float s[8] = {};
+        if (live)
+            for (int z = 0; z < splits; ++z) {
+                float v[8];
+                load8(part + z * a_split + (int64_t)n * D + c, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    s[e] += v[e];
+            }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            s[e] = live ? s[e] * w : 0.f;
+        store8(out + (size_t)n * D + c, s);
+    }
+}
+
+// dbias of a piece: the sums of 32 tokens each, in order.
+__global__ void __launch_bounds__(kS)
+    join_bias_kernel(const float *colsum, float *dbias, int V, int blocks, int ldc) {
+    __shared__ float red[kS / 32][33];
+    griddep_launch_dependents();
+    griddep_wait();
+    colsum = after_wait(colsum);
+    const int i = threadIdx.x & 31, w = threadIdx.x >> 5, v = blockIdx.x * 32 + i;
+    float s = 0.f;
+    for (int k = w; k < blocks; k += kS / 32 * 8) {
+        float t[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            t[u] = k + u * (kS / 32) < blocks ? __ldcg(colsum + (size_t)(k + u * (kS / 32)) * ldc + v) : 0.f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            s += t[u];
+    }
+    red[w][i] = s;
+    __syncthreads();
+    if (w == 0 && v < V) {
+        s = 0.f;
+#pragma unroll
+        for (int k = 0; k < kS / 32; ++k)
+            s += red[k][i];
+        dbias[v] = s;
+    }
+}
+
+// ------------------------------------------------------------------- plans
+constexpr int kPairs = 76; // of a GB300's SMs: what the splits (and so the workspaces) go by
+constexpr size_t kPieceBytes = (size_t)512 << 20;
+
+int tiles_of(int64_t n) { return (int)((n + kTile - 1) / kTile); }
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Splits of a contraction of kb steps for an output of `tiles`: where the
+// tiles leave more than half of the pairs idle, as many as fill them, of four
+// steps at least.
+struct Splits {
+    int n, per;
+};
+Splits splits_of(int64_t tiles, int kb) {
+    int64_t n = tiles * 2 > kPairs ? 1 : std::min<int64_t>(kPairs / tiles, (kb + 3) / 4);
+    n = std::max<int64_t>(1, n);
+    const int per = (int)((kb + n - 1) / n);
+    return {(kb + per - 1) / per, per};
+}
+
+struct Plan {
+    int width;      // vocabulary entries of a piece (a multiple of 256)
+    int ldg;        // row stride of G
+    Splits dh, dw;
+    size_t G, wh, dh_part, dw_part, colsum, bytes; // offsets
+};
+Plan plan_of(int N, int V, int D) {
+    Plan p;
+    const int vt = tiles_of(V), kt = (D + kTile - 1) / kTile;
+    const int64_t most = std::max<int64_t>(1, (int64_t)(kPieceBytes / ((size_t)2 * kTile * N)));
+    const int64_t pieces = (vt + most - 1) / most;
+    p.width = (int)((vt + pieces - 1) / pieces) * kTile;
+    p.ldg = p.width;
+    p.dh = splits_of((int64_t)tiles_of(N) * kt, (std::min(p.width, V) + 63) / 64);
+    p.dw = splits_of((int64_t)(p.width / kTile) * kt, (N + 63) / 64);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += up256(bytes);
+        return o;
+    };
+    p.G = take((size_t)2 * N * p.ldg);
+    p.wh = take((size_t)2 * N * D);
+    p.dh_part = take((size_t)4 * p.dh.n * tiles_of(N) * kTile * D);
+    p.dw_part = take(p.dw.n > 1 ? (size_t)4 * p.dw.n * p.width * D : 0);
+    p.colsum = take((size_t)4 * ((N + 31) / 32) * p.width);
+    p.bytes = at;
+    return p;
+}
+
+// log2 of the threads of a row of D channels, 8 a thread (at most a CTA's).
+int group_log2(int D) {
+    int lg = 0;
+    while ((8 << lg) < D && lg < 8)
+        ++lg;
+    return lg;
+}
+
+// Pairs of CTAs that the device runs at once.
+template <typename K> cudaError_t pairs_of(K *kern, int *out) {
+    static std::atomic<int> known[64]; // by device; what it holds does not depend on who asks first
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const int have = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (have > 0) {
+        *out = have;
+        return cudaSuccess;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kT);
+    cfg.dynamicSmemBytes = kSmem;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+    if (e != cudaSuccess)
+        return e;
+    n = std::max(1, n);
+    if (dev < 64)
+        known[dev].store(n, std::memory_order_relaxed);
+    *out = n;
+    return cudaSuccess;
+}
+
+template <Mode MODE, bool A_MN, bool B_MN>
+cudaError_t launch_gemm(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tc_, const GemmArgs &g,
+                        cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    auto kern = vocab_gemm_kernel<MODE, A_MN, B_MN>;
+    cudaError_t e = allow_smem(kern, done);
+    unsigned *status = nullptr;
+    if (e == cudaSuccess)
+        e = status_word(&status);
+    int pairs = 0;
+    if (e == cudaSuccess)
+        e = pairs_of(kern, &pairs);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t tiles = (int64_t)g.mt * g.nt * g.splits;
+    return launch_pdl(kern, dim3((unsigned)(2 * std::min<int64_t>(pairs, tiles))), dim3(kT), kSmem, st, ta, tb, tc_, g,
+                      status);
+}
+
+// Tile rows walked together in the products over tokens: their rows of A stay in L2 (32 MB of them).
+int token_group(int N, int D) { return (int)std::max<int64_t>(8, std::min<int64_t>(tiles_of(N), (32 << 20) / ((int64_t)kTile * D * 2))); }
+
+} // namespace
+
+size_t vocab_loss_workspace_bytes(int N, int V, int D) {
+    (void)D;
+    return up256(sizeof(float2) * (size_t)((V + 127) / 128) * N) + up256(sizeof(float) * (size_t)N);
+}
+
+cudaError_t launch_vocab_loss(const void *h, const void *W, const float *bias, Tokens targets, float *loss, float *lse,
+                              void *workspace, int N, int V, int D, cudaStream_t st) {
+    const int nparts = (V + 127) / 128;
+    GemmArgs g = {};
+    g.mt = tiles_of(N);
+    g.nt = tiles_of(V);
+    g.kb = g.per = (D + 63) / 64;
+    g.splits = 1;
+    g.group = token_group(N, D);
+    g.N = N;
+    g.V = g.vocab = V;
+    g.bias = bias;
+    g.targets = targets;
+    g.part = static_cast<float2 *>(workspace);
+    g.target_z = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + up256(sizeof(float2) * (size_t)nparts * N));
+    CUtensorMap ta, tb;
+    cudaError_t e = make_bf16_map(&ta, h, N, D, D, 128);
+    if (e == cudaSuccess)
+        e = make_bf16_map(&tb, W, V, D, D, 128);
+    if (e == cudaSuccess)
+        e = launch_gemm<kLoss, false, false>(ta, tb, ta, g, st);
+    if (e != cudaSuccess)
+        return e;
+    const int tokens = N < 512 ? 1 : 32;
+    return launch_pdl(join_parts_kernel, dim3((N + tokens - 1) / tokens), dim3(kS), 0, st, (const float2 *)g.part,
+                      (const float *)g.target_z, targets, loss, lse, N, V, nparts, tokens);
+}
+
+size_t vocab_loss_backward_workspace_bytes(int N, int V, int D) { return plan_of(N, V, D).bytes; }
+
+cudaError_t launch_vocab_loss_backward(const void *h, const void *W, const float *bias, Tokens targets,
+                                       const float *loss, const float *lse, const float *dloss, void *dh, void *dW,
+                                       float *dbias, void *workspace, int N, int V, int D, cudaStream_t st) {
+    const Plan p = plan_of(N, V, D);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    __nv_bfloat16 *G = reinterpret_cast<__nv_bfloat16 *>(ws + p.G), *wh = reinterpret_cast<__nv_bfloat16 *>(ws + p.wh);
+    float *dh_part = reinterpret_cast<float *>(ws + p.dh_part), *dw_part = reinterpret_cast<float *>(ws + p.dw_part);
+    float *colsum = reinterpret_cast<float *>(ws + p.colsum);
+    const int nb = tiles_of(N), dt = (D + kTile - 1) / kTile, lg = group_log2(D), per_cta = kS >> lg;
+    CUtensorMap th, tw, tg, tg_t, tw_t, tdh, twh, tdw;
+    cudaError_t e = make_bf16_map(&th, h, N, D, D, 128);
+    if (e == cudaSuccess) e = make_bf16_map(&tw, W, V, D, D, 128);
+    if (e == cudaSuccess) e = make_bf16_map(&tw_t, W, V, D, D, 64);
+    if (e == cudaSuccess) e = make_bf16_map(&twh, wh, N, D, D, 64);
+    if (e == cudaSuccess) e = make_f32_sw128_map(&tdh, dh_part, p.dh.n * nb * kTile, D, D, 32);
+    if (e == cudaSuccess && dW)
+        e = launch_pdl(weighted_rows_kernel, dim3((N + per_cta - 1) / per_cta), dim3(kS), 0, st, (const __nv_bfloat16 *)h,
+                       targets, loss, dloss, wh, N, V, D, lg);
+    for (int v0 = 0; e == cudaSuccess && v0 < V; v0 += p.width) {
+        const int nv = std::min(p.width, V - v0), vt = tiles_of(nv);
+        CUtensorMap tgs;
+        e = make_bf16_map(&tg, G, N, p.ldg, p.ldg, 128);
+        if (e == cudaSuccess) e = make_bf16_map(&tgs, G, N, p.ldg, p.ldg, 32);
+        if (e == cudaSuccess) e = make_bf16_map(&tg_t, G, N, p.ldg, p.ldg, 64);
+        if (e != cudaSuccess)
+            break;
+        GemmArgs g = {};
+        g.mt = nb;
+        g.nt = vt;
+        g.kb = g.per = (D + 63) / 64;
+        g.splits = 1;
+        g.group = token_group(N, D);
+        g.b0 = v0;
+        g.N = N;
+        g.V = nv;
+        g.vocab = V;
+        g.bias = bias ? bias + v0 : nullptr;
+        g.targets = targets;
+        g.loss = loss;
+        g.lse = lse;
+        g.dloss = dloss;
+        g.colsum = dbias ? colsum : nullptr;
+        g.ldc = p.width;
+        e = launch_gemm<kGrad, false, false>(th, tw, tgs, g, st);
+        if (e == cudaSuccess && dbias)
+            e = launch_pdl(join_bias_kernel, dim3((nv + 31) / 32), dim3(kS), 0, st, (const float *)colsum, dbias + v0, nv,
+                           (N + 31) / 32, p.width);
+        if (e != cudaSuccess)
+            break;
+        if (dh) {
+            GemmArgs q = {};
+            q.mt = nb;
+            q.nt = dt;
+            q.kb = (nv + 63) / 64;
+            q.per = p.dh.per;
+            q.splits = (q.kb + q.per - 1) / q.per;
+            q.group = 8;
+            q.b0 = v0;
+            q.N = N;
+            q.V = D;
+            q.rows_a_split = nb * kTile;
+            q.add = v0 > 0;
+            e = launch_gemm<kSum, false, true>(tg, tw_t, tdh, q, st);
+        }
+        if (e == cudaSuccess && dW) {
+            GemmArgs q = {};
+            q.mt = vt;
+            q.nt = dt;
+            q.kb = (N + 63) / 64;
+            q.group = 8;
+            q.N = nv;
+            q.V = D;
+            __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(dW) + (size_t)v0 * D;
+            q.per = p.dw.per;
+            q.splits = p.dw.n;
+            if (p.dw.n == 1) {
+                e = make_bf16_map(&tdw, to, nv, D, D, 32);
+                if (e == cudaSuccess)
+                    e = launch_gemm<kOut, true, true>(tg_t, twh, tdw, q, st);
+            } else {
+                q.rows_a_split = p.width;
+                e = make_f32_sw128_map(&tdw, dw_part, p.dw.n * p.width, D, D, 32);
+                if (e == cudaSuccess)
+                    e = launch_gemm<kSum, true, true>(tg_t, twh, tdw, q, st);
+                if (e == cudaSuccess)
+                    e = launch_pdl(join_splits_kernel<false>, dim3((nv + per_cta - 1) / per_cta), dim3(kS), 0, st,
+                                   (const float *)dw_part, to, nv, D, p.dw.n, (int64_t)p.width * D, targets, loss, dloss, V,
+                                   lg);
+            }
+        }
+    }
+    if (e == cudaSuccess && dh)
+        e = launch_pdl(join_splits_kernel<true>, dim3((N + per_cta - 1) / per_cta), dim3(kS), 0, st, (const float *)dh_part,
+                       static_cast<__nv_bfloat16 *>(dh), N, D, p.dh.n, (int64_t)nb * kTile * D, targets, loss, dloss, V, lg);
+    return e;
+}
+
+} // namespace fw

@@ -560,6 +560,126 @@ FW_API int fw_group_norm_act_backward(const void *x, const void *gate, const flo
                                       int act, int io_dtype, float eps, void *stream);
 
 /*
+ * A model's two ends and the norm between its parts: the embedding of its
+ * tokens, the layer norm with the residual sum before it, and the softmax
+ * cross entropy of its answers over the vocabulary, each with its gradients.
+ * [Fast Weights Transformer guide, section "layer and model assembly" (the
+ * norm, the residual sums), and its training experiment (an embedding, the
+ * stack, a linear output map, the cross entropy over the characters)]
+ *
+ * Tokens (ids, targets) are int32 or int64, aligned to their own size.  A NEGATIVE token is padding: its
+ * row of the embedding is zero, its loss and lse are 0, and it has no part in
+ * any gradient, whatever its rows of h, dout and dloss hold (NaN as well).  A
+ * token at or past V is an error that cannot be seen on the host: its row of
+ * the embedding and its loss are NaN, and it has no part in any gradient.
+ *
+ * D is a multiple of 8 (FW_ERR_UNSUPPORTED otherwise), up to 65536; the layer
+ * norm's d up to 8192.  Calls return FW_ERR_INVALID_ARG for null or misaligned
+ * pointers, bad sizes, a scale or eps that is not finite, eps < 0 or a small
+ * workspace.  No call uses state of the library, so calls with workspaces of
+ * their own may run at the same time.  Results do not depend on the run (fixed
+ * summation orders, no atomics on values).
+ */
+typedef enum fw_index {
+    FW_INDEX_I32 = 0,
+    FW_INDEX_I64 = 1
+} fw_index;
+
+/*
+ * fw_embedding -- out_n = scale table[ids_n].
+ *   ids   : [N]     fw_index
+ *   table : [V, D]  io_dtype
+ *   out   : [N, D]  io_dtype   (written)
+ */
+FW_API int fw_embedding(const void *ids, const void *table, void *out, int64_t N, int V, int D, float scale,
+                        int index_type, int io_dtype, void *stream);
+
+/* About N (16 + D / 8) + 8 V bytes. */
+FW_API size_t fw_embedding_backward_workspace_size(int64_t N, int V, int D);
+
+/*
+ * fw_embedding_backward -- dtable[v] = scale (the sum of dout_n over the n
+ * with ids_n = v, in 32 bits, in the order of n), rounded once; with
+ * accumulate 1 that is added to what dtable holds (an output map that shares
+ * the table: its own gradient), and rows without a token are left as they are.
+ *   dout   : [N, D]  io_dtype
+ *   dtable : [V, D]  io_dtype   (written; read and written with accumulate)
+ */
+FW_API int fw_embedding_backward(const void *ids, const void *dout, void *dtable, void *workspace,
+                                 size_t workspace_bytes, int64_t N, int V, int D, float scale, int accumulate,
+                                 int index_type, int io_dtype, void *stream);
+
+/*
+ * fw_layer_norm -- s = x + residual (in 32 bits; x alone without a residual),
+ *   out = (s - mean(s)) / sqrt(var(s) + eps) gamma + beta
+ * over the d channels of a row (the biased variance).
+ *   x, residual, out, sum : [rows, d]  io_dtype; residual may be NULL, and sum
+ *                           (s, rounded) is written exactly when it is not
+ *   gamma, beta           : [d] fp32, or NULL (one / zero)
+ * out may be x, and sum may be x or residual (in place).
+ */
+FW_API int fw_layer_norm(const void *x, const void *residual, const float *gamma, const float *beta, void *out,
+                         void *sum, int64_t rows, int d, float eps, int io_dtype, void *stream);
+
+FW_API size_t fw_layer_norm_backward_workspace_size(int64_t rows, int d);
+
+/*
+ * fw_layer_norm_backward -- gradients from dout, at what was normalised (x
+ * without a residual, sum with one).
+ *   dsum          : the gradient that sum gets from elsewhere (the residual
+ *                   stream), added to dx; or NULL
+ *   dx            : [rows, d] io_dtype, the gradient of x (and of residual:
+ *                   they are the same)                          (written)
+ *   dgamma, dbeta : [d] fp32, summed over the rows in a fixed order; both NULL
+ *                   to skip them (the workspace is then not used)
+ * dx may be dout or dsum (in place).
+ */
+FW_API int fw_layer_norm_backward(const void *x, const float *gamma, const void *dout, const void *dsum, void *dx,
+                                  float *dgamma, float *dbeta, void *workspace, size_t workspace_bytes, int64_t rows,
+                                  int d, float eps, int io_dtype, void *stream);
+
+/* About 8 N V / 128 bytes: the logits are not kept. */
+FW_API size_t fw_vocab_loss_workspace_size(int N, int V, int D);
+
+/*
+ * fw_vocab_loss -- softmax cross entropy of N answers over a vocabulary:
+ *   z_n = W h_n + bias,  lse_n = log sum_v exp(z_nv),  loss_n = lse_n - z_n,target
+ *   h       : [N, D]  bf16
+ *   W       : [V, D]  bf16 (an embedding's table, for one)
+ *   bias    : [V]     fp32, or NULL; -infinity takes an entry out of the
+ *             vocabulary (its gradient is zero)
+ *   targets : [N]     fw_index
+ *   loss, lse : [N]   fp32     (written)
+ * Products of bf16 values summed in fp32 on the tensor cores, everything after
+ * them in fp32.  Any V; a token whose entries are all taken out has a NaN loss.
+ */
+FW_API int fw_vocab_loss(const void *h, const void *W, const float *bias, const void *targets, float *loss, float *lse,
+                         void *workspace, size_t workspace_bytes, int N, int V, int D, int index_type, void *stream);
+
+/*
+ * 2 N (V + D) bytes for a small vocabulary; a large one is worked off in pieces
+ * of N tokens x up to 512 MB of bf16 values, plus fp32 sums of dh.
+ */
+FW_API size_t fw_vocab_loss_backward_workspace_size(int N, int V, int D);
+
+/*
+ * fw_vocab_loss_backward -- gradients of sum_n dloss_n loss_n.
+ *   loss, lse : [N] fp32, as fw_vocab_loss wrote them for the same inputs
+ *   dloss     : [N] fp32
+ *   dh        : [N, D] bf16, dW : [V, D] bf16, dbias : [V] fp32, each written,
+ *               or NULL to skip it
+ * The logits are formed again; the softmax's gradient is rounded to bf16 on
+ * its way into the products with W and h, relative to 1 - exp(-loss) so that
+ * the target's entry is exact, and h times that and dloss once more: dh and dW
+ * are off by about what rounding them to bf16 alone costs.  dbias is in fp32
+ * throughout.
+ */
+FW_API int fw_vocab_loss_backward(const void *h, const void *W, const float *bias, const void *targets,
+                                  const float *loss, const float *lse, const float *dloss, void *dh, void *dW,
+                                  float *dbias, void *workspace, size_t workspace_bytes, int N, int V, int D,
+                                  int index_type, void *stream);
+
+/*
  * fw_device_status -- waits for `stream`, then reports and clears the
  * device-side status word of the current device: FW_ERR_TIMEOUT if any
  * kernel of this library gave up a bounded wait (its outputs are then
