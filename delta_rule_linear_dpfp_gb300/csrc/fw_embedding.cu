@@ -8,20 +8,19 @@
 // Bound by the bytes: each row that is named is read once for every time it is
 // named (from L2 where it is named often), each row of the output written once.
 //
-// The gradient goes by sorted tokens, so that every row is summed by one
-// group of threads in the order of the tokens (no atomics, the same bits in
-// every run), in three kernels:
+// The gradient goes by sorted tokens, so that every row is summed in the order
+// of the tokens (no atomics, the same bits in every run), in three kernels:
 //  1. One cluster of eight CTAs sorts the pairs (id, n) by id, eight bits at
 //     a time from the lowest, each pass stable.  A CTA owns an eighth of the
 //     sequence; the counts of the digits are exchanged through distributed
-//     shared memory; inside a tile of 4096 pairs a warp owns 128 and ranks
-//     equal digits by a match among its lanes.  Then begin and end of every
-//     id's run are noted by id.
-//  2. Where 32 pairs in a row from a multiple of 32 on have one id, their rows
-//     are added in 32 bits: a token that makes up a sixteenth of the batch is
-//     read by as many CTAs as it fills chunks.
-//  3. A group of threads per table row adds what the run has before, in and
-//     behind such chunks, and rounds once; rows without a token get zeros.
+//     shared memory; a warp owns 32 to 128 pairs in a row and ranks equal digits
+//     by a match among its lanes.  The sort is all latency and takes eight SMs:
+//     the others write the table's zeros meanwhile.
+//  2. A group of threads sums 32 sorted pairs (8 where there are few), run by run:
+//     a run that ends on both sides is rounded and written, one that goes on
+//     beyond leaves its sum in 32 bits.  Every group reads as many rows as any
+//     other, whatever a token's share of the batch is.
+//  3. The group in which such a run begins adds its parts in order.
 #include "fw_common.cuh"
 #include "fw_ends.h"
 #include "fw_pairs.cuh"
@@ -34,20 +33,31 @@ namespace {
 
 constexpr int kT = 256;
 
-FW_DEV void load8_cs(const float *p, float (&o)[8]) {
-    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-    o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
-    o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
-}
-FW_DEV void load8_cs(const __nv_bfloat16 *p, float (&o)[8]) {
-    const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(p));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        o[2 * i] = __uint_as_float(w[i] << 16);
-        o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// 8 channels as they were loaded, read once.
+template <typename T> struct Raw;
+template <> struct Raw<float> {
+    float4 a, b;
+    FW_DEV void load(const float *p) {
+        a = __ldcs(reinterpret_cast<const float4 *>(p));
+        b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
     }
-}
+    FW_DEV void add_to(float (&s)[8]) const {
+        s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
+        s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
+    }
+};
+template <> struct Raw<__nv_bfloat16> {
+    uint4 u;
+    FW_DEV void load(const __nv_bfloat16 *p) { u = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+    FW_DEV void add_to(float (&s)[8]) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s[2 * i] += __uint_as_float(w[i] << 16);
+            s[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
 
 // ------------------------------------------------------------------ lookup
 // A group of 2^lg threads takes kAhead rows at a time: their ids, then their
@@ -107,7 +117,8 @@ struct SortArgs {
     Tokens ids;
     int N, V, passes;
     int *key[2], *pos[2]; // the pairs, from one to the other and back
-    int *begin, *end;     // [V] of each id's run (0, 0 for none)
+    uint4 *zeros;         // what the CTAs past the first cluster fill, or null
+    int64_t nzeros;
 };
 
 // The lanes of the warp that hold this lane's digit (among `live` lanes).
@@ -117,16 +128,23 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortT) sort_
     __shared__ unsigned hist[256], offset[256], rows[kWarps][256];
     __shared__ unsigned scan[8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    unsigned rank;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     griddep_launch_dependents();
     griddep_wait();
+    if (blockIdx.x >= kCluster) { // (whole clusters: no barrier of theirs is left out)
+        const int64_t step = (int64_t)(gridDim.x - kCluster) * kSortT;
+        for (int64_t i = (int64_t)(blockIdx.x - kCluster) * kSortT + tid; i < a.nzeros; i += step)
+            a.zeros[i] = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    const unsigned rank = blockIdx.x;
     a.ids.p = after_wait(a.ids.p);
-    for (int64_t v = (int64_t)rank * kSortT + tid; v < a.V; v += kCluster * kSortT)
-        a.begin[v] = a.end[v] = 0;
-    // this CTA's part of the sequence, in whole tiles
-    const int64_t tiles = ((int64_t)a.N + kTile - 1) / kTile, mine = (tiles + kCluster - 1) / kCluster;
-    const int64_t lo = min((int64_t)a.N, mine * rank * kTile), hi = min((int64_t)a.N, mine * (rank + 1) * kTile);
+    // this CTA's part of the sequence: a multiple of 32 pairs, or of a tile where it does not fit one
+    int64_t part = (((int64_t)a.N + kCluster - 1) / kCluster + 31) / 32 * 32;
+    const bool one = part <= kTile;
+    if (!one)
+        part = (part + kTile - 1) / kTile * kTile;
+    const int64_t lo = min((int64_t)a.N, part * rank), hi = min((int64_t)a.N, part * (rank + 1));
+    const int per = one ? (int)((part + kSortT - 1) / kSortT) : kPerLane; // pairs of a lane in a tile
 
     for (int pass = 0; pass < a.passes; ++pass) {
         const int shift = 8 * pass;
@@ -138,15 +156,71 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortT) sort_
             const int t = token_at(a.ids, i, a.V);
             return t < 0 ? a.V : t; // padding behind every row
         };
-        if (tid < 256)
-            hist[tid] = 0;
-        __syncthreads();
-        for (int64_t i0 = lo; i0 < hi; i0 += kSortT) {
-            const int64_t i = i0 + tid;
-            const unsigned live = i < hi, digit = live ? (unsigned)key_at(i) >> shift & 255u : 0u;
-            const unsigned same = peers(digit, live);
-            if (live && lane == __ffs(same) - 1)
-                atomicAdd(hist + digit, __popc(same));
+        int key[kPerLane], pos[kPerLane];
+        unsigned at[kPerLane]; // rank among the warp's pairs with this digit
+        int64_t w0 = 0;
+        // a tile's pairs into registers, ranked; rows[w][d] = how many of warp w have digit d
+        auto rank_tile = [&](int64_t t0) {
+            w0 = t0 + (int64_t)warp * 32 * per + lane;
+#pragma unroll
+            for (int u = 0; u < kPerLane; ++u) {
+                const int64_t i = w0 + 32 * u;
+                const bool live = u < per && i < hi;
+                key[u] = live ? key_at(i) : 0;
+                pos[u] = live ? (pass ? __ldcg(pos_in + i) : (int)i) : 0;
+            }
+            for (int e = lane; e < 256; e += 32)
+                rows[warp][e] = 0;
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < kPerLane; ++u)
+                if (u < per) {
+                    const unsigned live = w0 + 32 * u < hi, digit = (unsigned)key[u] >> shift & 255u;
+                    const unsigned same = peers(live ? digit : 0u, live);
+                    const unsigned seen = rows[warp][digit];
+                    at[u] = seen + __popc(same & ((1u << lane) - 1));
+                    __syncwarp();
+                    if (live && lane == __ffs(same) - 1)
+                        rows[warp][digit] = seen + __popc(same);
+                    __syncwarp();
+                }
+            __syncthreads();
+        };
+        // rows[w][d] = o[d] + what the warps before w have of digit d; returns o + all (threads below 256)
+        auto scan_warps = [&](unsigned o) {
+#pragma unroll 16
+            for (int k = 0; k < kWarps; ++k) {
+                const unsigned n = rows[k][tid];
+                rows[k][tid] = o;
+                o += n;
+            }
+            return o;
+        };
+        auto scatter = [&](bool add) {
+#pragma unroll
+            for (int u = 0; u < kPerLane; ++u)
+                if (u < per && w0 + 32 * u < hi) {
+                    const unsigned d = (unsigned)key[u] >> shift & 255u;
+                    const unsigned o = rows[warp][d] + at[u] + (add ? offset[d] : 0u);
+                    key_out[o] = key[u];
+                    pos_out[o] = pos[u];
+                }
+        };
+        if (one) {
+            rank_tile(lo);
+            if (tid < 256)
+                hist[tid] = scan_warps(0);
+        } else {
+            if (tid < 256)
+                hist[tid] = 0;
+            __syncthreads();
+            for (int64_t i0 = lo; i0 < hi; i0 += kSortT) {
+                const int64_t i = i0 + tid;
+                const unsigned live = i < hi, digit = live ? (unsigned)key_at(i) >> shift & 255u : 0u;
+                const unsigned same = peers(digit, live);
+                if (live && lane == __ffs(same) - 1)
+                    atomicAdd(hist + digit, __popc(same));
+            }
         }
         cluster_sync(); // every CTA's counts stand
         if (tid < 256) {
@@ -170,181 +244,155 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortT) sort_
                 upto += scan[k];
             offset[tid] = upto - all + before;
         }
-        cluster_sync(); // (the counts are read: a CTA may clear its own)
-        for (int64_t t0 = lo; t0 < hi; t0 += kTile) {
-            for (int e = lane; e < 256; e += 32)
-                rows[warp][e] = 0;
-            __syncwarp();
-            int key[kPerLane], pos[kPerLane];
-            unsigned at[kPerLane]; // rank among the warp's pairs with this digit
-            const int64_t w0 = t0 + (int64_t)warp * 32 * kPerLane + lane;
-#pragma unroll
-            for (int u = 0; u < kPerLane; ++u) {
-                const int64_t i = w0 + 32 * u;
-                key[u] = i < hi ? key_at(i) : 0;
-                pos[u] = i < hi ? (pass ? __ldcg(pos_in + i) : (int)i) : 0;
-            }
-#pragma unroll
-            for (int u = 0; u < kPerLane; ++u) {
-                const unsigned live = w0 + 32 * u < hi, digit = (unsigned)key[u] >> shift & 255u;
-                const unsigned same = peers(live ? digit : 0u, live);
-                const unsigned seen = rows[warp][digit];
-                at[u] = seen + __popc(same & ((1u << lane) - 1));
-                __syncwarp();
-                if (live && lane == __ffs(same) - 1)
-                    rows[warp][digit] = seen + __popc(same);
-                __syncwarp();
-            }
+        if (one) {
             __syncthreads();
-            if (tid < 256) { // where each warp's pairs of this digit begin
-                unsigned o = offset[tid];
-#pragma unroll 8
-                for (int k = 0; k < kWarps; ++k) {
-                    const unsigned n = rows[k][tid];
-                    rows[k][tid] = o;
-                    o += n;
-                }
-                offset[tid] = o;
+            scatter(true);
+        } else {
+            cluster_sync(); // (the counts are read: a CTA may clear its own)
+            for (int64_t t0 = lo; t0 < hi; t0 += kTile) {
+                rank_tile(t0);
+                if (tid < 256)
+                    offset[tid] = scan_warps(offset[tid]);
+                __syncthreads();
+                scatter(false);
+                __syncwarp(); // (a warp clears its own row alone)
             }
-            __syncthreads();
-#pragma unroll
-            for (int u = 0; u < kPerLane; ++u)
-                if (w0 + 32 * u < hi) {
-                    const unsigned o = rows[warp][(unsigned)key[u] >> shift & 255u] + at[u];
-                    key_out[o] = key[u];
-                    pos_out[o] = pos[u];
-                }
-            __syncwarp(); // (a warp clears its own row alone)
         }
-        cluster_sync(); // the pairs stand, for every CTA
-    }
-    const int *key = a.passes & 1 ? a.key[1] : a.key[0];
-    for (int64_t i = lo + tid; i < hi; i += kSortT) {
-        const int k = __ldcg(key + i);
-        if (k < a.V) {
-            if (i == 0 || __ldcg(key + i - 1) != k)
-                a.begin[k] = (int)i;
-            if (i == a.N - 1 || __ldcg(key + i + 1) != k)
-                a.end[k] = (int)i + 1;
-        }
+        cluster_sync(); // the pairs stand, for every CTA; its counts are read
     }
 }
 
 // -------------------------------------------------------------------- sums
-constexpr int kChunk = 32;
+// Rows in flight: 128 bytes a thread.
+template <typename T> constexpr int kFlight = sizeof(T) == 2 ? 8 : 4;
 
-// The sum of rows pos[i], i = from, from + step, ... < to, 8 channels at c, added to s.
-template <typename T>
-FW_DEV void add_rows(const T *dout, const int *pos, int from, int to, int step, int D, int c, float (&s)[8]) {
-    constexpr int kU = 4; // rows in flight
-    int i = from;
-    for (; i + (kU - 1) * step < to; i += kU * step) {
-        float v[kU][8];
+struct SumArgs {
+    const int *key, *pos; // sorted
+    float *part;          // [chunks][2][D]: of the run that comes in, of the one that goes on
+    int N, V, D, lg, lgc; // 2^lg threads a group, 2^lgc pairs a chunk
+    float scale;
+    int accumulate;
+};
+
+template <typename T> FW_DEV void write_row(const SumArgs &a, T *to, float (&s)[8]) {
+    float old[8] = {};
+    if (a.accumulate)
+        load8(to, old);
 #pragma unroll
-        for (int u = 0; u < kU; ++u)
-            load8_cs(dout + (int64_t)__ldcg(pos + i + u * step) * D + c, v[u]);
-#pragma unroll
-        for (int u = 0; u < kU; ++u)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                s[e] += v[u][e];
-    }
-    for (; i < to; i += step) {
-        float v[8];
-        load8_cs(dout + (int64_t)__ldcg(pos + i) * D + c, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            s[e] += v[e];
-    }
+    for (int x = 0; x < 8; ++x)
+        s[x] = a.accumulate ? fmaf(s[x], a.scale, old[x]) : s[x] * a.scale;
+    store8(to, s);
 }
 
-// part[k] = the sum of chunk k's rows, where all of its 32 pairs have one id.
 template <typename T>
-__global__ void __launch_bounds__(kT)
-    chunk_sums_kernel(const int *key, const int *pos, const T *dout, float *part, int N, int V, int D, int lg) {
+__global__ void __launch_bounds__(kT, 3) chunk_sums_kernel(SumArgs a, const T *dout, T *dtable) {
     griddep_launch_dependents();
     griddep_wait();
-    key = after_wait(key);
-    pos = after_wait(pos);
+    a.key = after_wait(a.key);
+    a.pos = after_wait(a.pos);
     dout = after_wait(dout);
-    const int lane = threadIdx.x & ((1 << lg) - 1), per = kT >> lg;
-    const int k = blockIdx.x * per + (threadIdx.x >> lg);
-    if (k >= N / kChunk)
+    const int t = threadIdx.x & ((1 << a.lg) - 1), lane = threadIdx.x & 31;
+    const int64_t k = (int64_t)blockIdx.x * (kT >> a.lg) + (threadIdx.x >> a.lg), i0 = k << a.lgc;
+    const int count = (int)min((int64_t)1 << a.lgc, a.N - i0); // (groups are whole warps)
+    if (count <= 0)
         return;
-    const int i0 = k * kChunk;
-    const int id = __ldcg(key + i0);
-    if (id >= V || __ldcg(key + i0 + kChunk - 1) != id)
-        return;
-    for (int c = 8 * lane; c < D; c += 8 << lg) {
+    // a lane holds a pair; what comes before and behind
+    const int key = lane < count ? __ldcg(a.key + i0 + lane) : -1, pos = lane < count ? __ldcg(a.pos + i0 + lane) : 0;
+    const int left = i0 > 0 ? __ldcg(a.key + i0 - 1) : -1;
+    const int right = i0 + count < a.N ? __ldcg(a.key + i0 + count) : -1;
+    for (int c = 8 * t; c - 8 * t < a.D; c += 8 << a.lg) {
+        const bool on = c < a.D;
         float s[8] = {};
-        add_rows(dout, pos, i0, i0 + kChunk, 1, D, c, s);
-        store8(part + (int64_t)k * D + c, s);
-    }
-}
-
-// Table rows v0 .. v0 + kRows - 1 of each group of 2^lg threads.
-constexpr int kRows = 4;
-template <typename T>
-__global__ void __launch_bounds__(kT)
-    table_rows_kernel(const int *begin, const int *end, const int *pos, const T *dout, const float *part, T *dtable, int V,
-                      int D, int lg, float scale, int accumulate) {
-    griddep_launch_dependents();
-    griddep_wait();
-    begin = after_wait(begin);
-    end = after_wait(end);
-    pos = after_wait(pos);
-    dout = after_wait(dout);
-    part = after_wait(part);
-    const int lane = threadIdx.x & ((1 << lg) - 1), per = kT >> lg;
-    const int64_t v0 = ((int64_t)blockIdx.x * per + (threadIdx.x >> lg)) * kRows;
-    int b[kRows], e[kRows];
+        bool comes_in = __shfl_sync(0xffffffffu, key, 0) == left;
+        for (int j0 = 0; j0 < count; j0 += kFlight<T>) {
+            Raw<T> v[kFlight<T>];
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-        b[u] = v0 + u < V ? __ldcg(begin + v0 + u) : 0;
-        e[u] = v0 + u < V ? __ldcg(end + v0 + u) : 0;
-    }
+            for (int u = 0; u < kFlight<T>; ++u) {
+                const int p = __shfl_sync(0xffffffffu, pos, j0 + u), id = __shfl_sync(0xffffffffu, key, j0 + u);
+                if (on && id >= 0 && id < a.V)
+                    v[u].load(dout + (int64_t)p * a.D + c);
+            }
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-        if (v0 + u >= V || (accumulate && b[u] == e[u]))
-            continue;
-        for (int c = 8 * lane; c < D; c += 8 << lg) {
-            float s[8] = {};
-            // the whole chunks inside the run, and what is before and behind them
-            const int k0 = (b[u] + kChunk - 1) / kChunk, k1 = e[u] / kChunk;
-            if (k0 < k1) {
-                add_rows(dout, pos, b[u], k0 * kChunk, 1, D, c, s);
-                int k = k0;
-                for (; k + 3 < k1; k += 4) {
-                    float t[4][8];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        load8_cs(part + (int64_t)(k + j) * D + c, t[j]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int x = 0; x < 8; ++x)
-                            s[x] += t[j][x];
-                }
-                for (; k < k1; ++k) {
-                    float t[8];
-                    load8_cs(part + (int64_t)k * D + c, t);
+            for (int u = 0; u < kFlight<T>; ++u) {
+                const int j = j0 + u;
+                if (j >= count)
+                    break;
+                const int id = __shfl_sync(0xffffffffu, key, j);
+                const int next = j + 1 < count ? __shfl_sync(0xffffffffu, key, (j + 1) & 31) : right;
+                if (id >= a.V) // padding: nothing behind it either
+                    break;
+                v[u].add_to(s);
+                const bool last = j + 1 == count, goes_on = last && next == id;
+                if (next != id || last) {
+                    if (on) {
+                        if (comes_in || goes_on)
+                            store8(a.part + (2 * k + (comes_in ? 0 : 1)) * a.D + c, s);
+                        else
+                            write_row(a, dtable + (int64_t)id * a.D + c, s);
+                    }
+                    comes_in = false;
 #pragma unroll
                     for (int x = 0; x < 8; ++x)
-                        s[x] += t[x];
+                        s[x] = 0.f;
                 }
-                add_rows(dout, pos, k1 * kChunk, e[u], 1, D, c, s);
-            } else {
-                add_rows(dout, pos, b[u], e[u], 1, D, c, s);
             }
-            T *to = dtable + (v0 + u) * D + c;
-            float old[8] = {};
-            if (accumulate)
-                load8(to, old);
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-                s[x] = accumulate ? fmaf(s[x], scale, old[x]) : s[x] * scale;
-            store8(to, s);
         }
+    }
+}
+
+// The run that begins in chunk k and goes on beyond it: a CTA, its groups of
+// threads taking the parts in turn.
+template <typename T>
+__global__ void __launch_bounds__(kT) join_runs_kernel(SumArgs a, T *dtable) {
+    __shared__ float red[kT * 8];
+    griddep_launch_dependents();
+    griddep_wait();
+    a.key = after_wait(a.key);
+    a.part = after_wait(a.part);
+    const int64_t k = blockIdx.x, i0 = k << a.lgc, size = (int64_t)1 << a.lgc;
+    if (i0 + size >= a.N)
+        return;
+    const int id = __ldcg(a.key + i0 + size - 1);
+    if (id >= a.V || __ldcg(a.key + i0 + size) != id || (__ldcg(a.key + i0) == id && i0 > 0 && __ldcg(a.key + i0 - 1) == id))
+        return;
+    // the chunks after this one that the run comes into: their first pair has its id
+    int64_t end = k + 1;
+    for (bool more = true; more;) {
+        const int64_t i = (end + (threadIdx.x & 31)) << a.lgc;
+        const unsigned in = __ballot_sync(0xffffffffu, i < a.N && __ldcg(a.key + i) == id);
+        const int n = in == 0xffffffffu ? 32 : __ffs(~in) - 1;
+        end += n;
+        more = n == 32;
+    }
+    const int t = threadIdx.x & ((1 << a.lg) - 1), g = threadIdx.x >> a.lg, groups = kT >> a.lg;
+    for (int c = 8 * t; c - 8 * t < a.D; c += 8 << a.lg) {
+        const bool on = c < a.D;
+        float s[8] = {};
+        constexpr int kU = 4;
+        if (on)
+            for (int64_t j = k + g; j < end; j += groups * kU) {
+                Raw<float> v[kU];
+#pragma unroll
+                for (int u = 0; u < kU; ++u)
+                    if (j + u * groups < end)
+                        v[u].load(a.part + (2 * (j + u * groups) + (j + u * groups == k ? 1 : 0)) * a.D + c);
+#pragma unroll
+                for (int u = 0; u < kU; ++u)
+                    if (j + u * groups < end)
+                        v[u].add_to(s);
+            }
+        if (groups > 1) {
+            __syncthreads();
+            store8(red + threadIdx.x * 8, s);
+            __syncthreads();
+            if (g == 0)
+                for (int o = 1; o < groups; ++o)
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        s[x] += red[((o << a.lg) + t) * 8 + x];
+        }
+        if (on && g == 0)
+            write_row(a, dtable + (int64_t)id * a.D + c, s);
     }
 }
 
@@ -364,20 +412,18 @@ cudaError_t lookup(Tokens ids, const void *table, void *out, int64_t N, int V, i
                       (T *)out, N, V, D, lg, scale);
 }
 
+// Pairs of a chunk: 8 where the chunks are too few to occupy the SMs otherwise.
+int chunk_log2(int N) { return N <= 8192 ? 3 : 5; }
+int64_t chunks_of(int N) { return ((int64_t)N + (1 << chunk_log2(N)) - 1) >> chunk_log2(N); }
+
 template <typename T>
-cudaError_t sums(const SortArgs &a, const void *dout, void *dtable, float *part, int D, float scale, int accumulate,
-                 cudaStream_t st) {
-    const int lg = group_log2(D), per = kT >> lg, chunks = a.N / kChunk;
-    const int *key = a.key[a.passes & 1], *pos = a.pos[a.passes & 1];
-    if (chunks) {
-        const cudaError_t e = launch_pdl(chunk_sums_kernel<T>, dim3((chunks + per - 1) / per), dim3(kT), 0, st, key, pos,
-                                         (const T *)dout, part, a.N, a.V, D, lg);
-        if (e != cudaSuccess)
-            return e;
-    }
-    return launch_pdl(table_rows_kernel<T>, dim3((unsigned)(((int64_t)a.V + per * kRows - 1) / (per * kRows))), dim3(kT), 0, st,
-                      (const int *)a.begin, (const int *)a.end, pos, (const T *)dout, (const float *)part, (T *)dtable, a.V,
-                      D, lg, scale, accumulate);
+cudaError_t sums(const SumArgs &a, const void *dout, void *dtable, cudaStream_t st) {
+    const int64_t chunks = chunks_of(a.N), per = kT >> a.lg;
+    const cudaError_t e = launch_pdl(chunk_sums_kernel<T>, dim3((unsigned)((chunks + per - 1) / per)), dim3(kT), 0, st, a,
+                                     (const T *)dout, (T *)dtable);
+    if (e != cudaSuccess || chunks == 1)
+        return e;
+    return launch_pdl(join_runs_kernel<T>, dim3((unsigned)(chunks - 1)), dim3(kT), 0, st, a, (T *)dtable);
 }
 
 } // namespace
@@ -388,9 +434,10 @@ cudaError_t launch_embedding(Tokens ids, const void *table, void *out, int64_t N
                 : lookup<float>(ids, table, out, N, V, D, scale, st);
 }
 
-// keys and positions twice, begin and end of each id's run, the chunks' sums
+// keys and positions twice, two sums of each chunk
 size_t embedding_backward_workspace_bytes(int N, int V, int D) {
-    return 4 * up256(4 * (size_t)N) + 2 * up256(4 * (size_t)V) + up256(4 * (size_t)(N / kChunk) * D);
+    (void)V;
+    return 4 * up256(4 * (size_t)N) + 8 * (size_t)chunks_of(N) * D;
 }
 
 cudaError_t launch_embedding_backward(Tokens ids, const void *dout, void *dtable, void *workspace, int N, int V, int D,
@@ -402,23 +449,22 @@ cudaError_t launch_embedding_backward(Tokens ids, const void *dout, void *dtable
     while (a.passes < 4 && ((unsigned)V >> (8 * a.passes)) != 0) // keys are 0 .. V
         ++a.passes;
     uint8_t *p = static_cast<uint8_t *>(workspace);
-    auto take = [&](size_t bytes) {
-        uint8_t *q = p;
-        p += up256(bytes);
-        return q;
-    };
-    for (int i = 0; i < 2; ++i) {
-        a.key[i] = reinterpret_cast<int *>(take(4 * (size_t)N));
-        a.pos[i] = reinterpret_cast<int *>(take(4 * (size_t)N));
+    for (int **to : {&a.key[0], &a.key[1], &a.pos[0], &a.pos[1]}) {
+        *to = reinterpret_cast<int *>(p);
+        p += up256(4 * (size_t)N);
     }
-    a.begin = reinterpret_cast<int *>(take(4 * (size_t)V));
-    a.end = reinterpret_cast<int *>(take(4 * (size_t)V));
-    float *part = reinterpret_cast<float *>(p);
-    const cudaError_t e = launch_pdl(sort_tokens_kernel, dim3(kCluster), dim3(kSortT), 0, st, a);
+    // the table's zeros: 64 KB at least a CTA, whole clusters, two CTAs an SM at most
+    const int64_t vecs = accumulate ? 0 : (int64_t)V * D / (bf16 ? 8 : 4);
+    a.zeros = static_cast<uint4 *>(dtable);
+    a.nzeros = vecs;
+    const int64_t more = std::min<int64_t>((vecs + 8 * 4096 - 1) / (8 * 4096), 2 * 152 / kCluster - 1);
+    cudaError_t e = launch_pdl(sort_tokens_kernel, dim3((unsigned)(kCluster * (1 + more))), dim3(kSortT), 0, st, a);
     if (e != cudaSuccess)
         return e;
-    return bf16 ? sums<__nv_bfloat16>(a, dout, dtable, part, D, scale, accumulate, st)
-                : sums<float>(a, dout, dtable, part, D, scale, accumulate, st);
+    const int lg = std::max(5, group_log2(D)); // (whole warps)
+    const SumArgs s = {a.passes & 1 ? a.key[1] : a.key[0], a.passes & 1 ? a.pos[1] : a.pos[0], reinterpret_cast<float *>(p),
+                       N, V, D, lg, chunk_log2(N), scale, accumulate};
+    return bf16 ? sums<__nv_bfloat16>(s, dout, dtable, st) : sums<float>(s, dout, dtable, st);
 }
 
 } // namespace fw

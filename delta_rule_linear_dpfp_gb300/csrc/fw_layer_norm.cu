@@ -218,60 +218,70 @@ __global__ void __launch_bounds__(G > 32 ? G : kT, an_sm<G>(true))
     F2 ga[4], dga[4] = {}, dbe[4] = {};
     param_pairs(gamma, row.c, row.on, 1.f, ga);
     Walk<G> w(rows);
-    Raw<T> rx, rd, rs;
-    auto request = [&](int64_t r) {
-        const bool here = row.on && r < w.rows;
-        rx.load(x + r * d + row.c, here);
-        rd.load(dout + r * d + row.c, here);
+    constexpr int kAhead = sizeof(T) == 2 && G < 1024 ? 2 : 1; // rows requested ahead (1024 threads: registers)
+    Raw<T> rx[kAhead], rd[kAhead], rs[kAhead];
+    int64_t ahead = w.at; // the next row to request
+    auto request = [&](int u) {
+        const bool here = row.on && ahead < w.rows;
+        rx[u].load(x + ahead * d + row.c, here);
+        rd[u].load(dout + ahead * d + row.c, here);
         if (RES)
-            rs.load(dsum + r * d + row.c, here);
+            rs[u].load(dsum + ahead * d + row.c, here);
+        ahead += w.step;
     };
-    request(w.at);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+        request(u);
     int turn = 0;
-    for (int64_t base = w.at - (G > 32 ? 0 : threadIdx.x / G); base < rows; base += w.step, turn ^= 1) {
-        F2 s[4], dn[4], more[4];
-        const int64_t at = w.at;
-        const bool mine = row.on && at < rows;
-        rx.widen(s);
-        rd.widen(dn);
-        if (RES)
-            rs.widen(more);
-        w.at += w.step;
-        request(w.at);
-        const float2 st = centre<G>(s, row);
-        F2 t1 = {0}, t2 = {0};
+    for (int64_t base = w.at - (G > 32 ? 0 : threadIdx.x / G); base < rows; base += kAhead * w.step) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            dbe[e] = dbe[e] + dn[e];
-            const F2 g = dn[e] * ga[e];
-            t1 = t1 + g;
-            t2 = fma2(g, s[e], t2);
-        }
-        float s1 = lanes_sum<G>(sum(t1)), s2 = lanes_sum<G>(sum(t2)), ss = st.y, shift = 0.f;
-        if (G > 32) {
-            if ((threadIdx.x & 31) == 0)
-                part[turn][threadIdx.x / 32] = make_float4(st.x, st.y, s1, s2);
-            __syncthreads();
-            const float4 p = part[turn][(threadIdx.x & 31) % R::W];
-            const float mean = inv_d * parts_sum<R::W>(size * p.x), off = p.x - mean;
-            ss = parts_sum<R::W>(fmaf(size * off, off, p.y));
-            s1 = parts_sum<R::W>(p.z);
-            s2 = parts_sum<R::W>(fmaf(off, p.z, p.w));
-            shift = st.x - mean;
-        }
-        // (a row that is not there has no deviation: with eps 0 its r is infinite, and
-        // 0 times that would be in the sums over the rows)
-        const float r1 = mine ? rsqrtf(fmaf(ss, inv_d, eps)) : 0.f;
-        const F2 r = both(r1), sh = both(shift), m1 = both(-inv_d * s1), m2 = both(-inv_d * s2 * r1);
+        for (int u = 0; u < kAhead; ++u, turn ^= 1) {
+            if (u > 0 && base + u * w.step >= rows)
+                break;
+            F2 s[4], dn[4], more[4];
+            const int64_t at = w.at;
+            const bool mine = row.on && at < rows;
+            rx[u].widen(s);
+            rd[u].widen(dn);
+            if (RES)
+                rs[u].widen(more);
+            w.at += w.step;
+            request(u);
+            const float2 st = centre<G>(s, row);
+            F2 t1 = {0}, t2 = {0};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const F2 n = (G > 32 ? s[e] + sh : s[e]) * r;
-            dga[e] = fma2(dn[e], n, dga[e]);
-            const F2 g = r * fma2(n, m2, fma2(dn[e], ga[e], m1));
-            dn[e] = RES ? g + more[e] : g;
+            for (int e = 0; e < 4; ++e) {
+                dbe[e] = dbe[e] + dn[e];
+                const F2 g = dn[e] * ga[e];
+                t1 = t1 + g;
+                t2 = fma2(g, s[e], t2);
+            }
+            float s1 = lanes_sum<G>(sum(t1)), s2 = lanes_sum<G>(sum(t2)), ss = st.y, shift = 0.f;
+            if (G > 32) {
+                if ((threadIdx.x & 31) == 0)
+                    part[turn][threadIdx.x / 32] = make_float4(st.x, st.y, s1, s2);
+                __syncthreads();
+                const float4 p = part[turn][(threadIdx.x & 31) % R::W];
+                const float mean = inv_d * parts_sum<R::W>(size * p.x), off = p.x - mean;
+                ss = parts_sum<R::W>(fmaf(size * off, off, p.y));
+                s1 = parts_sum<R::W>(p.z);
+                s2 = parts_sum<R::W>(fmaf(off, p.z, p.w));
+                shift = st.x - mean;
+            }
+            // (a row that is not there has no deviation: with eps 0 its r is infinite, and
+            // 0 times that would be in the sums over the rows)
+            const float r1 = mine ? rsqrtf(fmaf(ss, inv_d, eps)) : 0.f;
+            const F2 r = both(r1), sh = both(shift), m1 = both(-inv_d * s1), m2 = both(-inv_d * s2 * r1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const F2 n = (G > 32 ? s[e] + sh : s[e]) * r;
+                dga[e] = fma2(dn[e], n, dga[e]);
+                const F2 g = r * fma2(n, m2, fma2(dn[e], ga[e], m1));
+                dn[e] = RES ? g + more[e] : g;
+            }
+            if (mine)
+                store_pairs(dx + at * d + row.c, dn);
         }
-        if (mine)
-            store_pairs(dx + at * d + row.c, dn);
     }
     if (!partial)
         return;
@@ -300,28 +310,30 @@ __global__ void __launch_bounds__(G > 32 ? G : kT, an_sm<G>(true))
     }
 }
 
-// dgamma, dbeta: the CTAs' partial rows in order, eight at a time.
-__global__ void __launch_bounds__(kT)
+// dgamma, dbeta: the CTAs' partial rows, 32 columns a CTA and the rows dealt to
+// its warps; eight of a warp's rows are in flight.
+constexpr int kP = 1024;
+__global__ void __launch_bounds__(kP)
     layer_norm_params_kernel(const float *partial, float *dgamma, float *dbeta, int nparts, int d) {
     griddep_launch_dependents();
     griddep_wait();
     partial = after_wait(partial);
     const int e = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
-    __shared__ float red[kT / 32][33];
+    __shared__ float red[kP / 32][33];
     float s = 0.f;
     if (e < 2 * d) {
         const float *p = partial + e;
         int k = w;
-        for (; k + 7 * (kT / 32) < nparts; k += 8 * (kT / 32)) {
+        for (; k + 7 * (kP / 32) < nparts; k += 8 * (kP / 32)) {
             float t[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-                t[u] = __ldcg(p + (size_t)(k + u * (kT / 32)) * 2 * d);
+                t[u] = __ldcg(p + (size_t)(k + u * (kP / 32)) * 2 * d);
 #pragma unroll
             for (int u = 0; u < 8; ++u)
                 s += t[u];
         }
-        for (; k < nparts; k += kT / 32)
+        for (; k < nparts; k += kP / 32)
             s += __ldcg(p + (size_t)k * 2 * d);
     }
     red[w][threadIdx.x & 31] = s;
@@ -329,7 +341,7 @@ __global__ void __launch_bounds__(kT)
     if (w == 0 && e < 2 * d) {
         s = 0.f;
 #pragma unroll
-        for (int p = 0; p < kT / 32; ++p)
+        for (int p = 0; p < kP / 32; ++p)
             s += red[p][threadIdx.x];
         (e < d ? dgamma : dbeta)[e % d] = s;
     }
@@ -416,7 +428,7 @@ cudaError_t launch_layer_norm_backward(const void *x, const float *gamma, const 
     e = Launch{x, dsum, gamma, nullptr, dout, dx, nullptr, partial, rows, d, eps, ctas, st}.go(bf16);
     if (e != cudaSuccess || !partial)
         return e;
-    return launch_pdl(layer_norm_params_kernel, dim3((2 * d + 31) / 32), dim3(kT), 0, st, (const float *)partial, dgamma,
+    return launch_pdl(layer_norm_params_kernel, dim3((2 * d + 31) / 32), dim3(kP), 0, st, (const float *)partial, dgamma,
                       dbeta, ctas, d);
 }
 

@@ -52,6 +52,10 @@ constexpr int kBarOff = kOutOff + kOutBytes;
 constexpr int kSmem = kBarOff + 256 + 1024;
 static_assert(kSmem <= 227 * 1024, "one CTA's shared memory");
 constexpr float kLog2e = 1.4426950408889634f;
+// Steps of 64 that an accumulator of logits takes: the tensor core truncates what it
+// adds, so that a sum of many terms of one sign falls short by about 2^-25 of itself with
+// every step of 16; chunks of 512 are added in the epilogue, where sums are rounded.
+constexpr int kLogitSteps = 8;
 constexpr float kQMin = 1e-7f; // q below it (p_t = 1 in 32 bits) divides nothing
 
 enum Mode {
@@ -64,6 +68,7 @@ enum Mode {
 struct GemmArgs {
     int mt, nt;         // tiles of the output
     int kb, per, splits; // 64-steps of the contraction, and those of a split (kSum)
+    int chunk;           // ... and those that one accumulator takes
     int group;          // tile rows that are walked together
     int b0;             // B's first row: this piece's first vocabulary entry (kOut: 0)
     int N, V;           // rows and columns of the output that are there
@@ -129,21 +134,42 @@ FW_DEV void commit_pair(uint64_t *bar) {
 FW_DEV void arrive_at(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// (the wait in the same statement: nothing that reads the registers gets between)
 FW_DEV void tmem_ld32(uint32_t taddr, float (&r)[32]) {
     uint32_t u[32];
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
                  "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
                  : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
                    "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]),
                    "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]),
                    "=r"(u[23]), "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]),
                    "=r"(u[30]), "=r"(u[31])
-                 : "r"(taddr));
-    tmem_ld_wait();
+                 : "r"(taddr)
+                 : "memory");
 #pragma unroll
     for (int i = 0; i < 32; ++i)
         r[i] = __uint_as_float(u[i]);
+}
+
+// 32 columns of an accumulator added to z, 16 at a time (registers).
+FW_DEV void add_tmem(uint32_t taddr, float (&z)[32]) {
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+        uint32_t u[16];
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                     "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+                     "tcgen05.wait::ld.sync.aligned;"
+                     : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+                       "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]),
+                       "=r"(u[15])
+                     : "r"(taddr + h)
+                     : "memory");
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            z[h + j] += __uint_as_float(u[j]);
+    }
 }
 
 // Columns c0 .. c0 + 31 of a row of logits: bias added, -inf past the vocabulary.
@@ -179,7 +205,9 @@ FW_DEV float columns_sum(float (&x)[32], int lane) {
 }
 
 // A_MN, B_MN: the operand's memory runs along the output (its rows are the contraction).
-template <Mode MODE, bool A_MN, bool B_MN>
+// CHUNKED (kLoss, kGrad): a tile's contraction goes by chunks, each from zero, that the
+// epilogue adds in registers.
+template <Mode MODE, bool A_MN, bool B_MN, bool CHUNKED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
     vocab_gemm_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                       const __grid_constant__ CUtensorMap tc_, GemmArgs g, unsigned *status) {
@@ -279,31 +307,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
         }
     } else if (warp == 1 && lane == 0 && rank == 0) { // products
         const uint32_t idesc = idesc_bf16(256, 256, A_MN, B_MN);
-        uint32_t step = 0, it = 0;
+        uint32_t step = 0, it = 0; // steps, and accumulators filled, so far
         bool ok = true;
-        for (int t = pair; ok && t < tiles; t += pairs, ++it) {
-            const At p = tile_at(t);
+        auto fill = [&](int k0, int k1) { // an accumulator takes steps k0 .. k1 - 1, from zero
             const uint32_t buf = it & 1, d = tm + buf * 256;
             if (it >= 2 && !mbar_wait(taken + buf, ((it >> 1) - 1) & 1, status))
-                break;
+                return false;
             tc_fence_after();
-            for (int k = p.k0; k < p.k1; ++k, ++step) {
+            for (int k = k0; k < k1; ++k, ++step) {
                 const uint32_t s = step % kStages;
-                if (!mbar_wait(full + s, (step / kStages) & 1, status)) {
-                    ok = false;
-                    break;
-                }
+                if (!mbar_wait(full + s, (step / kStages) & 1, status))
+                    return false;
                 tc_fence_after();
                 const uint32_t a = smem_u32(smem + s * kStageBytes), b = a + 16384;
 #pragma unroll
                 for (int st = 0; st < 4; ++st) {
                     const uint64_t da = A_MN ? desc_sw128(a + st * 2048, 8192, 1024) : desc_sw128(a + st * 32, 16, 1024);
                     const uint64_t db = B_MN ? desc_sw128(b + st * 2048, 8192, 1024) : desc_sw128(b + st * 32, 16, 1024);
-                    mma_pair(d, da, db, idesc, k > p.k0 || st > 0);
+                    mma_pair(d, da, db, idesc, k > k0 || st > 0);
                 }
                 commit_pair(empty + s);
             }
             commit_pair(ready + buf);
+            ++it;
+            return true;
+        };
+        for (int t = pair; ok && t < tiles; t += pairs) {
+            const At p = tile_at(t);
+            if (CHUNKED)
+                for (int k = p.k0; ok && k < p.k1; k += g.chunk)
+                    ok = fill(k, min(k + g.chunk, p.k1));
+            else
+                ok = fill(p.k0, p.k1);
         }
         // every read of an accumulator has been told of
         for (uint32_t buf = 0; ok && buf < 2 && buf < it; ++buf)
@@ -311,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
     } else if (warp >= 4) { // epilogue: lane = row
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         uint8_t *out = smem + kOutOff + (warp - 4) * 8192;
-        uint32_t it = 0, box = 0; // tiles, and boxes stored, so far
+        uint32_t it = 0, box = 0; // accumulators read, and boxes stored, so far
         // the next staging box, free of earlier stores
         auto next_box = [&]() {
             if (lane == 0)
@@ -332,11 +367,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                 bulk_commit();
             }
         };
-        for (int t = pair; t < tiles; t += pairs, ++it) {
+        // the accumulator that is complete next, and word that it has been read
+        auto next_acc = [&](uint32_t &acc) {
+            if (!mbar_wait(ready + (it & 1), (it >> 1) & 1, status))
+                return false;
+            tc_fence_after();
+            acc = tm + tmem_lane_base(warp) + (it & 1) * 256 + 128 * half;
+            return true;
+        };
+        auto done_with_acc = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                arrive_at(leader_addr(taken + (it & 1)));
+            ++it;
+        };
+        constexpr int kGroups = CHUNKED ? 4 : 1; // (unrolled where the sums are registers)
+        for (int t = pair; t < tiles; t += pairs) {
             const At p = tile_at(t);
-            const uint32_t buf = it & 1;
             const int row0 = p.mb * kTile + (int)rank * 128 + 32 * quarter, row = row0 + lane;
             const int col0 = p.nb * kTile + 128 * half;
+            const bool needed = row0 < g.N && col0 < g.V; // (else nothing of this warp's part is there)
             int target = -1;
             float lse = 0.f, rq = 0.f, at_target = 0.f, weight = 0.f;
             if (MODE == kLoss || MODE == kGrad) {
@@ -355,18 +406,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                 target -= g.b0; // (negative: not in this piece, or none)
             }
             const bool live = rq != 0.f;
-            if (!mbar_wait(ready + buf, (it >> 1) & 1, status))
+            uint32_t acc = 0;
+            bool ok = true;
+            float sums[kGroups][32]; // CHUNKED: of the chunks before the last
+            if (CHUNKED) {
+#pragma unroll
+                for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        sums[i][j] = 0.f;
+                for (int k = p.k0; ok && k + g.chunk < p.k1; k += g.chunk) {
+                    ok = next_acc(acc);
+                    if (!ok)
+                        break;
+                    if (needed)
+#pragma unroll
+                        for (int i = 0; i < kGroups; ++i)
+                            add_tmem(acc + 32 * i, sums[i]);
+                    done_with_acc();
+                }
+            }
+            if (!ok || !next_acc(acc))
                 break;
-            tc_fence_after();
-            const uint32_t acc = tm + tmem_lane_base(warp) + buf * 256 + 128 * half;
-            if (MODE == kLoss) {
+            // 32 columns of logits
+            auto logits = [&](int i, float (&z)[32]) {
+                if (CHUNKED)
+                    add_tmem(acc + 32 * i, z);
+                else
+                    tmem_ld32(acc + 32 * i, z);
+                finish_logits(z, g, col0 + 32 * i);
+            };
+            if (MODE == kLoss && needed) {
                 float top = -INFINITY, total = 0.f;
-#pragma unroll 1
-                for (int c = 0; c < 128 && col0 + c < g.V; c += 32) {
-                    float z[32];
-                    tmem_ld32(acc + c, z);
-                    finish_logits(z, g, col0 + c);
-                    const int k = target - col0 - c;
+#pragma unroll kGroups
+                for (int i = 0; i < 4; ++i) {
+                    if (col0 + 32 * i >= g.V)
+                        break;
+                    float(&z)[32] = sums[CHUNKED ? i : 0];
+                    logits(i, z);
+                    const int k = target - col0 - 32 * i;
                     if (k >= 0 && k < 32) {
                         float tz = z[0];
 #pragma unroll
@@ -374,65 +452,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                             tz = j == k ? z[j] : tz;
                         g.target_z[row] = tz;
                     }
-                    float m = z[0];
+                    float m = top;
 #pragma unroll
-                    for (int j = 1; j < 32; ++j)
+                    for (int j = 0; j < 32; ++j)
                         m = fmaxf(m, z[j]);
-                    m = fmaxf(m, top);
                     const float ref = m == -INFINITY ? 0.f : m; // (a part that is masked throughout sums to 0)
                     total *= ex2((top - ref) * kLog2e);
                     top = m;
-                    F2 s = {0};
+                    F2 s0 = {0}, s1 = {0};
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        const float2 e = unpack((pack(z[j], z[j + 1]) + both(-ref)) * both(kLog2e));
+                        const float2 f = unpack((pack(z[j + 2], z[j + 3]) + both(-ref)) * both(kLog2e));
+                        s0 = s0 + pack(ex2(e.x), ex2(e.y));
+                        s1 = s1 + pack(ex2(f.x), ex2(f.y));
+                    }
+                    total += sum(s0 + s1);
+                }
+                if (row < g.N)
+                    g.part[(size_t)(col0 / 128) * g.N + row] = make_float2(top, total);
+            } else if (MODE == kGrad && needed) {
+                uint8_t *to = nullptr;
+#pragma unroll kGroups
+                for (int i = 0; i < 4; ++i) {
+                    const int c = 32 * i;
+                    if (col0 + (c & 64) >= g.V) // (no product reads past the 64 columns that hold the last entry)
+                        break;
+                    if ((i & 1) == 0)
+                        to = next_box();
+                    float(&z)[32] = sums[CHUNKED ? i : 0];
+                    logits(i, z);
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
-                        const float2 e = unpack((pack(z[j], z[j + 1]) + both(-ref)) * both(kLog2e));
-                        s = s + pack(ex2(e.x), ex2(e.y));
+                        const float2 e = unpack((pack(z[j], z[j + 1]) + both(-lse)) * both(kLog2e));
+                        z[j] = live ? ex2(e.x) : 0.f;
+                        z[j + 1] = live ? ex2(e.y) : 0.f;
                     }
-                    total += sum(s);
-                }
-                if (row < g.N && col0 < g.V)
-                    g.part[(size_t)(col0 / 128) * g.N + row] = make_float2(top, total);
-            } else if (MODE == kGrad) {
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 64) {
-                    uint8_t *to = next_box();
-#pragma unroll 1
-                    for (int c1 = c; c1 < c + 64; c1 += 32) {
-                        float z[32];
-                        tmem_ld32(acc + c1, z);
-                        finish_logits(z, g, col0 + c1);
+                    const int k = target - col0 - c;
+                    if (k >= 0 && k < 32)
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            const float2 e = unpack((pack(z[j], z[j + 1]) + both(-lse)) * both(kLog2e));
-                            z[j] = live ? ex2(e.x) : 0.f;
-                            z[j + 1] = live ? ex2(e.y) : 0.f;
-                        }
-                        const int k = target - col0 - c1;
-                        if (k >= 0 && k < 32)
+                        for (int j = 0; j < 32; ++j)
+                            z[j] = j == k ? at_target : z[j];
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                z[j] = j == k ? at_target : z[j];
-#pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            uint4 u;
-                            u.x = pack_bf16x2(z[j] * rq, z[j + 1] * rq);
-                            u.y = pack_bf16x2(z[j + 2] * rq, z[j + 3] * rq);
-                            u.z = pack_bf16x2(z[j + 4] * rq, z[j + 5] * rq);
-                            u.w = pack_bf16x2(z[j + 6] * rq, z[j + 7] * rq);
-                            *reinterpret_cast<uint4 *>(to + lane * 128 + ((((c1 - c + j) >> 3) ^ (lane & 7)) << 4)) = u;
-                        }
-                        if (g.colsum) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                z[j] *= weight;
-                            const float s = columns_sum(z, lane);
-                            if (row0 < g.N)
-                                g.colsum[(size_t)(row0 / 32) * g.ldc + col0 + c1 + lane] = s;
-                        }
+                    for (int j = 0; j < 32; j += 8) {
+                        uint4 u;
+                        u.x = pack_bf16x2(z[j] * rq, z[j + 1] * rq);
+                        u.y = pack_bf16x2(z[j + 2] * rq, z[j + 3] * rq);
+                        u.z = pack_bf16x2(z[j + 4] * rq, z[j + 5] * rq);
+                        u.w = pack_bf16x2(z[j + 6] * rq, z[j + 7] * rq);
+                        *reinterpret_cast<uint4 *>(to + lane * 128 + (((((c & 32) + j) >> 3) ^ (lane & 7)) << 4)) = u;
                     }
-                    put(to, col0 + c, row0, row0 < g.N);
+                    if (g.colsum) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            z[j] *= weight;
+                        g.colsum[(size_t)(row0 / 32) * g.ldc + col0 + c + lane] = columns_sum(z, lane);
+                    }
+                    if (i & 1)
+                        put(to, col0 + (c & 64), row0, true);
                 }
-            } else {
+            } else if (MODE == kOut || MODE == kSum) {
                 constexpr int kW = MODE == kOut ? 64 : 32; // columns of a box of 128 bytes
                 const int y = row0 + (MODE == kSum ? p.z * g.rows_a_split : 0);
 #pragma unroll 1
@@ -462,10 +541,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                     put(to, col0 + c, y, row0 < g.N && col0 + c < g.V);
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                arrive_at(leader_addr(taken + buf));
+            done_with_acc();
         }
         if (MODE != kLoss && lane == 0)
             bulk_wait_all();
@@ -712,11 +788,11 @@ template <typename K> cudaError_t pairs_of(K *kern, int *out) {
     return cudaSuccess;
 }
 
-template <Mode MODE, bool A_MN, bool B_MN>
+template <Mode MODE, bool A_MN, bool B_MN, bool CHUNKED = false>
 cudaError_t launch_gemm(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tc_, const GemmArgs &g,
                         cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    auto kern = vocab_gemm_kernel<MODE, A_MN, B_MN>;
+    auto kern = vocab_gemm_kernel<MODE, A_MN, B_MN, CHUNKED>;
     cudaError_t e = allow_smem(kern, done);
     unsigned *status = nullptr;
     if (e == cudaSuccess)
@@ -729,6 +805,14 @@ cudaError_t launch_gemm(const CUtensorMap &ta, const CUtensorMap &tb, const CUte
     const int64_t tiles = (int64_t)g.mt * g.nt * g.splits;
     return launch_pdl(kern, dim3((unsigned)(2 * std::min<int64_t>(pairs, tiles))), dim3(kT), kSmem, st, ta, tb, tc_, g,
                       status);
+}
+
+// The products that form logits: by chunks where the width takes more than one.
+template <Mode MODE>
+cudaError_t launch_logits(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tc_, const GemmArgs &g,
+                          cudaStream_t st) {
+    return g.kb > g.chunk ? launch_gemm<MODE, false, false, true>(ta, tb, tc_, g, st)
+                          : launch_gemm<MODE, false, false>(ta, tb, tc_, g, st);
 }
 
 // Tile rows walked together in the products over tokens: their rows of A stay in L2 (32 MB of them).
@@ -748,6 +832,7 @@ cudaError_t launch_vocab_loss(const void *h, const void *W, const float *bias, T
     g.mt = tiles_of(N);
     g.nt = tiles_of(V);
     g.kb = g.per = (D + 63) / 64;
+    g.chunk = kLogitSteps;
     g.splits = 1;
     g.group = token_group(N, D);
     g.N = N;
@@ -761,7 +846,7 @@ cudaError_t launch_vocab_loss(const void *h, const void *W, const float *bias, T
     if (e == cudaSuccess)
         e = make_bf16_map(&tb, W, V, D, D, 128);
     if (e == cudaSuccess)
-        e = launch_gemm<kLoss, false, false>(ta, tb, ta, g, st);
+        e = launch_logits<kLoss>(ta, tb, ta, g, st);
     if (e != cudaSuccess)
         return e;
     const int tokens = N < 512 ? 1 : 32;
@@ -801,6 +886,7 @@ cudaError_t launch_vocab_loss_backward(const void *h, const void *W, const float
         g.mt = nb;
         g.nt = vt;
         g.kb = g.per = (D + 63) / 64;
+        g.chunk = kLogitSteps;
         g.splits = 1;
         g.group = token_group(N, D);
         g.b0 = v0;
@@ -814,7 +900,7 @@ cudaError_t launch_vocab_loss_backward(const void *h, const void *W, const float
         g.dloss = dloss;
         g.colsum = dbias ? colsum : nullptr;
         g.ldc = p.width;
-        e = launch_gemm<kGrad, false, false>(th, tw, tgs, g, st);
+        e = launch_logits<kGrad>(th, tw, tgs, g, st);
         if (e == cudaSuccess && dbias)
             e = launch_pdl(join_bias_kernel, dim3((nv + 31) / 32), dim3(kS), 0, st, (const float *)colsum, dbias + v0, nv,
                            (N + 31) / 32, p.width);
