@@ -51,11 +51,12 @@ constexpr int kOutBytes = 8 * 8192; // two boxes of 32 rows x 128 bytes per epil
 constexpr int kBarOff = kOutOff + kOutBytes;
 constexpr int kSmem = kBarOff + 256 + 1024;
 static_assert(kSmem <= 227 * 1024, "one CTA's shared memory");
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 // Steps of 64 that an accumulator of logits takes: the tensor core truncates what it
 // adds, so that a sum of many terms of one sign falls short by about 2^-25 of itself with
 // every step of 16; chunks of 512 are added in the epilogue, where sums are rounded.
 constexpr int kLogitSteps = 8;
+constexpr float kNoRef = -1e30f; // the reference of no entries: below every other
 constexpr float kQMin = 1e-7f; // q below it (p_t = 1 in 32 bits) divides nothing
 
 enum Mode {
@@ -68,7 +69,6 @@ enum Mode {
 struct GemmArgs {
     int mt, nt;         // tiles of the output
     int kb, per, splits; // 64-steps of the contraction, and those of a split (kSum)
-    int chunk;           // ... and those that one accumulator takes
     int group;          // tile rows that are walked together
     int b0;             // B's first row: this piece's first vocabulary entry (kOut: 0)
     int N, V;           // rows and columns of the output that are there
@@ -153,45 +153,30 @@ FW_DEV void tmem_ld32(uint32_t taddr, float (&r)[32]) {
         r[i] = __uint_as_float(u[i]);
 }
 
-// 32 columns of an accumulator added to z, 16 at a time (registers).
-FW_DEV void add_tmem(uint32_t taddr, float (&z)[32]) {
+// 16 columns of an accumulator added to z.
+FW_DEV void add_tmem(uint32_t taddr, F2 *z) {
+    uint32_t u[16];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+                   "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+                 : "r"(taddr)
+                 : "memory");
 #pragma unroll
-    for (int h = 0; h < 32; h += 16) {
-        uint32_t u[16];
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                     "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-                     "tcgen05.wait::ld.sync.aligned;"
-                     : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
-                       "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]),
-                       "=r"(u[15])
-                     : "r"(taddr + h)
-                     : "memory");
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            z[h + j] += __uint_as_float(u[j]);
-    }
+    for (int j = 0; j < 8; ++j)
+        z[j] = z[j] + pack(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
 }
 
-// Columns c0 .. c0 + 31 of a row of logits: bias added, -inf past the vocabulary.
-FW_DEV void finish_logits(float (&z)[32], const GemmArgs &a, int c0) {
-    if (a.bias && c0 + 32 <= a.V) {
+// Lane l's sum over the warp's lanes of value l of the 32 at p: halves are exchanged and added.
+FW_DEV float columns_sum(const F2 *p, int lane) {
+    float x[32];
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            const float4 b = __ldcg(reinterpret_cast<const float4 *>(a.bias + c0 + j));
-            z[j] += b.x;
-            z[j + 1] += b.y;
-            z[j + 2] += b.z;
-            z[j + 3] += b.w;
-        }
-    } else if (c0 + 32 > a.V) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            z[j] = c0 + j < a.V ? z[j] + (a.bias ? __ldcg(a.bias + c0 + j) : 0.f) : -INFINITY;
+    for (int j = 0; j < 16; ++j) {
+        const float2 v = unpack(p[j]);
+        x[2 * j] = v.x;
+        x[2 * j + 1] = v.y;
     }
-}
-
-// Lane l's sum over the warp's lanes of x[l]: halves are exchanged and added.
-FW_DEV float columns_sum(float (&x)[32], int lane) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const bool up = lane & o;
@@ -204,10 +189,12 @@ FW_DEV float columns_sum(float (&x)[32], int lane) {
     return x[0];
 }
 
+// A reference near x for exponentials: x log2 e to a sixteenth, so that z log2 e less
+// the reference takes one rounding (0 for a row that is masked throughout).
+FW_DEV float reference(float x) { return x == -INFINITY ? 0.f : rintf(x * kLog2e * 16.f) * 0.0625f; }
+
 // A_MN, B_MN: the operand's memory runs along the output (its rows are the contraction).
-// CHUNKED (kLoss, kGrad): a tile's contraction goes by chunks, each from zero, that the
-// epilogue adds in registers.
-template <Mode MODE, bool A_MN, bool B_MN, bool CHUNKED>
+template <Mode MODE, bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
     vocab_gemm_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                       const __grid_constant__ CUtensorMap tc_, GemmArgs g, unsigned *status) {
@@ -334,9 +321,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
         };
         for (int t = pair; ok && t < tiles; t += pairs) {
             const At p = tile_at(t);
-            if (CHUNKED)
-                for (int k = p.k0; ok && k < p.k1; k += g.chunk)
-                    ok = fill(k, min(k + g.chunk, p.k1));
+            if (MODE == kLoss || MODE == kGrad)
+                for (int k = p.k0; ok && k < p.k1; k += kLogitSteps)
+                    ok = fill(k, min(k + kLogitSteps, p.k1));
             else
                 ok = fill(p.k0, p.k1);
         }
@@ -382,136 +369,143 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                 arrive_at(leader_addr(taken + (it & 1)));
             ++it;
         };
-        constexpr int kGroups = CHUNKED ? 4 : 1; // (unrolled where the sums are registers)
         for (int t = pair; t < tiles; t += pairs) {
             const At p = tile_at(t);
             const int row0 = p.mb * kTile + (int)rank * 128 + 32 * quarter, row = row0 + lane;
             const int col0 = p.nb * kTile + 128 * half;
             const bool needed = row0 < g.N && col0 < g.V; // (else nothing of this warp's part is there)
-            int target = -1;
-            float lse = 0.f, rq = 0.f, at_target = 0.f, weight = 0.f;
+            uint32_t acc = 0;
             if (MODE == kLoss || MODE == kGrad) {
+                int target = -1;
                 if (row < g.N) {
                     target = token_at(g.targets, row, g.vocab);
                     if (target == g.vocab) // past the vocabulary: the loss is NaN, there is no gradient
                         target = -1;
                 }
-                if (MODE == kGrad && target >= 0) {
-                    const float qt = -expm1f(-__ldcg(g.loss + row));
-                    lse = __ldcg(g.lse + row);
-                    weight = __ldcg(g.dloss + row);
-                    rq = 1.f / fmaxf(qt, kQMin);
-                    at_target = -qt;
+                // kGrad: G = 2^(z log2 e - ref) rq off the target, at_target on it
+                float ref = 0.f, rq = 0.f, at_target = 0.f, weight = 0.f;
+                const bool live = target >= 0;
+                if (MODE == kGrad && live) {
+                    const float qt = -expm1f(-__ldcg(g.loss + row)), lse = __ldcg(g.lse + row);
+                    ref = reference(lse);
+                    const float f = ex2(fmaf(-lse, kLog2e, ref)); // (what the reference is off by)
+                    rq = f / fmaxf(qt, kQMin);
+                    at_target = -qt / fmaxf(qt, kQMin);
+                    weight = __ldcg(g.dloss + row) * fmaxf(qt, kQMin);
                 }
                 target -= g.b0; // (negative: not in this piece, or none)
-            }
-            const bool live = rq != 0.f;
-            uint32_t acc = 0;
-            bool ok = true;
-            float sums[kGroups][32]; // CHUNKED: of the chunks before the last
-            if (CHUNKED) {
+                // the row's 128 logits, from the bias on
+                F2 z[64];
 #pragma unroll
-                for (int i = 0; i < kGroups; ++i)
+                for (int j = 0; j < 64; ++j)
+                    z[j] = F2{0};
+                if (g.bias && needed) {
+                    if (col0 + 128 <= g.V) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        sums[i][j] = 0.f;
-                for (int k = p.k0; ok && k + g.chunk < p.k1; k += g.chunk) {
+                        for (int j = 0; j < 32; ++j) {
+                            const float4 b = __ldcg(reinterpret_cast<const float4 *>(g.bias + col0) + j);
+                            z[2 * j] = pack(b.x, b.y);
+                            z[2 * j + 1] = pack(b.z, b.w);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            z[j] = pack(col0 + 2 * j < g.V ? __ldcg(g.bias + col0 + 2 * j) : 0.f,
+                                        col0 + 2 * j + 1 < g.V ? __ldcg(g.bias + col0 + 2 * j + 1) : 0.f);
+                    }
+                }
+                bool ok = true;
+                for (int k = p.k0; k < p.k1; k += kLogitSteps) {
                     ok = next_acc(acc);
                     if (!ok)
                         break;
                     if (needed)
 #pragma unroll
-                        for (int i = 0; i < kGroups; ++i)
-                            add_tmem(acc + 32 * i, sums[i]);
+                        for (int i = 0; i < 8; ++i)
+                            add_tmem(acc + 16 * i, z + 8 * i);
                     done_with_acc();
                 }
-            }
-            if (!ok || !next_acc(acc))
-                break;
-            // 32 columns of logits
-            auto logits = [&](int i, float (&z)[32]) {
-                if (CHUNKED)
-                    add_tmem(acc + 32 * i, z);
-                else
-                    tmem_ld32(acc + 32 * i, z);
-                finish_logits(z, g, col0 + 32 * i);
-            };
-            if (MODE == kLoss && needed) {
-                float top = -INFINITY, total = 0.f;
-#pragma unroll kGroups
-                for (int i = 0; i < 4; ++i) {
-                    if (col0 + 32 * i >= g.V)
-                        break;
-                    float(&z)[32] = sums[CHUNKED ? i : 0];
-                    logits(i, z);
-                    const int k = target - col0 - 32 * i;
-                    if (k >= 0 && k < 32) {
-                        float tz = z[0];
+                if (!ok)
+                    break;
+                if (!needed)
+                    continue;
+                if (col0 + 128 > g.V) { // nothing past the vocabulary
 #pragma unroll
-                        for (int j = 1; j < 32; ++j)
-                            tz = j == k ? z[j] : tz;
+                    for (int j = 0; j < 64; ++j) {
+                        const float2 v = unpack(z[j]);
+                        z[j] = pack(col0 + 2 * j < g.V ? v.x : -INFINITY, col0 + 2 * j + 1 < g.V ? v.y : -INFINITY);
+                    }
+                }
+                const int tk = target - col0; // the target's place among the 128
+                if (MODE == kLoss) {
+                    if (tk >= 0 && tk < 128) {
+                        float tz = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) {
+                            const float2 v = unpack(z[j]);
+                            tz = 2 * j == tk ? v.x : 2 * j + 1 == tk ? v.y : tz;
+                        }
                         g.target_z[row] = tz;
                     }
-                    float m = top;
+                    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        m = fmaxf(m, z[j]);
-                    const float ref = m == -INFINITY ? 0.f : m; // (a part that is masked throughout sums to 0)
-                    total *= ex2((top - ref) * kLog2e);
-                    top = m;
-                    F2 s0 = {0}, s1 = {0};
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float2 e = unpack((pack(z[j], z[j + 1]) + both(-ref)) * both(kLog2e));
-                        const float2 f = unpack((pack(z[j + 2], z[j + 3]) + both(-ref)) * both(kLog2e));
-                        s0 = s0 + pack(ex2(e.x), ex2(e.y));
-                        s1 = s1 + pack(ex2(f.x), ex2(f.y));
+                    for (int j = 0; j < 64; ++j) {
+                        const float2 v = unpack(z[j]);
+                        m[j & 3] = fmaxf(m[j & 3], fmaxf(v.x, v.y));
                     }
-                    total += sum(s0 + s1);
+                    ref = reference(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
+                    F2 s[4] = {};
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) {
+                        const float2 e = unpack(fma2(z[j], both(kLog2e), both(-ref)));
+                        s[j & 3] = s[j & 3] + pack(ex2(e.x), ex2(e.y));
+                    }
+                    const float total = sum((s[0] + s[1]) + (s[2] + s[3]));
+                    if (row < g.N)
+                        g.part[(size_t)(col0 / 128) * g.N + row] = make_float2(total == 0.f ? kNoRef : ref, total);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 128; c += 64) {
+                        if (col0 + c >= g.V) // (no product reads past the 64 columns that hold the last entry)
+                            break;
+                        uint8_t *to = next_box();
+#pragma unroll
+                        for (int j = c; j < c + 64; j += 8) {
+                            F2 e[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const float2 v = unpack(fma2(z[(j >> 1) + x], both(kLog2e), both(-ref)));
+                                e[x] = pack(ex2(v.x), ex2(v.y)) * both(rq);
+                            }
+                            const int k = tk - j;
+                            if (k >= 0 && k < 8)
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) {
+                                    const float2 v = unpack(e[x]);
+                                    e[x] = pack(2 * x == k ? at_target : v.x, 2 * x + 1 == k ? at_target : v.y);
+                                }
+                            uint4 u;
+                            const float2 v0 = unpack(e[0]), v1 = unpack(e[1]), v2 = unpack(e[2]), v3 = unpack(e[3]);
+                            u.x = live ? pack_bf16x2(v0.x, v0.y) : 0u;
+                            u.y = live ? pack_bf16x2(v1.x, v1.y) : 0u;
+                            u.z = live ? pack_bf16x2(v2.x, v2.y) : 0u;
+                            u.w = live ? pack_bf16x2(v3.x, v3.y) : 0u;
+                            *reinterpret_cast<uint4 *>(to + lane * 128 + ((((j - c) >> 3) ^ (lane & 7)) << 4)) = u;
+                            if (g.colsum)
+#pragma unroll
+                                for (int x = 0; x < 4; ++x)
+                                    z[(j >> 1) + x] = live ? e[x] * both(weight) : F2{0};
+                        }
+                        put(to, col0 + c, row0, true);
+                        if (g.colsum)
+#pragma unroll
+                            for (int c1 = c; c1 < c + 64; c1 += 32)
+                                g.colsum[(size_t)(row0 / 32) * g.ldc + col0 + c1 + lane] = columns_sum(z + c1 / 2, lane);
+                    }
                 }
-                if (row < g.N)
-                    g.part[(size_t)(col0 / 128) * g.N + row] = make_float2(top, total);
-            } else if (MODE == kGrad && needed) {
-                uint8_t *to = nullptr;
-#pragma unroll kGroups
-                for (int i = 0; i < 4; ++i) {
-                    const int c = 32 * i;
-                    if (col0 + (c & 64) >= g.V) // (no product reads past the 64 columns that hold the last entry)
-                        break;
-                    if ((i & 1) == 0)
-                        to = next_box();
-                    float(&z)[32] = sums[CHUNKED ? i : 0];
-                    logits(i, z);
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float2 e = unpack((pack(z[j], z[j + 1]) + both(-lse)) * both(kLog2e));
-                        z[j] = live ? ex2(e.x) : 0.f;
-                        z[j + 1] = live ? ex2(e.y) : 0.f;
-                    }
-                    const int k = target - col0 - c;
-                    if (k >= 0 && k < 32)
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            z[j] = j == k ? at_target : z[j];
-#pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        uint4 u;
-                        u.x = pack_bf16x2(z[j] * rq, z[j + 1] * rq);
-                        u.y = pack_bf16x2(z[j + 2] * rq, z[j + 3] * rq);
-                        u.z = pack_bf16x2(z[j + 4] * rq, z[j + 5] * rq);
-                        u.w = pack_bf16x2(z[j + 6] * rq, z[j + 7] * rq);
-                        *reinterpret_cast<uint4 *>(to + lane * 128 + (((((c & 32) + j) >> 3) ^ (lane & 7)) << 4)) = u;
-                    }
-                    if (g.colsum) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            z[j] *= weight;
-                        g.colsum[(size_t)(row0 / 32) * g.ldc + col0 + c + lane] = columns_sum(z, lane);
-                    }
-                    if (i & 1)
-                        put(to, col0 + (c & 64), row0, true);
-                }
-            } else if (MODE == kOut || MODE == kSum) {
+            } else {
+                if (!next_acc(acc))
+                    break;
                 constexpr int kW = MODE == kOut ? 64 : 32; // columns of a box of 128 bytes
                 const int y = row0 + (MODE == kSum ? p.z * g.rows_a_split : 0);
 #pragma unroll 1
@@ -540,8 +534,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                     }
                     put(to, col0 + c, y, row0 < g.N && col0 + c < g.V);
                 }
+                done_with_acc();
             }
-            done_with_acc();
         }
         if (MODE != kLoss && lane == 0)
             bulk_wait_all();
@@ -553,6 +547,118 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
     tc_fence_after();
     if (warp == 2)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512) : "memory");
+}
+
+// ------------------------------------------------------------ few tokens
+// Up to four answers: bound by reading W once, so a product on CUDA cores from
+// registers, whose start and end cost less than the tensor cores' (one token
+// over 32 000 entries, D 512: FEW_US us against 16.5).  A warp takes four rows of W at
+// a time, its lanes 8 channels each; h sits in shared memory in 32 bits.  After
+// the lanes' sums have been exchanged each lane keeps the (reference, sum of
+// exponentials) of one token over the rows it got.
+constexpr int kFewT = 256, kFewRows = 4, kFewStep = kFewT / 32 * kFewRows;
+constexpr int kFewValues = 11264; // NT D: 44 KB of shared memory
+constexpr int few_an_sm(int nt) { return nt == 1 ? 4 : 2; } // (registers)
+
+template <int NT>
+__global__ void __launch_bounds__(kFewT, few_an_sm(NT))
+    vocab_few_kernel(const __nv_bfloat16 *h, const __nv_bfloat16 *W, const float *bias, Tokens targets, float2 *part,
+                     float *target_z, int N, int V, int D) {
+    extern __shared__ float hs[]; // [NT][D]
+    __shared__ float2 red[kFewT];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    griddep_launch_dependents();
+    griddep_wait();
+    h = after_wait(h);
+    W = after_wait(W);
+    bias = after_wait(bias);
+    targets.p = after_wait(targets.p);
+    for (int i = 8 * tid; i < NT * D; i += 8 * kFewT) {
+        float v[8] = {};
+        if (i < N * D)
+            load8(h + i, v);
+        store8(hs + i, v);
+    }
+    __syncthreads();
+    constexpr int n = kFewRows * NT; // a step's values: row r, token t at r NT + t
+    static_assert(n <= 32, "a lane keeps one value");
+    int mine = 0; // the value that this lane keeps
+#pragma unroll
+    for (int half = n / 2, o = 16; half > 0; half /= 2, o /= 2)
+        mine += lane & o ? half : 0;
+    const int t = mine % NT, r0 = mine / NT;
+    const bool owner = (lane & (32 / n - 1)) == 0 && t < N; // (of the lanes that end up with the same value)
+    const int target = t < N ? token_at(targets, t, V) : -1;
+    float top = kNoRef, total = 0.f;
+    for (int64_t v0 = ((int64_t)blockIdx.x * (kFewT / 32) + warp) * kFewRows; v0 < V; v0 += (int64_t)gridDim.x * kFewStep) {
+        F2 acc[kFewRows][NT] = {};
+        const float b = bias && owner && v0 + r0 < V ? __ldcg(bias + v0 + r0) : 0.f;
+#pragma unroll 2
+        for (int c = 8 * lane; c < D; c += 256) {
+            uint4 w[kFewRows];
+#pragma unroll
+            for (int r = 0; r < kFewRows; ++r)
+                w[r] = v0 + r < V ? __ldcs(reinterpret_cast<const uint4 *>(W + (v0 + r) * D + c)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int k = 0; k < NT; ++k) {
+                const float4 x = *reinterpret_cast<const float4 *>(hs + k * D + c);
+                const float4 y = *reinterpret_cast<const float4 *>(hs + k * D + c + 4);
+#pragma unroll
+                for (int r = 0; r < kFewRows; ++r) {
+                    auto two = [](uint32_t u) { return pack(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); };
+                    acc[r][k] = fma2(two(w[r].x), pack(x.x, x.y), acc[r][k]);
+                    acc[r][k] = fma2(two(w[r].y), pack(x.z, x.w), acc[r][k]);
+                    acc[r][k] = fma2(two(w[r].z), pack(y.x, y.y), acc[r][k]);
+                    acc[r][k] = fma2(two(w[r].w), pack(y.z, y.w), acc[r][k]);
+                }
+            }
+        }
+        float x[n];
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+            x[i] = sum(acc[i / NT][i % NT]);
+        int o = 16;
+#pragma unroll
+        for (int half = n / 2; half > 0; half /= 2, o /= 2) {
+            const bool up = lane & o;
+#pragma unroll
+            for (int j = 0; j < half; ++j) {
+                const float give = up ? x[j] : x[j + half], keep = up ? x[j + half] : x[j];
+                x[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+            }
+        }
+#pragma unroll
+        for (int o1 = 16 / n; o1 > 0; o1 /= 2)
+            x[0] += __shfl_xor_sync(0xffffffffu, x[0], o1);
+        if (owner && v0 + r0 < V) {
+            const float z = x[0] + b;
+            if (v0 + r0 == target)
+                target_z[t] = z;
+            if (z != -INFINITY) {
+                const float m = fmaxf(top, reference(z));
+                total = total * ex2(top - m) + ex2(fmaf(z, kLog2e, -m));
+                top = m;
+            }
+        }
+    }
+    red[tid] = make_float2(top, total);
+    __syncthreads();
+    if (warp < N) { // this warp's token: what the lanes that keep it have, of every warp
+        top = kNoRef;
+        total = 0.f;
+        auto join = [&](float2 p) {
+            const float m = fmaxf(top, p.x);
+            total = total * ex2(top - m) + p.y * ex2(p.x - m);
+            top = m;
+        };
+        if (t == warp && owner)
+            for (int w = 0; w < kFewT / 32; ++w)
+                join(red[32 * w + lane]);
+        for (int o = 16; o > 0; o >>= 1)
+            join(make_float2(__shfl_xor_sync(0xffffffffu, top, o), __shfl_xor_sync(0xffffffffu, total, o)));
+        if (lane == 0)
+            part[(size_t)blockIdx.x * N + warp] = make_float2(top, total);
+    }
 }
 
 // ------------------------------------------------------------ small kernels
@@ -571,10 +677,10 @@ __global__ void __launch_bounds__(kS)
     targets.p = after_wait(targets.p);
     const int slices = kS / tokens, i = threadIdx.x % tokens, w = threadIdx.x / tokens;
     const int n = blockIdx.x * tokens + i;
-    float top = -INFINITY, total = 0.f;
-    auto join = [&](float2 p) {
-        const float m = fmaxf(top, p.x), ref = m == -INFINITY ? 0.f : m;
-        total = total * ex2((top - ref) * kLog2e) + p.y * ex2((p.x - ref) * kLog2e);
+    float top = kNoRef, total = 0.f;
+    auto join = [&](float2 p) { // (references are sixteenths: their differences are exact)
+        const float m = fmaxf(top, p.x);
+        total = total * ex2(top - m) + p.y * ex2(p.x - m);
         top = m;
     };
     if (n < N)
@@ -583,7 +689,7 @@ __global__ void __launch_bounds__(kS)
 #pragma unroll
             for (int u = 0; u < 8; ++u)
                 p[u] = k + u * slices < nparts ? __ldcg(part + (size_t)(k + u * slices) * N + n)
-                                               : make_float2(-INFINITY, 0.f);
+                                               : make_float2(kNoRef, 0.f);
 #pragma unroll
             for (int u = 0; u < 8; ++u)
                 join(p[u]);
@@ -598,9 +704,9 @@ __global__ void __launch_bounds__(kS)
     }
     if (w == 0 && n < N) {
         const int t = token_at(targets, n, V);
-        const float l = logf(total);
-        loss[n] = t < 0 ? 0.f : t >= V ? __int_as_float(0x7fffffff) : (top - __ldcg(target_z + n)) + l;
-        lse[n] = t < 0 ? 0.f : top + l;
+        const float l = logf(total); // lse = top ln 2 + l
+        loss[n] = t < 0 ? 0.f : t >= V ? __int_as_float(0x7fffffff) : fmaf(fmaf(-__ldcg(target_z + n), kLog2e, top), kLn2, l);
+        lse[n] = t < 0 ? 0.f : fmaf(top, kLn2, l);
     }
 }
 
@@ -788,11 +894,11 @@ template <typename K> cudaError_t pairs_of(K *kern, int *out) {
     return cudaSuccess;
 }
 
-template <Mode MODE, bool A_MN, bool B_MN, bool CHUNKED = false>
+template <Mode MODE, bool A_MN, bool B_MN>
 cudaError_t launch_gemm(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tc_, const GemmArgs &g,
                         cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    auto kern = vocab_gemm_kernel<MODE, A_MN, B_MN, CHUNKED>;
+    auto kern = vocab_gemm_kernel<MODE, A_MN, B_MN>;
     cudaError_t e = allow_smem(kern, done);
     unsigned *status = nullptr;
     if (e == cudaSuccess)
@@ -807,32 +913,37 @@ cudaError_t launch_gemm(const CUtensorMap &ta, const CUtensorMap &tb, const CUte
                       status);
 }
 
-// The products that form logits: by chunks where the width takes more than one.
-template <Mode MODE>
-cudaError_t launch_logits(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tc_, const GemmArgs &g,
-                          cudaStream_t st) {
-    return g.kb > g.chunk ? launch_gemm<MODE, false, false, true>(ta, tb, tc_, g, st)
-                          : launch_gemm<MODE, false, false>(ta, tb, tc_, g, st);
-}
-
 // Tile rows walked together in the products over tokens: their rows of A stay in L2 (32 MB of them).
 int token_group(int N, int D) { return (int)std::max<int64_t>(8, std::min<int64_t>(tiles_of(N), (32 << 20) / ((int64_t)kTile * D * 2))); }
+
+
+// Few tokens: the form without tensor cores, and the parts that each form leaves of a token.
+int few_tokens(int N) { return N <= 2 ? N : 4; }
+bool few(int N, int D) { return N <= 4 && few_tokens(N) * (int64_t)D <= kFewValues; }
+int parts_of(int N, int V, int D) {
+    return few(N, D) ? std::min((V - 1) / kFewStep + 1, 2 * kPairs * few_an_sm(few_tokens(N))) : (V - 1) / 128 + 1;
+}
+
+template <int NT>
+cudaError_t launch_few(const void *h, const void *W, const float *bias, Tokens targets, float2 *part, float *target_z,
+                       int N, int V, int D, int nparts, cudaStream_t st) {
+    return launch_pdl(vocab_few_kernel<NT>, dim3(nparts), dim3(kFewT), sizeof(float) * NT * D, st, (const __nv_bfloat16 *)h,
+                      (const __nv_bfloat16 *)W, bias, targets, part, target_z, N, V, D);
+}
 
 } // namespace
 
 size_t vocab_loss_workspace_bytes(int N, int V, int D) {
-    (void)D;
-    return up256(sizeof(float2) * (size_t)((V + 127) / 128) * N) + up256(sizeof(float) * (size_t)N);
+    return up256(sizeof(float2) * (size_t)parts_of(N, V, D) * N) + up256(sizeof(float) * (size_t)N);
 }
 
 cudaError_t launch_vocab_loss(const void *h, const void *W, const float *bias, Tokens targets, float *loss, float *lse,
                               void *workspace, int N, int V, int D, cudaStream_t st) {
-    const int nparts = (V + 127) / 128;
+    const int nparts = parts_of(N, V, D);
     GemmArgs g = {};
     g.mt = tiles_of(N);
     g.nt = tiles_of(V);
     g.kb = g.per = (D + 63) / 64;
-    g.chunk = kLogitSteps;
     g.splits = 1;
     g.group = token_group(N, D);
     g.N = N;
@@ -841,12 +952,19 @@ cudaError_t launch_vocab_loss(const void *h, const void *W, const float *bias, T
     g.targets = targets;
     g.part = static_cast<float2 *>(workspace);
     g.target_z = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + up256(sizeof(float2) * (size_t)nparts * N));
-    CUtensorMap ta, tb;
-    cudaError_t e = make_bf16_map(&ta, h, N, D, D, 128);
-    if (e == cudaSuccess)
-        e = make_bf16_map(&tb, W, V, D, D, 128);
-    if (e == cudaSuccess)
-        e = launch_logits<kLoss>(ta, tb, ta, g, st);
+    cudaError_t e;
+    if (few(N, D)) {
+        e = N == 1   ? launch_few<1>(h, W, bias, targets, g.part, g.target_z, N, V, D, nparts, st)
+            : N == 2 ? launch_few<2>(h, W, bias, targets, g.part, g.target_z, N, V, D, nparts, st)
+                     : launch_few<4>(h, W, bias, targets, g.part, g.target_z, N, V, D, nparts, st);
+    } else {
+        CUtensorMap ta, tb;
+        e = make_bf16_map(&ta, h, N, D, D, 128);
+        if (e == cudaSuccess)
+            e = make_bf16_map(&tb, W, V, D, D, 128);
+        if (e == cudaSuccess)
+            e = launch_gemm<kLoss, false, false>(ta, tb, ta, g, st);
+    }
     if (e != cudaSuccess)
         return e;
     const int tokens = N < 512 ? 1 : 32;
@@ -886,8 +1004,7 @@ cudaError_t launch_vocab_loss_backward(const void *h, const void *W, const float
         g.mt = nb;
         g.nt = vt;
         g.kb = g.per = (D + 63) / 64;
-        g.chunk = kLogitSteps;
-        g.splits = 1;
+            g.splits = 1;
         g.group = token_group(N, D);
         g.b0 = v0;
         g.N = N;
@@ -900,7 +1017,7 @@ cudaError_t launch_vocab_loss_backward(const void *h, const void *W, const float
         g.dloss = dloss;
         g.colsum = dbias ? colsum : nullptr;
         g.ldc = p.width;
-        e = launch_logits<kGrad>(th, tw, tgs, g, st);
+        e = launch_gemm<kGrad, false, false>(th, tw, tgs, g, st);
         if (e == cudaSuccess && dbias)
             e = launch_pdl(join_bias_kernel, dim3((nv + 31) / 32), dim3(kS), 0, st, (const float *)colsum, dbias + v0, nv,
                            (N + 31) / 32, p.width);

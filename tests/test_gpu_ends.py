@@ -282,7 +282,8 @@ def loss_check(N, V, D, seed, index=torch.int64, **kw):
     assert torch.all(dh.cpu()[t < 0] == 0)
 
 
-@pytest.mark.parametrize("N, V, D", [(1, 1, 8), (1, 2, 64), (1, 1000, 512), (3, 33, 16), (5, 255, 72), (64, 256, 128),
+@pytest.mark.parametrize("N, V, D", [(1, 1, 8), (1, 2, 64), (1, 1000, 512), (2, 31, 24), (2, 20000, 264), (4, 3001, 2816),
+                                     (3, 40, 2824), (1, 70, 11264), (1, 70, 11272), (3, 33, 16), (5, 255, 72), (64, 256, 128),
                                      (100, 257, 64), (127, 65, 512), (128, 128, 1024), (129, 129, 136), (256, 300, 256),
                                      (257, 511, 264), (300, 1025, 40), (520, 65, 512), (700, 770, 2048)], ids=str)
 @pytest.mark.parametrize("bias", [False, True])
@@ -355,10 +356,15 @@ def test_vocab_loss_parts_and_repeats():
         ws.fill_(fill)
         again = fw.fw_vocab_loss_backward(h, W, t, loss, lse, dl, bias=b, workspace=ws)
         assert all(torch.equal(x, y) for x, y in zip(again, (dh, dW, db)))
-    # one token at a time: the same answers
+    # one token and a few at a time (summed on CUDA cores): off by the errors of two forms
+    S = (h.double().abs() @ W.double().abs().T + b.double().abs()).max(1).values
+    lim = 4 * ((256 / 16 + 1) * 2.0 ** -22 * S + 2.0 ** -18 * (1 + lse.double().abs()))
     for n in (0, 150, 299):
         one = fw.fw_vocab_loss(h[n], W, t[n], bias=b)
-        assert one[0].shape == () and torch.equal(one[0], loss[n]) and torch.equal(one[1], lse[n])
+        assert one[0].shape == () and abs(one[0] - loss[n]) <= lim[n] and abs(one[1] - lse[n]) <= lim[n]
+    for n in (2, 3, 4, 5):
+        some = fw.fw_vocab_loss(h[:n], W, t[:n], bias=b)
+        assert torch.all((some[0] - loss[:n]).abs() <= lim[:n]) and torch.all((some[1] - lse[:n]).abs() <= lim[:n])
     none = fw.fw_vocab_loss_backward(h[:0], W, t[:0], loss[:0], lse[:0], dl[:0], bias=b)
     assert none[0].shape == (0, 256) and torch.all(none[1] == 0) and torch.all(none[2] == 0)
     assert fw.fw_vocab_loss(h[:0], W, t[:0])[0].shape == (0,)
