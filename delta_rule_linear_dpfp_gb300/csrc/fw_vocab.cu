@@ -42,12 +42,14 @@ namespace {
 
 using namespace tc;
 
-constexpr int kT = 384;       // warp 0: copies, 1: products, 2: TMEM, 4 .. 11: epilogue
+constexpr int kEpiWarps = 16;  // each 32 rows x 64 columns of a CTA's 128 x 256
+constexpr int kT = 32 * (4 + kEpiWarps); // warp 0: copies, 1: products, 2: TMEM, 4 and on: epilogue
+constexpr int kCols = 64;      // columns of an epilogue warp
 constexpr int kTile = 256;    // rows and columns of a pair's tile
 constexpr int kStages = 5;
 constexpr int kStageBytes = 32768; // half of A's rows and half of B's, 64 of the contraction
 constexpr int kOutOff = kStages * kStageBytes;
-constexpr int kOutBytes = 8 * 8192; // two boxes of 32 rows x 128 bytes per epilogue warp
+constexpr int kOutBytes = kEpiWarps * 4096; // a box of 32 rows x 128 bytes per epilogue warp
 constexpr int kBarOff = kOutOff + kOutBytes;
 constexpr int kSmem = kBarOff + 256 + 1024;
 static_assert(kSmem <= 227 * 1024, "one CTA's shared memory");
@@ -66,8 +68,25 @@ enum Mode {
     kOut   // the product in bf16
 };
 
+// Division of numbers below 2^31 by a fixed one: n m >> 32 >> s with m = 2^(32 + s) / d
+// rounded up and 2^s < d <= 2^(s + 1), which errs by less than n d / 2^(32 + s) < 1 / d.
+struct Divisor {
+    uint32_t m, s, d;
+    Divisor() = default;
+    explicit Divisor(int by) : m(0), s(0), d((uint32_t)by) {
+        while ((2u << s) < d)
+            ++s;
+        if (d > 1)
+            m = (uint32_t)(((uint64_t)1 << (32 + s)) / d + 1);
+    }
+#ifdef __CUDACC__
+    FW_DEV int of(int n) const { return d > 1 ? (int)(__umulhi((uint32_t)n, m) >> s) : n; }
+#endif
+};
+
 struct GemmArgs {
     int mt, nt;         // tiles of the output
+    Divisor by_split, by_group, by_rows, by_last; // of a walk: its tiles, a group's, a group's rows, the last group's rows
     int kb, per, splits; // 64-steps of the contraction, and those of a split (kSum)
     int group;          // tile rows that are walked together
     int b0;             // B's first row: this piece's first vocabulary entry (kOut: 0)
@@ -77,9 +96,10 @@ struct GemmArgs {
     const float *bias;  // kLoss, kGrad: of this piece, or null
     Tokens targets;
     int vocab;          // all of the vocabulary's entries
-    float2 *part;       // kLoss: [ceil(V / 128)][N] (max, sum)
+    float2 *part;       // kLoss: [ceil(V / 64)][N] (reference, sum)
     float *target_z;    // kLoss: [N]
-    const float *loss, *lse, *dloss;
+    const float4 *row;  // kGrad: [N] of each token (see row_constants), and its target, -1 for none
+    const int *row_target;
     float *colsum;      // kGrad: [ceil(N / 32)][ldc] or null
     int ldc;
 };
@@ -116,7 +136,6 @@ FW_DEV void tma_add(const void *map, const void *src, int x, int y) {
                  "r"(smem_u32(src)), "r"(x), "r"(y)
                  : "memory");
 }
-FW_DEV void bulk_wait_read_but_one() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 FW_DEV void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile("{\n\t.reg .pred p;\n\t"
                  "setp.ne.b32 p, %4, 0;\n\t"
@@ -135,7 +154,7 @@ FW_DEV void arrive_at(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // (the wait in the same statement: nothing that reads the registers gets between)
-FW_DEV void tmem_ld32(uint32_t taddr, float (&r)[32]) {
+FW_DEV void tmem_ld32(uint32_t taddr, float *r) {
     uint32_t u[32];
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
                  "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -151,6 +170,18 @@ FW_DEV void tmem_ld32(uint32_t taddr, float (&r)[32]) {
 #pragma unroll
     for (int i = 0; i < 32; ++i)
         r[i] = __uint_as_float(u[i]);
+}
+
+// 64 columns of an accumulator into z, as pairs.
+FW_DEV void load_tmem64(uint32_t taddr, F2 *z) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float r[32];
+        tmem_ld32(taddr + 32 * h, r);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            z[16 * h + j] = pack(r[2 * j], r[2 * j + 1]);
+    }
 }
 
 // 16 columns of an accumulator added to z.
@@ -217,7 +248,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(ready + s, 1);
-            mbar_init(taken + s, 16);
+            mbar_init(taken + s, 2 * kEpiWarps);
         }
         fence_barrier_init();
     }
@@ -234,9 +265,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
     griddep_wait();
     g.bias = after_wait(g.bias);
     g.targets.p = after_wait(g.targets.p);
-    g.loss = after_wait(g.loss);
-    g.lse = after_wait(g.lse);
-    g.dloss = after_wait(g.dloss);
+    g.row = after_wait(g.row);
+    g.row_target = after_wait(g.row_target);
     const uint32_t tm = *slot;
 
     // tile t of this pair's walk: rows mb, columns nb (groups of tile rows, column by column), split z
@@ -245,13 +275,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
     };
     auto tile_at = [&](int t) {
         At p;
-        p.z = t / a_split;
+        p.z = g.by_split.of(t);
         int r = t - p.z * a_split;
-        const int whole = g.group * g.nt, gi = r / whole;
-        r -= gi * whole;
-        const int rows = min(g.group, g.mt - gi * g.group);
-        p.nb = r / rows;
-        p.mb = gi * g.group + r - p.nb * rows;
+        const int gi = g.by_group.of(r);
+        r -= gi * (int)g.by_group.d;
+        const bool last = (gi + 1) * g.group > g.mt;
+        p.nb = last ? g.by_last.of(r) : g.by_rows.of(r);
+        p.mb = gi * g.group + r - p.nb * (int)(last ? g.by_last.d : g.by_rows.d);
         p.k0 = p.z * g.per;
         p.k1 = min(g.kb, p.k0 + g.per);
         return p;
@@ -331,26 +361,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
         for (uint32_t buf = 0; ok && buf < 2 && buf < it; ++buf)
             ok = mbar_wait(taken + buf, (((it - buf + 1) >> 1) - 1) & 1, status);
     } else if (warp >= 4) { // epilogue: lane = row
-        const int quarter = warp & 3, half = (warp - 4) >> 2;
-        uint8_t *out = smem + kOutOff + (warp - 4) * 8192;
-        uint32_t it = 0, box = 0; // accumulators read, and boxes stored, so far
-        // the next staging box, free of earlier stores
-        auto next_box = [&]() {
+        const int quarter = warp & 3, part = (warp - 4) >> 2; // which 32 rows, which 64 columns
+        uint8_t *out = smem + kOutOff + (warp - 4) * 4096;
+        uint32_t it = 0; // accumulators read so far
+        auto free_box = [&]() { // the staging box is free of the store before
             if (lane == 0)
-                bulk_wait_read_but_one();
+                bulk_wait_read();
             __syncwarp();
-            return out + (box++ & 1) * 4096;
         };
-        auto put = [&](uint8_t *to, int x, int y, bool there) { // the box leaves
+        auto put = [&](int x, int y) { // it leaves
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
-                if (there) {
-                    if (MODE == kSum && g.add)
-                        tma_add(&tc_, to, x, y);
-                    else
-                        tma_store(&tc_, to, x, y);
-                }
+                if (MODE == kSum && g.add)
+                    tma_add(&tc_, out, x, y);
+                else
+                    tma_store(&tc_, out, x, y);
                 bulk_commit();
             }
         };
@@ -359,7 +385,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
             if (!mbar_wait(ready + (it & 1), (it >> 1) & 1, status))
                 return false;
             tc_fence_after();
-            acc = tm + tmem_lane_base(warp) + (it & 1) * 256 + 128 * half;
+            acc = tm + tmem_lane_base(warp) + (it & 1) * 256 + kCols * part;
             return true;
         };
         auto done_with_acc = [&]() {
@@ -372,44 +398,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
         for (int t = pair; t < tiles; t += pairs) {
             const At p = tile_at(t);
             const int row0 = p.mb * kTile + (int)rank * 128 + 32 * quarter, row = row0 + lane;
-            const int col0 = p.nb * kTile + 128 * half;
+            const int col0 = p.nb * kTile + kCols * part;
             const bool needed = row0 < g.N && col0 < g.V; // (else nothing of this warp's part is there)
             uint32_t acc = 0;
             if (MODE == kLoss || MODE == kGrad) {
+                // what the row brings (used once the logits are there: the loads are under way until then)
                 int target = -1;
-                if (row < g.N) {
-                    target = token_at(g.targets, row, g.vocab);
-                    if (target == g.vocab) // past the vocabulary: the loss is NaN, there is no gradient
-                        target = -1;
+                float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (needed && row < g.N) {
+                    if (MODE == kLoss) {
+                        target = token_at(g.targets, row, g.vocab);
+                    } else {
+                        target = __ldcg(g.row_target + row);
+                        c = __ldcg(g.row + row);
+                    }
                 }
-                // kGrad: G = 2^(z log2 e - ref) rq off the target, at_target on it
-                float ref = 0.f, rq = 0.f, at_target = 0.f, weight = 0.f;
-                const bool live = target >= 0;
-                if (MODE == kGrad && live) {
-                    const float qt = -expm1f(-__ldcg(g.loss + row)), lse = __ldcg(g.lse + row);
-                    ref = reference(lse);
-                    const float f = ex2(fmaf(-lse, kLog2e, ref)); // (what the reference is off by)
-                    rq = f / fmaxf(qt, kQMin);
-                    at_target = -qt / fmaxf(qt, kQMin);
-                    weight = __ldcg(g.dloss + row) * fmaxf(qt, kQMin);
-                }
-                target -= g.b0; // (negative: not in this piece, or none)
-                // the row's 128 logits, from the bias on
-                F2 z[64];
+                // its logits, from the bias on
+                F2 z[kCols / 2];
+                const bool from_bias = g.bias && needed;
+                if (from_bias) {
+                    if (col0 + kCols <= g.V) {
 #pragma unroll
-                for (int j = 0; j < 64; ++j)
-                    z[j] = F2{0};
-                if (g.bias && needed) {
-                    if (col0 + 128 <= g.V) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
+                        for (int j = 0; j < kCols / 4; ++j) {
                             const float4 b = __ldcg(reinterpret_cast<const float4 *>(g.bias + col0) + j);
                             z[2 * j] = pack(b.x, b.y);
                             z[2 * j + 1] = pack(b.z, b.w);
                         }
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 64; ++j)
+                        for (int j = 0; j < kCols / 2; ++j)
                             z[j] = pack(col0 + 2 * j < g.V ? __ldcg(g.bias + col0 + 2 * j) : 0.f,
                                         col0 + 2 * j + 1 < g.V ? __ldcg(g.bias + col0 + 2 * j + 1) : 0.f);
                     }
@@ -419,122 +436,130 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                     ok = next_acc(acc);
                     if (!ok)
                         break;
-                    if (needed)
+                    if (needed) {
+                        if (k == p.k0 && !from_bias)
+                            load_tmem64(acc, z);
+                        else
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            add_tmem(acc + 16 * i, z + 8 * i);
+                            for (int i = 0; i < kCols / 16; ++i)
+                                add_tmem(acc + 16 * i, z + 8 * i);
+                    }
                     done_with_acc();
                 }
                 if (!ok)
                     break;
                 if (!needed)
                     continue;
-                if (col0 + 128 > g.V) { // nothing past the vocabulary
+                if (col0 + kCols > g.V) { // nothing past the vocabulary
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) {
+                    for (int j = 0; j < kCols / 2; ++j) {
                         const float2 v = unpack(z[j]);
                         z[j] = pack(col0 + 2 * j < g.V ? v.x : -INFINITY, col0 + 2 * j + 1 < g.V ? v.y : -INFINITY);
                     }
                 }
-                const int tk = target - col0; // the target's place among the 128
+                const int tk = target < 0 ? -1 : target - g.b0 - col0; // the target's place among these (or not)
                 if (MODE == kLoss) {
-                    if (tk >= 0 && tk < 128) {
+                    if (tk >= 0 && tk < kCols) {
                         float tz = 0.f;
 #pragma unroll
-                        for (int j = 0; j < 64; ++j) {
+                        for (int j = 0; j < kCols / 2; ++j) {
                             const float2 v = unpack(z[j]);
                             tz = 2 * j == tk ? v.x : 2 * j + 1 == tk ? v.y : tz;
                         }
-                        g.target_z[row] = tz;
+                        if (target < g.vocab)
+                            g.target_z[row] = tz;
                     }
                     float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) {
+                    for (int j = 0; j < kCols / 2; ++j) {
                         const float2 v = unpack(z[j]);
                         m[j & 3] = fmaxf(m[j & 3], fmaxf(v.x, v.y));
                     }
-                    ref = reference(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
+                    const float ref = reference(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
                     F2 s[4] = {};
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) {
+                    for (int j = 0; j < kCols / 2; ++j) {
                         const float2 e = unpack(fma2(z[j], both(kLog2e), both(-ref)));
                         s[j & 3] = s[j & 3] + pack(ex2(e.x), ex2(e.y));
                     }
                     const float total = sum((s[0] + s[1]) + (s[2] + s[3]));
                     if (row < g.N)
-                        g.part[(size_t)(col0 / 128) * g.N + row] = make_float2(total == 0.f ? kNoRef : ref, total);
+                        g.part[(size_t)(col0 / kCols) * g.N + row] = make_float2(total == 0.f ? kNoRef : ref, total);
                 } else {
+                    const float ref = c.x, rq = c.y, at_target = c.z, weight = c.w;
+                    const bool live = target >= 0;
+                    free_box();
 #pragma unroll
-                    for (int c = 0; c < 128; c += 64) {
-                        if (col0 + c >= g.V) // (no product reads past the 64 columns that hold the last entry)
-                            break;
-                        uint8_t *to = next_box();
+                    for (int j = 0; j < kCols; j += 8) {
+                        F2 e[4];
 #pragma unroll
-                        for (int j = c; j < c + 64; j += 8) {
-                            F2 e[4];
+                        for (int x = 0; x < 4; ++x) {
+                            const float2 v = unpack(fma2(z[(j >> 1) + x], both(kLog2e), both(-ref)));
+                            e[x] = pack(ex2(v.x), ex2(v.y)) * both(rq);
+                        }
+                        const int k = tk - j;
+                        if (k >= 0 && k < 8)
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {
-                                const float2 v = unpack(fma2(z[(j >> 1) + x], both(kLog2e), both(-ref)));
-                                e[x] = pack(ex2(v.x), ex2(v.y)) * both(rq);
+                                const float2 v = unpack(e[x]);
+                                e[x] = pack(2 * x == k ? at_target : v.x, 2 * x + 1 == k ? at_target : v.y);
                             }
-                            const int k = tk - j;
-                            if (k >= 0 && k < 8)
-#pragma unroll
-                                for (int x = 0; x < 4; ++x) {
-                                    const float2 v = unpack(e[x]);
-                                    e[x] = pack(2 * x == k ? at_target : v.x, 2 * x + 1 == k ? at_target : v.y);
-                                }
-                            uint4 u;
-                            const float2 v0 = unpack(e[0]), v1 = unpack(e[1]), v2 = unpack(e[2]), v3 = unpack(e[3]);
-                            u.x = live ? pack_bf16x2(v0.x, v0.y) : 0u;
-                            u.y = live ? pack_bf16x2(v1.x, v1.y) : 0u;
-                            u.z = live ? pack_bf16x2(v2.x, v2.y) : 0u;
-                            u.w = live ? pack_bf16x2(v3.x, v3.y) : 0u;
-                            *reinterpret_cast<uint4 *>(to + lane * 128 + ((((j - c) >> 3) ^ (lane & 7)) << 4)) = u;
-                            if (g.colsum)
-#pragma unroll
-                                for (int x = 0; x < 4; ++x)
-                                    z[(j >> 1) + x] = live ? e[x] * both(weight) : F2{0};
-                        }
-                        put(to, col0 + c, row0, true);
+                        uint4 u;
+                        const float2 v0 = unpack(e[0]), v1 = unpack(e[1]), v2 = unpack(e[2]), v3 = unpack(e[3]);
+                        u.x = live ? pack_bf16x2(v0.x, v0.y) : 0u;
+                        u.y = live ? pack_bf16x2(v1.x, v1.y) : 0u;
+                        u.z = live ? pack_bf16x2(v2.x, v2.y) : 0u;
+                        u.w = live ? pack_bf16x2(v3.x, v3.y) : 0u;
+                        *reinterpret_cast<uint4 *>(out + lane * 128 + (((j >> 3) ^ (lane & 7)) << 4)) = u;
                         if (g.colsum)
 #pragma unroll
-                            for (int c1 = c; c1 < c + 64; c1 += 32)
-                                g.colsum[(size_t)(row0 / 32) * g.ldc + col0 + c1 + lane] = columns_sum(z + c1 / 2, lane);
+                            for (int x = 0; x < 4; ++x)
+                                z[(j >> 1) + x] = live ? e[x] * both(weight) : F2{0};
                     }
+                    put(col0, row0);
+                    if (g.colsum)
+#pragma unroll
+                        for (int c1 = 0; c1 < kCols; c1 += 32)
+                            g.colsum[(size_t)(row0 / 32) * g.ldc + col0 + c1 + lane] = columns_sum(z + c1 / 2, lane);
                 }
             } else {
                 if (!next_acc(acc))
                     break;
-                constexpr int kW = MODE == kOut ? 64 : 32; // columns of a box of 128 bytes
-                const int y = row0 + (MODE == kSum ? p.z * g.rows_a_split : 0);
-#pragma unroll 1
-                for (int c = 0; c < 128; c += kW) {
-                    uint8_t *to = next_box();
+                if (needed) {
+                    float v[kCols];
+                    tmem_ld32(acc, v);
+                    tmem_ld32(acc + 32, v + 32);
+                    done_with_acc();
+                    free_box();
+                    if (MODE == kOut) {
 #pragma unroll
-                    for (int c1 = 0; c1 < kW; c1 += 32) {
-                        float z[32];
-                        tmem_ld32(acc + c + c1, z);
-                        if (MODE == kOut) {
+                        for (int j = 0; j < kCols; j += 8) {
+                            uint4 u;
+                            u.x = pack_bf16x2(v[j], v[j + 1]);
+                            u.y = pack_bf16x2(v[j + 2], v[j + 3]);
+                            u.z = pack_bf16x2(v[j + 4], v[j + 5]);
+                            u.w = pack_bf16x2(v[j + 6], v[j + 7]);
+                            *reinterpret_cast<uint4 *>(out + lane * 128 + (((j >> 3) ^ (lane & 7)) << 4)) = u;
+                        }
+                        put(col0, row0);
+                    } else {
+                        const int y = row0 + p.z * g.rows_a_split;
 #pragma unroll
-                            for (int j = 0; j < 32; j += 8) {
-                                uint4 u;
-                                u.x = pack_bf16x2(z[j], z[j + 1]);
-                                u.y = pack_bf16x2(z[j + 2], z[j + 3]);
-                                u.z = pack_bf16x2(z[j + 4], z[j + 5]);
-                                u.w = pack_bf16x2(z[j + 6], z[j + 7]);
-                                *reinterpret_cast<uint4 *>(to + lane * 128 + ((((c1 + j) >> 3) ^ (lane & 7)) << 4)) = u;
-                            }
-                        } else {
+                        for (int c = 0; c < kCols; c += 32) { // 32 columns of fp32 a box
+                            if (c && col0 + c >= g.V)
+                                break;
+                            if (c)
+                                free_box();
 #pragma unroll
                             for (int j = 0; j < 32; j += 4)
-                                *reinterpret_cast<float4 *>(to + lane * 128 + (((j >> 2) ^ (lane & 7)) << 4)) =
-                                    make_float4(z[j], z[j + 1], z[j + 2], z[j + 3]);
+                                *reinterpret_cast<float4 *>(out + lane * 128 + (((j >> 2) ^ (lane & 7)) << 4)) =
+                                    make_float4(v[c + j], v[c + j + 1], v[c + j + 2], v[c + j + 3]);
+                            put(col0 + c, y);
                         }
                     }
-                    put(to, col0 + c, y, row0 < g.N && col0 + c < g.V);
+                } else {
+                    done_with_acc();
                 }
-                done_with_acc();
             }
         }
         if (MODE != kLoss && lane == 0)
@@ -552,7 +577,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
 // ------------------------------------------------------------ few tokens
 // Up to four answers: bound by reading W once, so a product on CUDA cores from
 // registers, whose start and end cost less than the tensor cores' (one token
-// over 32 000 entries, D 512: FEW_US us against 16.5).  A warp takes four rows of W at
+// over 32 000 entries, D 512: 8.4 us against 16.5).  A warp takes four rows of W at
 // a time, its lanes 8 channels each; h sits in shared memory in 32 bits.  After
 // the lanes' sums have been exchanged each lane keeps the (reference, sum of
 // exponentials) of one token over the rows it got.
@@ -664,18 +689,19 @@ __global__ void __launch_bounds__(kFewT, few_an_sm(NT))
 // ------------------------------------------------------------ small kernels
 constexpr int kS = 256;
 
-// A token's parts joined: 32 tokens of a CTA and 8 threads for each, or one
-// token and 256 where there are few.
-__global__ void __launch_bounds__(kS)
+// A token's parts joined: 32 tokens of a CTA and 32 threads for each, or one
+// token and 1024 where there are few.
+constexpr int kJ = 1024;
+__global__ void __launch_bounds__(kJ)
     join_parts_kernel(const float2 *part, const float *target_z, Tokens targets, float *loss, float *lse, int N, int V,
                       int nparts, int tokens) {
-    __shared__ float2 red[kS];
+    __shared__ float2 red[kJ];
     griddep_launch_dependents();
     griddep_wait();
     part = after_wait(part);
     target_z = after_wait(target_z);
     targets.p = after_wait(targets.p);
-    const int slices = kS / tokens, i = threadIdx.x % tokens, w = threadIdx.x / tokens;
+    const int slices = kJ / tokens, i = threadIdx.x % tokens, w = threadIdx.x / tokens;
     const int n = blockIdx.x * tokens + i;
     float top = kNoRef, total = 0.f;
     auto join = [&](float2 p) { // (references are sixteenths: their differences are exact)
@@ -710,59 +736,74 @@ __global__ void __launch_bounds__(kS)
     }
 }
 
-// w_n of a token, 0 for one without a gradient.
-FW_DEV float token_weight(const Tokens &targets, const float *loss, const float *dloss, int n, int V) {
+// What a token brings to G and to its row of dh: with q = max(-expm1(-loss), kQMin),
+//   G = 2^(z log2 e - row.x) row.y off the target, row.z on it; q dloss = row.w,
+// all 0 for a token without a gradient.
+FW_DEV bool row_constants(const Tokens &targets, const float *loss, const float *lse, const float *dloss, int n, int V,
+                          float4 &row, int &target) {
     const int t = token_at(targets, n, V);
-    return t < 0 || t >= V ? 0.f : fmaxf(-expm1f(-__ldcg(loss + n)), kQMin) * __ldcg(dloss + n);
-}
-FW_DEV bool has_target(const Tokens &targets, int n, int V) {
-    const int t = token_at(targets, n, V);
-    return t >= 0 && t < V;
+    target = t < V ? t : -1; // (past the vocabulary: the loss is NaN, there is no gradient)
+    row = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (target < 0)
+        return false;
+    const float q = -expm1f(-__ldcg(loss + n)), s = __ldcg(lse + n), over = fmaxf(q, kQMin);
+    row.x = reference(s);
+    row.y = ex2(fmaf(-s, kLog2e, row.x)) / over; // (what the reference is off by)
+    row.z = -q / over;
+    row.w = over * __ldcg(dloss + n);
+    return true;
 }
 
-// w h in bf16; zeros for the tokens without a gradient, whatever h holds there.
+// The tokens' constants, and w h in bf16 (wh, or null): zeros for the tokens without a
+// gradient, whatever h holds there.
 __global__ void __launch_bounds__(kS)
-    weighted_rows_kernel(const __nv_bfloat16 *h, Tokens targets, const float *loss, const float *dloss,
-                         __nv_bfloat16 *wh, int N, int V, int D, int lg) {
+    rows_kernel(const __nv_bfloat16 *h, Tokens targets, const float *loss, const float *lse, const float *dloss,
+                float4 *row, int *row_target, __nv_bfloat16 *wh, int N, int V, int D, int lg) {
     griddep_launch_dependents();
     griddep_wait();
     h = after_wait(h);
     targets.p = after_wait(targets.p);
     loss = after_wait(loss);
+    lse = after_wait(lse);
     dloss = after_wait(dloss);
     const int n = (int)(blockIdx.x * (kS >> lg) + (threadIdx.x >> lg)), lane = threadIdx.x & ((1 << lg) - 1);
     if (n >= N)
         return;
-    const bool live = has_target(targets, n, V);
-    const float w = token_weight(targets, loss, dloss, n, V);
-    for (int c = 8 * lane; c < D; c += 8 << lg) {
-        float v[8];
-        if (live)
-            load8(h + (size_t)n * D + c, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = live ? w * v[e] : 0.f;
-        store8(wh + (size_t)n * D + c, v);
+    float4 r;
+    int target;
+    const bool live = row_constants(targets, loss, lse, dloss, n, V, r, target);
+    if (lane == 0) {
+        row[n] = r;
+        row_target[n] = target;
     }
+    if (wh)
+        for (int c = 8 * lane; c < D; c += 8 << lg) {
+            float v[8] = {};
+            if (live) {
+                load8(h + (size_t)n * D + c, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] *= r.w;
+            }
+            store8(wh + (size_t)n * D + c, v);
+        }
 }
 
-// The splits' sums joined in order, rounded once; TOKENS: rows are tokens and
-// take their weight.
-template <bool TOKENS>
+// The splits' sums joined in order, rounded once; with `row`, rows are tokens and take
+// their weight (zeros without a gradient).
 __global__ void __launch_bounds__(kS)
-    join_splits_kernel(const float *part, __nv_bfloat16 *out, int rows, int D, int splits, int64_t a_split, Tokens targets,
-                       const float *loss, const float *dloss, int V, int lg) {
+    join_splits_kernel(const float *part, __nv_bfloat16 *out, int rows, int D, int splits, int64_t a_split,
+                       const float4 *row, const int *row_target, int lg) {
     griddep_launch_dependents();
     griddep_wait();
     part = after_wait(part);
-    targets.p = after_wait(targets.p);
-    loss = after_wait(loss);
-    dloss = after_wait(dloss);
+    row = after_wait(row);
+    row_target = after_wait(row_target);
     const int n = (int)(blockIdx.x * (kS >> lg) + (threadIdx.x >> lg)), lane = threadIdx.x & ((1 << lg) - 1);
     if (n >= rows)
         return;
-    const bool live = !TOKENS || has_target(targets, n, V);
-    const float w = TOKENS ? token_weight(targets, loss, dloss, n, V) : 1.f;
+    const bool live = !row || __ldcg(row_target + n) >= 0;
+    const float w = row ? __ldcg(row + n).w : 1.f;
     for (int c = 8 * lane; c < D; c += 8 << lg) {
         float s[8] = {};
         if (live)
@@ -833,7 +874,7 @@ struct Plan {
     int width;      // vocabulary entries of a piece (a multiple of 256)
     int ldg;        // row stride of G
     Splits dh, dw;
-    size_t G, wh, dh_part, dw_part, colsum, bytes; // offsets
+    size_t row, row_target, G, wh, dh_part, dw_part, colsum, bytes; // offsets
 };
 Plan plan_of(int N, int V, int D) {
     Plan p;
@@ -850,6 +891,8 @@ Plan plan_of(int N, int V, int D) {
         at += up256(bytes);
         return o;
     };
+    p.row = take(sizeof(float4) * (size_t)N);
+    p.row_target = take(sizeof(int) * (size_t)N);
     p.G = take((size_t)2 * N * p.ldg);
     p.wh = take((size_t)2 * N * D);
     p.dh_part = take((size_t)4 * p.dh.n * tiles_of(N) * kTile * D);
@@ -895,8 +938,13 @@ template <typename K> cudaError_t pairs_of(K *kern, int *out) {
 }
 
 template <Mode MODE, bool A_MN, bool B_MN>
-cudaError_t launch_gemm(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tc_, const GemmArgs &g,
+cudaError_t launch_gemm(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tc_, GemmArgs g,
                         cudaStream_t st) {
+    g.group = std::min(g.group, g.mt);
+    g.by_split = Divisor(g.mt * g.nt);
+    g.by_group = Divisor(g.group * g.nt);
+    g.by_rows = Divisor(g.group);
+    g.by_last = Divisor(g.mt % g.group ? g.mt % g.group : g.group);
     static std::atomic<uint64_t> done{0};
     auto kern = vocab_gemm_kernel<MODE, A_MN, B_MN>;
     cudaError_t e = allow_smem(kern, done);
@@ -921,7 +969,7 @@ int token_group(int N, int D) { return (int)std::max<int64_t>(8, std::min<int64_
 int few_tokens(int N) { return N <= 2 ? N : 4; }
 bool few(int N, int D) { return N <= 4 && few_tokens(N) * (int64_t)D <= kFewValues; }
 int parts_of(int N, int V, int D) {
-    return few(N, D) ? std::min((V - 1) / kFewStep + 1, 2 * kPairs * few_an_sm(few_tokens(N))) : (V - 1) / 128 + 1;
+    return few(N, D) ? std::min((V - 1) / kFewStep + 1, 2 * kPairs * few_an_sm(few_tokens(N))) : (V - 1) / kCols + 1;
 }
 
 template <int NT>
@@ -968,7 +1016,7 @@ cudaError_t launch_vocab_loss(const void *h, const void *W, const float *bias, T
     if (e != cudaSuccess)
         return e;
     const int tokens = N < 512 ? 1 : 32;
-    return launch_pdl(join_parts_kernel, dim3((N + tokens - 1) / tokens), dim3(kS), 0, st, (const float2 *)g.part,
+    return launch_pdl(join_parts_kernel, dim3((N + tokens - 1) / tokens), dim3(kJ), 0, st, (const float2 *)g.part,
                       (const float *)g.target_z, targets, loss, lse, N, V, nparts, tokens);
 }
 
@@ -989,9 +1037,11 @@ cudaError_t launch_vocab_loss_backward(const void *h, const void *W, const float
     if (e == cudaSuccess) e = make_bf16_map(&tw_t, W, V, D, D, 64);
     if (e == cudaSuccess) e = make_bf16_map(&twh, wh, N, D, D, 64);
     if (e == cudaSuccess) e = make_f32_sw128_map(&tdh, dh_part, p.dh.n * nb * kTile, D, D, 32);
-    if (e == cudaSuccess && dW)
-        e = launch_pdl(weighted_rows_kernel, dim3((N + per_cta - 1) / per_cta), dim3(kS), 0, st, (const __nv_bfloat16 *)h,
-                       targets, loss, dloss, wh, N, V, D, lg);
+    float4 *row = reinterpret_cast<float4 *>(ws + p.row);
+    int *row_target = reinterpret_cast<int *>(ws + p.row_target);
+    if (e == cudaSuccess)
+        e = launch_pdl(rows_kernel, dim3((N + per_cta - 1) / per_cta), dim3(kS), 0, st, (const __nv_bfloat16 *)h, targets,
+                       loss, lse, dloss, row, row_target, dW ? wh : nullptr, N, V, D, lg);
     for (int v0 = 0; e == cudaSuccess && v0 < V; v0 += p.width) {
         const int nv = std::min(p.width, V - v0), vt = tiles_of(nv);
         CUtensorMap tgs;
@@ -1011,10 +1061,8 @@ cudaError_t launch_vocab_loss_backward(const void *h, const void *W, const float
         g.V = nv;
         g.vocab = V;
         g.bias = bias ? bias + v0 : nullptr;
-        g.targets = targets;
-        g.loss = loss;
-        g.lse = lse;
-        g.dloss = dloss;
+        g.row = row;
+        g.row_target = row_target;
         g.colsum = dbias ? colsum : nullptr;
         g.ldc = p.width;
         e = launch_gemm<kGrad, false, false>(th, tw, tgs, g, st);
@@ -1059,15 +1107,16 @@ cudaError_t launch_vocab_loss_backward(const void *h, const void *W, const float
                 if (e == cudaSuccess)
                     e = launch_gemm<kSum, true, true>(tg_t, twh, tdw, q, st);
                 if (e == cudaSuccess)
-                    e = launch_pdl(join_splits_kernel<false>, dim3((nv + per_cta - 1) / per_cta), dim3(kS), 0, st,
-                                   (const float *)dw_part, to, nv, D, p.dw.n, (int64_t)p.width * D, targets, loss, dloss, V,
-                                   lg);
+                    e = launch_pdl(join_splits_kernel, dim3((nv + per_cta - 1) / per_cta), dim3(kS), 0, st,
+                                   (const float *)dw_part, to, nv, D, p.dw.n, (int64_t)p.width * D, (const float4 *)nullptr,
+                                   (const int *)nullptr, lg);
             }
         }
     }
     if (e == cudaSuccess && dh)
-        e = launch_pdl(join_splits_kernel<true>, dim3((N + per_cta - 1) / per_cta), dim3(kS), 0, st, (const float *)dh_part,
-                       static_cast<__nv_bfloat16 *>(dh), N, D, p.dh.n, (int64_t)nb * kTile * D, targets, loss, dloss, V, lg);
+        e = launch_pdl(join_splits_kernel, dim3((N + per_cta - 1) / per_cta), dim3(kS), 0, st, (const float *)dh_part,
+                       static_cast<__nv_bfloat16 *>(dh), N, D, p.dh.n, (int64_t)nb * kTile * D, (const float4 *)row,
+                       (const int *)row_target, lg);
     return e;
 }
 
