@@ -62,10 +62,16 @@ constexpr float kNoRef = -1e30f; // the reference of no entries: below every oth
 constexpr float kQMin = 1e-7f; // q below it (p_t = 1 in 32 bits) divides nothing
 
 enum Mode {
-    kLoss, // parts of the logits' log-sum-exp, the targets' logits
-    kGrad, // G, and its columns' sums
-    kSum,  // the product in fp32, written or added
-    kOut   // the product in bf16
+    kLoss,    // h W^T: parts of the logits' log-sum-exp, the targets' logits
+    kGrad,    // h W^T: G, and its columns' sums
+    kProducts // G W and G^T (w h), one after the other: dh's and dW's
+};
+// What becomes of a product.
+enum Out {
+    kBf16,     // rounded
+    kWeighted, // a row times its token's weight, rounded
+    kF32,      // in 32 bits, each split to a place of its own
+    kAdd       // ... added to what is there
 };
 
 // Division of numbers below 2^31 by a fixed one: n m >> 32 >> s with m = 2^(32 + s) / d
@@ -84,24 +90,34 @@ struct Divisor {
 #endif
 };
 
+// One product's tiles, 256 x 256 of the output each, and how they are walked.
+struct Product {
+    int mt, nt;          // tiles of the output
+    int kb, per, splits; // 64-steps of the contraction, and those of a split
+    int group;           // tile rows that are walked together, column by column
+    Divisor by_split, by_group, by_rows, by_last; // a split's tiles, a group's, a group's rows, the last group's rows
+    int b0;              // B's first row
+    int N, V;            // rows and columns of the output that are there
+    int out;             // Out (kProducts)
+    int rows_a_split;    // kF32, kAdd: rows between the splits' outputs
+    int tiles;           // of all splits
+};
+
 struct GemmArgs {
-    int mt, nt;         // tiles of the output
-    Divisor by_split, by_group, by_rows, by_last; // of a walk: its tiles, a group's, a group's rows, the last group's rows
-    int kb, per, splits; // 64-steps of the contraction, and those of a split (kSum)
-    int group;          // tile rows that are walked together
-    int b0;             // B's first row: this piece's first vocabulary entry (kOut: 0)
-    int N, V;           // rows and columns of the output that are there
-    int rows_a_split;   // kSum: rows between the splits' outputs
-    int add;            // kSum: added to what is there
+    Product of[2];      // (the second: kProducts alone)
+    int extra;          // see walk
     const float *bias;  // kLoss, kGrad: of this piece, or null
     Tokens targets;
     int vocab;          // all of the vocabulary's entries
     float2 *part;       // kLoss: [ceil(V / 64)][N] (reference, sum)
     float *target_z;    // kLoss: [N]
-    const float4 *row;  // kGrad: [N] of each token (see row_constants), and its target, -1 for none
+    const float4 *row;  // kGrad, kWeighted: [N] of each token (see row_constants), and its target, -1 for none
     const int *row_target;
     float *colsum;      // kGrad: [ceil(N / 32)][ldc] or null
     int ldc;
+};
+struct Maps {
+    CUtensorMap a, b, out; // of a product
 };
 
 FW_DEV uint32_t cluster_rank() {
@@ -224,11 +240,12 @@ FW_DEV float columns_sum(const F2 *p, int lane) {
 // the reference takes one rounding (0 for a row that is masked throughout).
 FW_DEV float reference(float x) { return x == -INFINITY ? 0.f : rintf(x * kLog2e * 16.f) * 0.0625f; }
 
-// A_MN, B_MN: the operand's memory runs along the output (its rows are the contraction).
-template <Mode MODE, bool A_MN, bool B_MN>
+// kLoss, kGrad: both operands' memory runs along the contraction.  kProducts: B's
+// runs along the output, and so does A's of the second product.
+template <Mode MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
-    vocab_gemm_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
-                      const __grid_constant__ CUtensorMap tc_, GemmArgs g, unsigned *status) {
+    vocab_gemm_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps maps1, GemmArgs g,
+                      unsigned *status) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *full = (uint64_t *)(smem + kBarOff); // [kStages] (leader's) both CTAs' copies of a step have landed
@@ -239,7 +256,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const int a_split = g.mt * g.nt, tiles = a_split * g.splits;
 
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -269,30 +285,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
     g.row_target = after_wait(g.row_target);
     const uint32_t tm = *slot;
 
-    // tile t of this pair's walk: rows mb, columns nb (groups of tile rows, column by column), split z
+    // Tile i of this pair's walk: of product w, rows mb, columns nb, split z; false past
+    // the last.  The first product's tiles are dealt to the pairs in turn, then the
+    // second's: `extra` each to the pairs that got one fewer of the first's (as many as make
+    // up for it), the rest in turn from those on.
     struct At {
-        int mb, nb, k0, k1, z;
+        int w, mb, nb, k0, k1, z;
     };
-    auto tile_at = [&](int t) {
-        At p;
-        p.z = g.by_split.of(t);
-        int r = t - p.z * a_split;
-        const int gi = g.by_group.of(r);
-        r -= gi * (int)g.by_group.d;
-        const bool last = (gi + 1) * g.group > g.mt;
-        p.nb = last ? g.by_last.of(r) : g.by_rows.of(r);
-        p.mb = gi * g.group + r - p.nb * (int)(last ? g.by_last.d : g.by_rows.d);
-        p.k0 = p.z * g.per;
-        p.k1 = min(g.kb, p.k0 + g.per);
-        return p;
+    auto walk = [&](int i, At &p) {
+        const int n0 = g.of[0].tiles;
+        int t = pair + i * pairs;
+        p.w = 0;
+        if (t >= n0) {
+            if (MODE != kProducts)
+                return false;
+            p.w = 1;
+            const int more = n0 % pairs; // pairs below it have one of the first product's more
+            int j = i - (n0 / pairs + (pair < more ? 1 : 0));
+            const int late = pairs - more;
+            if (more && pair >= more) {
+                if (j < g.extra) {
+                    t = pair - more + j * late;
+                    j = -1;
+                } else {
+                    j -= g.extra;
+                }
+            }
+            if (j >= 0)
+                t = (more ? g.extra * late : 0) + (pair >= more ? pair - more : pair + late) + j * pairs;
+            if (t >= g.of[1].tiles)
+                return false;
+        }
+        const Product &q = g.of[MODE == kProducts ? p.w : 0];
+        p.z = q.by_split.of(t);
+        int r = t - p.z * (int)q.by_split.d;
+        const int gi = q.by_group.of(r);
+        r -= gi * (int)q.by_group.d;
+        const bool last = (gi + 1) * q.group > q.mt;
+        p.nb = last ? q.by_last.of(r) : q.by_rows.of(r);
+        p.mb = gi * q.group + r - p.nb * (int)(last ? q.by_last.d : q.by_rows.d);
+        p.k0 = p.z * q.per;
+        p.k1 = min(q.kb, p.k0 + q.per);
+        return true;
     };
 
     if (warp == 0 && lane == 0) { // copies
         uint32_t step = 0;
         bool ok = true;
-        for (int t = pair; ok && t < tiles; t += pairs) {
-            const At p = tile_at(t);
+        At p;
+        for (int i = 0; ok && walk(i, p); ++i) {
             const int m = p.mb * kTile + (int)rank * 128, n = p.nb * kTile + (int)rank * 128;
+            const bool second = MODE == kProducts && p.w;
+            const CUtensorMap *ta = second ? &maps1.a : &maps0.a, *tb = second ? &maps1.b : &maps0.b;
+            const int b0 = g.of[second].b0;
             for (int k = p.k0; k < p.k1; ++k, ++step) {
                 const uint32_t s = step % kStages, use = step / kStages;
                 if (use > 0 && !mbar_wait(empty + s, (use - 1) & 1, status)) {
@@ -303,17 +348,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                 const uint32_t bar = leader_addr(full + s);
                 if (rank == 0)
                     mbar_arrive_expect_tx(full + s, 2 * kStageBytes);
-                if (A_MN) {
-                    tma_load_pair(a, &ta, m, 64 * k, bar);
-                    tma_load_pair(a + 8192, &ta, m + 64, 64 * k, bar);
+                if (second) {
+                    tma_load_pair(a, ta, m, 64 * k, bar);
+                    tma_load_pair(a + 8192, ta, m + 64, 64 * k, bar);
                 } else {
-                    tma_load_pair(a, &ta, 64 * k, m, bar);
+                    tma_load_pair(a, ta, 64 * k, m, bar);
                 }
-                if (B_MN) {
-                    tma_load_pair(b, &tb, n, g.b0 + 64 * k, bar);
-                    tma_load_pair(b + 8192, &tb, n + 64, g.b0 + 64 * k, bar);
+                if (MODE == kProducts) {
+                    tma_load_pair(b, tb, n, b0 + 64 * k, bar);
+                    tma_load_pair(b + 8192, tb, n + 64, b0 + 64 * k, bar);
                 } else {
-                    tma_load_pair(b, &tb, 64 * k, g.b0 + n, bar);
+                    tma_load_pair(b, tb, 64 * k, b0 + n, bar);
                 }
             }
         }
@@ -323,10 +368,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
             ok = mbar_wait(empty + s, (uses - 1) & 1, status);
         }
     } else if (warp == 1 && lane == 0 && rank == 0) { // products
-        const uint32_t idesc = idesc_bf16(256, 256, A_MN, B_MN);
         uint32_t step = 0, it = 0; // steps, and accumulators filled, so far
         bool ok = true;
-        auto fill = [&](int k0, int k1) { // an accumulator takes steps k0 .. k1 - 1, from zero
+        auto fill = [&](int k0, int k1, bool second) { // an accumulator takes steps k0 .. k1 - 1, from zero
+            constexpr int kBMn = MODE == kProducts;
+            const uint32_t idesc = second ? idesc_bf16(256, 256, 1, kBMn) : idesc_bf16(256, 256, 0, kBMn);
+            // (a step of 16 lies 32 bytes on in rows that run along the contraction, 16 rows on in others)
+            const uint32_t a_step = second ? 2048 : 32, b_step = kBMn ? 2048 : 32;
+            const uint32_t a_lbo = second ? 8192 : 16, b_lbo = kBMn ? 8192 : 16;
             const uint32_t buf = it & 1, d = tm + buf * 256;
             if (it >= 2 && !mbar_wait(taken + buf, ((it >> 1) - 1) & 1, status))
                 return false;
@@ -339,8 +388,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                 const uint32_t a = smem_u32(smem + s * kStageBytes), b = a + 16384;
 #pragma unroll
                 for (int st = 0; st < 4; ++st) {
-                    const uint64_t da = A_MN ? desc_sw128(a + st * 2048, 8192, 1024) : desc_sw128(a + st * 32, 16, 1024);
-                    const uint64_t db = B_MN ? desc_sw128(b + st * 2048, 8192, 1024) : desc_sw128(b + st * 32, 16, 1024);
+                    const uint64_t da = desc_sw128(a + st * a_step, a_lbo, 1024), db = desc_sw128(b + st * b_step, b_lbo, 1024);
                     mma_pair(d, da, db, idesc, k > k0 || st > 0);
                 }
                 commit_pair(empty + s);
@@ -349,13 +397,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
             ++it;
             return true;
         };
-        for (int t = pair; ok && t < tiles; t += pairs) {
-            const At p = tile_at(t);
-            if (MODE == kLoss || MODE == kGrad)
-                for (int k = p.k0; ok && k < p.k1; k += kLogitSteps)
-                    ok = fill(k, min(k + kLogitSteps, p.k1));
+        At p;
+        for (int i = 0; ok && walk(i, p); ++i) {
+            if (MODE == kProducts)
+                ok = fill(p.k0, p.k1, p.w);
             else
-                ok = fill(p.k0, p.k1);
+                for (int k = p.k0; ok && k < p.k1; k += kLogitSteps)
+                    ok = fill(k, min(k + kLogitSteps, p.k1), false);
         }
         // every read of an accumulator has been told of
         for (uint32_t buf = 0; ok && buf < 2 && buf < it; ++buf)
@@ -369,14 +417,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                 bulk_wait_read();
             __syncwarp();
         };
-        auto put = [&](int x, int y) { // it leaves
+        auto put = [&](const CUtensorMap *to, int x, int y, bool add) { // it leaves
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
-                if (MODE == kSum && g.add)
-                    tma_add(&tc_, out, x, y);
+                if (add)
+                    tma_add(to, out, x, y);
                 else
-                    tma_store(&tc_, out, x, y);
+                    tma_store(to, out, x, y);
                 bulk_commit();
             }
         };
@@ -395,17 +443,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                 arrive_at(leader_addr(taken + (it & 1)));
             ++it;
         };
-        for (int t = pair; t < tiles; t += pairs) {
-            const At p = tile_at(t);
+        At p;
+        for (int i = 0; walk(i, p); ++i) {
+            const Product &q = g.of[MODE == kProducts ? p.w : 0];
             const int row0 = p.mb * kTile + (int)rank * 128 + 32 * quarter, row = row0 + lane;
             const int col0 = p.nb * kTile + kCols * part;
-            const bool needed = row0 < g.N && col0 < g.V; // (else nothing of this warp's part is there)
+            const bool needed = row0 < q.N && col0 < q.V; // (else nothing of this warp's part is there)
             uint32_t acc = 0;
-            if (MODE == kLoss || MODE == kGrad) {
+            if (MODE != kProducts) {
                 // what the row brings (used once the logits are there: the loads are under way until then)
                 int target = -1;
                 float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (needed && row < g.N) {
+                if (needed && row < q.N) {
                     if (MODE == kLoss) {
                         target = token_at(g.targets, row, g.vocab);
                     } else {
@@ -417,7 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                 F2 z[kCols / 2];
                 const bool from_bias = g.bias && needed;
                 if (from_bias) {
-                    if (col0 + kCols <= g.V) {
+                    if (col0 + kCols <= q.V) {
 #pragma unroll
                         for (int j = 0; j < kCols / 4; ++j) {
                             const float4 b = __ldcg(reinterpret_cast<const float4 *>(g.bias + col0) + j);
@@ -427,8 +476,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                     } else {
 #pragma unroll
                         for (int j = 0; j < kCols / 2; ++j)
-                            z[j] = pack(col0 + 2 * j < g.V ? __ldcg(g.bias + col0 + 2 * j) : 0.f,
-                                        col0 + 2 * j + 1 < g.V ? __ldcg(g.bias + col0 + 2 * j + 1) : 0.f);
+                            z[j] = pack(col0 + 2 * j < q.V ? __ldcg(g.bias + col0 + 2 * j) : 0.f,
+                                        col0 + 2 * j + 1 < q.V ? __ldcg(g.bias + col0 + 2 * j + 1) : 0.f);
                     }
                 }
                 bool ok = true;
@@ -450,14 +499,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                     break;
                 if (!needed)
                     continue;
-                if (col0 + kCols > g.V) { // nothing past the vocabulary
+                if (col0 + kCols > q.V) { // nothing past the vocabulary
 #pragma unroll
                     for (int j = 0; j < kCols / 2; ++j) {
                         const float2 v = unpack(z[j]);
-                        z[j] = pack(col0 + 2 * j < g.V ? v.x : -INFINITY, col0 + 2 * j + 1 < g.V ? v.y : -INFINITY);
+                        z[j] = pack(col0 + 2 * j < q.V ? v.x : -INFINITY, col0 + 2 * j + 1 < q.V ? v.y : -INFINITY);
                     }
                 }
-                const int tk = target < 0 ? -1 : target - g.b0 - col0; // the target's place among these (or not)
+                const int tk = target < 0 ? -1 : target - q.b0 - col0; // the target's place among these (or not)
                 if (MODE == kLoss) {
                     if (tk >= 0 && tk < kCols) {
                         float tz = 0.f;
@@ -483,8 +532,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                         s[j & 3] = s[j & 3] + pack(ex2(e.x), ex2(e.y));
                     }
                     const float total = sum((s[0] + s[1]) + (s[2] + s[3]));
-                    if (row < g.N)
-                        g.part[(size_t)(col0 / kCols) * g.N + row] = make_float2(total == 0.f ? kNoRef : ref, total);
+                    if (row < q.N)
+                        g.part[(size_t)(col0 / kCols) * q.N + row] = make_float2(total == 0.f ? kNoRef : ref, total);
                 } else {
                     const float ref = c.x, rq = c.y, at_target = c.z, weight = c.w;
                     const bool live = target >= 0;
@@ -516,7 +565,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                             for (int x = 0; x < 4; ++x)
                                 z[(j >> 1) + x] = live ? e[x] * both(weight) : F2{0};
                     }
-                    put(col0, row0);
+                    put(&maps0.out, col0, row0, false);
                     if (g.colsum)
 #pragma unroll
                         for (int c1 = 0; c1 < kCols; c1 += 32)
@@ -525,40 +574,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
             } else {
                 if (!next_acc(acc))
                     break;
-                if (needed) {
-                    float v[kCols];
-                    tmem_ld32(acc, v);
-                    tmem_ld32(acc + 32, v + 32);
+                if (!needed) {
                     done_with_acc();
-                    free_box();
-                    if (MODE == kOut) {
+                    continue;
+                }
+                float v[kCols];
+                tmem_ld32(acc, v);
+                tmem_ld32(acc + 32, v + 32);
+                done_with_acc();
+                const CUtensorMap *to = p.w ? &maps1.out : &maps0.out;
+                if (q.out == kWeighted) {
+                    const bool there = row < q.N && __ldcg(g.row_target + row) >= 0;
+                    const float w = there ? __ldcg(g.row + row).w : 0.f;
 #pragma unroll
-                        for (int j = 0; j < kCols; j += 8) {
-                            uint4 u;
-                            u.x = pack_bf16x2(v[j], v[j + 1]);
-                            u.y = pack_bf16x2(v[j + 2], v[j + 3]);
-                            u.z = pack_bf16x2(v[j + 4], v[j + 5]);
-                            u.w = pack_bf16x2(v[j + 6], v[j + 7]);
-                            *reinterpret_cast<uint4 *>(out + lane * 128 + (((j >> 3) ^ (lane & 7)) << 4)) = u;
-                        }
-                        put(col0, row0);
-                    } else {
-                        const int y = row0 + p.z * g.rows_a_split;
+                    for (int j = 0; j < kCols; ++j)
+                        v[j] = there ? v[j] * w : 0.f;
+                }
+                free_box();
+                if (q.out == kBf16 || q.out == kWeighted) {
 #pragma unroll
-                        for (int c = 0; c < kCols; c += 32) { // 32 columns of fp32 a box
-                            if (c && col0 + c >= g.V)
-                                break;
-                            if (c)
-                                free_box();
-#pragma unroll
-                            for (int j = 0; j < 32; j += 4)
-                                *reinterpret_cast<float4 *>(out + lane * 128 + (((j >> 2) ^ (lane & 7)) << 4)) =
-                                    make_float4(v[c + j], v[c + j + 1], v[c + j + 2], v[c + j + 3]);
-                            put(col0 + c, y);
-                        }
+                    for (int j = 0; j < kCols; j += 8) {
+                        uint4 u;
+                        u.x = pack_bf16x2(v[j], v[j + 1]);
+                        u.y = pack_bf16x2(v[j + 2], v[j + 3]);
+                        u.z = pack_bf16x2(v[j + 4], v[j + 5]);
+                        u.w = pack_bf16x2(v[j + 6], v[j + 7]);
+                        *reinterpret_cast<uint4 *>(out + lane * 128 + (((j >> 3) ^ (lane & 7)) << 4)) = u;
                     }
+                    put(to, col0, row0, false);
                 } else {
-                    done_with_acc();
+#pragma unroll
+                    for (int c = 0; c < kCols; c += 32) { // 32 columns of fp32 a box
+                        if (c && col0 + c >= q.V)
+                            break;
+                        if (c)
+                            free_box();
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            *reinterpret_cast<float4 *>(out + lane * 128 + (((j >> 2) ^ (lane & 7)) << 4)) =
+                                make_float4(v[c + j], v[c + j + 1], v[c + j + 2], v[c + j + 3]);
+                        put(to, col0 + c, row0 + p.z * q.rows_a_split, q.out == kAdd);
+                    }
                 }
             }
         }
@@ -789,64 +845,96 @@ __global__ void __launch_bounds__(kS)
         }
 }
 
-// The splits' sums joined in order, rounded once; with `row`, rows are tokens and take
-// their weight (zeros without a gradient).
-__global__ void __launch_bounds__(kS)
-    join_splits_kernel(const float *part, __nv_bfloat16 *out, int rows, int D, int splits, int64_t a_split,
-                       const float4 *row, const int *row_target, int lg) {
-    griddep_launch_dependents();
-    griddep_wait();
-    part = after_wait(part);
-    row = after_wait(row);
-    row_target = after_wait(row_target);
-    const int n = (int)(blockIdx.x * (kS >> lg) + (threadIdx.x >> lg)), lane = threadIdx.x & ((1 << lg) - 1);
-    if (n >= rows)
+// What is left of a piece, by the CTA: dh's rows and dW's from the sums of the splits,
+// added in order and rounded once (dh's times their weight, zeros without a gradient),
+// and dbias from the sums of 32 tokens each, in order.
+struct Rest {
+    const float *part; // [splits][a_split]
+    __nv_bfloat16 *out;
+    int rows, splits, ctas;
+    int64_t a_split;
+};
+struct RestArgs {
+    Rest dh, dw; // (ctas 0: nothing to do)
+    const float4 *row;
+    const int *row_target;
+    const float *colsum;
+    float *dbias;
+    int D, lg, V, blocks, ldc;
+};
+
+FW_DEV void join_rows(const Rest &q, const RestArgs &a, int cta, bool tokens) {
+    const int n = cta * (kS >> a.lg) + (int)(threadIdx.x >> a.lg), lane = threadIdx.x & ((1 << a.lg) - 1);
+    if (n >= q.rows)
         return;
-    const bool live = !row || __ldcg(row_target + n) >= 0;
-    const float w = row ? __ldcg(row + n).w : 1.f;
-    for (int c = 8 * lane; c < D; c += 8 << lg) {
+    const bool live = !tokens || __ldcg(a.row_target + n) >= 0;
+    const float w = tokens ? __ldcg(a.row + n).w : 1.f;
+    for (int c = 8 * lane; c < a.D; c += 8 << a.lg) {
         float s[8] = {};
-        if (live)
-            for (int z = 0; z < splits; ++z) {
+        if (live) {
+            const float *p = q.part + (int64_t)n * a.D + c;
+            int z = 0;
+            for (; z + 3 < q.splits; z += 4) {
+                float v[4][8];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    load8(p + (z + u) * q.a_split, v[u]);
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        s[e] += v[u][e];
+            }
+            for (; z < q.splits; ++z) {
                 float v[8];
-                load8(part + z * a_split + (int64_t)n * D + c, v);
+                load8(p + z * q.a_split, v);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     s[e] += v[e];
             }
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             s[e] = live ? s[e] * w : 0.f;
-        store8(out + (size_t)n * D + c, s);
+        store8(q.out + (size_t)n * a.D + c, s);
     }
 }
 
-// dbias of a piece: the sums of 32 tokens each, in order.
-__global__ void __launch_bounds__(kS)
-    join_bias_kernel(const float *colsum, float *dbias, int V, int blocks, int ldc) {
+__global__ void __launch_bounds__(kS) rest_kernel(RestArgs a) {
     __shared__ float red[kS / 32][33];
     griddep_launch_dependents();
     griddep_wait();
-    colsum = after_wait(colsum);
-    const int i = threadIdx.x & 31, w = threadIdx.x >> 5, v = blockIdx.x * 32 + i;
+    a.dh.part = after_wait(a.dh.part);
+    a.dw.part = after_wait(a.dw.part);
+    a.row = after_wait(a.row);
+    a.row_target = after_wait(a.row_target);
+    a.colsum = after_wait(a.colsum);
+    int cta = (int)blockIdx.x;
+    if (cta < a.dh.ctas)
+        return join_rows(a.dh, a, cta, true);
+    cta -= a.dh.ctas;
+    if (cta < a.dw.ctas)
+        return join_rows(a.dw, a, cta, false);
+    cta -= a.dw.ctas;
+    const int i = threadIdx.x & 31, w = threadIdx.x >> 5, v = cta * 32 + i;
     float s = 0.f;
-    for (int k = w; k < blocks; k += kS / 32 * 8) {
+    for (int k = w; k < a.blocks; k += kS / 32 * 8) {
         float t[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-            t[u] = k + u * (kS / 32) < blocks ? __ldcg(colsum + (size_t)(k + u * (kS / 32)) * ldc + v) : 0.f;
+            t[u] = k + u * (kS / 32) < a.blocks ? __ldcg(a.colsum + (size_t)(k + u * (kS / 32)) * a.ldc + v) : 0.f;
 #pragma unroll
         for (int u = 0; u < 8; ++u)
             s += t[u];
     }
     red[w][i] = s;
     __syncthreads();
-    if (w == 0 && v < V) {
+    if (w == 0 && v < a.V) {
         s = 0.f;
 #pragma unroll
         for (int k = 0; k < kS / 32; ++k)
             s += red[k][i];
-        dbias[v] = s;
+        a.dbias[v] = s;
     }
 }
 
@@ -858,13 +946,13 @@ int tiles_of(int64_t n) { return (int)((n + kTile - 1) / kTile); }
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Splits of a contraction of kb steps for an output of `tiles`: where the
-// tiles leave more than half of the pairs idle, as many as fill them, of four
-// steps at least.
+// tiles occupy fewer than a quarter of the pairs, as many as fill half of them
+// (dh's and dW's products run together), of four steps at least.
 struct Splits {
     int n, per;
 };
 Splits splits_of(int64_t tiles, int kb) {
-    int64_t n = tiles * 2 > kPairs ? 1 : std::min<int64_t>(kPairs / tiles, (kb + 3) / 4);
+    int64_t n = tiles * 4 > kPairs ? 1 : std::min<int64_t>(kPairs / 2 / tiles, (kb + 3) / 4);
     n = std::max<int64_t>(1, n);
     const int per = (int)((kb + n - 1) / n);
     return {(kb + per - 1) / per, per};
@@ -873,6 +961,7 @@ Splits splits_of(int64_t tiles, int kb) {
 struct Plan {
     int width;      // vocabulary entries of a piece (a multiple of 256)
     int ldg;        // row stride of G
+    int pieces;
     Splits dh, dw;
     size_t row, row_target, G, wh, dh_part, dw_part, colsum, bytes; // offsets
 };
@@ -883,6 +972,7 @@ Plan plan_of(int N, int V, int D) {
     const int64_t pieces = (vt + most - 1) / most;
     p.width = (int)((vt + pieces - 1) / pieces) * kTile;
     p.ldg = p.width;
+    p.pieces = (V + p.width - 1) / p.width;
     p.dh = splits_of((int64_t)tiles_of(N) * kt, (std::min(p.width, V) + 63) / 64);
     p.dw = splits_of((int64_t)(p.width / kTile) * kt, (N + 63) / 64);
     size_t at = 0;
@@ -895,7 +985,8 @@ Plan plan_of(int N, int V, int D) {
     p.row_target = take(sizeof(int) * (size_t)N);
     p.G = take((size_t)2 * N * p.ldg);
     p.wh = take((size_t)2 * N * D);
-    p.dh_part = take((size_t)4 * p.dh.n * tiles_of(N) * kTile * D);
+    // dh goes through sums in 32 bits where it has several parts (rows in whole tiles)
+    p.dh_part = take(p.dh.n * p.pieces > 1 ? (size_t)4 * p.dh.n * tiles_of(N) * kTile * D : 0);
     p.dw_part = take(p.dw.n > 1 ? (size_t)4 * p.dw.n * p.width * D : 0);
     p.colsum = take((size_t)4 * ((N + 31) / 32) * p.width);
     p.bytes = at;
@@ -937,16 +1028,28 @@ template <typename K> cudaError_t pairs_of(K *kern, int *out) {
     return cudaSuccess;
 }
 
-template <Mode MODE, bool A_MN, bool B_MN>
-cudaError_t launch_gemm(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tc_, GemmArgs g,
-                        cudaStream_t st) {
-    g.group = std::min(g.group, g.mt);
-    g.by_split = Divisor(g.mt * g.nt);
-    g.by_group = Divisor(g.group * g.nt);
-    g.by_rows = Divisor(g.group);
-    g.by_last = Divisor(g.mt % g.group ? g.mt % g.group : g.group);
+// The tiles of a product of M x V by kb steps.
+Product product(int M, int V, int kb, int per, int group) {
+    Product q = {};
+    q.mt = tiles_of(M);
+    q.nt = tiles_of(V);
+    q.kb = kb;
+    q.per = per;
+    q.splits = (kb + per - 1) / per;
+    q.group = std::min(group, q.mt);
+    q.by_split = Divisor(q.mt * q.nt);
+    q.by_group = Divisor(q.group * q.nt);
+    q.by_rows = Divisor(q.group);
+    q.by_last = Divisor(q.mt % q.group ? q.mt % q.group : q.group);
+    q.N = M;
+    q.V = V;
+    q.tiles = q.mt * q.nt * q.splits;
+    return q;
+}
+
+template <Mode MODE> cudaError_t launch_gemm(const Maps &maps0, const Maps &maps1, GemmArgs g, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    auto kern = vocab_gemm_kernel<MODE, A_MN, B_MN>;
+    auto kern = vocab_gemm_kernel<MODE>;
     cudaError_t e = allow_smem(kern, done);
     unsigned *status = nullptr;
     if (e == cudaSuccess)
@@ -956,9 +1059,11 @@ cudaError_t launch_gemm(const CUtensorMap &ta, const CUtensorMap &tb, const CUte
         e = pairs_of(kern, &pairs);
     if (e != cudaSuccess)
         return e;
-    const int64_t tiles = (int64_t)g.mt * g.nt * g.splits;
-    return launch_pdl(kern, dim3((unsigned)(2 * std::min<int64_t>(pairs, tiles))), dim3(kT), kSmem, st, ta, tb, tc_, g,
-                      status);
+    pairs = (int)std::min<int64_t>(pairs, (int64_t)g.of[0].tiles + g.of[1].tiles);
+    const int more = g.of[0].tiles % pairs;
+    if (MODE == kProducts && more && g.of[1].tiles) // (see walk)
+        g.extra = std::min((g.of[0].per + g.of[1].per / 2) / g.of[1].per, g.of[1].tiles / (pairs - more));
+    return launch_pdl(kern, dim3((unsigned)(2 * pairs)), dim3(kT), kSmem, st, maps0, maps1, g, status);
 }
 
 // Tile rows walked together in the products over tokens: their rows of A stay in L2 (32 MB of them).
@@ -989,13 +1094,7 @@ cudaError_t launch_vocab_loss(const void *h, const void *W, const float *bias, T
                               void *workspace, int N, int V, int D, cudaStream_t st) {
     const int nparts = parts_of(N, V, D);
     GemmArgs g = {};
-    g.mt = tiles_of(N);
-    g.nt = tiles_of(V);
-    g.kb = g.per = (D + 63) / 64;
-    g.splits = 1;
-    g.group = token_group(N, D);
-    g.N = N;
-    g.V = g.vocab = V;
+    g.vocab = V;
     g.bias = bias;
     g.targets = targets;
     g.part = static_cast<float2 *>(workspace);
@@ -1006,12 +1105,15 @@ cudaError_t launch_vocab_loss(const void *h, const void *W, const float *bias, T
             : N == 2 ? launch_few<2>(h, W, bias, targets, g.part, g.target_z, N, V, D, nparts, st)
                      : launch_few<4>(h, W, bias, targets, g.part, g.target_z, N, V, D, nparts, st);
     } else {
-        CUtensorMap ta, tb;
-        e = make_bf16_map(&ta, h, N, D, D, 128);
+        const int kb = (D + 63) / 64;
+        g.of[0] = product(N, V, kb, kb, token_group(N, D));
+        Maps m;
+        e = make_bf16_map(&m.a, h, N, D, D, 128);
         if (e == cudaSuccess)
-            e = make_bf16_map(&tb, W, V, D, D, 128);
+            e = make_bf16_map(&m.b, W, V, D, D, 128);
+        m.out = m.a; // (not read)
         if (e == cudaSuccess)
-            e = launch_gemm<kLoss, false, false>(ta, tb, ta, g, st);
+            e = launch_gemm<kLoss>(m, m, g, st);
     }
     if (e != cudaSuccess)
         return e;
@@ -1030,93 +1132,81 @@ cudaError_t launch_vocab_loss_backward(const void *h, const void *W, const float
     __nv_bfloat16 *G = reinterpret_cast<__nv_bfloat16 *>(ws + p.G), *wh = reinterpret_cast<__nv_bfloat16 *>(ws + p.wh);
     float *dh_part = reinterpret_cast<float *>(ws + p.dh_part), *dw_part = reinterpret_cast<float *>(ws + p.dw_part);
     float *colsum = reinterpret_cast<float *>(ws + p.colsum);
-    const int nb = tiles_of(N), dt = (D + kTile - 1) / kTile, lg = group_log2(D), per_cta = kS >> lg;
-    CUtensorMap th, tw, tg, tg_t, tw_t, tdh, twh, tdw;
-    cudaError_t e = make_bf16_map(&th, h, N, D, D, 128);
-    if (e == cudaSuccess) e = make_bf16_map(&tw, W, V, D, D, 128);
-    if (e == cudaSuccess) e = make_bf16_map(&tw_t, W, V, D, D, 64);
-    if (e == cudaSuccess) e = make_bf16_map(&twh, wh, N, D, D, 64);
-    if (e == cudaSuccess) e = make_f32_sw128_map(&tdh, dh_part, p.dh.n * nb * kTile, D, D, 32);
+    const int lg = group_log2(D), per_cta = kS >> lg, kd = (D + 63) / 64, kn = (N + 63) / 64;
+    const int64_t dh_rows = (int64_t)tiles_of(N) * kTile;
+    const bool dh_direct = p.dh.n * p.pieces == 1, dw_direct = p.dw.n == 1;
     float4 *row = reinterpret_cast<float4 *>(ws + p.row);
     int *row_target = reinterpret_cast<int *>(ws + p.row_target);
+    // h and W along their width, G as it is written; G and W for dh, G and w h for dW
+    Maps logits, to_dh, to_dw;
+    cudaError_t e = make_bf16_map(&logits.a, h, N, D, D, 128);
+    if (e == cudaSuccess) e = make_bf16_map(&logits.b, W, V, D, D, 128);
+    if (e == cudaSuccess) e = make_bf16_map(&logits.out, G, N, p.ldg, p.ldg, 32);
+    if (e == cudaSuccess) e = make_bf16_map(&to_dh.a, G, N, p.ldg, p.ldg, 128);
+    if (e == cudaSuccess) e = make_bf16_map(&to_dh.b, W, V, D, D, 64);
+    if (e == cudaSuccess && dh)
+        e = dh_direct ? make_bf16_map(&to_dh.out, dh, N, D, D, 32)
+                      : make_f32_sw128_map(&to_dh.out, dh_part, (int)(p.dh.n * dh_rows), D, D, 32);
+    if (e == cudaSuccess) e = make_bf16_map(&to_dw.a, G, N, p.ldg, p.ldg, 64);
+    if (e == cudaSuccess) e = make_bf16_map(&to_dw.b, wh, N, D, D, 64);
+    if (e == cudaSuccess && dW && !dw_direct)
+        e = make_f32_sw128_map(&to_dw.out, dw_part, p.dw.n * p.width, D, D, 32);
     if (e == cudaSuccess)
         e = launch_pdl(rows_kernel, dim3((N + per_cta - 1) / per_cta), dim3(kS), 0, st, (const __nv_bfloat16 *)h, targets,
                        loss, lse, dloss, row, row_target, dW ? wh : nullptr, N, V, D, lg);
     for (int v0 = 0; e == cudaSuccess && v0 < V; v0 += p.width) {
-        const int nv = std::min(p.width, V - v0), vt = tiles_of(nv);
-        CUtensorMap tgs;
-        e = make_bf16_map(&tg, G, N, p.ldg, p.ldg, 128);
-        if (e == cudaSuccess) e = make_bf16_map(&tgs, G, N, p.ldg, p.ldg, 32);
-        if (e == cudaSuccess) e = make_bf16_map(&tg_t, G, N, p.ldg, p.ldg, 64);
-        if (e != cudaSuccess)
-            break;
+        const int nv = std::min(p.width, V - v0);
+        const bool last = v0 + p.width >= V;
         GemmArgs g = {};
-        g.mt = nb;
-        g.nt = vt;
-        g.kb = g.per = (D + 63) / 64;
-            g.splits = 1;
-        g.group = token_group(N, D);
-        g.b0 = v0;
-        g.N = N;
-        g.V = nv;
+        g.of[0] = product(N, nv, kd, kd, token_group(N, D));
+        g.of[0].b0 = v0;
         g.vocab = V;
         g.bias = bias ? bias + v0 : nullptr;
         g.row = row;
         g.row_target = row_target;
         g.colsum = dbias ? colsum : nullptr;
         g.ldc = p.width;
-        e = launch_gemm<kGrad, false, false>(th, tw, tgs, g, st);
-        if (e == cudaSuccess && dbias)
-            e = launch_pdl(join_bias_kernel, dim3((nv + 31) / 32), dim3(kS), 0, st, (const float *)colsum, dbias + v0, nv,
-                           (N + 31) / 32, p.width);
-        if (e != cudaSuccess)
-            break;
-        if (dh) {
+        e = launch_gemm<kGrad>(logits, logits, g, st);
+        __nv_bfloat16 *dw_piece = dW ? static_cast<__nv_bfloat16 *>(dW) + (size_t)v0 * D : nullptr;
+        if (e == cudaSuccess && (dh || dW)) {
             GemmArgs q = {};
-            q.mt = nb;
-            q.nt = dt;
-            q.kb = (nv + 63) / 64;
-            q.per = p.dh.per;
-            q.splits = (q.kb + q.per - 1) / q.per;
-            q.group = 8;
-            q.b0 = v0;
-            q.N = N;
-            q.V = D;
-            q.rows_a_split = nb * kTile;
-            q.add = v0 > 0;
-            e = launch_gemm<kSum, false, true>(tg, tw_t, tdh, q, st);
-        }
-        if (e == cudaSuccess && dW) {
-            GemmArgs q = {};
-            q.mt = vt;
-            q.nt = dt;
-            q.kb = (N + 63) / 64;
-            q.group = 8;
-            q.N = nv;
-            q.V = D;
-            __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(dW) + (size_t)v0 * D;
-            q.per = p.dw.per;
-            q.splits = p.dw.n;
-            if (p.dw.n == 1) {
-                e = make_bf16_map(&tdw, to, nv, D, D, 32);
-                if (e == cudaSuccess)
-                    e = launch_gemm<kOut, true, true>(tg_t, twh, tdw, q, st);
-            } else {
-                q.rows_a_split = p.width;
-                e = make_f32_sw128_map(&tdw, dw_part, p.dw.n * p.width, D, D, 32);
-                if (e == cudaSuccess)
-                    e = launch_gemm<kSum, true, true>(tg_t, twh, tdw, q, st);
-                if (e == cudaSuccess)
-                    e = launch_pdl(join_splits_kernel, dim3((nv + per_cta - 1) / per_cta), dim3(kS), 0, st,
-                                   (const float *)dw_part, to, nv, D, p.dw.n, (int64_t)p.width * D, (const float4 *)nullptr,
-                                   (const int *)nullptr, lg);
+            q.row = row;
+            q.row_target = row_target;
+            q.of[1].per = 1;
+            if (dh) {
+                q.of[0] = product(N, D, (nv + 63) / 64, p.dh.per, 8);
+                q.of[0].b0 = v0;
+                q.of[0].out = dh_direct ? kWeighted : v0 ? kAdd : kF32;
+                q.of[0].rows_a_split = (int)dh_rows;
             }
+            if (dW) {
+                q.of[1] = product(nv, D, kn, p.dw.per, 8);
+                q.of[1].out = dw_direct ? kBf16 : kF32;
+                q.of[1].rows_a_split = p.width;
+                if (dw_direct)
+                    e = make_bf16_map(&to_dw.out, dw_piece, nv, D, D, 32);
+            }
+            if (e == cudaSuccess)
+                e = launch_gemm<kProducts>(to_dh, to_dw, q, st);
         }
+        RestArgs r = {};
+        if (dh && last && !dh_direct)
+            r.dh = {dh_part, static_cast<__nv_bfloat16 *>(dh), N, p.dh.n, (N + per_cta - 1) / per_cta, dh_rows * D};
+        if (dW && !dw_direct)
+            r.dw = {dw_part, dw_piece, nv, p.dw.n, (nv + per_cta - 1) / per_cta, (int64_t)p.width * D};
+        r.row = row;
+        r.row_target = row_target;
+        r.colsum = colsum;
+        r.dbias = dbias ? dbias + v0 : nullptr;
+        r.D = D;
+        r.lg = lg;
+        r.V = nv;
+        r.blocks = (N + 31) / 32;
+        r.ldc = p.width;
+        const int ctas = r.dh.ctas + r.dw.ctas + (dbias ? (nv + 31) / 32 : 0);
+        if (e == cudaSuccess && ctas)
+            e = launch_pdl(rest_kernel, dim3(ctas), dim3(kS), 0, st, r);
     }
-    if (e == cudaSuccess && dh)
-        e = launch_pdl(join_splits_kernel, dim3((N + per_cta - 1) / per_cta), dim3(kS), 0, st, (const float *)dh_part,
-                       static_cast<__nv_bfloat16 *>(dh), N, D, p.dh.n, (int64_t)nb * kTile * D, (const float4 *)row,
-                       (const int *)row_target, lg);
     return e;
 }
 
