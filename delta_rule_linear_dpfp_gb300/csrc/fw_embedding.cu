@@ -16,7 +16,7 @@
 //     shared memory; a warp owns 32 to 128 pairs in a row and ranks equal digits
 //     by a match among its lanes.  The sort is all latency and takes eight SMs:
 //     the others write the table's zeros meanwhile.
-//  2. A group of threads sums 32 sorted pairs (8 where there are few), run by run:
+//  2. A group of threads sums 32 sorted pairs (8 or 16 where there are few), run by run:
 //     a run that ends on both sides is rounded and written, one that goes on
 //     beyond leaves its sum in 32 bits.  Every group reads as many rows as any
 //     other, whatever a token's share of the batch is.
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kT) join_runs_kernel(SumArgs a, T *dtable) {
     for (int c = 8 * t; c - 8 * t < a.D; c += 8 << a.lg) {
         const bool on = c < a.D;
         float s[8] = {};
-        constexpr int kU = 4;
+        constexpr int kU = 8;
         if (on)
             for (int64_t j = k + g; j < end; j += groups * kU) {
                 Raw<float> v[kU];
@@ -412,8 +412,8 @@ cudaError_t lookup(Tokens ids, const void *table, void *out, int64_t N, int V, i
                       (T *)out, N, V, D, lg, scale);
 }
 
-// Pairs of a chunk: 8 where the chunks are too few to occupy the SMs otherwise.
-int chunk_log2(int N) { return N <= 8192 ? 3 : 5; }
+// Pairs of a chunk: fewer where the chunks are too few to occupy the SMs otherwise.
+int chunk_log2(int N) { return N <= 8192 ? 3 : N <= 32768 ? 4 : 5; }
 int64_t chunks_of(int N) { return ((int64_t)N + (1 << chunk_log2(N)) - 1) >> chunk_log2(N); }
 
 template <typename T>

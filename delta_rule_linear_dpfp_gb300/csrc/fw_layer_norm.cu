@@ -17,8 +17,9 @@
 // and sum dn (s - mean) = sum over the warps of the latter + (m_w - mean) sum dn:
 // differences of nearby numbers only.  gamma, beta, dgamma and dbeta stay in
 // registers: one partial row of the parameters' gradients per CTA, added by a
-// second kernel in a fixed order (no atomics).  The next row is requested before
-// the current one is worked on.
+// second kernel in a fixed order (no atomics).  The next rows are requested before
+// the current ones are worked on, and the bf16 backward works on two at a time: the
+// chain of shuffles and the barrier are latency that two rows share.
 #include "fw_common.cuh"
 #include "fw_ends.h"
 #include "fw_pairs.cuh"
@@ -206,7 +207,8 @@ __global__ void __launch_bounds__(G > 32 ? G : kT, an_sm<G>(true))
     layer_norm_backward_kernel(const T *x, const float *gamma, const T *dout, const T *dsum, T *dx, float *partial,
                                int64_t rows, int d, float eps) {
     using R = Row<G>;
-    __shared__ float4 part[2][R::W];
+    constexpr int U = sizeof(T) == 2 && G < 1024 ? 2 : 1; // rows worked on together (registers)
+    __shared__ float4 part[2][U][R::W];
     const R row((int)(threadIdx.x % G), d);
     const float inv_d = 1.f / (float)d, size = R::part_size((threadIdx.x & 31) % R::W, d);
     griddep_launch_dependents();
@@ -218,69 +220,84 @@ __global__ void __launch_bounds__(G > 32 ? G : kT, an_sm<G>(true))
     F2 ga[4], dga[4] = {}, dbe[4] = {};
     param_pairs(gamma, row.c, row.on, 1.f, ga);
     Walk<G> w(rows);
-    constexpr int kAhead = sizeof(T) == 2 && G < 1024 ? 2 : 1; // rows requested ahead (1024 threads: registers)
-    Raw<T> rx[kAhead], rd[kAhead], rs[kAhead];
-    int64_t ahead = w.at; // the next row to request
-    auto request = [&](int u) {
-        const bool here = row.on && ahead < w.rows;
-        rx[u].load(x + ahead * d + row.c, here);
-        rd[u].load(dout + ahead * d + row.c, here);
-        if (RES)
-            rs[u].load(dsum + ahead * d + row.c, here);
-        ahead += w.step;
-    };
+    Raw<T> rx[U], rd[U], rs[U];
+    auto request = [&](int64_t r) { // rows r, r + step, ...
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-        request(u);
-    int turn = 0;
-    for (int64_t base = w.at - (G > 32 ? 0 : threadIdx.x / G); base < rows; base += kAhead * w.step) {
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u, turn ^= 1) {
-            if (u > 0 && base + u * w.step >= rows)
-                break;
-            F2 s[4], dn[4], more[4];
-            const int64_t at = w.at;
-            const bool mine = row.on && at < rows;
-            rx[u].widen(s);
-            rd[u].widen(dn);
+        for (int u = 0; u < U; ++u, r += w.step) {
+            const bool here = row.on && r < w.rows;
+            rx[u].load(x + r * d + row.c, here);
+            rd[u].load(dout + r * d + row.c, here);
             if (RES)
-                rs[u].widen(more);
-            w.at += w.step;
-            request(u);
-            const float2 st = centre<G>(s, row);
+                rs[u].load(dsum + r * d + row.c, here);
+        }
+    };
+    request(w.at);
+    int turn = 0;
+    for (int64_t base = w.at - (G > 32 ? 0 : threadIdx.x / G); base < rows; base += U * w.step, turn ^= 1) {
+        F2 s[U][4], dn[U][4], more[U][4];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            rx[u].widen(s[u]);
+            rd[u].widen(dn[u]);
+            if (RES)
+                rs[u].widen(more[u]);
+        }
+        const int64_t at = w.at;
+        w.at += U * w.step;
+        request(w.at);
+        float s1[U], s2[U], ss[U], shift[U];
+        float2 st[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            st[u] = centre<G>(s[u], row);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
             F2 t1 = {0}, t2 = {0};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                dbe[e] = dbe[e] + dn[e];
-                const F2 g = dn[e] * ga[e];
+                dbe[e] = dbe[e] + dn[u][e];
+                const F2 g = dn[u][e] * ga[e];
                 t1 = t1 + g;
-                t2 = fma2(g, s[e], t2);
+                t2 = fma2(g, s[u][e], t2);
             }
-            float s1 = lanes_sum<G>(sum(t1)), s2 = lanes_sum<G>(sum(t2)), ss = st.y, shift = 0.f;
-            if (G > 32) {
-                if ((threadIdx.x & 31) == 0)
-                    part[turn][threadIdx.x / 32] = make_float4(st.x, st.y, s1, s2);
-                __syncthreads();
-                const float4 p = part[turn][(threadIdx.x & 31) % R::W];
+            s1[u] = lanes_sum<G>(sum(t1));
+            s2[u] = lanes_sum<G>(sum(t2));
+            ss[u] = st[u].y;
+            shift[u] = 0.f;
+        }
+        if (G > 32) {
+            if ((threadIdx.x & 31) == 0)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    part[turn][u][threadIdx.x / 32] = make_float4(st[u].x, st[u].y, s1[u], s2[u]);
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float4 p = part[turn][u][(threadIdx.x & 31) % R::W];
                 const float mean = inv_d * parts_sum<R::W>(size * p.x), off = p.x - mean;
-                ss = parts_sum<R::W>(fmaf(size * off, off, p.y));
-                s1 = parts_sum<R::W>(p.z);
-                s2 = parts_sum<R::W>(fmaf(off, p.z, p.w));
-                shift = st.x - mean;
+                ss[u] = parts_sum<R::W>(fmaf(size * off, off, p.y));
+                s1[u] = parts_sum<R::W>(p.z);
+                s2[u] = parts_sum<R::W>(fmaf(off, p.z, p.w));
+                shift[u] = st[u].x - mean;
             }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t r0 = at + u * w.step;
+            const bool mine = row.on && r0 < rows;
             // (a row that is not there has no deviation: with eps 0 its r is infinite, and
             // 0 times that would be in the sums over the rows)
-            const float r1 = mine ? rsqrtf(fmaf(ss, inv_d, eps)) : 0.f;
-            const F2 r = both(r1), sh = both(shift), m1 = both(-inv_d * s1), m2 = both(-inv_d * s2 * r1);
+            const float r1 = mine ? rsqrtf(fmaf(ss[u], inv_d, eps)) : 0.f;
+            const F2 r = both(r1), sh = both(shift[u]), m1 = both(-inv_d * s1[u]), m2 = both(-inv_d * s2[u] * r1);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const F2 n = (G > 32 ? s[e] + sh : s[e]) * r;
-                dga[e] = fma2(dn[e], n, dga[e]);
-                const F2 g = r * fma2(n, m2, fma2(dn[e], ga[e], m1));
-                dn[e] = RES ? g + more[e] : g;
+                const F2 n = (G > 32 ? s[u][e] + sh : s[u][e]) * r;
+                dga[e] = fma2(dn[u][e], n, dga[e]);
+                const F2 g = r * fma2(n, m2, fma2(dn[u][e], ga[e], m1));
+                dn[u][e] = RES ? g + more[u][e] : g;
             }
             if (mine)
-                store_pairs(dx + at * d + row.c, dn);
+                store_pairs(dx + r0 * d + row.c, dn[u]);
         }
     }
     if (!partial)

@@ -244,8 +244,8 @@ FW_DEV float reference(float x) { return x == -INFINITY ? 0.f : rintf(x * kLog2e
 // runs along the output, and so does A's of the second product.
 template <Mode MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
-    vocab_gemm_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps maps1, GemmArgs g,
-                      unsigned *status) {
+    vocab_gemm_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps maps1,
+                      const __grid_constant__ GemmArgs g, unsigned *status) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *full = (uint64_t *)(smem + kBarOff); // [kStages] (leader's) both CTAs' copies of a step have landed
@@ -279,10 +279,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
     tc_fence_after();
     griddep_launch_dependents();
     griddep_wait();
-    g.bias = after_wait(g.bias);
-    g.targets.p = after_wait(g.targets.p);
-    g.row = after_wait(g.row);
-    g.row_target = after_wait(g.row_target);
+    const float *const bias = after_wait(g.bias);
+    const Tokens targets = {after_wait(g.targets.p), g.targets.wide};
+    const float4 *const rows = after_wait(g.row);
+    const int *const row_targets = after_wait(g.row_target);
     const uint32_t tm = *slot;
 
     // Tile i of this pair's walk: of product w, rows mb, columns nb, split z; false past
@@ -456,28 +456,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                 float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (needed && row < q.N) {
                     if (MODE == kLoss) {
-                        target = token_at(g.targets, row, g.vocab);
+                        target = token_at(targets, row, g.vocab);
                     } else {
-                        target = __ldcg(g.row_target + row);
-                        c = __ldcg(g.row + row);
+                        target = __ldcg(row_targets + row);
+                        c = __ldcg(rows + row);
                     }
                 }
                 // its logits, from the bias on
                 F2 z[kCols / 2];
-                const bool from_bias = g.bias && needed;
+                const bool from_bias = bias && needed;
                 if (from_bias) {
                     if (col0 + kCols <= q.V) {
 #pragma unroll
                         for (int j = 0; j < kCols / 4; ++j) {
-                            const float4 b = __ldcg(reinterpret_cast<const float4 *>(g.bias + col0) + j);
+                            const float4 b = __ldcg(reinterpret_cast<const float4 *>(bias + col0) + j);
                             z[2 * j] = pack(b.x, b.y);
                             z[2 * j + 1] = pack(b.z, b.w);
                         }
                     } else {
 #pragma unroll
                         for (int j = 0; j < kCols / 2; ++j)
-                            z[j] = pack(col0 + 2 * j < q.V ? __ldcg(g.bias + col0 + 2 * j) : 0.f,
-                                        col0 + 2 * j + 1 < q.V ? __ldcg(g.bias + col0 + 2 * j + 1) : 0.f);
+                            z[j] = pack(col0 + 2 * j < q.V ? __ldcg(bias + col0 + 2 * j) : 0.f,
+                                        col0 + 2 * j + 1 < q.V ? __ldcg(bias + col0 + 2 * j + 1) : 0.f);
                     }
                 }
                 bool ok = true;
@@ -584,8 +584,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                 done_with_acc();
                 const CUtensorMap *to = p.w ? &maps1.out : &maps0.out;
                 if (q.out == kWeighted) {
-                    const bool there = row < q.N && __ldcg(g.row_target + row) >= 0;
-                    const float w = there ? __ldcg(g.row + row).w : 0.f;
+                    const bool there = row < q.N && __ldcg(row_targets + row) >= 0;
+                    const float w = there ? __ldcg(rows + row).w : 0.f;
 #pragma unroll
                     for (int j = 0; j < kCols; ++j)
                         v[j] = there ? v[j] * w : 0.f;
@@ -946,13 +946,13 @@ int tiles_of(int64_t n) { return (int)((n + kTile - 1) / kTile); }
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Splits of a contraction of kb steps for an output of `tiles`: where the
-// tiles occupy fewer than a quarter of the pairs, as many as fill half of them
-// (dh's and dW's products run together), of four steps at least.
+// tiles occupy fewer than a quarter of the pairs, as many as fill them, of four
+// steps at least.
 struct Splits {
     int n, per;
 };
 Splits splits_of(int64_t tiles, int kb) {
-    int64_t n = tiles * 4 > kPairs ? 1 : std::min<int64_t>(kPairs / 2 / tiles, (kb + 3) / 4);
+    int64_t n = tiles * 4 > kPairs ? 1 : std::min<int64_t>(kPairs / tiles, (kb + 3) / 4);
     n = std::max<int64_t>(1, n);
     const int per = (int)((kb + n - 1) / n);
     return {(kb + per - 1) / per, per};
