@@ -166,8 +166,10 @@ FW_DEV void commit_pair(uint64_t *bar) {
                  "h"((uint16_t)3)
                  : "memory");
 }
+// (relaxed: what it tells of are this warp's reads of TMEM, which have completed; a release
+// would hold the warp at a cluster-scope fence)
 FW_DEV void arrive_at(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // (the wait in the same statement: nothing that reads the registers gets between)
 FW_DEV void tmem_ld32(uint32_t taddr, float *r) {
