@@ -548,25 +548,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                             const float2 v = unpack(fma2(z[(j >> 1) + x], both(kLog2e), both(-ref)));
                             e[x] = pack(ex2(v.x), ex2(v.y)) * both(rq);
                         }
-                        const int k = tk - j;
-                        if (k >= 0 && k < 8)
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const float2 v = unpack(e[x]);
-                                e[x] = pack(2 * x == k ? at_target : v.x, 2 * x + 1 == k ? at_target : v.y);
-                            }
                         uint4 u;
                         const float2 v0 = unpack(e[0]), v1 = unpack(e[1]), v2 = unpack(e[2]), v3 = unpack(e[3]);
-                        u.x = live ? pack_bf16x2(v0.x, v0.y) : 0u;
-                        u.y = live ? pack_bf16x2(v1.x, v1.y) : 0u;
-                        u.z = live ? pack_bf16x2(v2.x, v2.y) : 0u;
-                        u.w = live ? pack_bf16x2(v3.x, v3.y) : 0u;
+                        u.x = pack_bf16x2(v0.x, v0.y);
+                        u.y = pack_bf16x2(v1.x, v1.y);
+                        u.z = pack_bf16x2(v2.x, v2.y);
+                        u.w = pack_bf16x2(v3.x, v3.y);
                         *reinterpret_cast<uint4 *>(out + lane * 128 + (((j >> 3) ^ (lane & 7)) << 4)) = u;
                         if (g.colsum)
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                z[(j >> 1) + x] = live ? e[x] * both(weight) : F2{0};
+                            for (int x = 0; x < 4; ++x) {
+                                const float2 v = unpack(e[x]);
+                                const int k = tk - j - 2 * x;
+                                z[(j >> 1) + x] =
+                                    live ? pack(k == 0 ? at_target : v.x, k == 1 ? at_target : v.y) * both(weight) : F2{0};
+                            }
                     }
+                    if (tk >= 0 && tk < kCols) // the target's entry
+                        *reinterpret_cast<__nv_bfloat16 *>(out + lane * 128 + (((tk >> 3) ^ (lane & 7)) << 4) + 2 * (tk & 7)) =
+                            __float2bfloat16_rn(at_target);
+                    if (!live) // no gradient: zeros, whatever the logits are
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint4 *>(out + lane * 128 + 16 * j) = make_uint4(0, 0, 0, 0);
                     put(&maps0.out, col0, row0, false);
                     if (g.colsum)
 #pragma unroll
@@ -876,23 +880,18 @@ FW_DEV void join_rows(const Rest &q, const RestArgs &a, int cta, bool tokens) {
         if (live) {
             const float *p = q.part + (int64_t)n * a.D + c;
             int z = 0;
-            for (; z + 3 < q.splits; z += 4) {
-                float v[4][8];
+            for (; z < q.splits; z += 8) {
+                float v[8][8];
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    load8(p + (z + u) * q.a_split, v[u]);
+                for (int u = 0; u < 8; ++u)
+                    if (z + u < q.splits)
+                        load8(p + (z + u) * q.a_split, v[u]);
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
+                for (int u = 0; u < 8; ++u)
+                    if (z + u < q.splits)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        s[e] += v[u][e];
-            }
-            for (; z < q.splits; ++z) {
-                float v[8];
-                load8(p + z * q.a_split, v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    s[e] += v[e];
+                        for (int e = 0; e < 8; ++e)
+                            s[e] += v[u][e];
             }
         }
 #pragma unroll

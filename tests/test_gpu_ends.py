@@ -400,6 +400,121 @@ def test_vocab_loss_many_tiles(N, V, D):
             assert rel(x[i:i + 128], w[i:i + 128]) < 2.0 ** -5, i
 
 
+def test_graphs_and_streams():
+    """Two captured graphs replayed in turn and two streams at once: every call has scratch of its own."""
+    r, n = draws(13)
+    ins = [tuple(None if x is None else x.cuda() for x in loss_inputs(N, V, 128, V, bias=True)) for N, V in ((200, 900), (333, 70))]
+
+    def run(a):
+        h, W, t, b, dl = a
+        loss, lse = fw.fw_vocab_loss(h, W, t, bias=b)
+        grads = fw.fw_vocab_loss_backward(h, W, t, loss, lse, dl, bias=b)
+        out = fw.fw_embedding(t, W, scale=2.0)
+        dE = fw.fw_embedding_backward(t, out, W.shape[0])
+        o, s = fw.fw_layer_norm(out, residual=h)
+        return (loss, lse, *grads, out, dE, o, s, *fw.fw_layer_norm_backward(s, None, o, dsum=h))
+
+    want = [run(a) for a in ins]
+    graphs, kept = [], []
+    for a in ins:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            kept.append(run(a))
+    for i in (0, 1, 1, 0):
+        for x in kept[i]:
+            x.zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(kept[i], want[i]))
+    streams = [torch.cuda.Stream() for _ in ins]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(5):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i] = run(ins[i])
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(x, y) for x, y in zip(got[i], want[i]))
+    # a stream given to the call: its outputs belong to it
+    h, W, t, b, dl = ins[0]
+    loss, lse = fw.fw_vocab_loss(h, W, t, bias=b, stream=streams[0])
+    grads = fw.fw_vocab_loss_backward(h, W, t, loss, lse, dl, bias=b, stream=streams[0])
+    out = fw.fw_embedding(t, W, scale=2.0, stream=streams[0])
+    dE = fw.fw_embedding_backward(t, out, W.shape[0], stream=streams[0])
+    o, s = fw.fw_layer_norm(out, residual=h, stream=streams[0])
+    last = fw.fw_layer_norm_backward(s, None, o, dsum=h, stream=streams[0])
+    streams[0].synchronize()
+    assert all(torch.equal(x, y) for x, y in zip((loss, lse, *grads, out, dE, o, s, *last), want[0]))
+
+
+def room(gigabytes):
+    if torch.cuda.mem_get_info()[0] < gigabytes * 1e9:
+        pytest.skip(f"needs {gigabytes} GB")
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 values: the last rows have the bits of calls of their own."""
+    room(70)
+    r = torch.Generator(device="cuda").manual_seed(14)
+    rows, d = 2 ** 31 // 512 + 70, 512
+    x = torch.randn(rows, d, generator=r, device="cuda", dtype=torch.bfloat16)
+    g = torch.randn(d, generator=r, device="cuda")
+    out, s = fw.fw_layer_norm(x, g, residual=x)
+    dx, _, _ = fw.fw_layer_norm_backward(s, g, out, dsum=x)
+    end = slice(rows - 60, rows)
+    o1, s1 = fw.fw_layer_norm(x[end], g, residual=x[end])
+    assert torch.equal(out[end], o1) and torch.equal(s[end], s1)
+    assert torch.equal(dx[end], fw.fw_layer_norm_backward(s1, g, o1, dsum=x[end], return_params=False)[0])
+    del out, s, dx
+    # the same values as a table, and as the gradients of a batch
+    ids = torch.tensor([0, rows - 1, -1, rows // 2, rows - 1], device="cuda")
+    assert torch.equal(fw.fw_embedding(ids, x)[[0, 1, 3, 4]], x[ids[[0, 1, 3, 4]]])
+    dE = fw.fw_embedding_backward(ids, x[:5].contiguous(), rows)
+    assert torch.equal(dE[0], x[0]) and torch.equal(dE[rows // 2], x[3]) and dE[1:rows // 2].count_nonzero() == 0
+    assert torch.equal(dE[-1], (x[1].float() + x[4].float()).bfloat16())
+    del dE
+    big = torch.randint(0, 9, (rows,), generator=r, device="cuda")
+    out = fw.fw_embedding(big, x[:9].contiguous())
+    assert torch.equal(out[end], x[big[end]])
+    dE = fw.fw_embedding_backward(big, out, 9)
+    count = torch.bincount(big, minlength=9).double()
+    want = count[:, None] * x[:9].double()
+    assert torch.all((dE.double() - want).abs() <= (2.0 ** -8 + (96 + rows / 32) * U) * want.abs())
+    del out, x, dE
+    torch.cuda.empty_cache()
+
+
+def test_vocab_loss_offsets_past_32_bits():
+    """An output map of more than 2^31 values, its last entries met: as the same map's halves."""
+    room(40)
+    r = torch.Generator(device="cuda").manual_seed(15)
+    N, V, D = 40, 70001, 32768
+    W = torch.randn(V, D, generator=r, device="cuda", dtype=torch.bfloat16).mul_(D ** -0.5)
+    h = torch.randn(N, D, generator=r, device="cuda", dtype=torch.bfloat16)
+    t = torch.randint(0, V, (N,), generator=r, device="cuda")
+    t[:20] = V - 1 - torch.arange(20, device="cuda")
+    dl = torch.full((N,), 1.0 / N, device="cuda")
+    loss, lse = fw.fw_vocab_loss(h, W, t)
+    dh, dW, _ = fw.fw_vocab_loss_backward(h, W, t, loss, lse, dl)
+    z = torch.cat([h.double() @ W[i:i + 10000].double().T for i in range(0, V, 10000)], 1)
+    want = z.logsumexp(1)
+    assert torch.all((lse - want).abs() < 1e-4)
+    assert torch.all((loss - (want - z.gather(1, t[:, None])[:, 0])).abs() < 1e-4)
+    g = torch.softmax(z, 1)
+    g[torch.arange(N, device="cuda"), t] -= 1
+    g /= N
+    rel = lambda a, w: float((a.double() - w).norm() / w.norm())  # noqa: E731
+    for i in (0, 35000, V - 100):
+        assert rel(dW[i:i + 100], g[:, i:i + 100].T @ h.double()) < 2.0 ** -6
+    wh = sum(g[:, i:i + 10000] @ W[i:i + 10000].double() for i in range(0, V, 10000))
+    assert rel(dh, wh) < 2.0 ** -6
+    one = fw.fw_vocab_loss(h[:1, :8192].contiguous(), W[:, :8192].contiguous(), t[:1])
+    assert torch.isfinite(one[0]).all()
+    del W, dW, z, g
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------- a run of them
 def test_a_model_end_to_end():
     """Embedding, a gated layer between residual sums and norms, the loss over the same (tied) table, and every gradient
