@@ -33,13 +33,13 @@ namespace {
 
 constexpr int kT = 256;
 
-// 8 channels as they were loaded, read once.
+// 8 channels as they were loaded.
 template <typename T> struct Raw;
 template <> struct Raw<float> {
     float4 a, b;
     FW_DEV void load(const float *p) {
-        a = __ldcs(reinterpret_cast<const float4 *>(p));
-        b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+        a = __ldcg(reinterpret_cast<const float4 *>(p));
+        b = __ldcg(reinterpret_cast<const float4 *>(p) + 1);
     }
     FW_DEV void add_to(float (&s)[8]) const {
         s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
@@ -48,7 +48,7 @@ template <> struct Raw<float> {
 };
 template <> struct Raw<__nv_bfloat16> {
     uint4 u;
-    FW_DEV void load(const __nv_bfloat16 *p) { u = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+    FW_DEV void load(const __nv_bfloat16 *p) { u = __ldcg(reinterpret_cast<const uint4 *>(p)); }
     FW_DEV void add_to(float (&s)[8]) const {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -64,7 +64,7 @@ template <> struct Raw<__nv_bfloat16> {
 // rows, 8 channels a thread, are requested before any is written.
 constexpr int kAhead = 4;
 template <typename T>
-__global__ void __launch_bounds__(kT)
+__global__ void __launch_bounds__(kT, sizeof(T) == 2 ? 6 : 4)
     embedding_kernel(Tokens ids, const T *table, T *out, int64_t N, int V, int D, int lg, float scale) {
     griddep_launch_dependents();
     griddep_wait();
@@ -77,24 +77,21 @@ __global__ void __launch_bounds__(kT)
     for (int u = 0; u < kAhead; ++u)
         id[u] = n0 + u < N ? token_at(ids, n0 + u, V) : -1;
     for (int c = 8 * lane; c < D; c += 8 << lg) {
-        float v[kAhead][8];
+        Raw<T> v[kAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            if (id[u] >= 0 && id[u] < V) {
-                load8(table + (int64_t)id[u] * D + c, v[u]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[u][e] = id[u] < 0 ? 0.f : __int_as_float(0x7fffffff);
-            }
-        }
+        for (int u = 0; u < kAhead; ++u)
+            if (id[u] >= 0 && id[u] < V)
+                v[u].load(table + (int64_t)id[u] * D + c);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
             if (n0 + u < N) {
+                float o[8] = {};
+                if (id[u] >= 0 && id[u] < V)
+                    v[u].add_to(o);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    v[u][e] = id[u] < 0 ? 0.f : v[u][e] * scale;
-                store8(out + (n0 + u) * D + c, v[u]);
+                    o[e] = id[u] < V ? o[e] * scale : __int_as_float(0x7fffffff);
+                store8(out + (n0 + u) * D + c, o);
             }
     }
 }
