@@ -536,7 +536,7 @@ def fw_selftest_flag_timeout(limit_us: int = 2000, stream=None):
 def _here(names, *tensors):
     """The tensors (None aside) are contiguous and on the current CUDA device,
     the one the library launches on; returns the device's current stream."""
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()  # (a tensor of the device is there, or the check fails: CUDA is initialised)
     for i, t in enumerate(tensors):
         if t is not None and (t.get_device() != dev or not t.is_contiguous()):
             raise ValueError(f"{names.split()[i]} must be a contiguous tensor on the current CUDA device")
