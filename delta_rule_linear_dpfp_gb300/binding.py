@@ -152,11 +152,11 @@ def load(path: str = None) -> ctypes.CDLL:
     lib.fw_layer_norm_backward.argtypes = [vp] * 8 + [sz, i64, i32, f32, i32, vp]
     for n in ("fw_vocab_loss_workspace_size", "fw_vocab_loss_backward_workspace_size"):
         getattr(lib, n).restype = sz
-        getattr(lib, n).argtypes = [i32] * 3
+        getattr(lib, n).argtypes = [i32] * 4
     lib.fw_vocab_loss.restype = i32
-    lib.fw_vocab_loss.argtypes = [vp] * 7 + [sz] + [i32] * 4 + [vp]
+    lib.fw_vocab_loss.argtypes = [vp] * 7 + [sz] + [i32] * 5 + [vp]
     lib.fw_vocab_loss_backward.restype = i32
-    lib.fw_vocab_loss_backward.argtypes = [vp] * 11 + [sz] + [i32] * 4 + [vp]
+    lib.fw_vocab_loss_backward.argtypes = [vp] * 11 + [sz] + [i32] * 5 + [vp]
     lib.fw_selftest_umma.restype = i32
     lib.fw_selftest_umma.argtypes = [vp, vp, vp] + [i32] * 5 + [vp]
     if path is None:
@@ -876,11 +876,11 @@ def fw_layer_norm_backward(x, gamma, dout, dsum=None, eps: float = 1e-5, return_
 
 
 def _vocab_shapes(h, W, targets, bias, floats):
-    """(N, V, D) of h [..., D], W [V,D] and targets [...]."""
+    """(N, V, D, dtype code) of h [..., D], W [V,D] and targets [...]."""
     if h.dim() < 1 or W.dim() != 2 or h.shape[-1] != W.shape[1] or targets.shape != h.shape[:-1]:
         raise ValueError("h must be [..., D], W [V,D] and targets [...]")
-    if h.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
-        raise TypeError("h and W must be bf16")
+    if h.dtype != W.dtype:
+        raise ValueError("h and W must share the I/O dtype")
     if bias is not None and (bias.dtype != torch.float32 or bias.shape != W.shape[:1]):
         raise ValueError("bias must be fp32 [V]")
     for t in floats:
@@ -889,36 +889,38 @@ def _vocab_shapes(h, W, targets, bias, floats):
     N, (V, D) = targets.numel(), W.shape
     if max(N, V, D) > 0x7FFFFFFF:
         raise ValueError("every size must be below 2^31")
-    return N, V, D
+    return N, V, D, _dtype_code(h.dtype)
 
 
-def fw_vocab_loss_workspace_size(N, V, D) -> int:
-    return int(load().fw_vocab_loss_workspace_size(N, V, D))
+def fw_vocab_loss_workspace_size(N, V, D, io_dtype=torch.bfloat16) -> int:
+    code = io_dtype if isinstance(io_dtype, int) else _dtype_code(io_dtype)
+    return int(load().fw_vocab_loss_workspace_size(N, V, D, code))
 
 
 def fw_vocab_loss(h, W, targets, bias=None, loss=None, lse=None, workspace=None, stream=None):
     """Softmax cross entropy of the answers h [..., D] over the vocabulary of
-    the output map W [V,D] (bf16; bias fp32 [V] or None), without keeping the
+    the output map W [V,D] (bias fp32 [V] or None), without keeping the
     logits: (loss, lse), fp32 of the targets' shape.  A negative target is
     padding: both are 0."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return fw_vocab_loss(h, W, targets, bias, loss, lse, workspace)
     st = _here("h W targets bias loss lse workspace", h, W, targets, bias, loss, lse, workspace)
-    N, V, D = _vocab_shapes(h, W, targets, bias, (loss, lse))
+    N, V, D, code = _vocab_shapes(h, W, targets, bias, (loss, lse))
     if loss is None:
         loss = torch.empty(targets.shape, dtype=torch.float32, device=h.device)
     if lse is None:
         lse = torch.empty_like(loss)
-    workspace, ws_bytes = _scratch(_size("fw_vocab_loss_workspace_size", N, V, D), workspace, h)
+    workspace, ws_bytes = _scratch(_size("fw_vocab_loss_workspace_size", N, V, D, code), workspace, h)
     rc = load().fw_vocab_loss(h.data_ptr(), W.data_ptr(), _data(bias), targets.data_ptr(), loss.data_ptr(), lse.data_ptr(),
-                              workspace.data_ptr(), ws_bytes, N, V, D, _index_type(targets, "targets"), st)
+                              workspace.data_ptr(), ws_bytes, N, V, D, _index_type(targets, "targets"), code, st)
     _check(rc, "fw_vocab_loss")
     return loss, lse
 
 
-def fw_vocab_loss_backward_workspace_size(N, V, D) -> int:
-    return int(load().fw_vocab_loss_backward_workspace_size(N, V, D))
+def fw_vocab_loss_backward_workspace_size(N, V, D, io_dtype=torch.bfloat16) -> int:
+    code = io_dtype if isinstance(io_dtype, int) else _dtype_code(io_dtype)
+    return int(load().fw_vocab_loss_backward_workspace_size(N, V, D, code))
 
 
 def fw_vocab_loss_backward(h, W, targets, loss, lse, dloss, bias=None, return_dh: bool = True, return_dW: bool = True,
@@ -930,13 +932,13 @@ def fw_vocab_loss_backward(h, W, targets, loss, lse, dloss, bias=None, return_dh
             return fw_vocab_loss_backward(h, W, targets, loss, lse, dloss, bias, return_dh, return_dW, workspace)
     lib = load()
     st = _here("h W targets loss lse dloss bias workspace", h, W, targets, loss, lse, dloss, bias, workspace)
-    N, V, D = _vocab_shapes(h, W, targets, bias, (loss, lse, dloss))
+    N, V, D, code = _vocab_shapes(h, W, targets, bias, (loss, lse, dloss))
     dh = torch.empty_like(h) if return_dh else None
     dW = torch.empty_like(W) if return_dW else None
     dbias = None if bias is None else torch.empty_like(bias)
-    workspace, ws_bytes = _scratch(_size("fw_vocab_loss_backward_workspace_size", N, V, D), workspace, h)
+    workspace, ws_bytes = _scratch(_size("fw_vocab_loss_backward_workspace_size", N, V, D, code), workspace, h)
     rc = lib.fw_vocab_loss_backward(h.data_ptr(), W.data_ptr(), _data(bias), targets.data_ptr(), loss.data_ptr(),
                                     lse.data_ptr(), dloss.data_ptr(), _data(dh), _data(dW), _data(dbias),
-                                    workspace.data_ptr(), ws_bytes, N, V, D, _index_type(targets, "targets"), st)
+                                    workspace.data_ptr(), ws_bytes, N, V, D, _index_type(targets, "targets"), code, st)
     _check(rc, "fw_vocab_loss_backward")
     return dh, dW, dbias

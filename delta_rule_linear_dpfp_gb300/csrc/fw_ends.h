@@ -40,10 +40,10 @@ cudaError_t launch_layer_norm_backward(const void *x, const float *gamma, const 
 
 size_t vocab_loss_workspace_bytes(int N, int V, int D);
 cudaError_t launch_vocab_loss(const void *h, const void *W, const float *bias, Tokens targets, float *loss, float *lse,
-                              void *workspace, int N, int V, int D, cudaStream_t st);
-size_t vocab_loss_backward_workspace_bytes(int N, int V, int D);
+                              void *workspace, int N, int V, int D, int bf16, cudaStream_t st);
+size_t vocab_loss_backward_workspace_bytes(int N, int V, int D, int bf16);
 cudaError_t launch_vocab_loss_backward(const void *h, const void *W, const float *bias, Tokens targets,
                                        const float *loss, const float *lse, const float *dloss, void *dh, void *dW,
-                                       float *dbias, void *workspace, int N, int V, int D, cudaStream_t st);
+                                       float *dbias, void *workspace, int N, int V, int D, int bf16, cudaStream_t st);
 
 } // namespace fw

@@ -30,12 +30,15 @@ int check_norm(int64_t rows, int d, float eps) {
         return FW_ERR_INVALID_ARG;
     return d % 8 || d > kMaxNorm ? FW_ERR_UNSUPPORTED : FW_OK;
 }
-int check_loss(int N, int V, int D) {
+int check_loss(int N, int V, int D, int io_dtype) {
+    if (!dtype_ok(io_dtype))
+        return FW_ERR_INVALID_ARG;
     const int rc = check_table(N, V, D);
     if (rc != FW_OK)
         return rc;
     const int64_t mt = ((int64_t)N + 255) / 256, nt = ((int64_t)V + 255) / 256, dt = ((int64_t)D + 255) / 256;
-    return N > kMaxCount || mt * nt > INT_MAX || mt * dt > INT_MAX / 256 || nt * dt > INT_MAX / 256 ? FW_ERR_UNSUPPORTED
+    const int64_t most = io_dtype == FW_DTYPE_BF16 ? INT_MAX : INT_MAX / 4; // (fp32: tiles of half the edge)
+    return N > kMaxCount || mt * nt > most || mt * dt > INT_MAX / 256 || nt * dt > INT_MAX / 256 ? FW_ERR_UNSUPPORTED
                                                                                                     : FW_OK;
 }
 
@@ -135,57 +138,58 @@ FW_API int fw_layer_norm_backward(const void *x, const float *gamma, const void 
                                                       io_dtype == FW_DTYPE_BF16, st));
 }
 
-FW_API size_t fw_vocab_loss_workspace_size(int N, int V, int D) {
-    if (check_loss(N, V, D) != FW_OK || N == 0)
+FW_API size_t fw_vocab_loss_workspace_size(int N, int V, int D, int io_dtype) {
+    if (check_loss(N, V, D, io_dtype) != FW_OK || N == 0)
         return 0;
     return fw::vocab_loss_workspace_bytes(N, V, D);
 }
 
 FW_API int fw_vocab_loss(const void *h, const void *W, const float *bias, const void *targets, float *loss, float *lse,
-                         void *workspace, size_t workspace_bytes, int N, int V, int D, int index_type, void *stream) {
+                         void *workspace, size_t workspace_bytes, int N, int V, int D, int index_type, int io_dtype,
+                         void *stream) {
     if (!index_ok(index_type))
         return FW_ERR_INVALID_ARG;
-    const int rc = check_loss(N, V, D);
+    const int rc = check_loss(N, V, D, io_dtype);
     if (rc != FW_OK)
         return rc;
     if (N == 0)
         return FW_OK;
     if (!usable(h) || !usable(W) || !aligned16(bias) || !tokens_ok(targets, index_type) || !usable(loss) || !usable(lse) ||
-        !usable(workspace) || workspace_bytes < fw_vocab_loss_workspace_size(N, V, D))
+        !usable(workspace) || workspace_bytes < fw_vocab_loss_workspace_size(N, V, D, io_dtype))
         return FW_ERR_INVALID_ARG;
     return cuda_status(fw::launch_vocab_loss(h, W, bias, {targets, index_type}, loss, lse, workspace, N, V, D,
-                                             static_cast<cudaStream_t>(stream)));
+                                             io_dtype == FW_DTYPE_BF16, static_cast<cudaStream_t>(stream)));
 }
 
-FW_API size_t fw_vocab_loss_backward_workspace_size(int N, int V, int D) {
-    if (check_loss(N, V, D) != FW_OK || N == 0)
+FW_API size_t fw_vocab_loss_backward_workspace_size(int N, int V, int D, int io_dtype) {
+    if (check_loss(N, V, D, io_dtype) != FW_OK || N == 0)
         return 0;
-    return fw::vocab_loss_backward_workspace_bytes(N, V, D);
+    return fw::vocab_loss_backward_workspace_bytes(N, V, D, io_dtype == FW_DTYPE_BF16);
 }
 
 FW_API int fw_vocab_loss_backward(const void *h, const void *W, const float *bias, const void *targets,
                                   const float *loss, const float *lse, const float *dloss, void *dh, void *dW,
                                   float *dbias, void *workspace, size_t workspace_bytes, int N, int V, int D,
-                                  int index_type, void *stream) {
+                                  int index_type, int io_dtype, void *stream) {
     if (!index_ok(index_type))
         return FW_ERR_INVALID_ARG;
-    const int rc = check_loss(N, V, D);
+    const int rc = check_loss(N, V, D, io_dtype);
     if (rc != FW_OK)
         return rc;
     if (!aligned16(dh) || !aligned16(dW) || !aligned16(dbias))
         return FW_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (N == 0) { // no token: gradients of zero
-        cudaError_t e = dW ? cudaMemsetAsync(dW, 0, 2 * (size_t)V * D, st) : cudaSuccess;
+        cudaError_t e = dW ? cudaMemsetAsync(dW, 0, (io_dtype == FW_DTYPE_BF16 ? 2 : 4) * (size_t)V * D, st) : cudaSuccess;
         if (e == cudaSuccess && dbias)
             e = cudaMemsetAsync(dbias, 0, sizeof(float) * V, st);
         return cuda_status(e);
     }
     if (!usable(h) || !usable(W) || !aligned16(bias) || !tokens_ok(targets, index_type) || !usable(loss) || !usable(lse) ||
-        !usable(dloss) || !usable(workspace) || workspace_bytes < fw_vocab_loss_backward_workspace_size(N, V, D))
+        !usable(dloss) || !usable(workspace) || workspace_bytes < fw_vocab_loss_backward_workspace_size(N, V, D, io_dtype))
         return FW_ERR_INVALID_ARG;
     return cuda_status(fw::launch_vocab_loss_backward(h, W, bias, {targets, index_type}, loss, lse, dloss, dh, dW, dbias,
-                                                      workspace, N, V, D, st));
+                                                      workspace, N, V, D, io_dtype == FW_DTYPE_BF16, st));
 }
 
 } // extern "C"

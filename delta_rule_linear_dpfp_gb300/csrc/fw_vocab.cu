@@ -19,7 +19,7 @@
 //
 // Forward: the epilogue turns a row's 128 columns into (max, sum of
 // exponentials) and picks out the target's logit; a second kernel joins a
-// token's parts.  Backward, by pieces of the vocabulary of at most 512 MB of
+// token's parts.  Backward, by pieces of the vocabulary of at most 1 GB of
 // (bf16) g: one product forms the logits again and its epilogue writes
 //   G = (exp(z - lse) - [v = t]) / q,   q = 1 - p_t = -expm1(-loss),
 // then dh += G W and dW = G^T (w h) with w = q dloss (dh's rows take w at the
@@ -31,20 +31,19 @@
 
 #include <algorithm>
 
-#include "fw_ends.h"
 #include "fw_forward_tc.h"
-#include "fw_pairs.cuh"
 #include "fw_tc.cuh"
+#include "fw_vocab.h"
 
 namespace fw {
 
 namespace {
 
 using namespace tc;
+using namespace vocab;
 
-constexpr int kEpiWarps = 16;  // each 32 rows x 64 columns of a CTA's 128 x 256
+constexpr int kEpiWarps = 16;  // each 32 rows x kCols columns of a CTA's 128 x 256
 constexpr int kT = 32 * (4 + kEpiWarps); // warp 0: copies, 1: products, 2: TMEM, 4 and on: epilogue
-constexpr int kCols = 64;      // columns of an epilogue warp
 constexpr int kTile = 256;    // rows and columns of a pair's tile
 constexpr int kStages = 5;
 constexpr int kStageBytes = 32768; // half of A's rows and half of B's, 64 of the contraction
@@ -53,13 +52,10 @@ constexpr int kOutBytes = kEpiWarps * 4096; // a box of 32 rows x 128 bytes per 
 constexpr int kBarOff = kOutOff + kOutBytes;
 constexpr int kSmem = kBarOff + 256 + 1024;
 static_assert(kSmem <= 227 * 1024, "one CTA's shared memory");
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 // Steps of 64 that an accumulator of logits takes: the tensor core truncates what it
 // adds, so that a sum of many terms of one sign falls short by about 2^-25 of itself with
 // every step of 16; chunks of 512 are added in the epilogue, where sums are rounded.
 constexpr int kLogitSteps = 8;
-constexpr float kNoRef = -1e30f; // the reference of no entries: below every other
-constexpr float kQMin = 1e-7f; // q below it (p_t = 1 in 32 bits) divides nothing
 
 enum Mode {
     kLoss,    // h W^T: parts of the logits' log-sum-exp, the targets' logits
@@ -237,10 +233,6 @@ FW_DEV float columns_sum(const F2 *p, int lane) {
     }
     return x[0];
 }
-
-// A reference near x for exponentials: x log2 e to a sixteenth, so that z log2 e less
-// the reference takes one rounding (0 for a row that is masked throughout).
-FW_DEV float reference(float x) { return x == -INFINITY ? 0.f : rintf(x * kLog2e * 16.f) * 0.0625f; }
 
 // kLoss, kGrad: both operands' memory runs along the contraction.  kProducts: B's
 // runs along the output, and so does A's of the second product.
@@ -636,220 +628,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512) : "memory");
 }
 
-// ------------------------------------------------------------ few tokens
-// Up to four answers: bound by reading W once, so a product on CUDA cores from
-// registers, whose start and end cost less than the tensor cores' (one token
-// over 32 000 entries, D 512: 8.4 us against 16.5).  A warp takes four rows of W at
-// a time, its lanes 8 channels each; h sits in shared memory in 32 bits.  After
-// the lanes' sums have been exchanged each lane keeps the (reference, sum of
-// exponentials) of one token over the rows it got.
-constexpr int kFewT = 256, kFewRows = 4, kFewStep = kFewT / 32 * kFewRows;
-constexpr int kFewValues = 11264; // NT D: 44 KB of shared memory
-constexpr int few_an_sm(int nt) { return nt == 1 ? 4 : 2; } // (registers)
-
-template <int NT>
-__global__ void __launch_bounds__(kFewT, few_an_sm(NT))
-    vocab_few_kernel(const __nv_bfloat16 *h, const __nv_bfloat16 *W, const float *bias, Tokens targets, float2 *part,
-                     float *target_z, int N, int V, int D) {
-    extern __shared__ float hs[]; // [NT][D]
-    __shared__ float2 red[kFewT];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    griddep_launch_dependents();
-    griddep_wait();
-    h = after_wait(h);
-    W = after_wait(W);
-    bias = after_wait(bias);
-    targets.p = after_wait(targets.p);
-    for (int i = 8 * tid; i < NT * D; i += 8 * kFewT) {
-        float v[8] = {};
-        if (i < N * D)
-            load8(h + i, v);
-        store8(hs + i, v);
-    }
-    __syncthreads();
-    constexpr int n = kFewRows * NT; // a step's values: row r, token t at r NT + t
-    static_assert(n <= 32, "a lane keeps one value");
-    int mine = 0; // the value that this lane keeps
-#pragma unroll
-    for (int half = n / 2, o = 16; half > 0; half /= 2, o /= 2)
-        mine += lane & o ? half : 0;
-    const int t = mine % NT, r0 = mine / NT;
-    const bool owner = (lane & (32 / n - 1)) == 0 && t < N; // (of the lanes that end up with the same value)
-    const int target = t < N ? token_at(targets, t, V) : -1;
-    float top = kNoRef, total = 0.f;
-    for (int64_t v0 = ((int64_t)blockIdx.x * (kFewT / 32) + warp) * kFewRows; v0 < V; v0 += (int64_t)gridDim.x * kFewStep) {
-        F2 acc[kFewRows][NT] = {};
-        const float b = bias && owner && v0 + r0 < V ? __ldcg(bias + v0 + r0) : 0.f;
-#pragma unroll 2
-        for (int c = 8 * lane; c < D; c += 256) {
-            uint4 w[kFewRows];
-#pragma unroll
-            for (int r = 0; r < kFewRows; ++r)
-                w[r] = v0 + r < V ? __ldcs(reinterpret_cast<const uint4 *>(W + (v0 + r) * D + c)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int k = 0; k < NT; ++k) {
-                const float4 x = *reinterpret_cast<const float4 *>(hs + k * D + c);
-                const float4 y = *reinterpret_cast<const float4 *>(hs + k * D + c + 4);
-#pragma unroll
-                for (int r = 0; r < kFewRows; ++r) {
-                    auto two = [](uint32_t u) { return pack(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); };
-                    acc[r][k] = fma2(two(w[r].x), pack(x.x, x.y), acc[r][k]);
-                    acc[r][k] = fma2(two(w[r].y), pack(x.z, x.w), acc[r][k]);
-                    acc[r][k] = fma2(two(w[r].z), pack(y.x, y.y), acc[r][k]);
-                    acc[r][k] = fma2(two(w[r].w), pack(y.z, y.w), acc[r][k]);
-                }
-            }
-        }
-        float x[n];
-#pragma unroll
-        for (int i = 0; i < n; ++i)
-            x[i] = sum(acc[i / NT][i % NT]);
-        int o = 16;
-#pragma unroll
-        for (int half = n / 2; half > 0; half /= 2, o /= 2) {
-            const bool up = lane & o;
-#pragma unroll
-            for (int j = 0; j < half; ++j) {
-                const float give = up ? x[j] : x[j + half], keep = up ? x[j + half] : x[j];
-                x[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-            }
-        }
-#pragma unroll
-        for (int o1 = 16 / n; o1 > 0; o1 /= 2)
-            x[0] += __shfl_xor_sync(0xffffffffu, x[0], o1);
-        if (owner && v0 + r0 < V) {
-            const float z = x[0] + b;
-            if (v0 + r0 == target)
-                target_z[t] = z;
-            if (z != -INFINITY) {
-                const float m = fmaxf(top, reference(z));
-                total = total * ex2(top - m) + ex2(fmaf(z, kLog2e, -m));
-                top = m;
-            }
-        }
-    }
-    red[tid] = make_float2(top, total);
-    __syncthreads();
-    if (warp < N) { // this warp's token: what the lanes that keep it have, of every warp
-        top = kNoRef;
-        total = 0.f;
-        auto join = [&](float2 p) {
-            const float m = fmaxf(top, p.x);
-            total = total * ex2(top - m) + p.y * ex2(p.x - m);
-            top = m;
-        };
-        if (t == warp && owner)
-            for (int w = 0; w < kFewT / 32; ++w)
-                join(red[32 * w + lane]);
-        for (int o = 16; o > 0; o >>= 1)
-            join(make_float2(__shfl_xor_sync(0xffffffffu, top, o), __shfl_xor_sync(0xffffffffu, total, o)));
-        if (lane == 0)
-            part[(size_t)blockIdx.x * N + warp] = make_float2(top, total);
-    }
-}
-
-// ------------------------------------------------------------ small kernels
 constexpr int kS = 256;
-
-// A token's parts joined: 32 tokens of a CTA and 32 threads for each, or one
-// token and 1024 where there are few.
-constexpr int kJ = 1024;
-__global__ void __launch_bounds__(kJ)
-    join_parts_kernel(const float2 *part, const float *target_z, Tokens targets, float *loss, float *lse, int N, int V,
-                      int nparts, int tokens) {
-    __shared__ float2 red[kJ];
-    griddep_launch_dependents();
-    griddep_wait();
-    part = after_wait(part);
-    target_z = after_wait(target_z);
-    targets.p = after_wait(targets.p);
-    const int slices = kJ / tokens, i = threadIdx.x % tokens, w = threadIdx.x / tokens;
-    const int n = blockIdx.x * tokens + i;
-    float top = kNoRef, total = 0.f;
-    auto join = [&](float2 p) { // (references are sixteenths: their differences are exact)
-        const float m = fmaxf(top, p.x);
-        total = total * ex2(top - m) + p.y * ex2(p.x - m);
-        top = m;
-    };
-    if (n < N)
-        for (int k = w; k < nparts; k += 8 * slices) {
-            float2 p[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                p[u] = k + u * slices < nparts ? __ldcg(part + (size_t)(k + u * slices) * N + n)
-                                               : make_float2(kNoRef, 0.f);
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                join(p[u]);
-        }
-    red[threadIdx.x] = make_float2(top, total);
-    for (int o = slices / 2; o > 0; o >>= 1) {
-        __syncthreads();
-        if (w < o) {
-            join(red[threadIdx.x + o * tokens]);
-            red[threadIdx.x] = make_float2(top, total);
-        }
-    }
-    if (w == 0 && n < N) {
-        const int t = token_at(targets, n, V);
-        const float l = logf(total); // lse = top ln 2 + l
-        loss[n] = t < 0 ? 0.f : t >= V ? __int_as_float(0x7fffffff) : fmaf(fmaf(-__ldcg(target_z + n), kLog2e, top), kLn2, l);
-        lse[n] = t < 0 ? 0.f : fmaf(top, kLn2, l);
-    }
-}
-
-// What a token brings to G and to its row of dh: with q = max(-expm1(-loss), kQMin),
-//   G = 2^(z log2 e - row.x) row.y off the target, row.z on it; q dloss = row.w,
-// all 0 for a token without a gradient.
-FW_DEV bool row_constants(const Tokens &targets, const float *loss, const float *lse, const float *dloss, int n, int V,
-                          float4 &row, int &target) {
-    const int t = token_at(targets, n, V);
-    target = t < V ? t : -1; // (past the vocabulary: the loss is NaN, there is no gradient)
-    row = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (target < 0)
-        return false;
-    const float q = -expm1f(-__ldcg(loss + n)), s = __ldcg(lse + n), over = fmaxf(q, kQMin);
-    row.x = reference(s);
-    row.y = ex2(fmaf(-s, kLog2e, row.x)) / over; // (what the reference is off by)
-    row.z = -q / over;
-    row.w = over * __ldcg(dloss + n);
-    return true;
-}
-
-// The tokens' constants, and w h in bf16 (wh, or null): zeros for the tokens without a
-// gradient, whatever h holds there.
-__global__ void __launch_bounds__(kS)
-    rows_kernel(const __nv_bfloat16 *h, Tokens targets, const float *loss, const float *lse, const float *dloss,
-                float4 *row, int *row_target, __nv_bfloat16 *wh, int N, int V, int D, int lg) {
-    griddep_launch_dependents();
-    griddep_wait();
-    h = after_wait(h);
-    targets.p = after_wait(targets.p);
-    loss = after_wait(loss);
-    lse = after_wait(lse);
-    dloss = after_wait(dloss);
-    const int n = (int)(blockIdx.x * (kS >> lg) + (threadIdx.x >> lg)), lane = threadIdx.x & ((1 << lg) - 1);
-    if (n >= N)
-        return;
-    float4 r;
-    int target;
-    const bool live = row_constants(targets, loss, lse, dloss, n, V, r, target);
-    if (lane == 0) {
-        row[n] = r;
-        row_target[n] = target;
-    }
-    if (wh)
-        for (int c = 8 * lane; c < D; c += 8 << lg) {
-            float v[8] = {};
-            if (live) {
-                load8(h + (size_t)n * D + c, v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] *= r.w;
-            }
-            store8(wh + (size_t)n * D + c, v);
-        }
-}
 
 // What is left of a piece, by the CTA: dh's rows and dW's from the sums of the splits,
 // added in order and rounded once (dh's times their weight, zeros without a gradient),
@@ -940,11 +719,7 @@ __global__ void __launch_bounds__(kS) rest_kernel(RestArgs a) {
 }
 
 // ------------------------------------------------------------------- plans
-constexpr int kPairs = 76; // of a GB300's SMs: what the splits (and so the workspaces) go by
-constexpr size_t kPieceBytes = (size_t)512 << 20;
-
 int tiles_of(int64_t n) { return (int)((n + kTile - 1) / kTile); }
-size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Splits of a contraction of kb steps for an output of `tiles`: where the
 // tiles occupy fewer than a quarter of the pairs, as many as fill them, of four
@@ -992,14 +767,6 @@ Plan plan_of(int N, int V, int D) {
     p.colsum = take((size_t)4 * ((N + 31) / 32) * p.width);
     p.bytes = at;
     return p;
-}
-
-// log2 of the threads of a row of D channels, 8 a thread (at most a CTA's).
-int group_log2(int D) {
-    int lg = 0;
-    while ((8 << lg) < D && lg < 8)
-        ++lg;
-    return lg;
 }
 
 // Pairs of CTAs that the device runs at once.
@@ -1071,42 +838,41 @@ template <Mode MODE> cudaError_t launch_gemm(const Maps &maps0, const Maps &maps
 int token_group(int N, int D) { return (int)std::max<int64_t>(8, std::min<int64_t>(tiles_of(N), (32 << 20) / ((int64_t)kTile * D * 2))); }
 
 
-// Few tokens: the form without tensor cores, and the parts that each form leaves of a token.
-int few_tokens(int N) { return N <= 2 ? N : 4; }
-bool few(int N, int D) { return N <= 4 && few_tokens(N) * (int64_t)D <= kFewValues; }
-int parts_of(int N, int V, int D) {
-    return few(N, D) ? std::min((V - 1) / kFewStep + 1, 2 * kPairs * few_an_sm(few_tokens(N))) : (V - 1) / kCols + 1;
-}
-
-template <int NT>
-cudaError_t launch_few(const void *h, const void *W, const float *bias, Tokens targets, float2 *part, float *target_z,
-                       int N, int V, int D, int nparts, cudaStream_t st) {
-    return launch_pdl(vocab_few_kernel<NT>, dim3(nparts), dim3(kFewT), sizeof(float) * NT * D, st, (const __nv_bfloat16 *)h,
-                      (const __nv_bfloat16 *)W, bias, targets, part, target_z, N, V, D);
-}
-
 } // namespace
+
+cudaError_t vocab::launch_join_bias(const float *colsum, float *dbias, int V, int blocks, int ldc, cudaStream_t st) {
+    RestArgs r = {};
+    r.colsum = colsum;
+    r.dbias = dbias;
+    r.V = V;
+    r.blocks = blocks;
+    r.ldc = ldc;
+    return launch_pdl(rest_kernel, dim3((V + 31) / 32), dim3(kS), 0, st, r);
+}
 
 size_t vocab_loss_workspace_bytes(int N, int V, int D) {
     return up256(sizeof(float2) * (size_t)parts_of(N, V, D) * N) + up256(sizeof(float) * (size_t)N);
 }
 
 cudaError_t launch_vocab_loss(const void *h, const void *W, const float *bias, Tokens targets, float *loss, float *lse,
-                              void *workspace, int N, int V, int D, cudaStream_t st) {
+                              void *workspace, int N, int V, int D, int bf16, cudaStream_t st) {
     const int nparts = parts_of(N, V, D);
-    GemmArgs g = {};
-    g.vocab = V;
-    g.bias = bias;
-    g.targets = targets;
-    g.part = static_cast<float2 *>(workspace);
-    g.target_z = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + up256(sizeof(float2) * (size_t)nparts * N));
+    float2 *part = static_cast<float2 *>(workspace);
+    float *target_z = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + up256(sizeof(float2) * (size_t)nparts * N));
     cudaError_t e;
     if (few(N, D)) {
-        e = N == 1   ? launch_few<1>(h, W, bias, targets, g.part, g.target_z, N, V, D, nparts, st)
-            : N == 2 ? launch_few<2>(h, W, bias, targets, g.part, g.target_z, N, V, D, nparts, st)
-                     : launch_few<4>(h, W, bias, targets, g.part, g.target_z, N, V, D, nparts, st);
+        e = launch_few(h, W, bias, targets, part, target_z, N, V, D, bf16, st);
+    } else if (!bf16) {
+        e = loss_products_f32(static_cast<const float *>(h), static_cast<const float *>(W), bias, targets, part, target_z, N,
+                              V, D, st);
     } else {
         const int kb = (D + 63) / 64;
+        GemmArgs g = {};
+        g.vocab = V;
+        g.bias = bias;
+        g.targets = targets;
+        g.part = part;
+        g.target_z = target_z;
         g.of[0] = product(N, V, kb, kb, token_group(N, D));
         Maps m;
         e = make_bf16_map(&m.a, h, N, D, D, 128);
@@ -1116,18 +882,19 @@ cudaError_t launch_vocab_loss(const void *h, const void *W, const float *bias, T
         if (e == cudaSuccess)
             e = launch_gemm<kLoss>(m, m, g, st);
     }
-    if (e != cudaSuccess)
-        return e;
-    const int tokens = N < 512 ? 1 : 32;
-    return launch_pdl(join_parts_kernel, dim3((N + tokens - 1) / tokens), dim3(kJ), 0, st, (const float2 *)g.part,
-                      (const float *)g.target_z, targets, loss, lse, N, V, nparts, tokens);
+    return e != cudaSuccess ? e : launch_join_parts(part, target_z, targets, loss, lse, N, V, nparts, st);
 }
 
-size_t vocab_loss_backward_workspace_bytes(int N, int V, int D) { return plan_of(N, V, D).bytes; }
+size_t vocab_loss_backward_workspace_bytes(int N, int V, int D, int bf16) {
+    return bf16 ? plan_of(N, V, D).bytes : backward_workspace_f32(N, V, D);
+}
 
 cudaError_t launch_vocab_loss_backward(const void *h, const void *W, const float *bias, Tokens targets,
                                        const float *loss, const float *lse, const float *dloss, void *dh, void *dW,
-                                       float *dbias, void *workspace, int N, int V, int D, cudaStream_t st) {
+                                       float *dbias, void *workspace, int N, int V, int D, int bf16, cudaStream_t st) {
+    if (!bf16)
+        return backward_f32(static_cast<const float *>(h), static_cast<const float *>(W), bias, targets, loss, lse, dloss,
+                            static_cast<float *>(dh), static_cast<float *>(dW), dbias, workspace, N, V, D, st);
     const Plan p = plan_of(N, V, D);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     __nv_bfloat16 *G = reinterpret_cast<__nv_bfloat16 *>(ws + p.G), *wh = reinterpret_cast<__nv_bfloat16 *>(ws + p.wh);
@@ -1153,8 +920,7 @@ cudaError_t launch_vocab_loss_backward(const void *h, const void *W, const float
     if (e == cudaSuccess && dW && !dw_direct)
         e = make_f32_sw128_map(&to_dw.out, dw_part, p.dw.n * p.width, D, D, 32);
     if (e == cudaSuccess)
-        e = launch_pdl(rows_kernel, dim3((N + per_cta - 1) / per_cta), dim3(kS), 0, st, (const __nv_bfloat16 *)h, targets,
-                       loss, lse, dloss, row, row_target, dW ? wh : nullptr, N, V, D, lg);
+        e = launch_rows(h, targets, loss, lse, dloss, row, row_target, dW ? wh : nullptr, N, V, D, st);
     for (int v0 = 0; e == cudaSuccess && v0 < V; v0 += p.width) {
         const int nv = std::min(p.width, V - v0);
         const bool last = v0 + p.width >= V;
@@ -1175,13 +941,13 @@ cudaError_t launch_vocab_loss_backward(const void *h, const void *W, const float
             q.row_target = row_target;
             q.of[1].per = 1;
             if (dh) {
-                q.of[0] = product(N, D, (nv + 63) / 64, p.dh.per, 8);
+                q.of[0] = product(N, D, (nv + 63) / 64, p.dh.per, 4);
                 q.of[0].b0 = v0;
                 q.of[0].out = dh_direct ? kWeighted : v0 ? kAdd : kF32;
                 q.of[0].rows_a_split = (int)dh_rows;
             }
             if (dW) {
-                q.of[1] = product(nv, D, kn, p.dw.per, 8);
+                q.of[1] = product(nv, D, kn, p.dw.per, 4);
                 q.of[1].out = dw_direct ? kBf16 : kF32;
                 q.of[1].rows_a_split = p.width;
                 if (dw_direct)

@@ -594,7 +594,7 @@ typedef enum fw_index {
 FW_API int fw_embedding(const void *ids, const void *table, void *out, int64_t N, int V, int D, float scale,
                         int index_type, int io_dtype, void *stream);
 
-/* About N (16 + D / 8) + 8 V bytes. */
+/* 16 N bytes, and 8 D for every 8 (up to 8192 tokens), 16 (up to 32768) or 32 tokens. */
 FW_API size_t fw_embedding_backward_workspace_size(int64_t N, int V, int D);
 
 /*
@@ -638,46 +638,51 @@ FW_API int fw_layer_norm_backward(const void *x, const float *gamma, const void 
                                   float *dgamma, float *dbeta, void *workspace, size_t workspace_bytes, int64_t rows,
                                   int d, float eps, int io_dtype, void *stream);
 
-/* About 8 N V / 128 bytes: the logits are not kept. */
-FW_API size_t fw_vocab_loss_workspace_size(int N, int V, int D);
+/* About N V / 8 bytes: the logits are not kept. */
+FW_API size_t fw_vocab_loss_workspace_size(int N, int V, int D, int io_dtype);
 
 /*
  * fw_vocab_loss -- softmax cross entropy of N answers over a vocabulary:
  *   z_n = W h_n + bias,  lse_n = log sum_v exp(z_nv),  loss_n = lse_n - z_n,target
- *   h       : [N, D]  bf16
- *   W       : [V, D]  bf16 (an embedding's table, for one)
+ *   h       : [N, D]  io_dtype
+ *   W       : [V, D]  io_dtype (an embedding's table, for one)
  *   bias    : [V]     fp32, or NULL; -infinity takes an entry out of the
  *             vocabulary (its gradient is zero)
  *   targets : [N]     fw_index
  *   loss, lse : [N]   fp32     (written)
- * Products of bf16 values summed in fp32 on the tensor cores, everything after
- * them in fp32.  Any V; a token whose entries are all taken out has a NaN loss.
+ * bf16: products summed in fp32 on the tensor cores, by 512 channels (up to four
+ * tokens: on CUDA cores), everything after them in fp32.  fp32: fp32 arithmetic
+ * throughout, on CUDA cores.  Any V; a token whose entries are all taken out has
+ * a NaN loss.
  */
 FW_API int fw_vocab_loss(const void *h, const void *W, const float *bias, const void *targets, float *loss, float *lse,
-                         void *workspace, size_t workspace_bytes, int N, int V, int D, int index_type, void *stream);
+                         void *workspace, size_t workspace_bytes, int N, int V, int D, int index_type, int io_dtype,
+                         void *stream);
 
 /*
- * 2 N (V + D) bytes for a small vocabulary; a large one is worked off in pieces
- * of N tokens x up to 512 MB of bf16 values, plus fp32 sums of dh.
+ * bf16: 2 N (V + D) bytes, fp32: 4 N V; a large vocabulary is worked off in pieces
+ * for which that is 1 GB.  Beside it fp32 sums of dh (4 N D bytes and more where
+ * there are several pieces, or where a product is split) and of dbias (a
+ * sixteenth, or an eighth, of the piece).
  */
-FW_API size_t fw_vocab_loss_backward_workspace_size(int N, int V, int D);
+FW_API size_t fw_vocab_loss_backward_workspace_size(int N, int V, int D, int io_dtype);
 
 /*
  * fw_vocab_loss_backward -- gradients of sum_n dloss_n loss_n.
  *   loss, lse : [N] fp32, as fw_vocab_loss wrote them for the same inputs
  *   dloss     : [N] fp32
- *   dh        : [N, D] bf16, dW : [V, D] bf16, dbias : [V] fp32, each written,
- *               or NULL to skip it
- * The logits are formed again; the softmax's gradient is rounded to bf16 on
- * its way into the products with W and h, relative to 1 - exp(-loss) so that
- * the target's entry is exact, and h times that and dloss once more: dh and dW
- * are off by about what rounding them to bf16 alone costs.  dbias is in fp32
- * throughout.
+ *   dh        : [N, D] io_dtype, dW : [V, D] io_dtype, dbias : [V] fp32, each
+ *               written, or NULL to skip it
+ * The logits are formed again.  bf16: the softmax's gradient is rounded on its
+ * way into the products with W and h, relative to 1 - exp(-loss) so that the
+ * target's entry is exact, and h times that and dloss once more: dh and dW are
+ * off by about what rounding them to bf16 alone costs.  dbias, and everything
+ * with fp32 tensors, is in fp32 throughout.
  */
 FW_API int fw_vocab_loss_backward(const void *h, const void *W, const float *bias, const void *targets,
                                   const float *loss, const float *lse, const float *dloss, void *dh, void *dW,
                                   float *dbias, void *workspace, size_t workspace_bytes, int N, int V, int D,
-                                  int index_type, void *stream);
+                                  int index_type, int io_dtype, void *stream);
 
 /*
  * fw_device_status -- waits for `stream`, then reports and clears the

@@ -68,19 +68,20 @@ def test_layer_norm_refusals(lib):
     assert call(rows=0, x=None, out=None) == OK and back(rows=0, x=None, dgamma=None, dbeta=None, ws=None, wsb=0) == OK
 
 
-def test_vocab_loss_refusals(lib):
-    need = lib.fw_vocab_loss_workspace_size(5, 9, 64)
+@pytest.mark.parametrize("io", [0, 1])
+def test_vocab_loss_refusals(lib, io):
+    need = lib.fw_vocab_loss_workspace_size(5, 9, 64, io)
     call = _call(lib.fw_vocab_loss, dict(h=FAKE, W=FAKE, bias=None, targets=FAKE, loss=FAKE, lse=FAKE, ws=FAKE, wsb=need, N=5,
-                                         V=9, D=64, index=1, st=None))
-    bneed = lib.fw_vocab_loss_backward_workspace_size(5, 9, 64)
+                                         V=9, D=64, index=1, io=io, st=None))
+    bneed = lib.fw_vocab_loss_backward_workspace_size(5, 9, 64, io)
     back = _call(lib.fw_vocab_loss_backward,
                  dict(h=FAKE, W=FAKE, bias=None, targets=FAKE, loss=FAKE, lse=FAKE, dloss=FAKE, dh=FAKE, dW=FAKE, dbias=None,
-                      ws=FAKE, wsb=bneed, N=5, V=9, D=64, index=1, st=None))
+                      ws=FAKE, wsb=bneed, N=5, V=9, D=64, index=1, io=io, st=None))
     assert need > 0 and bneed > need
     for c, more in ((call, ()), (back, ("dloss",))):
         for n in ("h", "W", "loss", "lse", "ws", *more):
             assert c(**{n: None}) == E and c(**{n: MISALIGNED}) == E, n
-        assert c(bias=MISALIGNED) == E and c(targets=None) == E and c(targets=ODD) == E and c(index=7) == E
+        assert c(bias=MISALIGNED) == E and c(targets=None) == E and c(targets=ODD) == E and c(index=7) == E and c(io=2) == E
         assert c(N=-1) == E and c(V=0) == E and c(D=0) == E and c(D=20) == U and c(D=65544) == U
         assert c(N=2**31 - 1) == U and c(V=2**31 - 1) == U and c(N=2**30, V=2**30) == U
     for n in ("dh", "dW", "dbias"):
@@ -97,7 +98,8 @@ def test_workspace_queries(lib):
     f = lib.fw_layer_norm_backward_workspace_size
     assert f(5, 12) == 0 and f(0, 16) == 0 and f(2**40, 8192) == f(2**20, 8192) > 0
     f = lib.fw_vocab_loss_backward_workspace_size
-    assert f(5, 9, 12) == 0 and f(0, 9, 16) == 0 and f(1, 1, 8) > 0
-    assert f(8192, 10**6, 512) < 2**30                    # pieces of the vocabulary
+    for io in (0, 1):
+        assert f(5, 9, 12, io) == 0 and f(0, 9, 16, io) == 0 and f(1, 1, 8, io) > 0 and f(1, 1, 8, 2) == 0
+        assert f(8192, 10**6, 512, io) < 2**31 < 2 * 8192 * 10**6      # pieces of the vocabulary
     f = lib.fw_vocab_loss_workspace_size
-    assert f(8192, 10**6, 512) < 2**30 < 2 * 8192 * 10**6 and f(2**20, 2**16, 512) > 2**32
+    assert f(8192, 10**6, 512, 1) < 2**31 and f(2**20, 2**16, 512, 1) > 2**32 and f(1, 1, 8, 0) > 0 == f(1, 1, 8, 2)

@@ -236,12 +236,12 @@ def test_embedding_shapes_and_empty():
 
 
 # ------------------------------------------------------------ vocabulary loss
-def loss_inputs(N, V, D, seed, bias=False, padded=False, known=6.0, weights=False):
+def loss_inputs(N, V, D, seed, bias=False, padded=False, known=6.0, weights=False, dtype=torch.bfloat16):
     r, n = draws(seed)
-    W = (n(V, D) * D ** -0.5).bfloat16()
+    W = (n(V, D) * D ** -0.5).to(dtype)
     t = torch.randint(0, V, (N,), generator=r)
     t[0] = V - 1
-    h = (n(N, D) + known * torch.rand(N, 1, generator=r) * W[t].float()).bfloat16()
+    h = (n(N, D) + known * torch.rand(N, 1, generator=r) * W[t].float()).to(dtype)
     b = n(V) if bias else None
     dl = torch.full((N,), 1.0 / N) if not weights else n(N)
     if padded:
@@ -263,7 +263,11 @@ def loss_check(N, V, D, seed, index=torch.int64, **kw):
     W0, tl, d0 = W.double().numpy(), t.tolist(), torch.where(t >= 0, dl.double(), 0.0).numpy()
     rl, rs, p = ends.vocab_loss(h0, W0, tl, None if b is None else b.double().numpy())
     S = np.abs(h0) @ np.abs(W0).T + (0 if b is None else np.abs(b.double().numpy()))
-    zerr = ((D / 16 + 1) * 2.0 ** -22 * S.max(-1) + 2.0 ** -18 * (1 + np.abs(rs))) * live
+    half = HALF[h.dtype]
+    # (fp32: a sum of n products takes n roundings of u of the terms' sizes at most)
+    steps = lambda n: (n / 16 + 40) * 2.0 ** -22 if half else (n + 40) * U  # noqa: E731
+    zerr = ((D / 16 + 1) * 2.0 ** -22 * S.max(-1) if half else (D + 1) * U * S.max(-1)) + 2.0 ** -18 * (1 + np.abs(rs))
+    zerr = zerr * live
     near("loss", loss, rl, 2 * zerr)
     near("lse", lse, rs, 2 * zerr)
     rh, rW, rb = ends.vocab_loss_backward(h0, W0, tl, d0, None if b is None else b.double().numpy())
@@ -272,9 +276,9 @@ def loss_check(N, V, D, seed, index=torch.int64, **kw):
     hot[np.nonzero(live)[0], t.numpy()[live]] = 1
     g = np.abs(p - hot) * np.abs(d0)[:, None]            # the entries' sizes
     gerr = np.abs(d0)[:, None] * (p + hot) * 4 * zerr[:, None]   # what the logits and 1 - exp(-loss) leave
-    off = g * (1 - hot) * 2.0 ** -8                       # G's rounding
-    near("dh", dh, rh, (off + gerr) @ np.abs(W0) + (V / 16 + 40) * 2.0 ** -22 * (g @ np.abs(W0)))
-    near("dW", dW, rW, (off + gerr + g * 2.0 ** -8).T @ np.abs(h0) + (N / 16 + 40) * 2.0 ** -22 * (g.T @ np.abs(h0)))
+    off = g * (1 - hot) * half                            # G's rounding
+    near("dh", dh, rh, (off + gerr) @ np.abs(W0) + steps(V) * (g @ np.abs(W0)))
+    near("dW", dW, rW, (off + gerr + g * half).T @ np.abs(h0) + steps(N) * (g.T @ np.abs(h0)))
     if b is not None:
         near("dbias", db, rb, gerr.sum(0) + (N / 32 + 40) * U * g.sum(0))
     else:
@@ -287,27 +291,31 @@ def loss_check(N, V, D, seed, index=torch.int64, **kw):
                                      (100, 257, 64), (127, 65, 512), (128, 128, 1024), (129, 129, 136), (256, 300, 256),
                                      (257, 511, 264), (300, 1025, 40), (520, 65, 512), (700, 770, 2048)], ids=str)
 @pytest.mark.parametrize("bias", [False, True])
-def test_vocab_loss(N, V, D, bias):
-    loss_check(N, V, D, N + V + D, bias=bias)
+@BOTH
+def test_vocab_loss(N, V, D, bias, dtype):
+    loss_check(N, V, D, N + V + D, bias=bias, dtype=dtype)
 
 
 @pytest.mark.parametrize("N, V, D", [(4, 9, 24), (130, 300, 64), (600, 70, 512)], ids=str)
 @pytest.mark.parametrize("bias", [False, True])
 @pytest.mark.parametrize("index", [torch.int32, torch.int64], ids=["i32", "i64"])
-def test_vocab_loss_padded(N, V, D, bias, index):
+@BOTH
+def test_vocab_loss_padded(N, V, D, bias, index, dtype):
     """Padding's rows hold NaN: they reach nothing."""
-    loss_check(N, V, D, N, index=index, bias=bias, padded=True, weights=True)
+    loss_check(N, V, D, N, index=index, bias=bias, padded=True, weights=True, dtype=dtype)
 
 
 @pytest.mark.parametrize("known", [0.0, 40.0])
-def test_vocab_loss_confident(known):
+@BOTH
+def test_vocab_loss_confident(known, dtype):
     """Tokens that nothing, and that everything, is known about."""
-    loss_check(200, 500, 128, 7, known=known, bias=True)
+    loss_check(200, 500, 128, 7, known=known, bias=True, dtype=dtype)
 
 
-def test_vocab_loss_masked_entries():
+@BOTH
+def test_vocab_loss_masked_entries(dtype):
     """A bias of -infinity takes entries out, whole tiles of them; a target among them costs infinity."""
-    h, W, t, b, dl = loss_inputs(70, 900, 64, 8, bias=True)
+    h, W, t, b, dl = loss_inputs(70, 900, 64, 8, bias=True, dtype=dtype)
     b[100:700] = -float("inf")
     t[:] = 3
     t[5] = 200
@@ -328,8 +336,9 @@ def test_vocab_loss_masked_entries():
     assert torch.isnan(loss).all()
 
 
-def test_vocab_loss_past_the_vocabulary():
-    h, W, t, _, dl = loss_inputs(40, 50, 32, 9)
+@BOTH
+def test_vocab_loss_past_the_vocabulary(dtype):
+    h, W, t, _, dl = loss_inputs(40, 50, 32, 9, dtype=dtype)
     good = fw.fw_vocab_loss(h.cuda(), W.cuda(), t.cuda())[0]
     bad = t.clone()
     bad[7], bad[8] = 50, 2 ** 40
@@ -343,15 +352,16 @@ def test_vocab_loss_past_the_vocabulary():
     assert torch.equal(dh, dh2) and torch.equal(dW, dW2)
 
 
-def test_vocab_loss_parts_and_repeats():
+@BOTH
+def test_vocab_loss_parts_and_repeats(dtype):
     """Each gradient alone has the bits of all together, and every run the same."""
-    h, W, t, b, dl = (None if x is None else x.cuda() for x in loss_inputs(300, 700, 256, 10, bias=True))
+    h, W, t, b, dl = (None if x is None else x.cuda() for x in loss_inputs(300, 700, 256, 10, bias=True, dtype=dtype))
     loss, lse = fw.fw_vocab_loss(h, W, t, bias=b)
     dh, dW, db = fw.fw_vocab_loss_backward(h, W, t, loss, lse, dl, bias=b)
     assert torch.equal(fw.fw_vocab_loss_backward(h, W, t, loss, lse, dl, bias=b, return_dW=False)[0], dh)
     got = fw.fw_vocab_loss_backward(h, W, t, loss, lse, dl, bias=b, return_dh=False)
     assert got[0] is None and torch.equal(got[1], dW) and torch.equal(got[2], db)
-    ws = torch.empty(fw.fw_vocab_loss_backward_workspace_size(300, 700, 256), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(fw.fw_vocab_loss_backward_workspace_size(300, 700, 256, dtype), dtype=torch.uint8, device="cuda")
     for fill in (0, 255):
         ws.fill_(fill)
         again = fw.fw_vocab_loss_backward(h, W, t, loss, lse, dl, bias=b, workspace=ws)
@@ -383,21 +393,24 @@ def plain_loss(h, W, t, dl, b=None):
     return loss, lse, g @ W.double(), g.T @ h.double(), g.sum(0)
 
 
-@pytest.mark.parametrize("N, V, D", [(2500, 9001, 520), (70, 33000, 64), (20000, 300, 128), (33, 20011, 1024)], ids=str)
-def test_vocab_loss_many_tiles(N, V, D):
-    """More tiles than pairs of SMs, long contractions, splits of them: errors in the 2-norm.  An output's own rounding
-    leaves at most 2^-8 of it, G's and w h's as much each, the sums' steps less: 2^-6."""
-    h, W, t, b, dl = (None if x is None else x.cuda() for x in loss_inputs(N, V, D, N, bias=True))
+@pytest.mark.parametrize("N, V, D", [(2500, 9001, 520), (70, 33000, 64), (20000, 300, 128), (33, 20011, 1024), (9000, 60001, 64)], ids=str)
+@BOTH
+def test_vocab_loss_many_tiles(N, V, D, dtype):
+    """More tiles than pairs of SMs, long contractions, splits of them, pieces of the vocabulary: errors in the 2-norm.  bf16: an output's own
+    rounding leaves at most 2^-8 of it, G's and w h's as much each, the sums' steps less: 2^-6.  fp32: p is off by the
+    logits' error, at most 1e-5 here, and a sum of n terms by sqrt(n) u to n u of their sizes, n <= 60 000: 1e-4."""
+    tol = 2.0 ** -6 if dtype == torch.bfloat16 else 1e-4
+    h, W, t, b, dl = (None if x is None else x.cuda() for x in loss_inputs(N, V, D, N, bias=True, dtype=dtype))
     loss, lse = fw.fw_vocab_loss(h, W, t, bias=b)
     got = fw.fw_vocab_loss_backward(h, W, t, loss, lse, dl, bias=b)
     want = plain_loss(h, W, t, dl, b)
     rel = lambda a, w: float((a.double() - w).norm() / w.norm())  # noqa: E731
     assert rel(loss, want[0]) < 1e-5 and rel(lse, want[1]) < 1e-5
-    assert rel(got[0], want[2]) < 2.0 ** -6 and rel(got[1], want[3]) < 2.0 ** -6 and rel(got[2], want[4]) < 1e-4
+    assert rel(got[0], want[2]) < tol and rel(got[1], want[3]) < tol and rel(got[2], want[4]) < 1e-4
     # no tile is off by itself
     for x, w in ((got[0], want[2]), (got[1], want[3])):
         for i in range(0, len(w), 128):
-            assert rel(x[i:i + 128], w[i:i + 128]) < 2.0 ** -5, i
+            assert rel(x[i:i + 128], w[i:i + 128]) < 2 * tol, i
 
 
 def test_graphs_and_streams():
@@ -619,10 +632,10 @@ def test_refused():
         fw.fw_embedding_backward(ids[:3], x, 9)
     h, W = x.bfloat16(), n(9, 32).bfloat16().cuda()
     f = n(4).cuda()
-    for bad in (dict(h=x), dict(W=W.float()), dict(targets=ids.float())):
+    for bad in (dict(h=h.half(), W=W.half()), dict(targets=ids.float())):
         with pytest.raises(TypeError):
             fw.fw_vocab_loss(**{"h": h, "W": W, "targets": ids, **bad})
-    for bad in (dict(targets=ids[:3]), dict(bias=f), dict(bias=n(9).bfloat16().cuda()), dict(loss=f.double()), dict(W=W.t())):
+    for bad in (dict(h=x), dict(W=W.float()), dict(targets=ids[:3]), dict(bias=f), dict(bias=n(9).bfloat16().cuda()), dict(loss=f.double()), dict(W=W.t())):
         with pytest.raises(ValueError):
             fw.fw_vocab_loss(**{"h": h, "W": W, "targets": ids, **bad})
     with pytest.raises(ValueError):
