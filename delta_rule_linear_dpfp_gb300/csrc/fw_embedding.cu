@@ -13,7 +13,7 @@
 //  1. One cluster of eight CTAs sorts the pairs (id, n) by id, eight bits at
 //     a time from the lowest, each pass stable.  A CTA owns an eighth of the
 //     sequence; the counts of the digits are exchanged through distributed
-//     shared memory; a warp owns 32 to 128 pairs in a row and ranks equal digits
+//     shared memory; a warp owns 32 to 256 pairs in a row and ranks equal digits
 //     by a match among its lanes.  The sort is all latency and takes eight SMs:
 //     the others write the table's zeros meanwhile.
 //  2. A group of threads sums 32 sorted pairs (8 or 16 where there are few), run by run:
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kT, sizeof(T) == 2 ? 6 : 4)
 }
 
 // -------------------------------------------------------------------- sort
-constexpr int kCluster = 8, kSortT = 1024, kWarps = kSortT / 32, kPerLane = 4, kTile = kSortT * kPerLane;
+constexpr int kCluster = 8, kSortT = 1024, kWarps = kSortT / 32, kPerLane = 8, kTile = kSortT * kPerLane;
 
 FW_DEV void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -113,7 +113,7 @@ FW_DEV unsigned peer_load(const unsigned *p, unsigned rank) {
 struct SortArgs {
     Tokens ids;
     int N, V, passes;
-    int *key[2], *pos[2]; // the pairs, from one to the other and back
+    int2 *pair[2]; // (key, position), from one to the other and back
     uint4 *zeros;         // what the CTAs past the first cluster fill, or null
     int64_t nzeros;
 };
@@ -145,13 +145,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortT) sort_
 
     for (int pass = 0; pass < a.passes; ++pass) {
         const int shift = 8 * pass;
-        const int *key_in = pass & 1 ? a.key[1] : a.key[0], *pos_in = pass & 1 ? a.pos[1] : a.pos[0];
-        int *key_out = pass & 1 ? a.key[0] : a.key[1], *pos_out = pass & 1 ? a.pos[0] : a.pos[1];
-        auto key_at = [&](int64_t i) {
+        const int2 *in = pass & 1 ? a.pair[1] : a.pair[0];
+        int2 *out = pass & 1 ? a.pair[0] : a.pair[1];
+        auto pair_at = [&](int64_t i) {
             if (pass)
-                return __ldcg(key_in + i);
+                return __ldcg(in + i);
             const int t = token_at(a.ids, i, a.V);
-            return t < 0 ? a.V : t; // padding behind every row
+            return make_int2(t < 0 ? a.V : t, (int)i); // padding behind every row
         };
         int key[kPerLane], pos[kPerLane];
         unsigned at[kPerLane]; // rank among the warp's pairs with this digit
@@ -163,8 +163,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortT) sort_
             for (int u = 0; u < kPerLane; ++u) {
                 const int64_t i = w0 + 32 * u;
                 const bool live = u < per && i < hi;
-                key[u] = live ? key_at(i) : 0;
-                pos[u] = live ? (pass ? __ldcg(pos_in + i) : (int)i) : 0;
+                const int2 p = live ? pair_at(i) : make_int2(0, 0);
+                key[u] = p.x;
+                pos[u] = p.y;
             }
             for (int e = lane; e < 256; e += 32)
                 rows[warp][e] = 0;
@@ -199,8 +200,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortT) sort_
                 if (u < per && w0 + 32 * u < hi) {
                     const unsigned d = (unsigned)key[u] >> shift & 255u;
                     const unsigned o = rows[warp][d] + at[u] + (add ? offset[d] : 0u);
-                    key_out[o] = key[u];
-                    pos_out[o] = pos[u];
+                    out[o] = make_int2(key[u], pos[u]);
                 }
         };
         if (one) {
@@ -213,7 +213,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortT) sort_
             __syncthreads();
             for (int64_t i0 = lo; i0 < hi; i0 += kSortT) {
                 const int64_t i = i0 + tid;
-                const unsigned live = i < hi, digit = live ? (unsigned)key_at(i) >> shift & 255u : 0u;
+                const unsigned live = i < hi, digit = live ? (unsigned)pair_at(i).x >> shift & 255u : 0u;
                 const unsigned same = peers(digit, live);
                 if (live && lane == __ffs(same) - 1)
                     atomicAdd(hist + digit, __popc(same));
@@ -264,7 +264,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortT) sort_
 template <typename T> constexpr int kFlight = sizeof(T) == 2 ? 8 : 4;
 
 struct SumArgs {
-    const int *key, *pos; // sorted
+    const int2 *pair;     // sorted
     float *part;          // [chunks][2][D]: of the run that comes in, of the one that goes on
     int N, V, D, lg, lgc; // 2^lg threads a group, 2^lgc pairs a chunk
     float scale;
@@ -285,8 +285,7 @@ template <typename T>
 __global__ void __launch_bounds__(kT, 3) chunk_sums_kernel(SumArgs a, const T *dout, T *dtable) {
     griddep_launch_dependents();
     griddep_wait();
-    a.key = after_wait(a.key);
-    a.pos = after_wait(a.pos);
+    a.pair = after_wait(a.pair);
     dout = after_wait(dout);
     const int t = threadIdx.x & ((1 << a.lg) - 1), lane = threadIdx.x & 31;
     const int64_t k = (int64_t)blockIdx.x * (kT >> a.lg) + (threadIdx.x >> a.lg), i0 = k << a.lgc;
@@ -294,9 +293,10 @@ __global__ void __launch_bounds__(kT, 3) chunk_sums_kernel(SumArgs a, const T *d
     if (count <= 0)
         return;
     // a lane holds a pair; what comes before and behind
-    const int key = lane < count ? __ldcg(a.key + i0 + lane) : -1, pos = lane < count ? __ldcg(a.pos + i0 + lane) : 0;
-    const int left = i0 > 0 ? __ldcg(a.key + i0 - 1) : -1;
-    const int right = i0 + count < a.N ? __ldcg(a.key + i0 + count) : -1;
+    const int2 own = lane < count ? __ldcg(a.pair + i0 + lane) : make_int2(-1, 0);
+    const int key = own.x, pos = own.y;
+    const int left = i0 > 0 ? __ldcg(a.pair + i0 - 1).x : -1;
+    const int right = i0 + count < a.N ? __ldcg(a.pair + i0 + count).x : -1;
     for (int c = 8 * t; c - 8 * t < a.D; c += 8 << a.lg) {
         const bool on = c < a.D;
         float s[8] = {};
@@ -344,19 +344,21 @@ __global__ void __launch_bounds__(kT) join_runs_kernel(SumArgs a, T *dtable) {
     __shared__ float red[kT * 8];
     griddep_launch_dependents();
     griddep_wait();
-    a.key = after_wait(a.key);
+    a.pair = after_wait(a.pair);
     a.part = after_wait(a.part);
     const int64_t k = blockIdx.x, i0 = k << a.lgc, size = (int64_t)1 << a.lgc;
     if (i0 + size >= a.N)
         return;
-    const int id = __ldcg(a.key + i0 + size - 1);
-    if (id >= a.V || __ldcg(a.key + i0 + size) != id || (__ldcg(a.key + i0) == id && i0 > 0 && __ldcg(a.key + i0 - 1) == id))
+    // (all four requested at once)
+    const int id = __ldcg(a.pair + i0 + size - 1).x, next = __ldcg(a.pair + i0 + size).x, first = __ldcg(a.pair + i0).x;
+    const int before = i0 > 0 ? __ldcg(a.pair + i0 - 1).x : -1;
+    if (id >= a.V || next != id || (first == id && before == id))
         return;
     // the chunks after this one that the run comes into: their first pair has its id
     int64_t end = k + 1;
     for (bool more = true; more;) {
         const int64_t i = (end + (threadIdx.x & 31)) << a.lgc;
-        const unsigned in = __ballot_sync(0xffffffffu, i < a.N && __ldcg(a.key + i) == id);
+        const unsigned in = __ballot_sync(0xffffffffu, i < a.N && __ldcg(a.pair + i).x == id);
         const int n = in == 0xffffffffu ? 32 : __ffs(~in) - 1;
         end += n;
         more = n == 32;
@@ -431,10 +433,10 @@ cudaError_t launch_embedding(Tokens ids, const void *table, void *out, int64_t N
                 : lookup<float>(ids, table, out, N, V, D, scale, st);
 }
 
-// keys and positions twice, two sums of each chunk
+// the pairs twice, two sums of each chunk
 size_t embedding_backward_workspace_bytes(int N, int V, int D) {
     (void)V;
-    return 4 * up256(4 * (size_t)N) + 8 * (size_t)chunks_of(N) * D;
+    return 2 * up256(8 * (size_t)N) + 8 * (size_t)chunks_of(N) * D;
 }
 
 cudaError_t launch_embedding_backward(Tokens ids, const void *dout, void *dtable, void *workspace, int N, int V, int D,
@@ -446,9 +448,9 @@ cudaError_t launch_embedding_backward(Tokens ids, const void *dout, void *dtable
     while (a.passes < 4 && ((unsigned)V >> (8 * a.passes)) != 0) // keys are 0 .. V
         ++a.passes;
     uint8_t *p = static_cast<uint8_t *>(workspace);
-    for (int **to : {&a.key[0], &a.key[1], &a.pos[0], &a.pos[1]}) {
-        *to = reinterpret_cast<int *>(p);
-        p += up256(4 * (size_t)N);
+    for (int i = 0; i < 2; ++i) {
+        a.pair[i] = reinterpret_cast<int2 *>(p);
+        p += up256(8 * (size_t)N);
     }
     // the table's zeros: 64 KB at least a CTA, whole clusters, two CTAs an SM at most
     const int64_t vecs = accumulate ? 0 : (int64_t)V * D / (bf16 ? 8 : 4);
@@ -459,8 +461,8 @@ cudaError_t launch_embedding_backward(Tokens ids, const void *dout, void *dtable
     if (e != cudaSuccess)
         return e;
     const int lg = std::max(5, group_log2(D)); // (whole warps)
-    const SumArgs s = {a.passes & 1 ? a.key[1] : a.key[0], a.passes & 1 ? a.pos[1] : a.pos[0], reinterpret_cast<float *>(p),
-                       N, V, D, lg, chunk_log2(N), scale, accumulate};
+    const SumArgs s = {a.passes & 1 ? a.pair[1] : a.pair[0], reinterpret_cast<float *>(p), N, V, D, lg, chunk_log2(N),
+                       scale, accumulate};
     return bf16 ? sums<__nv_bfloat16>(s, dout, dtable, st) : sums<float>(s, dout, dtable, st);
 }
 
