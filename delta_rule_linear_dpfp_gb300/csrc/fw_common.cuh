@@ -102,13 +102,15 @@ template <class T> FW_DEV T *after_wait(T *p) {
 // latency is hidden behind its tail.  Every kernel launched this way calls
 // griddep_wait before its first global access.  Because each kernel lets its
 // successor launch early, a kernel may start while kernels two or more places
-// before it still run: a load before griddep_wait would race with them.  Two
+// before it still run: a load before griddep_wait would race with them.  Three
 // kernels go without it, and are safe because their predecessor lets them
 // start only after its own wait, when everything before it is complete: the
-// forward's scan reads W0, and the gated rule's preparation of a segment
+// forward's scan reads W0; the gated rule's preparation of a segment
 // beside the walk over the one before reads the call's inputs and writes
 // records that no earlier kernel of the call touches (its last CTA waits at
-// its end, so that what follows waits for that walk, too).
+// its end, so that what follows waits for that walk, too); and the embedding
+// gradient's zeros are written beside the sort, which does not touch the table
+// (every CTA waits at its end, for the same reason).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg = {};

@@ -15,7 +15,7 @@
 //     sequence; the counts of the digits are exchanged through distributed
 //     shared memory; a warp owns 32 to 256 pairs in a row and ranks equal digits
 //     by a match among its lanes.  The sort is all latency and takes eight SMs:
-//     the others write the table's zeros meanwhile.
+//     another kernel writes the table's zeros on the others meanwhile.
 //  2. A group of threads sums 32 sorted pairs (8 or 16 where there are few), run by run:
 //     a run that ends on both sides is rounded and written, one that goes on
 //     beyond leaves its sum in 32 bits.  Every group reads as many rows as any
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kT, sizeof(T) == 2 ? 6 : 4)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     o[e] = id[u] < V ? o[e] * scale : __int_as_float(0x7fffffff);
-                store8(out + (n0 + u) * D + c, o);
+                store8_stream(out + (n0 + u) * D + c, o);
             }
     }
 }
@@ -114,7 +114,7 @@ struct SortArgs {
     Tokens ids;
     int N, V, passes;
     int2 *pair[2]; // (key, position), from one to the other and back
-    uint4 *zeros;         // what the CTAs past the first cluster fill, or null
+    uint4 *zeros;         // a small table, cleared here
     int64_t nzeros;
 };
 
@@ -125,15 +125,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortT) sort_
     __shared__ unsigned hist[256], offset[256], rows[kWarps][256];
     __shared__ unsigned scan[8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    griddep_launch_dependents();
+    // (in this order: what starts beside this kernel does so when everything before it is complete)
     griddep_wait();
-    if (blockIdx.x >= kCluster) { // (whole clusters: no barrier of theirs is left out)
-        const int64_t step = (int64_t)(gridDim.x - kCluster) * kSortT;
-        for (int64_t i = (int64_t)(blockIdx.x - kCluster) * kSortT + tid; i < a.nzeros; i += step)
-            a.zeros[i] = make_uint4(0, 0, 0, 0);
-        return;
-    }
+    griddep_launch_dependents();
     const unsigned rank = blockIdx.x;
+    for (int64_t i = (int64_t)rank * kSortT + tid; i < a.nzeros; i += kCluster * kSortT)
+        a.zeros[i] = make_uint4(0, 0, 0, 0);
     a.ids.p = after_wait(a.ids.p);
     // this CTA's part of the sequence: a multiple of 32 pairs, or of a tile where it does not fit one
     int64_t part = (((int64_t)a.N + kCluster - 1) / kCluster + 31) / 32 * 32;
@@ -257,6 +254,22 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortT) sort_
         }
         cluster_sync(); // the pairs stand, for every CTA; its counts are read
     }
+}
+
+// A large table's zeros, beside the sort: no wait at the start (the sort lets this kernel
+// start only after its own), and one at the end, so that what follows this kernel follows
+// the sort as well.
+__global__ void __launch_bounds__(kT) zero_table_kernel(uint4 *zeros, int64_t n) {
+    griddep_launch_dependents();
+    const int64_t step = (int64_t)gridDim.x * kT;
+    int64_t i = (int64_t)blockIdx.x * kT + threadIdx.x;
+    for (; i + 3 * step < n; i += 4 * step)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            __stcs(zeros + i + u * step, make_uint4(0, 0, 0, 0));
+    for (; i < n; i += step)
+        __stcs(zeros + i, make_uint4(0, 0, 0, 0));
+    griddep_wait();
 }
 
 // -------------------------------------------------------------------- sums
@@ -452,12 +465,15 @@ cudaError_t launch_embedding_backward(Tokens ids, const void *dout, void *dtable
         a.pair[i] = reinterpret_cast<int2 *>(p);
         p += up256(8 * (size_t)N);
     }
-    // the table's zeros: 64 KB at least a CTA, whole clusters, two CTAs an SM at most
-    const int64_t vecs = accumulate ? 0 : (int64_t)V * D / (bf16 ? 8 : 4);
-    a.zeros = static_cast<uint4 *>(dtable);
-    a.nzeros = vecs;
-    const int64_t more = std::min<int64_t>((vecs + 8 * 4096 - 1) / (8 * 4096), 2 * 152 / kCluster - 1);
-    cudaError_t e = launch_pdl(sort_tokens_kernel, dim3((unsigned)(kCluster * (1 + more))), dim3(kSortT), 0, st, a);
+    // the table's zeros: within the sort, or from a megabyte on beside it
+    uint4 *zeros = static_cast<uint4 *>(dtable);
+    const int64_t nzeros = accumulate ? 0 : (int64_t)V * D / (bf16 ? 8 : 4);
+    const bool beside = nzeros > 1 << 16;
+    a.zeros = zeros;
+    a.nzeros = beside ? 0 : nzeros;
+    cudaError_t e = launch_pdl(sort_tokens_kernel, dim3(kCluster), dim3(kSortT), 0, st, a);
+    if (e == cudaSuccess && beside)
+        e = launch_pdl(zero_table_kernel, dim3(152 * 3), dim3(kT), 0, st, zeros, nzeros);
     if (e != cudaSuccess)
         return e;
     const int lg = std::max(5, group_log2(D)); // (whole warps)

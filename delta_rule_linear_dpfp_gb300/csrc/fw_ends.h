@@ -4,6 +4,9 @@
 // fw_ends_api.cu.
 #pragma once
 #include <cuda_runtime.h>
+#ifdef __CUDACC__
+#include "fw_common.cuh"
+#endif
 #include <stddef.h>
 #include <stdint.h>
 
@@ -18,6 +21,16 @@ struct Tokens {
     int wide;
 };
 #ifdef __CUDACC__
+// store8 for what is written once and not read by the same call: it is the first to leave L2.
+__device__ __forceinline__ void store8_stream(float *p, const float (&v)[8]) {
+    __stcs(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
+    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
+}
+__device__ __forceinline__ void store8_stream(__nv_bfloat16 *p, const float (&v)[8]) {
+    __stcs(reinterpret_cast<uint4 *>(p), make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                    pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+}
+
 // Token i within [0, V), -1 for any negative one, V for any past the end.
 __device__ __forceinline__ int token_at(const Tokens &t, int64_t i, int V) {
     const int64_t x = t.wide ? __ldcg(static_cast<const long long *>(t.p) + i) : __ldcg(static_cast<const int *>(t.p) + i);

@@ -59,15 +59,23 @@ template <> struct Raw<float> {
         o[3] = pack(b.z, b.w);
     }
 };
-template <typename T> FW_DEV void store_pairs(T *p, const F2 (&v)[4]) {
-    float o[8];
+FW_DEV void singles(const F2 (&v)[4], float (&o)[8]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float2 t = unpack(v[e]);
         o[2 * e] = t.x;
         o[2 * e + 1] = t.y;
     }
+}
+FW_DEV void store_pairs(float *p, const F2 (&v)[4]) { // (shared or global)
+    float o[8];
+    singles(v, o);
     store8(p, o);
+}
+template <typename T> FW_DEV void stream_pairs(T *p, const F2 (&v)[4]) { // (global)
+    float o[8];
+    singles(v, o);
+    store8_stream(p, o);
 }
 FW_DEV void param_pairs(const float *p, int c, bool on, float missing, F2 (&o)[4]) {
     float t[8];
@@ -177,7 +185,7 @@ __global__ void __launch_bounds__(G > 32 ? G : kT, an_sm<G>(false))
             for (int e = 0; e < 4; ++e)
                 s[e] = s[e] + t[e];
             if (mine)
-                store_pairs(sum_out + at * d + row.c, s);
+                stream_pairs(sum_out + at * d + row.c, s);
         }
         w.at += w.step;
         request(w.at);
@@ -197,7 +205,7 @@ __global__ void __launch_bounds__(G > 32 ? G : kT, an_sm<G>(false))
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 s[e] = fma2((G > 32 ? s[e] + sh : s[e]) * r, ga[e], be[e]);
-            store_pairs(out + at * d + row.c, s);
+            stream_pairs(out + at * d + row.c, s);
         }
     }
 }
@@ -297,7 +305,7 @@ __global__ void __launch_bounds__(G > 32 ? G : kT, an_sm<G>(true))
                 dn[u][e] = RES ? g + more[u][e] : g;
             }
             if (mine)
-                store_pairs(dx + r0 * d + row.c, dn[u]);
+                stream_pairs(dx + r0 * d + row.c, dn[u]);
         }
     }
     if (!partial)
