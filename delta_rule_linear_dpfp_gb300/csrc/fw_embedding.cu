@@ -16,7 +16,7 @@
 //     shared memory; a warp owns 32 to 256 pairs in a row and ranks equal digits
 //     by a match among its lanes.  The sort is all latency and takes eight SMs:
 //     another kernel writes the table's zeros on the others meanwhile.
-//  2. A group of threads sums 32 sorted pairs (8 or 16 where there are few), run by run:
+//  2. A group of threads sums 32 sorted pairs (8 where there are few), run by run:
 //     a run that ends on both sides is rounded and written, one that goes on
 //     beyond leaves its sum in 32 bits.  Every group reads as many rows as any
 //     other, whatever a token's share of the batch is.
@@ -305,37 +305,39 @@ __global__ void __launch_bounds__(kT, 3) chunk_sums_kernel(SumArgs a, const T *d
     const int count = (int)min((int64_t)1 << a.lgc, a.N - i0); // (groups are whole warps)
     if (count <= 0)
         return;
-    // a lane holds a pair; what comes before and behind
+    // a lane holds a pair; `n` of them have a row, `ends` are the last of their run here
     const int2 own = lane < count ? __ldcg(a.pair + i0 + lane) : make_int2(-1, 0);
     const int key = own.x, pos = own.y;
     const int left = i0 > 0 ? __ldcg(a.pair + i0 - 1).x : -1;
     const int right = i0 + count < a.N ? __ldcg(a.pair + i0 + count).x : -1;
+    const int next = __shfl_down_sync(0xffffffffu, key, 1);
+    const bool last = lane == count - 1;
+    const int n = __popc(__ballot_sync(0xffffffffu, lane < count && key < a.V)); // (padding is sorted behind)
+    const unsigned ends = __ballot_sync(0xffffffffu, lane < n && (last || key != next));
+    const bool first_comes_in = __shfl_sync(0xffffffffu, key, 0) == left;
+    const int goes_on = __shfl_sync(0xffffffffu, key, count - 1) == right ? count - 1 : -1; // the pair whose run does
     for (int c = 8 * t; c - 8 * t < a.D; c += 8 << a.lg) {
         const bool on = c < a.D;
         float s[8] = {};
-        bool comes_in = __shfl_sync(0xffffffffu, key, 0) == left;
-        for (int j0 = 0; j0 < count; j0 += kFlight<T>) {
+        bool comes_in = first_comes_in;
+        for (int j0 = 0; j0 < n; j0 += kFlight<T>) {
             Raw<T> v[kFlight<T>];
 #pragma unroll
             for (int u = 0; u < kFlight<T>; ++u) {
-                const int p = __shfl_sync(0xffffffffu, pos, j0 + u), id = __shfl_sync(0xffffffffu, key, j0 + u);
-                if (on && id >= 0 && id < a.V)
+                const int p = __shfl_sync(0xffffffffu, pos, j0 + u);
+                if (on && j0 + u < n)
                     v[u].load(dout + (int64_t)p * a.D + c);
             }
 #pragma unroll
             for (int u = 0; u < kFlight<T>; ++u) {
                 const int j = j0 + u;
-                if (j >= count)
-                    break;
-                const int id = __shfl_sync(0xffffffffu, key, j);
-                const int next = j + 1 < count ? __shfl_sync(0xffffffffu, key, (j + 1) & 31) : right;
-                if (id >= a.V) // padding: nothing behind it either
+                if (j >= n)
                     break;
                 v[u].add_to(s);
-                const bool last = j + 1 == count, goes_on = last && next == id;
-                if (next != id || last) {
+                if (ends >> j & 1) {
+                    const int id = __shfl_sync(0xffffffffu, key, j);
                     if (on) {
-                        if (comes_in || goes_on)
+                        if (comes_in || j == goes_on)
                             store8(a.part + (2 * k + (comes_in ? 0 : 1)) * a.D + c, s);
                         else
                             write_row(a, dtable + (int64_t)id * a.D + c, s);
@@ -424,8 +426,9 @@ cudaError_t lookup(Tokens ids, const void *table, void *out, int64_t N, int V, i
                       (T *)out, N, V, D, lg, scale);
 }
 
-// Pairs of a chunk: fewer where the chunks are too few to occupy the SMs otherwise.
-int chunk_log2(int N) { return N <= 8192 ? 3 : N <= 32768 ? 4 : 5; }
+// Pairs of a chunk: fewer where the chunks are too few to occupy the SMs otherwise
+// (16384 x 1024: 31.9 us with 32, 32.6 with 16, 36.6 with 8, whose open runs leave more sums).
+int chunk_log2(int N) { return N <= 8192 ? 3 : 5; }
 int64_t chunks_of(int N) { return ((int64_t)N + (1 << chunk_log2(N)) - 1) >> chunk_log2(N); }
 
 template <typename T>

@@ -594,7 +594,7 @@ typedef enum fw_index {
 FW_API int fw_embedding(const void *ids, const void *table, void *out, int64_t N, int V, int D, float scale,
                         int index_type, int io_dtype, void *stream);
 
-/* 16 N bytes, and 8 D for every 8 (up to 8192 tokens), 16 (up to 32768) or 32 tokens. */
+/* 16 N bytes, and 8 D for every 8 tokens (N up to 8192) or 32. */
 FW_API size_t fw_embedding_backward_workspace_size(int64_t N, int V, int D);
 
 /*
