@@ -14,7 +14,7 @@
 //     a time from the lowest, each pass stable.  A CTA owns an eighth of the
 //     sequence; the counts of the digits are exchanged through distributed
 //     shared memory; a warp owns 32 to 256 pairs in a row and ranks equal digits
-//     by a match among its lanes.  The sort is all latency and takes eight SMs:
+//     by its lanes' votes on the digits' bits.  The sort is all latency and takes eight SMs:
 //     another kernel writes the table's zeros on the others meanwhile.
 //  2. A group of threads sums 32 sorted pairs (8 where there are few), run by run:
 //     a run that ends on both sides is rounded and written, one that goes on
@@ -118,8 +118,17 @@ struct SortArgs {
     int64_t nzeros;
 };
 
-// The lanes of the warp that hold this lane's digit (among `live` lanes).
-FW_DEV unsigned peers(unsigned digit, unsigned live) { return __match_any_sync(0xffffffffu, digit | (live << 8)); }
+// The live lanes of the warp that hold this lane's digit, by the votes on its eight bits.
+FW_DEV unsigned peers(unsigned digit, unsigned live) {
+    unsigned same = __ballot_sync(0xffffffffu, live);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+        const bool one = digit >> b & 1;
+        const unsigned votes = __ballot_sync(0xffffffffu, one);
+        same &= one ? votes : ~votes;
+    }
+    return same;
+}
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortT) sort_tokens_kernel(SortArgs a) {
     __shared__ unsigned hist[256], offset[256], rows[kWarps][256];
