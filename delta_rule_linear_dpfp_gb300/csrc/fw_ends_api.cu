@@ -57,7 +57,7 @@ FW_API int fw_embedding(const void *ids, const void *table, void *out, int64_t N
         return FW_ERR_UNSUPPORTED;
     if (N == 0)
         return FW_OK;
-    if (!tokens_ok(ids, index_type) || !usable(table) || !usable(out))
+    if (!tokens_ok(ids, index_type) || !usable(table) || !usable(out) || out == table)
         return FW_ERR_INVALID_ARG;
     return cuda_status(fw::launch_embedding({ids, index_type}, table, out, N, V, D, scale, io_dtype == FW_DTYPE_BF16,
                                             static_cast<cudaStream_t>(stream)));
@@ -102,7 +102,7 @@ FW_API int fw_layer_norm(const void *x, const void *residual, const float *gamma
     if (rows == 0)
         return FW_OK;
     if (!usable(x) || !usable(out) || !aligned16(residual) || !aligned16(gamma) || !aligned16(beta) || !aligned16(sum) ||
-        !residual != !sum)
+        !residual != !sum || out == sum)
         return FW_ERR_INVALID_ARG;
     return cuda_status(fw::launch_layer_norm(x, residual, gamma, beta, out, sum, rows, d, eps, io_dtype == FW_DTYPE_BF16,
                                              static_cast<cudaStream_t>(stream)));
@@ -176,7 +176,7 @@ FW_API int fw_vocab_loss_backward(const void *h, const void *W, const float *bia
     const int rc = check_loss(N, V, D, io_dtype);
     if (rc != FW_OK)
         return rc;
-    if (!aligned16(dh) || !aligned16(dW) || !aligned16(dbias))
+    if (!aligned16(dh) || !aligned16(dW) || !aligned16(dbias) || (dh && dh == h) || (dW && dW == W))
         return FW_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (N == 0) { // no token: gradients of zero

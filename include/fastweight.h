@@ -616,7 +616,8 @@ FW_API int fw_embedding_backward(const void *ids, const void *dout, void *dtable
  *   x, residual, out, sum : [rows, d]  io_dtype; residual may be NULL, and sum
  *                           (s, rounded) is written exactly when it is not
  *   gamma, beta           : [d] fp32, or NULL (one / zero)
- * out may be x, and sum may be x or residual (in place).
+ * out may be x or residual, and sum may be the other of them or residual (in
+ * place); out and sum are two tensors.
  */
 FW_API int fw_layer_norm(const void *x, const void *residual, const float *gamma, const float *beta, void *out,
                          void *sum, int64_t rows, int d, float eps, int io_dtype, void *stream);
@@ -647,7 +648,8 @@ FW_API size_t fw_vocab_loss_workspace_size(int N, int V, int D, int io_dtype);
  *   h       : [N, D]  io_dtype
  *   W       : [V, D]  io_dtype (an embedding's table, for one)
  *   bias    : [V]     fp32, or NULL; -infinity takes an entry out of the
- *             vocabulary (its gradient is zero)
+ *             vocabulary (its gradient is zero; its row of W is finite, as
+ *             any other)
  *   targets : [N]     fw_index
  *   loss, lse : [N]   fp32     (written)
  * bf16: products summed in fp32 on the tensor cores, by 512 channels (up to four
@@ -672,7 +674,7 @@ FW_API size_t fw_vocab_loss_backward_workspace_size(int N, int V, int D, int io_
  *   loss, lse : [N] fp32, as fw_vocab_loss wrote them for the same inputs
  *   dloss     : [N] fp32
  *   dh        : [N, D] io_dtype, dW : [V, D] io_dtype, dbias : [V] fp32, each
- *               written, or NULL to skip it
+ *               written, or NULL to skip it; not h or W themselves
  * The logits are formed again.  bf16: the softmax's gradient is rounded on its
  * way into the products with W and h, relative to 1 - exp(-loss) so that the
  * target's entry is exact, and h times that and dloss once more: dh and dW are

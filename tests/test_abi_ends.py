@@ -7,6 +7,7 @@ import pytest
 from delta_rule_linear_dpfp_gb300 import binding, build
 
 FAKE, MISALIGNED, ODD = ctypes.c_void_p(0x10000), ctypes.c_void_p(0x10008), ctypes.c_void_p(0x10002)
+TO, TO2 = ctypes.c_void_p(0x20000), ctypes.c_void_p(0x30000)  # outputs
 E, U, OK = binding.FW_ERR_INVALID_ARG, binding.FW_ERR_UNSUPPORTED, binding.FW_OK
 
 
@@ -24,11 +25,11 @@ def _call(fn, base):
 
 
 def test_embedding_refusals(lib):
-    call = _call(lib.fw_embedding, dict(ids=FAKE, table=FAKE, out=FAKE, N=5, V=9, D=64, scale=1.0, index=1, io=1, st=None))
+    call = _call(lib.fw_embedding, dict(ids=FAKE, table=FAKE, out=TO, N=5, V=9, D=64, scale=1.0, index=1, io=1, st=None))
     need = lib.fw_embedding_backward_workspace_size(5, 9, 64)
     assert need > 0
     back = _call(lib.fw_embedding_backward,
-                 dict(ids=FAKE, dout=FAKE, dtable=FAKE, ws=FAKE, wsb=need, N=5, V=9, D=64, scale=1.0, acc=0, index=1, io=1,
+                 dict(ids=FAKE, dout=FAKE, dtable=TO, ws=FAKE, wsb=need, N=5, V=9, D=64, scale=1.0, acc=0, index=1, io=1,
                       st=None))
     for n in ("table", "out"):
         assert call(**{n: None}) == E and call(**{n: MISALIGNED}) == E, n
@@ -39,12 +40,13 @@ def test_embedding_refusals(lib):
         assert c(N=-1) == E and c(V=0) == E and c(D=0) == E and c(scale=float("nan")) == E and c(scale=float("inf")) == E
         assert c(D=12) == U and c(D=65544) == U and c(V=2**31 - 1) == U and c(N=2**40) == U
     assert back(wsb=need - 1) == E and back(acc=2) == E and back(N=2**31 - 1) == U
+    assert call(out=FAKE) == E                                   # the table itself
     assert call(N=0, ids=None, table=None, out=None) == OK
     assert back(N=0, ids=None, dout=None, ws=None, wsb=0, acc=1) == OK and back(N=0, dtable=None) == E
 
 
 def test_layer_norm_refusals(lib):
-    call = _call(lib.fw_layer_norm, dict(x=FAKE, res=None, gamma=FAKE, beta=FAKE, out=FAKE, sum=None, rows=5, d=64, eps=1e-5,
+    call = _call(lib.fw_layer_norm, dict(x=FAKE, res=None, gamma=FAKE, beta=FAKE, out=TO, sum=None, rows=5, d=64, eps=1e-5,
                                          io=1, st=None))
     need = lib.fw_layer_norm_backward_workspace_size(5, 64)
     assert need > 0
@@ -59,6 +61,7 @@ def test_layer_norm_refusals(lib):
         assert call(**{n: MISALIGNED}) == E, n
     assert call(res=MISALIGNED, sum=FAKE) == E and call(res=FAKE, sum=MISALIGNED) == E
     assert call(res=FAKE) == E and call(sum=FAKE) == E           # sum goes with residual
+    assert call(res=FAKE, sum=TO) == E                           # two outputs in one place
     for n in ("gamma", "dsum", "dgamma", "dbeta"):
         assert back(**{n: MISALIGNED}) == E, n
     assert back(dgamma=None) == E and back(dbeta=None) == E and back(wsb=need - 1) == E
@@ -75,7 +78,7 @@ def test_vocab_loss_refusals(lib, io):
                                          V=9, D=64, index=1, io=io, st=None))
     bneed = lib.fw_vocab_loss_backward_workspace_size(5, 9, 64, io)
     back = _call(lib.fw_vocab_loss_backward,
-                 dict(h=FAKE, W=FAKE, bias=None, targets=FAKE, loss=FAKE, lse=FAKE, dloss=FAKE, dh=FAKE, dW=FAKE, dbias=None,
+                 dict(h=FAKE, W=FAKE, bias=None, targets=FAKE, loss=FAKE, lse=FAKE, dloss=FAKE, dh=TO, dW=TO2, dbias=None,
                       ws=FAKE, wsb=bneed, N=5, V=9, D=64, index=1, io=io, st=None))
     assert need > 0 and bneed > need
     for c, more in ((call, ()), (back, ("dloss",))):
@@ -87,6 +90,7 @@ def test_vocab_loss_refusals(lib, io):
     for n in ("dh", "dW", "dbias"):
         assert back(**{n: MISALIGNED}) == E, n
     assert call(wsb=need - 1) == E and back(wsb=bneed - 1) == E
+    assert back(dh=FAKE) == E and back(dW=FAKE) == E             # the inputs themselves
     assert call(N=0, h=None, targets=None, loss=None, lse=None, ws=None, wsb=0) == OK
     assert back(N=0, h=None, targets=None, dW=None, ws=None, wsb=0) == OK
 
