@@ -186,20 +186,8 @@ FW_DEV void tmem_ld32(uint32_t taddr, float *r) {
         r[i] = __uint_as_float(u[i]);
 }
 
-// 64 columns of an accumulator into z, as pairs.
-FW_DEV void load_tmem64(uint32_t taddr, F2 *z) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float r[32];
-        tmem_ld32(taddr + 32 * h, r);
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            z[16 * h + j] = pack(r[2 * j], r[2 * j + 1]);
-    }
-}
-
 // 16 columns of an accumulator added to z.
-FW_DEV void add_tmem(uint32_t taddr, F2 *z) {
+FW_DEV void add_tmem(uint32_t taddr, float *z) {
     uint32_t u[16];
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
                  "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
@@ -209,19 +197,12 @@ FW_DEV void add_tmem(uint32_t taddr, F2 *z) {
                  : "r"(taddr)
                  : "memory");
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        z[j] = z[j] + pack(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+    for (int j = 0; j < 16; ++j)
+        z[j] += __uint_as_float(u[j]);
 }
 
-// Lane l's sum over the warp's lanes of value l of the 32 at p: halves are exchanged and added.
-FW_DEV float columns_sum(const F2 *p, int lane) {
-    float x[32];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        const float2 v = unpack(p[j]);
-        x[2 * j] = v.x;
-        x[2 * j + 1] = v.y;
-    }
+// Lane l's sum over the warp's lanes of value l of the 32 at x: halves are exchanged and added.
+FW_DEV float columns_sum(float *x, int lane) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const bool up = lane & o;
@@ -457,21 +438,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                     }
                 }
                 // its logits, from the bias on
-                F2 z[kCols / 2];
+                float z[kCols];
                 const bool from_bias = bias && needed;
                 if (from_bias) {
                     if (col0 + kCols <= q.V) {
 #pragma unroll
                         for (int j = 0; j < kCols / 4; ++j) {
                             const float4 b = __ldcg(reinterpret_cast<const float4 *>(bias + col0) + j);
-                            z[2 * j] = pack(b.x, b.y);
-                            z[2 * j + 1] = pack(b.z, b.w);
+                            z[4 * j] = b.x;
+                            z[4 * j + 1] = b.y;
+                            z[4 * j + 2] = b.z;
+                            z[4 * j + 3] = b.w;
                         }
                     } else {
 #pragma unroll
-                        for (int j = 0; j < kCols / 2; ++j)
-                            z[j] = pack(col0 + 2 * j < q.V ? __ldcg(bias + col0 + 2 * j) : 0.f,
-                                        col0 + 2 * j + 1 < q.V ? __ldcg(bias + col0 + 2 * j + 1) : 0.f);
+                        for (int j = 0; j < kCols; ++j)
+                            z[j] = col0 + j < q.V ? __ldcg(bias + col0 + j) : 0.f;
                     }
                 }
                 bool ok = true;
@@ -480,12 +462,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                     if (!ok)
                         break;
                     if (needed) {
-                        if (k == p.k0 && !from_bias)
-                            load_tmem64(acc, z);
-                        else
+                        if (k == p.k0 && !from_bias) {
+                            tmem_ld32(acc, z);
+                            tmem_ld32(acc + 32, z + 32);
+                        } else {
 #pragma unroll
-                            for (int i = 0; i < kCols / 16; ++i)
-                                add_tmem(acc + 16 * i, z + 8 * i);
+                            for (int i = 0; i < kCols; i += 16)
+                                add_tmem(acc + i, z + i);
+                        }
                     }
                     done_with_acc();
                 }
@@ -495,66 +479,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                     continue;
                 if (col0 + kCols > q.V) { // nothing past the vocabulary
 #pragma unroll
-                    for (int j = 0; j < kCols / 2; ++j) {
-                        const float2 v = unpack(z[j]);
-                        z[j] = pack(col0 + 2 * j < q.V ? v.x : -INFINITY, col0 + 2 * j + 1 < q.V ? v.y : -INFINITY);
-                    }
+                    for (int j = 0; j < kCols; ++j)
+                        z[j] = col0 + j < q.V ? z[j] : -INFINITY;
                 }
                 const int tk = target < 0 ? -1 : target - q.b0 - col0; // the target's place among these (or not)
                 if (MODE == kLoss) {
                     if (tk >= 0 && tk < kCols) {
                         float tz = 0.f;
 #pragma unroll
-                        for (int j = 0; j < kCols / 2; ++j) {
-                            const float2 v = unpack(z[j]);
-                            tz = 2 * j == tk ? v.x : 2 * j + 1 == tk ? v.y : tz;
-                        }
+                        for (int j = 0; j < kCols; ++j)
+                            tz = j == tk ? z[j] : tz;
                         if (target < g.vocab)
                             g.target_z[row] = tz;
                     }
                     float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int j = 0; j < kCols / 2; ++j) {
-                        const float2 v = unpack(z[j]);
-                        m[j & 3] = fmaxf(m[j & 3], fmaxf(v.x, v.y));
-                    }
+                    for (int j = 0; j < kCols; j += 2)
+                        m[(j >> 1) & 3] = fmaxf(m[(j >> 1) & 3], fmaxf(z[j], z[j + 1]));
                     const float ref = reference(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
-                    F2 s[4] = {};
+                    float s[4] = {};
 #pragma unroll
-                    for (int j = 0; j < kCols / 2; ++j) {
-                        const float2 e = unpack(fma2(z[j], both(kLog2e), both(-ref)));
-                        s[j & 3] = s[j & 3] + pack(ex2(e.x), ex2(e.y));
-                    }
-                    const float total = sum((s[0] + s[1]) + (s[2] + s[3]));
+                    for (int j = 0; j < kCols; ++j)
+                        s[j & 3] += ex2(fmaf(z[j], kLog2e, -ref));
+                    const float total = (s[0] + s[1]) + (s[2] + s[3]);
                     if (row < q.N)
                         g.part[(size_t)(col0 / kCols) * q.N + row] = make_float2(total == 0.f ? kNoRef : ref, total);
                 } else {
-                    const float ref = c.x, rq = c.y, at_target = c.z, weight = c.w;
+                    const float ref = c.x, at_target = c.z, weight = c.w;
                     const bool live = target >= 0;
                     free_box();
 #pragma unroll
                     for (int j = 0; j < kCols; j += 8) {
-                        F2 e[4];
+                        float e[8];
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const float2 v = unpack(fma2(z[(j >> 1) + x], both(kLog2e), both(-ref)));
-                            e[x] = pack(ex2(v.x), ex2(v.y)) * both(rq);
-                        }
-                        uint4 u;
-                        const float2 v0 = unpack(e[0]), v1 = unpack(e[1]), v2 = unpack(e[2]), v3 = unpack(e[3]);
-                        u.x = pack_bf16x2(v0.x, v0.y);
-                        u.y = pack_bf16x2(v1.x, v1.y);
-                        u.z = pack_bf16x2(v2.x, v2.y);
-                        u.w = pack_bf16x2(v3.x, v3.y);
-                        *reinterpret_cast<uint4 *>(out + lane * 128 + (((j >> 3) ^ (lane & 7)) << 4)) = u;
+                        for (int x = 0; x < 8; ++x)
+                            e[x] = ex2(fmaf(z[j + x], kLog2e, -ref));
+                        *reinterpret_cast<uint4 *>(out + lane * 128 + (((j >> 3) ^ (lane & 7)) << 4)) =
+                            make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
+                                       pack_bf16x2(e[6], e[7]));
                         if (g.colsum)
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const float2 v = unpack(e[x]);
-                                const int k = tk - j - 2 * x;
-                                z[(j >> 1) + x] =
-                                    live ? pack(k == 0 ? at_target : v.x, k == 1 ? at_target : v.y) * both(weight) : F2{0};
-                            }
+                            for (int x = 0; x < 8; ++x)
+                                z[j + x] = live ? (tk == j + x ? at_target : e[x]) * weight : 0.f;
                     }
                     if (tk >= 0 && tk < kCols) // the target's entry
                         *reinterpret_cast<__nv_bfloat16 *>(out + lane * 128 + (((tk >> 3) ^ (lane & 7)) << 4) + 2 * (tk & 7)) =
@@ -567,7 +533,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                     if (g.colsum)
 #pragma unroll
                         for (int c1 = 0; c1 < kCols; c1 += 32)
-                            g.colsum[(size_t)(row0 / 32) * g.ldc + col0 + c1 + lane] = columns_sum(z + c1 / 2, lane);
+                            g.colsum[(size_t)(row0 / 32) * g.ldc + col0 + c1 + lane] = columns_sum(z + c1, lane);
                 }
             } else {
                 if (!next_acc(acc))
@@ -920,7 +886,7 @@ cudaError_t launch_vocab_loss_backward(const void *h, const void *W, const float
     if (e == cudaSuccess && dW && !dw_direct)
         e = make_f32_sw128_map(&to_dw.out, dw_part, p.dw.n * p.width, D, D, 32);
     if (e == cudaSuccess)
-        e = launch_rows(h, targets, loss, lse, dloss, row, row_target, dW ? wh : nullptr, N, V, D, st);
+        e = launch_rows(h, targets, loss, lse, dloss, row, row_target, dW ? wh : nullptr, true, N, V, D, st);
     for (int v0 = 0; e == cudaSuccess && v0 < V; v0 += p.width) {
         const int nv = std::min(p.width, V - v0);
         const bool last = v0 + p.width >= V;

@@ -39,9 +39,10 @@ cudaError_t launch_few(const void *h, const void *W, const float *bias, Tokens t
                        int N, int V, int D, int bf16, cudaStream_t st);
 cudaError_t launch_join_parts(const float2 *part, const float *target_z, Tokens targets, float *loss, float *lse, int N,
                               int V, int nparts, cudaStream_t st);
-// The tokens' constants (see row_constants) and targets (-1 for none), and w h in bf16 (or null).
+// The tokens' constants (see row_constants; `folded`: row.y into row.x) and targets (-1
+// for none), and w h in bf16 (or null).
 cudaError_t launch_rows(const void *h, Tokens targets, const float *loss, const float *lse, const float *dloss,
-                        float4 *row, int *row_target, void *wh, int N, int V, int D, cudaStream_t st);
+                        float4 *row, int *row_target, void *wh, bool folded, int N, int V, int D, cudaStream_t st);
 
 // dbias of a piece from the sums of 32 tokens each ([blocks][ldc]), in order (fw_vocab.cu).
 cudaError_t launch_join_bias(const float *colsum, float *dbias, int V, int blocks, int ldc, cudaStream_t st);

@@ -196,17 +196,18 @@ __global__ void __launch_bounds__(kJ)
 
 // What a token brings to G and to its row of dh: with q = max(-expm1(-loss), kQMin),
 //   G = 2^(z log2 e - row.x) row.y off the target, row.z on it; q dloss = row.w,
-// all 0 for a token without a gradient.
-FW_DEV bool row_constants(const Tokens &targets, const float *loss, const float *lse, const float *dloss, int n, int V,
-                          float4 &row, int &target) {
+// all 0 for a token without a gradient.  Folded, row.y is 1: the rounding of row.x
+// (2^-21 of G for a row) is below G's own to bf16.
+FW_DEV bool row_constants(const Tokens &targets, const float *loss, const float *lse, const float *dloss, bool folded,
+                          int n, int V, float4 &row, int &target) {
     const int t = token_at(targets, n, V);
     target = t < V ? t : -1; // (past the vocabulary: the loss is NaN, there is no gradient)
     row = make_float4(0.f, 0.f, 0.f, 0.f);
     if (target < 0)
         return false;
     const float q = -expm1f(-__ldcg(loss + n)), s = __ldcg(lse + n), over = fmaxf(q, kQMin);
-    row.x = reference(s);
-    row.y = ex2(fmaf(-s, kLog2e, row.x)) / over; // (what the reference is off by)
+    row.x = folded ? fmaf(s, kLog2e, log2f(over)) : reference(s);
+    row.y = folded ? 1.f : ex2(fmaf(-s, kLog2e, row.x)) / over; // (what the reference is off by)
     row.z = -q / over;
     row.w = over * __ldcg(dloss + n);
     return true;
@@ -216,7 +217,7 @@ FW_DEV bool row_constants(const Tokens &targets, const float *loss, const float 
 // gradient, whatever h holds there.
 __global__ void __launch_bounds__(kS)
     rows_kernel(const __nv_bfloat16 *h, Tokens targets, const float *loss, const float *lse, const float *dloss,
-                float4 *row, int *row_target, __nv_bfloat16 *wh, int N, int V, int D, int lg) {
+                float4 *row, int *row_target, __nv_bfloat16 *wh, bool folded, int N, int V, int D, int lg) {
     griddep_launch_dependents();
     griddep_wait();
     h = after_wait(h);
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(kS)
         return;
     float4 r;
     int target;
-    const bool live = row_constants(targets, loss, lse, dloss, n, V, r, target);
+    const bool live = row_constants(targets, loss, lse, dloss, folded, n, V, r, target);
     if (lane == 0) {
         row[n] = r;
         row_target[n] = target;
@@ -286,10 +287,10 @@ cudaError_t launch_join_parts(const float2 *part, const float *target_z, Tokens 
 }
 
 cudaError_t launch_rows(const void *h, Tokens targets, const float *loss, const float *lse, const float *dloss,
-                        float4 *row, int *row_target, void *wh, int N, int V, int D, cudaStream_t st) {
+                        float4 *row, int *row_target, void *wh, bool folded, int N, int V, int D, cudaStream_t st) {
     const int lg = group_log2(D), per = kS >> lg;
     return launch_pdl(rows_kernel, dim3((N + per - 1) / per), dim3(kS), 0, st, (const __nv_bfloat16 *)h, targets, loss,
-                      lse, dloss, row, row_target, (__nv_bfloat16 *)wh, N, V, D, lg);
+                      lse, dloss, row, row_target, (__nv_bfloat16 *)wh, folded, N, V, D, lg);
 }
 
 } // namespace vocab
