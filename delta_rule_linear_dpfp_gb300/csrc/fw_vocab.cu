@@ -26,7 +26,8 @@
 // end, in 32 bits).  What is rounded to bf16 on the way is G, whose largest entry
 // is exactly -1 at the target, and w h, element by element: errors that are as
 // independent as those of the rounded outputs.  Rounding (p - 1) dloss itself
-// would put one relative error of up to 2^-8 into a whole row of dh and dW.
+// would put one relative error of up to 2^-8 into a whole row of dh and dW.  Up to
+// 256 tokens, whose contraction is short, w h goes in as two terms (2^-16 of it left).
 #include <cuda.h>
 
 #include <algorithm>
@@ -55,7 +56,9 @@ static_assert(kSmem <= 227 * 1024, "one CTA's shared memory");
 // Steps of 64 that an accumulator of logits takes: the tensor core truncates what it
 // adds, so that a sum of many terms of one sign falls short by about 2^-25 of itself with
 // every step of 16; chunks of 512 are added in the epilogue, where sums are rounded.
-constexpr int kLogitSteps = 8;
+constexpr int kLogitSteps = 8, kFewLogitSteps = 2, kFewTokens = 256;
+// (up to kFewTokens by 128, and w h in two terms: 64 tokens over 50 001 entries, D 1024, 87 us
+// for the gradients instead of 81)
 
 enum Mode {
     kLoss,    // h W^T: parts of the logits' log-sum-exp, the targets' logits
@@ -93,6 +96,7 @@ struct Product {
     int group;           // tile rows that are walked together, column by column
     Divisor by_split, by_group, by_rows, by_last; // a split's tiles, a group's, a group's rows, the last group's rows
     int b0;              // B's first row
+    int a_steps;         // steps after which A begins anew (B goes on: the second terms of its rows)
     int N, V;            // rows and columns of the output that are there
     int out;             // Out (kProducts)
     int rows_a_split;    // kF32, kAdd: rows between the splits' outputs
@@ -102,6 +106,7 @@ struct Product {
 struct GemmArgs {
     Product of[2];      // (the second: kProducts alone)
     int extra;          // see walk
+    int chunk;          // kLoss, kGrad: steps of an accumulator
     const float *bias;  // kLoss, kGrad: of this piece, or null
     Tokens targets;
     int vocab;          // all of the vocabulary's entries
@@ -324,8 +329,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                 if (rank == 0)
                     mbar_arrive_expect_tx(full + s, 2 * kStageBytes);
                 if (second) {
-                    tma_load_pair(a, ta, m, 64 * k, bar);
-                    tma_load_pair(a + 8192, ta, m + 64, 64 * k, bar);
+                    const int ka = k < g.of[1].a_steps ? k : k - g.of[1].a_steps;
+                    tma_load_pair(a, ta, m, 64 * ka, bar);
+                    tma_load_pair(a + 8192, ta, m + 64, 64 * ka, bar);
                 } else {
                     tma_load_pair(a, ta, 64 * k, m, bar);
                 }
@@ -377,8 +383,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
             if (MODE == kProducts)
                 ok = fill(p.k0, p.k1, p.w);
             else
-                for (int k = p.k0; ok && k < p.k1; k += kLogitSteps)
-                    ok = fill(k, min(k + kLogitSteps, p.k1), false);
+                for (int k = p.k0; ok && k < p.k1; k += g.chunk)
+                    ok = fill(k, min(k + g.chunk, p.k1), false);
         }
         // every read of an accumulator has been told of
         for (uint32_t buf = 0; ok && buf < 2 && buf < it; ++buf)
@@ -432,6 +438,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                 if (needed && row < q.N) {
                     if (MODE == kLoss) {
                         target = token_at(targets, row, g.vocab);
+                        target = target < g.vocab ? target : -1; // (past the vocabulary: none of the columns)
                     } else {
                         target = __ldcg(row_targets + row);
                         c = __ldcg(rows + row);
@@ -457,7 +464,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                     }
                 }
                 bool ok = true;
-                for (int k = p.k0; k < p.k1; k += kLogitSteps) {
+                for (int k = p.k0; k < p.k1; k += g.chunk) {
                     ok = next_acc(acc);
                     if (!ok)
                         break;
@@ -487,10 +494,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                     if (tk >= 0 && tk < kCols) {
                         float tz = 0.f;
 #pragma unroll
-                        for (int j = 0; j < kCols; ++j)
+                        for (int j = 0; j < kCols; ++j) { // (kept apart: the loss is log(1 + the others / it))
                             tz = j == tk ? z[j] : tz;
-                        if (target < g.vocab)
-                            g.target_z[row] = tz;
+                            z[j] = j == tk ? -INFINITY : z[j];
+                        }
+                        g.target_z[row] = tz;
                     }
                     float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -704,6 +712,7 @@ struct Plan {
     int width;      // vocabulary entries of a piece (a multiple of 256)
     int ldg;        // row stride of G
     int pieces;
+    int lo_rows;    // w h in two terms: the second ones from this row on (0: one term)
     Splits dh, dw;
     size_t row, row_target, G, wh, dh_part, dw_part, colsum, bytes; // offsets
 };
@@ -716,7 +725,9 @@ Plan plan_of(int N, int V, int D) {
     p.ldg = p.width;
     p.pieces = (V + p.width - 1) / p.width;
     p.dh = splits_of((int64_t)tiles_of(N) * kt, (std::min(p.width, V) + 63) / 64);
-    p.dw = splits_of((int64_t)(p.width / kTile) * kt, (N + 63) / 64);
+    const int kn = (N + 63) / 64;
+    p.lo_rows = N <= kFewTokens ? 64 * kn : 0;
+    p.dw = splits_of((int64_t)(p.width / kTile) * kt, p.lo_rows ? 2 * kn : kn);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t o = at;
@@ -726,7 +737,7 @@ Plan plan_of(int N, int V, int D) {
     p.row = take(sizeof(float4) * (size_t)N);
     p.row_target = take(sizeof(int) * (size_t)N);
     p.G = take((size_t)2 * N * p.ldg);
-    p.wh = take((size_t)2 * N * D);
+    p.wh = take((size_t)2 * (p.lo_rows ? 2 * p.lo_rows : N) * D);
     // dh goes through sums in 32 bits where it has several parts (rows in whole tiles)
     p.dh_part = take(p.dh.n * p.pieces > 1 ? (size_t)4 * p.dh.n * tiles_of(N) * kTile * D : 0);
     p.dw_part = take(p.dw.n > 1 ? (size_t)4 * p.dw.n * p.width * D : 0);
@@ -840,6 +851,7 @@ cudaError_t launch_vocab_loss(const void *h, const void *W, const float *bias, T
         g.part = part;
         g.target_z = target_z;
         g.of[0] = product(N, V, kb, kb, token_group(N, D));
+        g.chunk = N <= kFewTokens ? kFewLogitSteps : kLogitSteps;
         Maps m;
         e = make_bf16_map(&m.a, h, N, D, D, 128);
         if (e == cudaSuccess)
@@ -882,17 +894,18 @@ cudaError_t launch_vocab_loss_backward(const void *h, const void *W, const float
         e = dh_direct ? make_bf16_map(&to_dh.out, dh, N, D, D, 32)
                       : make_f32_sw128_map(&to_dh.out, dh_part, (int)(p.dh.n * dh_rows), D, D, 32);
     if (e == cudaSuccess) e = make_bf16_map(&to_dw.a, G, N, p.ldg, p.ldg, 64);
-    if (e == cudaSuccess) e = make_bf16_map(&to_dw.b, wh, N, D, D, 64);
+    if (e == cudaSuccess) e = make_bf16_map(&to_dw.b, wh, p.lo_rows ? 2 * p.lo_rows : N, D, D, 64);
     if (e == cudaSuccess && dW && !dw_direct)
         e = make_f32_sw128_map(&to_dw.out, dw_part, p.dw.n * p.width, D, D, 32);
     if (e == cudaSuccess)
-        e = launch_rows(h, targets, loss, lse, dloss, row, row_target, dW ? wh : nullptr, true, N, V, D, st);
+        e = launch_rows(h, targets, loss, lse, dloss, row, row_target, dW ? wh : nullptr, p.lo_rows, true, N, V, D, st);
     for (int v0 = 0; e == cudaSuccess && v0 < V; v0 += p.width) {
         const int nv = std::min(p.width, V - v0);
         const bool last = v0 + p.width >= V;
         GemmArgs g = {};
         g.of[0] = product(N, nv, kd, kd, token_group(N, D));
         g.of[0].b0 = v0;
+        g.chunk = N <= kFewTokens ? kFewLogitSteps : kLogitSteps;
         g.vocab = V;
         g.bias = bias ? bias + v0 : nullptr;
         g.row = row;
@@ -913,7 +926,8 @@ cudaError_t launch_vocab_loss_backward(const void *h, const void *W, const float
                 q.of[0].rows_a_split = (int)dh_rows;
             }
             if (dW) {
-                q.of[1] = product(nv, D, kn, p.dw.per, 4);
+                q.of[1] = product(nv, D, p.lo_rows ? 2 * kn : kn, p.dw.per, 4);
+                q.of[1].a_steps = kn;
                 q.of[1].out = dw_direct ? kBf16 : kF32;
                 q.of[1].rows_a_split = p.width;
                 if (dw_direct)

@@ -31,7 +31,8 @@ inline int group_log2(int D) {
 }
 
 // The parts that the products leave of a token, [parts][N] (reference, sum of
-// 2^(z log2 e - reference)), the targets' logits behind them.
+// 2^(z log2 e - reference) over the entries other than its target), the targets'
+// logits behind them.
 int parts_of(int N, int V, int D);
 // Up to four answers that fit: the whole product, on CUDA cores.
 bool few(int N, int D);
@@ -40,9 +41,9 @@ cudaError_t launch_few(const void *h, const void *W, const float *bias, Tokens t
 cudaError_t launch_join_parts(const float2 *part, const float *target_z, Tokens targets, float *loss, float *lse, int N,
                               int V, int nparts, cudaStream_t st);
 // The tokens' constants (see row_constants; `folded`: row.y into row.x) and targets (-1
-// for none), and w h in bf16 (or null).
+// for none), and w h in bf16 (or null), with lo_rows in two terms.
 cudaError_t launch_rows(const void *h, Tokens targets, const float *loss, const float *lse, const float *dloss,
-                        float4 *row, int *row_target, void *wh, bool folded, int N, int V, int D, cudaStream_t st);
+                        float4 *row, int *row_target, void *wh, int lo_rows, bool folded, int N, int V, int D, cudaStream_t st);
 
 // dbias of a piece from the sums of 32 tokens each ([blocks][ldc]), in order (fw_vocab.cu).
 cudaError_t launch_join_bias(const float *colsum, float *dbias, int V, int blocks, int ldc, cudaStream_t st);

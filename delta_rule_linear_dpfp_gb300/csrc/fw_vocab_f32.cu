@@ -180,8 +180,10 @@ template <Mode MODE> __global__ void __launch_bounds__(kT, 2) vocab_f32_kernel(A
                 float top = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (target == col + j && target < a.vocab)
+                    if (target == col + j && target < a.vocab) { // (kept apart from the others)
                         a.target_z[row] = v[j];
+                        v[j] = -INFINITY;
+                    }
                     top = fmaxf(top, v[j]);
                 }
                 const float ref = reference(over_row(top, true));
@@ -338,7 +340,7 @@ cudaError_t backward_f32(const float *h, const float *W, const float *bias, Toke
     int *row_target = reinterpret_cast<int *>(ws + p.row_target);
     float *g = reinterpret_cast<float *>(ws + p.g), *dh_part = reinterpret_cast<float *>(ws + p.dh_part);
     float *dw_part = reinterpret_cast<float *>(ws + p.dw_part), *colsum = reinterpret_cast<float *>(ws + p.colsum);
-    cudaError_t e = launch_rows(nullptr, targets, loss, lse, dloss, row, row_target, nullptr, false, N, V, D, st);
+    cudaError_t e = launch_rows(nullptr, targets, loss, lse, dloss, row, row_target, nullptr, 0, false, N, V, D, st);
     for (int v0 = 0; e == cudaSuccess && v0 < V; v0 += p.width) {
         const int nv = std::min(p.width, V - v0), blocks = (N + 31) / 32;
         Args a = {};

@@ -115,9 +115,9 @@ __global__ void __launch_bounds__(kFewT, few_an_sm(NT))
             x[0] += __shfl_xor_sync(0xffffffffu, x[0], o1);
         if (owner && v0 + r0 < V) {
             const float z = x[0] + b;
-            if (v0 + r0 == target)
-                target_z[t] = z;
-            if (z != -INFINITY) {
+            if (v0 + r0 == target) {
+                target_z[t] = z; // (kept apart from the others)
+            } else if (z != -INFINITY) {
                 const float m = fmaxf(top, reference(z));
                 total = total * ex2(top - m) + ex2(fmaf(z, kLog2e, -m));
                 top = m;
@@ -188,9 +188,25 @@ __global__ void __launch_bounds__(kJ)
     }
     if (w == 0 && n < N) {
         const int t = token_at(targets, n, V);
-        const float l = logf(total); // lse = top ln 2 + l
-        loss[n] = t < 0 ? 0.f : t >= V ? __int_as_float(0x7fffffff) : fmaf(fmaf(-__ldcg(target_z + n), kLog2e, top), kLn2, l);
-        lse[n] = t < 0 ? 0.f : fmaf(top, kLn2, l);
+        // the sum is that of the other entries: loss = log(1 + sum / exp(z_t)), without a
+        // difference of large numbers where the target is all but certain
+        const float l = logf(total);
+        float a = 0.f, b = 0.f;
+        if (t >= V) {
+            a = __int_as_float(0x7fffffff);
+            b = fmaf(top, kLn2, l);
+        } else if (t >= 0) {
+            const float z = __ldcg(target_z + n), x = fmaf(-z, kLog2e, top);
+            if (x > 64.f) { // (the target's own part is nothing beside them)
+                a = fmaf(x, kLn2, l);
+                b = fmaf(top, kLn2, l);
+            } else {
+                a = log1pf(total * ex2(x));
+                b = z + a;
+            }
+        }
+        loss[n] = a;
+        lse[n] = b;
     }
 }
 
@@ -214,10 +230,11 @@ FW_DEV bool row_constants(const Tokens &targets, const float *loss, const float 
 }
 
 // The tokens' constants, and w h in bf16 (wh, or null): zeros for the tokens without a
-// gradient, whatever h holds there.
+// gradient, whatever h holds there.  With lo_rows, what its rounding leaves follows from
+// that row on, rounded as well, and the rows between are zeros.
 __global__ void __launch_bounds__(kS)
     rows_kernel(const __nv_bfloat16 *h, Tokens targets, const float *loss, const float *lse, const float *dloss,
-                float4 *row, int *row_target, __nv_bfloat16 *wh, bool folded, int N, int V, int D, int lg) {
+                float4 *row, int *row_target, __nv_bfloat16 *wh, int lo_rows, bool folded, int N, int V, int D, int lg) {
     griddep_launch_dependents();
     griddep_wait();
     h = after_wait(h);
@@ -226,12 +243,12 @@ __global__ void __launch_bounds__(kS)
     lse = after_wait(lse);
     dloss = after_wait(dloss);
     const int n = (int)(blockIdx.x * (kS >> lg) + (threadIdx.x >> lg)), lane = threadIdx.x & ((1 << lg) - 1);
-    if (n >= N)
+    if (n >= max(N, wh ? lo_rows : 0))
         return;
-    float4 r;
-    int target;
-    const bool live = row_constants(targets, loss, lse, dloss, folded, n, V, r, target);
-    if (lane == 0) {
+    float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+    int target = -1;
+    const bool live = n < N && row_constants(targets, loss, lse, dloss, folded, n, V, r, target);
+    if (lane == 0 && n < N) {
         row[n] = r;
         row_target[n] = target;
     }
@@ -245,6 +262,12 @@ __global__ void __launch_bounds__(kS)
                     v[e] *= r.w;
             }
             store8(wh + (size_t)n * D + c, v);
+            if (lo_rows) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] -= __bfloat162float(__float2bfloat16_rn(v[e]));
+                store8(wh + (size_t)(lo_rows + n) * D + c, v);
+            }
         }
 }
 
@@ -287,10 +310,10 @@ cudaError_t launch_join_parts(const float2 *part, const float *target_z, Tokens 
 }
 
 cudaError_t launch_rows(const void *h, Tokens targets, const float *loss, const float *lse, const float *dloss,
-                        float4 *row, int *row_target, void *wh, bool folded, int N, int V, int D, cudaStream_t st) {
-    const int lg = group_log2(D), per = kS >> lg;
-    return launch_pdl(rows_kernel, dim3((N + per - 1) / per), dim3(kS), 0, st, (const __nv_bfloat16 *)h, targets, loss,
-                      lse, dloss, row, row_target, (__nv_bfloat16 *)wh, folded, N, V, D, lg);
+                        float4 *row, int *row_target, void *wh, int lo_rows, bool folded, int N, int V, int D, cudaStream_t st) {
+    const int lg = group_log2(D), per = kS >> lg, rows = std::max(N, lo_rows);
+    return launch_pdl(rows_kernel, dim3((rows + per - 1) / per), dim3(kS), 0, st, (const __nv_bfloat16 *)h, targets, loss,
+                      lse, dloss, row, row_target, (__nv_bfloat16 *)wh, lo_rows, folded, N, V, D, lg);
 }
 
 } // namespace vocab

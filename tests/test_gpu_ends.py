@@ -312,6 +312,24 @@ def test_vocab_loss_confident(known, dtype):
     loss_check(200, 500, 128, 7, known=known, bias=True, dtype=dtype)
 
 
+@pytest.mark.parametrize("N", [1, 3, 70, 300])
+@BOTH
+def test_vocab_loss_all_but_certain(N, dtype):
+    """A loss far below the logits' size keeps its digits: log(1 + sum exp(z_v - z_t)) is off by what the differences of
+    logits are, relative to itself, and the exponentials' and the sum's 2^-19."""
+    h, W, t, _, _ = loss_inputs(N, 400, 64, N, known=30.0, dtype=dtype)
+    loss, _ = fw.fw_vocab_loss(h.cuda(), W.cuda(), t.cuda())
+    z = h.double().numpy() @ W.double().numpy().T
+    at = np.arange(N), t.numpy()
+    d = z - z[at][:, None]
+    d[at] = -np.inf
+    ref = np.log1p(np.exp(d).sum(1))
+    S = (np.abs(h.double().numpy()) @ np.abs(W.double().numpy()).T).max(1)
+    rel = 4 * ((64 / 16 + 1) * 2.0 ** -22 if dtype == torch.bfloat16 else 65 * U) * S + 2.0 ** -19
+    assert np.all(np.abs(f64(loss) - ref) <= rel * ref + 1e-300)
+    assert ref.min() < 1e-3 or N < 70
+
+
 @BOTH
 def test_vocab_loss_masked_entries(dtype):
     """A bias of -infinity takes entries out, whole tiles of them; a target among them costs infinity."""
