@@ -348,6 +348,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
             const uint32_t uses = (step - s + kStages - 1) / kStages;
             ok = mbar_wait(empty + s, (uses - 1) & 1, status);
         }
+        // where a wait gave up: what both CTAs have under way lands before either leaves
+        // (they leave together, and the bytes of both are counted on the leader's barriers)
+        for (uint32_t j = step > kStages ? step - kStages : 0; !ok && rank == 0 && j < step; ++j)
+            (void)mbar_wait(full + j % kStages, (j / kStages) & 1, status);
     } else if (warp == 1 && lane == 0 && rank == 0) { // products
         uint32_t step = 0, it = 0; // steps, and accumulators filled, so far
         bool ok = true;
