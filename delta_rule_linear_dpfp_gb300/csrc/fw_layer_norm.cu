@@ -12,9 +12,10 @@
 // Mapping: G threads own a row, 8 channels each (16 bytes of bf16), all in
 // registers.  The statistics take two passes over them: a warp's own mean, then
 // the squares of the differences to it; a row of several warps (then G is the
-// CTA) combines the warps' (mean, squares) in shared memory, one barrier a row.  The backward's two means of products go through the same
-// exchange: with the warp's own mean m_w they are sum dn and sum dn (s - m_w),
-// and sum dn (s - mean) = sum over the warps of the latter + (m_w - mean) sum dn:
+// CTA) combines the warps' (mean, squares) in shared memory, one barrier a row.
+// The backward's two means of products go through the same exchange: with the
+// warp's own mean m_w they are sum dn and sum dn (s - m_w), and
+// sum dn (s - mean) = sum over the warps of the latter + (m_w - mean) sum dn:
 // differences of nearby numbers only.  gamma, beta, dgamma and dbeta stay in
 // registers: one partial row of the parameters' gradients per CTA, added by a
 // second kernel in a fixed order (no atomics).  The next rows are requested before

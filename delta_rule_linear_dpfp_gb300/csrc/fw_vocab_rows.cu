@@ -15,10 +15,11 @@ constexpr float kQMin = 1e-7f; // q below it (p_t = 1 in 32 bits) divides nothin
 // ------------------------------------------------------------ few tokens
 // Up to four answers: bound by reading W once, so a product on CUDA cores from
 // registers, whose start and end cost less than the tensor cores' (32 000
-// entries, D 512: one token 8.9 us, four 11.9, on tensor cores 15 to 17; eight would
-// take 17.9, and 27.8 against 22.9 at D 1024).  A warp takes four rows of W at a time, its lanes 8 channels each; h sits in shared memory in 32 bits.  After
-// the lanes' sums have been exchanged each lane keeps the (reference, sum of
-// exponentials) of one token over the rows it got.
+// entries, D 512: one token 8.9 us, four 11.9, on tensor cores 15 to 17; eight
+// would take 17.9, and 27.8 against 22.9 at D 1024).  A warp takes four rows of
+// W at a time, its lanes 8 channels each; h sits in shared memory in 32 bits.
+// After the lanes' sums have been exchanged each lane keeps the (reference, sum
+// of exponentials) of one token over the rows it got.
 constexpr int kFewT = 256, kFewRows = 4, kFewStep = kFewT / 32 * kFewRows;
 constexpr int kFewValues = 11264; // NT D: 44 KB of shared memory
 constexpr int few_an_sm(int nt) { return nt == 1 ? 4 : 2; } // (registers)
