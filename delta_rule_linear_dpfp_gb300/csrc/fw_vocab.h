@@ -11,14 +11,17 @@ namespace vocab {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 constexpr float kNoRef = -1e30f; // the reference of no entries: below every other
+// Logits below it are out of the vocabulary, as those of -infinity are.  (A mask may be any
+// low number; from 2^31 on a reference's own rounding is past what an exponential holds.)
+constexpr float kOut = -0x1p30f;
 constexpr int kCols = 64;        // vocabulary entries of a part of a token's sum
 constexpr int kPairs = 76;       // pairs of a GB300's SMs: what splits (and so the workspaces) go by
 constexpr size_t kPieceBytes = (size_t)1024 << 20; // of the softmax's gradient, tokens x a piece of the vocabulary
 
 #ifdef __CUDACC__
 // A reference near x for exponentials: x log2 e to a sixteenth, so that z log2 e less
-// the reference takes one rounding (0 for a row that is masked throughout).
-FW_DEV float reference(float x) { return x == -INFINITY ? 0.f : rintf(x * kLog2e * 16.f) * 0.0625f; }
+// the reference takes one rounding (0 where all of them are out: their exponentials are 0).
+FW_DEV float reference(float x) { return x < kOut ? 0.f : rintf(x * kLog2e * 16.f) * 0.0625f; }
 #endif
 
 inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }

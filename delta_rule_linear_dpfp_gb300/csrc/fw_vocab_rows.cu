@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kFewT, few_an_sm(NT))
             const float z = x[0] + b;
             if (v0 + r0 == target) {
                 target_z[t] = z; // (kept apart from the others)
-            } else if (z != -INFINITY) {
+            } else if (!(z < kOut)) {
                 const float m = fmaxf(top, reference(z));
                 total = total * ex2(top - m) + ex2(fmaf(z, kLog2e, -m));
                 top = m;
@@ -199,12 +199,14 @@ __global__ void __launch_bounds__(kJ)
         } else if (t >= 0) {
             const float z = __ldcg(target_z + n), x = fmaf(-z, kLog2e, top);
             if (x > 64.f) { // (the target's own part is nothing beside them)
-                a = fmaf(x, kLn2, l);
                 b = fmaf(top, kLn2, l);
+                a = z < kOut ? b - z : fmaf(x, kLn2, l); // (x may be past the largest float)
             } else {
                 a = log1pf(total * ex2(x));
                 b = z + a;
             }
+            if (z < kOut && total == 0.f) // every entry is out, the target too
+                a = __int_as_float(0x7fffffff);
         }
         loss[n] = a;
         lse[n] = b;

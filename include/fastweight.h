@@ -647,9 +647,9 @@ FW_API size_t fw_vocab_loss_workspace_size(int N, int V, int D, int io_dtype);
  *   z_n = W h_n + bias,  lse_n = log sum_v exp(z_nv),  loss_n = lse_n - z_n,target
  *   h       : [N, D]  io_dtype
  *   W       : [V, D]  io_dtype (an embedding's table, for one)
- *   bias    : [V]     fp32, or NULL; -infinity takes an entry out of the
- *             vocabulary (its gradient is zero; its row of W is finite, as
- *             any other)
+ *   bias    : [V]     fp32, or NULL; -infinity, or any number that leaves the
+ *             logit below -2^30, takes an entry out of the vocabulary (its
+ *             gradient is zero; its row of W is finite, as any other)
  *   targets : [N]     fw_index
  *   loss, lse : [N]   fp32     (written)
  * bf16: products summed in fp32 on the tensor cores, by 512 channels (up to four

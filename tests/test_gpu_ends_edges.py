@@ -1,0 +1,74 @@
+"""Calls of the vocabulary loss at the edges of its numbers: masks of low finite
+values, long sums of one sign, log-sum-exps of any size.
+
+Tolerances as in test_gpu_ends.py (u = 2^-24 is half a step of fp32), each
+derived where it stands."""
+import numpy as np
+import pytest
+import torch
+
+from delta_rule_linear_dpfp_gb300 import binding as fw
+from delta_rule_linear_dpfp_gb300 import build
+from tests.parity_util import f64
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+BOTH = pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    build.build()
+    fw.load()
+    yield
+    assert fw.fw_device_status() == fw.FW_OK
+
+
+def draws(seed):
+    r = torch.Generator(device="cuda").manual_seed(seed)
+    return r, lambda *s: torch.randn(*s, generator=r, device="cuda")
+
+
+@pytest.mark.parametrize("mask", [torch.finfo(torch.float32).min, -1e38, -2e37, -1e30, -1e29, -1e20, -1e10, -1e9, -1e4])
+@pytest.mark.parametrize("N", [1, 3, 70, 300])
+@BOTH
+def test_a_finite_mask_is_a_mask(mask, N, dtype):
+    """Entries whose bias is a low finite number, whole parts of the vocabulary of them: the bits of a bias of -infinity."""
+    V, D = 900, 64
+    r, n = draws(N)
+    W, h = (n(V, D) * D ** -0.5).to(dtype), n(N, D).to(dtype)
+    t = torch.randint(0, 100, (N,), generator=r, device="cuda")
+    dl = torch.rand(N, generator=r, device="cuda")
+    b = n(V)
+    b[100:700] = -float("inf")
+    low = torch.where(torch.isinf(b), mask, b)
+    want = fw.fw_vocab_loss(h, W, t, bias=b)
+    got = fw.fw_vocab_loss(h, W, t, bias=low)
+    assert torch.isfinite(want[0]).all()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    grads = (fw.fw_vocab_loss_backward(h, W, t, *want, dl, bias=x) for x in (b, low))
+    assert all(torch.equal(x, y) for x, y in zip(*grads))
+    # a target among them costs what it is below the others: two roundings of the mask's size, the logits beside it
+    t[0] = 333
+    loss, lse = fw.fw_vocab_loss(h, W, t, bias=low)
+    z = h[0].double() @ W[333].double() + low[333].double()
+    assert abs(float(loss[0]) - (float(lse[0]) - float(z))) <= 4 * U * abs(float(z)) + 2.0 ** -18 * 10
+    dW = fw.fw_vocab_loss_backward(h, W, t, loss, lse, dl, bias=low)[1]
+    assert torch.isfinite(dW).all()
+
+
+@pytest.mark.parametrize("N", [2, 40])
+@BOTH
+def test_all_taken_out(N, dtype):
+    _, n = draws(N)
+    W, h = n(100, 16).to(dtype), n(N, 16).to(dtype)
+    t = torch.arange(N, device="cuda")
+    for mask in (-float("inf"), torch.finfo(torch.float32).min, -1e20):
+        b = torch.full((100,), mask, device="cuda")
+        assert torch.isnan(fw.fw_vocab_loss(h, W, t, bias=b)[0]).all()
+        b[7] = 1.0  # one is left: it is certain
+        loss, lse = fw.fw_vocab_loss(h, W, torch.full_like(t, 7), bias=b)
+        z = h.double() @ W[7].double() + 1
+        assert torch.all(loss == 0) and torch.all((lse - z).abs() < 1e-4)
