@@ -575,8 +575,9 @@ FW_API int fw_group_norm_act_backward(const void *x, const void *gate, const flo
  *
  * D is a multiple of 8 (FW_ERR_UNSUPPORTED otherwise), up to 65536; the layer
  * norm's d up to 8192.  Calls return FW_ERR_INVALID_ARG for null or misaligned
- * pointers, bad sizes, a scale or eps that is not finite, eps < 0 or a small
- * workspace.  No call uses state of the library, so calls with workspaces of
+ * pointers, bad sizes, a scale or eps that is not finite, eps < 0, a small
+ * workspace, and for an output or workspace that shares memory with anything
+ * else of the call, where it does not say that it may.  No call uses state of the library, so calls with workspaces of
  * their own may run at the same time.  Results do not depend on the run (fixed
  * summation orders, no atomics on values).
  */
@@ -616,8 +617,8 @@ FW_API int fw_embedding_backward(const void *ids, const void *dout, void *dtable
  *   x, residual, out, sum : [rows, d]  io_dtype; residual may be NULL, and sum
  *                           (s, rounded) is written exactly when it is not
  *   gamma, beta           : [d] fp32, or NULL (one / zero)
- * out may be x or residual, and sum may be the other of them or residual (in
- * place); out and sum are two tensors.
+ * out may be x or residual, and so may sum (in place); out and sum are two
+ * tensors.
  */
 FW_API int fw_layer_norm(const void *x, const void *residual, const float *gamma, const float *beta, void *out,
                          void *sum, int64_t rows, int d, float eps, int io_dtype, void *stream);
@@ -633,7 +634,7 @@ FW_API size_t fw_layer_norm_backward_workspace_size(int64_t rows, int d);
  *                   they are the same)                          (written)
  *   dgamma, dbeta : [d] fp32, summed over the rows in a fixed order; both NULL
  *                   to skip them (the workspace is then not used)
- * dx may be dout or dsum (in place).
+ * dx may be x, dout or dsum, and dgamma may be gamma (in place).
  */
 FW_API int fw_layer_norm_backward(const void *x, const float *gamma, const void *dout, const void *dsum, void *dx,
                                   float *dgamma, float *dbeta, void *workspace, size_t workspace_bytes, int64_t rows,
@@ -674,7 +675,7 @@ FW_API size_t fw_vocab_loss_backward_workspace_size(int N, int V, int D, int io_
  *   loss, lse : [N] fp32, as fw_vocab_loss wrote them for the same inputs
  *   dloss     : [N] fp32
  *   dh        : [N, D] io_dtype, dW : [V, D] io_dtype, dbias : [V] fp32, each
- *               written, or NULL to skip it; not h or W themselves
+ *               written, or NULL to skip it; dbias may be bias (in place)
  * The logits are formed again.  bf16: the softmax's gradient is rounded on its
  * way into the products with W and h, relative to 1 - exp(-loss) so that the
  * target's entry is exact, and h times that and dloss once more: dh and dW are

@@ -107,3 +107,86 @@ def test_workspace_queries(lib):
         assert f(8192, 10**6, 512, io) < 2**31 < 2 * 8192 * 10**6      # pieces of the vocabulary
     f = lib.fw_vocab_loss_workspace_size
     assert f(8192, 10**6, 512, 1) < 2**31 and f(2**20, 2**16, 512, 1) > 2**32 and f(1, 1, 8, 0) > 0 == f(1, 1, 8, 2)
+
+
+# ------------------------------------------------------------- shared memory
+def _spread(fn, args, nbytes):
+    """A call whose tensors lie apart from one another, and each one's address by name; `nbytes`: their sizes."""
+    at = {n: 0x100000 * (i + 1) for i, n in enumerate(nbytes)}
+    ptr = {n: ctypes.c_void_p(a) for n, a in at.items()}
+
+    def call(**kw):
+        assert set(kw) <= set(args)
+        return fn(*{**args, **ptr, **kw}.values())
+    return call, at
+
+
+def _refused(call, at, nbytes, out, allowed=(), with_=None):
+    """Each output on each other tensor: at its start, at its last 16 bytes, and with its own last 16 on the start."""
+    with_ = with_ or {}
+    for o in out:
+        for n in nbytes:
+            if n == o:
+                continue
+            for where in (at[n], at[n] + nbytes[n] - 16, at[n] - nbytes[o] + 16):
+                if where == at[n] and (o, n) in allowed:
+                    continue
+                assert call(**{**with_, o: ctypes.c_void_p(where)}) == E, (o, n, hex(where))
+
+
+@pytest.mark.parametrize("io", [0, 1])
+def test_embedding_outputs_apart(lib, io):
+    e, N, V, D = 2 if io else 4, 24, 10, 64
+    size = dict(ids=8 * N, table=e * V * D, out=e * N * D)
+    call, at = _spread(lib.fw_embedding, dict(ids=0, table=0, out=0, N=N, V=V, D=D, scale=1.0, index=1, io=io, st=None), size)
+    _refused(call, at, size, ["out"])
+    need = lib.fw_embedding_backward_workspace_size(N, V, D)
+    size = dict(ids=8 * N, dout=e * N * D, dtable=e * V * D, ws=need)
+    call, at = _spread(lib.fw_embedding_backward, dict(ids=0, dout=0, dtable=0, ws=0, wsb=need, N=N, V=V, D=D, scale=1.0, acc=0,
+                                                       index=1, io=io, st=None), size)
+    for acc in (0, 1):
+        _refused(call, at, size, ["dtable", "ws"], with_=dict(acc=acc))
+
+
+@pytest.mark.parametrize("io", [0, 1])
+def test_layer_norm_outputs_apart(lib, io):
+    e, rows, d = 2 if io else 4, 24, 64
+    row, par = e * rows * d, 4 * d
+    size = dict(x=row, res=row, gamma=par, beta=par, out=row, sum=row)
+    call, at = _spread(lib.fw_layer_norm, dict(x=0, res=0, gamma=0, beta=0, out=0, sum=0, rows=rows, d=d, eps=1e-5, io=io,
+                                               st=None), size)
+    _refused(call, at, size, ["out", "sum"], allowed=[(o, n) for o in ("out", "sum") for n in ("x", "res")])
+    need = lib.fw_layer_norm_backward_workspace_size(rows, d)
+    size = dict(x=row, gamma=par, dout=row, dsum=row, dx=row, dgamma=par, dbeta=par, ws=need)
+    call, at = _spread(lib.fw_layer_norm_backward, dict(x=0, gamma=0, dout=0, dsum=0, dx=0, dgamma=0, dbeta=0, ws=0, wsb=need,
+                                                        rows=rows, d=d, eps=1e-5, io=io, st=None), size)
+    _refused(call, at, size, ["dx", "dgamma", "dbeta", "ws"],
+             allowed=[("dx", n) for n in ("x", "dout", "dsum")] + [("dgamma", "gamma")])
+
+
+@pytest.mark.parametrize("io", [0, 1])
+@pytest.mark.parametrize("N", [3, 24])
+def test_vocab_loss_outputs_apart(lib, io, N):
+    e, V, D = 2 if io else 4, 16, 64
+    given = dict(h=e * N * D, W=e * V * D, bias=4 * V, targets=8 * N)
+    need = lib.fw_vocab_loss_workspace_size(N, V, D, io)
+    size = dict(given, loss=16 * ((4 * N + 15) // 16), lse=16 * ((4 * N + 15) // 16), ws=need)
+    call, at = _spread(lib.fw_vocab_loss, dict(h=0, W=0, bias=0, targets=0, loss=0, lse=0, ws=0, wsb=need, N=N, V=V, D=D, index=1,
+                                               io=io, st=None), size)
+    out = ["loss", "lse", "ws"]
+    if N % 4:  # (what ends between two aligned places has none before its end)
+        size = {n: b for n, b in size.items() if n in ("loss", "lse", "ws", "h", "W")}
+        for o in out:
+            for n in size:
+                if n != o:
+                    assert call(**{o: ctypes.c_void_p(at[n])}) == E, (o, n)
+    else:
+        _refused(call, at, size, out)
+    need = lib.fw_vocab_loss_backward_workspace_size(N, V, D, io)
+    size = dict(given, loss=4 * N, lse=4 * N, dloss=4 * N, dh=e * N * D, dW=e * V * D, dbias=4 * V, ws=need)
+    call, at = _spread(lib.fw_vocab_loss_backward, dict(h=0, W=0, bias=0, targets=0, loss=0, lse=0, dloss=0, dh=0, dW=0, dbias=0,
+                                                        ws=0, wsb=need, N=N, V=V, D=D, index=1, io=io, st=None), size)
+    if N % 4 == 0:
+        _refused(call, at, size, ["dh", "dW", "dbias", "ws"], allowed=[("dbias", "bias")])
+    # without tokens there is nothing to share but the map and its gradient
+    assert call(N=0, dW=ctypes.c_void_p(at["W"])) == E

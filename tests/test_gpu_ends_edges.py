@@ -72,3 +72,58 @@ def test_all_taken_out(N, dtype):
         loss, lse = fw.fw_vocab_loss(h, W, torch.full_like(t, 7), bias=b)
         z = h.double() @ W[7].double() + 1
         assert torch.all(loss == 0) and torch.all((lse - z).abs() < 1e-4)
+
+
+@BOTH
+def test_gradients_in_place(dtype):
+    """What the header allows: dx in place of x, dout or dsum, dgamma of gamma; sum and out of x or the residual."""
+    _, n = draws(31)
+    rows, d = 300, 520
+    x, do, ds = (n(rows, d).to(dtype) for _ in range(3))
+    gamma, beta = n(d), n(d)
+    want = fw.fw_layer_norm_backward(x, gamma, do, dsum=ds)
+    lib, code = fw.load(), fw._dtype_code(dtype)
+    for place in range(3):
+        t = [x.clone(), do.clone(), ds.clone()]
+        g, db = gamma.clone(), torch.empty_like(gamma)
+        ws = torch.empty(fw.fw_layer_norm_backward_workspace_size(rows, d), dtype=torch.uint8, device="cuda")
+        rc = lib.fw_layer_norm_backward(t[0].data_ptr(), g.data_ptr(), t[1].data_ptr(), t[2].data_ptr(), t[place].data_ptr(),
+                                        g.data_ptr(), db.data_ptr(), ws.data_ptr(), ws.numel(), rows, d, 1e-5, code,
+                                        torch.cuda.current_stream().cuda_stream)
+        assert rc == fw.FW_OK
+        assert torch.equal(t[place], want[0]) and torch.equal(g, want[1]) and torch.equal(db, want[2])
+    out, s = fw.fw_layer_norm(x, gamma, beta, residual=do)
+    for swap in (False, True):
+        a, b = x.clone(), do.clone()
+        to = (b, a) if swap else (a, b)
+        fw.fw_layer_norm(a, gamma, beta, residual=b, out=to[0], sum=to[1])
+        assert torch.equal(to[0], out) and torch.equal(to[1], s)
+    for bad in (dict(out=x, sum=x), dict(out=x.view(-1)[d:].view(rows - 1, d))):
+        with pytest.raises((fw.FwError, ValueError)):
+            fw.fw_layer_norm(x, gamma, beta, residual=do, **bad)
+    # a row behind: the next row's values would be gone before they are read
+    both = torch.cat([x, x[:1]])
+    with pytest.raises(fw.FwError):
+        fw.fw_layer_norm(both[:rows], gamma, beta, out=both[1:])
+
+
+@BOTH
+def test_bias_gradient_in_place(dtype):
+    """dbias in place of bias, over several tiles; the other outputs' places are refused."""
+    r, n = draws(32)
+    N, V, D = 130, 700, 64
+    h, W, b, dl = n(N, D).to(dtype), n(V, D).to(dtype), n(V), n(N)
+    t = torch.randint(0, V, (N,), generator=r, device="cuda")
+    loss, lse = fw.fw_vocab_loss(h, W, t, bias=b)
+    dh, dW, db = fw.fw_vocab_loss_backward(h, W, t, loss, lse, dl, bias=b)
+    c, dh2, dW2 = b.clone(), torch.empty_like(h), torch.empty_like(W)
+    ws = torch.empty(fw.fw_vocab_loss_backward_workspace_size(N, V, D, dtype), dtype=torch.uint8, device="cuda")
+    rc = fw.load().fw_vocab_loss_backward(h.data_ptr(), W.data_ptr(), c.data_ptr(), t.data_ptr(), loss.data_ptr(), lse.data_ptr(),
+                                          dl.data_ptr(), dh2.data_ptr(), dW2.data_ptr(), c.data_ptr(), ws.data_ptr(), ws.numel(),
+                                          N, V, D, 1, fw._dtype_code(dtype), torch.cuda.current_stream().cuda_stream)
+    assert rc == fw.FW_OK
+    assert torch.equal(dh2, dh) and torch.equal(dW2, dW) and torch.equal(c, db)
+    with pytest.raises(fw.FwError):
+        fw.fw_vocab_loss(h, W, t, bias=b, loss=loss, lse=loss)
+    with pytest.raises(fw.FwError):
+        fw.fw_embedding_backward(t, h, dtable=h, scale=1.0)
