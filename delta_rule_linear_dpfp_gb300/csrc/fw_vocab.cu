@@ -59,6 +59,10 @@ static_assert(kSmem <= 227 * 1024, "one CTA's shared memory");
 constexpr int kLogitSteps = 8, kFewLogitSteps = 2, kFewTokens = 256;
 // (up to kFewTokens by 128, and w h in two terms: 64 tokens over 50 001 entries, D 1024, 87 us
 // for the gradients instead of 81)
+// Those of an accumulator of the gradients' products: 2^20 terms of one sign in one accumulator
+// fell short by 4.3e-3 of themselves, more than the output's rounding leaves; by 8192 no shortfall
+// is left to be seen (8e-6), at 0 to 0.5 % of the time (8192 x 50 001, D 512: 801 us, 805).
+constexpr int kSumSteps = 128;
 
 enum Mode {
     kLoss,    // h W^T: parts of the logits' log-sum-exp, the targets' logits
@@ -106,7 +110,7 @@ struct Product {
 struct GemmArgs {
     Product of[2];      // (the second: kProducts alone)
     int extra;          // see walk
-    int chunk;          // kLoss, kGrad: steps of an accumulator
+    int chunk;          // steps of an accumulator
     const float *bias;  // kLoss, kGrad: of this piece, or null
     Tokens targets;
     int vocab;          // all of the vocabulary's entries
@@ -384,11 +388,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
         };
         At p;
         for (int i = 0; ok && walk(i, p); ++i) {
-            if (MODE == kProducts)
-                ok = fill(p.k0, p.k1, p.w);
-            else
-                for (int k = p.k0; ok && k < p.k1; k += g.chunk)
-                    ok = fill(k, min(k + g.chunk, p.k1), false);
+            for (int k = p.k0; ok && k < p.k1; k += g.chunk)
+                ok = fill(k, min(k + g.chunk, p.k1), MODE == kProducts && p.w);
         }
         // every read of an accumulator has been told of
         for (uint32_t buf = 0; ok && buf < 2 && buf < it; ++buf)
@@ -548,16 +549,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                             g.colsum[(size_t)(row0 / 32) * g.ldc + col0 + c1 + lane] = columns_sum(z + c1, lane);
                 }
             } else {
-                if (!next_acc(acc))
-                    break;
-                if (!needed) {
-                    done_with_acc();
-                    continue;
-                }
                 float v[kCols];
-                tmem_ld32(acc, v);
-                tmem_ld32(acc + 32, v + 32);
-                done_with_acc();
+                bool ok = true;
+                for (int k = p.k0; k < p.k1; k += g.chunk) {
+                    ok = next_acc(acc);
+                    if (!ok)
+                        break;
+                    if (needed) {
+                        if (k == p.k0) {
+                            tmem_ld32(acc, v);
+                            tmem_ld32(acc + 32, v + 32);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < kCols; j += 16)
+                                add_tmem(acc + j, v + j);
+                        }
+                    }
+                    done_with_acc();
+                }
+                if (!ok)
+                    break;
+                if (!needed)
+                    continue;
                 const CUtensorMap *to = p.w ? &maps1.out : &maps0.out;
                 if (q.out == kWeighted) {
                     const bool there = row < q.N && __ldcg(row_targets + row) >= 0;
@@ -922,6 +935,7 @@ cudaError_t launch_vocab_loss_backward(const void *h, const void *W, const float
             GemmArgs q = {};
             q.row = row;
             q.row_target = row_target;
+            q.chunk = kSumSteps;
             q.of[1].per = 1;
             if (dh) {
                 q.of[0] = product(N, D, (nv + 63) / 64, p.dh.per, 4);

@@ -127,3 +127,57 @@ def test_bias_gradient_in_place(dtype):
         fw.fw_vocab_loss(h, W, t, bias=b, loss=loss, lse=loss)
     with pytest.raises(fw.FwError):
         fw.fw_embedding_backward(t, h, dtable=h, scale=1.0)
+
+
+def room(gigabytes):
+    if torch.cuda.mem_get_info()[0] < gigabytes * 1e9:
+        pytest.skip(f"needs {gigabytes} GB")
+
+
+def uniform(n, d, r):
+    """[n, d] of one sign in bf16, each column with a scale of its own."""
+    scale = 1 + torch.rand(d, generator=r, device="cuda")
+    x = torch.empty(n, d, dtype=torch.bfloat16, device="cuda")
+    for i in range(0, n, 2 ** 17):
+        x[i:i + 2 ** 17] = torch.rand(x[i:i + 2 ** 17].shape, generator=r, device="cuda") * scale
+    return x
+
+
+def column_sums(x):
+    return sum(x[i:i + 2 ** 17].double().sum(0) for i in range(0, len(x), 2 ** 17))
+
+
+def test_long_sums_of_one_sign():
+    """dW over 2^20 tokens and dh over 2^20 entries, all terms of one sign, too many tiles for the contraction to be split.
+    Equal logits make G (2^-10, 2^-20) and w h exact, so that what is off is the sum and the output's own rounding.  Of a
+    sum of 8192 terms at most the tensor core truncates 512 steps by 2^-22 of what there is so far: 2^-14 on average.  A
+    column's rounding is spread over 2^-8 either way, with a deviation of at most 2^-8 / sqrt(3); the mean of D of them
+    is within six of its own."""
+    room(30)
+    r, _ = draws(33)
+    D = 2560
+    lim = 2.0 ** -14 + 6 * 2.0 ** -8 / (3 * D) ** 0.5
+    N, V = 2 ** 20, 1025
+    h, W = uniform(N, D, r), torch.zeros(V, D, dtype=torch.bfloat16, device="cuda")
+    t = torch.zeros(N, dtype=torch.int64, device="cuda")
+    loss, lse = fw.fw_vocab_loss(h, W, t)
+    dl = torch.full((N,), V / (V - 1), device="cuda")
+    dW = fw.fw_vocab_loss_backward(h, W, t, loss, lse, dl, return_dh=False)[1]
+    want = column_sums(h) / (V - 1)
+    off = (dW[1:].double() - want) / want
+    assert abs(float(off[0].mean())) <= lim and float(off.abs().max()) <= 2.0 ** -8 + 2.0 ** -13
+    off = dW[0].double() / (-want * (V - 1)) - 1
+    assert abs(float(off.mean())) <= lim and float(off.abs().max()) <= 2.0 ** -8 + 2.0 ** -13
+    del h, dW
+    N, V = 300, 2 ** 20 + 1
+    h, W = torch.zeros(N, D, dtype=torch.bfloat16, device="cuda"), uniform(V, D, r)
+    W[0] = 0
+    t = torch.zeros(N, dtype=torch.int64, device="cuda")
+    loss, lse = fw.fw_vocab_loss(h, W, t)
+    dh = fw.fw_vocab_loss_backward(h, W, t, loss, lse, torch.ones(N, device="cuda"), return_dW=False)[0]
+    want = column_sums(W) / V
+    off = (dh.double() - want) / want
+    assert torch.equal(dh, dh[:1].expand(N, D))
+    assert abs(float(off[0].mean())) <= lim and float(off.abs().max()) <= 2.0 ** -8 + 2.0 ** -13
+    del W
+    torch.cuda.empty_cache()
