@@ -518,7 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                     if (row < q.N)
                         g.part[(size_t)(col0 / kCols) * q.N + row] = make_float2(total == 0.f ? kNoRef : ref, total);
                 } else {
-                    const float ref = c.x, at_target = c.z, weight = c.w;
+                    const float ref = c.x, at_target = c.z, weight = c.w, weight_off = c.w * c.y;
                     const bool live = target >= 0;
                     free_box();
 #pragma unroll
@@ -533,7 +533,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kT, 1)
                         if (g.colsum)
 #pragma unroll
                             for (int x = 0; x < 8; ++x)
-                                z[j + x] = live ? (tk == j + x ? at_target : e[x]) * weight : 0.f;
+                                z[j + x] = live ? (tk == j + x ? at_target * weight : e[x] * weight_off) : 0.f;
                     }
                     if (tk >= 0 && tk < kCols) // the target's entry
                         *reinterpret_cast<__nv_bfloat16 *>(out + lane * 128 + (((tk >> 3) ^ (lane & 7)) << 4) + 2 * (tk & 7)) =

@@ -43,7 +43,7 @@ cudaError_t launch_few(const void *h, const void *W, const float *bias, Tokens t
                        int N, int V, int D, int bf16, cudaStream_t st);
 cudaError_t launch_join_parts(const float2 *part, const float *target_z, Tokens targets, float *loss, float *lse, int N,
                               int V, int nparts, cudaStream_t st);
-// The tokens' constants (see row_constants; `folded`: row.y into row.x) and targets (-1
+// The tokens' constants (see row_constants; `folded`: log2 q into row.x) and targets (-1
 // for none), and w h in bf16 (or null), with lo_rows in two terms.
 cudaError_t launch_rows(const void *h, Tokens targets, const float *loss, const float *lse, const float *dloss,
                         float4 *row, int *row_target, void *wh, int lo_rows, bool folded, int N, int V, int D, cudaStream_t st);

@@ -215,8 +215,9 @@ __global__ void __launch_bounds__(kJ)
 
 // What a token brings to G and to its row of dh: with q = max(-expm1(-loss), kQMin),
 //   G = 2^(z log2 e - row.x) row.y off the target, row.z on it; q dloss = row.w,
-// all 0 for a token without a gradient.  Folded, row.y is 1: the rounding of row.x
-// (2^-21 of G for a row) is below G's own to bf16.
+// all 0 for a token without a gradient.  Folded, row.x takes in log2 q and row.y is what
+// its rounding is off by, 1 to within 2^-25 |row.x|: left out of what is rounded to
+// bf16 anyway, not of the sums that are kept in 32 bits.
 FW_DEV bool row_constants(const Tokens &targets, const float *loss, const float *lse, const float *dloss, bool folded,
                           int n, int V, float4 &row, int &target) {
     const int t = token_at(targets, n, V);
@@ -226,7 +227,7 @@ FW_DEV bool row_constants(const Tokens &targets, const float *loss, const float 
         return false;
     const float q = -expm1f(-__ldcg(loss + n)), s = __ldcg(lse + n), over = fmaxf(q, kQMin);
     row.x = folded ? fmaf(s, kLog2e, log2f(over)) : reference(s);
-    row.y = folded ? 1.f : ex2(fmaf(-s, kLog2e, row.x)) / over; // (what the reference is off by)
+    row.y = ex2(fmaf(-s, kLog2e, row.x)) / over; // (what the reference is off by)
     row.z = -q / over;
     row.w = over * __ldcg(dloss + n);
     return true;

@@ -181,3 +181,25 @@ def test_long_sums_of_one_sign():
     assert abs(float(off[0].mean())) <= lim and float(off.abs().max()) <= 2.0 ** -8 + 2.0 ** -13
     del W
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("base", [0, 20, 1000, 30000])
+@BOTH
+def test_bias_gradient_of_large_logits(base, dtype):
+    """Logits that are the bias alone, exact at any size: dbias, with the log-sum-exp as it was handed over, is off by the
+    exponent's rounding (2^-21 for entries down to 2^-16 of the sum), the exponential's 2^-22, the constants' few u and the
+    additions', and by the conversion to powers of two: 2^-25 of the distance to the log-sum-exp twice."""
+    N, V, D = 70, 300, 8
+    r, _ = draws(base)
+    b = base + torch.randint(0, 40, (V,), generator=r, device="cuda") / 8
+    h, W = (torch.zeros(n, D, dtype=dtype, device="cuda") for n in (N, V))
+    t = torch.randint(0, V, (N,), generator=r, device="cuda")
+    dl = torch.rand(N, generator=r, device="cuda")
+    loss, lse = fw.fw_vocab_loss(h, W, t, bias=b)
+    db = fw.fw_vocab_loss_backward(h, W, t, loss, lse, dl, bias=b)[2]
+    p = torch.exp(b.double()[None] - lse.double()[:, None])
+    want = (p * dl.double()[:, None]).sum(0)
+    off = torch.ones(V, dtype=torch.bool, device="cuda")
+    off[t] = False
+    rel = ((db.double() - want) / want).abs()[off]
+    assert off.sum() > 200 and float(rel.max()) <= 2.0 ** -21 + 2.0 ** -22 + 2 * 16 * 2.0 ** -25 + 16 * U
