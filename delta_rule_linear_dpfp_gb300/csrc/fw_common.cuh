@@ -127,9 +127,10 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 }
 
 // Give a kernel leave for all of an SM's shared memory (its launches ask for
-// what they need), the whole unified L1 / shared array given to shared
-// memory: once per kernel (`done`: that kernel's own) and device.
-template <typename K> cudaError_t allow_smem(K *kern, std::atomic<uint64_t> &done) {
+// what they need; `bytes`: less, where it has an array of its own besides),
+// the whole unified L1 / shared array given to shared memory: once per kernel
+// (`done`: that kernel's own) and device.
+template <typename K> cudaError_t allow_smem(K *kern, std::atomic<uint64_t> &done, int bytes = 227 * 1024) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
@@ -137,7 +138,7 @@ template <typename K> cudaError_t allow_smem(K *kern, std::atomic<uint64_t> &don
     const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
     if (done.load(std::memory_order_relaxed) & bit)
         return cudaSuccess;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e == cudaSuccess)

@@ -7,7 +7,11 @@
 // by steps of 16 through two stages of shared memory, the next step's values on
 // their way in registers meanwhile.  An operand whose memory runs along the
 // contraction is transposed on its way into shared memory, one that runs along the
-// output is copied.  The softmax's gradient g is kept in fp32, in pieces of the
+// output is copied.  A sum of more than 512 terms goes by chunks of so many, added to
+// totals in shared memory (LONG): one sum over 16 384 equal channels was off by 2.4e-4 of
+// itself, and the gradients at 8192 x 50 001 by 2.8e-6 instead of 4.2e-7; chunks of 256 leave
+// 3.4e-7.  The totals cost 1 % of the gradients' time and 6 % of the loss's (4096 x 20 001,
+// D 1024: 3.06 ms, 3.23).  The softmax's gradient g is kept in fp32, in pieces of the
 // vocabulary; a contraction is split where the tiles are few, and the splits' sums
 // are added in order.
 #include "fw_vocab.h"
@@ -20,6 +24,8 @@ namespace vocab {
 namespace {
 
 constexpr int kT = 256, kTile = 128, kStep = 16, kLd = kTile + 4;
+constexpr int kChunk = 32;               // steps of a chunk
+constexpr int kTotalBytes = kT * 64 * 4; // the chunks' totals, where there are several
 
 enum Mode {
     kLoss, // h W^T: parts of the logits' log-sum-exp, the targets' logits
@@ -90,8 +96,9 @@ FW_DEV float over_row(float x, bool top) { // the maximum or the sum over a row'
     return x;
 }
 
-template <Mode MODE> __global__ void __launch_bounds__(kT, 2) vocab_f32_kernel(Args a) {
+template <Mode MODE, bool LONG> __global__ void __launch_bounds__(kT, 2) vocab_f32_kernel(Args a) {
     __shared__ __align__(16) float As[2][kStep][kLd], Bs[2][kStep][kLd];
+    extern __shared__ float4 total[]; // (LONG) [16][kT]: a thread's own
     griddep_launch_dependents();
     griddep_wait();
     a.A = after_wait(a.A);
@@ -127,31 +134,57 @@ template <Mode MODE> __global__ void __launch_bounds__(kT, 2) vocab_f32_kernel(A
             store_across(Bs[b], vb);
     };
     // sums of rows 4 ty .. + 3 and 64 further, columns 4 tx .. + 3 and 64 further
-    F2 acc[8][4] = {};
+    F2 acc[8][4];
     load(s0);
     store(0);
     __syncthreads();
-    for (int s = s0; s < s1; ++s) {
-        const int b = (s - s0) & 1;
-        if (s + 1 < s1)
-            load(s + 1);
+    int c1;
+    for (int c0 = s0; c0 < s1; c0 = c1) {
+        c1 = LONG ? min(c0 + kChunk, s1) : s1;
 #pragma unroll
-        for (int k = 0; k < kStep; ++k) {
-            const float4 a0 = *reinterpret_cast<const float4 *>(&As[b][k][4 * ty]);
-            const float4 a1 = *reinterpret_cast<const float4 *>(&As[b][k][64 + 4 * ty]);
-            const float4 b0 = *reinterpret_cast<const float4 *>(&Bs[b][k][4 * tx]);
-            const float4 b1 = *reinterpret_cast<const float4 *>(&Bs[b][k][64 + 4 * tx]);
-            const float x[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-            const F2 y[4] = {pack(b0.x, b0.y), pack(b0.z, b0.w), pack(b1.x, b1.y), pack(b1.z, b1.w)};
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int j = 0; j < 4; ++j)
+                acc[i][j] = F2{0};
+        for (int s = c0; s < c1; ++s) {
+            const int b = (s - s0) & 1;
+            if (s + 1 < s1)
+                load(s + 1);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] = fma2(both(x[i]), y[j], acc[i][j]);
+            for (int k = 0; k < kStep; ++k) {
+                const float4 a0 = *reinterpret_cast<const float4 *>(&As[b][k][4 * ty]);
+                const float4 a1 = *reinterpret_cast<const float4 *>(&As[b][k][64 + 4 * ty]);
+                const float4 b0 = *reinterpret_cast<const float4 *>(&Bs[b][k][4 * tx]);
+                const float4 b1 = *reinterpret_cast<const float4 *>(&Bs[b][k][64 + 4 * tx]);
+                const float x[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+                const F2 y[4] = {pack(b0.x, b0.y), pack(b0.z, b0.w), pack(b1.x, b1.y), pack(b1.z, b1.w)};
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        acc[i][j] = fma2(both(x[i]), y[j], acc[i][j]);
+            }
+            if (s + 1 < s1)
+                store(b ^ 1);
+            __syncthreads();
         }
-        if (s + 1 < s1)
-            store(b ^ 1);
-        __syncthreads();
+        if (!LONG || s1 - s0 <= kChunk) // (the one chunk)
+            break;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+                float4 *const p = total + (2 * i + j / 2) * kT + threadIdx.x;
+                if (c0 > s0) {
+                    const float4 t = *p;
+                    acc[i][j] = acc[i][j] + pack(t.x, t.y);
+                    acc[i][j + 1] = acc[i][j + 1] + pack(t.z, t.w);
+                }
+                if (c1 < s1) {
+                    const float2 u = unpack(acc[i][j]), v = unpack(acc[i][j + 1]);
+                    *p = make_float4(u.x, u.y, v.x, v.y);
+                }
+            }
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -302,7 +335,12 @@ Plan plan_of(int N, int V, int D) {
 template <Mode MODE> cudaError_t launch(Args a, int splits, cudaStream_t st) {
     a.mt = tiles_of(a.M);
     a.nt = tiles_of(a.N);
-    return launch_pdl(vocab_f32_kernel<MODE>, dim3((unsigned)((int64_t)a.mt * a.nt * splits)), dim3(kT), 0, st, a);
+    const dim3 grid((unsigned)((int64_t)a.mt * a.nt * splits));
+    if (a.per <= kChunk)
+        return launch_pdl(vocab_f32_kernel<MODE, false>, grid, dim3(kT), 0, st, a);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(vocab_f32_kernel<MODE, true>, done, kTotalBytes);
+    return e != cudaSuccess ? e : launch_pdl(vocab_f32_kernel<MODE, true>, grid, dim3(kT), kTotalBytes, st, a);
 }
 
 cudaError_t join(const float *part, float *out, int64_t values, int splits, int64_t a_split, int add, cudaStream_t st) {

@@ -203,3 +203,43 @@ def test_bias_gradient_of_large_logits(base, dtype):
     off[t] = False
     rel = ((db.double() - want) / want).abs()[off]
     assert off.sum() > 200 and float(rel.max()) <= 2.0 ** -21 + 2.0 ** -22 + 2 * 16 * 2.0 ** -25 + 16 * U
+
+
+@pytest.mark.parametrize("N", [1, 70])
+@pytest.mark.parametrize("D", [504, 512, 520, 1024, 16384, 65536])
+def test_fp32_sums_of_equal_terms(N, D):
+    """Logits that are sums of D equal terms, whose roundings all go one way: chunks of 512, then the chunks', each addition
+    off by u of the sum so far at most.  (One token of up to 11264 channels: a lane's channels in two sums, then the lanes'.)"""
+    V = 130
+    r, _ = draws(D)
+    c = (1 + torch.rand(V, generator=r, device="cuda")) * 8 / D
+    W, h = c[:, None].expand(V, D).contiguous(), torch.ones(N, D, device="cuda")
+    t = torch.arange(N, device="cuda")
+    loss, lse = fw.fw_vocab_loss(h, W, t)
+    z = W.double().sum(1)
+    want = z.logsumexp(0)
+    lim = (min(D, 512) + D / 512 + 8) * U * 16 + 2.0 ** -18
+    assert float((lse - want).abs().max()) <= lim and float((loss - (want - z[t])).abs().max()) <= 2 * lim
+
+
+def test_fp32_gradients_of_equal_terms():
+    """The same of the products with g (2^-11 and the like for every entry but the target), not split."""
+    r, _ = draws(34)
+    for N, V, D in ((20000, 2049, 2560), (2560, 20001, 2560)):
+        c = 1 + torch.rand(D, generator=r, device="cuda")
+        h, W = c[None].expand(N, D).contiguous(), torch.zeros(V, D, device="cuda")
+        t = torch.zeros(N, dtype=torch.int64, device="cuda")
+        bias = torch.zeros(V, device="cuda")
+        if V > N:  # for dh: the logits are equal all the same
+            h, W = torch.zeros_like(h), c[None].expand(V, D).contiguous()
+            W[0] = 0
+        loss, lse = fw.fw_vocab_loss(h, W, t, bias=bias)
+        dh, dW, _ = fw.fw_vocab_loss_backward(h, W, t, loss, lse, torch.ones(N, device="cuda"), bias=bias)
+        n = max(N, V)
+        lim = (512 + n / 512 + 8) * U + 2.0 ** -18  # (g: the logarithm's and the exponential's)
+        if V > N:
+            want = c.double() * (V - 1) / V
+            assert float((dh.double() / want - 1).abs().max()) <= lim
+        else:
+            want = c.double() * N / V
+            assert float((dW[1:].double() / want - 1).abs().max()) <= lim
