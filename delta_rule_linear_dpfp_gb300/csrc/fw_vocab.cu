@@ -27,7 +27,8 @@
 // is exactly -1 at the target, and w h, element by element: errors that are as
 // independent as those of the rounded outputs.  Rounding (p - 1) dloss itself
 // would put one relative error of up to 2^-8 into a whole row of dh and dW.  Up to
-// 256 tokens, whose contraction is short, w h goes in as two terms (2^-16 of it left).
+// 256 tokens, whose contraction is short, and for small vocabularies (second_terms)
+// w h goes in as two terms (2^-16 of it left).
 #include <cuda.h>
 
 #include <algorithm>
@@ -59,6 +60,12 @@ static_assert(kSmem <= 227 * 1024, "one CTA's shared memory");
 constexpr int kLogitSteps = 8, kFewLogitSteps = 2, kFewTokens = 256;
 // (up to kFewTokens by 128, and w h in two terms: 64 tokens over 50 001 entries, D 1024, 87 us
 // for the gradients instead of 81)
+// w h in two terms beyond that as well where the entries fit one tile and h has no more values
+// than this: a row of dW is then the sum of many tokens', whose roundings come on top of its own
+// (2048 x 65, D 512: dW off by 1.7e-3 of itself instead of 2.4e-3, 18.3 us -> 19.9; at the limit,
+// 4096 x 65, D 1024, 30.2 -> 30.7; twice as many values 37.0 -> 41.1).  Over more entries a row
+// has fewer tokens (1024 x 1000: 1.95e-3, 2048 x 8000: 1.67e-3), and the term costs up to a third.
+constexpr int64_t kSecondValues = 1 << 22;
 // Those of an accumulator of the gradients' products: 2^20 terms of one sign in one accumulator
 // fell short by 4.3e-3 of themselves, more than the output's rounding leaves; by 8192 no shortfall
 // is left to be seen (8e-6), at 0 to 0.5 % of the time (8192 x 50 001, D 512: 801 us, 805).
@@ -725,6 +732,10 @@ Splits splits_of(int64_t tiles, int kb) {
     return {(kb + per - 1) / per, per};
 }
 
+// Whether w h goes into dW's product in two terms.
+bool second_terms(int N, int V, int D) {
+    return N <= kFewTokens || (V <= kTile && (int64_t)N * D <= kSecondValues);
+}
 struct Plan {
     int width;      // vocabulary entries of a piece (a multiple of 256)
     int ldg;        // row stride of G
@@ -743,8 +754,10 @@ Plan plan_of(int N, int V, int D) {
     p.pieces = (V + p.width - 1) / p.width;
     p.dh = splits_of((int64_t)tiles_of(N) * kt, (std::min(p.width, V) + 63) / 64);
     const int kn = (N + 63) / 64;
-    p.lo_rows = N <= kFewTokens ? 64 * kn : 0;
-    p.dw = splits_of((int64_t)(p.width / kTile) * kt, p.lo_rows ? 2 * kn : kn);
+    p.lo_rows = second_terms(N, V, D) ? 64 * kn : 0;
+    p.dw = splits_of((int64_t)(p.width / kTile) * kt, kn);
+    if (p.lo_rows)
+        p.dw.per *= 2;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t o = at;

@@ -243,3 +243,29 @@ def test_fp32_gradients_of_equal_terms():
         else:
             want = c.double() * N / V
             assert float((dW[1:].double() / want - 1).abs().max()) <= lim
+
+
+@pytest.mark.parametrize("N, V, D", [(2, 129, 8), (64, 129, 64), (130, 1025, 72), (256, 4097, 64), (258, 129, 512),
+                                     (2048, 65, 512), (8192, 129, 512)], ids=str)
+def test_second_terms_of_the_answers(N, V, D):
+    """Pairs of tokens with the same answer and weights of opposite sign, 2^-12 apart: dW is 2^-12 of either's part, which one
+    rounding of w h to bf16 (2^-8 of it) would lose.  Equal logits make G exact (1 / (V - 1), and -1 for the target).  Two
+    terms leave 2^-16 of each token's part; w itself is off by 4 u, the sums by two steps of 2^-22 of the parts so far."""
+    r, n = draws(N)
+    half = n(N // 2, D).bfloat16()
+    half[16:] = 0  # (and the sum of 32 tokens' parts at most: zeros leave it as it is)
+    h = torch.stack([half, half], 1).view(N, D)
+    W = torch.zeros(V, D, dtype=torch.bfloat16, device="cuda")
+    t = torch.zeros(N, dtype=torch.int64, device="cuda")
+    up = V / (V - 1)
+    dl = torch.tensor([(1 + 2.0 ** -12) * up, -up], device="cuda").repeat(N // 2)
+    loss, lse = fw.fw_vocab_loss(h, W, t)
+    dW = fw.fw_vocab_loss_backward(h, W, t, loss, lse, dl, return_dh=False)[1]
+    w = dl.double() / up
+    want = (w[:, None] * h.double()).sum(0)
+    size = h.double().abs().sum(0)
+    lim = (2.0 ** -16 + 4 * U) * size + 2 * 2.0 ** -22 * size + 2.0 ** -8 * want.abs()
+    assert torch.all((dW[1:].double() * (V - 1) - want).abs() <= lim)
+    assert torch.all((dW[0].double() + want).abs() <= lim)
+    if N == 2:
+        assert float(want.abs().max()) > 4 * float(lim.max())
