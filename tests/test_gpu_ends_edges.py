@@ -269,3 +269,20 @@ def test_second_terms_of_the_answers(N, V, D):
     assert torch.all((dW[0].double() + want).abs() <= lim)
     if N == 2:
         assert float(want.abs().max()) > 4 * float(lim.max())
+
+
+@pytest.mark.parametrize("N, most", [(64, 128), (600, 512)])
+def test_logits_of_one_sign(N, most):
+    """Logits of 32 768 products of one sign: an accumulator takes 128 channels (up to 256 tokens) or 512, whose steps of 16
+    truncate at most 2^-22 of the sum so far each, and the accumulators are added with roundings of u each.  One accumulator
+    for all channels would fall short by 2048 steps of 2^-24 of half the sum, which is past the bound."""
+    V, D = 300, 32768
+    r, _ = draws(N)
+    h, W = uniform(N, D, r), (uniform(V, D, r).float() * 2.0 ** -6).bfloat16()
+    t = torch.randint(0, V, (N,), generator=r, device="cuda")
+    loss, lse = fw.fw_vocab_loss(h, W, t)
+    z = h.double() @ W.double().T
+    want = z.logsumexp(1)
+    lim = (most / 16 / 2 * 2.0 ** -22 + D / most * U) * z.max(1).values + 2.0 ** -18 * 10 + 2 * U * want
+    assert 2.0 * float(lim.max()) < 2048 / 2 * 2.0 ** -24 * float(z.max())
+    assert torch.all((lse - want).abs() <= lim)
