@@ -286,3 +286,131 @@ def test_logits_of_one_sign(N, most):
     lim = (most / 16 / 2 * 2.0 ** -22 + D / most * U) * z.max(1).values + 2.0 ** -18 * 10 + 2 * U * want
     assert 2.0 * float(lim.max()) < 2048 / 2 * 2.0 ** -24 * float(z.max())
     assert torch.all((lse - want).abs() <= lim)
+
+
+# ------------------------------------------------------- calls of other kinds
+@pytest.mark.parametrize("N", [1, 4, 5, 300])
+@BOTH
+def test_nothing_but_padding(N, dtype):
+    _, n = draws(N)
+    V, D = 200, 64
+    h, W, b = torch.full((N, D), float("nan"), device="cuda").to(dtype), n(V, D).to(dtype), n(V)
+    t = torch.full((N,), -1, dtype=torch.int32, device="cuda")
+    loss, lse = fw.fw_vocab_loss(h, W, t, bias=b)
+    assert torch.all(loss == 0) and torch.all(lse == 0)
+    nan = torch.full((N,), float("nan"), device="cuda")
+    for x in fw.fw_vocab_loss_backward(h, W, t, loss, lse, nan, bias=b):
+        assert torch.all(x == 0)
+    assert torch.all(fw.fw_embedding(t, W) == 0) and torch.all(fw.fw_embedding_backward(t, h, V) == 0)
+
+
+@pytest.mark.parametrize("index", [torch.int32, torch.int64])
+@BOTH
+def test_slices_of_a_batch_of_tokens(index, dtype):
+    """Ids and targets are read one at a time: a batch's sequence shifted by one is an argument as it is."""
+    r, n = draws(41)
+    V, D = 70, 32
+    W = n(V, D).to(dtype)
+    ids = torch.randint(-1, V, (91,), generator=r, device="cuda", dtype=index)
+    h, dl = n(90, D).to(dtype), n(90)
+    for a, b in ((ids[:90], ids[1:]), (ids[1:], ids[:90])):
+        x, e = fw.fw_embedding(a, W), fw.fw_embedding(a.clone(), W)
+        assert torch.equal(x, e)
+        assert torch.equal(fw.fw_embedding_backward(a, h, V), fw.fw_embedding_backward(a.clone(), h, V))
+        got, want = fw.fw_vocab_loss(h, W, b), fw.fw_vocab_loss(h, W, b.clone())
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        got = fw.fw_vocab_loss_backward(h, W, b, *want, dl)
+        want = fw.fw_vocab_loss_backward(h, W, b.clone(), *want, dl)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("N, V", [(1, 9), (3, 300), (40, 70)])
+@BOTH
+def test_the_widest(N, V, dtype):
+    """D 65536 in every call; errors as sums of D, N or V products (the bounds of test_gpu_ends.py, in the 2-norm)."""
+    r, n = draws(N)
+    D = 65536
+    W, h = (n(V, D) * D ** -0.5).to(dtype), n(N, D).to(dtype)
+    t, dl = torch.randint(0, V, (N,), generator=r, device="cuda"), n(N)
+    loss, lse = fw.fw_vocab_loss(h, W, t)
+    z = h.double() @ W.double().T
+    want = z.logsumexp(1)
+    S = (h.double().abs() @ W.double().abs().T).max()
+    lim = 520 * U * S + 2.0 ** -18 * (1 + want.abs().max())
+    assert torch.all((lse - want).abs() <= lim)
+    assert torch.all((loss - (want - z.gather(1, t[:, None])[:, 0])).abs() <= 2 * lim)
+    dh, dW, _ = fw.fw_vocab_loss_backward(h, W, t, loss, lse, dl)
+    g = torch.softmax(z, 1)
+    g[torch.arange(N, device="cuda"), t] -= 1
+    g *= dl.double()[:, None]
+    tol = 3 * 2.0 ** -8 if dtype == torch.bfloat16 else float(2 * lim)
+    for x, w in ((dh, g @ W.double()), (dW, g.T @ h.double())):
+        assert float((x.double() - w).norm()) <= tol * float(w.norm())
+    out = fw.fw_embedding(t, W, scale=2.0)
+    assert torch.equal(out, 2 * W[t])
+    dE = fw.fw_embedding_backward(t, h, V)
+    w = torch.zeros(V, D, dtype=torch.float64, device="cuda").index_add_(0, t, h.double())
+    assert torch.all((dE.double() - w).abs() <= (2.0 ** -8 if dtype == torch.bfloat16 else 0) * w.abs() + 40 * U * 40)
+
+
+def test_one_workspace_of_two_graphs():
+    """Two captured steps of different sizes on one workspace, replayed in turn, with new inputs in the same places."""
+    r, n = draws(42)
+    sizes = ((600, 700, 512), (33, 3000, 64))
+    need = max(max(fw.fw_vocab_loss_backward_workspace_size(*s), fw.fw_vocab_loss_workspace_size(*s),
+                   fw.fw_embedding_backward_workspace_size(*s), fw.fw_layer_norm_backward_workspace_size(s[0], s[2]))
+               for s in sizes)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def step(h, W, t, dl, w):
+        loss, lse = fw.fw_vocab_loss(h, W, t, workspace=w)
+        dh, dW, _ = fw.fw_vocab_loss_backward(h, W, t, loss, lse, dl, workspace=w)
+        dx, dg, db = fw.fw_layer_norm_backward(h, None, dh, workspace=w)
+        fw.fw_embedding_backward(t, dx, dtable=dW, accumulate=True, workspace=w)
+        return loss, lse, dh, dW, dx, dg, db
+
+    def fresh(N, V, D):
+        return n(N, D).bfloat16(), (n(V, D) * D ** -0.5).bfloat16(), torch.randint(-1, V, (N,), generator=r, device="cuda"), n(N)
+
+    ins = [fresh(*s) for s in sizes]
+    graphs, kept = [], []
+    for i in ins:
+        step(*i, ws)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            kept.append(step(*i, ws))
+    for turn in range(3):
+        for s, i in zip(sizes, ins):
+            for a, b in zip(i, fresh(*s)):
+                a.copy_(b)
+        for k in kept:
+            for x in k:
+                x.fill_(float("nan"))
+        ws.fill_(255)
+        for g in (graphs if turn % 2 else graphs[::-1]):
+            g.replay()
+        want = [step(*i, None) for i in ins]
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for k, w in zip(kept, want) for x, y in zip(k, w))
+
+
+@pytest.mark.parametrize("d", [8, 4104, 8192])
+@BOTH
+def test_more_rows_than_threads_of_rows(d, dtype):
+    """Every group of threads walks many rows, the last walk ragged; gradients against the 64-bit formula in the 2-norm."""
+    _, n = draws(d)
+    rows = 2 ** 22 // d + 77
+    x, do = (n(rows, d) + 0.5).to(dtype), n(rows, d).to(dtype)
+    gamma = 1 + 0.1 * n(d)
+    dx, dg, db = fw.fw_layer_norm_backward(x, gamma, do, dsum=do)
+    a, g = x.double(), do.double() * gamma.double()
+    c = a - a.mean(-1, keepdim=True)
+    r1 = torch.rsqrt((c * c).mean(-1, keepdim=True) + 1e-5)
+    m = c * r1
+    want = r1 * (g - g.mean(-1, keepdim=True) - m * (g * m).mean(-1, keepdim=True)) + do.double()
+    rel = lambda p, q: float((p.double() - q).norm() / q.norm())  # noqa: E731
+    half = 2.0 ** -8 if dtype == torch.bfloat16 else 0.0
+    assert rel(dx, want) <= half + 2.0 ** -18
+    assert rel(dg, (do.double() * m).sum(0)) <= 2.0 ** -15 and rel(db, do.double().sum(0)) <= 2.0 ** -15
+    out = fw.fw_layer_norm(x, gamma)
+    assert rel(out, m * gamma.double()) <= half + 2.0 ** -18
