@@ -785,8 +785,8 @@ def fw_embedding_backward_workspace_size(N, V, D) -> int:
 
 def fw_embedding_backward(ids, dout, V: int = None, scale: float = 1.0, dtable=None, accumulate: bool = False,
                           workspace=None, stream=None):
-    """The table's gradient [V,D] from dout [*ids.shape, D], summed in the
-    tokens' order; with accumulate it is added to dtable (in place)."""
+    """The table's gradient [V,D] from dout [*ids.shape, D], summed in an
+    order that the ids fix; with accumulate it is added to dtable (in place)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return fw_embedding_backward(ids, dout, V, scale, dtable, accumulate, workspace)

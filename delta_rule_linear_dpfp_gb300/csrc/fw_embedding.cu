@@ -8,8 +8,8 @@
 // Bound by the bytes: each row that is named is read once for every time it is
 // named (from L2 where it is named often), each row of the output written once.
 //
-// The gradient goes by sorted tokens, so that every row is summed in the order
-// of the tokens (no atomics, the same bits in every run), in three kernels:
+// The gradient goes by sorted tokens, so that every row is summed in an order that
+// depends on the ids alone (no atomics, the same bits in every run), in three kernels:
 //  1. One cluster of eight CTAs sorts the pairs (id, n) by id, eight bits at
 //     a time from the lowest, each pass stable.  A CTA owns an eighth of the
 //     sequence; the counts of the digits are exchanged through distributed
@@ -20,7 +20,9 @@
 //     a run that ends on both sides is rounded and written, one that goes on
 //     beyond leaves its sum in 32 bits.  Every group reads as many rows as any
 //     other, whatever a token's share of the batch is.
-//  3. The group in which such a run begins adds its parts in order.
+//  3. A CTA for each such run adds its parts, its groups of threads taking them
+//     in turn, the groups' sums in order.  (One CTA even where one token is the whole
+//     batch: 65 536 of D 1024 take 214 us instead of 91.)
 #include "fw_common.cuh"
 #include "fw_ends.h"
 #include "fw_pairs.cuh"
@@ -436,7 +438,8 @@ cudaError_t lookup(Tokens ids, const void *table, void *out, int64_t N, int V, i
 }
 
 // Pairs of a chunk: fewer where the chunks are too few to occupy the SMs otherwise
-// (16384 x 1024: 31.9 us with 32, 32.6 with 16, 36.6 with 8, whose open runs leave more sums).
+// (16384 x 1024: 31.9 us with 32, 32.6 with 16, 36.6 with 8, whose open runs leave more sums;
+// 65 rows of D 512: 2048 tokens 10.8 us with 8, 12.7 with 32, 4096 12.3 and 12.9, 8192 16.7 and 14.6).
 int chunk_log2(int N) { return N <= 8192 ? 3 : 5; }
 int64_t chunks_of(int N) { return ((int64_t)N + (1 << chunk_log2(N)) - 1) >> chunk_log2(N); }
 
@@ -477,7 +480,9 @@ cudaError_t launch_embedding_backward(Tokens ids, const void *dout, void *dtable
         a.pair[i] = reinterpret_cast<int2 *>(p);
         p += up256(8 * (size_t)N);
     }
-    // the table's zeros: within the sort, or from a megabyte on beside it
+    // the table's zeros: within the sort, or above a megabyte beside it (4096 tokens of D 512:
+    // a table of a quarter of a megabyte 15.0 us within, 15.3 beside, half 15.6 and 15.5, one 16.7 and 15.6,
+    // four 26 and 15.6)
     uint4 *zeros = static_cast<uint4 *>(dtable);
     const int64_t nzeros = accumulate ? 0 : (int64_t)V * D / (bf16 ? 8 : 4);
     const bool beside = nzeros > 1 << 16;

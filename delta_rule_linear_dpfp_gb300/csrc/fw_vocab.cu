@@ -14,12 +14,12 @@
 // steps of 64 of the contraction, each CTA fetching half of A's rows and half of
 // B's, and one thread of the pair issues the MMAs (tcgen05, cta_group::2, fp32
 // accumulators in both CTAs' TMEM, 128 rows each).  A tile's accumulator takes
-// half of TMEM, so the epilogue of one tile (8 warps, 128 columns of a row per
-// thread) runs while the next is formed.
+// half of TMEM, so the epilogue of one tile (16 warps in either CTA, 64 columns of
+// a row per thread) runs while the next is formed.
 //
-// Forward: the epilogue turns a row's 128 columns into (max, sum of
-// exponentials) and picks out the target's logit; a second kernel joins a
-// token's parts.  Backward, by pieces of the vocabulary of at most 1 GB of
+// Forward: the epilogue turns a row's 64 columns into (reference, sum of
+// 2^(z log2 e - reference)), the target's entry left out, and writes the target's
+// logit apart; a second kernel joins a token's parts.  Backward, by pieces of the vocabulary of at most 1 GB of
 // (bf16) g: one product forms the logits again and its epilogue writes
 //   G = (exp(z - lse) - [v = t]) / q,   q = 1 - p_t = -expm1(-loss),
 // then dh += G W and dW = G^T (w h) with w = q dloss (dh's rows take w at the
@@ -55,8 +55,9 @@ constexpr int kBarOff = kOutOff + kOutBytes;
 constexpr int kSmem = kBarOff + 256 + 1024;
 static_assert(kSmem <= 227 * 1024, "one CTA's shared memory");
 // Steps of 64 that an accumulator of logits takes: the tensor core truncates what it
-// adds, so that a sum of many terms of one sign falls short by about 2^-25 of itself with
-// every step of 16; chunks of 512 are added in the epilogue, where sums are rounded.
+// adds, so that a sum of many terms of one sign falls short (1024 terms in one accumulator:
+// by 1.6e-6 of itself, 32 768: by 1.6e-4).  Chunks of 512, which leave 7e-7 at any width, are
+// added in the epilogue, where sums are rounded; of 128 1.5e-7.
 constexpr int kLogitSteps = 8, kFewLogitSteps = 2, kFewTokens = 256;
 // (up to kFewTokens by 128, and w h in two terms: 64 tokens over 50 001 entries, D 1024, 87 us
 // for the gradients instead of 81)
@@ -720,8 +721,10 @@ __global__ void __launch_bounds__(kS) rest_kernel(RestArgs a) {
 int tiles_of(int64_t n) { return (int)((n + kTile - 1) / kTile); }
 
 // Splits of a contraction of kb steps for an output of `tiles`: where the
-// tiles occupy fewer than a quarter of the pairs, as many as fill them, of four
-// steps at least.
+// tiles occupy no more than a quarter of the pairs, as many as fill them, of four
+// steps at least.  (16 tiles, gradients of 2048 x 8000 at D 512: 52 us, not split 61; of
+// 4096 x 32 000 at D 256: 186, 236.  Splits of few steps cost more in sums than they gain:
+// 2048 x 2500 at D 512 37 us, not split 30; 1024 x 1000 at D 1024 30.5, 22.4.)
 struct Splits {
     int n, per;
 };

@@ -149,7 +149,10 @@ __global__ void __launch_bounds__(kFewT, few_an_sm(NT))
 constexpr int kS = 256;
 
 // A token's parts joined: 32 tokens of a CTA and 32 threads for each, or one
-// token and 1024 where there are few.
+// token and 1024 where there are few (the loss of 128 tokens over 32 000 entries, D 256:
+// 12.6 us by one, 13.5 by 32; of 512 18.8 and 16.8, over 8000, D 512, 14.1 and 10.5;
+// below 512 the parts of a small vocabulary are joined sooner by 32, too: 128 over 8000
+// 11.1 and 10.3).
 constexpr int kJ = 1024;
 __global__ void __launch_bounds__(kJ)
     join_parts_kernel(const float2 *part, const float *target_z, Tokens targets, float *loss, float *lse, int N, int V,

@@ -567,19 +567,21 @@ FW_API int fw_group_norm_act_backward(const void *x, const void *gate, const flo
  * norm, the residual sums), and its training experiment (an embedding, the
  * stack, a linear output map, the cross entropy over the characters)]
  *
- * Tokens (ids, targets) are int32 or int64, aligned to their own size.  A NEGATIVE token is padding: its
- * row of the embedding is zero, its loss and lse are 0, and it has no part in
- * any gradient, whatever its rows of h, dout and dloss hold (NaN as well).  A
- * token at or past V is an error that cannot be seen on the host: its row of
- * the embedding and its loss are NaN, and it has no part in any gradient.
+ * Tokens (ids, targets) are int32 or int64, aligned to their own size.  A
+ * NEGATIVE token is padding: its row of the embedding is zero, its loss and lse
+ * are 0, and it has no part in any gradient, whatever its rows of h, dout and
+ * dloss hold (NaN as well).  A token at or past V is an error that cannot be
+ * seen on the host: its row of the embedding and its loss are NaN, and it has
+ * no part in any gradient.
  *
  * D is a multiple of 8 (FW_ERR_UNSUPPORTED otherwise), up to 65536; the layer
  * norm's d up to 8192.  Calls return FW_ERR_INVALID_ARG for null or misaligned
  * pointers, bad sizes, a scale or eps that is not finite, eps < 0, a small
  * workspace, and for an output or workspace that shares memory with anything
- * else of the call, where it does not say that it may.  No call uses state of the library, so calls with workspaces of
- * their own may run at the same time.  Results do not depend on the run (fixed
- * summation orders, no atomics on values).
+ * else of the call, where it does not say that it may.  No call uses state of
+ * the library, so calls with workspaces of their own may run at the same time.
+ * Results do not depend on the run (fixed summation orders, no atomics on
+ * values).
  */
 typedef enum fw_index {
     FW_INDEX_I32 = 0,
@@ -600,9 +602,11 @@ FW_API size_t fw_embedding_backward_workspace_size(int64_t N, int V, int D);
 
 /*
  * fw_embedding_backward -- dtable[v] = scale (the sum of dout_n over the n
- * with ids_n = v, in 32 bits, in the order of n), rounded once; with
- * accumulate 1 that is added to what dtable holds (an output map that shares
- * the table: its own gradient), and rows without a token are left as they are.
+ * with ids_n = v, in 32 bits), rounded once; with accumulate 1 that is added to
+ * what dtable holds (an output map that shares the table: its own gradient),
+ * and rows without a token are left as they are.  The order of a sum depends on
+ * the ids and the sizes alone: n's order within a few tokens, and then that of
+ * these parts, several of which may be added side by side.
  *   dout   : [N, D]  io_dtype
  *   dtable : [V, D]  io_dtype   (written; read and written with accumulate)
  */
@@ -650,23 +654,30 @@ FW_API size_t fw_vocab_loss_workspace_size(int N, int V, int D, int io_dtype);
  *   W       : [V, D]  io_dtype (an embedding's table, for one)
  *   bias    : [V]     fp32, or NULL; -infinity, or any number that leaves the
  *             logit below -2^30, takes an entry out of the vocabulary (its
- *             gradient is zero; its row of W is finite, as any other)
+ *             gradient is zero, but where it is a token's target: that token's
+ *             loss is what it is below the others, infinite for -infinity, and
+ *             pulls on it as any other; its row of W is finite all the same).
+ *             Other logits are below 2^30 in size
  *   targets : [N]     fw_index
  *   loss, lse : [N]   fp32     (written)
- * bf16: products summed in fp32 on the tensor cores, by 512 channels (up to four
- * tokens: on CUDA cores), everything after them in fp32.  fp32: fp32 arithmetic
- * throughout, on CUDA cores.  Any V; a token whose entries are all taken out has
- * a NaN loss.
+ * bf16: products summed in fp32 on the tensor cores, by 512 channels (up to 256
+ * tokens by 128; up to four: on CUDA cores), everything after them in fp32.
+ * fp32: fp32 arithmetic throughout, on CUDA cores, by 512 channels.  Any V; a
+ * token whose entries are all taken out has a NaN loss.
  */
 FW_API int fw_vocab_loss(const void *h, const void *W, const float *bias, const void *targets, float *loss, float *lse,
                          void *workspace, size_t workspace_bytes, int N, int V, int D, int index_type, int io_dtype,
                          void *stream);
 
 /*
- * bf16: 2 N (V + D) bytes, fp32: 4 N V; a large vocabulary is worked off in pieces
- * for which that is 1 GB.  Beside it fp32 sums of dh (4 N D bytes and more where
- * there are several pieces, or where a product is split) and of dbias (a
- * sixteenth, or an eighth, of the piece).
+ * The softmax's gradient, 2 N V bytes with bf16 and 4 N V with fp32 tensors, in
+ * pieces of the vocabulary of 1 GB where it is larger than that.  Beside it: with
+ * bf16 the weighted answers, 2 N D bytes, or twice that (of N rounded up to a
+ * multiple of 64) where they go in as two terms; fp32 sums of dh, 4 N D bytes a
+ * split (N up to a multiple of 256 with bf16), where there are several pieces or
+ * its product is split, and of dW, 4 V D a split, where that one is (small outputs
+ * alone: at most 20 MB either); those of dbias, N V / 8 bytes for the V of a piece;
+ * 20 N.
  */
 FW_API size_t fw_vocab_loss_backward_workspace_size(int N, int V, int D, int io_dtype);
 
@@ -678,9 +689,11 @@ FW_API size_t fw_vocab_loss_backward_workspace_size(int N, int V, int D, int io_
  *               written, or NULL to skip it; dbias may be bias (in place)
  * The logits are formed again.  bf16: the softmax's gradient is rounded on its
  * way into the products with W and h, relative to 1 - exp(-loss) so that the
- * target's entry is exact, and h times that and dloss once more: dh and dW are
- * off by about what rounding them to bf16 alone costs.  dbias, and everything
- * with fp32 tensors, is in fp32 throughout.
+ * target's entry is exact, and h times that and dloss once more (up to 256
+ * tokens, and over at most 256 entries while N D <= 2^22, in two terms): dh and
+ * dW are off by 1 to 1.4 times what rounding them to bf16 alone costs, whatever N
+ * and V are (an accumulator of the tensor cores takes 8192 terms at most).  dbias,
+ * and everything with fp32 tensors, is in fp32 behind the logits.
  */
 FW_API int fw_vocab_loss_backward(const void *h, const void *W, const float *bias, const void *targets,
                                   const float *loss, const float *lse, const float *dloss, void *dh, void *dW,
