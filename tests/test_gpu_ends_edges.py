@@ -414,3 +414,53 @@ def test_more_rows_than_threads_of_rows(d, dtype):
     assert rel(dg, (do.double() * m).sum(0)) <= 2.0 ** -15 and rel(db, do.double().sum(0)) <= 2.0 ** -15
     out = fw.fw_layer_norm(x, gamma)
     assert rel(out, m * gamma.double()) <= half + 2.0 ** -18
+
+
+@pytest.mark.parametrize("base", [1e4, 1e6, 5e8, 1.07e9, -1e6, -1.07e9])
+@pytest.mark.parametrize("N", [3, 70])
+@BOTH
+def test_the_loss_of_large_logits(base, N, dtype):
+    """Logits that are the bias alone, up to 2^30 in size: the losses are those of their differences, which are exact.  The
+    exponents take one rounding, of the few units that the differences are, and a reference's own, up to 2^6, is in both
+    terms of the quotient; lse is as its own size allows."""
+    V, D = 300, 8
+    r, _ = draws(N)
+    step = max(2.0 ** -4, 2.0 ** (np.floor(np.log2(abs(base))) - 23))   # of fp32 at that size
+    b = base + torch.randint(0, 60, (V,), generator=r, device="cuda") * step
+    h, W = (torch.zeros(n, D, dtype=dtype, device="cuda") for n in (N, V))
+    t = torch.randint(0, V, (N,), generator=r, device="cuda")
+    loss, lse = fw.fw_vocab_loss(h, W, t, bias=b)
+    z = b.double()
+    want = z.logsumexp(0) - z[t]
+    span = float(z.max() - z.min())
+    # (the constant of the conversion is off by 2^-26 of a difference, an exponent rounded by 2^-24 of it)
+    lim = 2.0 ** -18 * (1 + want) + 2.0 ** -22 * span
+    assert torch.all((loss - want).abs() <= lim)
+    assert torch.all((lse - z.logsumexp(0)).abs() <= 4 * U * abs(base) + 2.0 ** -18 * 10 + lim)
+
+
+@pytest.mark.parametrize("N, V, D", [(2500, 9001, 520), (300, 33000, 64), (20000, 300, 128), (9000, 60001, 64), (2048, 65, 512),
+                                     (4096, 250, 1024)], ids=str)
+@BOTH
+def test_large_gradients_to_the_last_rounding(N, V, D, dtype):
+    """In the 2-norm.  bf16: an element's rounding is spread over 2^-8 of it either way at most, with a deviation of
+    2^-8 / sqrt(3); an output has its own, G's and that of w h (none of the latter in two terms), which are independent:
+    2^-8 in all, 2^-8 sqrt(2/3) without it, and 2^-12 beside them for the sums and the logits.  fp32: a sum of n terms goes by
+    chunks of 512 and by splits; roundings are independent, too, so that sqrt(512 + n / 512 + 64) u of the terms' size is
+    above what they leave; logits D products in the same way, twice, the constants and the exponential 2^-20."""
+    from tests.test_gpu_ends import loss_inputs, plain_loss
+    h, W, t, b, dl = (None if x is None else x.cuda() for x in loss_inputs(N, V, D, N + 1, bias=True, dtype=dtype))
+    loss, lse = fw.fw_vocab_loss(h, W, t, bias=b)
+    got = fw.fw_vocab_loss_backward(h, W, t, loss, lse, dl, bias=b)
+    want = plain_loss(h, W, t, dl, b)
+    rel = lambda a, w: float((a.double() - w).norm() / w.norm())  # noqa: E731
+    if dtype == torch.bfloat16:
+        two = N <= 256 or (V <= 256 and N * D <= 2 ** 22)
+        assert rel(got[0], want[2]) <= 2.0 ** -8 * (2 / 3) ** 0.5 + 2.0 ** -12
+        assert rel(got[1], want[3]) <= 2.0 ** -8 * ((2 if two else 3) / 3) ** 0.5 + 2.0 ** -12
+    else:
+        S = float((h.abs() @ W.abs().T).max()) + 5
+        logits = 2 * (512 + D / 512 + 64) ** 0.5 * U * S + 2.0 ** -20
+        for x, w, n in ((got[0], want[2], V), (got[1], want[3], N)):
+            assert rel(x, w) <= 4 * (512 + n / 512 + 64) ** 0.5 * U + logits
+    assert rel(got[2], want[4]) <= 1e-5
